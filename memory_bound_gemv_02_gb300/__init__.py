@@ -12,7 +12,9 @@ Names follow the C entry points: ``gemv``, ``gemv_ex``, ``gemv_fused``, ``gemv_p
 ``gemv_plan``, ``gemv_last_config``, ``gemv_status_string``,
 ``gemv_last_cuda_error``, ``gemv_debug_inject``, ``gemv_release``,
 ``gemv_host``, ``gemv_splitk_noalloc``, ``gemv_wait_timeouts``,
-``gemv_debug_wait_budget``, ``gla_decode``, ``gla_decode_ex``.
+``gemv_debug_wait_budget``, ``gla_decode``, ``gla_decode_ex``, and the operators
+of include/gemv_ops.h: ``rms_norm_fused``, ``gemm_fused``, ``gated_scan``,
+``gated_scan_backward``.
 """
 from __future__ import annotations
 
@@ -49,6 +51,10 @@ ENTRY_POINTS = ("gemv", "gemv_ex", "gemv_fused", "gemv_prepare", "gemv_plan", "g
                 "gemv_wait_timeouts", "gemv_debug_wait_budget", "gla_decode", "gla_decode_ex")
 
 
+#: the entry points of include/gemv_ops.h
+OPERATOR_ENTRY_POINTS = ("rms_norm_fused", "gemm_fused", "gated_scan", "gated_scan_backward")
+
+
 class GemvConfig(ctypes.Structure):
     """Mirror of ``gemv_config`` in include/gemv.h."""
     _fields_ = [("variant", ctypes.c_int32), ("rows_per_warp", ctypes.c_int32),
@@ -80,6 +86,7 @@ class GemvError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_operators_ready = False
 
 
 def lib() -> ctypes.CDLL:
@@ -119,6 +126,25 @@ def lib() -> ctypes.CDLL:
                     getattr(L, name).restype = i32
             _lib = L
     return _lib
+
+
+def _lib_with_operators() -> ctypes.CDLL:
+    """The loaded library with the argument types of the operators set."""
+    global _operators_ready
+    L = _lib if _lib is not None else lib()
+    if _operators_ready:
+        return L
+    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+    seq = [vp, i64, i64]
+    L.rms_norm_fused.argtypes = [vp, i64, vp, i64, vp, i32, vp, i64, vp, vp, i64, i64, i64, ctypes.c_float, i32, i32,
+                                 vp]
+    L.gemm_fused.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp, vp]
+    L.gated_scan.argtypes = seq + seq + [vp] + seq + [vp, i64, i64, i64, i32, vp]
+    L.gated_scan_backward.argtypes = seq * 3 + [vp, vp] + seq * 2 + [vp, i64, i64, i64, i32, vp]
+    for name in OPERATOR_ENTRY_POINTS:
+        getattr(L, name).restype = i32
+    _operators_ready = True
+    return L
 
 
 # ------------------------------------------------------------- helpers --
@@ -366,3 +392,9 @@ def gla_decode(q, k, v, gk, S, scale: float, S_new=None, o=None, stream=None, va
             st = lib().gla_decode(*args, _stream_handle(stream))
     _check(st, "gla_decode")
     return S_new, o
+
+
+# The operators around the product, built on the helpers above.
+from ._operators import (GEMM_ACTIVATIONS, GEMV_ACT_LOG_SIGMOID, GEMV_TYPE_BF16, GEMV_TYPE_E4M3,  # noqa: E402
+                         GEMV_TYPE_F16, GEMV_TYPE_F32, GemmEpilogue, gated_scan, gated_scan_backward, gemm_fused,
+                         rms_norm_fused)

@@ -827,6 +827,22 @@ int run(const void *B, const void *a, void *c, int64_t n, int64_t k, int dtype, 
 }
 
 }  // namespace
+
+int current_device(int *dev, int *sms) {
+  if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) {
+    cudaGetLastError();
+    return GEMV_ERR_DEVICE;
+  }
+  std::lock_guard<std::mutex> lk(g_mu);
+  const DeviceInfo &di = device_info_locked(*dev);
+  *sms = di.sm_count;
+  return di.ok ? GEMV_OK : GEMV_ERR_DEVICE;
+}
+
+int cuda_failure(int cuda_error) { return cuda_fail(static_cast<cudaError_t>(cuda_error)); }
+
+int wait_counter(int dev, uint32_t **out) { return timeout_counter(dev, out); }
+
 }  // namespace gemvk
 
 using namespace gemvk;

@@ -89,6 +89,17 @@ inline bool on_device(int dev, std::initializer_list<const void *> ptrs) {
   return true;
 }
 
+// The current device, checked to be one this library runs on, with its SM
+// count; GEMV_OK or GEMV_ERR_DEVICE.  Attributes are queried once per device.
+int current_device(int *dev, int *sms);
+
+// Records a CUDA error for gemv_last_cuda_error() and returns GEMV_ERR_CUDA.
+int cuda_failure(int cuda_error);
+
+// Device address of the current device's counter of waits that gave up
+// (gemv_wait_timeouts()).
+int wait_counter(int dev, uint32_t **out);
+
 // Loads per lane issued back to back (per row) for R rows per warp.
 inline int unroll_for_rows(int R) { return R == 1 ? 8 : (R == 2 ? 4 : 2); }
 

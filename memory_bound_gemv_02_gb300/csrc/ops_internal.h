@@ -1,0 +1,121 @@
+// Shared by the operators of gemv_ops.h: element access for their storage
+// types, argument checks on strided buffers, and the launch.
+#pragma once
+
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gemv_kernels.cuh"
+#include "gemv_ops.h"
+
+namespace gemvk {
+
+// Element access for fp16, bf16 and fp32 storage, by GEMV_TYPE_* code.
+template <int TYPE>
+struct Elem;
+
+template <>
+struct Elem<GEMV_TYPE_F16> {
+  typedef uint16_t raw;
+  static constexpr int VEC = 8;  // elements per 16 bytes
+  static __device__ __forceinline__ float get(uint16_t v) { return F16::to_float(v); }
+  static __device__ __forceinline__ uint16_t put(float v) { return F16::from_float(v); }
+  static __device__ __forceinline__ void unpack(const uint4 &w, float (&f)[8]) { widen8<F16>(w, f); }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+  }
+};
+
+template <>
+struct Elem<GEMV_TYPE_BF16> {
+  typedef uint16_t raw;
+  static constexpr int VEC = 8;
+  static __device__ __forceinline__ float get(uint16_t v) { return BF16::to_float(v); }
+  static __device__ __forceinline__ uint16_t put(float v) { return BF16::from_float(v); }
+  static __device__ __forceinline__ void unpack(const uint4 &w, float (&f)[8]) { widen8<BF16>(w, f); }
+  static __device__ __forceinline__ uint32_t pair(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+  }
+};
+
+template <>
+struct Elem<GEMV_TYPE_F32> {
+  typedef float raw;
+  static constexpr int VEC = 4;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+  static __device__ __forceinline__ void unpack(const uint4 &w, float (&f)[4]) {
+    f[0] = __uint_as_float(w.x); f[1] = __uint_as_float(w.y); f[2] = __uint_as_float(w.z); f[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+inline int type_bytes(int type) { return type == GEMV_TYPE_F32 ? 4 : type == GEMV_TYPE_E4M3 ? 1 : 2; }
+
+// Rows of `width` bytes, `pitch` bytes apart, `rows` of them, from p.
+struct Rows {
+  const void *p;
+  int64_t rows, width, pitch;
+};
+
+// Whether two buffers share a byte.  Rows on one common pitch that lie in
+// disjoint column ranges do not; otherwise the spans from first to last byte
+// decide.
+inline bool rows_overlap(const Rows &a, const Rows &b) {
+  if (a.p == nullptr || b.p == nullptr || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const uintptr_t a0 = (uintptr_t)a.p, a1 = a0 + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
+  const uintptr_t b0 = (uintptr_t)b.p, b1 = b0 + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
+  if (a1 <= b0 || b1 <= a0) return false;
+  if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch && a.pitch > 0) {
+    const int64_t off = b0 >= a0 ? (int64_t)((b0 - a0) % (uintptr_t)a.pitch)
+                                 : (a.pitch - (int64_t)((a0 - b0) % (uintptr_t)a.pitch)) % a.pitch;
+    if (off >= a.width && off + b.width <= a.pitch) return false;
+  }
+  return true;
+}
+
+// The largest count of rows x pitch elements that any buffer may span: sizes
+// beyond it would overflow 64-bit byte offsets.
+inline bool span_fits(int64_t rows, int64_t pitch) {
+  return rows <= 0 || pitch <= 0 || rows <= (INT64_MAX / 16) / pitch;
+}
+
+// One kernel as a programmatic dependent launch, in clusters of `cluster`
+// CTAs along x.
+template <class P>
+int launch_op(void (*fn)(P), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream, const P &p) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  lc.attrs = attr;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, fn, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
+  }
+  return GEMV_OK;
+}
+
+}  // namespace gemvk
