@@ -1,35 +1,70 @@
 // C = act(alpha * sa_i sb_j (A B^T)_ij + beta * bias_j) + residual (see
-// gemm_fused() in gemv_ops.h).
+// gemm_fused() in gemv_ops.h), on the fifth-generation tensor cores.
+//
+// The weights B take the M side of every tcgen05.mma and the vectors A the N
+// side: a CTA's accumulator holds 128 rows of B (TMEM lanes) by up to 256
+// vectors (columns).  So a few vectors cost a few columns and the weights still
+// stream at full width, and each epilogue thread owns one output column j: its
+// bias and scale are registers, and the 32 lanes of a warp write 32 neighbours
+// of a row of C.
+//
+// Operand tiles are 128 bytes of k wide (64 16-bit or 128 8-bit elements) in
+// the 128-byte swizzle, in a ring of stages.  Warp 0 fills the ring by TMA (or
+// warps 6 to 9 by plain loads, where a base or row stride is not a multiple of
+// 16 bytes), one thread of warp 1 issues the matrix instructions, warps 2 to 5
+// write the result.
+//
+// Two kernels:
+//  * gemm_split_kernel, one tile per CTA: clusters of up to 8 CTAs share a tile
+//    and split its k; their partial sums are exchanged through distributed
+//    shared memory, each CTA finishing its share of the columns, in CTA order.
+//  * gemm_pair_kernel, persistent: pairs of CTAs compute 256 x 256 tiles with
+//    cta_group::2 instructions (each CTA loads half of both operands), two
+//    accumulators in TMEM so that a tile's epilogue overlaps the next product.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "ops_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gemvk {
 namespace {
 
+constexpr int kRowBytes = 128;                   // bytes of k per tile row
+constexpr int kTileRows = 128;                   // rows of B per CTA
+constexpr int kTileBytes = kTileRows * kRowBytes;
+constexpr int kMaxStages = 8;
+constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
+constexpr int kPolls = 1 << 20;                  // polls of one wait before it gives up
+constexpr int kThreadsTma = 192, kThreadsGather = 320;
+constexpr int kGatherWarps = 4;
+
 struct GemmParams {
-  const void *B, *A;
+  CUtensorMap map_b, map_a;
+  const char *B, *A;
   void *C;
-  int64_t ldb, lda, ldc, ldr;
-  int32_t m, n, k;
+  int64_t ldb_bytes, lda_bytes, ldc, ldr;
+  int32_t m, n;
+  int64_t k_bytes;
+  int32_t steps;              // 128-byte steps of k
+  int32_t cols;               // columns (vectors) per tile
+  int32_t tiles_n, tiles_m;   // tiles along n and along m
+  int32_t stages;
+  int32_t splits;             // CTAs that share a tile's k
   float alpha, beta;
   const float *scale_a, *scale_b;
   const void *bias, *residual;
-  int32_t bias_f32, act, in_type, out_type;
+  int32_t bias_f32, act, out_type;
+  uint32_t idesc;             // without the column count
+  int32_t polls;              // of the waits for operands
+  uint32_t *timeouts;
 };
 
-__device__ __forceinline__ float load_in(const void *p, int64_t i, int type) {
-  if (type == GEMV_TYPE_E4M3) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t *>(p)[i], __NV_E4M3);
-    return __half2float(__half(h));
-  }
-  const uint16_t v = static_cast<const uint16_t *>(p)[i];
-  return type == GEMV_TYPE_F16 ? F16::to_float(v) : BF16::to_float(v);
-}
+// ------------------------------------------------------------------ epilogue --
 
-__device__ __forceinline__ float load_out_type(const void *p, int64_t i, int type) {
+__device__ __forceinline__ float load_typed(const void *p, int64_t i, int type) {
   if (type == GEMV_TYPE_F32) return static_cast<const float *>(p)[i];
   const uint16_t v = static_cast<const uint16_t *>(p)[i];
   return type == GEMV_TYPE_F16 ? F16::to_float(v) : BF16::to_float(v);
@@ -43,42 +78,372 @@ __device__ __forceinline__ float activate(float y, int act) {
   return y;
 }
 
-constexpr int kTile = 64, kStep = 16, kGemmThreads = 256;
+// One thread's column j of C.
+struct Column {
+  int64_t j;
+  bool live;
+  float factor, shift;
+  __device__ Column(const GemmParams &p, int64_t j_) : j(j_), live(j_ < p.n), factor(p.alpha), shift(0.f) {
+    if (!live) return;
+    if (p.scale_b) factor *= p.scale_b[j];
+    if (p.bias) shift = p.beta * load_typed(p.bias, j, p.bias_f32 ? GEMV_TYPE_F32 : p.out_type);
+  }
+  // rows i0 .. i0 + COUNT - 1 of C from their sums
+  template <int COUNT>
+  __device__ __forceinline__ void write(const GemmParams &p, int64_t i0, const float (&sum)[COUNT]) const {
+    if (!live) return;
+    float res[COUNT];
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c)
+      res[c] = p.residual && i0 + c < p.m ? load_typed(p.residual, (i0 + c) * p.ldr + j, p.out_type) : 0.f;
+#pragma unroll
+    for (int c = 0; c < COUNT; ++c) {
+      const int64_t i = i0 + c;
+      if (i >= p.m) break;
+      float y = sum[c] * factor;
+      if (p.scale_a) y *= p.scale_a[i];
+      y = activate(y + shift, p.act) + res[c];
+      const int64_t at = i * p.ldc + j;
+      if (p.out_type == GEMV_TYPE_F32) static_cast<float *>(p.C)[at] = y;
+      else static_cast<uint16_t *>(p.C)[at] = p.out_type == GEMV_TYPE_F16 ? F16::from_float(y) : BF16::from_float(y);
+    }
+  }
+};
 
-__global__ void __launch_bounds__(kGemmThreads) gemm_kernel(GemmParams p) {
-  __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
+// --------------------------------------------------------------------- waits --
+
+// Polls a barrier until its phase `parity` completes.  False if the polls run
+// out or another role of this CTA has given up.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int polls) {
+  while (polls > 0) {
+    if (CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
+    if (*failed) return false;
+    --polls;
+  }
+  *failed = 1;
+  return false;
+}
+
+// The ring's position after each step.
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// ------------------------------------------------------- operands without TMA --
+
+// The 16 bytes that start `shift` bytes into the 32 bytes lo ++ hi.
+__device__ __forceinline__ uint4 funnel(const uint4 &lo, const uint4 &hi, int shift) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (shift & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (shift & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const int bits = (shift & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// The first `bytes` of v, the rest zero.
+__device__ __forceinline__ uint4 head_bytes(uint4 v, int64_t bytes) {
+  if (bytes >= 16) return v;
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t keep = bytes - 4 * i;
+    if (keep <= 0) w[i] = 0u;
+    else if (keep < 4) w[i] &= (1u << (8 * (int)keep)) - 1u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Rows [row0, row0 + rows) x 128 bytes of k from `kb`, read as the aligned
+// 16-byte blocks that hold their bytes (a lane's upper block is its
+// neighbour's lower one), shifted into place and stored swizzled.  Eight lanes
+// cover a row; `t` numbers the 128 gathering threads.
+template <int BATCH>
+__device__ __forceinline__ void gather_rows(const char *base, int64_t ld, int64_t row0, int64_t limit, int64_t kb,
+                                            int64_t k_bytes, int rows, uint32_t tile, int t) {
+  const int chunk = t & 7;
+  for (int r0 = t >> 3; r0 < rows; r0 += 16 * BATCH) {
+    uint4 lo[BATCH], hi[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int64_t row = row0 + r0 + 16 * u;
+      const uintptr_t start = (uintptr_t)base + (uintptr_t)(row * ld), end = start + (uintptr_t)k_bytes;
+      const uintptr_t block = (start + (uintptr_t)(kb + 16 * chunk)) & ~(uintptr_t)15;
+      const bool in = r0 + 16 * u < rows && row < limit;
+      lo[u] = in && block < end ? __ldg(reinterpret_cast<const uint4 *>(block)) : zero4();
+      hi[u] = in && chunk == 7 && (start & 15) && block + 16 < end ? __ldg(reinterpret_cast<const uint4 *>(block + 16))
+                                                                   : zero4();
+    }
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      const int r = r0 + 16 * u;
+      uint4 up;
+      up.x = __shfl_down_sync(0xffffffffu, lo[u].x, 1, 8);
+      up.y = __shfl_down_sync(0xffffffffu, lo[u].y, 1, 8);
+      up.z = __shfl_down_sync(0xffffffffu, lo[u].z, 1, 8);
+      up.w = __shfl_down_sync(0xffffffffu, lo[u].w, 1, 8);
+      if (chunk == 7) up = hi[u];
+      const int shift = (int)(((uintptr_t)base + (uintptr_t)((row0 + r) * ld)) & 15);
+      const uint4 v = head_bytes(funnel(lo[u], up, shift), k_bytes - kb - 16 * chunk);
+      if (r < rows) {
+        const uint32_t at = tile + (uint32_t)r * kRowBytes + (uint32_t)((chunk ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- split kernel --
+
+struct alignas(16) SplitShared {
+  uint64_t full[kMaxStages], empty[kMaxStages], done;
+  uint32_t tmem;
+  int failed;
+  int issued;  // steps whose copies were started
+};
+
+template <bool E4M3, bool GATHER>
+__global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
+    gemm_split_kernel(const __grid_constant__ GemmParams p) {
+  extern __shared__ char dynamic[];
+  __shared__ SplitShared sh;
+  const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;  // swizzled tiles start on 1024 bytes
+  const uint32_t stage_bytes = kTileBytes + (uint32_t)p.cols * kRowBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = p.splits > 1 ? (int)cluster_rank() : 0;
+  const int tile = blockIdx.x / p.splits;
+  const int64_t j0 = (int64_t)(tile % p.tiles_n) * kTileRows, i0 = (int64_t)(tile / p.tiles_n) * p.cols;
+  // this CTA's share of k, whole steps, as even as they come
+  const int begin = (int)((int64_t)p.steps * split / p.splits), end = (int)((int64_t)p.steps * (split + 1) / p.splits);
+  const uint32_t columns = p.cols <= 32 ? 32 : p.cols <= 64 ? 64 : p.cols <= 128 ? 128 : 256;
+
+  if (threadIdx.x == 0) {
+    sh.failed = 0;
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&sh.full[s]), GATHER ? kGatherWarps : 1);
+      mbar_init(smem_u32(&sh.empty[s]), 1);
+    }
+    mbar_init(smem_u32(&sh.done), 1);
+    mbar_init_fence();
+    if (!GATHER) {
+      prefetch_map(&p.map_b);
+      prefetch_map(&p.map_a);
+    }
+  }
+  if (warp == 1) tmem_alloc<1>(smem_u32(&sh.tmem), columns);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  // After the allocation: a dependent kernel that started first could hold the
+  // TMEM that this one waits for.
   allow_dependents();
   wait_for_predecessor();
-  const int64_t j0 = (int64_t)blockIdx.x * kTile, i0 = (int64_t)blockIdx.y * kTile;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int64_t t0 = 0; t0 < p.k; t0 += kStep) {
-    for (int e = threadIdx.x; e < kTile * kStep; e += kGemmThreads) {
-      const int r = e / kStep, t = e % kStep;
-      const bool in = t0 + t < p.k;
-      as[t][r] = in && i0 + r < p.m ? load_in(p.A, (i0 + r) * p.lda + t0 + t, p.in_type) : 0.f;
-      bs[t][r] = in && j0 + r < p.n ? load_in(p.B, (j0 + r) * p.ldb + t0 + t, p.in_type) : 0.f;
+
+  if (!GATHER && warp == 0) {
+    if (lane == 0) {
+      Ring r;
+      int step = begin;
+      for (; step < end; ++step) {
+        if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
+        const uint32_t bar = smem_u32(&sh.full[r.stage]), at = tiles + r.stage * stage_bytes;
+        mbar_expect_tx(bar, stage_bytes);
+        const int32_t x = step * (E4M3 ? kRowBytes : kRowBytes / 2);
+        tma_load<1>(at, &p.map_b, x, (int32_t)j0, bar);
+        tma_load<1>(at + kTileBytes, &p.map_a, x, (int32_t)i0, bar);
+        r.next(p.stages);
+      }
+      sh.issued = step - begin;
     }
-    __syncthreads();
-    for (int t = 0; t < kStep; ++t)
-      for (int u = 0; u < 4; ++u)
-        for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(as[t][ty + 16 * u], bs[t][tx + 16 * v], acc[u][v]);
+    __syncwarp();
+  } else if (GATHER && warp >= 6) {
+    Ring r;
+    const int t = threadIdx.x - 6 * 32;
+    for (int step = begin; step < end; ++step) {
+      int go = 1;
+      if (step - begin >= p.stages) {
+        if (lane == 0) go = wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls);
+        go = __shfl_sync(0xffffffffu, go, 0);
+      }
+      if (!go) break;
+      const uint32_t at = tiles + r.stage * stage_bytes;
+      const int64_t kb = (int64_t)step * kRowBytes;
+      gather_rows<8>(p.B, p.ldb_bytes, j0, p.n, kb, p.k_bytes, kTileRows, at, t);
+      gather_rows<4>(p.A, p.lda_bytes, i0, p.m, kb, p.k_bytes, p.cols, at + kTileBytes, t);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.full[r.stage]));
+      r.next(p.stages);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      Ring r;
+      const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+      for (int step = begin; step < end; ++step) {
+        if (!wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls)) break;
+        tc_fence_after();
+        const uint32_t at = tiles + r.stage * stage_bytes;
+        const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
+#pragma unroll
+        for (int s = 0; s < kMmaSteps; ++s)
+          tc_mma<1, E4M3>(tmem, db + 2 * s, da + 2 * s, idesc, step > begin || s > 0);
+        tc_commit<1>(smem_u32(&sh.empty[r.stage]));
+        r.next(p.stages);
+      }
+      // Also after a wait that gave up: the instructions issued so far read
+      // shared memory until they complete.
+      tc_commit<1>(smem_u32(&sh.done));
+      int zero = 0;
+      wait_for<false>(smem_u32(&sh.done), 0, &zero, kPolls);
+      if (sh.failed) atomicAdd(p.timeouts, 1u);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();  // the sums are complete; shared memory is free
+  tc_fence_after();
+  const float nan = __int_as_float(0x7fc00000);
+  const bool empty = begin == end, failed = sh.failed != 0;
+  if (!GATHER && failed) {  // copies in flight land before their memory is used again
+    if (threadIdx.x == 0) {
+      int none = 0;
+      Ring d;
+      for (int s = 0; s < sh.issued; ++s, d.next(p.stages))
+        if (s + p.stages >= sh.issued) wait_for<false>(smem_u32(&sh.full[d.stage]), d.phase, &none, kPolls);
+    }
     __syncthreads();
   }
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const int64_t i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-      if (i >= p.m || j >= p.n) continue;
-      float y = acc[u][v] * p.alpha;
-      if (p.scale_a) y *= p.scale_a[i];
-      if (p.scale_b) y *= p.scale_b[j];
-      if (p.bias) y = fmaf(p.beta, load_out_type(p.bias, j, p.bias_f32 ? GEMV_TYPE_F32 : p.out_type), y);
-      y = activate(y, p.act);
-      if (p.residual) y += load_out_type(p.residual, i * p.ldr + j, p.out_type);
-      if (p.out_type == GEMV_TYPE_F32) static_cast<float *>(p.C)[i * p.ldc + j] = y;
-      else static_cast<uint16_t *>(p.C)[i * p.ldc + j] =
-          p.out_type == GEMV_TYPE_F16 ? F16::from_float(y) : BF16::from_float(y);
+  if (p.splits > 1) cluster_sync();
+
+  if (warp >= 2 && warp < 6) {
+    const int quarter = warp & 3;  // the 32 lanes of TMEM that this warp may read
+    const int l = quarter * 32 + lane;
+    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+    if (p.splits == 1) {
+      const Column col(p, j0 + l);
+      for (int c = 0; c < p.cols && i0 + c < p.m; c += 16) {
+        float v[16];
+        tmem_load16(from + c, v);
+        if (empty || failed) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = failed ? nan : 0.f;
+        }
+        col.write(p, i0 + c, v);
+      }
+    } else {
+      // Column c goes to CTA c / share, as [source][column][lane].
+      const int share = p.cols / p.splits;
+      for (int c = 0; c < p.cols; c += 16) {
+        float v[16];
+        tmem_load16(from + c, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int to = (c + e) / share, at = (c + e) % share;
+          st_cluster(cluster_address(tiles + (uint32_t)(((split * share + at) * kTileRows + l) * 4), to),
+                     failed ? nan : empty ? 0.f : v[e]);
+        }
+      }
     }
+  }
+  if (p.splits > 1) {
+    cluster_sync();
+    if (warp >= 2 && warp < 6) {
+      const int share = p.cols / p.splits, l = (warp & 3) * 32 + lane;
+      const Column col(p, j0 + l);
+      const float *parts = reinterpret_cast<const float *>(dynamic + (tiles - smem_u32(dynamic)));
+      for (int c = 0; c < share; ++c) {
+        float v[1] = {0.f};
+        for (int s = 0; s < p.splits; ++s) v[0] += parts[(s * share + c) * kTileRows + l];
+        const int64_t i = i0 + (int64_t)split * share + c;
+        if (i < p.m) col.write(p, i, v);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free<1>(tmem, columns);
+  }
+}
+
+// ---------------------------------------------------------------------- host --
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder (looked up once).
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      f = nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A (rows, k) operand with `ld_bytes` between rows, in boxes of 128 bytes of k
+// by `box_rows` rows; what lies outside reads as zero.
+bool encode(CUtensorMap *map, const void *p, int dtype, int64_t rows, int64_t k, int64_t ld_bytes, int box_rows) {
+  const EncodeFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int es = type_bytes(dtype);
+  if (rows == 1) ld_bytes = (k * es + 15) / 16 * 16;
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows}, one[2] = {1, 1};
+  const CUtensorMapDataType t = dtype == GEMV_TYPE_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                : dtype == GEMV_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  return fn(map, t, 2, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tma_ok(const void *p, int64_t rows, int64_t ld_bytes) {
+  return (uintptr_t)p % 16 == 0 && (rows == 1 || (ld_bytes % 16 == 0 && ld_bytes < (1ll << 40)));
+}
+
+int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int kSmemPair = 112 * 1024;   // dynamic shared memory that leaves room for two CTAs per SM
+constexpr int kSmemAlone = 225 * 1024;  // and for one
+
+// Tile shape, split and ring of gemm_split_kernel.
+void plan_split(GemmParams &p, int sms, size_t *smem) {
+  p.tiles_m = (int32_t)cdiv64(p.m, 256);
+  p.cols = (int32_t)(cdiv64(cdiv64(p.m, p.tiles_m), 16) * 16);
+  p.tiles_n = (int32_t)cdiv64(p.n, kTileRows);
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  const int stage = kTileBytes + p.cols * kRowBytes;
+  const int budget = p.cols <= 96 ? kSmemPair : kSmemAlone;
+  const int64_t slots = (int64_t)sms * (p.cols <= 96 ? 2 : 1);
+  p.stages = (budget - 1024) / stage;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= slots && p.steps / (p.splits * 2) >= 4) p.splits *= 2;
+  const int64_t ring = (int64_t)p.stages * stage, exchange = p.splits > 1 ? (int64_t)p.cols * kTileRows * 4 : 0;
+  *smem = (size_t)((ring > exchange ? ring : exchange) + 1024);
 }
 
 }  // namespace
@@ -121,15 +486,36 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   if (st != GEMV_OK) return st;
   if (!on_device(dev, {k > 0 ? A : nullptr, k > 0 ? B : nullptr, C, ep.scale_a, ep.scale_b, ep.bias, ep.residual}))
     return GEMV_ERR_DEVICE;
-  GemmParams p;
-  p.B = B; p.A = A; p.C = C;
-  p.ldb = ldb; p.lda = lda; p.ldc = ldc; p.ldr = ep.ldr;
-  p.m = (int32_t)m; p.n = (int32_t)n; p.k = (int32_t)k;
+  GemmParams p = {};
+  p.B = static_cast<const char *>(B); p.A = static_cast<const char *>(A); p.C = C;
+  p.ldb_bytes = ldb * es; p.lda_bytes = lda * es; p.ldc = ldc; p.ldr = ep.ldr;
+  p.m = (int32_t)m; p.n = (int32_t)n; p.k_bytes = k * es;
+  const int64_t steps = cdiv64(p.k_bytes, kRowBytes);
+  if (steps > INT32_MAX) return GEMV_ERR_ARG;
+  p.steps = (int32_t)steps;
   p.alpha = ep.alpha; p.beta = ep.beta;
   p.scale_a = ep.scale_a; p.scale_b = ep.scale_b; p.bias = ep.bias; p.residual = ep.residual;
   p.bias_f32 = ep.bias_dtype == GEMV_TYPE_F32 ? 1 : 0;
-  p.act = ep.activation; p.in_type = dtype; p.out_type = out_dtype;
-  if ((m + kTile - 1) / kTile > 65535) return GEMV_ERR_ARG;
-  return launch_op(gemm_kernel, dim3((unsigned)((n + kTile - 1) / kTile), (unsigned)((m + kTile - 1) / kTile)),
-                   kGemmThreads, 0, 1, stream, p);
+  p.act = ep.activation; p.out_type = out_dtype;
+  // fp32 accumulators (bit 4); operand types in bits 7 and 10: 0 fp16 or e4m3, 1 bf16
+  p.idesc = (1u << 4) | (dtype == GEMV_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
+  p.polls = take_wait_budget(kPolls);
+  int st2 = wait_counter(dev, &p.timeouts);
+  if (st2 != GEMV_OK) return st2;
+  size_t smem = 0;
+  plan_split(p, sms, &smem);
+  const int64_t grid = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+  if (grid > INT32_MAX) return GEMV_ERR_ARG;
+  const bool tma = k > 0 && tma_ok(B, n, p.ldb_bytes) && tma_ok(A, m, p.lda_bytes) &&
+                   encode(&p.map_b, B, dtype, n, k, p.ldb_bytes, kTileRows) &&
+                   encode(&p.map_a, A, dtype, m, k, p.lda_bytes, p.cols);
+  const bool e4m3 = dtype == GEMV_TYPE_E4M3;
+  void (*fn)(GemmParams) = tma ? (e4m3 ? gemm_split_kernel<true, false> : gemm_split_kernel<false, false>)
+                               : (e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>);
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
+  }
+  return launch_op(fn, dim3((unsigned)grid), tma ? kThreadsTma : kThreadsGather, smem, p.splits, stream, p);
 }

@@ -843,6 +843,11 @@ int cuda_failure(int cuda_error) { return cuda_fail(static_cast<cudaError_t>(cud
 
 int wait_counter(int dev, uint32_t **out) { return timeout_counter(dev, out); }
 
+int take_wait_budget(int usual) {
+  const int budget = g_wait_budget.exchange(-1);
+  return budget >= 0 ? budget : usual;
+}
+
 }  // namespace gemvk
 
 using namespace gemvk;

@@ -100,6 +100,9 @@ int cuda_failure(int cuda_error);
 // (gemv_wait_timeouts()).
 int wait_counter(int dev, uint32_t **out);
 
+// The one-shot poll budget of gemv_debug_wait_budget(), or `usual` if none is set.
+int take_wait_budget(int usual);
+
 // Loads per lane issued back to back (per row) for R rows per warp.
 inline int unroll_for_rows(int R) { return R == 1 ? 8 : (R == 2 ? 4 : 2); }
 

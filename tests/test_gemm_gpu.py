@@ -232,3 +232,18 @@ def test_refusals(cuda_dev):
         g.gemm_fused(B, A, wide[:, :16], residual=wide[:, 1:17])
     assert e.value.status == g.GEMV_ERR_ALIAS
     g.gemm_fused(B, A, wide[:, :16], residual=wide[:, 16:32])  # column ranges of one matrix do not overlap
+
+
+@pytest.mark.parametrize("m,n,k,pad", [(3, 200, 4096, 0), (3, 200, 4095, 1), (150, 900, 640, 0)])
+def test_a_wait_that_gives_up(cuda_dev, m, n, k, pad):
+    """A wait for operands given no polls: the call returns, its tiles hold NaN, the
+    counter says so, and the next call is right."""
+    A, B = _operands(m, n, k, torch.bfloat16, cuda_dev, 23, pad, 0)
+    torch.cuda.synchronize()
+    g.gemv_wait_timeouts(reset=True)
+    g.gemv_debug_wait_budget(0)
+    c = g.gemm_fused(B, A)
+    torch.cuda.synchronize()
+    assert torch.isnan(c).all() and g.gemv_wait_timeouts(reset=True) > 0
+    _check(g.gemm_fused(B, A), B, A, "after")
+    assert g.gemv_wait_timeouts() == 0
