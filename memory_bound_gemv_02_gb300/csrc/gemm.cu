@@ -40,6 +40,9 @@ constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
 constexpr int kPolls = 1 << 20;                  // polls of one wait before it gives up
 constexpr int kThreadsTma = 192, kThreadsGather = 320;
 constexpr int kGatherWarps = 4;
+constexpr int kSplitBand = 16, kPairBand = 8;    // tiles along n that run side by side
+constexpr int kAccumulators = 2;                 // of gemm_pair_kernel
+constexpr int kAccumulatorColumns = 256;
 
 struct GemmParams {
   CUtensorMap map_b, map_a;
@@ -115,7 +118,7 @@ struct Column {
 // Polls a barrier until its phase `parity` completes.  False if the polls run
 // out or another role of this CTA has given up.
 template <bool CLUSTER>
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int polls) {
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int64_t polls) {
   while (polls > 0) {
     if (CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
     if (*failed) return false;
@@ -123,6 +126,11 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
   }
   *failed = 1;
   return false;
+}
+
+// Tells every role of a pair's two CTAs to give up.
+__device__ __forceinline__ void fail_pair(int *failed) {
+  for (uint32_t r = 0; r < 2; ++r) st_cluster(cluster_address(smem_u32(failed), r), 1);
 }
 
 // The ring's position after each step.
@@ -136,6 +144,18 @@ struct Ring {
     }
   }
 };
+
+// Tile number -> tile along n and along m: bands of `band` tiles along n,
+// walked along m, so that the tiles computed at one time share few operand
+// rows and the L2 serves the rest of their reads.
+__device__ __forceinline__ void tile_at(int64_t t, int tiles_n, int tiles_m, int band, int *tn, int *tm) {
+  const int64_t whole = (int64_t)band * tiles_m;
+  const int first = (int)(t / whole) * band;
+  const int width = tiles_n - first < band ? tiles_n - first : band;
+  const int in = (int)(t % whole);
+  *tm = in / width;
+  *tn = first + in % width;
+}
 
 // ------------------------------------------------------- operands without TMA --
 
@@ -226,8 +246,9 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
   const uint32_t stage_bytes = kTileBytes + (uint32_t)p.cols * kRowBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = p.splits > 1 ? (int)cluster_rank() : 0;
-  const int tile = blockIdx.x / p.splits;
-  const int64_t j0 = (int64_t)(tile % p.tiles_n) * kTileRows, i0 = (int64_t)(tile / p.tiles_n) * p.cols;
+  int tile_n, tile_m;
+  tile_at(blockIdx.x / p.splits, p.tiles_n, p.tiles_m, kSplitBand, &tile_n, &tile_m);
+  const int64_t j0 = (int64_t)tile_n * kTileRows, i0 = (int64_t)tile_m * p.cols;
   // this CTA's share of k, whole steps, as even as they come
   const int begin = (int)((int64_t)p.steps * split / p.splits), end = (int)((int64_t)p.steps * (split + 1) / p.splits);
   const uint32_t columns = p.cols <= 32 ? 32 : p.cols <= 64 ? 64 : p.cols <= 128 ? 128 : 256;
@@ -324,7 +345,8 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
       int none = 0;
       Ring d;
       for (int s = 0; s < sh.issued; ++s, d.next(p.stages))
-        if (s + p.stages >= sh.issued) wait_for<false>(smem_u32(&sh.full[d.stage]), d.phase, &none, kPolls);
+        if (s + p.stages >= sh.issued && !wait_for<false>(smem_u32(&sh.full[d.stage]), d.phase, &none, kPolls))
+          atomicOr(p.timeouts, kDrainTimeoutBit);
     }
     __syncthreads();
   }
@@ -382,6 +404,181 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
   }
 }
 
+// -------------------------------------------------------------- pair kernel --
+
+struct alignas(16) PairShared {
+  uint64_t full[kMaxStages], empty[kMaxStages];      // full: the leader's count for both CTAs
+  uint64_t sums[kAccumulators], free_[kAccumulators];  // accumulator complete; read by both epilogues (leader's)
+  uint64_t done;
+  int64_t issued;
+  uint32_t tmem;
+  int failed;
+};
+
+// Persistent over tiles of 256 rows of B by p.cols vectors.  CTA r of a pair
+// holds rows 128 r .. 128 r + 127 of the tile's B and half of its vectors; the
+// leader (r = 0) issues the instructions, which read both CTAs' shared memory
+// and write each CTA's 128 rows of the accumulator to its own TMEM.
+template <bool E4M3>
+__global__ void __launch_bounds__(kThreadsTma) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+  extern __shared__ char dynamic[];
+  __shared__ PairShared sh;
+  const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
+  const int half = p.cols / 2;
+  const uint32_t stage_bytes = kTileBytes + (uint32_t)half * kRowBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int64_t count = (int64_t)p.tiles_n * p.tiles_m, pairs = gridDim.x / 2, first = blockIdx.x / 2;
+
+  if (threadIdx.x == 0) {
+    sh.failed = 0;
+    sh.issued = 0;
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&sh.full[s]), 1);
+      mbar_init(smem_u32(&sh.empty[s]), 1);
+    }
+    for (int a = 0; a < kAccumulators; ++a) {
+      mbar_init(smem_u32(&sh.sums[a]), 1);
+      mbar_init(smem_u32(&sh.free_[a]), 8);  // four epilogue warps of each CTA
+    }
+    mbar_init(smem_u32(&sh.done), 1);
+    mbar_init_fence();
+    prefetch_map(&p.map_b);
+    prefetch_map(&p.map_a);
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(&sh.tmem), kAccumulators * kAccumulatorColumns);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  allow_dependents();  // after the allocation, as in gemm_split_kernel
+  wait_for_predecessor();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      Ring r;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t t = first; ok && t < count; t += pairs) {
+        int tn, tm;
+        tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
+        const int32_t j0 = tn * (2 * kTileRows) + rank * kTileRows, i0 = tm * p.cols + rank * half;
+        for (int step = 0; step < p.steps; ++step) {
+          ok = issued < p.stages || wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls);
+          if (!ok) break;
+          const uint32_t full = smem_u32(&sh.full[r.stage]), at = tiles + r.stage * stage_bytes;
+          if (rank == 0) mbar_expect_tx(full, 2 * stage_bytes);
+          const uint32_t bar = cluster_address(full, 0);
+          const int32_t x = step * (E4M3 ? kRowBytes : kRowBytes / 2);
+          tma_load<2>(at, &p.map_b, x, j0, bar);
+          tma_load<2>(at + kTileBytes, &p.map_a, x, i0, bar);
+          ++issued;
+          r.next(p.stages);
+        }
+      }
+      sh.issued = issued;
+      if (!ok) fail_pair(&sh.failed);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      Ring r;
+      const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(2 * kTileRows >> 4) << 24);
+      bool ok = true;
+      int turn = 0;
+      for (int64_t t = first; ok && t < count; t += pairs, ++turn) {
+        const int acc = turn & 1;
+        const uint32_t d = tmem + (uint32_t)(acc * kAccumulatorColumns);
+        ok = turn < kAccumulators ||
+             wait_for<true>(smem_u32(&sh.free_[acc]), ((turn >> 1) & 1) ^ 1, &sh.failed, kPolls);
+        tc_fence_after();
+        for (int step = 0; ok && step < p.steps; ++step) {
+          ok = wait_for<true>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = tiles + r.stage * stage_bytes;
+          const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
+#pragma unroll
+          for (int s = 0; s < kMmaSteps; ++s) tc_mma<2, E4M3>(d, db + 2 * s, da + 2 * s, idesc, step > 0 || s > 0);
+          tc_commit<2>(smem_u32(&sh.empty[r.stage]));
+          r.next(p.stages);
+        }
+        if (ok) tc_commit<2>(smem_u32(&sh.sums[acc]));
+      }
+      if (!ok) fail_pair(&sh.failed);
+      // Also after a wait that gave up: the instructions issued so far read
+      // both CTAs' shared memory until they complete.
+      tc_commit<2>(smem_u32(&sh.done));
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, l = quarter * 32 + lane;
+    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+    bool ok = true;
+    int turn = 0;
+    for (int64_t t = first; t < count; t += pairs, ++turn) {
+      const int acc = turn & 1;
+      int tn, tm;
+      tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
+      const int64_t i0 = (int64_t)tm * p.cols;
+      const Column col(p, (int64_t)tn * (2 * kTileRows) + rank * kTileRows + l);
+      if (ok) {
+        int go = 0;
+        // a whole product: some polls for each of its steps
+        if (lane == 0)
+          go = wait_for<true>(smem_u32(&sh.sums[acc]), (turn >> 1) & 1, &sh.failed, kPolls + 64ll * p.steps);
+        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+        if (!ok && lane == 0) fail_pair(&sh.failed);
+        tc_fence_after();
+      }
+      for (int c = 0; c < p.cols && i0 + c < p.m; c += 16) {
+        float v[16];
+        if (ok) {
+          tmem_load16(from + (uint32_t)(acc * kAccumulatorColumns + c), v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fc00000);
+        }
+        col.write(p, i0 + c, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive_cluster(cluster_address(smem_u32(&sh.free_[acc]), 0));
+    }
+  }
+  __syncthreads();
+  // Every instruction issued has completed, in both CTAs' view.
+  if (warp == 1 && lane == 0) {
+    int none = 0;
+    wait_for<true>(smem_u32(&sh.done), 0, &none, kPolls);
+  }
+  __syncthreads();
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    const int other_failed = ld_cluster(cluster_address(smem_u32(&sh.failed), 1));
+    if (sh.failed || other_failed) {
+      atomicAdd(p.timeouts, 1u);
+      // Copies in flight land before the CTAs leave: the barriers of the last
+      // steps are completed by what each CTA did start.
+      const int64_t mine = sh.issued, other = ld_cluster64(cluster_address(smem_u32(&sh.issued), 1));
+      const int64_t most = mine > other ? mine : other;
+      Ring d;
+      for (int64_t s = 0; s < most; ++s, d.next(p.stages)) {
+        if (s + p.stages < most) continue;
+        const uint32_t bar = smem_u32(&sh.full[d.stage]);
+        if (s >= mine) mbar_expect_tx(bar, stage_bytes);
+        else if (s >= other) mbar_complete_tx(bar, stage_bytes);
+        int none = 0;
+        if (!wait_for<true>(bar, d.phase, &none, kPolls)) atomicOr(p.timeouts, kDrainTimeoutBit);
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) tmem_free<2>(tmem, kAccumulators * kAccumulatorColumns);
+}
+
 // ---------------------------------------------------------------------- host --
 
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -428,6 +625,18 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int kSmemPair = 112 * 1024;   // dynamic shared memory that leaves room for two CTAs per SM
 constexpr int kSmemAlone = 225 * 1024;  // and for one
+
+// Tiles and ring of gemm_pair_kernel.
+void plan_pair(GemmParams &p, size_t *smem) {
+  p.splits = 1;
+  p.tiles_m = (int32_t)cdiv64(p.m, kAccumulatorColumns);
+  p.cols = (int32_t)(cdiv64(cdiv64(p.m, p.tiles_m), 32) * 32);
+  p.tiles_n = (int32_t)cdiv64(p.n, 2 * kTileRows);
+  const int stage = kTileBytes + p.cols / 2 * kRowBytes;
+  p.stages = (kSmemAlone - 1024) / stage;
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  *smem = (size_t)p.stages * stage + 1024;
+}
 
 // Tile shape, split and ring of gemm_split_kernel.
 void plan_split(GemmParams &p, int sms, size_t *smem) {
@@ -503,19 +712,25 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   int st2 = wait_counter(dev, &p.timeouts);
   if (st2 != GEMV_OK) return st2;
   size_t smem = 0;
-  plan_split(p, sms, &smem);
-  const int64_t grid = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-  if (grid > INT32_MAX) return GEMV_ERR_ARG;
-  const bool tma = k > 0 && tma_ok(B, n, p.ldb_bytes) && tma_ok(A, m, p.lda_bytes) &&
-                   encode(&p.map_b, B, dtype, n, k, p.ldb_bytes, kTileRows) &&
-                   encode(&p.map_a, A, dtype, m, k, p.lda_bytes, p.cols);
   const bool e4m3 = dtype == GEMV_TYPE_E4M3;
-  void (*fn)(GemmParams) = tma ? (e4m3 ? gemm_split_kernel<true, false> : gemm_split_kernel<false, false>)
-                               : (e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>);
+  const bool tma = k > 0 && tma_ok(B, n, p.ldb_bytes) && tma_ok(A, m, p.lda_bytes);
+  const bool pair = tma && m > 256;
+  if (pair) plan_pair(p, &smem);
+  else plan_split(p, sms, &smem);
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+  if (tiles * p.splits > INT32_MAX) return GEMV_ERR_ARG;
+  if (tma && (!encode(&p.map_b, B, dtype, n, k, p.ldb_bytes, kTileRows) ||
+              !encode(&p.map_a, A, dtype, m, k, p.lda_bytes, pair ? p.cols / 2 : p.cols)))
+    return cuda_failure((int)cudaErrorNotSupported);
+  void (*fn)(GemmParams) = pair   ? (e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>)
+                           : tma  ? (e4m3 ? gemm_split_kernel<true, false> : gemm_split_kernel<false, false>)
+                           : e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>;
+  int64_t grid = tiles * p.splits;
+  if (pair) grid = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_failure((int)e);
   }
-  return launch_op(fn, dim3((unsigned)grid), tma ? kThreadsTma : kThreadsGather, smem, p.splits, stream, p);
+  return launch_op(fn, dim3((unsigned)grid), tma ? kThreadsTma : kThreadsGather, smem, pair ? 2 : p.splits, stream, p);
 }
