@@ -10,8 +10,8 @@
 //
 // Operand tiles are 128 bytes of k wide (64 16-bit or 128 8-bit elements) in
 // the 128-byte swizzle, in a ring of stages.  Warp 0 fills the ring by TMA (or
-// warps 6 to 9 by plain loads, where a base or row stride is not a multiple of
-// 16 bytes), one thread of warp 1 issues the matrix instructions, warps 2 to 5
+// warps 4 to 7 by plain loads, where a base or row stride is not a multiple of
+// 16 bytes), one thread of warp 1 issues the matrix instructions, eight warps
 // write the result.
 //
 // Two kernels:
@@ -38,8 +38,8 @@ constexpr int kTileBytes = kTileRows * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
 constexpr int kPolls = 1 << 20;                  // polls of one wait before it gives up
-constexpr int kThreadsTma = 192, kThreadsGather = 320;
-constexpr int kGatherWarps = 4;
+constexpr int kSplitThreads = 256, kPairThreads = 320;
+constexpr int kGatherWarps = 4;                  // warps 4 to 7
 constexpr int kSplitBand = 16, kPairBand = 8;    // tiles along n that run side by side
 constexpr int kAccumulators = 2;                 // of gemm_pair_kernel
 constexpr int kAccumulatorColumns = 256;
@@ -73,15 +73,23 @@ __device__ __forceinline__ float load_typed(const void *p, int64_t i, int type) 
   return type == GEMV_TYPE_F16 ? F16::to_float(v) : BF16::to_float(v);
 }
 
-__device__ __forceinline__ float activate(float y, int act) {
-  if (act == GEMV_ACT_RELU) return y != y ? y : fmaxf(y, 0.f);
-  if (act == GEMV_ACT_SIGMOID) return 1.f / (1.f + expf(-y));
-  if (act == GEMV_ACT_SILU) return y / (1.f + expf(-y));
-  if (act == GEMV_ACT_LOG_SIGMOID) return fminf(y, 0.f) - log1pf(expf(-fabsf(y)));
+template <int ACT>
+__device__ __forceinline__ float activated(float y) {
+  if (ACT == GEMV_ACT_RELU) return y != y ? y : fmaxf(y, 0.f);
+  if (ACT == GEMV_ACT_SIGMOID) return 1.f / (1.f + expf(-y));
+  if (ACT == GEMV_ACT_SILU) return y / (1.f + expf(-y));
+  if (ACT == GEMV_ACT_LOG_SIGMOID) return fminf(y, 0.f) - log1pf(expf(-fabsf(y)));
   return y;
 }
+template <int ACT, int COUNT>
+__device__ __forceinline__ void activate_all(float (&y)[COUNT]) {
+#pragma unroll
+  for (int c = 0; c < COUNT; ++c) y[c] = activated<ACT>(y[c]);
+}
 
-// One thread's column j of C.
+// One thread's column j of C.  The epilogue's choices are made once for COUNT
+// rows and each is a loop without branches: with a few warps per SM, a row at
+// a time left every instruction's latency exposed (49 us per 256 x 256 tile).
 struct Column {
   int64_t j;
   bool live;
@@ -91,25 +99,67 @@ struct Column {
     if (p.scale_b) factor *= p.scale_b[j];
     if (p.bias) shift = p.beta * load_typed(p.bias, j, p.bias_f32 ? GEMV_TYPE_F32 : p.out_type);
   }
-  // rows i0 .. i0 + COUNT - 1 of C from their sums
-  template <int COUNT>
-  __device__ __forceinline__ void write(const GemmParams &p, int64_t i0, const float (&sum)[COUNT]) const {
-    if (!live) return;
-    float res[COUNT];
+
+  template <class Out, int COUNT, class Convert>
+  __device__ __forceinline__ void store(const GemmParams &p, int64_t i0, int rows, const float (&y)[COUNT],
+                                        Convert convert) const {
+    Out *c = static_cast<Out *>(p.C) + i0 * p.ldc + j;
+    if (rows >= COUNT) {
 #pragma unroll
-    for (int c = 0; c < COUNT; ++c)
-      res[c] = p.residual && i0 + c < p.m ? load_typed(p.residual, (i0 + c) * p.ldr + j, p.out_type) : 0.f;
+      for (int e = 0; e < COUNT; ++e) c[e * p.ldc] = convert(y[e]);
+    } else {
 #pragma unroll
-    for (int c = 0; c < COUNT; ++c) {
-      const int64_t i = i0 + c;
-      if (i >= p.m) break;
-      float y = sum[c] * factor;
-      if (p.scale_a) y *= p.scale_a[i];
-      y = activate(y + shift, p.act) + res[c];
-      const int64_t at = i * p.ldc + j;
-      if (p.out_type == GEMV_TYPE_F32) static_cast<float *>(p.C)[at] = y;
-      else static_cast<uint16_t *>(p.C)[at] = p.out_type == GEMV_TYPE_F16 ? F16::from_float(y) : BF16::from_float(y);
+      for (int e = 0; e < COUNT; ++e)
+        if (e < rows) c[e * p.ldc] = convert(y[e]);
     }
+  }
+
+  // rows i0 .. of C from their sums: as many of the COUNT as there are, at most `most`
+  template <int COUNT>
+  __device__ __forceinline__ void write(const GemmParams &p, int64_t i0, const float (&sum)[COUNT],
+                                        int most = COUNT) const {
+    if (!live) return;
+    const int rows = p.m - i0 < most ? (int)(p.m - i0) : most;
+    float res[COUNT];
+    if (p.residual) {
+      if (p.out_type == GEMV_TYPE_F32) {
+        const float *r = static_cast<const float *>(p.residual) + i0 * p.ldr + j;
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) res[e] = e < rows ? r[e * p.ldr] : 0.f;
+      } else {
+        const uint16_t *r = static_cast<const uint16_t *>(p.residual) + i0 * p.ldr + j;
+        uint16_t raw[COUNT];
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) raw[e] = e < rows ? r[e * p.ldr] : 0;
+        if (p.out_type == GEMV_TYPE_F16) {
+#pragma unroll
+          for (int e = 0; e < COUNT; ++e) res[e] = F16::to_float(raw[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < COUNT; ++e) res[e] = BF16::to_float(raw[e]);
+        }
+      }
+    }
+    float y[COUNT];
+#pragma unroll
+    for (int e = 0; e < COUNT; ++e) y[e] = sum[e] * factor;
+    if (p.scale_a) {
+#pragma unroll
+      for (int e = 0; e < COUNT; ++e) y[e] *= e < rows ? p.scale_a[i0 + e] : 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < COUNT; ++e) y[e] += shift;
+    if (p.act == GEMV_ACT_RELU) activate_all<GEMV_ACT_RELU>(y);
+    else if (p.act == GEMV_ACT_SIGMOID) activate_all<GEMV_ACT_SIGMOID>(y);
+    else if (p.act == GEMV_ACT_SILU) activate_all<GEMV_ACT_SILU>(y);
+    else if (p.act == GEMV_ACT_LOG_SIGMOID) activate_all<GEMV_ACT_LOG_SIGMOID>(y);
+    if (p.residual) {
+#pragma unroll
+      for (int e = 0; e < COUNT; ++e) y[e] += res[e];
+    }
+    if (p.out_type == GEMV_TYPE_F32) store<float>(p, i0, rows, y, [](float v) { return v; });
+    else if (p.out_type == GEMV_TYPE_F16) store<uint16_t>(p, i0, rows, y, [](float v) { return F16::from_float(v); });
+    else store<uint16_t>(p, i0, rows, y, [](float v) { return BF16::from_float(v); });
   }
 };
 
@@ -238,8 +288,7 @@ struct alignas(16) SplitShared {
 };
 
 template <bool E4M3, bool GATHER>
-__global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
-    gemm_split_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ char dynamic[];
   __shared__ SplitShared sh;
   const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;  // swizzled tiles start on 1024 bytes
@@ -292,9 +341,9 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
       sh.issued = step - begin;
     }
     __syncwarp();
-  } else if (GATHER && warp >= 6) {
+  } else if (GATHER && warp >= 4) {
     Ring r;
-    const int t = threadIdx.x - 6 * 32;
+    const int t = threadIdx.x - 4 * 32;
     for (int step = begin; step < end; ++step) {
       int go = 1;
       if (step - begin >= p.stages) {
@@ -352,48 +401,50 @@ __global__ void __launch_bounds__(GATHER ? kThreadsGather : kThreadsTma)
   }
   if (p.splits > 1) cluster_sync();
 
-  if (warp >= 2 && warp < 6) {
-    const int quarter = warp & 3;  // the 32 lanes of TMEM that this warp may read
-    const int l = quarter * 32 + lane;
-    const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
-    if (p.splits == 1) {
-      const Column col(p, j0 + l);
-      for (int c = 0; c < p.cols && i0 + c < p.m; c += 16) {
-        float v[16];
-        tmem_load16(from + c, v);
-        if (empty || failed) {
+  // All eight warps: a quarter of the lanes each (the one TMEM gives them), and
+  // every other 16 columns.
+  const int quarter = warp & 3, turn = warp >> 2, l = quarter * 32 + lane;
+  const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+  if (p.splits == 1) {
+    const Column col(p, j0 + l);
+    for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 32) {
+      float v[16];
+      tmem_load16(from + c, v);
+      if (empty || failed) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = failed ? nan : 0.f;
-        }
-        col.write(p, i0 + c, v);
+        for (int e = 0; e < 16; ++e) v[e] = failed ? nan : 0.f;
       }
-    } else {
-      // Column c goes to CTA c / share, as [source][column][lane].
-      const int share = p.cols / p.splits;
-      for (int c = 0; c < p.cols; c += 16) {
-        float v[16];
-        tmem_load16(from + c, v);
+      col.write(p, i0 + c, v);
+    }
+  } else {
+    // Column c goes to CTA c / share, as [source][column][lane].
+    const int share = p.cols / p.splits;
+    for (int c = turn * 16; c < p.cols; c += 32) {
+      float v[16];
+      tmem_load16(from + c, v);
+      int to = c / share, at = c - to * share;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int to = (c + e) / share, at = (c + e) % share;
-          st_cluster(cluster_address(tiles + (uint32_t)(((split * share + at) * kTileRows + l) * 4), to),
-                     failed ? nan : empty ? 0.f : v[e]);
+      for (int e = 0; e < 16; ++e) {
+        st_cluster(cluster_address(tiles + (uint32_t)(((split * share + at) * kTileRows + l) * 4), to),
+                   failed ? nan : empty ? 0.f : v[e]);
+        if (++at == share) {
+          at = 0;
+          ++to;
         }
       }
     }
-  }
-  if (p.splits > 1) {
     cluster_sync();
-    if (warp >= 2 && warp < 6) {
-      const int share = p.cols / p.splits, l = (warp & 3) * 32 + lane;
-      const Column col(p, j0 + l);
-      const float *parts = reinterpret_cast<const float *>(dynamic + (tiles - smem_u32(dynamic)));
-      for (int c = 0; c < share; ++c) {
-        float v[1] = {0.f};
-        for (int s = 0; s < p.splits; ++s) v[0] += parts[(s * share + c) * kTileRows + l];
-        const int64_t i = i0 + (int64_t)split * share + c;
-        if (i < p.m) col.write(p, i, v);
+    const Column col(p, j0 + l);
+    const float *parts = reinterpret_cast<const float *>(dynamic + (tiles - smem_u32(dynamic))) + l;
+    constexpr int kAtOnce = 4;
+    for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += 2 * kAtOnce) {
+      float v[kAtOnce] = {};
+      for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e)
+          if (c + e < share) v[e] += parts[(s * share + c + e) * kTileRows];
       }
+      col.write(p, i0 + split * share + c, v, share - c);
     }
   }
   tc_fence_before();
@@ -420,7 +471,7 @@ struct alignas(16) PairShared {
 // leader (r = 0) issues the instructions, which read both CTAs' shared memory
 // and write each CTA's 128 rows of the accumulator to its own TMEM.
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreadsTma) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ char dynamic[];
   __shared__ PairShared sh;
   const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
@@ -439,7 +490,7 @@ __global__ void __launch_bounds__(kThreadsTma) gemm_pair_kernel(const __grid_con
     }
     for (int a = 0; a < kAccumulators; ++a) {
       mbar_init(smem_u32(&sh.sums[a]), 1);
-      mbar_init(smem_u32(&sh.free_[a]), 8);  // four epilogue warps of each CTA
+      mbar_init(smem_u32(&sh.free_[a]), 16);  // eight epilogue warps of each CTA
     }
     mbar_init(smem_u32(&sh.done), 1);
     mbar_init_fence();
@@ -513,7 +564,7 @@ __global__ void __launch_bounds__(kThreadsTma) gemm_pair_kernel(const __grid_con
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, l = quarter * 32 + lane;
+    const int quarter = warp & 3, half_turn = (warp - 2) >> 2, l = quarter * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
     bool ok = true;
     int turn = 0;
@@ -532,7 +583,7 @@ __global__ void __launch_bounds__(kThreadsTma) gemm_pair_kernel(const __grid_con
         if (!ok && lane == 0) fail_pair(&sh.failed);
         tc_fence_after();
       }
-      for (int c = 0; c < p.cols && i0 + c < p.m; c += 16) {
+      for (int c = half_turn * 16; c < p.cols && i0 + c < p.m; c += 32) {
         float v[16];
         if (ok) {
           tmem_load16(from + (uint32_t)(acc * kAccumulatorColumns + c), v);
@@ -732,5 +783,5 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
     cudaGetLastError();
     return cuda_failure((int)e);
   }
-  return launch_op(fn, dim3((unsigned)grid), tma ? kThreadsTma : kThreadsGather, smem, pair ? 2 : p.splits, stream, p);
+  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : kSplitThreads, smem, pair ? 2 : p.splits, stream, p);
 }
