@@ -60,6 +60,7 @@ struct GemmParams {
   const float *scale_a, *scale_b;
   const void *bias, *residual;
   int32_t bias_f32, act, out_type;
+  int32_t pairs;              // 16-bit rows of C start on 4-byte boundaries
   uint32_t idesc;             // without the column count
   int32_t polls;              // of the waits for operands
   uint32_t *timeouts;
@@ -76,8 +77,9 @@ __device__ __forceinline__ float load_typed(const void *p, int64_t i, int type) 
 template <int ACT>
 __device__ __forceinline__ float activated(float y) {
   if (ACT == GEMV_ACT_RELU) return y != y ? y : fmaxf(y, 0.f);
-  if (ACT == GEMV_ACT_SIGMOID) return 1.f / (1.f + expf(-y));
-  if (ACT == GEMV_ACT_SILU) return y / (1.f + expf(-y));
+  // __fdividef: 2 ulp; a denominator above 2^126 gives 0, as it should here
+  if (ACT == GEMV_ACT_SIGMOID) return __fdividef(1.f, 1.f + expf(-y));
+  if (ACT == GEMV_ACT_SILU) return __fdividef(y, 1.f + expf(-y));
   if (ACT == GEMV_ACT_LOG_SIGMOID) return fminf(y, 0.f) - log1pf(expf(-fabsf(y)));
   return y;
 }
@@ -114,14 +116,33 @@ struct Column {
     }
   }
 
+  // 16-bit rows written 4 bytes per lane: lanes of even j take the even rows and
+  // their odd neighbours the odd ones, after exchanging one value of each pair
+  // (needs rows of C on 4-byte boundaries and every lane's column in range).
+  template <int COUNT, class Pack>
+  __device__ __forceinline__ void store_pairs(const GemmParams &p, int64_t i0, int rows, const float (&y)[COUNT],
+                                              Pack pack) const {
+    const int odd = (int)(j & 1);
+    uint32_t *c = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.C) + (i0 + odd) * p.ldc + (j - odd));
+    const int64_t step = p.ldc;  // two rows, in 4-byte words
+    const bool whole = rows == COUNT;
+#pragma unroll
+    for (int e = 0; e < COUNT; e += 2) {
+      const uint32_t mine = pack(y[e], y[e + 1]);  // rows e (low half) and e + 1 of this column
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+      const uint32_t w = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+      if (whole || e + odd < rows) c[(e / 2) * step] = w;
+    }
+  }
+
   // rows i0 .. of C from their sums: as many of the COUNT as there are, at most `most`
   template <int COUNT>
   __device__ __forceinline__ void write(const GemmParams &p, int64_t i0, const float (&sum)[COUNT],
                                         int most = COUNT) const {
-    if (!live) return;
+    if (!live && !p.pairs) return;
     const int rows = p.m - i0 < most ? (int)(p.m - i0) : most;
     float res[COUNT];
-    if (p.residual) {
+    if (p.residual && live) {
       if (p.out_type == GEMV_TYPE_F32) {
         const float *r = static_cast<const float *>(p.residual) + i0 * p.ldr + j;
 #pragma unroll
@@ -153,10 +174,18 @@ struct Column {
     else if (p.act == GEMV_ACT_SIGMOID) activate_all<GEMV_ACT_SIGMOID>(y);
     else if (p.act == GEMV_ACT_SILU) activate_all<GEMV_ACT_SILU>(y);
     else if (p.act == GEMV_ACT_LOG_SIGMOID) activate_all<GEMV_ACT_LOG_SIGMOID>(y);
-    if (p.residual) {
+    if (p.residual && live) {
 #pragma unroll
       for (int e = 0; e < COUNT; ++e) y[e] += res[e];
     }
+    if (p.pairs && __all_sync(0xffffffffu, live)) {
+      if (p.out_type == GEMV_TYPE_F16)
+        store_pairs(p, i0, rows, y, [](float a, float b) { return Elem<GEMV_TYPE_F16>::pair(a, b); });
+      else
+        store_pairs(p, i0, rows, y, [](float a, float b) { return Elem<GEMV_TYPE_BF16>::pair(a, b); });
+      return;
+    }
+    if (!live) return;
     if (p.out_type == GEMV_TYPE_F32) store<float>(p, i0, rows, y, [](float v) { return v; });
     else if (p.out_type == GEMV_TYPE_F16) store<uint16_t>(p, i0, rows, y, [](float v) { return F16::from_float(v); });
     else store<uint16_t>(p, i0, rows, y, [](float v) { return BF16::from_float(v); });
@@ -165,13 +194,16 @@ struct Column {
 
 // --------------------------------------------------------------------- waits --
 
-// Polls a barrier until its phase `parity` completes.  False if the polls run
-// out or another role of this CTA has given up.
+// Polls a barrier until its phase `parity` completes, the whole warp together:
+// the issuing loops stay uniform, so that the operands of the matrix and copy
+// instructions live in uniform registers (issued from a lone thread's loop,
+// one tcgen05.mma took 95 cycles to issue: 590 us against 8192 x 14336 x 4096's
+// ... ).  False if the polls run out or another role of this CTA has given up.
 template <bool CLUSTER>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int64_t polls) {
   while (polls > 0) {
-    if (CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity)) return true;
-    if (*failed) return false;
+    if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *failed != 0)) return false;
     --polls;
   }
   *failed = 1;
@@ -326,31 +358,26 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   wait_for_predecessor();
 
   if (!GATHER && warp == 0) {
-    if (lane == 0) {
-      Ring r;
-      int step = begin;
-      for (; step < end; ++step) {
-        if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
+    const bool elected = elect_one();
+    Ring r;
+    int step = begin;
+    for (; step < end; ++step) {
+      if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
+      if (elected) {
         const uint32_t bar = smem_u32(&sh.full[r.stage]), at = tiles + r.stage * stage_bytes;
         mbar_expect_tx(bar, stage_bytes);
         const int32_t x = step * (E4M3 ? kRowBytes : kRowBytes / 2);
         tma_load<1>(at, &p.map_b, x, (int32_t)j0, bar);
         tma_load<1>(at + kTileBytes, &p.map_a, x, (int32_t)i0, bar);
-        r.next(p.stages);
       }
-      sh.issued = step - begin;
+      r.next(p.stages);
     }
-    __syncwarp();
+    if (elected) sh.issued = step - begin;
   } else if (GATHER && warp >= 4) {
     Ring r;
     const int t = threadIdx.x - 4 * 32;
     for (int step = begin; step < end; ++step) {
-      int go = 1;
-      if (step - begin >= p.stages) {
-        if (lane == 0) go = wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls);
-        go = __shfl_sync(0xffffffffu, go, 0);
-      }
-      if (!go) break;
+      if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
       const uint32_t at = tiles + r.stage * stage_bytes;
       const int64_t kb = (int64_t)step * kRowBytes;
       gather_rows<8>(p.B, p.ldb_bytes, j0, p.n, kb, p.k_bytes, kTileRows, at, t);
@@ -361,28 +388,27 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
       r.next(p.stages);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      Ring r;
-      const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
-      for (int step = begin; step < end; ++step) {
-        if (!wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls)) break;
-        tc_fence_after();
-        const uint32_t at = tiles + r.stage * stage_bytes;
-        const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
+    const bool elected = elect_one();
+    Ring r;
+    const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+    for (int step = begin; step < end; ++step) {
+      if (!wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls)) break;
+      tc_fence_after();
+      const uint32_t at = tiles + r.stage * stage_bytes;
+      const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
+      if (elected) {
 #pragma unroll
-        for (int s = 0; s < kMmaSteps; ++s)
-          tc_mma<1, E4M3>(tmem, db + 2 * s, da + 2 * s, idesc, step > begin || s > 0);
+        for (int s = 0; s < kMmaSteps; ++s) tc_mma<1, E4M3>(tmem, db + 2 * s, da + 2 * s, idesc, step > begin || s > 0);
         tc_commit<1>(smem_u32(&sh.empty[r.stage]));
-        r.next(p.stages);
       }
-      // Also after a wait that gave up: the instructions issued so far read
-      // shared memory until they complete.
-      tc_commit<1>(smem_u32(&sh.done));
-      int zero = 0;
-      wait_for<false>(smem_u32(&sh.done), 0, &zero, kPolls);
-      if (sh.failed) atomicAdd(p.timeouts, 1u);
+      r.next(p.stages);
     }
-    __syncwarp();
+    // Also after a wait that gave up: the instructions issued so far read
+    // shared memory until they complete.
+    if (elected) tc_commit<1>(smem_u32(&sh.done));
+    int none = 0;
+    wait_for<false>(smem_u32(&sh.done), 0, &none, kPolls);
+    if (sh.failed && elected) atomicAdd(p.timeouts, 1u);
   }
   tc_fence_before();
   __syncthreads();  // the sums are complete; shared memory is free
@@ -390,11 +416,12 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   const float nan = __int_as_float(0x7fc00000);
   const bool empty = begin == end, failed = sh.failed != 0;
   if (!GATHER && failed) {  // copies in flight land before their memory is used again
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
       int none = 0;
       Ring d;
       for (int s = 0; s < sh.issued; ++s, d.next(p.stages))
-        if (s + p.stages >= sh.issued && !wait_for<false>(smem_u32(&sh.full[d.stage]), d.phase, &none, kPolls))
+        if (s + p.stages >= sh.issued && !wait_for<false>(smem_u32(&sh.full[d.stage]), d.phase, &none, kPolls) &&
+            lane == 0)
           atomicOr(p.timeouts, kDrainTimeoutBit);
     }
     __syncthreads();
@@ -471,7 +498,7 @@ struct alignas(16) PairShared {
 // leader (r = 0) issues the instructions, which read both CTAs' shared memory
 // and write each CTA's 128 rows of the accumulator to its own TMEM.
 template <bool E4M3>
-__global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ char dynamic[];
   __shared__ PairShared sh;
   const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;
@@ -507,33 +534,36 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
   wait_for_predecessor();
 
   if (warp == 0) {
-    if (lane == 0) {
-      Ring r;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int64_t t = first; ok && t < count; t += pairs) {
-        int tn, tm;
-        tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
-        const int32_t j0 = tn * (2 * kTileRows) + rank * kTileRows, i0 = tm * p.cols + rank * half;
-        for (int step = 0; step < p.steps; ++step) {
-          ok = issued < p.stages || wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls);
-          if (!ok) break;
+    const bool elected = elect_one();
+    Ring r;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int64_t t = first; ok && t < count; t += pairs) {
+      int tn, tm;
+      tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
+      const int32_t j0 = tn * (2 * kTileRows) + rank * kTileRows, i0 = tm * p.cols + rank * half;
+      for (int step = 0; step < p.steps; ++step) {
+        ok = issued < p.stages || wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls);
+        if (!ok) break;
+        if (elected) {
           const uint32_t full = smem_u32(&sh.full[r.stage]), at = tiles + r.stage * stage_bytes;
           if (rank == 0) mbar_expect_tx(full, 2 * stage_bytes);
           const uint32_t bar = cluster_address(full, 0);
           const int32_t x = step * (E4M3 ? kRowBytes : kRowBytes / 2);
           tma_load<2>(at, &p.map_b, x, j0, bar);
           tma_load<2>(at + kTileBytes, &p.map_a, x, i0, bar);
-          ++issued;
-          r.next(p.stages);
         }
+        ++issued;
+        r.next(p.stages);
       }
+    }
+    if (elected) {
       sh.issued = issued;
       if (!ok) fail_pair(&sh.failed);
     }
-    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool elected = elect_one();
       Ring r;
       const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(2 * kTileRows >> 4) << 24);
       bool ok = true;
@@ -545,24 +575,27 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
              wait_for<true>(smem_u32(&sh.free_[acc]), ((turn >> 1) & 1) ^ 1, &sh.failed, kPolls);
         tc_fence_after();
         for (int step = 0; ok && step < p.steps; ++step) {
-          ok = wait_for<true>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls);
+          ok = wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls);
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = tiles + r.stage * stage_bytes;
           const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
+          if (elected) {
 #pragma unroll
-          for (int s = 0; s < kMmaSteps; ++s) tc_mma<2, E4M3>(d, db + 2 * s, da + 2 * s, idesc, step > 0 || s > 0);
-          tc_commit<2>(smem_u32(&sh.empty[r.stage]));
+            for (int s = 0; s < kMmaSteps; ++s) tc_mma<2, E4M3>(d, db + 2 * s, da + 2 * s, idesc, step > 0 || s > 0);
+            tc_commit<2>(smem_u32(&sh.empty[r.stage]));
+          }
           r.next(p.stages);
         }
-        if (ok) tc_commit<2>(smem_u32(&sh.sums[acc]));
+        if (ok && elected) tc_commit<2>(smem_u32(&sh.sums[acc]));
       }
-      if (!ok) fail_pair(&sh.failed);
-      // Also after a wait that gave up: the instructions issued so far read
-      // both CTAs' shared memory until they complete.
-      tc_commit<2>(smem_u32(&sh.done));
+      if (elected) {
+        if (!ok) fail_pair(&sh.failed);
+        // Also after a wait that gave up: the instructions issued so far read
+        // both CTAs' shared memory until they complete.
+        tc_commit<2>(smem_u32(&sh.done));
+      }
     }
-    __syncwarp();
   } else {
     const int quarter = warp & 3, half_turn = (warp - 2) >> 2, l = quarter * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -575,23 +608,33 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
       const int64_t i0 = (int64_t)tm * p.cols;
       const Column col(p, (int64_t)tn * (2 * kTileRows) + rank * kTileRows + l);
       if (ok) {
-        int go = 0;
         // a whole product: some polls for each of its steps
-        if (lane == 0)
-          go = wait_for<true>(smem_u32(&sh.sums[acc]), (turn >> 1) & 1, &sh.failed, kPolls + 64ll * p.steps);
-        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+        ok = wait_for<false>(smem_u32(&sh.sums[acc]), (turn >> 1) & 1, &sh.failed, kPolls + 64ll * p.steps);
         if (!ok && lane == 0) fail_pair(&sh.failed);
         tc_fence_after();
       }
-      for (int c = half_turn * 16; c < p.cols && i0 + c < p.m; c += 32) {
-        float v[16];
+      const uint32_t at = from + (uint32_t)(acc * kAccumulatorColumns);
+      const int end = p.cols < p.m - i0 ? p.cols : (int)(p.m - i0);
+      // 16 columns are requested while the 16 before them are written
+      float even[16], odd[16];
+      auto request = [&](int c, float (&v)[16]) {
+        if (ok && c < end) tmem_request16(at + c, v);
+      };
+      auto write = [&](int c, float (&v)[16], float (&next)[16]) {
+        if (c >= end) return;
         if (ok) {
-          tmem_load16(from + (uint32_t)(acc * kAccumulatorColumns + c), v);
+          tmem_arrived16(v);
+          request(c + 32, next);
         } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fc00000);
         }
         col.write(p, i0 + c, v);
+      };
+      request(half_turn * 16, even);
+      for (int c = half_turn * 16; c < end; c += 64) {
+        write(c, even, odd);
+        write(c + 32, odd, even);
       }
       tc_fence_before();
       __syncwarp();
@@ -600,16 +643,16 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
   }
   __syncthreads();
   // Every instruction issued has completed, in both CTAs' view.
-  if (warp == 1 && lane == 0) {
+  if (warp == 1) {
     int none = 0;
-    wait_for<true>(smem_u32(&sh.done), 0, &none, kPolls);
+    wait_for<false>(smem_u32(&sh.done), 0, &none, kPolls);
   }
   __syncthreads();
   cluster_sync();
-  if (rank == 0 && threadIdx.x == 0) {
+  if (rank == 0 && warp == 0) {
     const int other_failed = ld_cluster(cluster_address(smem_u32(&sh.failed), 1));
     if (sh.failed || other_failed) {
-      atomicAdd(p.timeouts, 1u);
+      if (lane == 0) atomicAdd(p.timeouts, 1u);
       // Copies in flight land before the CTAs leave: the barriers of the last
       // steps are completed by what each CTA did start.
       const int64_t mine = sh.issued, other = ld_cluster64(cluster_address(smem_u32(&sh.issued), 1));
@@ -618,10 +661,10 @@ __global__ void __launch_bounds__(kPairThreads) gemm_pair_kernel(const __grid_co
       for (int64_t s = 0; s < most; ++s, d.next(p.stages)) {
         if (s + p.stages < most) continue;
         const uint32_t bar = smem_u32(&sh.full[d.stage]);
-        if (s >= mine) mbar_expect_tx(bar, stage_bytes);
-        else if (s >= other) mbar_complete_tx(bar, stage_bytes);
+        if (lane == 0 && s >= mine) mbar_expect_tx(bar, stage_bytes);
+        else if (lane == 0 && s >= other) mbar_complete_tx(bar, stage_bytes);
         int none = 0;
-        if (!wait_for<true>(bar, d.phase, &none, kPolls)) atomicOr(p.timeouts, kDrainTimeoutBit);
+        if (!wait_for<false>(bar, d.phase, &none, kPolls) && lane == 0) atomicOr(p.timeouts, kDrainTimeoutBit);
       }
     }
   }
@@ -757,6 +800,7 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   p.scale_a = ep.scale_a; p.scale_b = ep.scale_b; p.bias = ep.bias; p.residual = ep.residual;
   p.bias_f32 = ep.bias_dtype == GEMV_TYPE_F32 ? 1 : 0;
   p.act = ep.activation; p.out_type = out_dtype;
+  p.pairs = oe == 2 && ((uintptr_t)C | (uintptr_t)(ldc * oe)) % 4 == 0 ? 1 : 0;
   // fp32 accumulators (bit 4); operand types in bits 7 and 10: 0 fp16 or e4m3, 1 bf16
   p.idesc = (1u << 4) | (dtype == GEMV_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
   p.polls = take_wait_budget(kPolls);
