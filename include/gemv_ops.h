@@ -113,7 +113,8 @@ typedef struct gemm_epilogue {
  *             _F32 for GEMV_TYPE_E4M3.
  *  epilogue   may be NULL (identity).
  *
- * 0 <= m, n, k <= INT32_MAX; m == 0 or n == 0 launches nothing, k == 0 gives the
+ * 0 <= m, n, k <= INT32_MAX, and rows of C and of the residual (m > 1) start less
+ * than 4 GiB apart; m == 0 or n == 0 launches nothing, k == 0 gives the
  * epilogue of 0.  Elements between k and a row stride are never used.  Any
  * element alignment and stride work; operands whose base and row stride in
  * bytes are multiples of 16 are copied by TMA.  Products and sums run on the

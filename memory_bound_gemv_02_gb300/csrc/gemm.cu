@@ -38,7 +38,8 @@ constexpr int kTileBytes = kTileRows * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
 constexpr int kPolls = 1 << 20;                  // polls of one wait before it gives up
-constexpr int kSplitThreads = 256, kPairThreads = 320;
+constexpr int kEpilogueWarps = 8;                 // of gemm_pair_kernel
+constexpr int kSplitThreads = 256, kPairThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kGatherWarps = 4;                  // warps 4 to 7
 constexpr int kSplitBand = 16, kPairBand = 8;    // tiles along n that run side by side
 constexpr int kAccumulators = 2;                 // of gemm_pair_kernel
@@ -83,122 +84,157 @@ __device__ __forceinline__ float activated(float y) {
   if (ACT == GEMV_ACT_LOG_SIGMOID) return fminf(y, 0.f) - log1pf(expf(-fabsf(y)));
   return y;
 }
-template <int ACT, int COUNT>
-__device__ __forceinline__ void activate_all(float (&y)[COUNT]) {
-#pragma unroll
-  for (int c = 0; c < COUNT; ++c) y[c] = activated<ACT>(y[c]);
+// A value that the compiler keeps in a register: what the epilogue asks for in
+// every turn (a load and a branch on a kernel parameter took about 25 cycles
+// each, half of the epilogue's time).
+template <class T>
+__device__ __forceinline__ T in_register(T v) {
+  asm volatile("" : "+r"(v));
+  return v;
+}
+template <class T>
+__device__ __forceinline__ T *in_register(T *v) {
+  asm volatile("" : "+l"(v));
+  return v;
 }
 
-// One thread's column j of C.  The epilogue's choices are made once for COUNT
-// rows and each is a loop without branches: with a few warps per SM, a row at
-// a time left every instruction's latency exposed (49 us per 256 x 256 tile).
+// The epilogue of one launch, and of one thread's column j of C.  ACT is its
+// activation: the caller's loop over the columns is compiled for each.
+template <int ACT>
 struct Column {
-  int64_t j;
-  bool live;
+  static constexpr int kF16 = 1, kF32 = 2, kPairs = 4;  // bits of `how`
+  int32_t m, how;
+  uint32_t pitch, res_pitch;
+  const float *scale_a;
+  char *c;
+  const char *res;
+  bool live, odd, together;
   float factor, shift;
-  __device__ Column(const GemmParams &p, int64_t j_) : j(j_), live(j_ < p.n), factor(p.alpha), shift(0.f) {
+
+  __device__ explicit Column(const GemmParams &p)
+      : m(in_register(p.m)),
+        how(in_register((p.out_type == GEMV_TYPE_F16 ? kF16 : p.out_type == GEMV_TYPE_F32 ? kF32 : 0) |
+                        (p.pairs ? kPairs : 0))),
+        scale_a(in_register(p.scale_a)) {
+    const uint32_t es = p.out_type == GEMV_TYPE_F32 ? 4 : 2;
+    pitch = in_register((uint32_t)p.ldc * es);
+    res_pitch = in_register((uint32_t)p.ldr * es);
+  }
+
+  __device__ __forceinline__ void begin(const GemmParams &p, int64_t j) {
+    const uint32_t es = how & kF32 ? 4 : 2;
+    live = j < p.n;
+    odd = (j & 1) != 0;
+    together = (how & kPairs) && __all_sync(0xffffffffu, live);
+    factor = p.alpha;
+    shift = 0.f;
+    c = static_cast<char *>(p.C) + j * es;
+    res = p.residual ? static_cast<const char *>(p.residual) + j * es : nullptr;
     if (!live) return;
     if (p.scale_b) factor *= p.scale_b[j];
     if (p.bias) shift = p.beta * load_typed(p.bias, j, p.bias_f32 ? GEMV_TYPE_F32 : p.out_type);
   }
 
+  // Element e of rows `pitch` bytes apart.
+  template <class T>
+  static __device__ __forceinline__ T *row(const char *base, uint32_t pitch, int e) {
+    return reinterpret_cast<T *>(const_cast<char *>(base) + (uint64_t)pitch * (uint32_t)e);
+  }
+
   template <class Out, int COUNT, class Convert>
-  __device__ __forceinline__ void store(const GemmParams &p, int64_t i0, int rows, const float (&y)[COUNT],
-                                        Convert convert) const {
-    Out *c = static_cast<Out *>(p.C) + i0 * p.ldc + j;
-    if (rows >= COUNT) {
+  __device__ __forceinline__ void store(char *at, int rows, const float (&y)[COUNT], Convert convert) const {
 #pragma unroll
-      for (int e = 0; e < COUNT; ++e) c[e * p.ldc] = convert(y[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < COUNT; ++e)
-        if (e < rows) c[e * p.ldc] = convert(y[e]);
-    }
+    for (int e = 0; e < COUNT; ++e)
+      if (e < rows) *row<Out>(at, pitch, e) = convert(y[e]);
   }
 
   // 16-bit rows written 4 bytes per lane: lanes of even j take the even rows and
   // their odd neighbours the odd ones, after exchanging one value of each pair
   // (needs rows of C on 4-byte boundaries and every lane's column in range).
   template <int COUNT, class Pack>
-  __device__ __forceinline__ void store_pairs(const GemmParams &p, int64_t i0, int rows, const float (&y)[COUNT],
-                                              Pack pack) const {
-    const int odd = (int)(j & 1);
-    uint32_t *c = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.C) + (i0 + odd) * p.ldc + (j - odd));
-    const int64_t step = p.ldc;  // two rows, in 4-byte words
-    const bool whole = rows == COUNT;
+  __device__ __forceinline__ void store_pairs(char *at, int rows, const float (&y)[COUNT], Pack pack) const {
+    const uint32_t pick = odd ? 0x3276u : 0x5410u;  // odd: both high halves, the neighbour's first; even: both low ones
+    at += odd ? (int64_t)pitch - 2 : 0;
+    if (rows == COUNT) {
 #pragma unroll
-    for (int e = 0; e < COUNT; e += 2) {
-      const uint32_t mine = pack(y[e], y[e + 1]);  // rows e (low half) and e + 1 of this column
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-      const uint32_t w = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-      if (whole || e + odd < rows) c[(e / 2) * step] = w;
+      for (int e = 0; e < COUNT; e += 2) {
+        const uint32_t mine = pack(y[e], y[e + 1]);  // rows e (low half) and e + 1 of this column
+        *row<uint32_t>(at, pitch, e) = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < COUNT; e += 2) {
+        const uint32_t mine = pack(y[e], y[e + 1]);
+        const uint32_t w = __byte_perm(mine, __shfl_xor_sync(0xffffffffu, mine, 1), pick);
+        if (e + odd < rows) *row<uint32_t>(at, pitch, e) = w;
+      }
     }
   }
 
   // rows i0 .. of C from their sums: as many of the COUNT as there are, at most `most`
   template <int COUNT>
-  __device__ __forceinline__ void write(const GemmParams &p, int64_t i0, const float (&sum)[COUNT],
-                                        int most = COUNT) const {
-    if (!live && !p.pairs) return;
-    const int rows = p.m - i0 < most ? (int)(p.m - i0) : most;
-    float res[COUNT];
-    if (p.residual && live) {
-      if (p.out_type == GEMV_TYPE_F32) {
-        const float *r = static_cast<const float *>(p.residual) + i0 * p.ldr + j;
+  __device__ __forceinline__ void write(int i0, const float (&sum)[COUNT], int most = COUNT) const {
+    const int rows = m - i0 < most ? m - i0 : most;
+    float y[COUNT];
+    if (scale_a) {
+      const float *sa = scale_a + i0;
 #pragma unroll
-        for (int e = 0; e < COUNT; ++e) res[e] = e < rows ? r[e * p.ldr] : 0.f;
+      for (int e = 0; e < COUNT; ++e) y[e] = fmaf(sum[e], factor * (e < rows ? sa[e] : 0.f), shift);
+    } else {
+#pragma unroll
+      for (int e = 0; e < COUNT; ++e) y[e] = fmaf(sum[e], factor, shift);
+    }
+#pragma unroll
+    for (int e = 0; e < COUNT; ++e) y[e] = activated<ACT>(y[e]);
+    if (res && live) {
+      const char *r = res + (int64_t)i0 * res_pitch;
+      if (how & kF32) {
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) y[e] += e < rows ? *row<float>(r, res_pitch, e) : 0.f;
       } else {
-        const uint16_t *r = static_cast<const uint16_t *>(p.residual) + i0 * p.ldr + j;
         uint16_t raw[COUNT];
 #pragma unroll
-        for (int e = 0; e < COUNT; ++e) raw[e] = e < rows ? r[e * p.ldr] : 0;
-        if (p.out_type == GEMV_TYPE_F16) {
+        for (int e = 0; e < COUNT; ++e) raw[e] = e < rows ? *row<uint16_t>(r, res_pitch, e) : 0;
+        if (how & kF16) {
 #pragma unroll
-          for (int e = 0; e < COUNT; ++e) res[e] = F16::to_float(raw[e]);
+          for (int e = 0; e < COUNT; ++e) y[e] += F16::to_float(raw[e]);
         } else {
 #pragma unroll
-          for (int e = 0; e < COUNT; ++e) res[e] = BF16::to_float(raw[e]);
+          for (int e = 0; e < COUNT; ++e) y[e] += BF16::to_float(raw[e]);
         }
       }
     }
-    float y[COUNT];
-#pragma unroll
-    for (int e = 0; e < COUNT; ++e) y[e] = sum[e] * factor;
-    if (p.scale_a) {
-#pragma unroll
-      for (int e = 0; e < COUNT; ++e) y[e] *= e < rows ? p.scale_a[i0 + e] : 1.f;
+    char *at = c + (int64_t)i0 * pitch;
+    if (together) {
+      if (how & kF16) store_pairs(at, rows, y, [](float a, float b) { return Elem<GEMV_TYPE_F16>::pair(a, b); });
+      else store_pairs(at, rows, y, [](float a, float b) { return Elem<GEMV_TYPE_BF16>::pair(a, b); });
+    } else if (live) {
+      if (how & kF32) store<float>(at, rows, y, [](float v) { return v; });
+      else if (how & kF16) store<uint16_t>(at, rows, y, [](float v) { return F16::from_float(v); });
+      else store<uint16_t>(at, rows, y, [](float v) { return BF16::from_float(v); });
     }
-#pragma unroll
-    for (int e = 0; e < COUNT; ++e) y[e] += shift;
-    if (p.act == GEMV_ACT_RELU) activate_all<GEMV_ACT_RELU>(y);
-    else if (p.act == GEMV_ACT_SIGMOID) activate_all<GEMV_ACT_SIGMOID>(y);
-    else if (p.act == GEMV_ACT_SILU) activate_all<GEMV_ACT_SILU>(y);
-    else if (p.act == GEMV_ACT_LOG_SIGMOID) activate_all<GEMV_ACT_LOG_SIGMOID>(y);
-    if (p.residual && live) {
-#pragma unroll
-      for (int e = 0; e < COUNT; ++e) y[e] += res[e];
-    }
-    if (p.pairs && __all_sync(0xffffffffu, live)) {
-      if (p.out_type == GEMV_TYPE_F16)
-        store_pairs(p, i0, rows, y, [](float a, float b) { return Elem<GEMV_TYPE_F16>::pair(a, b); });
-      else
-        store_pairs(p, i0, rows, y, [](float a, float b) { return Elem<GEMV_TYPE_BF16>::pair(a, b); });
-      return;
-    }
-    if (!live) return;
-    if (p.out_type == GEMV_TYPE_F32) store<float>(p, i0, rows, y, [](float v) { return v; });
-    else if (p.out_type == GEMV_TYPE_F16) store<uint16_t>(p, i0, rows, y, [](float v) { return F16::from_float(v); });
-    else store<uint16_t>(p, i0, rows, y, [](float v) { return BF16::from_float(v); });
   }
 };
+
+// run(Column<act>) for the launch's activation.
+template <class Run>
+__device__ __forceinline__ void with_column(const GemmParams &p, Run run) {
+  switch (p.act) {
+    case GEMV_ACT_RELU: run(Column<GEMV_ACT_RELU>(p)); break;
+    case GEMV_ACT_SIGMOID: run(Column<GEMV_ACT_SIGMOID>(p)); break;
+    case GEMV_ACT_SILU: run(Column<GEMV_ACT_SILU>(p)); break;
+    case GEMV_ACT_LOG_SIGMOID: run(Column<GEMV_ACT_LOG_SIGMOID>(p)); break;
+    default: run(Column<GEMV_ACT_NONE>(p)); break;
+  }
+}
 
 // --------------------------------------------------------------------- waits --
 
 // Polls a barrier until its phase `parity` completes, the whole warp together:
 // the issuing loops stay uniform, so that the operands of the matrix and copy
 // instructions live in uniform registers (issued from a lone thread's loop,
-// one tcgen05.mma took 95 cycles to issue: 590 us against 8192 x 14336 x 4096's
-// ... ).  False if the polls run out or another role of this CTA has given up.
+// one tcgen05.mma took about 95 cycles to issue and 8192 x 14336 x 4096 bf16
+// 590 us instead of 503).  False if the polls run out or another role of this CTA has given up.
 template <bool CLUSTER>
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int64_t polls) {
   while (polls > 0) {
@@ -227,16 +263,28 @@ struct Ring {
   }
 };
 
+// Whether the next stage's operands are there already: asked before this
+// stage's instructions are issued, so that the answer's latency overlaps them.
+__device__ __forceinline__ bool peek(const uint64_t *full, Ring r, int stages, int polls) {
+  r.next(stages);
+  return polls > 0 && __all_sync(0xffffffffu, mbar_test(smem_u32(&full[r.stage]), r.phase));
+}
+
 // Tile number -> tile along n and along m: bands of `band` tiles along n,
 // walked along m, so that the tiles computed at one time share few operand
 // rows and the L2 serves the rest of their reads.
-__device__ __forceinline__ void tile_at(int64_t t, int tiles_n, int tiles_m, int band, int *tn, int *tm) {
+__device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int band, int *tn, int *tm) {
+  if (tiles_n <= band) {  // one band
+    *tm = t / tiles_n;
+    *tn = t - *tm * tiles_n;
+    return;
+  }
   const int64_t whole = (int64_t)band * tiles_m;
-  const int first = (int)(t / whole) * band;
+  const int number = whole > t ? 0 : t / (int)whole;  // whole fits 32 bits where t reaches it
+  const int first = number * band, in = t - number * (int)whole;
   const int width = tiles_n - first < band ? tiles_n - first : band;
-  const int in = (int)(t % whole);
   *tm = in / width;
-  *tn = first + in % width;
+  *tn = first + in - *tm * width;
 }
 
 // ------------------------------------------------------- operands without TMA --
@@ -391,9 +439,11 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     const bool elected = elect_one();
     Ring r;
     const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(kTileRows >> 4) << 24);
+    bool ready = false;
     for (int step = begin; step < end; ++step) {
-      if (!wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls)) break;
+      if (!ready && !wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls)) break;
       tc_fence_after();
+      ready = peek(sh.full, r, p.stages, p.polls);
       const uint32_t at = tiles + r.stage * stage_bytes;
       const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
       if (elected) {
@@ -433,16 +483,19 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   const int quarter = warp & 3, turn = warp >> 2, l = quarter * 32 + lane;
   const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
   if (p.splits == 1) {
-    const Column col(p, j0 + l);
-    for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 32) {
-      float v[16];
-      tmem_load16(from + c, v);
-      if (empty || failed) {
+    with_column(p, [&](auto col) {
+      col.begin(p, j0 + l);
+#pragma unroll 1
+      for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 32) {
+        float v[16];
+        tmem_load16(from + c, v);
+        if (empty || failed) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = failed ? nan : 0.f;
+          for (int e = 0; e < 16; ++e) v[e] = failed ? nan : 0.f;
+        }
+        col.write((int)i0 + c, v);
       }
-      col.write(p, i0 + c, v);
-    }
+    });
   } else {
     // Column c goes to CTA c / share, as [source][column][lane].
     const int share = p.cols / p.splits;
@@ -461,18 +514,21 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
       }
     }
     cluster_sync();
-    const Column col(p, j0 + l);
     const float *parts = reinterpret_cast<const float *>(dynamic + (tiles - smem_u32(dynamic))) + l;
-    constexpr int kAtOnce = 4;
-    for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += 2 * kAtOnce) {
-      float v[kAtOnce] = {};
-      for (int s = 0; s < p.splits; ++s) {
+    with_column(p, [&](auto col) {
+      col.begin(p, j0 + l);
+      constexpr int kAtOnce = 4;
+#pragma unroll 1
+      for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += 2 * kAtOnce) {
+        float v[kAtOnce] = {};
+        for (int s = 0; s < p.splits; ++s) {
 #pragma unroll
-        for (int e = 0; e < kAtOnce; ++e)
-          if (c + e < share) v[e] += parts[(s * share + c + e) * kTileRows];
+          for (int e = 0; e < kAtOnce; ++e)
+            if (c + e < share) v[e] += parts[(s * share + c + e) * kTileRows];
+        }
+        col.write((int)i0 + split * share + c, v, share - c);
       }
-      col.write(p, i0 + split * share + c, v, share - c);
-    }
+    });
   }
   tc_fence_before();
   __syncthreads();
@@ -506,7 +562,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
   const uint32_t stage_bytes = kTileBytes + (uint32_t)half * kRowBytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
-  const int64_t count = (int64_t)p.tiles_n * p.tiles_m, pairs = gridDim.x / 2, first = blockIdx.x / 2;
+  const int count = p.tiles_n * p.tiles_m, pairs = gridDim.x / 2, first = blockIdx.x / 2;
 
   if (threadIdx.x == 0) {
     sh.failed = 0;
@@ -517,7 +573,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
     }
     for (int a = 0; a < kAccumulators; ++a) {
       mbar_init(smem_u32(&sh.sums[a]), 1);
-      mbar_init(smem_u32(&sh.free_[a]), 16);  // eight epilogue warps of each CTA
+      mbar_init(smem_u32(&sh.free_[a]), 2 * kEpilogueWarps);  // of both CTAs
     }
     mbar_init(smem_u32(&sh.done), 1);
     mbar_init_fence();
@@ -538,7 +594,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
     Ring r;
     int64_t issued = 0;
     bool ok = true;
-    for (int64_t t = first; ok && t < count; t += pairs) {
+    for (int t = first; ok && t < count; t += pairs) {
       int tn, tm;
       tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
       const int32_t j0 = tn * (2 * kTileRows) + rank * kTileRows, i0 = tm * p.cols + rank * half;
@@ -566,18 +622,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
       const bool elected = elect_one();
       Ring r;
       const uint32_t idesc = p.idesc | ((uint32_t)(p.cols >> 3) << 17) | ((uint32_t)(2 * kTileRows >> 4) << 24);
-      bool ok = true;
+      bool ok = true, ready = false;
       int turn = 0;
-      for (int64_t t = first; ok && t < count; t += pairs, ++turn) {
+      for (int t = first; ok && t < count; t += pairs, ++turn) {
         const int acc = turn & 1;
         const uint32_t d = tmem + (uint32_t)(acc * kAccumulatorColumns);
         ok = turn < kAccumulators ||
              wait_for<true>(smem_u32(&sh.free_[acc]), ((turn >> 1) & 1) ^ 1, &sh.failed, kPolls);
         tc_fence_after();
         for (int step = 0; ok && step < p.steps; ++step) {
-          ok = wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls);
+          ok = ready || wait_for<false>(smem_u32(&sh.full[r.stage]), r.phase, &sh.failed, p.polls);
           if (!ok) break;
           tc_fence_after();
+          ready = peek(sh.full, r, p.stages, p.polls);
           const uint32_t at = tiles + r.stage * stage_bytes;
           const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
           if (elected) {
@@ -597,49 +654,39 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
       }
     }
   } else {
-    const int quarter = warp & 3, half_turn = (warp - 2) >> 2, l = quarter * 32 + lane;
+    const int quarter = warp & 3, part = (warp - 2) >> 2, l = quarter * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
-    bool ok = true;
-    int turn = 0;
-    for (int64_t t = first; t < count; t += pairs, ++turn) {
-      const int acc = turn & 1;
-      int tn, tm;
-      tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
-      const int64_t i0 = (int64_t)tm * p.cols;
-      const Column col(p, (int64_t)tn * (2 * kTileRows) + rank * kTileRows + l);
-      if (ok) {
-        // a whole product: some polls for each of its steps
-        ok = wait_for<false>(smem_u32(&sh.sums[acc]), (turn >> 1) & 1, &sh.failed, kPolls + 64ll * p.steps);
-        if (!ok && lane == 0) fail_pair(&sh.failed);
-        tc_fence_after();
-      }
-      const uint32_t at = from + (uint32_t)(acc * kAccumulatorColumns);
-      const int end = p.cols < p.m - i0 ? p.cols : (int)(p.m - i0);
-      // 16 columns are requested while the 16 before them are written
-      float even[16], odd[16];
-      auto request = [&](int c, float (&v)[16]) {
-        if (ok && c < end) tmem_request16(at + c, v);
-      };
-      auto write = [&](int c, float (&v)[16], float (&next)[16]) {
-        if (c >= end) return;
+    with_column(p, [&](auto col) {
+      bool ok = true;
+      int turn = 0;
+      for (int t = first; t < count; t += pairs, ++turn) {
+        const int acc = turn & 1;
+        int tn, tm;
+        tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
+        const int i0 = tm * p.cols, end = min(p.cols, p.m - i0);
+        col.begin(p, (int64_t)tn * (2 * kTileRows) + rank * kTileRows + l);
         if (ok) {
-          tmem_arrived16(v);
-          request(c + 32, next);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fc00000);
+          // a whole product: some polls for each of its steps
+          ok = wait_for<false>(smem_u32(&sh.sums[acc]), (turn >> 1) & 1, &sh.failed, kPolls + 64ll * p.steps);
+          if (!ok && lane == 0) fail_pair(&sh.failed);
+          tc_fence_after();
         }
-        col.write(p, i0 + c, v);
-      };
-      request(half_turn * 16, even);
-      for (int c = half_turn * 16; c < end; c += 64) {
-        write(c, even, odd);
-        write(c + 32, odd, even);
+        const uint32_t at = from + (uint32_t)(acc * kAccumulatorColumns);
+#pragma unroll 1
+        for (int c = part * 16; c < end; c += kEpilogueWarps * 4) {
+          float v[16];
+          tmem_load16(at + c, v);
+          if (!ok) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fc00000);
+          }
+          col.write(i0 + c, v);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive_cluster(cluster_address(smem_u32(&sh.free_[acc]), 0));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive_cluster(cluster_address(smem_u32(&sh.free_[acc]), 0));
-    }
+    });
   }
   __syncthreads();
   // Every instruction issued has completed, in both CTAs' view.
@@ -789,6 +836,8 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   if (st != GEMV_OK) return st;
   if (!on_device(dev, {k > 0 ? A : nullptr, k > 0 ? B : nullptr, C, ep.scale_a, ep.scale_b, ep.bias, ep.residual}))
     return GEMV_ERR_DEVICE;
+  if (m == 1) ldc = ep.ldr = n;
+  if ((ldc > ep.ldr ? ldc : ep.ldr) * oe > (int64_t)UINT32_MAX) return GEMV_ERR_ARG;
   GemmParams p = {};
   p.B = static_cast<const char *>(B); p.A = static_cast<const char *>(A); p.C = C;
   p.ldb_bytes = ldb * es; p.lda_bytes = lda * es; p.ldc = ldc; p.ldr = ep.ldr;
@@ -813,7 +862,7 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   if (pair) plan_pair(p, &smem);
   else plan_split(p, sms, &smem);
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  if (tiles * p.splits > INT32_MAX) return GEMV_ERR_ARG;
+  if (tiles * p.splits > INT32_MAX / 2) return GEMV_ERR_ARG;
   if (tma && (!encode(&p.map_b, B, dtype, n, k, p.ldb_bytes, kTileRows) ||
               !encode(&p.map_a, A, dtype, m, k, p.lda_bytes, pair ? p.cols / 2 : p.cols)))
     return cuda_failure((int)cudaErrorNotSupported);
