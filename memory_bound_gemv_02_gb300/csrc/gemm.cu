@@ -764,36 +764,92 @@ bool tma_ok(const void *p, int64_t rows, int64_t ld_bytes) {
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kSmemPair = 112 * 1024;   // dynamic shared memory that leaves room for two CTAs per SM
+constexpr int kSmemHalf = 112 * 1024;   // dynamic shared memory that leaves room for two CTAs per SM
 constexpr int kSmemAlone = 225 * 1024;  // and for one
+constexpr int kMinStages = 3;
 
-// Tiles and ring of gemm_pair_kernel.
-void plan_pair(GemmParams &p, size_t *smem) {
-  p.splits = 1;
-  p.tiles_m = (int32_t)cdiv64(p.m, kAccumulatorColumns);
-  p.cols = (int32_t)(cdiv64(cdiv64(p.m, p.tiles_m), 32) * 32);
-  p.tiles_n = (int32_t)cdiv64(p.n, 2 * kTileRows);
-  const int stage = kTileBytes + p.cols / 2 * kRowBytes;
-  p.stages = (kSmemAlone - 1024) / stage;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  *smem = (size_t)p.stages * stage + 1024;
-}
+// The launch that gemm_plan() chooses.
+struct GemmPlan {
+  bool pair;
+  int cols, tiles_m, tiles_n, splits, stages;
+  int64_t smem;
+  double us;  // estimated
+};
 
-// Tile shape, split and ring of gemm_split_kernel.
-void plan_split(GemmParams &p, int sms, size_t *smem) {
-  p.tiles_m = (int32_t)cdiv64(p.m, 256);
-  p.cols = (int32_t)(cdiv64(cdiv64(p.m, p.tiles_m), 16) * 16);
-  p.tiles_n = (int32_t)cdiv64(p.n, kTileRows);
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
-  const int stage = kTileBytes + p.cols * kRowBytes;
-  const int budget = p.cols <= 96 ? kSmemPair : kSmemAlone;
-  const int64_t slots = (int64_t)sms * (p.cols <= 96 ? 2 : 1);
-  p.stages = (budget - 1024) / stage;
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= slots && p.steps / (p.splits * 2) >= 4) p.splits *= 2;
-  const int64_t ring = (int64_t)p.stages * stage, exchange = p.splits > 1 ? (int64_t)p.cols * kTileRows * 4 : 0;
-  *smem = (size_t)((ring > exchange ? ring : exchange) + 1024);
+// Kernel, tile width, split and ring for m x n x steps, by estimated time: the
+// operands' stream at 6.2 TB/s and the waves of CTAs times their steps, the
+// larger of the two and a quarter of the other, plus what a call costs besides.
+// The constants are a fit to 110 shapes of both operand widths (m = 1 .. 2048,
+// n x k = 1024 x 1024 .. 28672 x 8192), each measured in every form with cold
+// weights (us):
+//   gemm_split_kernel   0.13 + 0.00085 cols per step alone on its SM, 1.75
+//                       times that with a second CTA beside it; 0.008 per
+//                       column written; 3 per call, with a split 4.2 and 0.02
+//                       per column exchanged
+//   gemm_pair_kernel    0.286 per step of 256 columns, no less than 0.2; 6 per
+//                       call
+// Clusters are only taken where all run at once, with a seventh of the slots
+// left for where they do not fit (256 x 28672 x 8192 bf16, 256 columns over 2
+// CTAs in several waves: 121 against 94 in pairs).  The choice is within 5 % of
+// the fastest form on all but six of the shapes and within 10 % on all.  Some
+// of them (bf16, measured): 512 x 4096 x 4096 pairs of 128 columns 18.6, of 256
+// 23.0; 256 x 14336 x 4096 pairs 27.5, one tile per CTA 33.7; 256 x 1024 x 1024
+// 64 columns 6.8, 256 columns 12.0.
+GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, bool tma, int sms) {
+  GemmPlan best = {};
+  best.us = 1e30;
+  const double stream = (double)operand_bytes / 6.2e6;
+  auto take = [&](GemmPlan p, double work, double call) {
+    p.us = (work > stream ? work + 0.25 * stream : stream + 0.25 * work) + call;
+    if (p.us < best.us) best = p;
+  };
+  const int64_t fewest = cdiv64(m, kAccumulatorColumns);
+  for (int64_t t = fewest; t < fewest + 8; ++t) {
+    GemmPlan p = {};
+    p.cols = (int)(cdiv64(cdiv64(m, t), 16) * 16);
+    p.tiles_m = (int)cdiv64(m, p.cols);
+    p.tiles_n = (int)cdiv64(n, kTileRows);
+    if (p.tiles_m < t) break;  // 16 columns already
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    const int stage = kTileBytes + p.cols * kRowBytes;
+    for (int alone = 0; alone < 2; ++alone) {
+      const int room = alone ? kSmemAlone : kSmemHalf;
+      p.stages = (room - 1024) / stage < kMaxStages ? (room - 1024) / stage : kMaxStages;
+      if (p.stages < kMinStages) continue;
+      for (p.splits = 1; p.splits <= 8; p.splits *= 2) {
+        if (p.splits > 1 && steps / p.splits < 4) break;
+        const int64_t ctas = tiles * p.splits;
+        const int64_t ring = (int64_t)p.stages * stage;
+        const int64_t exchange = p.splits > 1 ? (int64_t)p.cols * kTileRows * 4 : 0;
+        if (exchange > room - 1024) break;
+        p.smem = (ring > exchange ? ring : exchange) + 1024;
+        if (p.splits > 1 && 7 * ctas > 6 * (alone ? sms : 2 * sms)) break;
+        const bool shared = !alone && ctas > sms;
+        const double step = (0.13 + 0.00085 * p.cols) * (shared ? 1.75 : 1.0);
+        const double waves = (double)cdiv64(ctas, shared ? 2 * sms : sms);
+        const double work = waves * (cdiv64(steps, p.splits) * step + 0.008 * p.cols / p.splits);
+        // a deeper ring where it costs nothing
+        take(p, work, (p.splits > 1 ? 4.2 + 0.02 * p.cols : 3.0) + (alone ? 0.0 : 0.2));
+      }
+    }
+  }
+  if (!tma) return best;
+  for (int64_t t = fewest; t < fewest + 4; ++t) {
+    GemmPlan p = {};
+    p.pair = true;
+    p.splits = 1;
+    p.cols = (int)(cdiv64(cdiv64(m, t), 32) * 32);
+    p.tiles_m = (int)cdiv64(m, p.cols);
+    p.tiles_n = (int)cdiv64(n, 2 * kTileRows);
+    if (p.tiles_m < t) break;
+    const int stage = kTileBytes + p.cols / 2 * kRowBytes;
+    p.stages = (kSmemAlone - 1024) / stage < kMaxStages ? (kSmemAlone - 1024) / stage : kMaxStages;
+    p.smem = (int64_t)p.stages * stage + 1024;
+    const double step = 0.286 * p.cols / 256 > 0.2 ? 0.286 * p.cols / 256 : 0.2;
+    const double work = (double)cdiv64((int64_t)p.tiles_m * p.tiles_n, sms / 2) * steps * step;
+    take(p, work, 6.0);
+  }
+  return best;
 }
 
 }  // namespace
@@ -855,12 +911,12 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   p.polls = take_wait_budget(kPolls);
   int st2 = wait_counter(dev, &p.timeouts);
   if (st2 != GEMV_OK) return st2;
-  size_t smem = 0;
   const bool e4m3 = dtype == GEMV_TYPE_E4M3;
   const bool tma = k > 0 && tma_ok(B, n, p.ldb_bytes) && tma_ok(A, m, p.lda_bytes);
-  const bool pair = tma && m > 256;
-  if (pair) plan_pair(p, &smem);
-  else plan_split(p, sms, &smem);
+  const GemmPlan plan = gemm_plan(m, n, steps, (m + n) * k * es, tma, sms);
+  const bool pair = plan.pair;
+  p.cols = plan.cols; p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
+  p.splits = plan.splits; p.stages = plan.stages;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles * p.splits > INT32_MAX / 2) return GEMV_ERR_ARG;
   if (tma && (!encode(&p.map_b, B, dtype, n, k, p.ldb_bytes, kTileRows) ||
@@ -871,10 +927,10 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
                            : e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>;
   int64_t grid = tiles * p.splits;
   if (pair) grid = 2 * (tiles < sms / 2 ? tiles : sms / 2);
-  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlone);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_failure((int)e);
   }
-  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : kSplitThreads, smem, pair ? 2 : p.splits, stream, p);
+  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : kSplitThreads, (size_t)plan.smem, pair ? 2 : p.splits, stream, p);
 }
