@@ -133,8 +133,8 @@ int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda, void *C, 
  *     h[t] = exp(g[t]) * h[t-1] + x[t]     (0 <= t < steps, h[-1] = h0)
  *
  * in fp32; h is rounded once per element when stored, the carried state is not
- * rounded.  A g of minus infinity (or any g whose exponential is 0 in fp32)
- * drops what came before, whatever it holds: tokens of packed documents do not
+ * rounded.  A g of minus infinity (or below -87.3, where the exponential leaves
+ * fp32's normal range) drops what came before, whatever it holds: tokens of packed documents do not
  * see one another, NaN and infinities included.
  *
  *  x, g, h      (batch, steps, width) of `dtype` (GEMV_TYPE_F16, _BF16 or _F32),
@@ -164,7 +164,7 @@ int gated_scan(const void *x, int64_t x_batch, int64_t x_step, const void *g, in
  *
  * in fp32 on the stored h (rounded to `dtype` by the forward pass: keeping it
  * in 16 bits halves what the gradient reads, and its rounding moves dg by at
- * most half an ulp of h, relative).  Where exp(g[t]) is 0, dg[t] is 0 and
+ * most half an ulp of h, relative).  Where exp(g[t]) counts as 0, dg[t] is 0 and
  * nothing is passed to step t-1.
  *
  *  dh, g, h     as in gated_scan().       dx, dg  (batch, steps, width) of `dtype`.

@@ -26,7 +26,8 @@ HOST_TOOL = os.path.join(LIBDIR, "gemv_bench_tool")  # native host-overhead and 
 SOURCES = ["gemv_api.cu", "gemv_kernels_f16.cu", "gemv_kernels_bf16.cu", "gemv_bulk_f16.cu", "gemv_bulk_bf16.cu",
            "gla_decode.cu", "rms_norm.cu", "gated_scan.cu", "gemm.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("gemv_internal.h", "gemv_kernels.cuh", "gemv_tiles.cuh",
-                                           "gemv_bulk.cuh", "ops_internal.h", "tc_ptx.cuh")] + \
+                                           "gemv_bulk.cuh", "ops_internal.h", "tc_ptx.cuh",
+                                           "tensor_map.h")] + \
     [os.path.join(INCLUDE, h) for h in ("gemv.h", "gemv_ops.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

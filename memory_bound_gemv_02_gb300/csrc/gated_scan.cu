@@ -22,6 +22,7 @@
 
 #include "ops_internal.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace gemvk {
 namespace {
@@ -54,10 +55,15 @@ __device__ __forceinline__ raw *at(const Strided &s, int64_t b, int64_t t, int64
 // a * v, where a decay of zero drops v.
 __device__ __forceinline__ float decayed(float a, float v) { return a == 0.f ? 0.f : a * v; }
 
+// exp(g) in two instructions: within 2 ulp near 1, where a decay is carried
+// far (2 + 1.2 |g| ulp in general), and zero below the normal range.  With
+// expf() the recurrence was bound by instructions, not by memory.
+__device__ __forceinline__ float decay(float g) { return __expf(g); }
+
 // One step of the recurrence from v; p is x or dh.  Backward, v + p is D.
 template <bool BACK>
 __device__ __forceinline__ float advance(float a, float v, float p) {
-  return BACK ? decayed(a, v + p) : decayed(a, v) + p;
+  return BACK ? decayed(a, v + p) : a == 0.f ? p : fmaf(a, v, p);
 }
 
 // The product of two runs' decays: zero only where one of them is.  (A NaN may
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float a = expf(gf[e]);
+          const float a = decay(gf[e]);
           out[e] = v[e] + xf[e];
           v[e] = decayed(a, out[e]);
           dg[e] = a == 0.f ? 0.f : v[e] * hf[e];
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
         L::store(at<raw>(p.dg, b, t, c), dg);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = advance<false>(expf(gf[e]), v[e], xf[e]);
+        for (int e = 0; e < V; ++e) v[e] = advance<false>(decay(gf[e]), v[e], xf[e]);
         L::store(at<raw>(p.h, b, t, c), v);
       }
     }
@@ -166,122 +172,214 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
 
 // -------------------------------------------------------------------- tiles --
 
-// Shape of a tile: `kLanes` threads side by side cover `kWidth` channels of a
-// step (128 bytes, or 32 single elements), `kGroups` groups of them take kSteps
-// steps each.
-template <int TYPE, bool VECTOR, bool BACK>
+// Shape of a tile: 16 threads side by side take 8 bytes each of a step (128
+// bytes, kWidth channels), 16 such groups take kSteps steps each.
+template <int TYPE, bool TMA, bool BACK>
 struct Tile {
-  static constexpr int V = Lane<TYPE, VECTOR>::V;
-  static constexpr int kLanes = VECTOR ? 8 : 32;
+  static constexpr int V = 8 / (int)sizeof(typename Elem<TYPE>::raw);
+  static constexpr int kLanes = 16;
   static constexpr int kWidth = kLanes * V;
   static constexpr int kGroups = kScanThreads / kLanes;
-  static constexpr int kPerWarp = 32 / kLanes;  // groups in a warp
-  static constexpr int kSteps = VECTOR ? 4 : 16;
+  static constexpr int kSteps = 8;
   static constexpr int kTime = kGroups * kSteps;
   static constexpr int kArrays = BACK ? 3 : 2;
-  static constexpr int kStages = VECTOR ? (BACK ? 2 : 3) : 0;
-  static constexpr int kStageBytes = kArrays * kSteps * kScanThreads * 16;
+  static constexpr int kArrayBytes = kTime * 128;
+  static constexpr int kCtas = TMA ? 2 : 1;  // per SM
+  static constexpr int kStages = TMA ? (BACK ? 2 : 3) : 4;
+  static constexpr int kExtra = TMA ? 0 : kArrays * kSteps * kGroups * 8;    // a 17th block of each group's rows
+  static constexpr int kStageBytes = kArrays * kArrayBytes + kExtra;
   static constexpr int kWarps = kScanThreads / 32;
-  // maps of the warps, values handed to the warps, maps of the cluster's CTAs (two rounds)
-  static constexpr int kFloats = (2 * kWarps + kWarps + 2 * 2 * kMaxScanCluster) * kWidth;
-  static constexpr int kSmem = kStages * kStageBytes + kFloats * 4;
+  static constexpr int kWarpMaps = kWarps * kWidth * 2;                      // floats: [warp][channel][A, B]
+  static constexpr int kCtaMaps = kMaxScanCluster * kWidth * 2;              // [CTA][channel][A, B]
+  static constexpr int kSmem = kStages * kStageBytes + 2 * (kWarpMaps + kCtaMaps) * 4;  // two rounds of maps
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+// Maps of V adjacent channels in shared memory, as [channel][A, B].
+template <int V>
+__device__ __forceinline__ void load_maps(const float *p, float (&A)[V], float (&B)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; e += 2) {
+    const float4 m = *reinterpret_cast<const float4 *>(p + 2 * e);
+    A[e] = m.x; B[e] = m.y; A[e + 1] = m.z; B[e + 1] = m.w;
+  }
 }
+template <int V>
+__device__ __forceinline__ void store_maps(float *p, const float (&A)[V], const float (&B)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; e += 2) *reinterpret_cast<float4 *>(p + 2 * e) = make_float4(A[e], B[e], A[e + 1], B[e + 1]);
+}
+
+// 8 bytes to shared memory without passing a register, zeros if not `in`.
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+}
+
+// NaN if any of the values is an infinity or a NaN, else 0.
+template <int V>
+__device__ __forceinline__ float not_finite(const float (&f)[V]) {
+  float r = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) r = fmaf(f[e], 0.f, r);
+  return r;
+}
+
+struct TileParams : ScanParams {
+  CUtensorMap maps[3];  // TMA: of x, g, h, each as (width, steps, batch)
+  uint32_t *timeouts;
+};
+
+struct alignas(8) TileShared {
+  uint64_t full[4];      // a stage's copies have landed (TMA)
+  uint64_t exchanged[2]; // the cluster's maps of a round are here
+  int failed;
+};
 
 // A cluster of p.cluster CTAs owns a chain: kWidth channels of one sequence.  In
 // a round its CTAs take consecutive tiles of kTime steps, and a tile goes
-//   1. each thread folds its kSteps steps per channel; maps are chained across
-//      the warp by shuffles, and the warps' across the CTA in shared memory;
-//   2. each CTA sends its map to all CTAs of the cluster, one barrier;
-//   3. one thread per channel walks the maps: CTAs before this one, then this
-//      CTA's warps; every thread takes its value from there and walks its steps
-//      again, now writing them.
-// Tiles of the rounds ahead are copied into thread-private slots of shared
-// memory meanwhile (VECTOR), so that memory never waits for the barriers.
-template <int TYPE, bool VECTOR, bool BACK>
-__global__ void __launch_bounds__(kScanThreads, VECTOR ? 2 : 3) gated_tile_kernel(ScanParams p) {
-  using L = Lane<TYPE, VECTOR>;
-  using S = Tile<TYPE, VECTOR, BACK>;
-  typedef typename L::raw raw;
-  typedef typename L::Block Block;
-  constexpr int V = L::V, N = S::kSteps;
-  extern __shared__ __align__(16) char dynamic[];
-  float *warp_maps = reinterpret_cast<float *>(dynamic + S::kStages * S::kStageBytes);  // [A, B][warp][channel]
-  float *handed = warp_maps + 2 * S::kWarps * S::kWidth;                                // [warp][channel]
-  float *cta_maps = handed + S::kWarps * S::kWidth;                                     // [round parity][A, B][CTA][channel]
+//   1. each thread folds its kSteps steps into a map per channel; the two
+//      groups of a warp are composed by shuffles, the warp's map goes to shared
+//      memory; one barrier;
+//   2. (clusters) each CTA sends its map to all CTAs of the cluster with stores
+//      that count themselves at the receiver's barrier: a cluster barrier would
+//      wait for the tile's stores to global memory as well;
+//   3. each thread applies the maps before its own to the carried value, which
+//      all threads of a channel keep, and walks its steps again, writing them.
+// Rounds alternate between two sets of maps, so that no further barrier is
+// needed: a CTA sends the maps of a round after its threads have read those of
+// the round before.  The tiles of the rounds ahead are copied into shared memory
+// meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, as
+// the aligned 8-byte blocks that cover each thread's channels, of which a
+// thread joins its own and the next.
+//
+// Steps run on plain products and sums, which are right as long as everything
+// is finite and no product of decays is 0; since what is not finite stays so to
+// the end of a run, one look there tells, and the run is then done again with a
+// look at every decay.
+template <int TYPE, bool TMA, bool BACK>
+__global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
+    gated_tile_kernel(const __grid_constant__ TileParams p) {
+  using E = Elem<TYPE>;
+  using S = Tile<TYPE, TMA, BACK>;
+  typedef typename E::raw raw;
+  constexpr int V = S::V, N = S::kSteps, ES = (int)sizeof(raw);
+  extern __shared__ __align__(128) char dynamic[];
+  __shared__ TileShared sh;
+  float *all_warp_maps = reinterpret_cast<float *>(dynamic + S::kStages * S::kStageBytes);
+  float *all_cta_maps = all_warp_maps + 2 * S::kWarpMaps;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int side = tid % S::kLanes, group = tid / S::kLanes;
-  const int rank = p.cluster > 1 ? (int)cluster_rank() : 0;
-  const int64_t unit = blockIdx.x / p.cluster;
-  const int64_t b = unit / p.chains, c0 = (unit - b * p.chains) * S::kWidth, c = c0 + side * V;
-  const bool in_row = c < p.width;
-  const int round_steps = S::kTime * p.cluster, rounds = (p.steps + round_steps - 1) / round_steps;
-  // one thread per channel of the chain carries its value between rounds
-  const bool owner = tid < S::kWidth && c0 + tid < p.width;
+  const int cluster = p.cluster, steps = p.steps;
+  const int rank = cluster > 1 ? (int)cluster_rank() : 0;
+  const int unit = blockIdx.x / cluster, sequence = unit / p.chains;
+  const int64_t b = sequence, c0 = (int64_t)(unit - sequence * p.chains) * S::kWidth, c = c0 + side * V;
+  const int64_t cell = b * p.width + c;
+  const int channels = c >= p.width ? 0 : p.width - c < V ? (int)(p.width - c) : V;  // this thread's
+  const int round_steps = S::kTime * cluster, rounds = (steps + round_steps - 1) / round_steps;
 
+  if (tid == 0) {
+    sh.failed = 0;
+    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.exchanged[i]), 1);
+    mbar_init_fence();
+  }
+  __syncthreads();
   allow_dependents();
   wait_for_predecessor();
-  if (p.cluster > 1) cluster_sync();  // the other CTAs' shared memory exists
+  if (cluster > 1) cluster_sync();  // the other CTAs' barriers exist
 
-  float carried = owner && p.first ? p.first[b * p.width + c0 + tid] : 0.f;
-  const raw *px = at<raw>(p.x, b, 0, c), *pg = at<raw>(p.g, b, 0, c), *ph = at<raw>(p.h, b, 0, c);
-  auto first_step = [&](int round) { return (round * p.cluster + rank) * S::kTime + group * N; };
-  auto time_of = [&](int s) { return BACK ? p.steps - 1 - s : s; };
-  auto slot = [&](int stage, int array, int u) {
-    return dynamic + stage * S::kStageBytes + ((array * N + u) * kScanThreads + tid) * 16;
+  float carried[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) carried[e] = e < channels && p.first ? p.first[cell + e] : 0.f;
+
+  auto tile_step = [&](int round) { return (round * cluster + rank) * S::kTime; };
+  // element row of step s in an array (backward: h is read one step earlier)
+  auto row_of = [&](int s, int array) { return BACK ? steps - 1 - s - (array == 2 ? 1 : 0) : s; };
+  const raw *inputs[3] = {at<raw>(p.x, b, 0, c), at<raw>(p.g, b, 0, c), at<raw>(p.h, b, 0, c)};
+  const int64_t pitch[3] = {p.x.step, p.g.step, p.h.step};
+  auto slot = [&](int stage, int array, int u, int thread) {
+    return dynamic + stage * S::kStageBytes + array * S::kArrayBytes + (u * kScanThreads + thread) * 8;
+  };
+  auto extra = [&](int stage, int array, int u) {
+    return dynamic + stage * S::kStageBytes + S::kArrays * S::kArrayBytes + ((array * N + u) * S::kGroups + group) * 8;
   };
   auto request = [&](int round) {
-    if constexpr (VECTOR) {
-      if (round < rounds) {
-        const int s0 = first_step(round), stage = round % S::kStages;
+    const int stage = round % S::kStages, s0 = tile_step(round);
+    if constexpr (TMA) {
+      if (tid == 0 && round < rounds && !sh.failed) {
+        const uint32_t bar = smem_u32(&sh.full[stage]);
+        mbar_expect_tx(bar, S::kArrays * S::kArrayBytes);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-          const bool in = in_row && s0 + u < p.steps;
-          const int64_t t = in ? time_of(s0 + u) : 0;
-          copy16(smem_u32(slot(stage, 0, u)), px + (in ? t * p.x.step : 0), in);
-          copy16(smem_u32(slot(stage, 1, u)), pg + (in ? t * p.g.step : 0), in);
-          if constexpr (BACK) {
-            const bool before = in && t > 0;
-            copy16(smem_u32(slot(stage, 2, u)), ph + (before ? (t - 1) * p.h.step : 0), before);
+        for (int array = 0; array < S::kArrays; ++array)  // rows before the first or past the last read as zeros
+          tma_load3(smem_u32(dynamic + stage * S::kStageBytes + array * S::kArrayBytes), &p.maps[array], (int)c0,
+                    BACK ? row_of(s0 + S::kTime - 1, array) : s0, sequence, bar);
+      }
+    } else {
+      if (round < rounds) {
+#pragma unroll
+        for (int array = 0; array < S::kArrays; ++array) {
+#pragma unroll
+          for (int u = 0; u < N; ++u) {
+            const int s = s0 + group * N + u, row = row_of(s, array);
+            const bool in = s < steps && row >= 0;
+            const uintptr_t start = (uintptr_t)(inputs[array] + (in ? row * pitch[array] : 0));
+            const uintptr_t block = start & ~(uintptr_t)7;
+            const int64_t left = (p.width - c) * ES + (int64_t)(start - block);  // bytes from the block to the row's end
+            copy8(smem_u32(slot(stage, array, u, tid)), reinterpret_cast<const void *>(block), in && left > 0);
+            if (side == S::kLanes - 1)
+              copy8(smem_u32(extra(stage, array, u)), reinterpret_cast<const void *>(block + 8), in && left > 8);
           }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
   };
-  if constexpr (VECTOR) {
-    for (int r = 0; r < S::kStages - 1; ++r) request(r);
-  }
+  for (int r = 0; r < S::kStages - 1; ++r) request(r);
 
   for (int round = 0; round < rounds; ++round) {
-    const int s0 = first_step(round), stage = VECTOR ? round % (S::kStages > 0 ? S::kStages : 1) : 0;
-    Block xb[VECTOR ? 1 : N], hb[VECTOR || !BACK ? 1 : N];
-    float a[N][V];
-    if constexpr (VECTOR) {
+    const int stage = round % S::kStages, s0 = tile_step(round) + group * N;
+    float *warp_maps = all_warp_maps + (round & 1) * S::kWarpMaps;
+    if (cluster > 1 && tid == 0) mbar_expect_tx(smem_u32(&sh.exchanged[round & 1]), (uint32_t)cluster * S::kWidth * 8);
+    if constexpr (TMA) {
+      wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, kWaitPolls);
+    } else {
+      __syncwarp();  // neighbours are done with the slots that are refilled now
       request(round + S::kStages - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
-    } else {
-      Block gb[N];
-#pragma unroll
-      for (int u = 0; u < N; ++u) {
-        const bool in = in_row && s0 + u < p.steps;
-        const int64_t t = in ? time_of(s0 + u) : 0;
-        xb[u] = in ? L::load(px + t * p.x.step) : L::zero();
-        gb[u] = in ? L::load(pg + t * p.g.step) : L::zero();
-        if constexpr (BACK) hb[u] = in && t > 0 ? L::load(ph + (t - 1) * p.h.step) : L::zero();
-      }
-#pragma unroll
-      for (int u = 0; u < N; ++u) L::unpack(gb[u], a[u]);
+      __syncwarp();
     }
-    auto input = [&](int u, float (&f)[V]) {
-      if constexpr (VECTOR) L::unpack(*reinterpret_cast<const Block *>(slot(stage, 0, u)), f);
-      else L::unpack(xb[u], f);
+    const char *mine = dynamic + stage * S::kStageBytes + side * 8 + (BACK ? S::kTime - 1 - group * N : group * N) * 128;
+    auto input = [&](int u, int array, float (&f)[V]) {
+      uint2 w;
+      if constexpr (TMA) {
+        w = *reinterpret_cast<const uint2 *>(mine + array * S::kArrayBytes + (BACK ? -u : u) * 128);
+      } else {
+        w = *reinterpret_cast<const uint2 *>(slot(stage, array, u, tid));
+        const uint2 hi = *reinterpret_cast<const uint2 *>(side == S::kLanes - 1 ? extra(stage, array, u)
+                                                                              : slot(stage, array, u, tid + 1));
+        const uint32_t off = (uint32_t)(uintptr_t)inputs[array] +
+                             (uint32_t)row_of(s0 + u, array) * (uint32_t)pitch[array] * (uint32_t)ES;
+        const uint32_t bits = (off & 3) * 8;
+        if (off & 4) w = make_uint2(__funnelshift_r(w.y, hi.x, bits), __funnelshift_r(hi.x, hi.y, bits));
+        else w = make_uint2(__funnelshift_r(w.x, w.y, bits), __funnelshift_r(w.y, hi.x, bits));
+      }
+      if constexpr (V == 4) {
+        const float2 lo = TYPE == GEMV_TYPE_F16 ? F16::pair(w.x) : BF16::pair(w.x);
+        const float2 up = TYPE == GEMV_TYPE_F16 ? F16::pair(w.y) : BF16::pair(w.y);
+        f[0] = lo.x; f[1] = lo.y; f[2] = up.x; f[3] = up.y;
+      } else {
+        f[0] = __uint_as_float(w.x);
+        f[1] = __uint_as_float(w.y);
+      }
+      if constexpr (!TMA) {  // what follows a row's end is not its own
+        if (channels < V) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[e] = e < channels ? f[e] : 0.f;
+        }
+      }
     };
-    // 1. this thread's map: steps beyond the end have decay 1 and add 0
-    float A[V], B[V];
+
+    // 1. this thread's map: steps beyond the end read zeros, decay 1 and 0 added
+    float a[N][V], A[V], B[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       A[e] = 1.f;
@@ -289,124 +387,186 @@ __global__ void __launch_bounds__(kScanThreads, VECTOR ? 2 : 3) gated_tile_kerne
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
-      if constexpr (VECTOR) L::unpack(*reinterpret_cast<const Block *>(slot(stage, 1, u)), a[u]);
       float xf[V];
-      input(u, xf);
+      input(u, 1, a[u]);
+      input(u, 0, xf);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        a[u][e] = expf(a[u][e]);
-        B[e] = advance<BACK>(a[u][e], B[e], xf[e]);
-        A[e] = chain(A[e], a[u][e]);
+        a[u][e] = decay(a[u][e]);
+        B[e] = BACK ? a[u][e] * (B[e] + xf[e]) : fmaf(a[u][e], B[e], xf[e]);
+        A[e] *= a[u][e];
       }
     }
-    // chained across the warp's groups: inclusive, then shifted to what precedes this thread
+    bool plain = not_finite(A) + not_finite(B) == 0.f;
 #pragma unroll
-    for (int d = 1; d < S::kPerWarp; d *= 2) {
+    for (int e = 0; e < V; ++e) plain = plain && A[e] != 0.f;
+    if (!plain) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float A1 = __shfl_up_sync(0xffffffffu, A[e], d * S::kLanes);
-        const float B1 = __shfl_up_sync(0xffffffffu, B[e], d * S::kLanes);
-        if (lane >= d * S::kLanes) {
-          B[e] = apply(A[e], B[e], B1);
-          A[e] = chain(A1, A[e]);
-        }
-      }
-    }
-    if (lane >= 32 - S::kLanes) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        warp_maps[warp * S::kWidth + side * V + e] = A[e];
-        warp_maps[(S::kWarps + warp) * S::kWidth + side * V + e] = B[e];
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if constexpr (S::kPerWarp > 1) {
-        A[e] = __shfl_up_sync(0xffffffffu, A[e], S::kLanes);
-        B[e] = __shfl_up_sync(0xffffffffu, B[e], S::kLanes);
-      }
-      if (lane < S::kLanes) {  // the warp's first group
         A[e] = 1.f;
         B[e] = 0.f;
       }
+#pragma unroll 1
+      for (int u = 0; u < N; ++u) {
+        float xf[V], gf[V];
+        input(u, 1, gf);
+        input(u, 0, xf);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float d = decay(gf[e]);
+          B[e] = advance<BACK>(d, B[e], xf[e]);
+          A[e] = chain(A[e], d);
+        }
+      }
     }
+    // the map of what precedes this thread in its warp, and the warp's own
+    float A0[V], B0[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      A0[e] = __shfl_up_sync(0xffffffffu, A[e], S::kLanes);
+      B0[e] = __shfl_up_sync(0xffffffffu, B[e], S::kLanes);
+      B[e] = apply(A[e], B[e], B0[e]);
+      A[e] = chain(A0[e], A[e]);
+    }
+    if (lane >= S::kLanes) store_maps(warp_maps + (warp * S::kWidth + side * V) * 2, A, B);
     __syncthreads();
-    // 2. and 3. chained across the warps and the cluster
-    if (p.cluster > 1) {
-      float *maps = cta_maps + (round & 1) * 2 * kMaxScanCluster * S::kWidth;
+    if constexpr (TMA) request(round + S::kStages - 1);  // into the stage that the round before has read
+
+    // 2. the maps of the cluster's CTAs
+    float v[V], start[V];  // the value at the start of the CTA's tile, and of this thread's steps
+    if (cluster > 1) {
+      float *cta_maps = all_cta_maps + (round & 1) * S::kCtaMaps;
+      const uint32_t bar = smem_u32(&sh.exchanged[round & 1]);
       if (tid < S::kWidth) {
         float A1 = 1.f, B1 = 0.f;
 #pragma unroll
         for (int w = 0; w < S::kWarps; ++w) {
-          const float A2 = warp_maps[w * S::kWidth + tid], B2 = warp_maps[(S::kWarps + w) * S::kWidth + tid];
-          B1 = apply(A2, B2, B1);
-          A1 = chain(A1, A2);
+          const float2 m = *reinterpret_cast<const float2 *>(warp_maps + (w * S::kWidth + tid) * 2);
+          B1 = apply(m.x, m.y, B1);
+          A1 = chain(A1, m.x);
         }
-        for (int r = 0; r < p.cluster; ++r) {
-          st_cluster(cluster_address(smem_u32(maps + rank * S::kWidth + tid), r), A1);
-          st_cluster(cluster_address(smem_u32(maps + (kMaxScanCluster + rank) * S::kWidth + tid), r), B1);
-        }
+        const uint32_t to = smem_u32(cta_maps + (rank * S::kWidth + tid) * 2);
+        for (int r = 0; r < cluster; ++r) st_cluster_counted(cluster_address(to, r), A1, B1, cluster_address(bar, r));
       }
-      cluster_sync();
-      if (tid < S::kWidth) {
-        float v = carried;
-        for (int r = 0; r < p.cluster; ++r) {
-          if (r == rank) {
-            float u = v;
+      if (!wait_for<true>(bar, (round >> 1) & 1, &sh.failed, kWaitPolls)) {
 #pragma unroll
-            for (int w = 0; w < S::kWarps; ++w) {
-              handed[w * S::kWidth + tid] = u;
-              u = apply(warp_maps[w * S::kWidth + tid], warp_maps[(S::kWarps + w) * S::kWidth + tid], u);
-            }
-          }
-          v = apply(maps[r * S::kWidth + tid], maps[(kMaxScanCluster + r) * S::kWidth + tid], v);
-        }
-        carried = v;
+        for (int e = 0; e < V; ++e) carried[e] = __int_as_float(0x7fc00000);
       }
-    } else if (tid < S::kWidth) {
+      for (int r = 0; r < cluster; ++r) {
+        float Ar[V], Br[V];
+        load_maps(cta_maps + (r * S::kWidth + side * V) * 2, Ar, Br);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (r == rank) v[e] = carried[e];
+          carried[e] = apply(Ar[e], Br[e], carried[e]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = carried[e];
+    }
+    // 3. the maps of the CTA's warps: plain first, as above
+    auto fold = [&](const bool robust) {
 #pragma unroll
       for (int w = 0; w < S::kWarps; ++w) {
-        handed[w * S::kWidth + tid] = carried;
-        carried = apply(warp_maps[w * S::kWidth + tid], warp_maps[(S::kWarps + w) * S::kWidth + tid], carried);
+        float Aw[V], Bw[V];
+        load_maps(warp_maps + (w * S::kWidth + side * V) * 2, Aw, Bw);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (w == warp) start[e] = v[e];
+          v[e] = robust ? apply(Aw[e], Bw[e], v[e]) : fmaf(Aw[e], v[e], Bw[e]);
+        }
       }
+    };
+    float begin[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) begin[e] = v[e];
+    fold(false);
+    if (!(not_finite(v) == 0.f)) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = begin[e];
+      fold(true);
     }
-    __syncthreads();
-    float v[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = apply(A[e], B[e], handed[warp * S::kWidth + side * V + e]);
+    for (int e = 0; e < V; ++e) {
+      if (cluster == 1) carried[e] = v[e];
+      v[e] = start[e] = lane >= S::kLanes ? apply(A0[e], B0[e], start[e]) : start[e];
+    }
+    // this thread's steps again
+    raw *out0 = at<raw>(BACK ? p.dx : p.h, b, row_of(s0, 0), c), *out1 = at<raw>(p.dg, b, row_of(s0, 0), c);
+    const int64_t out_pitch0 = BACK ? -p.dx.step : p.h.step, out_pitch1 = -p.dg.step;
+    auto write = [&](raw *to, const float (&f)[V]) {
+      if constexpr (TMA && V == 4) {
+        const uint2 w = TYPE == GEMV_TYPE_F16
+                            ? make_uint2(Elem<GEMV_TYPE_F16>::pair(f[0], f[1]), Elem<GEMV_TYPE_F16>::pair(f[2], f[3]))
+                            : make_uint2(Elem<GEMV_TYPE_BF16>::pair(f[0], f[1]), Elem<GEMV_TYPE_BF16>::pair(f[2], f[3]));
+        *reinterpret_cast<uint2 *>(to) = w;
+      } else if constexpr (TMA) {
+        *reinterpret_cast<float2 *>(to) = make_float2(f[0], f[1]);
+      } else {
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const bool in = in_row && s0 + u < p.steps;
-      const int64_t t = in ? time_of(s0 + u) : 0;
+        for (int e = 0; e < V; ++e)
+          if (e < channels) to[e] = E::put(f[e]);
+      }
+    };
+    auto step = [&](int u, const float (&d)[V], const bool robust) {
+      const bool in = channels > 0 && s0 + u < steps;
       float xf[V];
-      input(u, xf);
+      input(u, 0, xf);
       if constexpr (BACK) {
         float hf[V], dx[V], dg[V];
-        if constexpr (VECTOR) L::unpack(*reinterpret_cast<const Block *>(slot(stage, 2, u)), hf);
-        else L::unpack(hb[u], hf);
-        if (in && t == 0) {
+        input(u, 2, hf);
+        if (s0 + u == steps - 1 && p.h0) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) hf[e] = p.h0 ? p.h0[b * p.width + c + e] : 0.f;
+          for (int e = 0; e < V; ++e)
+            if (e < channels) hf[e] = p.h0[cell + e];
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           dx[e] = v[e] + xf[e];
-          v[e] = decayed(a[u][e], dx[e]);
-          dg[e] = a[u][e] == 0.f ? 0.f : v[e] * hf[e];
+          v[e] = robust ? decayed(d[e], dx[e]) : d[e] * dx[e];
+          dg[e] = d[e] == 0.f ? 0.f : v[e] * hf[e];
         }
         if (in) {
-          L::store(at<raw>(p.dx, b, t, c), dx);
-          L::store(at<raw>(p.dg, b, t, c), dg);
+          write(out0 + u * out_pitch0, dx);
+          write(out1 + u * out_pitch1, dg);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = advance<false>(a[u][e], v[e], xf[e]);
-        if (in) L::store(at<raw>(p.h, b, t, c), v);
+        for (int e = 0; e < V; ++e) v[e] = robust ? advance<false>(d[e], v[e], xf[e]) : fmaf(d[e], v[e], xf[e]);
+        if (in) write(out0 + u * out_pitch0, v);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < N; ++u) step(u, a[u], false);
+    if (!(not_finite(v) == 0.f)) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = start[e];
+#pragma unroll 1
+      for (int u = 0; u < N; ++u) {
+        float d[V];
+        input(u, 1, d);
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] = decay(d[e]);
+        step(u, d, true);
       }
     }
   }
-  if (rank == 0 && owner && p.last) p.last[b * p.width + c0 + tid] = carried;
-  if (p.cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
+  if (rank == 0 && group == 0 && p.last) {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < channels) p.last[cell + e] = carried[e];
+  }
+  if (cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
+  if (sh.failed && warp == 0) {     // after a wait that gave up: copies in flight land first
+    if (lane == 0) atomicAdd(p.timeouts, 1u);
+    if constexpr (TMA) {
+      int none = 0;
+      for (int r = rounds < S::kStages ? 0 : rounds - S::kStages; r < rounds; ++r)
+        if (!wait_for<false>(smem_u32(&sh.full[r % S::kStages]), (r / S::kStages) & 1, &none, 1 << 10) && lane == 0)
+          atomicOr(p.timeouts, kDrainTimeoutBit);
+    }
+  }
 }
 
 bool strides_ok(const Strided &s, int64_t batch, int64_t steps) {
@@ -439,55 +599,84 @@ Rows as_rows(const Strided &s, int64_t batch, int64_t steps, int64_t width, int 
   return Rows{s.p, 1, span * es, span * es};
 }
 
-// Buffers whose rows of V elements start on 16-byte boundaries.
-bool on_vectors(const Strided &s, const ScanParams &p, int es) {
-  const int64_t v = 16 / es;
-  return (uintptr_t)s.p % 16 == 0 && (p.batch == 1 || s.batch % v == 0) && (p.steps == 1 || s.step % v == 0);
+// Whether every row of a buffer starts on 16 bytes.
+bool on_boundary(const Strided &s, const ScanParams &p, int es) {
+  return (uintptr_t)s.p % 16 == 0 && (p.batch == 1 || s.batch * es % 16 == 0) && (p.steps == 1 || s.step * es % 16 == 0);
 }
 
-constexpr int kTileCtasPerSm = 2;
-
 template <int TYPE, bool VECTOR, bool BACK>
-int launch_scan(ScanParams p, int sms, cudaStream_t stream) {
-  using S = Tile<TYPE, VECTOR, BACK>;
-  const int64_t threads = p.batch * (p.width / S::V);
-  if (p.steps <= 4 || (p.steps <= 64 && threads >= (int64_t)sms * 128)) {
-    const int64_t blocks = (threads + kWalkThreads - 1) / kWalkThreads;
-    if (blocks > INT32_MAX) return GEMV_ERR_ARG;
-    return launch_op(gated_walk_kernel<TYPE, VECTOR, BACK>, dim3((unsigned)blocks), kWalkThreads, 0, 1, stream, p);
-  }
+int launch_walk(const ScanParams &p, cudaStream_t stream) {
+  const int64_t blocks = (p.batch * (p.width / Lane<TYPE, VECTOR>::V) + kWalkThreads - 1) / kWalkThreads;
+  if (blocks > INT32_MAX) return GEMV_ERR_ARG;
+  return launch_op(gated_walk_kernel<TYPE, VECTOR, BACK>, dim3((unsigned)blocks), kWalkThreads, 0, 1, stream, p);
+}
+
+template <int TYPE, bool TMA, bool BACK>
+int launch_tiles(const ScanParams &scan, int sms, uint32_t *timeouts, cudaStream_t stream) {
+  using S = Tile<TYPE, TMA, BACK>;
+  TileParams p = {};
+  static_cast<ScanParams &>(p) = scan;
+  p.timeouts = timeouts;
   p.chains = (int32_t)((p.width + S::kWidth - 1) / S::kWidth);
   const int64_t units = p.batch * p.chains;
   // Few chains: clusters split their sequences, as far as all CTAs fit at once.
   p.cluster = 1;
-  while (p.cluster < kMaxScanCluster && units * p.cluster * 2 <= (int64_t)sms * kTileCtasPerSm &&
+  while (p.cluster < kMaxScanCluster && units * p.cluster * 2 <= (int64_t)sms * S::kCtas &&
          (int64_t)p.cluster * S::kTime < p.steps)
     p.cluster *= 2;
   if (units * p.cluster > INT32_MAX) return GEMV_ERR_ARG;
-  auto fn = gated_tile_kernel<TYPE, VECTOR, BACK>;
-  if (S::kSmem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return cuda_failure((int)e);
+  if (TMA) {
+    const Strided *const in[3] = {&p.x, &p.g, &p.h};
+    const int es = type_bytes(TYPE);
+    for (int i = 0; i < S::kArrays; ++i) {
+      // a single step or sequence may have any stride
+      const int64_t row = (p.width * es + 15) / 16 * 16;
+      const cuuint64_t dims[3] = {(cuuint64_t)p.width, (cuuint64_t)p.steps, (cuuint64_t)p.batch};
+      const cuuint64_t strides[2] = {(cuuint64_t)(p.steps > 1 ? in[i]->step * es : row),
+                                     (cuuint64_t)(p.batch > 1 ? in[i]->batch * es : row)};
+      const cuuint32_t box[3] = {(cuuint32_t)S::kWidth, (cuuint32_t)S::kTime, 1};
+      if (!encode_map(&p.maps[i], in[i]->p, TYPE, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cuda_failure((int)cudaErrorNotSupported);
     }
+  }
+  auto fn = gated_tile_kernel<TYPE, TMA, BACK>;
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
   }
   return launch_op(fn, dim3((unsigned)(units * p.cluster)), kScanThreads, S::kSmem, p.cluster, stream, p);
 }
 
-template <int TYPE>
-int launch_scan_type(const ScanParams &p, bool backward, int sms, cudaStream_t stream) {
+template <int TYPE, bool BACK>
+int launch_scan(const ScanParams &p, int sms, uint32_t *timeouts, cudaStream_t stream) {
   const int es = type_bytes(TYPE);
-  const bool vector = p.width % (16 / es) == 0 && on_vectors(p.x, p, es) && on_vectors(p.g, p, es) &&
-                      on_vectors(p.h, p, es) && (!backward || (on_vectors(p.dx, p, es) && on_vectors(p.dg, p, es)));
-  if (backward) return vector ? launch_scan<TYPE, true, true>(p, sms, stream) : launch_scan<TYPE, false, true>(p, sms, stream);
-  return vector ? launch_scan<TYPE, true, false>(p, sms, stream) : launch_scan<TYPE, false, false>(p, sms, stream);
+  const bool vectors = p.width * es % 16 == 0 && on_boundary(p.x, p, es) && on_boundary(p.g, p, es) &&
+                       on_boundary(p.h, p, es) && (!BACK || (on_boundary(p.dx, p, es) && on_boundary(p.dg, p, es)));
+  if (p.steps <= 4 || (p.steps <= 64 && p.batch * p.width * es >= (int64_t)sms * 128 * 16))
+    return vectors ? launch_walk<TYPE, true, BACK>(p, stream) : launch_walk<TYPE, false, BACK>(p, stream);
+  // TMA copies need strides that are not 0 (shared rows) and fit their maps.
+  auto mapped = [&](const Strided &s) {
+    return (p.steps == 1 || (s.step > 0 && s.step * es < (1ll << 40))) &&
+           (p.batch == 1 || (s.batch > 0 && s.batch * es < (1ll << 40)));
+  };
+  const bool tma = vectors && mapped(p.x) && mapped(p.g) && (!BACK || mapped(p.h));
+  return tma ? launch_tiles<TYPE, true, BACK>(p, sms, timeouts, stream)
+             : launch_tiles<TYPE, false, BACK>(p, sms, timeouts, stream);
 }
 
-int dispatch_scan(const ScanParams &p, bool backward, int dtype, int sms, cudaStream_t stream) {
-  return dtype == GEMV_TYPE_F16    ? launch_scan_type<GEMV_TYPE_F16>(p, backward, sms, stream)
-         : dtype == GEMV_TYPE_BF16 ? launch_scan_type<GEMV_TYPE_BF16>(p, backward, sms, stream)
-                                   : launch_scan_type<GEMV_TYPE_F32>(p, backward, sms, stream);
+int dispatch_scan(const ScanParams &p, bool backward, int dtype, int dev, int sms, cudaStream_t stream) {
+  uint32_t *timeouts = nullptr;
+  const int st = wait_counter(dev, &timeouts);
+  if (st != GEMV_OK) return st;
+  if (dtype == GEMV_TYPE_F16)
+    return backward ? launch_scan<GEMV_TYPE_F16, true>(p, sms, timeouts, stream)
+                    : launch_scan<GEMV_TYPE_F16, false>(p, sms, timeouts, stream);
+  if (dtype == GEMV_TYPE_BF16)
+    return backward ? launch_scan<GEMV_TYPE_BF16, true>(p, sms, timeouts, stream)
+                    : launch_scan<GEMV_TYPE_BF16, false>(p, sms, timeouts, stream);
+  return backward ? launch_scan<GEMV_TYPE_F32, true>(p, sms, timeouts, stream)
+                  : launch_scan<GEMV_TYPE_F32, false>(p, sms, timeouts, stream);
 }
 
 // Sizes, strides and types common to both directions.
@@ -549,7 +738,7 @@ extern "C" int gated_scan(const void *x, int64_t x_batch, int64_t x_step, const 
   if (!on_device(dev, {steps > 0 ? x : nullptr, steps > 0 ? g : nullptr, steps > 0 ? h : nullptr, h0, state}))
     return GEMV_ERR_DEVICE;
   if (steps == 0) return copy_carry(h0, state, cells, stream);
-  return dispatch_scan(p, false, dtype, sms, stream);
+  return dispatch_scan(p, false, dtype, dev, sms, stream);
 }
 
 extern "C" int gated_scan_backward(const void *dh, int64_t dh_batch, int64_t dh_step, const void *g, int64_t g_batch,
@@ -598,5 +787,5 @@ extern "C" int gated_scan_backward(const void *dh, int64_t dh_batch, int64_t dh_
                        steps > 0 ? (const void *)dx : nullptr, steps > 0 ? (const void *)dg : nullptr, h0, dstate, dh0}))
     return GEMV_ERR_DEVICE;
   if (steps == 0) return copy_carry(dstate, dh0, cells, stream);
-  return dispatch_scan(p, true, dtype, sms, stream);
+  return dispatch_scan(p, true, dtype, dev, sms, stream);
 }

@@ -28,6 +28,7 @@
 
 #include "ops_internal.h"
 #include "tc_ptx.cuh"
+#include "tensor_map.h"
 
 namespace gemvk {
 namespace {
@@ -37,7 +38,7 @@ constexpr int kTileRows = 128;                   // rows of B per CTA
 constexpr int kTileBytes = kTileRows * kRowBytes;
 constexpr int kMaxStages = 8;
 constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
-constexpr int kPolls = 1 << 20;                  // polls of one wait before it gives up
+constexpr int kPolls = kWaitPolls;               // polls of one wait before it gives up
 constexpr int kEpilogueWarps = 8;                 // of gemm_pair_kernel
 constexpr int kSplitThreads = 256, kPairThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kGatherWarps = 4;                  // warps 4 to 7
@@ -229,22 +230,6 @@ __device__ __forceinline__ void with_column(const GemmParams &p, Run run) {
 }
 
 // --------------------------------------------------------------------- waits --
-
-// Polls a barrier until its phase `parity` completes, the whole warp together:
-// the issuing loops stay uniform, so that the operands of the matrix and copy
-// instructions live in uniform registers (issued from a lone thread's loop,
-// one tcgen05.mma took about 95 cycles to issue and 8192 x 14336 x 4096 bf16
-// 590 us instead of 503).  False if the polls run out or another role of this CTA has given up.
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int64_t polls) {
-  while (polls > 0) {
-    if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, *failed != 0)) return false;
-    --polls;
-  }
-  *failed = 1;
-  return false;
-}
 
 // Tells every role of a pair's two CTAs to give up.
 __device__ __forceinline__ void fail_pair(int *failed) {
@@ -722,40 +707,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
 
 // ---------------------------------------------------------------------- host --
 
-typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The driver's tensor-map encoder (looked up once).
-EncodeFn encode_fn() {
-  static const EncodeFn fn = [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      f = nullptr;
-    }
-    return reinterpret_cast<EncodeFn>(f);
-  }();
-  return fn;
-}
-
 // A (rows, k) operand with `ld_bytes` between rows, in boxes of 128 bytes of k
 // by `box_rows` rows; what lies outside reads as zero.
 bool encode(CUtensorMap *map, const void *p, int dtype, int64_t rows, int64_t k, int64_t ld_bytes, int box_rows) {
-  const EncodeFn fn = encode_fn();
-  if (fn == nullptr) return false;
   const int es = type_bytes(dtype);
   if (rows == 1) ld_bytes = (k * es + 15) / 16 * 16;
   const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld_bytes};
-  const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows}, one[2] = {1, 1};
-  const CUtensorMapDataType t = dtype == GEMV_TYPE_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                : dtype == GEMV_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  return fn(map, t, 2, const_cast<void *>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[2] = {(cuuint32_t)(kRowBytes / es), (cuuint32_t)box_rows};
+  return encode_map(map, p, dtype, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 bool tma_ok(const void *p, int64_t rows, int64_t ld_bytes) {

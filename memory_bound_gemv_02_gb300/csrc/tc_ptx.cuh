@@ -57,6 +57,22 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
   return ok != 0;
 }
 
+// Polls a barrier until its phase `parity` completes, the whole warp together:
+// the issuing loops stay uniform, so that the operands of the matrix and copy
+// instructions live in uniform registers (issued from a lone thread's loop,
+// one tcgen05.mma took about 95 cycles to issue and 8192 x 14336 x 4096 bf16
+// 590 us instead of 503).  False if the polls run out or another role of this CTA has given up.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int *failed, int64_t polls) {
+  while (polls > 0) {
+    if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_cluster(bar, parity) : mbar_try(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *failed != 0)) return false;
+    --polls;
+  }
+  *failed = 1;
+  return false;
+}
+
 // One thread of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
@@ -89,6 +105,13 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Two floats to another CTA of the cluster, counted as 8 bytes at its barrier
+// once they are there (both are addresses from cluster_address()).
+__device__ __forceinline__ void st_cluster_counted(uint32_t addr, float a, float b, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(a),
+               "f"(b), "r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ int ld_cluster(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -108,6 +131,13 @@ __device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y, uint32_t bar) {
