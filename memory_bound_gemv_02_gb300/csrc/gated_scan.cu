@@ -55,10 +55,36 @@ __device__ __forceinline__ raw *at(const Strided &s, int64_t b, int64_t t, int64
 // a * v, where a decay of zero drops v.
 __device__ __forceinline__ float decayed(float a, float v) { return a == 0.f ? 0.f : a * v; }
 
+// 2^t in one instruction, within 2 ulp; below the normal range it is zero.
+__device__ __forceinline__ float exp2_fast(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
 // exp(g) in two instructions: within 2 ulp near 1, where a decay is carried
-// far (2 + 1.2 |g| ulp in general), and zero below the normal range.  With
-// expf() the recurrence was bound by instructions, not by memory.
-__device__ __forceinline__ float decay(float g) { return __expf(g); }
+// far (the product's rounding adds |g| u elsewhere).  With expf() the
+// recurrence was bound by instructions, not by memory.
+__device__ __forceinline__ float decay(float g) { return exp2_fast(g * kLog2e); }
+
+// Two fused multiply-adds, or products, in one instruction.
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 c, a, b, c;\nmov.b64 {%0, %1}, c;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
 
 // One step of the recurrence from v; p is x or dh.  Backward, v + p is D.
 template <bool BACK>
@@ -189,10 +215,27 @@ struct Tile {
   static constexpr int kExtra = TMA ? 0 : kArrays * kSteps * kGroups * 8;    // a 17th block of each group's rows
   static constexpr int kStageBytes = kArrays * kArrayBytes + kExtra;
   static constexpr int kWarps = kScanThreads / 32;
-  static constexpr int kWarpMaps = kWarps * kWidth * 2;                      // floats: [warp][channel][A, B]
+  static constexpr int kWarpMaps = kWarps * kWidth * 2;                      // floats: [warp][A, B][channel]
   static constexpr int kCtaMaps = kMaxScanCluster * kWidth * 2;              // [CTA][channel][A, B]
-  static constexpr int kSmem = kStages * kStageBytes + 2 * (kWarpMaps + kCtaMaps) * 4;  // two rounds of maps
+  static constexpr int kSmem = kStages * kStageBytes + 2 * (kWarpMaps + kCtaMaps + kWidth) * 4;  // two rounds of maps and carried values
 };
+
+// V adjacent floats of shared memory.
+template <int V>
+__device__ __forceinline__ void load_floats(const float *p, float (&f)[V]) {
+  if constexpr (V == 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2 *>(p);
+    f[0] = v.x; f[1] = v.y;
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_floats(float *p, const float (&f)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  else *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+}
 
 // Maps of V adjacent channels in shared memory, as [channel][A, B].
 template <int V>
@@ -203,12 +246,6 @@ __device__ __forceinline__ void load_maps(const float *p, float (&A)[V], float (
     A[e] = m.x; B[e] = m.y; A[e + 1] = m.z; B[e + 1] = m.w;
   }
 }
-template <int V>
-__device__ __forceinline__ void store_maps(float *p, const float (&A)[V], const float (&B)[V]) {
-#pragma unroll
-  for (int e = 0; e < V; e += 2) *reinterpret_cast<float4 *>(p + 2 * e) = make_float4(A[e], B[e], A[e + 1], B[e + 1]);
-}
-
 // 8 bytes to shared memory without passing a register, zeros if not `in`.
 __device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
@@ -266,6 +303,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
   __shared__ TileShared sh;
   float *all_warp_maps = reinterpret_cast<float *>(dynamic + S::kStages * S::kStageBytes);
   float *all_cta_maps = all_warp_maps + 2 * S::kWarpMaps;
+  float *all_carried = all_cta_maps + 2 * S::kCtaMaps;  // [round parity][channel], one CTA per chain
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int side = tid % S::kLanes, group = tid / S::kLanes;
   const int cluster = p.cluster, steps = p.steps;
@@ -290,6 +328,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
   float carried[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) carried[e] = e < channels && p.first ? p.first[cell + e] : 0.f;
+  if (group == 0) store_floats(all_carried + side * V, carried);  // read after the first round's barrier
 
   auto tile_step = [&](int round) { return (round * cluster + rank) * S::kTime; };
   // element row of step s in an array (backward: h is read one step earlier)
@@ -391,10 +430,18 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
       input(u, 1, a[u]);
       input(u, 0, xf);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        a[u][e] = decay(a[u][e]);
-        B[e] = BACK ? a[u][e] * (B[e] + xf[e]) : fmaf(a[u][e], B[e], xf[e]);
-        A[e] *= a[u][e];
+      for (int e = 0; e < V; e += 2) {
+        float &a0 = a[u][e], &a1 = a[u][e + 1];
+        mul2(a0, a1, a0, a1, kLog2e, kLog2e);
+        a0 = exp2_fast(a0);
+        a1 = exp2_fast(a1);
+        if constexpr (BACK) {
+          add2(B[e], B[e + 1], B[e], B[e + 1], xf[e], xf[e + 1]);
+          mul2(B[e], B[e + 1], B[e], B[e + 1], a0, a1);
+        } else {
+          fma2(B[e], B[e + 1], a0, a1, B[e], B[e + 1], xf[e], xf[e + 1]);
+        }
+        mul2(A[e], A[e + 1], A[e], A[e + 1], a0, a1);
       }
     }
     bool plain = not_finite(A) + not_finite(B) == 0.f;
@@ -428,7 +475,10 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
       B[e] = apply(A[e], B[e], B0[e]);
       A[e] = chain(A0[e], A[e]);
     }
-    if (lane >= S::kLanes) store_maps(warp_maps + (warp * S::kWidth + side * V) * 2, A, B);
+    if (lane >= S::kLanes) {
+      store_floats(warp_maps + (warp * 2) * S::kWidth + side * V, A);
+      store_floats(warp_maps + (warp * 2 + 1) * S::kWidth + side * V, B);
+    }
     __syncthreads();
     if constexpr (TMA) request(round + S::kStages - 1);  // into the stage that the round before has read
 
@@ -441,17 +491,14 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
         float A1 = 1.f, B1 = 0.f;
 #pragma unroll
         for (int w = 0; w < S::kWarps; ++w) {
-          const float2 m = *reinterpret_cast<const float2 *>(warp_maps + (w * S::kWidth + tid) * 2);
-          B1 = apply(m.x, m.y, B1);
-          A1 = chain(A1, m.x);
+          const float A2 = warp_maps[(w * 2) * S::kWidth + tid], B2 = warp_maps[(w * 2 + 1) * S::kWidth + tid];
+          B1 = apply(A2, B2, B1);
+          A1 = chain(A1, A2);
         }
         const uint32_t to = smem_u32(cta_maps + (rank * S::kWidth + tid) * 2);
         for (int r = 0; r < cluster; ++r) st_cluster_counted(cluster_address(to, r), A1, B1, cluster_address(bar, r));
       }
-      if (!wait_for<true>(bar, (round >> 1) & 1, &sh.failed, kWaitPolls)) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) carried[e] = __int_as_float(0x7fc00000);
-      }
+      wait_for<true>(bar, (round >> 1) & 1, &sh.failed, kWaitPolls);
       for (int r = 0; r < cluster; ++r) {
         float Ar[V], Br[V];
         load_maps(cta_maps + (r * S::kWidth + side * V) * 2, Ar, Br);
@@ -462,36 +509,30 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
         }
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = carried[e];
+      load_floats(all_carried + (round & 1) * S::kWidth + side * V, v);
     }
-    // 3. the maps of the CTA's warps: plain first, as above
+    // 3. the maps of the CTA's warps before this one: plain first, as above
     auto fold = [&](const bool robust) {
 #pragma unroll
-      for (int w = 0; w < S::kWarps; ++w) {
+      for (int w = 0; w < S::kWarps - 1; ++w) {
+        if (w >= warp) break;
         float Aw[V], Bw[V];
-        load_maps(warp_maps + (w * S::kWidth + side * V) * 2, Aw, Bw);
+        load_floats(warp_maps + (w * 2) * S::kWidth + side * V, Aw);
+        load_floats(warp_maps + (w * 2 + 1) * S::kWidth + side * V, Bw);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (w == warp) start[e] = v[e];
-          v[e] = robust ? apply(Aw[e], Bw[e], v[e]) : fmaf(Aw[e], v[e], Bw[e]);
-        }
+        for (int e = 0; e < V; ++e) v[e] = robust ? apply(Aw[e], Bw[e], v[e]) : fmaf(Aw[e], v[e], Bw[e]);
       }
     };
-    float begin[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) begin[e] = v[e];
+    for (int e = 0; e < V; ++e) start[e] = v[e];
     fold(false);
     if (!(not_finite(v) == 0.f)) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = begin[e];
+      for (int e = 0; e < V; ++e) v[e] = start[e];
       fold(true);
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (cluster == 1) carried[e] = v[e];
-      v[e] = start[e] = lane >= S::kLanes ? apply(A0[e], B0[e], start[e]) : start[e];
-    }
+    for (int e = 0; e < V; ++e) v[e] = start[e] = lane >= S::kLanes ? apply(A0[e], B0[e], v[e]) : v[e];
     // this thread's steps again
     raw *out0 = at<raw>(BACK ? p.dx : p.h, b, row_of(s0, 0), c), *out1 = at<raw>(p.dg, b, row_of(s0, 0), c);
     const int64_t out_pitch0 = BACK ? -p.dx.step : p.h.step, out_pitch1 = -p.dg.step;
@@ -509,6 +550,16 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
           if (e < channels) to[e] = E::put(f[e]);
       }
     };
+    if (*(volatile int *)&sh.failed) {
+#pragma unroll 1
+      for (int u = 0; u < N && s0 + u < steps && channels > 0; ++u) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = __int_as_float(0x7fc00000);
+        write(out0 + u * out_pitch0, v);
+        if (BACK) write(out1 + u * out_pitch1, v);
+      }
+      continue;
+    }
     auto step = [&](int u, const float (&d)[V], const bool robust) {
       const bool in = channels > 0 && s0 + u < steps;
       float xf[V];
@@ -522,10 +573,17 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
             if (e < channels) hf[e] = p.h0[cell + e];
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          dx[e] = v[e] + xf[e];
-          v[e] = robust ? decayed(d[e], dx[e]) : d[e] * dx[e];
-          dg[e] = d[e] == 0.f ? 0.f : v[e] * hf[e];
+        for (int e = 0; e < V; e += 2) {
+          add2(dx[e], dx[e + 1], v[e], v[e + 1], xf[e], xf[e + 1]);
+          if (robust) {
+            v[e] = decayed(d[e], dx[e]);
+            v[e + 1] = decayed(d[e + 1], dx[e + 1]);
+          } else {
+            mul2(v[e], v[e + 1], d[e], d[e + 1], dx[e], dx[e + 1]);
+          }
+          mul2(dg[e], dg[e + 1], v[e], v[e + 1], hf[e], hf[e + 1]);
+          dg[e] = d[e] == 0.f ? 0.f : dg[e];
+          dg[e + 1] = d[e + 1] == 0.f ? 0.f : dg[e + 1];
         }
         if (in) {
           write(out0 + u * out_pitch0, dx);
@@ -533,7 +591,14 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = robust ? advance<false>(d[e], v[e], xf[e]) : fmaf(d[e], v[e], xf[e]);
+        for (int e = 0; e < V; e += 2) {
+          if (robust) {
+            v[e] = advance<false>(d[e], v[e], xf[e]);
+            v[e + 1] = advance<false>(d[e + 1], v[e + 1], xf[e + 1]);
+          } else {
+            fma2(v[e], v[e + 1], d[e], d[e + 1], v[e], v[e + 1], xf[e], xf[e + 1]);
+          }
+        }
         if (in) write(out0 + u * out_pitch0, v);
       }
     };
@@ -551,8 +616,15 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
         step(u, d, true);
       }
     }
+    // the last group's value is the next round's, read after that round's barrier
+    if (cluster == 1 && group == S::kGroups - 1) store_floats(all_carried + ((round + 1) & 1) * S::kWidth + side * V, v);
+    if (cluster == 1) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) carried[e] = v[e];
+    }
   }
-  if (rank == 0 && group == 0 && p.last) {
+  // the sequence's last value: every thread's of a cluster's CTA, the last group's of a CTA alone
+  if (p.last && rank == 0 && group == (cluster > 1 ? 0 : S::kGroups - 1)) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
       if (e < channels) p.last[cell + e] = carried[e];
