@@ -131,14 +131,14 @@ def lib() -> ctypes.CDLL:
 def _lib_with_operators() -> ctypes.CDLL:
     """The loaded library with the argument types of the operators set."""
     global _operators_ready
-    L = _lib if _lib is not None else lib()
     if _operators_ready:
-        return L
+        return _lib
+    L = lib()
     vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
     seq = [vp, i64, i64]
     L.rms_norm_fused.argtypes = [vp, i64, vp, i64, vp, i32, vp, i64, vp, vp, i64, i64, i64, ctypes.c_float, i32, i32,
                                  vp]
-    L.gemm_fused.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp, vp]
+    L.gemm_fused.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp, vp]  # epilogue: a structure or its bytes
     L.gated_scan.argtypes = seq + seq + [vp] + seq + [vp, i64, i64, i64, i32, vp]
     L.gated_scan_backward.argtypes = seq * 3 + [vp, vp] + seq * 2 + [vp, i64, i64, i64, i32, vp]
     for name in OPERATOR_ENTRY_POINTS:
