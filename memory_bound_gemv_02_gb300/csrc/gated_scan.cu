@@ -55,19 +55,6 @@ __device__ __forceinline__ raw *at(const Strided &s, int64_t b, int64_t t, int64
 // a * v, where a decay of zero drops v.
 __device__ __forceinline__ float decayed(float a, float v) { return a == 0.f ? 0.f : a * v; }
 
-// 2^t in one instruction, within 2 ulp; below the normal range it is zero.
-__device__ __forceinline__ float exp2_fast(float t) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
-  return r;
-}
-constexpr float kLog2e = 1.4426950408889634f;
-
-// exp(g) in two instructions: within 2 ulp near 1, where a decay is carried
-// far (the product's rounding adds |g| u elsewhere).  With expf() the
-// recurrence was bound by instructions, not by memory.
-__device__ __forceinline__ float decay(float g) { return exp2_fast(g * kLog2e); }
-
 // Two fused multiply-adds, or products, in one instruction.
 __device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
   asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
@@ -86,6 +73,36 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1, f
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
+// exp(g) of two values.  Near 1, where a decay is carried over many steps, by
+// its series (the next term is below 6e-9 relative): within 0.6 u and without
+// the bias of a third of a unit per step that the special function unit's 2^t
+// has there, which gave the last state of 8192 steps 1.6e-6 of relative error
+// instead of 2e-7.  Elsewhere in two instructions, zero below the normal range.
+constexpr float kLog2e = 1.4426950408889634f, kNearOne = 0.125f;
+__device__ __forceinline__ float exp2_fast(float t) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
+  return r;
+}
+__device__ __forceinline__ void decay2(float &g0, float &g1) {
+  float t0, t1, p0, p1;
+  mul2(t0, t1, g0, g1, kLog2e, kLog2e);
+  t0 = exp2_fast(t0);
+  t1 = exp2_fast(t1);
+  fma2(p0, p1, g0, g1, 1.f / 120, 1.f / 120, 1.f / 24, 1.f / 24);
+  fma2(p0, p1, g0, g1, p0, p1, 1.f / 6, 1.f / 6);
+  fma2(p0, p1, g0, g1, p0, p1, 0.5f, 0.5f);
+  fma2(p0, p1, g0, g1, p0, p1, 1.f, 1.f);
+  fma2(p0, p1, g0, g1, p0, p1, 1.f, 1.f);
+  g0 = fabsf(g0) < kNearOne ? p0 : t0;
+  g1 = fabsf(g1) < kNearOne ? p1 : t1;
+}
+__device__ __forceinline__ float decay(float g) {
+  float other = 0.f;
+  decay2(g, other);
+  return g;
+}
+
 // One step of the recurrence from v; p is x or dh.  Backward, v + p is D.
 template <bool BACK>
 __device__ __forceinline__ float advance(float a, float v, float p) {
@@ -97,7 +114,7 @@ __device__ __forceinline__ float advance(float a, float v, float p) {
 __device__ __forceinline__ float chain(float a1, float a2) { return fmaxf(a1 * a2, fminf(fminf(a1, a2), 1e-45f)); }
 
 // A run's map applied to v.  A state of zero stays zero however far A grew.
-__device__ __forceinline__ float apply(float A, float B, float v) { return (A == 0.f || v == 0.f ? 0.f : A * v) + B; }
+__device__ __forceinline__ float apply(float A, float B, float v) { return A == 0.f || v == 0.f ? B : fmaf(A, v, B); }
 
 // Element access by 16 bytes (VECTOR) or one element.
 template <int TYPE, bool VECTOR>
@@ -198,25 +215,27 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
 
 // -------------------------------------------------------------------- tiles --
 
-// Shape of a tile: 16 threads side by side take 8 bytes each of a step (128
-// bytes, kWidth channels), 16 such groups take kSteps steps each.
-template <int TYPE, bool TMA, bool BACK>
+// Shape of a tile: LANES threads side by side take 8 bytes each of a step
+// (kWidth channels), kGroups such groups take kSteps steps each.  16 lanes read
+// whole 128-byte lines; 8 lanes make twice as many chains of the same work, for
+// sequences whose chains do not fill the GPU.
+template <int TYPE, bool TMA, bool BACK, int LANES>
 struct Tile {
   static constexpr int V = 8 / (int)sizeof(typename Elem<TYPE>::raw);
-  static constexpr int kLanes = 16;
-  static constexpr int kWidth = kLanes * V;
-  static constexpr int kGroups = kScanThreads / kLanes;
+  static constexpr int kWidth = LANES * V;
+  static constexpr int kGroups = kScanThreads / LANES;
+  static constexpr int kPerWarp = 32 / LANES;
   static constexpr int kSteps = 8;
   static constexpr int kTime = kGroups * kSteps;
   static constexpr int kArrays = BACK ? 3 : 2;
-  static constexpr int kArrayBytes = kTime * 128;
-  static constexpr int kCtas = TMA ? 2 : 1;  // per SM
-  static constexpr int kStages = TMA ? (BACK ? 2 : 3) : 4;
-  static constexpr int kExtra = TMA ? 0 : kArrays * kSteps * kGroups * 8;    // a 17th block of each group's rows
-  static constexpr int kStageBytes = kArrays * kArrayBytes + kExtra;
+  static constexpr int kRowPitch = LANES * 8 + (TMA ? 0 : 16);  // without TMA a row starts anywhere in its 16 bytes
+  static constexpr int kArrayBytes = kTime * kRowPitch;
+  static constexpr int kStageBytes = kArrays * kArrayBytes;
+  static constexpr int kCtas = TMA || !BACK ? 2 : 1;            // per SM
+  static constexpr int kStages = TMA ? (BACK ? 2 : 3) : BACK ? 3 : 2;
   static constexpr int kWarps = kScanThreads / 32;
-  static constexpr int kWarpMaps = kWarps * kWidth * 2;                      // floats: [warp][A, B][channel]
-  static constexpr int kCtaMaps = kMaxScanCluster * kWidth * 2;              // [CTA][channel][A, B]
+  static constexpr int kWarpMaps = kWarps * kWidth * 2;         // floats: [warp][A, B][channel]
+  static constexpr int kCtaMaps = kMaxScanCluster * kWidth * 2; // [CTA][channel][A, B]
   static constexpr int kSmem = kStages * kStageBytes + 2 * (kWarpMaps + kCtaMaps + kWidth) * 4;  // two rounds of maps and carried values
 };
 
@@ -246,10 +265,13 @@ __device__ __forceinline__ void load_maps(const float *p, float (&A)[V], float (
     A[e] = m.x; B[e] = m.y; A[e + 1] = m.z; B[e + 1] = m.w;
   }
 }
-// 8 bytes to shared memory without passing a register, zeros if not `in`.
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool in) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8 : 0) : "memory");
+// `bytes` (a multiple of 16, from a multiple of 16) to shared memory, counted at `bar`.
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
+__device__ __forceinline__ uint32_t lds32(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // NaN if any of the values is an infinity or a NaN, else 0.
 template <int V>
@@ -284,19 +306,19 @@ struct alignas(8) TileShared {
 // Rounds alternate between two sets of maps, so that no further barrier is
 // needed: a CTA sends the maps of a round after its threads have read those of
 // the round before.  The tiles of the rounds ahead are copied into shared memory
-// meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, as
-// the aligned 8-byte blocks that cover each thread's channels, of which a
-// thread joins its own and the next.
+// meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, row
+// by row as the aligned 16-byte blocks that cover its channels, whose words a
+// thread joins to its own.
 //
 // Steps run on plain products and sums, which are right as long as everything
 // is finite and no product of decays is 0; since what is not finite stays so to
 // the end of a run, one look there tells, and the run is then done again with a
 // look at every decay.
-template <int TYPE, bool TMA, bool BACK>
-__global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
+template <int TYPE, bool TMA, bool BACK, int LANES>
+__global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kCtas)
     gated_tile_kernel(const __grid_constant__ TileParams p) {
   using E = Elem<TYPE>;
-  using S = Tile<TYPE, TMA, BACK>;
+  using S = Tile<TYPE, TMA, BACK, LANES>;
   typedef typename E::raw raw;
   constexpr int V = S::V, N = S::kSteps, ES = (int)sizeof(raw);
   extern __shared__ __align__(128) char dynamic[];
@@ -305,7 +327,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
   float *all_cta_maps = all_warp_maps + 2 * S::kWarpMaps;
   float *all_carried = all_cta_maps + 2 * S::kCtaMaps;  // [round parity][channel], one CTA per chain
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int side = tid % S::kLanes, group = tid / S::kLanes;
+  const int side = tid % LANES, group = tid / LANES;
   const int cluster = p.cluster, steps = p.steps;
   const int rank = cluster > 1 ? (int)cluster_rank() : 0;
   const int unit = blockIdx.x / cluster, sequence = unit / p.chains;
@@ -316,7 +338,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
 
   if (tid == 0) {
     sh.failed = 0;
-    for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
+    for (int i = 0; i < S::kStages; ++i) mbar_init(smem_u32(&sh.full[i]), TMA ? 1 : kScanThreads);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.exchanged[i]), 1);
     mbar_init_fence();
   }
@@ -333,43 +355,44 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
   auto tile_step = [&](int round) { return (round * cluster + rank) * S::kTime; };
   // element row of step s in an array (backward: h is read one step earlier)
   auto row_of = [&](int s, int array) { return BACK ? steps - 1 - s - (array == 2 ? 1 : 0) : s; };
-  const raw *inputs[3] = {at<raw>(p.x, b, 0, c), at<raw>(p.g, b, 0, c), at<raw>(p.h, b, 0, c)};
+  const raw *inputs[3] = {at<raw>(p.x, b, 0, c0), at<raw>(p.g, b, 0, c0), at<raw>(p.h, b, 0, c0)};
   const int64_t pitch[3] = {p.x.step, p.g.step, p.h.step};
-  auto slot = [&](int stage, int array, int u, int thread) {
-    return dynamic + stage * S::kStageBytes + array * S::kArrayBytes + (u * kScanThreads + thread) * 8;
-  };
-  auto extra = [&](int stage, int array, int u) {
-    return dynamic + stage * S::kStageBytes + S::kArrays * S::kArrayBytes + ((array * N + u) * S::kGroups + group) * 8;
-  };
+  // Row r of a tile in shared memory holds step r of it, backward step kTime - 1 - r.
   auto request = [&](int round) {
+    if (round >= rounds || *(volatile int *)&sh.failed) return;
     const int stage = round % S::kStages, s0 = tile_step(round);
+    const uint32_t bar = smem_u32(&sh.full[stage]);
+    char *to = dynamic + stage * S::kStageBytes;
     if constexpr (TMA) {
-      if (tid == 0 && round < rounds && !sh.failed) {
-        const uint32_t bar = smem_u32(&sh.full[stage]);
-        mbar_expect_tx(bar, S::kArrays * S::kArrayBytes);
+      if (tid == 0) {
+        mbar_expect_tx(bar, S::kStageBytes);
 #pragma unroll
         for (int array = 0; array < S::kArrays; ++array)  // rows before the first or past the last read as zeros
-          tma_load3(smem_u32(dynamic + stage * S::kStageBytes + array * S::kArrayBytes), &p.maps[array], (int)c0,
+          tma_load3(smem_u32(to + array * S::kArrayBytes), &p.maps[array], (int)c0,
                     BACK ? row_of(s0 + S::kTime - 1, array) : s0, sequence, bar);
       }
     } else {
-      if (round < rounds) {
+      const int span = (int)(p.width - c0 < S::kWidth ? p.width - c0 : S::kWidth) * ES;
+      constexpr int kRows = S::kArrays * S::kTime, kEach = (kRows + kScanThreads - 1) / kScanThreads;
+      const void *from[kEach];
+      uint32_t bytes[kEach], total = 0;
 #pragma unroll
-        for (int array = 0; array < S::kArrays; ++array) {
-#pragma unroll
-          for (int u = 0; u < N; ++u) {
-            const int s = s0 + group * N + u, row = row_of(s, array);
-            const bool in = s < steps && row >= 0;
-            const uintptr_t start = (uintptr_t)(inputs[array] + (in ? row * pitch[array] : 0));
-            const uintptr_t block = start & ~(uintptr_t)7;
-            const int64_t left = (p.width - c) * ES + (int64_t)(start - block);  // bytes from the block to the row's end
-            copy8(smem_u32(slot(stage, array, u, tid)), reinterpret_cast<const void *>(block), in && left > 0);
-            if (side == S::kLanes - 1)
-              copy8(smem_u32(extra(stage, array, u)), reinterpret_cast<const void *>(block + 8), in && left > 8);
-          }
-        }
+      for (int i = 0; i < kEach; ++i) {
+        const int n = tid + i * kScanThreads, array = n / S::kTime, r = n % S::kTime;
+        const int row = BACK ? row_of(s0 + S::kTime - 1, array) + r : s0 + r;
+        const bool in = n < kRows && row >= 0 && row < steps;
+        const uintptr_t start = (uintptr_t)(inputs[array < 2 ? array : 2] + (in ? row * pitch[array < 2 ? array : 2] : 0));
+        from[i] = reinterpret_cast<const void *>(start & ~(uintptr_t)15);
+        bytes[i] = in ? (uint32_t)(((int)(start & 15) + span + 15) & ~15) : 0u;
+        total += bytes[i];
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (total) mbar_expect_tx(bar, total);
+      else mbar_arrive(bar);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int n = tid + i * kScanThreads;
+        if (bytes[i]) copy_bulk(smem_u32(to + n * S::kRowPitch), from[i], bytes[i], bar);
+      }
     }
   };
   for (int r = 0; r < S::kStages - 1; ++r) request(r);
@@ -378,28 +401,24 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
     const int stage = round % S::kStages, s0 = tile_step(round) + group * N;
     float *warp_maps = all_warp_maps + (round & 1) * S::kWarpMaps;
     if (cluster > 1 && tid == 0) mbar_expect_tx(smem_u32(&sh.exchanged[round & 1]), (uint32_t)cluster * S::kWidth * 8);
-    if constexpr (TMA) {
-      wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, kWaitPolls);
-    } else {
-      __syncwarp();  // neighbours are done with the slots that are refilled now
-      request(round + S::kStages - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
-      __syncwarp();
-    }
-    const char *mine = dynamic + stage * S::kStageBytes + side * 8 + (BACK ? S::kTime - 1 - group * N : group * N) * 128;
+    wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, kWaitPolls);
+    const char *mine = dynamic + stage * S::kStageBytes + side * 8 +
+                       (BACK ? S::kTime - 1 - group * N : group * N) * S::kRowPitch;
     auto input = [&](int u, int array, float (&f)[V]) {
+      const char *from = mine + array * S::kArrayBytes + (BACK ? -u : u) * S::kRowPitch;
       uint2 w;
       if constexpr (TMA) {
-        w = *reinterpret_cast<const uint2 *>(mine + array * S::kArrayBytes + (BACK ? -u : u) * 128);
+        w = *reinterpret_cast<const uint2 *>(from);
       } else {
-        w = *reinterpret_cast<const uint2 *>(slot(stage, array, u, tid));
-        const uint2 hi = *reinterpret_cast<const uint2 *>(side == S::kLanes - 1 ? extra(stage, array, u)
-                                                                              : slot(stage, array, u, tid + 1));
-        const uint32_t off = (uint32_t)(uintptr_t)inputs[array] +
-                             (uint32_t)row_of(s0 + u, array) * (uint32_t)pitch[array] * (uint32_t)ES;
-        const uint32_t bits = (off & 3) * 8;
-        if (off & 4) w = make_uint2(__funnelshift_r(w.y, hi.x, bits), __funnelshift_r(hi.x, hi.y, bits));
-        else w = make_uint2(__funnelshift_r(w.x, w.y, bits), __funnelshift_r(w.y, hi.x, bits));
+        const uint32_t off = ((uint32_t)(uintptr_t)inputs[array] +
+                              (uint32_t)row_of(s0 + u, array) * (uint32_t)pitch[array] * (uint32_t)ES) & 15;
+        from += off & 12;
+        w = make_uint2(lds32(from), lds32(from + 4));
+        if constexpr (ES == 2) {
+          const uint32_t bits = (off & 2) * 8;
+          w = make_uint2(__funnelshift_r(w.x, w.y, bits), __funnelshift_r(w.y, lds32(from + 8), bits));
+        }
+        if (s0 + u >= steps) w = make_uint2(0u, 0u);  // rows that were not copied
       }
       if constexpr (V == 4) {
         const float2 lo = TYPE == GEMV_TYPE_F16 ? F16::pair(w.x) : BF16::pair(w.x);
@@ -432,9 +451,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
 #pragma unroll
       for (int e = 0; e < V; e += 2) {
         float &a0 = a[u][e], &a1 = a[u][e + 1];
-        mul2(a0, a1, a0, a1, kLog2e, kLog2e);
-        a0 = exp2_fast(a0);
-        a1 = exp2_fast(a1);
+        decay2(a0, a1);
         if constexpr (BACK) {
           add2(B[e], B[e + 1], B[e], B[e + 1], xf[e], xf[e + 1]);
           mul2(B[e], B[e + 1], B[e], B[e + 1], a0, a1);
@@ -469,18 +486,30 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
     // the map of what precedes this thread in its warp, and the warp's own
     float A0[V], B0[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      A0[e] = __shfl_up_sync(0xffffffffu, A[e], S::kLanes);
-      B0[e] = __shfl_up_sync(0xffffffffu, B[e], S::kLanes);
-      B[e] = apply(A[e], B[e], B0[e]);
-      A[e] = chain(A0[e], A[e]);
+    for (int d = 1; d < S::kPerWarp; d *= 2) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        A0[e] = __shfl_up_sync(0xffffffffu, A[e], d * LANES);
+        B0[e] = __shfl_up_sync(0xffffffffu, B[e], d * LANES);
+        if (lane >= d * LANES) {
+          B[e] = apply(A[e], B[e], B0[e]);
+          A[e] = chain(A0[e], A[e]);
+        }
+      }
     }
-    if (lane >= S::kLanes) {
+    if constexpr (S::kPerWarp > 2) {  // of two groups, the exchanged map is the one before
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        A0[e] = __shfl_up_sync(0xffffffffu, A[e], LANES);
+        B0[e] = __shfl_up_sync(0xffffffffu, B[e], LANES);
+      }
+    }
+    if (lane >= 32 - LANES) {
       store_floats(warp_maps + (warp * 2) * S::kWidth + side * V, A);
       store_floats(warp_maps + (warp * 2 + 1) * S::kWidth + side * V, B);
     }
     __syncthreads();
-    if constexpr (TMA) request(round + S::kStages - 1);  // into the stage that the round before has read
+    request(round + S::kStages - 1);  // into the stage that the round before has read
 
     // 2. the maps of the cluster's CTAs
     float v[V], start[V];  // the value at the start of the CTA's tile, and of this thread's steps
@@ -532,31 +561,53 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
       fold(true);
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = start[e] = lane >= S::kLanes ? apply(A0[e], B0[e], v[e]) : v[e];
+    for (int e = 0; e < V; ++e) v[e] = start[e] = lane >= LANES ? apply(A0[e], B0[e], v[e]) : v[e];
     // this thread's steps again
     raw *out0 = at<raw>(BACK ? p.dx : p.h, b, row_of(s0, 0), c), *out1 = at<raw>(p.dg, b, row_of(s0, 0), c);
     const int64_t out_pitch0 = BACK ? -p.dx.step : p.h.step, out_pitch1 = -p.dg.step;
-    auto write = [&](raw *to, const float (&f)[V]) {
-      if constexpr (TMA && V == 4) {
-        const uint2 w = TYPE == GEMV_TYPE_F16
-                            ? make_uint2(Elem<GEMV_TYPE_F16>::pair(f[0], f[1]), Elem<GEMV_TYPE_F16>::pair(f[2], f[3]))
-                            : make_uint2(Elem<GEMV_TYPE_BF16>::pair(f[0], f[1]), Elem<GEMV_TYPE_BF16>::pair(f[2], f[3]));
-        *reinterpret_cast<uint2 *>(to) = w;
-      } else if constexpr (TMA) {
-        *reinterpret_cast<float2 *>(to) = make_float2(f[0], f[1]);
-      } else {
+    const bool whole = c0 + S::kWidth <= p.width;
+    // All lanes of the warp call it together; `in`: this thread's step exists.
+    auto write = [&](raw *to, const float (&f)[V], const bool in) {
+      if constexpr (V == 2) {
+        if (TMA) {
+          if (in) *reinterpret_cast<float2 *>(to) = make_float2(f[0], f[1]);
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (e < channels) to[e] = E::put(f[e]);
+          for (int e = 0; e < V; ++e)
+            if (in && e < channels) to[e] = E::put(f[e]);
+        }
+      } else {
+        constexpr int T = TYPE == GEMV_TYPE_F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16;
+        const uint32_t lo = Elem<T>::pair(f[0], f[1]), hi = Elem<T>::pair(f[2], f[3]);
+        if constexpr (TMA) {
+          if (in) *reinterpret_cast<uint2 *>(to) = make_uint2(lo, hi);
+        } else if (!whole) {
+#pragma unroll
+          for (int e = 0; e < V; ++e)
+            if (in && e < channels) to[e] = E::put(f[e]);
+        } else if (((uintptr_t)to & 2) == 0) {  // the same for all groups of a warp, 8 rows apart
+          if (in) {
+            *reinterpret_cast<uint32_t *>(to) = lo;
+            *reinterpret_cast<uint32_t *>(to + 2) = hi;
+          }
+        } else {  // 4-byte words across neighbouring lanes
+          const uint32_t next = __shfl_down_sync(0xffffffffu, lo, 1, LANES);
+          if (in) {
+            if (side == 0) to[0] = (raw)(lo & 0xffffu);
+            *reinterpret_cast<uint32_t *>(to + 1) = __funnelshift_r(lo, hi, 16);
+            if (side < LANES - 1) *reinterpret_cast<uint32_t *>(to + 3) = __funnelshift_r(hi, next, 16);
+            else to[3] = (raw)(hi >> 16);
+          }
+        }
       }
     };
-    if (*(volatile int *)&sh.failed) {
+    if (__any_sync(0xffffffffu, *(volatile int *)&sh.failed != 0)) {
 #pragma unroll 1
-      for (int u = 0; u < N && s0 + u < steps && channels > 0; ++u) {
+      for (int u = 0; u < N; ++u) {
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = __int_as_float(0x7fc00000);
-        write(out0 + u * out_pitch0, v);
-        if (BACK) write(out1 + u * out_pitch1, v);
+        write(out0 + u * out_pitch0, v, channels > 0 && s0 + u < steps);
+        if (BACK) write(out1 + u * out_pitch1, v, channels > 0 && s0 + u < steps);
       }
       continue;
     }
@@ -567,10 +618,9 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
       if constexpr (BACK) {
         float hf[V], dx[V], dg[V];
         input(u, 2, hf);
-        if (s0 + u == steps - 1 && p.h0) {
+        if (s0 + u == steps - 1) {
 #pragma unroll
-          for (int e = 0; e < V; ++e)
-            if (e < channels) hf[e] = p.h0[cell + e];
+          for (int e = 0; e < V; ++e) hf[e] = p.h0 && e < channels ? p.h0[cell + e] : 0.f;
         }
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
@@ -585,10 +635,8 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
           dg[e] = d[e] == 0.f ? 0.f : dg[e];
           dg[e + 1] = d[e + 1] == 0.f ? 0.f : dg[e + 1];
         }
-        if (in) {
-          write(out0 + u * out_pitch0, dx);
-          write(out1 + u * out_pitch1, dg);
-        }
+        write(out0 + u * out_pitch0, dx, in);
+        write(out1 + u * out_pitch1, dg, in);
       } else {
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
@@ -599,12 +647,12 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
             fma2(v[e], v[e + 1], d[e], d[e + 1], v[e], v[e + 1], xf[e], xf[e + 1]);
           }
         }
-        if (in) write(out0 + u * out_pitch0, v);
+        write(out0 + u * out_pitch0, v, in);
       }
     };
 #pragma unroll
     for (int u = 0; u < N; ++u) step(u, a[u], false);
-    if (!(not_finite(v) == 0.f)) {
+    if (__any_sync(0xffffffffu, !(not_finite(v) == 0.f))) {
 #pragma unroll
       for (int e = 0; e < V; ++e) v[e] = start[e];
 #pragma unroll 1
@@ -632,7 +680,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK>::kCtas)
   if (cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
   if (sh.failed && warp == 0) {     // after a wait that gave up: copies in flight land first
     if (lane == 0) atomicAdd(p.timeouts, 1u);
-    if constexpr (TMA) {
+    {
       int none = 0;
       for (int r = rounds < S::kStages ? 0 : rounds - S::kStages; r < rounds; ++r)
         if (!wait_for<false>(smem_u32(&sh.full[r % S::kStages]), (r / S::kStages) & 1, &none, 1 << 10) && lane == 0)
@@ -683,9 +731,9 @@ int launch_walk(const ScanParams &p, cudaStream_t stream) {
   return launch_op(gated_walk_kernel<TYPE, VECTOR, BACK>, dim3((unsigned)blocks), kWalkThreads, 0, 1, stream, p);
 }
 
-template <int TYPE, bool TMA, bool BACK>
+template <int TYPE, bool TMA, bool BACK, int LANES>
 int launch_tiles(const ScanParams &scan, int sms, uint32_t *timeouts, cudaStream_t stream) {
-  using S = Tile<TYPE, TMA, BACK>;
+  using S = Tile<TYPE, TMA, BACK, LANES>;
   TileParams p = {};
   static_cast<ScanParams &>(p) = scan;
   p.timeouts = timeouts;
@@ -711,7 +759,7 @@ int launch_tiles(const ScanParams &scan, int sms, uint32_t *timeouts, cudaStream
         return cuda_failure((int)cudaErrorNotSupported);
     }
   }
-  auto fn = gated_tile_kernel<TYPE, TMA, BACK>;
+  auto fn = gated_tile_kernel<TYPE, TMA, BACK, LANES>;
   const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -733,8 +781,13 @@ int launch_scan(const ScanParams &p, int sms, uint32_t *timeouts, cudaStream_t s
            (p.batch == 1 || (s.batch > 0 && s.batch * es < (1ll << 40)));
   };
   const bool tma = vectors && mapped(p.x) && mapped(p.g) && (!BACK || mapped(p.h));
-  return tma ? launch_tiles<TYPE, true, BACK>(p, sms, timeouts, stream)
-             : launch_tiles<TYPE, false, BACK>(p, sms, timeouts, stream);
+  // Chains of 128 bytes; of 64 where clusters of those would leave SMs without a CTA.
+  const int64_t wide = p.batch * ((p.width * es + 127) / 128) * kMaxScanCluster;
+  if (wide < sms)
+    return tma ? launch_tiles<TYPE, true, BACK, 8>(p, sms, timeouts, stream)
+               : launch_tiles<TYPE, false, BACK, 8>(p, sms, timeouts, stream);
+  return tma ? launch_tiles<TYPE, true, BACK, 16>(p, sms, timeouts, stream)
+             : launch_tiles<TYPE, false, BACK, 16>(p, sms, timeouts, stream);
 }
 
 int dispatch_scan(const ScanParams &p, bool backward, int dtype, int dev, int sms, cudaStream_t stream) {
