@@ -9,10 +9,11 @@
 // of a row of C.
 //
 // Operand tiles are 128 bytes of k wide (64 16-bit or 128 8-bit elements) in
-// the 128-byte swizzle, in a ring of stages.  Warp 0 fills the ring by TMA (or
-// warps 4 to 7 by plain loads, where a base or row stride is not a multiple of
-// 16 bytes), one thread of warp 1 issues the matrix instructions, eight warps
-// write the result.
+// the 128-byte swizzle, in a ring of stages.  Warp 0 fills the ring by TMA, one
+// thread of warp 1 issues the matrix instructions, eight warps write the result.
+// Where a base or row stride is not a multiple of 16 bytes, warps 4 to 11 copy
+// the aligned 16-byte blocks that cover each row instead (cp.async, two steps
+// ahead) and shift them into place.
 //
 // Two kernels:
 //  * gemm_split_kernel, one tile per CTA: clusters of up to 8 CTAs share a tile
@@ -40,8 +41,11 @@ constexpr int kMaxStages = 8;
 constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
 constexpr int kPolls = kWaitPolls;               // polls of one wait before it gives up
 constexpr int kEpilogueWarps = 8;                 // of gemm_pair_kernel
-constexpr int kSplitThreads = 256, kPairThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kGatherWarps = 4;                  // warps 4 to 7
+constexpr int kSplitThreads = 256, kGatherThreads = 384, kPairThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kGatherWarps = 8;                  // warps 4 to 11
+constexpr int kGatherRows = kGatherWarps * 4;    // that they take at once: eight lanes a row
+constexpr int kRawStages = 3;                    // of their copies, each thread's blocks and one more per row:
+constexpr int kRawUnit = kGatherWarps * (512 + 64);  // bytes for kGatherRows rows
 constexpr int kSplitBand = 16, kPairBand = 8;    // tiles along n that run side by side
 constexpr int kAccumulators = 2;                 // of gemm_pair_kernel
 constexpr int kAccumulatorColumns = 256;
@@ -274,73 +278,63 @@ __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int ban
 
 // ------------------------------------------------------- operands without TMA --
 
-// The 16 bytes that start `shift` bytes into the 32 bytes lo ++ hi.
-__device__ __forceinline__ uint4 funnel(const uint4 &lo, const uint4 &hi, int shift) {
-  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  if (shift & 8) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (shift & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const int bits = (shift & 3) * 8;
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
 // The first `bytes` of v, the rest zero.
-__device__ __forceinline__ uint4 head_bytes(uint4 v, int64_t bytes) {
+__device__ __forceinline__ uint4 head_bytes(uint4 v, int bytes) {
   if (bytes >= 16) return v;
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t keep = bytes - 4 * i;
+    const int keep = bytes - 4 * i;
     if (keep <= 0) w[i] = 0u;
-    else if (keep < 4) w[i] &= (1u << (8 * (int)keep)) - 1u;
+    else if (keep < 4) w[i] &= (1u << (8 * keep)) - 1u;
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows [row0, row0 + rows) x 128 bytes of k from `kb`, read as the aligned
-// 16-byte blocks that hold their bytes (a lane's upper block is its
-// neighbour's lower one), shifted into place and stored swizzled.  Eight lanes
-// cover a row; `t` numbers the 128 gathering threads.
-template <int BATCH>
-__device__ __forceinline__ void gather_rows(const char *base, int64_t ld, int64_t row0, int64_t limit, int64_t kb,
-                                            int64_t k_bytes, int rows, uint32_t tile, int t) {
-  const int chunk = t & 7;
-  for (int r0 = t >> 3; r0 < rows; r0 += 16 * BATCH) {
-    uint4 lo[BATCH], hi[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int64_t row = row0 + r0 + 16 * u;
-      const uintptr_t start = (uintptr_t)base + (uintptr_t)(row * ld), end = start + (uintptr_t)k_bytes;
-      const uintptr_t block = (start + (uintptr_t)(kb + 16 * chunk)) & ~(uintptr_t)15;
-      const bool in = r0 + 16 * u < rows && row < limit;
-      lo[u] = in && block < end ? __ldg(reinterpret_cast<const uint4 *>(block)) : zero4();
-      hi[u] = in && chunk == 7 && (start & 15) && block + 16 < end ? __ldg(reinterpret_cast<const uint4 *>(block + 16))
-                                                                   : zero4();
-    }
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const int r = r0 + 16 * u;
-      uint4 up;
-      up.x = __shfl_down_sync(0xffffffffu, lo[u].x, 1, 8);
-      up.y = __shfl_down_sync(0xffffffffu, lo[u].y, 1, 8);
-      up.z = __shfl_down_sync(0xffffffffu, lo[u].z, 1, 8);
-      up.w = __shfl_down_sync(0xffffffffu, lo[u].w, 1, 8);
-      if (chunk == 7) up = hi[u];
-      const int shift = (int)(((uintptr_t)base + (uintptr_t)((row0 + r) * ld)) & 15);
-      const uint4 v = head_bytes(funnel(lo[u], up, shift), k_bytes - kb - 16 * chunk);
-      if (r < rows) {
-        const uint32_t at = tile + (uint32_t)r * kRowBytes + (uint32_t)((chunk ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-      }
+// 16 bytes to shared memory without passing a register, zeros if not `in`.
+__device__ __forceinline__ void copy16(uint32_t dst, uintptr_t src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// One thread's part of an operand without TMA: 16-byte chunk `chunk` of rows
+// row, row + 32, ... of a tile.  Rows 32 apart start at the same offset within
+// 16 bytes whatever the stride, so a thread shifts by one amount.
+struct Gathered {
+  uintptr_t at;     // its first row's chunk, at the first byte of k
+  int64_t between;  // bytes from row to row of its own
+  int off, live;    // offset within 16 bytes, rows that exist
+  __device__ Gathered(const char *base, int64_t ld, int64_t first, int64_t count, int row, int chunk)
+      : at((uintptr_t)base + (uintptr_t)((first + row) * ld) + 16 * chunk), between(kGatherRows * ld),
+        off((int)(at & 15)), live((int)(count > row ? (count - row + kGatherRows - 1) / kGatherRows : 0)) {}
+  // Blocks of a step that begins kb bytes into k, of which `left` remain from
+  // this chunk on; `last`: also the block after, for a row's last chunk.
+  __device__ __forceinline__ void request(uint32_t to, uint32_t extra, int units, int64_t kb, int left, bool last) const {
+    uintptr_t src = (at + (uintptr_t)kb) & ~(uintptr_t)15;
+    const bool in = left + off > 0, more = left + off > 16;
+#pragma unroll 4
+    for (int u = 0; u < units; ++u) {
+      copy16(to + u * kRawUnit, src, in && u < live);
+      if (last) copy16(extra + u * kRawUnit, src + 16, more && u < live);
+      src += (uintptr_t)between;
     }
   }
+};
+
+// The 16 bytes `off` into lo ++ hi, by selections: off differs between the
+// rows of a warp.
+__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int off) {
+  const bool by8 = off & 8, by4 = off & 4;
+  const int bits = (off & 3) * 8;
+  const uint32_t a0 = by8 ? lo.z : lo.x, a1 = by8 ? lo.w : lo.y, a2 = by8 ? hi.x : lo.z, a3 = by8 ? hi.y : lo.w,
+                 a4 = by8 ? hi.z : hi.x, a5 = by8 ? hi.w : hi.y;
+  const uint32_t b0 = by4 ? a1 : a0, b1 = by4 ? a2 : a1, b2 = by4 ? a3 : a2, b3 = by4 ? a4 : a3, b4 = by4 ? a5 : a4;
+  return make_uint4(__funnelshift_r(b0, b1, bits), __funnelshift_r(b1, b2, bits), __funnelshift_r(b2, b3, bits),
+                    __funnelshift_r(b3, b4, bits));
 }
 
 // ------------------------------------------------------------- split kernel --
@@ -353,7 +347,9 @@ struct alignas(16) SplitShared {
 };
 
 template <bool E4M3, bool GATHER>
-__global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmParams p) {
+__global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
+    gemm_split_kernel(const __grid_constant__ GemmParams p) {
+  constexpr int kThreads = GATHER ? kGatherThreads : kSplitThreads;
   extern __shared__ char dynamic[];
   __shared__ SplitShared sh;
   const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;  // swizzled tiles start on 1024 bytes
@@ -407,19 +403,68 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     }
     if (elected) sh.issued = step - begin;
   } else if (GATHER && warp >= 4) {
+    const int id = threadIdx.x - 128, row = id >> 3, chunk = id & 7;
+    const bool last = chunk == 7;
+    const int64_t rows_left = p.m - i0 < p.cols ? p.m - i0 : p.cols;
+    const Gathered rows_b(p.B, p.ldb_bytes, j0, p.n - j0, row, chunk), rows_a(p.A, p.lda_bytes, i0, rows_left, row, chunk);
+    constexpr int kUnitsB = kTileRows / kGatherRows, kBatch = 4;
+    const int units_a = (p.cols + kGatherRows - 1) / kGatherRows;
+    const uint32_t raw = tiles + p.stages * stage_bytes + (warp - 4) * (512 + 64), raw_bytes = (kUnitsB + units_a) * kRawUnit;
+    const uint32_t own = lane * 16, extra = 512 + (lane >> 3) * 16, after = last ? extra : own + 16;
+    const int64_t k_here = p.k_bytes - 16 * chunk;
+    auto left_of = [&](int step) {  // bytes of k from this thread's chunk on, as far as they matter
+      const int64_t left = k_here - (int64_t)step * kRowBytes;
+      return (int)(left > 64 ? 64 : left < -64 ? -64 : left);
+    };
+    auto request = [&](int step) {
+      if (step < end) {
+        const uint32_t to = raw + (uint32_t)((step - begin) % kRawStages) * raw_bytes;
+        const int left = left_of(step);
+        rows_b.request(to + own, to + extra, kUnitsB, (int64_t)step * kRowBytes, left, last);
+        rows_a.request(to + kUnitsB * kRawUnit + own, to + kUnitsB * kRawUnit + extra, units_a, (int64_t)step * kRowBytes,
+                       left, last);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int s = 0; s < kRawStages - 1; ++s) request(begin + s);
     Ring r;
-    const int t = threadIdx.x - 4 * 32;
     for (int step = begin; step < end; ++step) {
+      request(step + kRawStages - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRawStages - 1) : "memory");
+      __syncwarp();
       if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
-      const uint32_t at = tiles + r.stage * stage_bytes;
-      const int64_t kb = (int64_t)step * kRowBytes;
-      gather_rows<8>(p.B, p.ldb_bytes, j0, p.n, kb, p.k_bytes, kTileRows, at, t);
-      gather_rows<4>(p.A, p.lda_bytes, i0, p.m, kb, p.k_bytes, p.cols, at + kTileBytes, t);
+      const int left = left_of(step);
+      const uint32_t from = raw + (uint32_t)((step - begin) % kRawStages) * raw_bytes;
+      const uint32_t to = tiles + r.stage * stage_bytes + row * kRowBytes + (uint32_t)((chunk ^ (row & 7)) << 4);
+      // kBatch units of rows at a time, their loads together
+      auto shift = [&](int u0, int units, int off, int rows) {
+        uint4 lo[kBatch], hi[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (u < units) {
+            lo[u] = lds128(from + (u0 + u) * kRawUnit + own);
+            hi[u] = lds128(from + (u0 + u) * kRawUnit + after);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          if (u < units && row + u * kGatherRows < rows) {
+            uint4 v = shifted(lo[u], hi[u], off);
+            if (left < 16) v = head_bytes(v, left);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (u0 + u) * kGatherRows * kRowBytes),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+        }
+      };
+      shift(0, kUnitsB, rows_b.off, kTileRows);
+      shift(kUnitsB, units_a, rows_a.off, p.cols);
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.full[r.stage]));
       r.next(p.stages);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     const bool elected = elect_one();
     Ring r;
@@ -463,15 +508,16 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   }
   if (p.splits > 1) cluster_sync();
 
-  // All eight warps: a quarter of the lanes each (the one TMEM gives them), and
-  // every other 16 columns.
+  // All warps: a quarter of the lanes each (the one TMEM gives them), and 16
+  // columns in turn.
+  constexpr int kTurns = kThreads / 128;
   const int quarter = warp & 3, turn = warp >> 2, l = quarter * 32 + lane;
   const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
   if (p.splits == 1) {
     with_column(p, [&](auto col) {
       col.begin(p, j0 + l);
 #pragma unroll 1
-      for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 32) {
+      for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 16 * kTurns) {
         float v[16];
         tmem_load16(from + c, v);
         if (empty || failed) {
@@ -484,7 +530,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   } else {
     // Column c goes to CTA c / share, as [source][column][lane].
     const int share = p.cols / p.splits;
-    for (int c = turn * 16; c < p.cols; c += 32) {
+    for (int c = turn * 16; c < p.cols; c += 16 * kTurns) {
       float v[16];
       tmem_load16(from + c, v);
       int to = c / share, at = c - to * share;
@@ -504,7 +550,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
       col.begin(p, j0 + l);
       constexpr int kAtOnce = 4;
 #pragma unroll 1
-      for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += 2 * kAtOnce) {
+      for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += kTurns * kAtOnce) {
         float v[kAtOnce] = {};
         for (int s = 0; s < p.splits; ++s) {
 #pragma unroll
@@ -726,6 +772,7 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kSmemHalf = 112 * 1024;   // dynamic shared memory that leaves room for two CTAs per SM
 constexpr int kSmemAlone = 225 * 1024;  // and for one
 constexpr int kMinStages = 3;
+constexpr int kGatherColumns = 128;  // most columns per tile of operands without TMA: their copies take the rest
 
 // The launch that gemm_plan() chooses.
 struct GemmPlan {
@@ -762,8 +809,8 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, b
     p.us = (work > stream ? work + 0.25 * stream : stream + 0.25 * work) + call;
     if (p.us < best.us) best = p;
   };
-  const int64_t fewest = cdiv64(m, kAccumulatorColumns);
-  for (int64_t t = fewest; t < fewest + 8; ++t) {
+  const int64_t fewest = cdiv64(m, kAccumulatorColumns), fewest_split = tma ? fewest : cdiv64(m, kGatherColumns);
+  for (int64_t t = fewest_split; t < fewest_split + 8; ++t) {
     GemmPlan p = {};
     p.cols = (int)(cdiv64(cdiv64(m, t), 16) * 16);
     p.tiles_m = (int)cdiv64(m, p.cols);
@@ -771,20 +818,21 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, b
     if (p.tiles_m < t) break;  // 16 columns already
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     const int stage = kTileBytes + p.cols * kRowBytes;
+    const int raw = tma ? 0 : kRawStages * (int)(kTileRows / kGatherRows + cdiv64(p.cols, kGatherRows)) * kRawUnit;
     for (int alone = 0; alone < 2; ++alone) {
       const int room = alone ? kSmemAlone : kSmemHalf;
-      p.stages = (room - 1024) / stage < kMaxStages ? (room - 1024) / stage : kMaxStages;
-      if (p.stages < kMinStages) continue;
+      p.stages = (room - 1024 - raw) / stage < kMaxStages ? (room - 1024 - raw) / stage : kMaxStages;
+      if (p.stages < (tma ? kMinStages : 2)) continue;
       for (p.splits = 1; p.splits <= 8; p.splits *= 2) {
         if (p.splits > 1 && steps / p.splits < 4) break;
         const int64_t ctas = tiles * p.splits;
-        const int64_t ring = (int64_t)p.stages * stage;
+        const int64_t ring = (int64_t)p.stages * stage + raw;
         const int64_t exchange = p.splits > 1 ? (int64_t)p.cols * kTileRows * 4 : 0;
         if (exchange > room - 1024) break;
         p.smem = (ring > exchange ? ring : exchange) + 1024;
         if (p.splits > 1 && 7 * ctas > 6 * (alone ? sms : 2 * sms)) break;
         const bool shared = !alone && ctas > sms;
-        const double step = (0.13 + 0.00085 * p.cols) * (shared ? 1.75 : 1.0);
+        const double step = (tma ? 0.13 + 0.00085 * p.cols : 0.1 + 0.0017 * (kTileRows + p.cols)) * (shared ? 1.75 : 1.0);
         const double waves = (double)cdiv64(ctas, shared ? 2 * sms : sms);
         const double work = waves * (cdiv64(steps, p.splits) * step + 0.008 * p.cols / p.splits);
         // a deeper ring where it costs nothing
@@ -891,5 +939,5 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
     cudaGetLastError();
     return cuda_failure((int)e);
   }
-  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : kSplitThreads, (size_t)plan.smem, pair ? 2 : p.splits, stream, p);
+  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : tma ? kSplitThreads : kGatherThreads, (size_t)plan.smem, pair ? 2 : p.splits, stream, p);
 }
