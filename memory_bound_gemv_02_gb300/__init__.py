@@ -13,8 +13,8 @@ Names follow the C entry points: ``gemv``, ``gemv_ex``, ``gemv_fused``, ``gemv_p
 ``gemv_last_cuda_error``, ``gemv_debug_inject``, ``gemv_release``,
 ``gemv_host``, ``gemv_splitk_noalloc``, ``gemv_wait_timeouts``,
 ``gemv_debug_wait_budget``, ``gla_decode``, ``gla_decode_ex``, and the operators
-of include/gemv_ops.h: ``rms_norm_fused``, ``gemm_fused``, ``gated_scan``,
-``gated_scan_backward``.
+of include/gemv_ops.h: ``rms_norm_fused``, ``gemm_fused``,
+``gemm_workspace``, ``gated_scan``, ``gated_scan_backward``.
 """
 from __future__ import annotations
 
@@ -52,7 +52,7 @@ ENTRY_POINTS = ("gemv", "gemv_ex", "gemv_fused", "gemv_prepare", "gemv_plan", "g
 
 
 #: the entry points of include/gemv_ops.h
-OPERATOR_ENTRY_POINTS = ("rms_norm_fused", "gemm_fused", "gated_scan", "gated_scan_backward")
+OPERATOR_ENTRY_POINTS = ("rms_norm_fused", "gemm_fused", "gemm_workspace", "gated_scan", "gated_scan_backward")
 
 
 class GemvConfig(ctypes.Structure):
@@ -138,7 +138,9 @@ def _lib_with_operators() -> ctypes.CDLL:
     seq = [vp, i64, i64]
     L.rms_norm_fused.argtypes = [vp, i64, vp, i64, vp, i32, vp, i64, vp, vp, i64, i64, i64, ctypes.c_float, i32, i32,
                                  vp]
-    L.gemm_fused.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp, vp]  # epilogue: a structure or its bytes
+    L.gemm_fused.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, i32, i32, vp, vp, i64,
+                             vp]  # epilogue: a structure or its bytes
+    L.gemm_workspace.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, ctypes.POINTER(i64)]
     L.gated_scan.argtypes = seq + seq + [vp] + seq + [vp, i64, i64, i64, i32, vp]
     L.gated_scan_backward.argtypes = seq * 3 + [vp, vp] + seq * 2 + [vp, i64, i64, i64, i32, vp]
     for name in OPERATOR_ENTRY_POINTS:
@@ -397,4 +399,4 @@ def gla_decode(q, k, v, gk, S, scale: float, S_new=None, o=None, stream=None, va
 # The operators around the product, built on the helpers above.
 from ._operators import (GEMM_ACTIVATIONS, GEMV_ACT_LOG_SIGMOID, GEMV_TYPE_BF16, GEMV_TYPE_E4M3,  # noqa: E402
                          GEMV_TYPE_F16, GEMV_TYPE_F32, GemmEpilogue, gated_scan, gated_scan_backward, gemm_fused,
-                         rms_norm_fused)
+                         gemm_workspace, rms_norm_fused)

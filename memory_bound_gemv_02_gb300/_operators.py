@@ -1,5 +1,5 @@
 """Python entry points of the operators in include/gemv_ops.h, with the C
-names: ``rms_norm_fused``, ``gemm_fused``, ``gated_scan`` and
+names: ``rms_norm_fused``, ``gemm_fused``, ``gemm_workspace``, ``gated_scan`` and
 ``gated_scan_backward`` (imported into the package).  As in the package
 itself, tensors are only turned into pointers, sizes and strides.
 
@@ -147,7 +147,8 @@ def gemm_fused(B, A, c=None, out_dtype=None, alpha: float = 1.0, beta: float = 1
     ``scale_a`` (m,) and ``scale_b`` (n,): float32.  ``bias``: (n,), float32 or
     the output's dtype.  ``residual``: (m, n) in the output's dtype, may be
     ``c``.  ``activation``: 'none', 'relu', 'sigmoid', 'silu' or 'log_sigmoid'.
-    Returns c (m, n)."""
+    Operands with rows off 16 bytes are copied first (memory from torch's
+    allocator).  Returns c (m, n)."""
     dt, shape_a, shape_b, dev = A.dtype, A.shape, B.shape, A.get_device()
     if len(shape_a) != 2 or len(shape_b) != 2 or shape_a[1] != shape_b[1]:
         raise ValueError(f"shape mismatch: B {tuple(shape_b)}, A {tuple(shape_a)}")
@@ -175,10 +176,32 @@ def gemm_fused(B, A, c=None, out_dtype=None, alpha: float = 1.0, beta: float = 1
                         _vector(bias, "bias", n, _F32, out_dtype, dev) or 0, rp, ldr,
                         out_code if bias is not None and bias.dtype is out_dtype else GEMV_TYPE_F32,
                         GEMM_ACTIVATIONS[activation])
+    pb, pa = B.data_ptr(), A.data_ptr()
+    es = 1 if dt is _E4M3 else 2
+    space = ws = None
+    if k and m and n and (pa | pb | (lda * es if m > 1 else 0) | (ldb * es if n > 1 else 0)) & 15:
+        need = ctypes.c_int64(0)
+        _check(_lib_with_operators().gemm_workspace(pb, ldb, pa, lda, m, n, k, TYPE_CODES[dt], ctypes.byref(need)),
+               "gemm_workspace")
+        space = need.value
+        ws = torch.empty(space, dtype=torch.uint8, device=A.device)
+        if stream is not None:  # keep the memory until that stream is past the call
+            ws.record_stream(torch.cuda.ExternalStream(_stream_handle(stream), device=A.device))
     _launch(dev, stream, _lib_with_operators().gemm_fused,
-            (B.data_ptr(), ldb, A.data_ptr(), lda, c.data_ptr(), ldc, m, n, k, TYPE_CODES[dt], out_code, ep),
-            "gemm_fused")
+            (pb, ldb, pa, lda, c.data_ptr(), ldc, m, n, k, TYPE_CODES[dt], out_code, ep,
+             None if ws is None else ws.data_ptr(), space or 0), "gemm_fused")
     return c
+
+
+def gemm_workspace(B, A) -> int:
+    """Bytes that ``gemm_fused`` copies for these operands: 0 where their bases
+    and row strides are multiples of 16 bytes."""
+    dt, dev = A.dtype, A.get_device()
+    lda, ldb = _rows(A, "A", A.shape, dt, dev), _rows(B, "B", B.shape, dt, dev)
+    need = ctypes.c_int64(0)
+    _check(_lib_with_operators().gemm_workspace(B.data_ptr(), ldb, A.data_ptr(), lda, A.shape[0], B.shape[0],
+                                                A.shape[1], TYPE_CODES[dt], ctypes.byref(need)), "gemm_workspace")
+    return need.value
 
 
 def _sequence(t, name: str, shape, dtype, device: int):

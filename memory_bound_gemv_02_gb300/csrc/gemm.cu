@@ -11,9 +11,12 @@
 // Operand tiles are 128 bytes of k wide (64 16-bit or 128 8-bit elements) in
 // the 128-byte swizzle, in a ring of stages.  Warp 0 fills the ring by TMA, one
 // thread of warp 1 issues the matrix instructions, eight warps write the result.
-// Where a base or row stride is not a multiple of 16 bytes, warps 4 to 11 copy
-// the aligned 16-byte blocks that cover each row instead (cp.async, two steps
-// ahead) and shift them into place.
+// An operand whose base or row stride is not a multiple of 16 bytes is first
+// copied to the workspace with rows that are (gemm_align_kernel).  Shifting its
+// rows into place within the product was slower at every size, even for a
+// single vector (77 x 4099 x 7169 fp16: 72 us with cp.async of the covering
+// blocks, 220 with a bulk copy per row): each CTA's 128-byte pieces of 128 rows
+// are the wrong shape for anything but a tensor map.
 //
 // Two kernels:
 //  * gemm_split_kernel, one tile per CTA: clusters of up to 8 CTAs share a tile
@@ -41,22 +44,16 @@ constexpr int kMaxStages = 8;
 constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
 constexpr int kPolls = kWaitPolls;               // polls of one wait before it gives up
 constexpr int kEpilogueWarps = 8;                 // of gemm_pair_kernel
-constexpr int kSplitThreads = 256, kGatherThreads = 384, kPairThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kGatherWarps = 8;                  // warps 4 to 11
-constexpr int kGatherRows = kGatherWarps * 4;    // that they take at once: eight lanes a row
-constexpr int kRawStages = 3;                    // of their copies, each thread's blocks and one more per row:
-constexpr int kRawUnit = kGatherWarps * (512 + 64);  // bytes for kGatherRows rows
+constexpr int kSplitThreads = 256, kAlignThreads = 256, kPairThreads = 64 + 32 * kEpilogueWarps;
 constexpr int kSplitBand = 16, kPairBand = 8;    // tiles along n that run side by side
 constexpr int kAccumulators = 2;                 // of gemm_pair_kernel
 constexpr int kAccumulatorColumns = 256;
 
 struct GemmParams {
   CUtensorMap map_b, map_a;
-  const char *B, *A;
   void *C;
-  int64_t ldb_bytes, lda_bytes, ldc, ldr;
+  int64_t ldc, ldr;
   int32_t m, n;
-  int64_t k_bytes;
   int32_t steps;              // 128-byte steps of k
   int32_t cols;               // columns (vectors) per tile
   int32_t tiles_n, tiles_m;   // tiles along n and along m
@@ -276,65 +273,67 @@ __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int ban
   *tn = first + in - *tm * width;
 }
 
-// ------------------------------------------------------- operands without TMA --
+// -------------------------------------------------------- rows off 16 bytes --
 
-// The first `bytes` of v, the rest zero.
-__device__ __forceinline__ uint4 head_bytes(uint4 v, int bytes) {
-  if (bytes >= 16) return v;
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int keep = bytes - 4 * i;
-    if (keep <= 0) w[i] = 0u;
-    else if (keep < 4) w[i] &= (1u << (8 * keep)) - 1u;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// 16 bytes to shared memory without passing a register, zeros if not `in`.
-__device__ __forceinline__ void copy16(uint32_t dst, uintptr_t src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
-// One thread's part of an operand without TMA: 16-byte chunk `chunk` of rows
-// row, row + 32, ... of a tile.  Rows 32 apart start at the same offset within
-// 16 bytes whatever the stride, so a thread shifts by one amount.
-struct Gathered {
-  uintptr_t at;     // its first row's chunk, at the first byte of k
-  int64_t between;  // bytes from row to row of its own
-  int off, live;    // offset within 16 bytes, rows that exist
-  __device__ Gathered(const char *base, int64_t ld, int64_t first, int64_t count, int row, int chunk)
-      : at((uintptr_t)base + (uintptr_t)((first + row) * ld) + 16 * chunk), between(kGatherRows * ld),
-        off((int)(at & 15)), live((int)(count > row ? (count - row + kGatherRows - 1) / kGatherRows : 0)) {}
-  // Blocks of a step that begins kb bytes into k, of which `left` remain from
-  // this chunk on; `last`: also the block after, for a row's last chunk.
-  __device__ __forceinline__ void request(uint32_t to, uint32_t extra, int units, int64_t kb, int left, bool last) const {
-    uintptr_t src = (at + (uintptr_t)kb) & ~(uintptr_t)15;
-    const bool in = left + off > 0, more = left + off > 16;
-#pragma unroll 4
-    for (int u = 0; u < units; ++u) {
-      copy16(to + u * kRawUnit, src, in && u < live);
-      if (last) copy16(extra + u * kRawUnit, src + 16, more && u < live);
-      src += (uintptr_t)between;
-    }
-  }
+// One operand to copy: `rows` rows of `bytes` bytes, `ld` apart, to rows of
+// `pitch` (a multiple of 16) in the workspace; `pieces` of 2 KB per row.
+struct AlignJob {
+  const char *src;
+  char *dst;
+  int64_t ld, bytes, pitch, pieces, total;  // total: rows x pieces
+};
+struct AlignParams {
+  AlignJob job[2];
 };
 
-// The 16 bytes `off` into lo ++ hi, by selections: off differs between the
-// rows of a warp.
+// The 16 bytes `off` into lo ++ hi; off is the same for the whole warp.
+template <int WORD>
+__device__ __forceinline__ uint4 shifted_words(const uint4 &lo, const uint4 &hi, int bits) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  return make_uint4(__funnelshift_r(w[WORD], w[WORD + 1], bits), __funnelshift_r(w[WORD + 1], w[WORD + 2], bits),
+                    __funnelshift_r(w[WORD + 2], w[WORD + 3], bits), __funnelshift_r(w[WORD + 3], w[WORD + 4], bits));
+}
 __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int off) {
-  const bool by8 = off & 8, by4 = off & 4;
   const int bits = (off & 3) * 8;
-  const uint32_t a0 = by8 ? lo.z : lo.x, a1 = by8 ? lo.w : lo.y, a2 = by8 ? hi.x : lo.z, a3 = by8 ? hi.y : lo.w,
-                 a4 = by8 ? hi.z : hi.x, a5 = by8 ? hi.w : hi.y;
-  const uint32_t b0 = by4 ? a1 : a0, b1 = by4 ? a2 : a1, b2 = by4 ? a3 : a2, b3 = by4 ? a4 : a3, b4 = by4 ? a5 : a4;
-  return make_uint4(__funnelshift_r(b0, b1, bits), __funnelshift_r(b1, b2, bits), __funnelshift_r(b2, b3, bits),
-                    __funnelshift_r(b3, b4, bits));
+  if (off < 8) return off < 4 ? shifted_words<0>(lo, hi, bits) : shifted_words<1>(lo, hi, bits);
+  return off < 12 ? shifted_words<2>(lo, hi, bits) : shifted_words<3>(lo, hi, bits);
+}
+
+// A warp copies a piece: four times 512 bytes of a row, read as the aligned
+// 16-byte blocks that hold them (a lane's upper block is its neighbour's lower
+// one).  Memory-bound: it reads and writes the operand once.
+__global__ void __launch_bounds__(kAlignThreads) gemm_align_kernel(AlignParams p) {
+  allow_dependents();
+  wait_for_predecessor();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kAlignThreads / 32);
+  for (int64_t i = (int64_t)blockIdx.x * (kAlignThreads / 32) + (threadIdx.x >> 5); i < p.job[0].total + p.job[1].total;
+       i += warps) {
+    const AlignJob &j = i < p.job[0].total ? p.job[0] : p.job[1];
+    const int64_t n = i < p.job[0].total ? i : i - p.job[0].total, row = n / j.pieces, piece = n - row * j.pieces;
+    const uintptr_t start = (uintptr_t)(j.src + row * j.ld), end = start + (uintptr_t)j.bytes;
+    const int off = (int)(start & 15);
+    const uintptr_t block = start - off + (uintptr_t)(piece * 2048 + lane * 16);
+    char *to = j.dst + row * j.pitch + piece * 2048 + lane * 16;
+    uint4 lo[4], hi[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uintptr_t at = block + (uintptr_t)(u * 512);
+      lo[u] = at < end ? ldg_stream(reinterpret_cast<const uint4 *>(at)) : zero4();
+      hi[u] = lane == 31 && at + 16 < end ? ldg_stream(reinterpret_cast<const uint4 *>(at + 16)) : zero4();
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint4 up;
+      up.x = __shfl_down_sync(0xffffffffu, lo[u].x, 1);
+      up.y = __shfl_down_sync(0xffffffffu, lo[u].y, 1);
+      up.z = __shfl_down_sync(0xffffffffu, lo[u].z, 1);
+      up.w = __shfl_down_sync(0xffffffffu, lo[u].w, 1);
+      if (lane == 31) up = hi[u];
+      if (piece * 2048 + u * 512 + lane * 16 < j.pitch)
+        *reinterpret_cast<uint4 *>(to + u * 512) = shifted(lo[u], up, off);
+    }
+  }
 }
 
 // ------------------------------------------------------------- split kernel --
@@ -346,10 +345,8 @@ struct alignas(16) SplitShared {
   int issued;  // steps whose copies were started
 };
 
-template <bool E4M3, bool GATHER>
-__global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
-    gemm_split_kernel(const __grid_constant__ GemmParams p) {
-  constexpr int kThreads = GATHER ? kGatherThreads : kSplitThreads;
+template <bool E4M3>
+__global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ char dynamic[];
   __shared__ SplitShared sh;
   const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;  // swizzled tiles start on 1024 bytes
@@ -366,12 +363,12 @@ __global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
   if (threadIdx.x == 0) {
     sh.failed = 0;
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(smem_u32(&sh.full[s]), GATHER ? kGatherWarps : 1);
+      mbar_init(smem_u32(&sh.full[s]), 1);
       mbar_init(smem_u32(&sh.empty[s]), 1);
     }
     mbar_init(smem_u32(&sh.done), 1);
     mbar_init_fence();
-    if (!GATHER) {
+    if (p.steps > 0) {
       prefetch_map(&p.map_b);
       prefetch_map(&p.map_a);
     }
@@ -386,7 +383,7 @@ __global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
   allow_dependents();
   wait_for_predecessor();
 
-  if (!GATHER && warp == 0) {
+  if (warp == 0) {
     const bool elected = elect_one();
     Ring r;
     int step = begin;
@@ -402,69 +399,6 @@ __global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
       r.next(p.stages);
     }
     if (elected) sh.issued = step - begin;
-  } else if (GATHER && warp >= 4) {
-    const int id = threadIdx.x - 128, row = id >> 3, chunk = id & 7;
-    const bool last = chunk == 7;
-    const int64_t rows_left = p.m - i0 < p.cols ? p.m - i0 : p.cols;
-    const Gathered rows_b(p.B, p.ldb_bytes, j0, p.n - j0, row, chunk), rows_a(p.A, p.lda_bytes, i0, rows_left, row, chunk);
-    constexpr int kUnitsB = kTileRows / kGatherRows, kBatch = 4;
-    const int units_a = (p.cols + kGatherRows - 1) / kGatherRows;
-    const uint32_t raw = tiles + p.stages * stage_bytes + (warp - 4) * (512 + 64), raw_bytes = (kUnitsB + units_a) * kRawUnit;
-    const uint32_t own = lane * 16, extra = 512 + (lane >> 3) * 16, after = last ? extra : own + 16;
-    const int64_t k_here = p.k_bytes - 16 * chunk;
-    auto left_of = [&](int step) {  // bytes of k from this thread's chunk on, as far as they matter
-      const int64_t left = k_here - (int64_t)step * kRowBytes;
-      return (int)(left > 64 ? 64 : left < -64 ? -64 : left);
-    };
-    auto request = [&](int step) {
-      if (step < end) {
-        const uint32_t to = raw + (uint32_t)((step - begin) % kRawStages) * raw_bytes;
-        const int left = left_of(step);
-        rows_b.request(to + own, to + extra, kUnitsB, (int64_t)step * kRowBytes, left, last);
-        rows_a.request(to + kUnitsB * kRawUnit + own, to + kUnitsB * kRawUnit + extra, units_a, (int64_t)step * kRowBytes,
-                       left, last);
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    for (int s = 0; s < kRawStages - 1; ++s) request(begin + s);
-    Ring r;
-    for (int step = begin; step < end; ++step) {
-      request(step + kRawStages - 1);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRawStages - 1) : "memory");
-      __syncwarp();
-      if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
-      const int left = left_of(step);
-      const uint32_t from = raw + (uint32_t)((step - begin) % kRawStages) * raw_bytes;
-      const uint32_t to = tiles + r.stage * stage_bytes + row * kRowBytes + (uint32_t)((chunk ^ (row & 7)) << 4);
-      // kBatch units of rows at a time, their loads together
-      auto shift = [&](int u0, int units, int off, int rows) {
-        uint4 lo[kBatch], hi[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (u < units) {
-            lo[u] = lds128(from + (u0 + u) * kRawUnit + own);
-            hi[u] = lds128(from + (u0 + u) * kRawUnit + after);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          if (u < units && row + u * kGatherRows < rows) {
-            uint4 v = shifted(lo[u], hi[u], off);
-            if (left < 16) v = head_bytes(v, left);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + (u0 + u) * kGatherRows * kRowBytes),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
-        }
-      };
-      shift(0, kUnitsB, rows_b.off, kTileRows);
-      shift(kUnitsB, units_a, rows_a.off, p.cols);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.full[r.stage]));
-      r.next(p.stages);
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 1) {
     const bool elected = elect_one();
     Ring r;
@@ -495,7 +429,7 @@ __global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
   tc_fence_after();
   const float nan = __int_as_float(0x7fc00000);
   const bool empty = begin == end, failed = sh.failed != 0;
-  if (!GATHER && failed) {  // copies in flight land before their memory is used again
+  if (failed) {  // copies in flight land before their memory is used again
     if (warp == 0) {
       int none = 0;
       Ring d;
@@ -510,7 +444,7 @@ __global__ void __launch_bounds__(GATHER ? kGatherThreads : kSplitThreads)
 
   // All warps: a quarter of the lanes each (the one TMEM gives them), and 16
   // columns in turn.
-  constexpr int kTurns = kThreads / 128;
+  constexpr int kTurns = kSplitThreads / 128;
   const int quarter = warp & 3, turn = warp >> 2, l = quarter * 32 + lane;
   const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
   if (p.splits == 1) {
@@ -772,7 +706,6 @@ int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kSmemHalf = 112 * 1024;   // dynamic shared memory that leaves room for two CTAs per SM
 constexpr int kSmemAlone = 225 * 1024;  // and for one
 constexpr int kMinStages = 3;
-constexpr int kGatherColumns = 128;  // most columns per tile of operands without TMA: their copies take the rest
 
 // The launch that gemm_plan() chooses.
 struct GemmPlan {
@@ -801,7 +734,7 @@ struct GemmPlan {
 // of them (bf16, measured): 512 x 4096 x 4096 pairs of 128 columns 18.6, of 256
 // 23.0; 256 x 14336 x 4096 pairs 27.5, one tile per CTA 33.7; 256 x 1024 x 1024
 // 64 columns 6.8, 256 columns 12.0.
-GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, bool tma, int sms) {
+GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, int sms) {
   GemmPlan best = {};
   best.us = 1e30;
   const double stream = (double)operand_bytes / 6.2e6;
@@ -809,8 +742,8 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, b
     p.us = (work > stream ? work + 0.25 * stream : stream + 0.25 * work) + call;
     if (p.us < best.us) best = p;
   };
-  const int64_t fewest = cdiv64(m, kAccumulatorColumns), fewest_split = tma ? fewest : cdiv64(m, kGatherColumns);
-  for (int64_t t = fewest_split; t < fewest_split + 8; ++t) {
+  const int64_t fewest = cdiv64(m, kAccumulatorColumns);
+  for (int64_t t = fewest; t < fewest + 8; ++t) {
     GemmPlan p = {};
     p.cols = (int)(cdiv64(cdiv64(m, t), 16) * 16);
     p.tiles_m = (int)cdiv64(m, p.cols);
@@ -818,21 +751,20 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, b
     if (p.tiles_m < t) break;  // 16 columns already
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     const int stage = kTileBytes + p.cols * kRowBytes;
-    const int raw = tma ? 0 : kRawStages * (int)(kTileRows / kGatherRows + cdiv64(p.cols, kGatherRows)) * kRawUnit;
     for (int alone = 0; alone < 2; ++alone) {
       const int room = alone ? kSmemAlone : kSmemHalf;
-      p.stages = (room - 1024 - raw) / stage < kMaxStages ? (room - 1024 - raw) / stage : kMaxStages;
-      if (p.stages < (tma ? kMinStages : 2)) continue;
+      p.stages = (room - 1024) / stage < kMaxStages ? (room - 1024) / stage : kMaxStages;
+      if (p.stages < kMinStages) continue;
       for (p.splits = 1; p.splits <= 8; p.splits *= 2) {
         if (p.splits > 1 && steps / p.splits < 4) break;
         const int64_t ctas = tiles * p.splits;
-        const int64_t ring = (int64_t)p.stages * stage + raw;
+        const int64_t ring = (int64_t)p.stages * stage;
         const int64_t exchange = p.splits > 1 ? (int64_t)p.cols * kTileRows * 4 : 0;
         if (exchange > room - 1024) break;
         p.smem = (ring > exchange ? ring : exchange) + 1024;
         if (p.splits > 1 && 7 * ctas > 6 * (alone ? sms : 2 * sms)) break;
         const bool shared = !alone && ctas > sms;
-        const double step = (tma ? 0.13 + 0.00085 * p.cols : 0.1 + 0.0017 * (kTileRows + p.cols)) * (shared ? 1.75 : 1.0);
+        const double step = (0.13 + 0.00085 * p.cols) * (shared ? 1.75 : 1.0);
         const double waves = (double)cdiv64(ctas, shared ? 2 * sms : sms);
         const double work = waves * (cdiv64(steps, p.splits) * step + 0.008 * p.cols / p.splits);
         // a deeper ring where it costs nothing
@@ -840,7 +772,7 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, b
       }
     }
   }
-  if (!tma) return best;
+  if (steps == 0) return best;
   for (int64_t t = fewest; t < fewest + 4; ++t) {
     GemmPlan p = {};
     p.pair = true;
@@ -864,15 +796,43 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, b
 
 using namespace gemvk;
 
+namespace {
+
+int64_t aligned_pitch(int64_t k_bytes) { return (k_bytes + 15) / 16 * 16; }
+
+// Workspace for one operand: 0 where TMA reads it in place.
+int64_t operand_space(const void *p, int64_t rows, int64_t k_bytes, int64_t ld_bytes) {
+  if (rows == 0 || k_bytes == 0 || tma_ok(p, rows, ld_bytes)) return 0;
+  return (rows * aligned_pitch(k_bytes) + 255) / 256 * 256;
+}
+
+int check_sizes(int64_t ldb, int64_t lda, int64_t m, int64_t n, int64_t k, int dtype) {
+  if (dtype != GEMV_TYPE_F16 && dtype != GEMV_TYPE_BF16 && dtype != GEMV_TYPE_E4M3) return GEMV_ERR_DTYPE;
+  if (m < 0 || n < 0 || k < 0 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX) return GEMV_ERR_ARG;
+  if (ldb < k || lda < k || !span_fits(n, ldb) || !span_fits(m, lda)) return GEMV_ERR_ARG;
+  return GEMV_OK;
+}
+
+}  // namespace
+
+extern "C" int gemm_workspace(const void *B, int64_t ldb, const void *A, int64_t lda, int64_t m, int64_t n, int64_t k,
+                              int dtype, int64_t *bytes) {
+  const int st = check_sizes(ldb, lda, m, n, k, dtype);
+  if (st != GEMV_OK) return st;
+  if (bytes == nullptr) return GEMV_ERR_ARG;
+  const int es = type_bytes(dtype);
+  *bytes = m == 0 || n == 0 ? 0 : operand_space(B, n, k * es, ldb * es) + operand_space(A, m, k * es, lda * es);
+  return GEMV_OK;
+}
+
 extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda, void *C, int64_t ldc, int64_t m,
                           int64_t n, int64_t k, int dtype, int out_dtype, const gemm_epilogue *epilogue,
-                          cudaStream_t stream) {
-  if (dtype != GEMV_TYPE_F16 && dtype != GEMV_TYPE_BF16 && dtype != GEMV_TYPE_E4M3) return GEMV_ERR_DTYPE;
+                          void *workspace, int64_t workspace_bytes, cudaStream_t stream) {
+  int st = check_sizes(ldb, lda, m, n, k, dtype);
+  if (st != GEMV_OK) return st;
   if (out_dtype != GEMV_TYPE_F32 && out_dtype != GEMV_TYPE_F16 && out_dtype != GEMV_TYPE_BF16) return GEMV_ERR_DTYPE;
   if (dtype != GEMV_TYPE_E4M3 && out_dtype != dtype && out_dtype != GEMV_TYPE_F32) return GEMV_ERR_DTYPE;
-  if (m < 0 || n < 0 || k < 0 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX) return GEMV_ERR_ARG;
-  if (ldb < k || lda < k || ldc < n || !span_fits(n, ldb) || !span_fits(m, lda) || !span_fits(m, ldc))
-    return GEMV_ERR_ARG;
+  if (ldc < n || !span_fits(m, ldc)) return GEMV_ERR_ARG;
   gemm_epilogue ep = {};
   ep.alpha = 1.f;
   if (epilogue != nullptr) ep = *epilogue;
@@ -887,27 +847,34 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   if (((uintptr_t)C | (uintptr_t)ep.residual) % (uintptr_t)oe || (uintptr_t)ep.bias % (uintptr_t)be ||
       ((uintptr_t)ep.scale_a | (uintptr_t)ep.scale_b) % 4u)
     return GEMV_ERR_ALIGN;
-  const Rows RC{C, m, n * oe, ldc * oe}, RR{ep.residual, m, n * oe, ep.ldr * oe};
-  if (rows_overlap(RC, Rows{k > 0 ? A : nullptr, m, k * es, lda * es}) ||
-      rows_overlap(RC, Rows{k > 0 ? B : nullptr, n, k * es, ldb * es}) ||
-      rows_overlap(RC, Rows{ep.bias, 1, n * be, n * be}) || rows_overlap(RC, Rows{ep.scale_a, 1, m * 4, m * 4}) ||
-      rows_overlap(RC, Rows{ep.scale_b, 1, n * 4, n * 4}) ||
-      (rows_overlap(RC, RR) && !(ep.residual == C && ep.ldr == ldc)))
-    return GEMV_ERR_ALIAS;
+  const int64_t space_b = operand_space(B, n, k * es, ldb * es), space_a = operand_space(A, m, k * es, lda * es);
+  const int64_t space = space_b + space_a;
+  if (space > 0) {
+    if (workspace == nullptr || workspace_bytes < space) return GEMV_ERR_SCRATCH;
+    if ((uintptr_t)workspace % 16u) return GEMV_ERR_ALIGN;
+  } else {
+    workspace = nullptr;
+  }
+  const Rows RC{C, m, n * oe, ldc * oe}, RR{ep.residual, m, n * oe, ep.ldr * oe}, RW{workspace, 1, space, space};
+  const Rows inputs[] = {{k > 0 ? A : nullptr, m, k * es, lda * es}, {k > 0 ? B : nullptr, n, k * es, ldb * es},
+                         {ep.bias, 1, n * be, n * be}, {ep.scale_a, 1, m * 4, m * 4}, {ep.scale_b, 1, n * 4, n * 4}};
+  for (const Rows &r : inputs)
+    if (rows_overlap(RC, r) || rows_overlap(RW, r)) return GEMV_ERR_ALIAS;
+  if (rows_overlap(RW, RC) || rows_overlap(RW, RR)) return GEMV_ERR_ALIAS;
+  if (rows_overlap(RC, RR) && !(ep.residual == C && ep.ldr == ldc)) return GEMV_ERR_ALIAS;
   int dev = -1, sms = 0;
-  const int st = current_device(&dev, &sms);
+  st = current_device(&dev, &sms);
   if (st != GEMV_OK) return st;
-  if (!on_device(dev, {k > 0 ? A : nullptr, k > 0 ? B : nullptr, C, ep.scale_a, ep.scale_b, ep.bias, ep.residual}))
+  if (!on_device(dev, {k > 0 ? A : nullptr, k > 0 ? B : nullptr, C, ep.scale_a, ep.scale_b, ep.bias, ep.residual,
+                       workspace}))
     return GEMV_ERR_DEVICE;
   if (m == 1) ldc = ep.ldr = n;
   if ((ldc > ep.ldr ? ldc : ep.ldr) * oe > (int64_t)UINT32_MAX) return GEMV_ERR_ARG;
   GemmParams p = {};
-  p.B = static_cast<const char *>(B); p.A = static_cast<const char *>(A); p.C = C;
-  p.ldb_bytes = ldb * es; p.lda_bytes = lda * es; p.ldc = ldc; p.ldr = ep.ldr;
-  p.m = (int32_t)m; p.n = (int32_t)n; p.k_bytes = k * es;
-  const int64_t steps = cdiv64(p.k_bytes, kRowBytes);
-  if (steps > INT32_MAX) return GEMV_ERR_ARG;
-  p.steps = (int32_t)steps;
+  p.C = C;
+  p.ldc = ldc; p.ldr = ep.ldr;
+  p.m = (int32_t)m; p.n = (int32_t)n;
+  p.steps = (int32_t)cdiv64(k * es, kRowBytes);
   p.alpha = ep.alpha; p.beta = ep.beta;
   p.scale_a = ep.scale_a; p.scale_b = ep.scale_b; p.bias = ep.bias; p.residual = ep.residual;
   p.bias_f32 = ep.bias_dtype == GEMV_TYPE_F32 ? 1 : 0;
@@ -916,22 +883,43 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   // fp32 accumulators (bit 4); operand types in bits 7 and 10: 0 fp16 or e4m3, 1 bf16
   p.idesc = (1u << 4) | (dtype == GEMV_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
   p.polls = take_wait_budget(kPolls);
-  int st2 = wait_counter(dev, &p.timeouts);
-  if (st2 != GEMV_OK) return st2;
+  st = wait_counter(dev, &p.timeouts);
+  if (st != GEMV_OK) return st;
   const bool e4m3 = dtype == GEMV_TYPE_E4M3;
-  const bool tma = k > 0 && tma_ok(B, n, p.ldb_bytes) && tma_ok(A, m, p.lda_bytes);
-  const GemmPlan plan = gemm_plan(m, n, steps, (m + n) * k * es, tma, sms);
+  const GemmPlan plan = gemm_plan(m, n, p.steps, (m + n) * k * es, sms);
   const bool pair = plan.pair;
   p.cols = plan.cols; p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
   p.splits = plan.splits; p.stages = plan.stages;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles * p.splits > INT32_MAX / 2) return GEMV_ERR_ARG;
-  if (tma && (!encode(&p.map_b, B, dtype, n, k, p.ldb_bytes, kTileRows) ||
-              !encode(&p.map_a, A, dtype, m, k, p.lda_bytes, pair ? p.cols / 2 : p.cols)))
+  // operands that TMA cannot read in place, copied with rows that it can
+  int64_t ldb_bytes = ldb * es, lda_bytes = lda * es;
+  if (space > 0) {
+    AlignParams ap = {};
+    const int64_t pitch = aligned_pitch(k * es), pieces = cdiv64(pitch, 2048);
+    char *to = static_cast<char *>(workspace);
+    int jobs = 0;
+    if (space_b > 0) {
+      ap.job[jobs++] = {static_cast<const char *>(B), to, ldb_bytes, k * es, pitch, pieces, n * pieces};
+      B = to;
+      ldb_bytes = pitch;
+      to += space_b;
+    }
+    if (space_a > 0) {
+      ap.job[jobs++] = {static_cast<const char *>(A), to, lda_bytes, k * es, pitch, pieces, m * pieces};
+      A = to;
+      lda_bytes = pitch;
+    }
+    const int64_t blocks = cdiv64(ap.job[0].total + ap.job[1].total, kAlignThreads / 32);
+    st = launch_op(gemm_align_kernel, dim3((unsigned)(blocks < 64ll * sms ? blocks : 64ll * sms)), kAlignThreads, 0, 1,
+                   stream, ap);
+    if (st != GEMV_OK) return st;
+  }
+  if (k > 0 && (!encode(&p.map_b, B, dtype, n, k, ldb_bytes, kTileRows) ||
+                !encode(&p.map_a, A, dtype, m, k, lda_bytes, pair ? p.cols / 2 : p.cols)))
     return cuda_failure((int)cudaErrorNotSupported);
-  void (*fn)(GemmParams) = pair   ? (e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>)
-                           : tma  ? (e4m3 ? gemm_split_kernel<true, false> : gemm_split_kernel<false, false>)
-                           : e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>;
+  void (*fn)(GemmParams) = pair ? (e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>)
+                                : (e4m3 ? gemm_split_kernel<true> : gemm_split_kernel<false>);
   int64_t grid = tiles * p.splits;
   if (pair) grid = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlone);
@@ -939,5 +927,6 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
     cudaGetLastError();
     return cuda_failure((int)e);
   }
-  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : tma ? kSplitThreads : kGatherThreads, (size_t)plan.smem, pair ? 2 : p.splits, stream, p);
+  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : kSplitThreads, (size_t)plan.smem,
+                   pair ? 2 : p.splits, stream, p);
 }

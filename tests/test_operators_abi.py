@@ -54,11 +54,11 @@ def test_rms_norm_refusals(gemv_lib):
 def test_gemm_refusals(gemv_lib):
     g, L = gemv_lib, gemv_lib._lib_with_operators()
 
-    def call(B=P[0], ldb=64, A=P[1], lda=64, C=P[2], ldc=32, m=4, n=32, k=64, dt=1, ot=1, **ep):
+    def call(B=P[0], ldb=64, A=P[1], lda=64, C=P[2], ldc=32, m=4, n=32, k=64, dt=1, ot=1, ws=None, wb=0, **ep):
         e = g.GemmEpilogue(1.0, 1.0, None, None, None, None, 32, 2, 0)
         for key, v in ep.items():
             setattr(e, key, v)
-        return L.gemm_fused(B, ldb, A, lda, C, ldc, m, n, k, dt, ot, ctypes.byref(e), None)
+        return L.gemm_fused(B, ldb, A, lda, C, ldc, m, n, k, dt, ot, ctypes.byref(e), ws, wb, None)
 
     for kw in ({"dt": 2}, {"dt": 7}, {"ot": 3}, {"ot": 0}, {"ot": -1}):
         assert call(**kw) == g.GEMV_ERR_DTYPE, kw
@@ -74,9 +74,34 @@ def test_gemm_refusals(gemv_lib):
                {"residual": P[2] + 2}, {"residual": P[2], "ldr": 40}):
         assert call(**kw) == g.GEMV_ERR_ALIAS, kw
     assert call(m=0) == g.GEMV_OK and call(n=0) == g.GEMV_OK
-    for kw in ({"residual": P[2]}, {"dt": 3, "A": P[1] + 1}, {"k": 0, "A": None, "B": None}):
-        assert call(**kw) not in (g.GEMV_ERR_ALIAS, g.GEMV_ERR_ALIGN, g.GEMV_ERR_ARG), kw
-    assert L.gemm_fused(P[0], 64, P[1], 64, P[2], 32, 4, 32, 64, 1, 0, None, None) == g.GEMV_ERR_DTYPE
+    # unaligned operands need their workspace: A's 4 rows of 128 bytes, B's 32 rows, 256 bytes at a time
+    for kw in ({"A": P[1] + 2}, {"lda": 65}, {"A": P[1] + 2, "ws": P[7], "wb": 511}, {"ldb": 67, "ws": P[7], "wb": 4095},
+               {"lda": 65, "ldb": 65, "ws": P[7], "wb": 4607}, {"dt": 3, "A": P[1] + 1}):
+        assert call(**kw) == g.GEMV_ERR_SCRATCH, kw
+    assert call(lda=65, ws=P[7] + 8, wb=512) == g.GEMV_ERR_ALIGN
+    for at in (P[0] + 64, P[1], P[2] + 32):
+        assert call(lda=65, ws=at, wb=512) == g.GEMV_ERR_ALIAS
+    for kw in ({"residual": P[2]}, {"lda": 65, "ws": P[7], "wb": 512}, {"ws": P[0], "wb": 1 << 20},
+               {"k": 0, "A": None, "B": None}):
+        assert call(**kw) not in (g.GEMV_ERR_ALIAS, g.GEMV_ERR_ALIGN, g.GEMV_ERR_ARG, g.GEMV_ERR_SCRATCH), kw
+    assert L.gemm_fused(P[0], 64, P[1], 64, P[2], 32, 4, 32, 64, 1, 0, None, None, 0, None) == g.GEMV_ERR_DTYPE
+
+
+def test_gemm_workspace(gemv_lib):
+    g, L = gemv_lib, gemv_lib._lib_with_operators()
+
+    def need(B=P[0], ldb=64, A=P[1], lda=64, m=4, n=32, k=64, dt=1):
+        out = ctypes.c_int64(-1)
+        st = L.gemm_workspace(B, ldb, A, lda, m, n, k, dt, ctypes.byref(out))
+        return out.value if st == g.GEMV_OK else st
+
+    assert need() == 0 and need(k=57) == 0 and need(m=0, lda=65) == 0 and need(k=0, lda=3) == 0
+    assert need(m=1, lda=65) == 0  # one row has no stride
+    assert need(lda=65) == 512 and need(ldb=65) == 4096 and need(B=P[0] + 2) == 4096
+    assert need(lda=65, ldb=65) == 4608 and need(m=1, A=P[1] + 2, k=9) == 256
+    assert need(dt=3, lda=80) == 0 and need(dt=3, lda=72) == 256
+    assert need(dt=2) == g.GEMV_ERR_DTYPE and need(lda=63) == g.GEMV_ERR_ARG and need(m=-1) == g.GEMV_ERR_ARG
+    assert L.gemm_workspace(P[0], 64, P[1], 64, 4, 32, 64, 1, None) == g.GEMV_ERR_ARG
 
 
 def test_scan_refusals(gemv_lib):
@@ -126,6 +151,6 @@ def test_scan_backward_refusals(gemv_lib):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU error path")
 def test_valid_calls_without_gpu(gemv_lib):
     g, L = gemv_lib, gemv_lib._lib_with_operators()
-    assert L.gemm_fused(P[0], 64, P[1], 64, P[2], 32, 4, 32, 64, 1, 1, None, None) == g.GEMV_ERR_DEVICE
+    assert L.gemm_fused(P[0], 64, P[1], 64, P[2], 32, 4, 32, 64, 1, 1, None, None, 0, None) == g.GEMV_ERR_DEVICE
     assert L.gated_scan(P[0], 320, 32, P[1], 320, 32, None, P[3], 320, 32, None, 2, 10, 32, 1, None) == \
         g.GEMV_ERR_DEVICE
