@@ -55,24 +55,6 @@ __device__ __forceinline__ raw *at(const Strided &s, int64_t b, int64_t t, int64
 // a * v, where a decay of zero drops v.
 __device__ __forceinline__ float decayed(float a, float v) { return a == 0.f ? 0.f : a * v; }
 
-// Two fused multiply-adds, or products, in one instruction.
-__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
-  asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
-      "fma.rn.f32x2 c, a, b, c;\nmov.b64 {%0, %1}, c;\n}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
-  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
-  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
-      : "=f"(d0), "=f"(d1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
 // exp(g) of two values.  Near 1, where a decay is carried over many steps, by
 // its series (the next term is below 6e-9 relative): within 0.6 u and without
 // the bias of a third of a unit per step that the special function unit's 2^t

@@ -286,19 +286,6 @@ struct AlignParams {
   AlignJob job[2];
 };
 
-// The 16 bytes `off` into lo ++ hi; off is the same for the whole warp.
-template <int WORD>
-__device__ __forceinline__ uint4 shifted_words(const uint4 &lo, const uint4 &hi, int bits) {
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  return make_uint4(__funnelshift_r(w[WORD], w[WORD + 1], bits), __funnelshift_r(w[WORD + 1], w[WORD + 2], bits),
-                    __funnelshift_r(w[WORD + 2], w[WORD + 3], bits), __funnelshift_r(w[WORD + 3], w[WORD + 4], bits));
-}
-__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int off) {
-  const int bits = (off & 3) * 8;
-  if (off < 8) return off < 4 ? shifted_words<0>(lo, hi, bits) : shifted_words<1>(lo, hi, bits);
-  return off < 12 ? shifted_words<2>(lo, hi, bits) : shifted_words<3>(lo, hi, bits);
-}
-
 // A warp copies a piece: four times 512 bytes of a row, read as the aligned
 // 16-byte blocks that hold them (a lane's upper block is its neighbour's lower
 // one).  Memory-bound: it reads and writes the operand once.

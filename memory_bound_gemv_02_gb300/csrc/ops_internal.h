@@ -62,6 +62,37 @@ struct Elem<GEMV_TYPE_F32> {
   }
 };
 
+// Two fused multiply-adds, or products, in one instruction.
+__device__ __forceinline__ void fma2(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n.reg .b64 a, b, c;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+      "fma.rn.f32x2 c, a, b, c;\nmov.b64 {%0, %1}, c;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float &d0, float &d1, float a0, float a1, float b0, float b1) {
+  asm("{\n.reg .b64 a, b;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// The 16 bytes `off` into lo ++ hi; off is the same for the whole warp.
+template <int WORD>
+__device__ __forceinline__ uint4 shifted_words(const uint4 &lo, const uint4 &hi, int bits) {
+  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  return make_uint4(__funnelshift_r(w[WORD], w[WORD + 1], bits), __funnelshift_r(w[WORD + 1], w[WORD + 2], bits),
+                    __funnelshift_r(w[WORD + 2], w[WORD + 3], bits), __funnelshift_r(w[WORD + 3], w[WORD + 4], bits));
+}
+__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int off) {
+  const int bits = (off & 3) * 8;
+  if (off < 8) return off < 4 ? shifted_words<0>(lo, hi, bits) : shifted_words<1>(lo, hi, bits);
+  return off < 12 ? shifted_words<2>(lo, hi, bits) : shifted_words<3>(lo, hi, bits);
+}
+
 inline int type_bytes(int type) { return type == GEMV_TYPE_F32 ? 4 : type == GEMV_TYPE_E4M3 ? 1 : 2; }
 
 // Rows of `width` bytes, `pitch` bytes apart, `rows` of them, from p.

@@ -19,7 +19,8 @@ constexpr float kE4m3Max = 448.f;
 // Rows whose squares overflow fp32 (or nearly vanish in it) are scaled by a
 // power of two for their statistics.
 constexpr float kShrink = 0x1p-64f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
-constexpr int kMaxRowThreads = 512;  // 128 registers a thread: 32 values of s and their units in flight
+constexpr int kMaxRowThreads = 512;  // 128 registers a thread: 64 values of s at most and their units in flight
+constexpr int kSmallThreads = 256;   // of CTAs that hold several rows
 constexpr int kLongThreads = 512;
 
 struct NormParams {
@@ -33,59 +34,65 @@ struct NormParams {
 };
 
 // Maximum that keeps a NaN of either side.
-__device__ __forceinline__ float max_nan(float a, float b) { return a != a ? a : (b != b ? b : fmaxf(a, b)); }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-// Units a thread handles at a time: 16 bytes of x (VECTOR) or one element.
-template <int TYPE, bool VECTOR>
-struct Unit {
-  using E = Elem<TYPE>;
-  typedef typename E::raw raw;
-  static constexpr int V = VECTOR ? E::VEC : 1;
+// Two values in 8 bits, the first in the low byte; beyond 448 they stop at it.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 
-  static __device__ __forceinline__ void load(const void *p, int64_t i, float (&f)[V]) {
-    if constexpr (VECTOR) {
-      E::unpack(static_cast<const uint4 *>(p)[i], f);
-    } else {
-      f[0] = E::get(static_cast<const raw *>(p)[i]);
-    }
-  }
-  // weights: of the rows' type, or fp32
-  static __device__ __forceinline__ void load_weight(const void *p, int64_t i, bool f32, float (&f)[V]) {
-    if (!f32 || TYPE == GEMV_TYPE_F32) {
-      load(p, i, f);
-    } else if constexpr (VECTOR) {
+// Bytes 16 i .. 16 i + 15 of a buffer of `bytes` bytes that starts at `start`.
+// SHIFT: from the aligned blocks that hold them, 0 beyond the end; the start's
+// offset within 16 bytes has to be the same for the whole warp.
+template <bool SHIFT>
+__device__ __forceinline__ uint4 window(uintptr_t start, int64_t bytes, int i) {
+  if constexpr (!SHIFT) {
+    return *reinterpret_cast<const uint4 *>(start + (uintptr_t)(16ll * i));
+  } else {
+    const int off = (int)(start & 15);
+    const uintptr_t block = start - off + (uintptr_t)(16ll * i), end = start + (uintptr_t)bytes;
+    const uint4 lo = block < end ? *reinterpret_cast<const uint4 *>(block) : zero4();
+    const uint4 hi = off && block + 16 < end ? *reinterpret_cast<const uint4 *>(block + 16) : zero4();
+    uint4 v = shifted(lo, hi, off);
+    const int64_t left = bytes - 16ll * i;
+    if (left < 16) {  // the last window's bytes beyond the end are a neighbour's
+      uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int q = 0; q < V / 4; ++q) {
-        const float4 w = static_cast<const float4 *>(p)[i * (V / 4) + q];
-        f[4 * q] = w.x; f[4 * q + 1] = w.y; f[4 * q + 2] = w.z; f[4 * q + 3] = w.w;
+      for (int q = 0; q < 4; ++q) {
+        const int keep = (int)left - 4 * q;
+        w[q] = keep >= 4 ? w[q] : keep <= 0 ? 0u : w[q] & ((1u << (8 * keep)) - 1u);
       }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return v;
+  }
+}
+
+// A row of shared memory (from a multiple of 16, a block beyond the end is
+// readable) to global memory at any byte, by 16-byte stores of the blocks that
+// lie within the row and single elements at its ends.  `off` is the same for
+// the whole warp.
+template <class Element>
+__device__ __forceinline__ void copy_out(const char *row, int bytes, char *to, int lane, int tpr) {
+  const int off = (int)((uintptr_t)to & 15), blocks = (off + bytes + 15) / 16;
+  for (int j = lane; j < blocks; j += tpr) {
+    const int first = 16 * j - off;  // of the row's bytes
+    if (first >= 0 && first + 16 <= bytes) {
+      uint4 v = *reinterpret_cast<const uint4 *>(row + 16 * j);
+      if (off) v = shifted(*reinterpret_cast<const uint4 *>(row + 16 * j - 16), v, 16 - off);
+      *reinterpret_cast<uint4 *>(to + first) = v;
     } else {
-      f[0] = static_cast<const float *>(p)[i];
+      for (int b = first < 0 ? 0 : first; b < first + 16 && b < bytes; b += (int)sizeof(Element))
+        *reinterpret_cast<Element *>(to + b) = *reinterpret_cast<const Element *>(row + b);
     }
   }
-  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&f)[V]) {
-    if constexpr (VECTOR) {
-      static_cast<uint4 *>(p)[i] = E::pack(f);
-    } else {
-      static_cast<raw *>(p)[i] = E::put(f[0]);
-    }
-  }
-  static __device__ __forceinline__ void store8(void *p, int64_t i, const float (&f)[V]) {
-    if constexpr (VECTOR) {
-      uint32_t w[V / 4];
-#pragma unroll
-      for (int q = 0; q < V / 4; ++q) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q], f[4 * q + 1]), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * q + 2], f[4 * q + 3]), __NV_SATFINITE, __NV_E4M3);
-        w[q] = lo | (hi << 16);
-      }
-      if constexpr (V == 8) static_cast<uint2 *>(p)[i] = make_uint2(w[0], w[1]);
-      else static_cast<uint32_t *>(p)[i] = w[0];
-    } else {
-      static_cast<uint8_t *>(p)[i] = (uint8_t)__nv_cvt_float_to_fp8(f[0], __NV_SATFINITE, __NV_E4M3);
-    }
-  }
-};
+}
 
 // The row's sum and maximum over its `tpr` threads, in a fixed order; every
 // thread gets both.  `part` holds 2 x 32 floats per use (two uses alternate,
@@ -112,10 +119,13 @@ __device__ __forceinline__ void row_reduce(float &sum, float &top, int tpr, floa
   }
 }
 
-// What a row's elements are multiplied by once its statistics are known: y =
-// ((s * pre) * w) * mul, and the 8-bit form's scale.
+// Shared memory for a staged row, so that the next starts on 16 bytes.
+__host__ __device__ constexpr int staged_bytes(int bytes) { return (bytes + 15) / 16 * 16; }
+
+// What a row's t = s w are multiplied by once its statistics are known (s
+// scaled by `pre`), and the 8-bit form's scale.
 struct RowFactors {
-  float pre, mul, scale;
+  float mul, scale;
 };
 
 // The factor that brings a row's squares into fp32's range (1 nearly always).
@@ -126,7 +136,7 @@ __device__ __forceinline__ float rescale(float sum) {
 template <bool EIGHT>
 __device__ __forceinline__ RowFactors row_factors(float pre, float sum, float top, int64_t d, float eps) {
   const float rstd = rsqrtf(sum / (float)d + eps * pre * pre);  // pre is a power of two: exact
-  RowFactors f{pre, rstd, 0.f};
+  RowFactors f{rstd, 0.f};
   if (EIGHT) {
     // top is max|t|: a row of zeros has scale 1; one with a NaN or an
     // infinity (rstd 0) has no scale.
@@ -136,84 +146,158 @@ __device__ __forceinline__ RowFactors row_factors(float pre, float sum, float to
   return f;
 }
 
-// Rows of up to tpr * N units, held in registers between the reduction and the
-// output: x and the residual are read once.  Memory-bound (7 bytes an element
-// at 16 bits with a residual and 8-bit output).  Rows that fit 32 lanes share
-// a CTA of 256 threads (tpr lanes each); longer rows take a CTA each.  The
-// weights are read per row (L1 and L2 hold them), not kept: the registers go
-// to rows in flight.
-template <int TYPE, bool EIGHT, bool VECTOR, int N>
+// Rows of up to tpr * N units of 16 bytes, held in registers between the
+// reduction and the output: x and the residual are read once.  Memory-bound (7
+// bytes an element at 16 bits with a residual and 8-bit output).  Rows that fit
+// a few lanes share a CTA of kSmallThreads; longer rows take a CTA each.  The
+// weights are read per row (L1 and L2 hold them), not kept: the registers go to
+// rows in flight.
+//
+// SHIFT: some row starts off a 16-byte boundary.  Inputs are then read as the
+// aligned blocks that cover them and shifted in registers, outputs pass through
+// shared memory (a row of y and one of residual_out per slot) and leave by
+// aligned blocks again; tpr is 32 or the CTA, so that a warp has one offset.
+template <int TYPE, bool EIGHT, bool SHIFT, int N>
 __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) {
-  using U = Unit<TYPE, VECTOR>;
-  typedef typename U::raw raw;
-  constexpr int V = U::V;
+  using E = Elem<TYPE>;
+  typedef typename E::raw raw;
+  constexpr int V = E::VEC, ES = (int)sizeof(raw), OE = EIGHT ? 1 : ES;
   __shared__ float part[2][64];
+  extern __shared__ __align__(16) char staged[];
   allow_dependents();
   wait_for_predecessor();
   const int tpr = p.tpr, rows_per_cta = blockDim.x / tpr;
   const int lane = threadIdx.x % tpr, slot = threadIdx.x / tpr;
-  const int units = (int)(p.d / V);
-  const bool w_f32 = p.w_f32 != 0;
+  const int d = (int)p.d, units = (d + V - 1) / V;
+  const int64_t row_bytes = (int64_t)d * ES;
+  const bool wide_weights = p.w_f32 != 0 && TYPE != GEMV_TYPE_F32;
+  const uintptr_t weights = (uintptr_t)p.w;
+  const int y_space = staged_bytes(units * V * OE);
+  char *const row_y = staged + slot * (y_space + units * 16), *const row_s = row_y + y_space;
+  auto load_weights = [&](int u, float (&w)[V]) {
+    if (!wide_weights) {
+      E::unpack(window<SHIFT>(weights, row_bytes, u), w);
+    } else if constexpr (V == 8) {
+      float lo[4], hi[4];
+      Elem<GEMV_TYPE_F32>::unpack(window<SHIFT>(weights, (int64_t)d * 4, 2 * u), lo);
+      Elem<GEMV_TYPE_F32>::unpack(window<SHIFT>(weights, (int64_t)d * 4, 2 * u + 1), hi);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = lo[e];
+        w[e + 4] = hi[e];
+      }
+    }
+  };
   int turn = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * rows_per_cta; row0 < p.rows; row0 += (int64_t)gridDim.x * rows_per_cta) {
     const int64_t row = row0 + slot;
     const bool live = row < p.rows;
-    const raw *x = static_cast<const raw *>(p.x) + row * p.ldx;
-    const raw *r = p.r ? static_cast<const raw *>(p.r) + row * p.ldr : nullptr;
+    const uintptr_t x = (uintptr_t)(static_cast<const raw *>(p.x) + row * p.ldx);
     float s[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[i][e] = 0.f;
-      if (live && lane + i * tpr < units) U::load(x, lane + i * tpr, s[i]);
+      const int u = lane + i * tpr;
+      uint4 v = zero4();
+      if (live && u < units) v = window<SHIFT>(x, row_bytes, u);
+      E::unpack(v, s[i]);
     }
-    if (r != nullptr) {
+    if (p.r != nullptr) {
+      const uintptr_t r = (uintptr_t)(static_cast<const raw *>(p.r) + row * p.ldr);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float f[V] = {};
-        if (live && lane + i * tpr < units) U::load(r, lane + i * tpr, f);
+        const int u = lane + i * tpr;
+        uint4 v = zero4();
+        if (live && u < units) v = window<SHIFT>(r, row_bytes, u);
+        float f[V];
+        E::unpack(v, f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[i][e] += f[e];
+        for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], f[e], f[e + 1]);
       }
     }
-    auto reduce = [&](float pre, float &sum, float &top) {
-      sum = 0.f;
+    float sum, top;
+    auto reduce = [&]() {
+      float s0 = 0.f, s1 = 0.f;
       top = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
+        const int u = lane + i * tpr;
         float w[V] = {};
-        if (EIGHT && live && lane + i * tpr < units) U::load_weight(p.w, lane + i * tpr, w_f32, w);
+        if (EIGHT && live && u < units) load_weights(u, w);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float v = s[i][e] * pre;
-          sum = fmaf(v, v, sum);
-          if (EIGHT) top = max_nan(top, fabsf(v * w[e]));
+        for (int e = 0; e < V; e += 2) {
+          fma2(s0, s1, s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], s0, s1);
+          if (EIGHT) {
+            float t0, t1;
+            mul2(t0, t1, s[i][e], s[i][e + 1], w[e], w[e + 1]);
+            top = max_nan(top, max_nan(fabsf(t0), fabsf(t1)));
+          }
         }
       }
+      sum = s0 + s1;
       row_reduce<EIGHT>(sum, top, tpr, part[turn]);
       turn ^= 1;
     };
-    float sum, top, pre = 1.f;
-    reduce(pre, sum, top);
+    reduce();
+    auto store_residual = [&]() {
+      if (!p.ro || !live) return;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int u = lane + i * tpr;
+        if (u >= units) break;
+        if (SHIFT) reinterpret_cast<uint4 *>(row_s)[u] = E::pack(s[i]);
+        else reinterpret_cast<uint4 *>(static_cast<raw *>(p.ro) + row * p.ldo)[u] = E::pack(s[i]);
+      }
+    };
+    store_residual();
     // Rare: squares beyond fp32's range.  (All threads of a CTA-wide row agree;
     // lanes of short rows reduce together whichever row needs it.)
-    pre = rescale(sum);
-    if (tpr > 32 ? pre != 1.f : __any_sync(0xffffffffu, pre != 1.f)) reduce(pre, sum, top);
+    const float pre = rescale(sum);
+    if (tpr > 32 ? pre != 1.f : __any_sync(0xffffffffu, pre != 1.f)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[i][e] *= pre;
+      }
+      reduce();
+    }
     const RowFactors f = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
-    if (!live) continue;
-    if (EIGHT && lane == 0) p.scale[row] = f.scale;
-    raw *ro = p.ro ? static_cast<raw *>(p.ro) + row * p.ldo : nullptr;
+    if (live) {
+      if (EIGHT && lane == 0) p.scale[row] = f.scale;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = lane + i * tpr;
-      if (u >= units) break;
-      float w[V], y[V];
-      U::load_weight(p.w, u, w_f32, w);
+      for (int i = 0; i < N; ++i) {
+        const int u = lane + i * tpr;
+        if (u >= units) break;
+        float w[V], y[V];
+        load_weights(u, w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = ((s[i][e] * f.pre) * w[e]) * f.mul;
-      if (ro) U::store(ro, u, s[i]);
-      if constexpr (EIGHT) U::store8(static_cast<uint8_t *>(p.y) + row * p.ldy, u, y);
-      else U::store(static_cast<raw *>(p.y) + row * p.ldy, u, y);
+        for (int e = 0; e < V; e += 2) {
+          mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+          mul2(y[e], y[e + 1], y[e], y[e + 1], f.mul, f.mul);
+        }
+        if constexpr (!EIGHT) {
+          if (SHIFT) reinterpret_cast<uint4 *>(row_y)[u] = E::pack(y);
+          else reinterpret_cast<uint4 *>(static_cast<raw *>(p.y) + row * p.ldy)[u] = E::pack(y);
+        } else {
+          char *to = SHIFT ? row_y : static_cast<char *>(p.y) + row * p.ldy;
+          if constexpr (V == 8)
+            reinterpret_cast<uint2 *>(to)[u] = make_uint2(e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16,
+                                                          e4m3_pair(y[4], y[5]) | e4m3_pair(y[6], y[7]) << 16);
+          else
+            reinterpret_cast<uint32_t *>(to)[u] = e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
+        }
+      }
+    }
+    if constexpr (SHIFT) {
+      if (tpr > 32) __syncthreads();
+      else __syncwarp();
+      if (live) {
+        if constexpr (EIGHT) copy_out<uint8_t>(row_y, d, static_cast<char *>(p.y) + row * p.ldy, lane, tpr);
+        else copy_out<raw>(row_y, d * OE, static_cast<char *>(p.y) + row * p.ldy * OE, lane, tpr);
+        if (p.ro) copy_out<raw>(row_s, d * ES, static_cast<char *>(p.ro) + row * p.ldo * ES, lane, tpr);
+      }
+      // The next row's outputs are staged after its reduction: a CTA-wide
+      // barrier, but for a warp's rows only its shuffles.
+      if (tpr <= 32) __syncwarp();
     }
   }
 }
@@ -222,8 +306,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
 // for the output.
 template <int TYPE, bool EIGHT>
 __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams p) {
-  using U = Unit<TYPE, false>;
-  typedef typename U::raw raw;
+  using E = Elem<TYPE>;
+  typedef typename E::raw raw;
   __shared__ float part[2][64];
   allow_dependents();
   wait_for_predecessor();
@@ -231,16 +315,9 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const raw *x = static_cast<const raw *>(p.x) + row * p.ldx;
     const raw *r = p.r ? static_cast<const raw *>(p.r) + row * p.ldr : nullptr;
-    auto value = [&](int64_t j) {
-      float a[1], b[1] = {0.f};
-      U::load(x, j, a);
-      if (r) U::load(r, j, b);
-      return a[0] + b[0];
-    };
+    auto value = [&](int64_t j) { return E::get(x[j]) + (r ? E::get(r[j]) : 0.f); };
     auto weight = [&](int64_t j) {
-      float w[1];
-      U::load_weight(p.w, j, p.w_f32 != 0, w);
-      return w[0];
+      return p.w_f32 ? static_cast<const float *>(p.w)[j] : E::get(static_cast<const raw *>(p.w)[j]);
     };
     float sum, top, pre = 1.f;
     for (;;) {
@@ -262,54 +339,60 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
     raw *ro = p.ro ? static_cast<raw *>(p.ro) + row * p.ldo : nullptr;
 #pragma unroll 4
     for (int64_t j = threadIdx.x; j < p.d; j += kLongThreads) {
-      const float s[1] = {value(j)}, y[1] = {((s[0] * f.pre) * weight(j)) * f.mul};
-      if (ro) U::store(ro, j, s);
-      if constexpr (EIGHT) U::store8(static_cast<uint8_t *>(p.y) + row * p.ldy, j, y);
-      else U::store(static_cast<raw *>(p.y) + row * p.ldy, j, y);
+      const float s = value(j), y = ((s * pre) * weight(j)) * f.mul;
+      if (ro) ro[j] = E::put(s);
+      if (EIGHT) static_cast<uint8_t *>(p.y)[row * p.ldy + j] = (uint8_t)e4m3_pair(y, 0.f);
+      else static_cast<raw *>(p.y)[row * p.ldy + j] = E::put(y);
     }
   }
 }
 
-constexpr int kVecUnits = 4;      // 16-byte units per thread and row,
-constexpr int kScalarUnits = 16;  // and single elements; twice as many for rows that 512 threads do not cover
+constexpr int kUnits = 4;  // 16-byte units per thread and row; twice as many for rows that 512 threads do not cover
 
-template <int TYPE, bool EIGHT>
-int launch_norm(NormParams p, bool vector, int sms, cudaStream_t stream) {
-  const int64_t units = vector ? p.d / Elem<TYPE>::VEC : p.d;
-  const int64_t per = vector ? kVecUnits : kScalarUnits;
-  const bool small = vector && units <= 32;  // a unit per lane
+template <int TYPE, bool EIGHT, bool SHIFT>
+int launch_norm(NormParams p, int sms, cudaStream_t stream) {
+  constexpr int V = Elem<TYPE>::VEC, OE = EIGHT ? 1 : 16 / V;
+  const int64_t units = (p.d + V - 1) / V;
+  const bool small = units <= 32;  // a unit per lane
   bool twice = false;
-  int64_t need = small ? units : (units + per - 1) / per;
+  int64_t need = small ? units : (units + kUnits - 1) / kUnits;
   if (need > kMaxRowThreads) {
     twice = true;
-    need = (units + 2 * per - 1) / (2 * per);
+    need = (units + 2 * kUnits - 1) / (2 * kUnits);
   }
   if (need > kMaxRowThreads) {
     const int64_t grid = p.rows < (int64_t)sms * 4 ? p.rows : (int64_t)sms * 4;
     return launch_op(rms_norm_long_kernel<TYPE, EIGHT>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
   }
-  int threads;
+  int threads = kSmallThreads;
   if (need <= 32) {
-    p.tpr = 1;
+    p.tpr = SHIFT ? 32 : 1;
     while (p.tpr < need) p.tpr *= 2;
-    threads = 256;
   } else {
     threads = p.tpr = (int)((need + 31) / 32 * 32);
   }
   const int64_t rows_per_cta = threads / p.tpr;
   int64_t grid = (p.rows + rows_per_cta - 1) / rows_per_cta;
   if (grid > (1 << 20)) grid = 1 << 20;
-  void (*fn)(NormParams) = small    ? rms_norm_kernel<TYPE, EIGHT, true, 1>
-                           : vector ? (twice ? rms_norm_kernel<TYPE, EIGHT, true, 2 * kVecUnits>
-                                             : rms_norm_kernel<TYPE, EIGHT, true, kVecUnits>)
-                                    : (twice ? rms_norm_kernel<TYPE, EIGHT, false, 2 * kScalarUnits>
-                                             : rms_norm_kernel<TYPE, EIGHT, false, kScalarUnits>);
-  return launch_op(fn, dim3((unsigned)grid), threads, 0, 1, stream, p);
+  // staged rows, and a block that may be read beyond the last
+  const size_t smem = SHIFT ? (size_t)(rows_per_cta * (staged_bytes((int)units * V * OE) + units * 16) + 16) : 0;
+  void (*fn)(NormParams) = small   ? rms_norm_kernel<TYPE, EIGHT, SHIFT, 1>
+                           : twice ? rms_norm_kernel<TYPE, EIGHT, SHIFT, 2 * kUnits>
+                                   : rms_norm_kernel<TYPE, EIGHT, SHIFT, kUnits>;
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_failure((int)e);
+    }
+  }
+  return launch_op(fn, dim3((unsigned)grid), threads, smem, 1, stream, p);
 }
 
 template <int TYPE>
 int launch_norm_type(const NormParams &p, bool eight, bool vector, int sms, cudaStream_t stream) {
-  return eight ? launch_norm<TYPE, true>(p, vector, sms, stream) : launch_norm<TYPE, false>(p, vector, sms, stream);
+  if (eight) return vector ? launch_norm<TYPE, true, false>(p, sms, stream) : launch_norm<TYPE, true, true>(p, sms, stream);
+  return vector ? launch_norm<TYPE, false, false>(p, sms, stream) : launch_norm<TYPE, false, true>(p, sms, stream);
 }
 
 }  // namespace
