@@ -19,7 +19,8 @@ constexpr float kE4m3Max = 448.f;
 // Rows whose squares overflow fp32 (or nearly vanish in it) are scaled by a
 // power of two for their statistics.
 constexpr float kShrink = 0x1p-64f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
-constexpr int kMaxRowThreads = 512;  // 128 registers a thread: 64 values of s at most and their units in flight
+constexpr int kUnits = 2;            // 16-byte units per thread and row: 64 registers a thread, and 1024 threads,
+constexpr int kMaxRowThreads = 1024;  // hold more rows in flight than 4 units in 126 registers
 constexpr int kSmallThreads = 256;   // of CTAs that hold several rows
 constexpr int kLongThreads = 512;
 
@@ -47,32 +48,41 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return r;
 }
 
-// Bytes 16 i .. 16 i + 15 of a buffer of `bytes` bytes that starts at `start`.
-// SHIFT: from the aligned blocks that hold them, 0 beyond the end; the start's
-// offset within 16 bytes has to be the same for the whole warp.
+// Bytes 16 i .. 16 i + 15 of a buffer of `bytes` bytes that starts at `start`,
+// in two halves, so that a thread's loads are all under way before the first is
+// waited for: Window(...) requests them, value() has them.  SHIFT: from the
+// aligned blocks that hold them, 0 beyond the end; the start's offset within 16
+// bytes has to be the same for the whole warp.
 template <bool SHIFT>
-__device__ __forceinline__ uint4 window(uintptr_t start, int64_t bytes, int i) {
-  if constexpr (!SHIFT) {
-    return *reinterpret_cast<const uint4 *>(start + (uintptr_t)(16ll * i));
-  } else {
-    const int off = (int)(start & 15);
-    const uintptr_t block = start - off + (uintptr_t)(16ll * i), end = start + (uintptr_t)bytes;
-    const uint4 lo = block < end ? *reinterpret_cast<const uint4 *>(block) : zero4();
-    const uint4 hi = off && block + 16 < end ? *reinterpret_cast<const uint4 *>(block + 16) : zero4();
-    uint4 v = shifted(lo, hi, off);
-    const int64_t left = bytes - 16ll * i;
+struct Window {
+  uint4 lo, hi;
+  __device__ __forceinline__ Window() {}
+  __device__ __forceinline__ Window(uintptr_t start, int bytes, int i, bool in) {
+    if constexpr (!SHIFT) {
+      lo = in ? *reinterpret_cast<const uint4 *>(start + (uintptr_t)(16 * i)) : zero4();
+    } else {
+      const int off = (int)(start & 15), left = bytes + off - 16 * i;  // from the lower block to the end
+      const uint4 *block = reinterpret_cast<const uint4 *>(start - off) + i;
+      lo = in && left > 0 ? block[0] : zero4();
+      hi = in && left > 16 ? block[1] : zero4();
+    }
+  }
+  __device__ __forceinline__ uint4 value(uintptr_t start, int bytes, int i) const {
+    if constexpr (!SHIFT) return lo;
+    uint4 v = shifted(lo, hi, (int)(start & 15));
+    const int left = bytes - 16 * i;
     if (left < 16) {  // the last window's bytes beyond the end are a neighbour's
       uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int keep = (int)left - 4 * q;
+        const int keep = left - 4 * q;
         w[q] = keep >= 4 ? w[q] : keep <= 0 ? 0u : w[q] & ((1u << (8 * keep)) - 1u);
       }
       v = make_uint4(w[0], w[1], w[2], w[3]);
     }
     return v;
   }
-}
+};
 
 // A row of shared memory (from a multiple of 16, a block beyond the end is
 // readable) to global memory at any byte, by 16-byte stores of the blocks that
@@ -169,18 +179,25 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
   const int tpr = p.tpr, rows_per_cta = blockDim.x / tpr;
   const int lane = threadIdx.x % tpr, slot = threadIdx.x / tpr;
   const int d = (int)p.d, units = (d + V - 1) / V;
-  const int64_t row_bytes = (int64_t)d * ES;
+  const int row_bytes = d * ES;
   const bool wide_weights = p.w_f32 != 0 && TYPE != GEMV_TYPE_F32;
   const uintptr_t weights = (uintptr_t)p.w;
   const int y_space = staged_bytes(units * V * OE);
   char *const row_y = staged + slot * (y_space + units * 16), *const row_s = row_y + y_space;
-  auto load_weights = [&](int u, float (&w)[V]) {
+  // weights of this thread's units, requested and waited for together (fp32 ones of 16-bit rows unit by unit)
+  auto request_weights = [&](Window<SHIFT> (&win)[N]) {
+    if (wide_weights) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) win[i] = Window<SHIFT>(weights, row_bytes, lane + i * tpr, lane + i * tpr < units);
+  };
+  auto get_weights = [&](const Window<SHIFT> &win, int u, float (&w)[V]) {
     if (!wide_weights) {
-      E::unpack(window<SHIFT>(weights, row_bytes, u), w);
+      E::unpack(win.value(weights, row_bytes, u), w);
     } else if constexpr (V == 8) {
+      const Window<SHIFT> a(weights, d * 4, 2 * u, u < units), b(weights, d * 4, 2 * u + 1, u < units && 8 * u + 4 < d);
       float lo[4], hi[4];
-      Elem<GEMV_TYPE_F32>::unpack(window<SHIFT>(weights, (int64_t)d * 4, 2 * u), lo);
-      Elem<GEMV_TYPE_F32>::unpack(window<SHIFT>(weights, (int64_t)d * 4, 2 * u + 1), hi);
+      Elem<GEMV_TYPE_F32>::unpack(a.value(weights, d * 4, 2 * u), lo);
+      Elem<GEMV_TYPE_F32>::unpack(b.value(weights, d * 4, 2 * u + 1), hi);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         w[e] = lo[e];
@@ -193,23 +210,19 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
     const int64_t row = row0 + slot;
     const bool live = row < p.rows;
     const uintptr_t x = (uintptr_t)(static_cast<const raw *>(p.x) + row * p.ldx);
+    const uintptr_t r = p.r ? (uintptr_t)(static_cast<const raw *>(p.r) + row * p.ldr) : 0;
     float s[N][V];
+    {
+      Window<SHIFT> xw[N], rw[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = lane + i * tpr;
-      uint4 v = zero4();
-      if (live && u < units) v = window<SHIFT>(x, row_bytes, u);
-      E::unpack(v, s[i]);
-    }
-    if (p.r != nullptr) {
-      const uintptr_t r = (uintptr_t)(static_cast<const raw *>(p.r) + row * p.ldr);
+      for (int i = 0; i < N; ++i) xw[i] = Window<SHIFT>(x, row_bytes, lane + i * tpr, live && lane + i * tpr < units);
+#pragma unroll
+      for (int i = 0; i < N; ++i) rw[i] = Window<SHIFT>(r, row_bytes, lane + i * tpr, r && live && lane + i * tpr < units);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int u = lane + i * tpr;
-        uint4 v = zero4();
-        if (live && u < units) v = window<SHIFT>(r, row_bytes, u);
         float f[V];
-        E::unpack(v, f);
+        E::unpack(xw[i].value(x, row_bytes, lane + i * tpr), s[i]);
+        E::unpack(rw[i].value(r, row_bytes, lane + i * tpr), f);
 #pragma unroll
         for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], f[e], f[e + 1]);
       }
@@ -218,11 +231,12 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
     auto reduce = [&]() {
       float s0 = 0.f, s1 = 0.f;
       top = 0.f;
+      Window<SHIFT> win[N];
+      if (EIGHT) request_weights(win);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int u = lane + i * tpr;
-        float w[V] = {};
-        if (EIGHT && live && u < units) load_weights(u, w);
+        float w[V];
+        if (EIGHT) get_weights(win[i], lane + i * tpr, w);
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           fma2(s0, s1, s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], s0, s1);
@@ -260,6 +274,8 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
       }
       reduce();
     }
+    Window<SHIFT> win[N];
+    request_weights(win);
     const RowFactors f = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
     if (live) {
       if (EIGHT && lane == 0) p.scale[row] = f.scale;
@@ -268,7 +284,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
         const int u = lane + i * tpr;
         if (u >= units) break;
         float w[V], y[V];
-        load_weights(u, w);
+        get_weights(win[i], u, w);
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
@@ -303,30 +319,53 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
 }
 
 // Rows too long for a CTA's registers: read once for the statistics, and again
-// for the output.
-template <int TYPE, bool EIGHT>
+// for the output.  By units of 16 bytes (VECTOR) or single elements.
+template <int TYPE, bool EIGHT, bool VECTOR>
 __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams p) {
   using E = Elem<TYPE>;
   typedef typename E::raw raw;
+  constexpr int V = VECTOR ? E::VEC : 1;
   __shared__ float part[2][64];
   allow_dependents();
   wait_for_predecessor();
   int turn = 0;
+  const int64_t units = p.d / V;
+  auto load = [&](const void *from, int64_t u, float (&f)[V]) {
+    if constexpr (VECTOR) E::unpack(static_cast<const uint4 *>(from)[u], f);
+    else f[0] = E::get(static_cast<const raw *>(from)[u]);
+  };
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const raw *x = static_cast<const raw *>(p.x) + row * p.ldx;
     const raw *r = p.r ? static_cast<const raw *>(p.r) + row * p.ldr : nullptr;
-    auto value = [&](int64_t j) { return E::get(x[j]) + (r ? E::get(r[j]) : 0.f); };
-    auto weight = [&](int64_t j) {
-      return p.w_f32 ? static_cast<const float *>(p.w)[j] : E::get(static_cast<const raw *>(p.w)[j]);
+    auto values = [&](int64_t u, float (&s)[V]) {
+      float f[V] = {};
+      load(x, u, s);
+      if (r) load(r, u, f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] += f[e];
+    };
+    auto weights = [&](int64_t u, float (&w)[V]) {
+      if (!p.w_f32 || TYPE == GEMV_TYPE_F32) {
+        load(p.w, u, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) w[e] = static_cast<const float *>(p.w)[u * V + e];
+      }
     };
     float sum, top, pre = 1.f;
     for (;;) {
       sum = top = 0.f;
-#pragma unroll 8
-      for (int64_t j = threadIdx.x; j < p.d; j += kLongThreads) {
-        const float v = value(j) * pre;
-        sum = fmaf(v, v, sum);
-        if (EIGHT) top = max_nan(top, fabsf(v * weight(j)));
+#pragma unroll 4
+      for (int64_t u = threadIdx.x; u < units; u += kLongThreads) {
+        float s[V], w[V];
+        values(u, s);
+        if (EIGHT) weights(u, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          s[e] *= pre;
+          sum = fmaf(s[e], s[e], sum);
+          if (EIGHT) top = max_nan(top, fabsf(s[e] * w[e]));
+        }
       }
       row_reduce<EIGHT>(sum, top, kLongThreads, part[turn]);
       turn ^= 1;
@@ -337,32 +376,40 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
     const RowFactors f = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
     if (EIGHT && threadIdx.x == 0) p.scale[row] = f.scale;
     raw *ro = p.ro ? static_cast<raw *>(p.ro) + row * p.ldo : nullptr;
-#pragma unroll 4
-    for (int64_t j = threadIdx.x; j < p.d; j += kLongThreads) {
-      const float s = value(j), y = ((s * pre) * weight(j)) * f.mul;
-      if (ro) ro[j] = E::put(s);
-      if (EIGHT) static_cast<uint8_t *>(p.y)[row * p.ldy + j] = (uint8_t)e4m3_pair(y, 0.f);
-      else static_cast<raw *>(p.y)[row * p.ldy + j] = E::put(y);
+#pragma unroll 2
+    for (int64_t u = threadIdx.x; u < units; u += kLongThreads) {
+      float s[V], w[V], y[V];
+      values(u, s);
+      weights(u, w);
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = ((s[e] * pre) * w[e]) * f.mul;
+      if constexpr (VECTOR) {
+        if (ro) reinterpret_cast<uint4 *>(ro)[u] = E::pack(s);
+        if constexpr (!EIGHT) {
+          reinterpret_cast<uint4 *>(static_cast<raw *>(p.y) + row * p.ldy)[u] = E::pack(y);
+        } else {
+          uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + row * p.ldy) + u * (V / 4);
+#pragma unroll
+          for (int q = 0; q < V / 4; ++q) to[q] = e4m3_pair(y[4 * q], y[4 * q + 1]) | e4m3_pair(y[4 * q + 2], y[4 * q + 3]) << 16;
+        }
+      } else {
+        if (ro) ro[u] = E::put(s[0]);
+        if (EIGHT) static_cast<uint8_t *>(p.y)[row * p.ldy + u] = (uint8_t)e4m3_pair(y[0], 0.f);
+        else static_cast<raw *>(p.y)[row * p.ldy + u] = E::put(y[0]);
+      }
     }
   }
 }
-
-constexpr int kUnits = 4;  // 16-byte units per thread and row; twice as many for rows that 512 threads do not cover
 
 template <int TYPE, bool EIGHT, bool SHIFT>
 int launch_norm(NormParams p, int sms, cudaStream_t stream) {
   constexpr int V = Elem<TYPE>::VEC, OE = EIGHT ? 1 : 16 / V;
   const int64_t units = (p.d + V - 1) / V;
   const bool small = units <= 32;  // a unit per lane
-  bool twice = false;
-  int64_t need = small ? units : (units + kUnits - 1) / kUnits;
-  if (need > kMaxRowThreads) {
-    twice = true;
-    need = (units + 2 * kUnits - 1) / (2 * kUnits);
-  }
+  const int64_t need = small ? units : (units + kUnits - 1) / kUnits;
   if (need > kMaxRowThreads) {
     const int64_t grid = p.rows < (int64_t)sms * 4 ? p.rows : (int64_t)sms * 4;
-    return launch_op(rms_norm_long_kernel<TYPE, EIGHT>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
+    return launch_op(rms_norm_long_kernel<TYPE, EIGHT, !SHIFT>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
   }
   int threads = kSmallThreads;
   if (need <= 32) {
@@ -376,9 +423,7 @@ int launch_norm(NormParams p, int sms, cudaStream_t stream) {
   if (grid > (1 << 20)) grid = 1 << 20;
   // staged rows, and a block that may be read beyond the last
   const size_t smem = SHIFT ? (size_t)(rows_per_cta * (staged_bytes((int)units * V * OE) + units * 16) + 16) : 0;
-  void (*fn)(NormParams) = small   ? rms_norm_kernel<TYPE, EIGHT, SHIFT, 1>
-                           : twice ? rms_norm_kernel<TYPE, EIGHT, SHIFT, 2 * kUnits>
-                                   : rms_norm_kernel<TYPE, EIGHT, SHIFT, kUnits>;
+  void (*fn)(NormParams) = small ? rms_norm_kernel<TYPE, EIGHT, SHIFT, 1> : rms_norm_kernel<TYPE, EIGHT, SHIFT, kUnits>;
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     if (e != cudaSuccess) {
