@@ -247,12 +247,6 @@ __device__ __forceinline__ void load_maps(const float *p, float (&A)[V], float (
     A[e] = m.x; B[e] = m.y; A[e + 1] = m.z; B[e + 1] = m.w;
   }
 }
-// `bytes` (a multiple of 16, from a multiple of 16) to shared memory, counted at `bar`.
-__device__ __forceinline__ void copy_bulk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(bar)
-               : "memory");
-}
 __device__ __forceinline__ uint32_t lds32(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // NaN if any of the values is an infinity or a NaN, else 0.
@@ -273,6 +267,7 @@ struct alignas(8) TileShared {
   uint64_t full[4];      // a stage's copies have landed (TMA)
   uint64_t exchanged[2]; // the cluster's maps of a round are here
   int failed;
+  int issued;            // rounds whose copies were started
 };
 
 // A cluster of p.cluster CTAs owns a chain: kWidth channels of one sequence.  In
@@ -319,7 +314,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   const int round_steps = S::kTime * cluster, rounds = (steps + round_steps - 1) / round_steps;
 
   if (tid == 0) {
-    sh.failed = 0;
+    sh.failed = sh.issued = 0;
     for (int i = 0; i < S::kStages; ++i) mbar_init(smem_u32(&sh.full[i]), TMA ? 1 : kScanThreads);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.exchanged[i]), 1);
     mbar_init_fence();
@@ -342,6 +337,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   // Row r of a tile in shared memory holds step r of it, backward step kTime - 1 - r.
   auto request = [&](int round) {
     if (round >= rounds || *(volatile int *)&sh.failed) return;
+    if (tid == 0) sh.issued = round + 1;
     const int stage = round % S::kStages, s0 = tile_step(round);
     const uint32_t bar = smem_u32(&sh.full[stage]);
     char *to = dynamic + stage * S::kStageBytes;
@@ -660,14 +656,13 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
       if (e < channels) p.last[cell + e] = carried[e];
   }
   if (cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
-  if (sh.failed && warp == 0) {     // after a wait that gave up: copies in flight land first
+  __syncthreads();
+  if (sh.failed && warp == 0) {  // after a wait that gave up: copies in flight land before the CTA leaves
+    int none = 0;
     if (lane == 0) atomicAdd(p.timeouts, 1u);
-    {
-      int none = 0;
-      for (int r = rounds < S::kStages ? 0 : rounds - S::kStages; r < rounds; ++r)
-        if (!wait_for<false>(smem_u32(&sh.full[r % S::kStages]), (r / S::kStages) & 1, &none, 1 << 10) && lane == 0)
-          atomicOr(p.timeouts, kDrainTimeoutBit);
-    }
+    for (int r = sh.issued < S::kStages ? 0 : sh.issued - S::kStages; r < sh.issued; ++r)
+      if (!wait_for<false>(smem_u32(&sh.full[r % S::kStages]), (r / S::kStages) & 1, &none, kWaitPolls) && lane == 0)
+        atomicOr(p.timeouts, kDrainTimeoutBit);
   }
 }
 

@@ -11,6 +11,7 @@
 #include <cstdint>
 
 #include "ops_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gemvk {
 namespace {
@@ -19,8 +20,8 @@ constexpr float kE4m3Max = 448.f;
 // Rows whose squares overflow fp32 (or nearly vanish in it) are scaled by a
 // power of two for their statistics.
 constexpr float kShrink = 0x1p-64f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
-constexpr int kUnits = 2;            // 16-byte units per thread and row: 64 registers a thread, and 1024 threads,
-constexpr int kMaxRowThreads = 1024;  // hold more rows in flight than 4 units in 126 registers
+constexpr int kUnits = 2;             // 16-byte units per thread and row,
+constexpr int kMaxRowThreads = 1024;  // at 64 registers a thread
 constexpr int kSmallThreads = 256;   // of CTAs that hold several rows
 constexpr int kLongThreads = 512;
 
@@ -32,6 +33,8 @@ struct NormParams {
   float eps;
   int32_t w_f32;
   int32_t tpr;  // threads per row: a power of two up to 32, or the whole CTA
+  int32_t stages;  // rms_norm_ring_kernel: rows in shared memory
+  uint32_t *timeouts;
 };
 
 // Maximum that keeps a NaN of either side.
@@ -84,6 +87,28 @@ struct Window {
   }
 };
 
+template <int TYPE, bool EIGHT>
+struct OutType {
+  typedef typename Elem<TYPE>::raw type;
+};
+template <int TYPE>
+struct OutType<TYPE, true> {
+  typedef uint8_t type;
+};
+
+// Unit u of an output row that starts on its unit's boundary.
+template <int TYPE, bool EIGHT, int V>
+__device__ __forceinline__ void store_y(char *row, int u, const float (&y)[V]) {
+  if constexpr (!EIGHT) {
+    reinterpret_cast<uint4 *>(row)[u] = Elem<TYPE>::pack(y);
+  } else if constexpr (V == 8) {
+    reinterpret_cast<uint2 *>(row)[u] =
+        make_uint2(e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16, e4m3_pair(y[4], y[5]) | e4m3_pair(y[6], y[7]) << 16);
+  } else {
+    reinterpret_cast<uint32_t *>(row)[u] = e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
+  }
+}
+
 // A row of shared memory (from a multiple of 16, a block beyond the end is
 // readable) to global memory at any byte, by 16-byte stores of the blocks that
 // lie within the row and single elements at its ends.  `off` is the same for
@@ -104,17 +129,17 @@ __device__ __forceinline__ void copy_out(const char *row, int bytes, char *to, i
   }
 }
 
-// The row's sum and maximum over its `tpr` threads, in a fixed order; every
+// A row's sum and maximum over the CTA's `threads`, in a fixed order; every
 // thread gets both.  `part` holds 2 x 32 floats per use (two uses alternate,
 // so that one barrier per reduction is enough).
 template <bool EIGHT>
-__device__ __forceinline__ void row_reduce(float &sum, float &top, int tpr, float *part) {
-  for (int m = tpr < 32 ? tpr >> 1 : 16; m; m >>= 1) {
+__device__ __forceinline__ void row_reduce(float &sum, float &top, int threads, float *part) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) {
     sum += __shfl_xor_sync(0xffffffffu, sum, m);
     if (EIGHT) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, m));
   }
-  if (tpr <= 32) return;
-  const int warps = tpr >> 5, lane = threadIdx.x & 31;
+  const int warps = threads >> 5, lane = threadIdx.x & 31;
   if (lane == 0) {
     part[threadIdx.x >> 5] = sum;
     if (EIGHT) part[32 + (threadIdx.x >> 5)] = top;
@@ -131,6 +156,10 @@ __device__ __forceinline__ void row_reduce(float &sum, float &top, int tpr, floa
 
 // Shared memory for a staged row, so that the next starts on 16 bytes.
 __host__ __device__ constexpr int staged_bytes(int bytes) { return (bytes + 15) / 16 * 16; }
+
+// And for a row of `units` units as copied: its blocks, one more if it starts
+// between two, and one that may be read beyond.
+__host__ __device__ constexpr int ring_area(int units) { return (units + 2) * 16; }
 
 // What a row's t = s w are multiplied by once its statistics are known (s
 // scaled by `pre`), and the 8-bit form's scale.
@@ -156,48 +185,155 @@ __device__ __forceinline__ RowFactors row_factors(float pre, float sum, float to
   return f;
 }
 
-// Rows of up to tpr * N units of 16 bytes, held in registers between the
-// reduction and the output: x and the residual are read once.  Memory-bound (7
-// bytes an element at 16 bits with a residual and 8-bit output).  Rows that fit
-// a few lanes share a CTA of kSmallThreads; longer rows take a CTA each.  The
-// weights are read per row (L1 and L2 hold them), not kept: the registers go to
-// rows in flight.
+// Short rows, of up to 32 units of 16 bytes: `tpr` lanes each, a unit per lane,
+// held in a register between the reduction and the output.
 //
-// SHIFT: some row starts off a 16-byte boundary.  Inputs are then read as the
-// aligned blocks that cover them and shifted in registers, outputs pass through
-// shared memory (a row of y and one of residual_out per slot) and leave by
-// aligned blocks again; tpr is 32 or the CTA, so that a warp has one offset.
-template <int TYPE, bool EIGHT, bool SHIFT, int N>
-__global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) {
+// SHIFT (in both kernels): some row starts off a 16-byte boundary.  Inputs are
+// then read as the aligned blocks that cover them and shifted in registers,
+// outputs pass through shared memory and leave by aligned blocks again; tpr is
+// 32, so that a warp has one offset.
+template <int TYPE, bool EIGHT, bool SHIFT>
+__global__ void __launch_bounds__(kSmallThreads) rms_norm_small_kernel(NormParams p) {
   using E = Elem<TYPE>;
   typedef typename E::raw raw;
   constexpr int V = E::VEC, ES = (int)sizeof(raw), OE = EIGHT ? 1 : ES;
-  __shared__ float part[2][64];
   extern __shared__ __align__(16) char staged[];
   allow_dependents();
   wait_for_predecessor();
-  const int tpr = p.tpr, rows_per_cta = blockDim.x / tpr;
-  const int lane = threadIdx.x % tpr, slot = threadIdx.x / tpr;
-  const int d = (int)p.d, units = (d + V - 1) / V;
-  const int row_bytes = d * ES;
+  const int tpr = p.tpr, rows_per_cta = kSmallThreads / tpr;
+  const int u = threadIdx.x % tpr, slot = threadIdx.x / tpr;
+  const int d = (int)p.d, units = (d + V - 1) / V, row_bytes = d * ES;
   const bool wide_weights = p.w_f32 != 0 && TYPE != GEMV_TYPE_F32;
-  const uintptr_t weights = (uintptr_t)p.w;
   const int y_space = staged_bytes(units * V * OE);
   char *const row_y = staged + slot * (y_space + units * 16), *const row_s = row_y + y_space;
-  // weights of this thread's units, requested and waited for together (fp32 ones of 16-bit rows unit by unit)
-  auto request_weights = [&](Window<SHIFT> (&win)[N]) {
-    if (wide_weights) return;
+  float w[V];
+  if (!wide_weights) {
+    E::unpack(Window<SHIFT>((uintptr_t)p.w, row_bytes, u, u < units).value((uintptr_t)p.w, row_bytes, u), w);
+  } else if constexpr (V == 8) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) win[i] = Window<SHIFT>(weights, row_bytes, lane + i * tpr, lane + i * tpr < units);
+    for (int h = 0; h < 2; ++h) {
+      float f[4];
+      const Window<SHIFT> win((uintptr_t)p.w, d * 4, 2 * u + h, 8 * u + 4 * h < d);
+      Elem<GEMV_TYPE_F32>::unpack(win.value((uintptr_t)p.w, d * 4, 2 * u + h), f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * h + e] = f[e];
+    }
+  }
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_per_cta; row0 < p.rows; row0 += (int64_t)gridDim.x * rows_per_cta) {
+    const int64_t row = row0 + slot;
+    const bool in = row < p.rows && u < units;
+    const uintptr_t x = (uintptr_t)(static_cast<const raw *>(p.x) + row * p.ldx);
+    const uintptr_t r = p.r ? (uintptr_t)(static_cast<const raw *>(p.r) + row * p.ldr) : 0;
+    float s[V], f[V];
+    const Window<SHIFT> xw(x, row_bytes, u, in), rw(r, row_bytes, u, r && in);
+    E::unpack(xw.value(x, row_bytes, u), s);
+    E::unpack(rw.value(r, row_bytes, u), f);
+    float sum, top;
+    auto reduce = [&]() {
+      sum = top = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        sum = fmaf(s[e], s[e], sum);
+        if (EIGHT) top = max_nan(top, fabsf(s[e] * w[e]));
+      }
+      for (int m = tpr >> 1; m; m >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (EIGHT) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, m));
+      }
+    };
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] += f[e];
+    reduce();
+    if (p.ro && in) {
+      if (SHIFT) reinterpret_cast<uint4 *>(row_s)[u] = E::pack(s);
+      else reinterpret_cast<uint4 *>(static_cast<raw *>(p.ro) + row * p.ldo)[u] = E::pack(s);
+    }
+    const float pre = rescale(sum);
+    if (__any_sync(0xffffffffu, pre != 1.f)) {  // rare; lanes reduce together whichever row needs it
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] *= pre;
+      reduce();
+    }
+    const RowFactors g = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
+    if (EIGHT && u == 0 && in) p.scale[row] = g.scale;
+    if (in) {
+      float y[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) y[e] = (s[e] * w[e]) * g.mul;
+      store_y<TYPE, EIGHT>(SHIFT ? row_y : static_cast<char *>(p.y) + row * p.ldy * OE, u, y);
+    }
+    if constexpr (SHIFT) {
+      __syncwarp();
+      if (row < p.rows) {
+        copy_out<typename OutType<TYPE, EIGHT>::type>(row_y, d * OE, static_cast<char *>(p.y) + row * p.ldy * OE, u, tpr);
+        if (p.ro) copy_out<raw>(row_s, d * ES, static_cast<char *>(p.ro) + row * p.ldo * ES, u, tpr);
+      }
+      __syncwarp();
+    }
+  }
+}
+
+constexpr int kRingStages = 3;
+constexpr int64_t kHalfSm = 110 * 1024, kWholeSm = 224 * 1024;  // shared memory for a CTA beside another, and alone
+
+// Longer rows: a CTA takes a row at a time, kUnits units per thread, held in
+// registers between the reduction and the output.  Memory-bound (7 bytes an
+// element at 16 bits with a residual and 8-bit output); the rows ahead are
+// copied into a ring in shared memory meanwhile, one bulk copy per row of x and
+// of the residual, so that memory does not wait for the reductions.  (With
+// plain loads and as many rows in flight as registers allow, 8192 x 7168 bf16
+// took 88 us.)  The weights are kept in shared memory.  SHIFT: a copy takes the
+// aligned blocks that cover its row, and a row's outputs are staged in the
+// memory of its inputs.
+template <int TYPE, bool EIGHT, bool SHIFT>
+__global__ void __launch_bounds__(kMaxRowThreads) rms_norm_ring_kernel(NormParams p) {
+  using E = Elem<TYPE>;
+  typedef typename E::raw raw;
+  constexpr int V = E::VEC, ES = (int)sizeof(raw), OE = EIGHT ? 1 : ES, N = kUnits;
+  __shared__ float part[2][64];
+  __shared__ uint64_t full[kRingStages];
+  __shared__ int failed_flag, issued;
+  extern __shared__ __align__(16) char ring[];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int d = (int)p.d, units = (d + V - 1) / V, row_bytes = d * ES;
+  const bool wide_weights = p.w_f32 != 0 && TYPE != GEMV_TYPE_F32;
+  const int w_space = units * 16 * (wide_weights ? 2 : 1), area = ring_area(units), areas = SHIFT || p.r ? 2 : 1;
+  const uint4 *weights = reinterpret_cast<const uint4 *>(ring);
+  auto stage_of = [&](int stage, int which) { return ring + w_space + (stage * areas + which) * area; };
+  if (tid == 0) {
+    failed_flag = issued = 0;
+    for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&full[s]), 1);
+    mbar_init_fence();
+  }
+  allow_dependents();
+  wait_for_predecessor();
+  auto start_x = [&](int64_t row) { return (uintptr_t)(static_cast<const raw *>(p.x) + row * p.ldx); };
+  auto start_r = [&](int64_t row) { return (uintptr_t)(static_cast<const raw *>(p.r) + row * p.ldr); };
+  auto request = [&](int64_t row, int stage) {
+    if (row >= p.rows || *(volatile int *)&failed_flag) return;
+    const uintptr_t x = start_x(row), r = p.r ? start_r(row) : 0;
+    const uint32_t bx = (uint32_t)((int)(x & 15) + row_bytes + 15) & ~15u, br = (uint32_t)((int)(r & 15) + row_bytes + 15) & ~15u;
+    const uint32_t bar = smem_u32(&full[stage]);
+    mbar_expect_tx(bar, bx + (p.r ? br : 0));
+    ++issued;
+    copy_bulk(smem_u32(stage_of(stage, 0)), reinterpret_cast<const void *>(x & ~(uintptr_t)15), bx, bar);
+    if (p.r) copy_bulk(smem_u32(stage_of(stage, 1)), reinterpret_cast<const void *>(r & ~(uintptr_t)15), br, bar);
   };
-  auto get_weights = [&](const Window<SHIFT> &win, int u, float (&w)[V]) {
+  if (tid == 0)
+    for (int s = 0; s < p.stages - 1; ++s) request(blockIdx.x + (int64_t)s * gridDim.x, s);
+  for (int i = tid; i < w_space / 16; i += threads) {
+    const int bytes = d * (wide_weights ? 4 : ES);
+    const Window<SHIFT> win((uintptr_t)p.w, bytes, i, 16 * i < bytes);
+    reinterpret_cast<uint4 *>(ring)[i] = win.value((uintptr_t)p.w, bytes, i);
+  }
+  __syncthreads();
+  auto load_weights = [&](int u, float (&w)[V]) {
     if (!wide_weights) {
-      E::unpack(win.value(weights, row_bytes, u), w);
+      E::unpack(weights[u], w);
     } else if constexpr (V == 8) {
-      const Window<SHIFT> a(weights, d * 4, 2 * u, u < units), b(weights, d * 4, 2 * u + 1, u < units && 8 * u + 4 < d);
       float lo[4], hi[4];
-      Elem<GEMV_TYPE_F32>::unpack(a.value(weights, d * 4, 2 * u), lo);
-      Elem<GEMV_TYPE_F32>::unpack(b.value(weights, d * 4, 2 * u + 1), hi);
+      Elem<GEMV_TYPE_F32>::unpack(weights[2 * u], lo);
+      Elem<GEMV_TYPE_F32>::unpack(weights[2 * u + 1], hi);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         w[e] = lo[e];
@@ -205,38 +341,54 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
       }
     }
   };
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * rows_per_cta; row0 < p.rows; row0 += (int64_t)gridDim.x * rows_per_cta) {
-    const int64_t row = row0 + slot;
-    const bool live = row < p.rows;
-    const uintptr_t x = (uintptr_t)(static_cast<const raw *>(p.x) + row * p.ldx);
-    const uintptr_t r = p.r ? (uintptr_t)(static_cast<const raw *>(p.r) + row * p.ldr) : 0;
+  // unit u of a row that was copied to `from`; what lies beyond the row's end is 0
+  auto row_unit = [&](const char *from, uintptr_t start, int u, float (&f)[V]) {
+    const uint4 *at = reinterpret_cast<const uint4 *>(from) + u;
+    uint4 v = at[0];
+    if (SHIFT && (start & 15)) v = shifted(v, at[1], (int)(start & 15));
+    E::unpack(v, f);
+    if (SHIFT && u == units - 1) {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (u * V + e >= d) f[e] = 0.f;
+    }
+  };
+  int turn = 0, stage = 0;
+  uint32_t phase = 0;
+  int64_t ahead = blockIdx.x + (int64_t)(p.stages - 1) * gridDim.x;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ahead += gridDim.x) {
+    const bool ok = wait_for<false>(smem_u32(&full[stage]), phase, &failed_flag, kWaitPolls);
+    char *const from_x = stage_of(stage, 0), *const from_r = stage_of(stage, 1);
     float s[N][V];
-    {
-      Window<SHIFT> xw[N], rw[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) xw[i] = Window<SHIFT>(x, row_bytes, lane + i * tpr, live && lane + i * tpr < units);
+    for (int i = 0; i < N; ++i) {
+      const int u = tid + i * threads;
 #pragma unroll
-      for (int i = 0; i < N; ++i) rw[i] = Window<SHIFT>(r, row_bytes, lane + i * tpr, r && live && lane + i * tpr < units);
+      for (int e = 0; e < V; ++e) s[i][e] = 0.f;
+      if (u < units) {
+        row_unit(from_x, SHIFT ? start_x(row) : 0, u, s[i]);
+        if (p.r) {
+          float f[V];
+          row_unit(from_r, SHIFT ? start_r(row) : 0, u, f);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float f[V];
-        E::unpack(xw[i].value(x, row_bytes, lane + i * tpr), s[i]);
-        E::unpack(rw[i].value(r, row_bytes, lane + i * tpr), f);
+          for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], f[e], f[e + 1]);
+        }
+        if (!ok) {
 #pragma unroll
-        for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], f[e], f[e + 1]);
+          for (int e = 0; e < V; ++e) s[i][e] = __int_as_float(0x7fc00000);
+        }
       }
     }
     float sum, top;
     auto reduce = [&]() {
       float s0 = 0.f, s1 = 0.f;
       top = 0.f;
-      Window<SHIFT> win[N];
-      if (EIGHT) request_weights(win);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
+        const int u = tid + i * threads;
+        if (u >= units) break;
         float w[V];
-        if (EIGHT) get_weights(win[i], lane + i * tpr, w);
+        if (EIGHT) load_weights(u, w);
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           fma2(s0, s1, s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], s0, s1);
@@ -248,25 +400,23 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
         }
       }
       sum = s0 + s1;
-      row_reduce<EIGHT>(sum, top, tpr, part[turn]);
+      row_reduce<EIGHT>(sum, top, threads, part[turn]);
       turn ^= 1;
     };
     reduce();
-    auto store_residual = [&]() {
-      if (!p.ro || !live) return;
+    // All threads are past the row before: its stage is free.
+    if (tid == 0) request(ahead, stage == 0 ? p.stages - 1 : stage - 1);
+    if (p.ro) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const int u = lane + i * tpr;
+        const int u = tid + i * threads;
         if (u >= units) break;
-        if (SHIFT) reinterpret_cast<uint4 *>(row_s)[u] = E::pack(s[i]);
+        if (SHIFT) reinterpret_cast<uint4 *>(from_x)[u] = E::pack(s[i]);
         else reinterpret_cast<uint4 *>(static_cast<raw *>(p.ro) + row * p.ldo)[u] = E::pack(s[i]);
       }
-    };
-    store_residual();
-    // Rare: squares beyond fp32's range.  (All threads of a CTA-wide row agree;
-    // lanes of short rows reduce together whichever row needs it.)
+    }
     const float pre = rescale(sum);
-    if (tpr > 32 ? pre != 1.f : __any_sync(0xffffffffu, pre != 1.f)) {
+    if (pre != 1.f) {  // rare: squares beyond fp32's range
 #pragma unroll
       for (int i = 0; i < N; ++i) {
 #pragma unroll
@@ -274,47 +424,39 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_kernel(NormParams p) 
       }
       reduce();
     }
-    Window<SHIFT> win[N];
-    request_weights(win);
     const RowFactors f = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
-    if (live) {
-      if (EIGHT && lane == 0) p.scale[row] = f.scale;
+    if (EIGHT && tid == 0) p.scale[row] = f.scale;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int u = lane + i * tpr;
-        if (u >= units) break;
-        float w[V], y[V];
-        get_weights(win[i], u, w);
+    for (int i = 0; i < N; ++i) {
+      const int u = tid + i * threads;
+      if (u >= units) break;
+      float w[V], y[V];
+      load_weights(u, w);
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
-          mul2(y[e], y[e + 1], y[e], y[e + 1], f.mul, f.mul);
-        }
-        if constexpr (!EIGHT) {
-          if (SHIFT) reinterpret_cast<uint4 *>(row_y)[u] = E::pack(y);
-          else reinterpret_cast<uint4 *>(static_cast<raw *>(p.y) + row * p.ldy)[u] = E::pack(y);
-        } else {
-          char *to = SHIFT ? row_y : static_cast<char *>(p.y) + row * p.ldy;
-          if constexpr (V == 8)
-            reinterpret_cast<uint2 *>(to)[u] = make_uint2(e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16,
-                                                          e4m3_pair(y[4], y[5]) | e4m3_pair(y[6], y[7]) << 16);
-          else
-            reinterpret_cast<uint32_t *>(to)[u] = e4m3_pair(y[0], y[1]) | e4m3_pair(y[2], y[3]) << 16;
-        }
+      for (int e = 0; e < V; e += 2) {
+        mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+        mul2(y[e], y[e + 1], y[e], y[e + 1], f.mul, f.mul);
       }
+      store_y<TYPE, EIGHT>(SHIFT ? from_r : static_cast<char *>(p.y) + row * p.ldy * OE, u, y);
     }
     if constexpr (SHIFT) {
-      if (tpr > 32) __syncthreads();
-      else __syncwarp();
-      if (live) {
-        if constexpr (EIGHT) copy_out<uint8_t>(row_y, d, static_cast<char *>(p.y) + row * p.ldy, lane, tpr);
-        else copy_out<raw>(row_y, d * OE, static_cast<char *>(p.y) + row * p.ldy * OE, lane, tpr);
-        if (p.ro) copy_out<raw>(row_s, d * ES, static_cast<char *>(p.ro) + row * p.ldo * ES, lane, tpr);
-      }
-      // The next row's outputs are staged after its reduction: a CTA-wide
-      // barrier, but for a warp's rows only its shuffles.
-      if (tpr <= 32) __syncwarp();
+      __syncthreads();
+      copy_out<typename OutType<TYPE, EIGHT>::type>(from_r, d * OE, static_cast<char *>(p.y) + row * p.ldy * OE, tid, threads);
+      if (p.ro) copy_out<raw>(from_x, d * ES, static_cast<char *>(p.ro) + row * p.ldo * ES, tid, threads);
+      fence_async_smem();  // before the copy that refills the stage
     }
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+  }
+  __syncthreads();
+  if (failed_flag && tid < 32) {  // after a wait that gave up: copies in flight land before the CTA leaves
+    int none = 0;
+    if (tid == 0) atomicAdd(p.timeouts, 1u);
+    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+      if (!wait_for<false>(smem_u32(&full[i % p.stages]), (i / p.stages) & 1, &none, kWaitPolls) && tid == 0)
+        atomicOr(p.timeouts, kDrainTimeoutBit);
   }
 }
 
@@ -405,32 +547,40 @@ template <int TYPE, bool EIGHT, bool SHIFT>
 int launch_norm(NormParams p, int sms, cudaStream_t stream) {
   constexpr int V = Elem<TYPE>::VEC, OE = EIGHT ? 1 : 16 / V;
   const int64_t units = (p.d + V - 1) / V;
-  const bool small = units <= 32;  // a unit per lane
-  const int64_t need = small ? units : (units + kUnits - 1) / kUnits;
+  if (units <= 32) {
+    p.tpr = SHIFT ? 32 : 1;
+    while (p.tpr < units) p.tpr *= 2;
+    const int64_t rows_per_cta = kSmallThreads / p.tpr, ctas = (p.rows + rows_per_cta - 1) / rows_per_cta;
+    // staged rows, and a block that may be read beyond the last
+    const size_t smem = SHIFT ? (size_t)(rows_per_cta * (staged_bytes((int)units * V * OE) + units * 16) + 16) : 0;
+    return launch_op(rms_norm_small_kernel<TYPE, EIGHT, SHIFT>, dim3((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20)),
+                     kSmallThreads, smem, 1, stream, p);
+  }
+  const int64_t need = (units + kUnits - 1) / kUnits;
   if (need > kMaxRowThreads) {
     const int64_t grid = p.rows < (int64_t)sms * 4 ? p.rows : (int64_t)sms * 4;
     return launch_op(rms_norm_long_kernel<TYPE, EIGHT, !SHIFT>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
   }
-  int threads = kSmallThreads;
-  if (need <= 32) {
-    p.tpr = SHIFT ? 32 : 1;
-    while (p.tpr < need) p.tpr *= 2;
-  } else {
-    threads = p.tpr = (int)((need + 31) / 32 * 32);
-  }
-  const int64_t rows_per_cta = threads / p.tpr;
-  int64_t grid = (p.rows + rows_per_cta - 1) / rows_per_cta;
-  if (grid > (1 << 20)) grid = 1 << 20;
-  // staged rows, and a block that may be read beyond the last
-  const size_t smem = SHIFT ? (size_t)(rows_per_cta * (staged_bytes((int)units * V * OE) + units * 16) + 16) : 0;
-  void (*fn)(NormParams) = small ? rms_norm_kernel<TYPE, EIGHT, SHIFT, 1> : rms_norm_kernel<TYPE, EIGHT, SHIFT, kUnits>;
+  const int threads = (int)((need + 31) / 32 * 32);
+  // As many rows in the ring as leave room for two CTAs per SM, or one.
+  const int64_t w_space = units * 16 * (p.w_f32 && TYPE != GEMV_TYPE_F32 ? 2 : 1);
+  const int64_t per_stage = ring_area((int)units) * (SHIFT || p.r ? 2 : 1);
+  p.stages = kRingStages;
+  if (w_space + p.stages * per_stage > kHalfSm) p.stages = 2;
+  const size_t smem = (size_t)(w_space + p.stages * per_stage);
+  auto fn = rms_norm_ring_kernel<TYPE, EIGHT, SHIFT>;
   if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+    const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kWholeSm);
     if (e != cudaSuccess) {
       cudaGetLastError();
       return cuda_failure((int)e);
     }
   }
+  int64_t per_sm = kWholeSm / (int64_t)(smem + 2048);
+  if (per_sm > 2048 / (threads < 64 ? 64 : threads)) per_sm = 2048 / (threads < 64 ? 64 : threads);
+  if (per_sm * threads > kMaxRowThreads) per_sm = kMaxRowThreads / threads;  // 64 registers each
+  if (per_sm < 1) per_sm = 1;
+  const int64_t grid = p.rows < sms * per_sm ? p.rows : sms * per_sm;
   return launch_op(fn, dim3((unsigned)grid), threads, smem, 1, stream, p);
 }
 
@@ -472,13 +622,15 @@ extern "C" int rms_norm_fused(const void *x, int64_t ldx, const void *residual, 
   if (rows_overlap(O, X) && !(residual_out == x && ldo == ldx)) return GEMV_ERR_ALIAS;
   if (rows_overlap(O, R) && !(residual_out == residual && ldo == ldr)) return GEMV_ERR_ALIAS;
   int dev = -1, sms = 0;
-  const int st = current_device(&dev, &sms);
+  int st = current_device(&dev, &sms);
   if (st != GEMV_OK) return st;
   if (!on_device(dev, {x, residual, weight, y, scale, residual_out})) return GEMV_ERR_DEVICE;
   NormParams p;
   p.x = x; p.r = residual; p.w = weight; p.y = y; p.ro = residual_out; p.scale = scale;
   p.ldx = ldx; p.ldr = ldr; p.ldy = ldy; p.ldo = ldo; p.rows = rows; p.d = d;
-  p.eps = eps; p.w_f32 = weight_dtype == GEMV_TYPE_F32 ? 1 : 0; p.tpr = 0;
+  p.eps = eps; p.w_f32 = weight_dtype == GEMV_TYPE_F32 ? 1 : 0; p.tpr = 0; p.stages = 0;
+  st = wait_counter(dev, &p.timeouts);
+  if (st != GEMV_OK) return st;
   // 16-byte accesses where every row starts on a 16-byte boundary (8-bit rows:
   // on one of the 8 or 4 bytes that a 16-byte unit of x becomes).
   const int vec = 16 / es;
