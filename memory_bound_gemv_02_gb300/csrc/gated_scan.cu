@@ -247,6 +247,10 @@ __device__ __forceinline__ void load_maps(const float *p, float (&A)[V], float (
     A[e] = m.x; B[e] = m.y; A[e + 1] = m.z; B[e + 1] = m.w;
   }
 }
+// 16 bytes to shared memory without passing a register, zeros if not `in`.
+__device__ __forceinline__ void copy16(uint32_t dst, uintptr_t src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ uint32_t lds32(const char *p) { return *reinterpret_cast<const uint32_t *>(p); }
 
 // NaN if any of the values is an infinity or a NaN, else 0.
@@ -283,9 +287,10 @@ struct alignas(8) TileShared {
 // Rounds alternate between two sets of maps, so that no further barrier is
 // needed: a CTA sends the maps of a round after its threads have read those of
 // the round before.  The tiles of the rounds ahead are copied into shared memory
-// meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, row
-// by row as the aligned 16-byte blocks that cover its channels, whose words a
-// thread joins to its own.
+// meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, as
+// the aligned 16-byte blocks that cover its channels, whose words a thread joins
+// to its own.  (A bulk copy per row instead: one per 17 cycles and SM at best,
+// 245 us forward for 1 x 65537 x 1001 fp16.)
 //
 // Steps run on plain products and sums, which are right as long as everything
 // is finite and no product of decays is 0; since what is not finite stays so to
@@ -350,27 +355,39 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
                     BACK ? row_of(s0 + S::kTime - 1, array) : s0, sequence, bar);
       }
     } else {
+      // Blocks of a row side by side, then the one more that a row off its
+      // boundary needs.  A thread's rows are a multiple of 32 apart and so start
+      // at the same place within their 16 bytes.
+      constexpr int kBlocks = LANES / 2, kRows = kScanThreads / kBlocks;
       const int span = (int)(p.width - c0 < S::kWidth ? p.width - c0 : S::kWidth) * ES;
-      constexpr int kRows = S::kArrays * S::kTime, kEach = (kRows + kScanThreads - 1) / kScanThreads;
-      const void *from[kEach];
-      uint32_t bytes[kEach], total = 0;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int n = tid + i * kScanThreads, array = n / S::kTime, r = n % S::kTime;
-        const int row = BACK ? row_of(s0 + S::kTime - 1, array) + r : s0 + r;
-        const bool in = n < kRows && row >= 0 && row < steps;
-        const uintptr_t start = (uintptr_t)(inputs[array < 2 ? array : 2] + (in ? row * pitch[array < 2 ? array : 2] : 0));
-        from[i] = reinterpret_cast<const void *>(start & ~(uintptr_t)15);
-        bytes[i] = in ? (uint32_t)(((int)(start & 15) + span + 15) & ~15) : 0u;
-        total += bytes[i];
-      }
-      if (total) mbar_expect_tx(bar, total);
-      else mbar_arrive(bar);
+      for (int array = 0; array < S::kArrays; ++array) {
+        const int first = BACK ? row_of(s0 + S::kTime - 1, array) : s0;  // the tile's row 0
+        const char *base = reinterpret_cast<const char *>(inputs[array]);
+        const int64_t bytes = pitch[array] * ES;
+        {
+          const int r0 = tid / kBlocks, block = tid % kBlocks;
+          int row = first + r0;
+          const uintptr_t start = (uintptr_t)(base + row * bytes);
+          const bool in = (int)(start & 15) + span > 16 * block;
+          uintptr_t src = (start & ~(uintptr_t)15) + 16 * block;
+          const uint32_t dst = smem_u32(to + array * S::kArrayBytes + r0 * S::kRowPitch + block * 16);
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int n = tid + i * kScanThreads;
-        if (bytes[i]) copy_bulk(smem_u32(to + n * S::kRowPitch), from[i], bytes[i], bar);
+          for (int i = 0; i < S::kTime / kRows; ++i) {
+            copy16(dst + i * kRows * S::kRowPitch, src, in && row >= 0 && row < steps);
+            src += (uintptr_t)(kRows * bytes);
+            row += kRows;
+          }
+        }
+        if (tid < S::kTime) {
+          const int row = first + tid;
+          const uintptr_t start = (uintptr_t)(base + row * bytes);
+          copy16(smem_u32(to + array * S::kArrayBytes + tid * S::kRowPitch + kBlocks * 16),
+                 (start & ~(uintptr_t)15) + 16 * kBlocks,
+                 (int)(start & 15) + span > 16 * kBlocks && row >= 0 && row < steps);
+        }
       }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
     }
   };
   for (int r = 0; r < S::kStages - 1; ++r) request(r);
@@ -382,22 +399,27 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
     wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, kWaitPolls);
     const char *mine = dynamic + stage * S::kStageBytes + side * 8 +
                        (BACK ? S::kTime - 1 - group * N : group * N) * S::kRowPitch;
-    auto input = [&](int u, int array, float (&f)[V]) {
+    // without TMA: where this thread's first row of each array starts within its 16 bytes
+    uint32_t offset[3];
+    if constexpr (!TMA) {
+#pragma unroll
+      for (int array = 0; array < S::kArrays; ++array)
+        offset[array] = (uint32_t)(uintptr_t)inputs[array] +
+                        (uint32_t)row_of(s0, array) * (uint32_t)pitch[array] * (uint32_t)ES;
+    }
+    auto words = [&](int u, int array) {
       const char *from = mine + array * S::kArrayBytes + (BACK ? -u : u) * S::kRowPitch;
-      uint2 w;
-      if constexpr (TMA) {
-        w = *reinterpret_cast<const uint2 *>(from);
-      } else {
-        const uint32_t off = ((uint32_t)(uintptr_t)inputs[array] +
-                              (uint32_t)row_of(s0 + u, array) * (uint32_t)pitch[array] * (uint32_t)ES) & 15;
-        from += off & 12;
-        w = make_uint2(lds32(from), lds32(from + 4));
-        if constexpr (ES == 2) {
-          const uint32_t bits = (off & 2) * 8;
-          w = make_uint2(__funnelshift_r(w.x, w.y, bits), __funnelshift_r(w.y, lds32(from + 8), bits));
-        }
-        if (s0 + u >= steps) w = make_uint2(0u, 0u);  // rows that were not copied
+      if constexpr (TMA) return *reinterpret_cast<const uint2 *>(from);
+      const uint32_t off = offset[array] + (uint32_t)(BACK ? -u : u) * (uint32_t)pitch[array] * (uint32_t)ES;
+      from += off & 12;
+      uint2 w = make_uint2(lds32(from), lds32(from + 4));
+      if constexpr (ES == 2) {
+        const uint32_t bits = (off & 2) * 8;
+        w = make_uint2(__funnelshift_r(w.x, w.y, bits), __funnelshift_r(w.y, lds32(from + 8), bits));
       }
+      return w;
+    };
+    auto widen = [&](uint2 w, float (&f)[V]) {
       if constexpr (V == 4) {
         const float2 lo = TYPE == GEMV_TYPE_F16 ? F16::pair(w.x) : BF16::pair(w.x);
         const float2 up = TYPE == GEMV_TYPE_F16 ? F16::pair(w.y) : BF16::pair(w.y);
@@ -413,6 +435,8 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
         }
       }
     };
+    auto input = [&](int u, int array, float (&f)[V]) { widen(words(u, array), f); };
+    uint2 kept[TMA ? 1 : N];  // x, or dh: joining its words again would cost more than the registers
 
     // 1. this thread's map: steps beyond the end read zeros, decay 1 and 0 added
     float a[N][V], A[V], B[V];
@@ -425,7 +449,9 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
     for (int u = 0; u < N; ++u) {
       float xf[V];
       input(u, 1, a[u]);
-      input(u, 0, xf);
+      const uint2 x = words(u, 0);
+      if constexpr (!TMA) kept[u] = x;
+      widen(x, xf);
 #pragma unroll
       for (int e = 0; e < V; e += 2) {
         float &a0 = a[u][e], &a1 = a[u][e + 1];
@@ -592,7 +618,8 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
     auto step = [&](int u, const float (&d)[V], const bool robust) {
       const bool in = channels > 0 && s0 + u < steps;
       float xf[V];
-      input(u, 0, xf);
+      if (TMA || robust) input(u, 0, xf);
+      else widen(kept[TMA ? 0 : u], xf);
       if constexpr (BACK) {
         float hf[V], dx[V], dg[V];
         input(u, 2, hf);
