@@ -362,15 +362,16 @@ int gemv_debug_inject(int status);
  * warp's bounded wait for the copies it had already issued also ran out:
  * its CTA then exited with a bulk copy possibly still writing shared
  * memory, and the device's state is unspecified -- treat the device as
- * unusable for the rest of the process.
+ * unusable for the rest of the process.  The kernels of gemv_ops.h that wait on
+ * copies count here too (CTAs that gave up, whose outputs are NaN from there on).
  */
 #define GEMV_DRAIN_TIMEOUT 0x80000000u
 int gemv_wait_timeouts(int reset, uint32_t *count);
 
 /*
  * Test hook (no counterpart on the pages): the next launch of the bulk
- * variant (on any thread) gives each
- * ring wait `polls` polls instead of 2^20 (0 = every wait gives up at once,
+ * variant, or of a kernel of gemv_ops.h that waits on copies (on any thread),
+ * gives each ring wait `polls` polls instead of 2^20 (0 = every wait gives up at once,
  * exercising the path above without any hang); -1 clears it.  The waits
  * that drain copies already issued keep the full limit.
  */

@@ -23,6 +23,10 @@
  * preceding kernel has completed).  Results are bitwise reproducible: every sum
  * runs in an order fixed by the sizes, strides and alignment.
  *
+ * Kernels that wait on their own copies or on another CTA of their cluster do so
+ * for a bounded number of polls: a wait that runs out writes NaN to what its CTA
+ * had still to write and is counted by gemv_wait_timeouts().
+ *
  * An output overlaps no other buffer of its call, except where an entry says
  * that it may be the very same buffer as an input; a partial overlap returns
  * GEMV_ERR_ALIAS.  Buffers whose rows interleave without sharing an element
@@ -122,9 +126,7 @@ typedef struct gemm_epilogue {
  * nothing, free again after the call's work on the stream; a shorter one returns
  * GEMV_ERR_SCRATCH), and the call launches a second kernel.  Weights kept with
  * 16-byte rows need none.  Products and sums run on the tensor cores with fp32
- * accumulation.  The kernel's waits on its own copies
- * are bounded: one that runs out writes NaN for its tile and is counted by
- * gemv_wait_timeouts().
+ * accumulation. 
  */
 int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda, void *C, int64_t ldc, int64_t m,
                int64_t n, int64_t k, int dtype, int out_dtype, const gemm_epilogue *epilogue,

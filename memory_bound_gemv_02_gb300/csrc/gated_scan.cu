@@ -264,13 +264,15 @@ __device__ __forceinline__ float not_finite(const float (&f)[V]) {
 
 struct TileParams : ScanParams {
   CUtensorMap maps[3];  // TMA: of x, g, h, each as (width, steps, batch)
+  int32_t polls;        // of the waits for copies
   uint32_t *timeouts;
 };
 
 struct alignas(8) TileShared {
   uint64_t full[4];      // a stage's copies have landed (TMA)
   uint64_t exchanged[2]; // the cluster's maps of a round are here
-  int failed;
+  int failed;            // a wait for copies gave up
+  int lost;              // a wait for the cluster's maps gave up
   int issued;            // rounds whose copies were started
 };
 
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   const int round_steps = S::kTime * cluster, rounds = (steps + round_steps - 1) / round_steps;
 
   if (tid == 0) {
-    sh.failed = sh.issued = 0;
+    sh.failed = sh.lost = sh.issued = 0;
     for (int i = 0; i < S::kStages; ++i) mbar_init(smem_u32(&sh.full[i]), TMA ? 1 : kScanThreads);
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&sh.exchanged[i]), 1);
     mbar_init_fence();
@@ -395,8 +397,9 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   for (int round = 0; round < rounds; ++round) {
     const int stage = round % S::kStages, s0 = tile_step(round) + group * N;
     float *warp_maps = all_warp_maps + (round & 1) * S::kWarpMaps;
-    if (cluster > 1 && tid == 0) mbar_expect_tx(smem_u32(&sh.exchanged[round & 1]), (uint32_t)cluster * S::kWidth * 8);
-    wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, kWaitPolls);
+    if (cluster > 1 && tid == 0 && !*(volatile int *)&sh.lost)
+      mbar_expect_tx(smem_u32(&sh.exchanged[round & 1]), (uint32_t)cluster * S::kWidth * 8);
+    wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, p.polls);
     const char *mine = dynamic + stage * S::kStageBytes + side * 8 +
                        (BACK ? S::kTime - 1 - group * N : group * N) * S::kRowPitch;
     // without TMA: where this thread's first row of each array starts within its 16 bytes
@@ -528,10 +531,12 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
           B1 = apply(A2, B2, B1);
           A1 = chain(A1, A2);
         }
+        if (*(volatile int *)&sh.failed) A1 = B1 = __int_as_float(0x7fc00000);  // what follows is not known
         const uint32_t to = smem_u32(cta_maps + (rank * S::kWidth + tid) * 2);
-        for (int r = 0; r < cluster; ++r) st_cluster_counted(cluster_address(to, r), A1, B1, cluster_address(bar, r));
+        for (int r = 0; r < (*(volatile int *)&sh.lost ? 0 : cluster); ++r)
+          st_cluster_counted(cluster_address(to, r), A1, B1, cluster_address(bar, r));
       }
-      wait_for<true>(bar, (round >> 1) & 1, &sh.failed, kWaitPolls);
+      wait_for<true>(bar, (round >> 1) & 1, &sh.lost, kWaitPolls);
       for (int r = 0; r < cluster; ++r) {
         float Ar[V], Br[V];
         load_maps(cta_maps + (r * S::kWidth + side * V) * 2, Ar, Br);
@@ -605,7 +610,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
         }
       }
     };
-    if (__any_sync(0xffffffffu, *(volatile int *)&sh.failed != 0)) {
+    if (__any_sync(0xffffffffu, *(volatile int *)&sh.failed != 0 || *(volatile int *)&sh.lost != 0)) {
 #pragma unroll 1
       for (int u = 0; u < N; ++u) {
 #pragma unroll
@@ -676,20 +681,25 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
       for (int e = 0; e < V; ++e) carried[e] = v[e];
     }
   }
+  if (cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
+  __syncthreads();
+  const bool gave_up = sh.failed || sh.lost;
   // the sequence's last value: every thread's of a cluster's CTA, the last group's of a CTA alone
   if (p.last && rank == 0 && group == (cluster > 1 ? 0 : S::kGroups - 1)) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      if (e < channels) p.last[cell + e] = carried[e];
+      if (e < channels) p.last[cell + e] = gave_up ? __int_as_float(0x7fc00000) : carried[e];
   }
-  if (cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
-  __syncthreads();
-  if (sh.failed && warp == 0) {  // after a wait that gave up: copies in flight land before the CTA leaves
-    int none = 0;
-    if (lane == 0) atomicAdd(p.timeouts, 1u);
-    for (int r = sh.issued < S::kStages ? 0 : sh.issued - S::kStages; r < sh.issued; ++r)
-      if (!wait_for<false>(smem_u32(&sh.full[r % S::kStages]), (r / S::kStages) & 1, &none, kWaitPolls) && lane == 0)
-        atomicOr(p.timeouts, kDrainTimeoutBit);
+  if (gave_up) {  // copies in flight land before the CTA leaves
+    if (tid == 0) atomicAdd(p.timeouts, 1u);
+    if constexpr (!TMA) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 0) {
+      int none = 0;
+      for (int r = sh.issued < S::kStages ? 0 : sh.issued - S::kStages; r < sh.issued; ++r)
+        if (!wait_for<false>(smem_u32(&sh.full[r % S::kStages]), (r / S::kStages) & 1, &none, kWaitPolls) && lane == 0)
+          atomicOr(p.timeouts, kDrainTimeoutBit);
+    }
   }
 }
 
@@ -741,6 +751,7 @@ int launch_tiles(const ScanParams &scan, int sms, uint32_t *timeouts, cudaStream
   TileParams p = {};
   static_cast<ScanParams &>(p) = scan;
   p.timeouts = timeouts;
+  p.polls = take_wait_budget(kWaitPolls);
   p.chains = (int32_t)((p.width + S::kWidth - 1) / S::kWidth);
   const int64_t units = p.batch * p.chains;
   // Few chains: clusters split their sequences, as far as all CTAs fit at once.

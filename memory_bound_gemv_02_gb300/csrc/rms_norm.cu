@@ -34,6 +34,7 @@ struct NormParams {
   int32_t w_f32;
   int32_t tpr;  // threads per row: a power of two up to 32, or the whole CTA
   int32_t stages;  // rms_norm_ring_kernel: rows in shared memory
+  int32_t polls;   // of its waits for copies
   uint32_t *timeouts;
 };
 
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_ring_kernel(NormParam
   uint32_t phase = 0;
   int64_t ahead = blockIdx.x + (int64_t)(p.stages - 1) * gridDim.x;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ahead += gridDim.x) {
-    const bool ok = wait_for<false>(smem_u32(&full[stage]), phase, &failed_flag, kWaitPolls);
+    const bool ok = wait_for<false>(smem_u32(&full[stage]), phase, &failed_flag, p.polls) && !*(volatile int *)&failed_flag;
     char *const from_x = stage_of(stage, 0), *const from_r = stage_of(stage, 1);
     float s[N][V];
 #pragma unroll
@@ -566,6 +567,7 @@ int launch_norm(NormParams p, int sms, cudaStream_t stream) {
   const int64_t w_space = units * 16 * (p.w_f32 && TYPE != GEMV_TYPE_F32 ? 2 : 1);
   const int64_t per_stage = ring_area((int)units) * (SHIFT || p.r ? 2 : 1);
   p.stages = kRingStages;
+  p.polls = take_wait_budget(kWaitPolls);
   if (w_space + p.stages * per_stage > kHalfSm) p.stages = 2;
   const size_t smem = (size_t)(w_space + p.stages * per_stage);
   auto fn = rms_norm_ring_kernel<TYPE, EIGHT, SHIFT>;

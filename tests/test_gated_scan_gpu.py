@@ -224,6 +224,28 @@ def test_repeatable_and_on_a_stream(cuda_dev):
         assert all(torch.equal(p, q) for p, q in zip(grads, grads2))
 
 
+@pytest.mark.parametrize("b,t,d", [(2, 700, 64), (1, 5000, 512), (2, 700, 65), (40, 200, 512)])
+def test_a_wait_that_gives_up(cuda_dev, b, t, d):
+    """Waits for copies given no polls: the calls return, their outputs are NaN, the
+    counter says so, and the next calls are right."""
+    x, gate, h0 = _inputs(b, t, d, torch.bfloat16, cuda_dev, 53)
+    dh = ref.uniform(x.shape, torch.bfloat16, 59, cuda_dev)
+    torch.cuda.synchronize()
+    g.gemv_wait_timeouts(reset=True)
+    g.gemv_debug_wait_budget(0)
+    h, _ = g.gated_scan(x, gate, h0=h0)
+    torch.cuda.synchronize()
+    assert torch.isnan(h).all() and g.gemv_wait_timeouts(reset=True) > 0
+    h, state = g.gated_scan(x, gate, h0=h0)
+    _check_forward(x, gate, h0, h, state, "after")
+    g.gemv_debug_wait_budget(0)
+    dx, dg, _ = g.gated_scan_backward(dh, gate, h, h0=h0)
+    torch.cuda.synchronize()
+    assert torch.isnan(dx).all() and torch.isnan(dg).all() and g.gemv_wait_timeouts(reset=True) > 0
+    _check_backward(dh, gate, h, h0, None, *g.gated_scan_backward(dh, gate, h, h0=h0), "after")
+    assert g.gemv_wait_timeouts() == 0
+
+
 def test_refusals(cuda_dev):
     x, gate, h0 = _inputs(2, 6, 16, torch.bfloat16, cuda_dev, 47)
     with pytest.raises(TypeError):

@@ -138,6 +138,21 @@ def test_repeatable(cuda_dev):
         assert torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("rows,d", [(5, 4096), (2000, 1024), (300, 7169)])
+def test_a_wait_that_gives_up(cuda_dev, rows, d):
+    """A wait for copies given no polls: the call returns, its outputs are NaN, the
+    counter says so, and the next call is right."""
+    x, r, w = _inputs(rows, d, torch.bfloat16, cuda_dev, 81)
+    torch.cuda.synchronize()
+    g.gemv_wait_timeouts(reset=True)
+    g.gemv_debug_wait_budget(0)
+    y, scale, _ = g.rms_norm_fused(x, w, residual=r, eight_bit=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(y.float()).all() and torch.isnan(scale).all() and g.gemv_wait_timeouts(reset=True) > 0
+    _check(x, w, r, 1e-6, *g.rms_norm_fused(x, w, residual=r, eight_bit=True), "after")
+    assert g.gemv_wait_timeouts() == 0
+
+
 def test_refusals(cuda_dev):
     x, r, w = _inputs(4, 32, torch.bfloat16, cuda_dev, 71)
     with pytest.raises(TypeError):
