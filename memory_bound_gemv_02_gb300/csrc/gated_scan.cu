@@ -95,6 +95,9 @@ __device__ __forceinline__ float advance(float a, float v, float p) {
 // get lost here; the runs' B hold one too.)
 __device__ __forceinline__ float chain(float a1, float a2) { return fmaxf(a1 * a2, fminf(fminf(a1, a2), 1e-45f)); }
 
+// The product A of several runs' decays, of which `least` is the smallest.
+__device__ __forceinline__ float kept_above_zero(float A, float least) { return fmaxf(A, fminf(least, 1e-45f)); }
+
 // A run's map applied to v.  A state of zero stays zero however far A grew.
 __device__ __forceinline__ float apply(float A, float B, float v) { return A == 0.f || v == 0.f ? B : fmaf(A, v, B); }
 
@@ -119,7 +122,6 @@ struct Lane {
     }
     return b;
   }
-  static __device__ __forceinline__ Block zero() { return Block{}; }
   static __device__ __forceinline__ void unpack(const Block &b, float (&f)[V]) {
     if constexpr (VECTOR) E::unpack(make_uint4(b.w[0], b.w[1], b.w[2], b.w[3]), f);
     else if constexpr (sizeof(raw) == 4) f[0] = __uint_as_float(b.w[0]);
@@ -207,18 +209,18 @@ struct Tile {
   static constexpr int kWidth = LANES * V;
   static constexpr int kGroups = kScanThreads / LANES;
   static constexpr int kPerWarp = 32 / LANES;
-  static constexpr int kSteps = 8;
+  static constexpr int kSteps = TMA || !BACK ? 8 : 4;
   static constexpr int kTime = kGroups * kSteps;
   static constexpr int kArrays = BACK ? 3 : 2;
   static constexpr int kRowPitch = LANES * 8 + (TMA ? 0 : 16);  // without TMA a row starts anywhere in its 16 bytes
   static constexpr int kArrayBytes = kTime * kRowPitch;
   static constexpr int kStageBytes = kArrays * kArrayBytes;
-  static constexpr int kCtas = TMA || !BACK ? 2 : 1;            // per SM
+  static constexpr int kCtas = 2;  // per SM
   static constexpr int kStages = TMA ? (BACK ? 2 : 3) : BACK ? 3 : 2;
   static constexpr int kWarps = kScanThreads / 32;
   static constexpr int kWarpMaps = kWarps * kWidth * 2;         // floats: [warp][A, B][channel]
   static constexpr int kCtaMaps = kMaxScanCluster * kWidth * 2; // [CTA][channel][A, B]
-  static constexpr int kSmem = kStages * kStageBytes + 2 * (kWarpMaps + kCtaMaps + kWidth) * 4;  // two rounds of maps and carried values
+  static constexpr int kSmem = kStages * kStageBytes + 2 * (kWarpMaps + kCtaMaps) * 4;  // two rounds of maps
 };
 
 // V adjacent floats of shared memory.
@@ -227,9 +229,11 @@ __device__ __forceinline__ void load_floats(const float *p, float (&f)[V]) {
   if constexpr (V == 4) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  } else {
+  } else if constexpr (V == 2) {
     const float2 v = *reinterpret_cast<const float2 *>(p);
     f[0] = v.x; f[1] = v.y;
+  } else {
+    f[0] = *p;
   }
 }
 template <int V>
@@ -238,15 +242,6 @@ __device__ __forceinline__ void store_floats(float *p, const float (&f)[V]) {
   else *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
 }
 
-// Maps of V adjacent channels in shared memory, as [channel][A, B].
-template <int V>
-__device__ __forceinline__ void load_maps(const float *p, float (&A)[V], float (&B)[V]) {
-#pragma unroll
-  for (int e = 0; e < V; e += 2) {
-    const float4 m = *reinterpret_cast<const float4 *>(p + 2 * e);
-    A[e] = m.x; B[e] = m.y; A[e + 1] = m.z; B[e + 1] = m.w;
-  }
-}
 // 16 bytes to shared memory without passing a register, zeros if not `in`.
 __device__ __forceinline__ void copy16(uint32_t dst, uintptr_t src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -278,21 +273,27 @@ struct alignas(8) TileShared {
 
 // A cluster of p.cluster CTAs owns a chain: kWidth channels of one sequence.  In
 // a round its CTAs take consecutive tiles of kTime steps, and a tile goes
-//   1. each thread folds its kSteps steps into a map per channel; the two
-//      groups of a warp are composed by shuffles, the warp's map goes to shared
-//      memory; one barrier;
-//   2. (clusters) each CTA sends its map to all CTAs of the cluster with stores
-//      that count themselves at the receiver's barrier: a cluster barrier would
-//      wait for the tile's stores to global memory as well;
-//   3. each thread applies the maps before its own to the carried value, which
-//      all threads of a channel keep, and walks its steps again, writing them.
+//   1. each thread folds its kSteps steps into a map per channel; the groups of
+//      a warp are composed by shuffles, the warp's map goes to shared memory;
+//      one barrier;
+//   2. a lane takes a channel or two and composes the warps' maps for them.  In
+//      clusters the CTA's map goes to all CTAs, warp r's lanes sending to CTA r,
+//      with stores that count themselves at the receiver's barrier: a cluster
+//      barrier would wait for the tile's stores to global memory as well.  The
+//      maps before the warp's own are applied to the carried value, which every
+//      warp of every CTA keeps;
+//   3. shuffles give each thread the value at its steps, and it walks them
+//      again, writing them.
+// (With threads composing the maps of all their channels, four times as many
+// words, and one warp sending for all, step 2 was half of a round: 1 x 65536 x
+// 1024 bf16 125 us forward, 149 backward, now 91 and 118.)
 // Rounds alternate between two sets of maps, so that no further barrier is
 // needed: a CTA sends the maps of a round after its threads have read those of
 // the round before.  The tiles of the rounds ahead are copied into shared memory
 // meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, as
 // the aligned 16-byte blocks that cover its channels, whose words a thread joins
 // to its own.  (A bulk copy per row instead: one per 17 cycles and SM at best,
-// 245 us forward for 1 x 65537 x 1001 fp16.)
+// 245 us forward for 1 x 65537 x 1001 fp16; now 198.)
 //
 // Steps run on plain products and sums, which are right as long as everything
 // is finite and no product of decays is 0; since what is not finite stays so to
@@ -309,7 +310,6 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   __shared__ TileShared sh;
   float *all_warp_maps = reinterpret_cast<float *>(dynamic + S::kStages * S::kStageBytes);
   float *all_cta_maps = all_warp_maps + 2 * S::kWarpMaps;
-  float *all_carried = all_cta_maps + 2 * S::kCtaMaps;  // [round parity][channel], one CTA per chain
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int side = tid % LANES, group = tid / LANES;
   const int cluster = p.cluster, steps = p.steps;
@@ -331,10 +331,13 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   wait_for_predecessor();
   if (cluster > 1) cluster_sync();  // the other CTAs' barriers exist
 
-  float carried[V];
+  // the carried values, a lane's channels in every warp
+  constexpr int C = S::kWidth > 32 ? S::kWidth / 32 : 1;
+  const int ch = lane * C % S::kWidth;
+  float carried[C];
 #pragma unroll
-  for (int e = 0; e < V; ++e) carried[e] = e < channels && p.first ? p.first[cell + e] : 0.f;
-  if (group == 0) store_floats(all_carried + side * V, carried);  // read after the first round's barrier
+  for (int i = 0; i < C; ++i)
+    carried[i] = p.first && c0 + ch + i < p.width ? p.first[b * p.width + c0 + ch + i] : 0.f;
 
   auto tile_step = [&](int round) { return (round * cluster + rank) * S::kTime; };
   // element row of step s in an array (backward: h is read one step earlier)
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
     const char *mine = dynamic + stage * S::kStageBytes + side * 8 +
                        (BACK ? S::kTime - 1 - group * N : group * N) * S::kRowPitch;
     // without TMA: where this thread's first row of each array starts within its 16 bytes
-    uint32_t offset[3];
+    uint32_t offset[3] = {};
     if constexpr (!TMA) {
 #pragma unroll
       for (int array = 0; array < S::kArrays; ++array)
@@ -439,7 +442,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
       }
     };
     auto input = [&](int u, int array, float (&f)[V]) { widen(words(u, array), f); };
-    uint2 kept[TMA ? 1 : N];  // x, or dh: joining its words again would cost more than the registers
+    uint2 kept[TMA ? 1 : N] = {};  // x, or dh: joining its words again would cost more than the registers
 
     // 1. this thread's map: steps beyond the end read zeros, decay 1 and 0 added
     float a[N][V], A[V], B[V];
@@ -516,61 +519,117 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
       store_floats(warp_maps + (warp * 2 + 1) * S::kWidth + side * V, B);
     }
     __syncthreads();
-    request(round + S::kStages - 1);  // into the stage that the round before has read
+    if (cluster == 1) request(round + S::kStages - 1);  // into the stage that the round before has read
 
-    // 2. the maps of the cluster's CTAs
-    float v[V], start[V];  // the value at the start of the CTA's tile, and of this thread's steps
-    if (cluster > 1) {
-      float *cta_maps = all_cta_maps + (round & 1) * S::kCtaMaps;
-      const uint32_t bar = smem_u32(&sh.exchanged[round & 1]);
-      if (tid < S::kWidth) {
-        float A1 = 1.f, B1 = 0.f;
+    // 2. the value at the start of the warp's steps, of each lane's channels; the
+    // carried value moves on to the next round
+    const float *maps = warp_maps + ch;
+    float v[C], before[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) before[i] = carried[i];
+    if (cluster == 1) {
+      auto fold = [&](const bool robust) {
 #pragma unroll
         for (int w = 0; w < S::kWarps; ++w) {
-          const float A2 = warp_maps[(w * 2) * S::kWidth + tid], B2 = warp_maps[(w * 2 + 1) * S::kWidth + tid];
-          B1 = apply(A2, B2, B1);
-          A1 = chain(A1, A2);
-        }
-        if (*(volatile int *)&sh.failed) A1 = B1 = __int_as_float(0x7fc00000);  // what follows is not known
-        const uint32_t to = smem_u32(cta_maps + (rank * S::kWidth + tid) * 2);
-        for (int r = 0; r < (*(volatile int *)&sh.lost ? 0 : cluster); ++r)
-          st_cluster_counted(cluster_address(to, r), A1, B1, cluster_address(bar, r));
-      }
-      wait_for<true>(bar, (round >> 1) & 1, &sh.lost, kWaitPolls);
-      for (int r = 0; r < cluster; ++r) {
-        float Ar[V], Br[V];
-        load_maps(cta_maps + (r * S::kWidth + side * V) * 2, Ar, Br);
+          float A2[C], B2[C];
+          load_floats(maps + (w * 2) * S::kWidth, A2);
+          load_floats(maps + (w * 2 + 1) * S::kWidth, B2);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (r == rank) v[e] = carried[e];
-          carried[e] = apply(Ar[e], Br[e], carried[e]);
+          for (int i = 0; i < C; ++i) {
+            if (w == warp) v[i] = carried[i];
+            carried[i] = robust ? apply(A2[i], B2[i], carried[i]) : fmaf(A2[i], carried[i], B2[i]);
+          }
         }
+      };
+      fold(false);
+      if (!(not_finite(carried) == 0.f)) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) carried[i] = before[i];
+        fold(true);
       }
     } else {
-      load_floats(all_carried + (round & 1) * S::kWidth + side * V, v);
-    }
-    // 3. the maps of the CTA's warps before this one: plain first, as above
-    auto fold = [&](const bool robust) {
+      // the maps of the warps before this one (P, Q), and of the CTA, which this
+      // warp sends to the cluster's CTA of its own number
+      float A1[C], B1[C], P[C], Q[C], least[C];
 #pragma unroll
-      for (int w = 0; w < S::kWarps - 1; ++w) {
-        if (w >= warp) break;
-        float Aw[V], Bw[V];
-        load_floats(warp_maps + (w * 2) * S::kWidth + side * V, Aw);
-        load_floats(warp_maps + (w * 2 + 1) * S::kWidth + side * V, Bw);
-#pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = robust ? apply(Aw[e], Bw[e], v[e]) : fmaf(Aw[e], v[e], Bw[e]);
+      for (int i = 0; i < C; ++i) {
+        A1[i] = P[i] = least[i] = 1.f;
+        B1[i] = Q[i] = 0.f;
       }
-    };
 #pragma unroll
-    for (int e = 0; e < V; ++e) start[e] = v[e];
-    fold(false);
-    if (!(not_finite(v) == 0.f)) {
+      for (int w = 0; w < S::kWarps; ++w) {
+        float A2[C], B2[C];
+        load_floats(maps + (w * 2) * S::kWidth, A2);
+        load_floats(maps + (w * 2 + 1) * S::kWidth, B2);
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = start[e];
-      fold(true);
+        for (int i = 0; i < C; ++i) {
+          if (w == warp) {
+            P[i] = kept_above_zero(A1[i], least[i]);
+            Q[i] = B1[i];
+          }
+          least[i] = fminf(least[i], A2[i]);
+          A1[i] *= A2[i];
+          B1[i] = fmaf(A2[i], B1[i], B2[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) A1[i] = kept_above_zero(A1[i], least[i]);
+      if (!(not_finite(B1) == 0.f)) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          B1[i] = 0.f;
+#pragma unroll 1
+          for (int w = 0; w < S::kWarps; ++w) {
+            if (w == warp) Q[i] = B1[i];
+            B1[i] = apply(maps[(w * 2) * S::kWidth + i], maps[(w * 2 + 1) * S::kWidth + i], B1[i]);
+          }
+        }
+      }
+      if (*(volatile int *)&sh.failed) {  // what follows is not known
+#pragma unroll
+        for (int i = 0; i < C; ++i) A1[i] = B1[i] = __int_as_float(0x7fc00000);
+      }
+      float *cta_maps = all_cta_maps + (round & 1) * S::kCtaMaps;
+      const uint32_t bar = smem_u32(&sh.exchanged[round & 1]);
+      if (warp < cluster && lane < S::kWidth && !*(volatile int *)&sh.lost) {
+        const uint32_t to = cluster_address(smem_u32(cta_maps + (rank * S::kWidth + ch) * 2), warp);
+        const uint32_t count = cluster_address(bar, warp);
+#pragma unroll
+        for (int i = 0; i < C; ++i) st_cluster_counted(to + 8 * i, A1[i], B1[i], count);
+      }
+      request(round + S::kStages - 1);
+      wait_for<true>(bar, (round >> 1) & 1, &sh.lost, kWaitPolls);
+      auto pass = [&](const bool robust) {
+#pragma unroll 2
+        for (int r = 0; r < cluster; ++r) {
+          float m[2 * C];
+          load_floats(cta_maps + (r * S::kWidth + ch) * 2, m);
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            if (r == rank) v[i] = carried[i];
+            carried[i] = robust ? apply(m[2 * i], m[2 * i + 1], carried[i]) : fmaf(m[2 * i], carried[i], m[2 * i + 1]);
+          }
+        }
+      };
+      pass(false);
+      if (!(not_finite(carried) == 0.f)) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) carried[i] = before[i];
+        pass(true);
+      }
+#pragma unroll
+      for (int i = 0; i < C; ++i) v[i] = apply(P[i], Q[i], v[i]);
     }
+    // 3. the value at the start of this thread's steps
+    float start[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = start[e] = lane >= LANES ? apply(A0[e], B0[e], v[e]) : v[e];
+    for (int e = 0; e < V; ++e) {
+      const float w = __shfl_sync(0xffffffffu, v[e % C], (side * V + e) / C);
+      start[e] = lane >= LANES ? apply(A0[e], B0[e], w) : w;
+    }
+    float now[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) now[e] = start[e];
     // this thread's steps again
     raw *out0 = at<raw>(BACK ? p.dx : p.h, b, row_of(s0, 0), c), *out1 = at<raw>(p.dg, b, row_of(s0, 0), c);
     const int64_t out_pitch0 = BACK ? -p.dx.step : p.h.step, out_pitch1 = -p.dg.step;
@@ -614,9 +673,9 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
 #pragma unroll 1
       for (int u = 0; u < N; ++u) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = __int_as_float(0x7fc00000);
-        write(out0 + u * out_pitch0, v, channels > 0 && s0 + u < steps);
-        if (BACK) write(out1 + u * out_pitch1, v, channels > 0 && s0 + u < steps);
+        for (int e = 0; e < V; ++e) now[e] = __int_as_float(0x7fc00000);
+        write(out0 + u * out_pitch0, now, channels > 0 && s0 + u < steps);
+        if (BACK) write(out1 + u * out_pitch1, now, channels > 0 && s0 + u < steps);
       }
       continue;
     }
@@ -634,14 +693,14 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
         }
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
-          add2(dx[e], dx[e + 1], v[e], v[e + 1], xf[e], xf[e + 1]);
+          add2(dx[e], dx[e + 1], now[e], now[e + 1], xf[e], xf[e + 1]);
           if (robust) {
-            v[e] = decayed(d[e], dx[e]);
-            v[e + 1] = decayed(d[e + 1], dx[e + 1]);
+            now[e] = decayed(d[e], dx[e]);
+            now[e + 1] = decayed(d[e + 1], dx[e + 1]);
           } else {
-            mul2(v[e], v[e + 1], d[e], d[e + 1], dx[e], dx[e + 1]);
+            mul2(now[e], now[e + 1], d[e], d[e + 1], dx[e], dx[e + 1]);
           }
-          mul2(dg[e], dg[e + 1], v[e], v[e + 1], hf[e], hf[e + 1]);
+          mul2(dg[e], dg[e + 1], now[e], now[e + 1], hf[e], hf[e + 1]);
           dg[e] = d[e] == 0.f ? 0.f : dg[e];
           dg[e + 1] = d[e + 1] == 0.f ? 0.f : dg[e + 1];
         }
@@ -651,20 +710,20 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
           if (robust) {
-            v[e] = advance<false>(d[e], v[e], xf[e]);
-            v[e + 1] = advance<false>(d[e + 1], v[e + 1], xf[e + 1]);
+            now[e] = advance<false>(d[e], now[e], xf[e]);
+            now[e + 1] = advance<false>(d[e + 1], now[e + 1], xf[e + 1]);
           } else {
-            fma2(v[e], v[e + 1], d[e], d[e + 1], v[e], v[e + 1], xf[e], xf[e + 1]);
+            fma2(now[e], now[e + 1], d[e], d[e + 1], now[e], now[e + 1], xf[e], xf[e + 1]);
           }
         }
-        write(out0 + u * out_pitch0, v, in);
+        write(out0 + u * out_pitch0, now, in);
       }
     };
 #pragma unroll
     for (int u = 0; u < N; ++u) step(u, a[u], false);
-    if (__any_sync(0xffffffffu, !(not_finite(v) == 0.f))) {
+    if (__any_sync(0xffffffffu, !(not_finite(now) == 0.f))) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = start[e];
+      for (int e = 0; e < V; ++e) now[e] = start[e];
 #pragma unroll 1
       for (int u = 0; u < N; ++u) {
         float d[V];
@@ -674,21 +733,14 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
         step(u, d, true);
       }
     }
-    // the last group's value is the next round's, read after that round's barrier
-    if (cluster == 1 && group == S::kGroups - 1) store_floats(all_carried + ((round + 1) & 1) * S::kWidth + side * V, v);
-    if (cluster == 1) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) carried[e] = v[e];
-    }
   }
   if (cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
   __syncthreads();
   const bool gave_up = sh.failed || sh.lost;
-  // the sequence's last value: every thread's of a cluster's CTA, the last group's of a CTA alone
-  if (p.last && rank == 0 && group == (cluster > 1 ? 0 : S::kGroups - 1)) {
+  if (p.last && rank == 0 && warp == 0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < channels) p.last[cell + e] = gave_up ? __int_as_float(0x7fc00000) : carried[e];
+    for (int i = 0; i < C; ++i)
+      if (c0 + ch + i < p.width) p.last[b * p.width + c0 + ch + i] = gave_up ? __int_as_float(0x7fc00000) : carried[i];
   }
   if (gave_up) {  // copies in flight land before the CTA leaves
     if (tid == 0) atomicAdd(p.timeouts, 1u);
