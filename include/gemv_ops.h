@@ -18,9 +18,9 @@
  * device (anything else returns GEMV_ERR_DEVICE), asynchronous on `stream`,
  * GEMV_* status codes, nothing launched on failure, nothing thrown.  The calls
  * allocate nothing and keep nothing, so any number may run at once on any
- * streams, and all can be captured in a CUDA graph.  Each launches one kernel,
- * gemm_fused() two for unaligned operands (a programmatic dependent launch that reads and writes nothing before the
- * preceding kernel has completed).  Results are bitwise reproducible: every sum
+ * streams, and all can be captured in a CUDA graph.  Each launches one kernel
+ * (gemm_fused() two for unaligned operands) as a programmatic dependent launch,
+ * which reads and writes nothing before the preceding kernel has completed.  Results are bitwise reproducible: every sum
  * runs in an order fixed by the sizes, strides and alignment.
  *
  * Kernels that wait on their own copies or on another CTA of their cluster do so
@@ -120,13 +120,13 @@ typedef struct gemm_epilogue {
  * 0 <= m, n, k <= INT32_MAX, and rows of C and of the residual (m > 1) start less
  * than 4 GiB apart; m == 0 or n == 0 launches nothing, k == 0 gives the
  * epilogue of 0.  Elements between k and a row stride are never used.  Any
- * element alignment and stride work.  An operand whose base or row stride is
- * not a multiple of 16 bytes is copied on the device first, to `workspace`:
- * gemm_workspace() bytes of the caller's (16-byte aligned, overlapping
- * nothing, free again after the call's work on the stream; a shorter one returns
- * GEMV_ERR_SCRATCH), and the call launches a second kernel.  Weights kept with
- * 16-byte rows need none.  Products and sums run on the tensor cores with fp32
- * accumulation. 
+ * element alignment and stride work.  If the base or row stride of an operand is
+ * not a multiple of 16 bytes, a second kernel copies the operand to `workspace`
+ * first (or, for few vectors, A only, once per way in which B's rows start
+ * within 16 bytes): gemm_workspace() bytes of the caller's (16-byte aligned,
+ * overlapping nothing, free again after the call's work on the stream; a
+ * shorter one returns GEMV_ERR_SCRATCH).  Weights kept with 16-byte rows need
+ * none.  Products and sums run on the tensor cores with fp32 accumulation.
  */
 int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda, void *C, int64_t ldc, int64_t m,
                int64_t n, int64_t k, int dtype, int out_dtype, const gemm_epilogue *epilogue,
@@ -134,8 +134,8 @@ int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda, void *C, 
 
 /*
  * The workspace that gemm_fused() needs for these operands, in *bytes: 0 where
- * bases and row strides are multiples of 16 bytes, otherwise the size of what
- * has to be copied.  A pure host function.
+ * bases and row strides are multiples of 16 bytes, otherwise the size of the
+ * copies.  A pure host function.
  */
 int gemm_workspace(const void *B, int64_t ldb, const void *A, int64_t lda, int64_t m, int64_t n, int64_t k,
                    int dtype, int64_t *bytes);

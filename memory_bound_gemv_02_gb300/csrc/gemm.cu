@@ -11,12 +11,14 @@
 // Operand tiles are 128 bytes of k wide (64 16-bit or 128 8-bit elements) in
 // the 128-byte swizzle, in a ring of stages.  Warp 0 fills the ring by TMA, one
 // thread of warp 1 issues the matrix instructions, eight warps write the result.
-// An operand whose base or row stride is not a multiple of 16 bytes is first
-// copied to the workspace with rows that are (gemm_align_kernel).  Shifting its
-// rows into place within the product was slower at every size, even for a
-// single vector (77 x 4099 x 7169 fp16: 72 us with cp.async of the covering
-// blocks, 220 with a bulk copy per row): each CTA's 128-byte pieces of 128 rows
-// are the wrong shape for anything but a tensor map.
+// An operand whose base or row stride is not a multiple of 16 bytes is no tensor
+// map's.  Many vectors: it is first copied to the workspace with rows that are
+// (gemm_align_kernel).  Few: B is read in place by one tensor map for each of
+// its classes of rows that start alike (ShiftedParams).  Shifting rows into place
+// within the product was slower than either at every size (77 x 4099 x 7169 fp16:
+// 72 us with cp.async of the covering blocks, 220 with a bulk copy per row, 37
+// copied first, 26 by classes): 128-byte pieces of 128 rows are the wrong shape
+// for anything but a tensor map.
 //
 // Two kernels:
 //  * gemm_split_kernel, one tile per CTA: clusters of up to 8 CTAs share a tile
@@ -67,6 +69,25 @@ struct GemmParams {
   uint32_t idesc;             // without the column count
   int32_t polls;              // of the waits for operands
   uint32_t *timeouts;
+};
+
+// Rows of B that start off 16 bytes, read in place: the rows j, j + classes, ..
+// start at one offset within their 16 bytes, and one tensor map, based on the
+// 16-byte boundary before row j, reads them.  A tile takes rows of one class,
+// and the vectors come with as many zeros in front (a copy for each class).
+constexpr int kMaxClasses = 16;
+struct ShiftedParams : GemmParams {
+  CUtensorMap map_class[kMaxClasses];
+  int32_t classes;
+  uint32_t base, pitch;       // of B's rows, in bytes modulo 16
+};
+template <bool SHIFTED>
+struct SplitParams {
+  typedef GemmParams type;
+};
+template <>
+struct SplitParams<true> {
+  typedef ShiftedParams type;
 };
 
 // ------------------------------------------------------------------ epilogue --
@@ -276,11 +297,14 @@ __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int ban
 // -------------------------------------------------------- rows off 16 bytes --
 
 // One operand to copy: `rows` rows of `bytes` bytes, `ld` apart, to rows of
-// `pitch` (a multiple of 16) in the workspace; `pieces` of 2 KB per row.
+// `pitch` (a multiple of 16) in the workspace; `pieces` of 2 KB per row.  For
+// each of the classes of ShiftedParams once, behind as many zeros as the class
+// has bytes before its rows; zeros follow the row up to the pitch.
 struct AlignJob {
   const char *src;
   char *dst;
-  int64_t ld, bytes, pitch, pieces, total;  // total: rows x pieces
+  int64_t ld, bytes, pitch, pieces, rows, total;  // total: classes x rows x pieces
+  uint32_t class_base, class_pitch;               // modulo 16
 };
 struct AlignParams {
   AlignJob job[2];
@@ -297,17 +321,20 @@ __global__ void __launch_bounds__(kAlignThreads) gemm_align_kernel(AlignParams p
   for (int64_t i = (int64_t)blockIdx.x * (kAlignThreads / 32) + (threadIdx.x >> 5); i < p.job[0].total + p.job[1].total;
        i += warps) {
     const AlignJob &j = i < p.job[0].total ? p.job[0] : p.job[1];
-    const int64_t n = i < p.job[0].total ? i : i - p.job[0].total, row = n / j.pieces, piece = n - row * j.pieces;
+    const int64_t n = i < p.job[0].total ? i : i - p.job[0].total, line = n / j.pieces, piece = n - line * j.pieces;
+    const int64_t number = line / j.rows, row = line - number * j.rows;
+    const int lead = (int)((j.class_base + (uint32_t)number * j.class_pitch) & 15);
+    // byte d of the copy is byte d - lead of the row
     const uintptr_t start = (uintptr_t)(j.src + row * j.ld), end = start + (uintptr_t)j.bytes;
-    const int off = (int)(start & 15);
-    const uintptr_t block = start - off + (uintptr_t)(piece * 2048 + lane * 16);
-    char *to = j.dst + row * j.pitch + piece * 2048 + lane * 16;
+    const int off = (int)((start - lead) & 15);
+    const uintptr_t block = start - lead - off + (uintptr_t)(piece * 2048 + lane * 16);
+    char *to = j.dst + line * j.pitch + piece * 2048 + lane * 16;
     uint4 lo[4], hi[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uintptr_t at = block + (uintptr_t)(u * 512);
-      lo[u] = at < end ? ldg_stream(reinterpret_cast<const uint4 *>(at)) : zero4();
-      hi[u] = lane == 31 && at + 16 < end ? ldg_stream(reinterpret_cast<const uint4 *>(at + 16)) : zero4();
+      lo[u] = at < end && at + 16 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at)) : zero4();
+      hi[u] = lane == 31 && at + 16 < end && at + 32 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at + 16)) : zero4();
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -317,8 +344,16 @@ __global__ void __launch_bounds__(kAlignThreads) gemm_align_kernel(AlignParams p
       up.z = __shfl_down_sync(0xffffffffu, lo[u].z, 1);
       up.w = __shfl_down_sync(0xffffffffu, lo[u].w, 1);
       if (lane == 31) up = hi[u];
-      if (piece * 2048 + u * 512 + lane * 16 < j.pitch)
-        *reinterpret_cast<uint4 *>(to + u * 512) = shifted(lo[u], up, off);
+      uint4 v = shifted(lo[u], up, off);
+      const int64_t d = piece * 2048 + u * 512 + lane * 16;
+      if (d < lead || d + 16 > lead + j.bytes) {  // the row's ends: zeros outside
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+          if (d + b < lead || d + b >= lead + j.bytes) w[b / 4] &= ~(0xffu << (b % 4 * 8));
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (d < j.pitch) *reinterpret_cast<uint4 *>(to + u * 512) = v;
     }
   }
 }
@@ -332,8 +367,24 @@ struct alignas(16) SplitShared {
   int issued;  // steps whose copies were started
 };
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_constant__ GemmParams p) {
+// Zeros in the first `bytes` (below 16) of 16 bytes of shared memory.
+__device__ __forceinline__ void clear_front(uint32_t at, int bytes) {
+  uint32_t w[4];
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int clear = bytes - 4 * i;
+    w[i] = clear >= 4 ? 0u : clear <= 0 ? w[i] : w[i] & ~((1u << (8 * clear)) - 1);
+  }
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+               : "memory");
+}
+
+// SHIFTED: B's rows start off 16 bytes and are read in place.
+template <bool E4M3, bool SHIFTED>
+__global__ void __launch_bounds__(kSplitThreads)
+    gemm_split_kernel(const __grid_constant__ typename SplitParams<SHIFTED>::type p) {
   extern __shared__ char dynamic[];
   __shared__ SplitShared sh;
   const uint32_t tiles = (smem_u32(dynamic) + 1023u) & ~1023u;  // swizzled tiles start on 1024 bytes
@@ -342,9 +393,21 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   const int split = p.splits > 1 ? (int)cluster_rank() : 0;
   int tile_n, tile_m;
   tile_at(blockIdx.x / p.splits, p.tiles_n, p.tiles_m, kSplitBand, &tile_n, &tile_m);
-  const int64_t j0 = (int64_t)tile_n * kTileRows, i0 = (int64_t)tile_m * p.cols;
+  int64_t j0 = (int64_t)tile_n * kTileRows;
+  const int64_t i0 = (int64_t)tile_m * p.cols;
+  int64_t row0 = i0;                          // of the vectors
+  int number = 0, classes = 1, lead = 0;      // class of the tile's rows, bytes before them
+  if constexpr (SHIFTED) {
+    classes = p.classes;
+    number = tile_n % classes;
+    j0 = (int64_t)(tile_n / classes) * kTileRows;
+    row0 += (int64_t)number * p.m;
+    lead = (int)((p.base + (uint32_t)number * p.pitch) & 15);
+  }
   // this CTA's share of k, whole steps, as even as they come
   const int begin = (int)((int64_t)p.steps * split / p.splits), end = (int)((int64_t)p.steps * (split + 1) / p.splits);
+  const CUtensorMap *map_b = &p.map_b;
+  if constexpr (SHIFTED) map_b = &p.map_class[number];
   const uint32_t columns = p.cols <= 32 ? 32 : p.cols <= 64 ? 64 : p.cols <= 128 ? 128 : 256;
 
   if (threadIdx.x == 0) {
@@ -356,7 +419,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     mbar_init(smem_u32(&sh.done), 1);
     mbar_init_fence();
     if (p.steps > 0) {
-      prefetch_map(&p.map_b);
+      prefetch_map(map_b);
       prefetch_map(&p.map_a);
     }
   }
@@ -380,8 +443,8 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
         const uint32_t bar = smem_u32(&sh.full[r.stage]), at = tiles + r.stage * stage_bytes;
         mbar_expect_tx(bar, stage_bytes);
         const int32_t x = step * (E4M3 ? kRowBytes : kRowBytes / 2);
-        tma_load<1>(at, &p.map_b, x, (int32_t)j0, bar);
-        tma_load<1>(at + kTileBytes, &p.map_a, x, (int32_t)i0, bar);
+        tma_load<1>(at, map_b, x, (int32_t)j0, bar);
+        tma_load<1>(at + kTileBytes, &p.map_a, x, (int32_t)row0, bar);
       }
       r.next(p.stages);
     }
@@ -397,6 +460,13 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
       ready = peek(sh.full, r, p.stages, p.polls);
       const uint32_t at = tiles + r.stage * stage_bytes;
       const uint64_t db = tile_descriptor(at), da = tile_descriptor(at + kTileBytes);
+      if (SHIFTED && step == 0 && lead > 0) {
+        // what precedes the rows is not B's (and 0 x infinity would be NaN)
+        for (int row = lane; row < kTileRows; row += 32)
+          clear_front(at + row * kRowBytes + ((row & 7) << 4), lead);  // the swizzle's place of a row's first 16 bytes
+        fence_async_smem();
+        __syncwarp();
+      }
       if (elected) {
 #pragma unroll
         for (int s = 0; s < kMmaSteps; ++s) tc_mma<1, E4M3>(tmem, db + 2 * s, da + 2 * s, idesc, step > begin || s > 0);
@@ -436,7 +506,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
   const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
   if (p.splits == 1) {
     with_column(p, [&](auto col) {
-      col.begin(p, j0 + l);
+      col.begin(p, number + classes * (j0 + l));
 #pragma unroll 1
       for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 16 * kTurns) {
         float v[16];
@@ -468,7 +538,7 @@ __global__ void __launch_bounds__(kSplitThreads) gemm_split_kernel(const __grid_
     cluster_sync();
     const float *parts = reinterpret_cast<const float *>(dynamic + (tiles - smem_u32(dynamic))) + l;
     with_column(p, [&](auto col) {
-      col.begin(p, j0 + l);
+      col.begin(p, number + classes * (j0 + l));
       constexpr int kAtOnce = 4;
 #pragma unroll 1
       for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += kTurns * kAtOnce) {
@@ -721,7 +791,7 @@ struct GemmPlan {
 // of them (bf16, measured): 512 x 4096 x 4096 pairs of 128 columns 18.6, of 256
 // 23.0; 256 x 14336 x 4096 pairs 27.5, one tile per CTA 33.7; 256 x 1024 x 1024
 // 64 columns 6.8, 256 columns 12.0.
-GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, int sms) {
+GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, int sms, bool split_only) {
   GemmPlan best = {};
   best.us = 1e30;
   const double stream = (double)operand_bytes / 6.2e6;
@@ -759,7 +829,7 @@ GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, i
       }
     }
   }
-  if (steps == 0) return best;
+  if (steps == 0 || split_only) return best;
   for (int64_t t = fewest; t < fewest + 4; ++t) {
     GemmPlan p = {};
     p.pair = true;
@@ -787,10 +857,59 @@ namespace {
 
 int64_t aligned_pitch(int64_t k_bytes) { return (k_bytes + 15) / 16 * 16; }
 
+// B off 16 bytes, read in place (ShiftedParams): the row classes, and the copies
+// of A that they take.
+struct Shifted {
+  int classes;      // 0: B is aligned, or is copied
+  int lead;         // the most bytes before a class's rows
+  int64_t pitch;    // of A's copies
+};
+
+// In place where reading B twice and writing it once costs more than the copies
+// of A, the rows of C written 16 bytes apart and each class's last tile.  Measured
+// with cold weights, in place / copied (us): fp16 n x k = 4099 x 7169, m = 1 18 / 33,
+// 77 26 / 39, 256 54 / 69, 512 80 / 60; 18433 x 4095, m = 1 31 / 72, 128 46 / 83,
+// 256 69 / 84, 512 127 / 106; 1001 x 999, m = 1 7.8 / 7.9, 128 10.8 / 9.9.  8 bits (twice the
+// classes, half the copy): 4099 x 7169, m = 1 15 / 20, 77 20 / 23, 128 31 / 27;
+// 18433 x 4095, m = 16 22 / 35, 128 43 / 42, 256 88 / 43.
+Shifted shifted_rows(const void *B, int64_t n, int64_t ldb_bytes, int64_t m, int64_t k, int es) {
+  const int64_t k_bytes = k * es;
+  Shifted s = {};
+  if (n == 0 || k_bytes == 0 || tma_ok(B, n, ldb_bytes)) return s;
+  int classes = 1;
+  while (n > 1 && ldb_bytes * classes % 16 != 0) classes *= 2;
+  if (n * k_bytes < (1 << 20) || classes * m > n || classes * m > 1024 * es) return s;
+  if (ldb_bytes * classes >= (1ll << 40) || m * classes > INT32_MAX) return s;
+  s.classes = classes;
+  for (int j = 0; j < classes; ++j) {
+    const int lead = (int)(((uintptr_t)B + (uintptr_t)(j * ldb_bytes)) & 15);
+    if (lead > s.lead) s.lead = lead;
+  }
+  s.pitch = aligned_pitch(s.lead + k_bytes);
+  return s;
+}
+
 // Workspace for one operand: 0 where TMA reads it in place.
 int64_t operand_space(const void *p, int64_t rows, int64_t k_bytes, int64_t ld_bytes) {
   if (rows == 0 || k_bytes == 0 || tma_ok(p, rows, ld_bytes)) return 0;
   return (rows * aligned_pitch(k_bytes) + 255) / 256 * 256;
+}
+
+template <class P>
+int launch_gemm(void (*fn)(P), const P &p, int64_t grid, const GemmPlan &plan, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlone);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
+  }
+  return launch_op(fn, dim3((unsigned)grid), plan.pair ? kPairThreads : kSplitThreads, (size_t)plan.smem,
+                   plan.pair ? 2 : plan.splits, stream, p);
+}
+
+int64_t workspace_of(const Shifted &s, const void *B, int64_t ldb_bytes, const void *A, int64_t lda_bytes, int64_t m,
+                     int64_t n, int64_t k_bytes) {
+  if (s.classes) return (s.classes * m * s.pitch + 255) / 256 * 256;
+  return operand_space(B, n, k_bytes, ldb_bytes) + operand_space(A, m, k_bytes, lda_bytes);
 }
 
 int check_sizes(int64_t ldb, int64_t lda, int64_t m, int64_t n, int64_t k, int dtype) {
@@ -808,7 +927,8 @@ extern "C" int gemm_workspace(const void *B, int64_t ldb, const void *A, int64_t
   if (st != GEMV_OK) return st;
   if (bytes == nullptr) return GEMV_ERR_ARG;
   const int es = type_bytes(dtype);
-  *bytes = m == 0 || n == 0 ? 0 : operand_space(B, n, k * es, ldb * es) + operand_space(A, m, k * es, lda * es);
+  *bytes = m == 0 || n == 0 ? 0
+                            : workspace_of(shifted_rows(B, n, ldb * es, m, k, es), B, ldb * es, A, lda * es, m, n, k * es);
   return GEMV_OK;
 }
 
@@ -834,8 +954,8 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   if (((uintptr_t)C | (uintptr_t)ep.residual) % (uintptr_t)oe || (uintptr_t)ep.bias % (uintptr_t)be ||
       ((uintptr_t)ep.scale_a | (uintptr_t)ep.scale_b) % 4u)
     return GEMV_ERR_ALIGN;
-  const int64_t space_b = operand_space(B, n, k * es, ldb * es), space_a = operand_space(A, m, k * es, lda * es);
-  const int64_t space = space_b + space_a;
+  const Shifted shift = shifted_rows(B, n, ldb * es, m, k, es);
+  const int64_t space = workspace_of(shift, B, ldb * es, A, lda * es, m, n, k * es);
   if (space > 0) {
     if (workspace == nullptr || workspace_bytes < space) return GEMV_ERR_SCRATCH;
     if ((uintptr_t)workspace % 16u) return GEMV_ERR_ALIGN;
@@ -857,63 +977,80 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
     return GEMV_ERR_DEVICE;
   if (m == 1) ldc = ep.ldr = n;
   if ((ldc > ep.ldr ? ldc : ep.ldr) * oe > (int64_t)UINT32_MAX) return GEMV_ERR_ARG;
-  GemmParams p = {};
+  ShiftedParams p = {};
   p.C = C;
   p.ldc = ldc; p.ldr = ep.ldr;
   p.m = (int32_t)m; p.n = (int32_t)n;
-  p.steps = (int32_t)cdiv64(k * es, kRowBytes);
+  p.steps = (int32_t)cdiv64(shift.lead + k * es, kRowBytes);
   p.alpha = ep.alpha; p.beta = ep.beta;
   p.scale_a = ep.scale_a; p.scale_b = ep.scale_b; p.bias = ep.bias; p.residual = ep.residual;
   p.bias_f32 = ep.bias_dtype == GEMV_TYPE_F32 ? 1 : 0;
   p.act = ep.activation; p.out_type = out_dtype;
-  p.pairs = oe == 2 && ((uintptr_t)C | (uintptr_t)(ldc * oe)) % 4 == 0 ? 1 : 0;
+  p.pairs = oe == 2 && shift.classes <= 1 && ((uintptr_t)C | (uintptr_t)(ldc * oe)) % 4 == 0 ? 1 : 0;
   // fp32 accumulators (bit 4); operand types in bits 7 and 10: 0 fp16 or e4m3, 1 bf16
   p.idesc = (1u << 4) | (dtype == GEMV_TYPE_BF16 ? (1u << 7) | (1u << 10) : 0u);
   p.polls = take_wait_budget(kPolls);
   st = wait_counter(dev, &p.timeouts);
   if (st != GEMV_OK) return st;
   const bool e4m3 = dtype == GEMV_TYPE_E4M3;
-  const GemmPlan plan = gemm_plan(m, n, p.steps, (m + n) * k * es, sms);
+  // rows of B as tiles hold them: each class ends in a tile of its own
+  const int64_t tiled = shift.classes ? shift.classes * cdiv64(cdiv64(n, shift.classes), kTileRows) * kTileRows : n;
+  const GemmPlan plan = gemm_plan(m, tiled, p.steps, (m + n) * k * es, sms, shift.classes != 0);
   const bool pair = plan.pair;
   p.cols = plan.cols; p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
   p.splits = plan.splits; p.stages = plan.stages;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
   if (tiles * p.splits > INT32_MAX / 2) return GEMV_ERR_ARG;
+  p.classes = shift.classes;
+  p.base = (uint32_t)(uintptr_t)B & 15;
+  p.pitch = (uint32_t)(ldb * es) & 15;
   // operands that TMA cannot read in place, copied with rows that it can
   int64_t ldb_bytes = ldb * es, lda_bytes = lda * es;
   if (space > 0) {
     AlignParams ap = {};
-    const int64_t pitch = aligned_pitch(k * es), pieces = cdiv64(pitch, 2048);
     char *to = static_cast<char *>(workspace);
     int jobs = 0;
-    if (space_b > 0) {
-      ap.job[jobs++] = {static_cast<const char *>(B), to, ldb_bytes, k * es, pitch, pieces, n * pieces};
-      B = to;
-      ldb_bytes = pitch;
-      to += space_b;
-    }
-    if (space_a > 0) {
-      ap.job[jobs++] = {static_cast<const char *>(A), to, lda_bytes, k * es, pitch, pieces, m * pieces};
-      A = to;
-      lda_bytes = pitch;
+    auto copy = [&](const void **from, int64_t rows, int64_t *ld, int64_t pitch, int copies) {
+      AlignJob &job = ap.job[jobs++];
+      job = {static_cast<const char *>(*from), to, *ld, k * es, pitch, cdiv64(pitch, 2048), rows, 0, 0, 0};
+      job.total = copies * rows * job.pieces;
+      *from = to;
+      *ld = pitch;
+      to += (copies * rows * pitch + 255) / 256 * 256;
+    };
+    if (shift.classes) {
+      copy(&A, m, &lda_bytes, shift.pitch, shift.classes);
+      ap.job[0].class_base = p.base;
+      ap.job[0].class_pitch = p.pitch;
+    } else {
+      if (operand_space(B, n, k * es, ldb_bytes)) copy(&B, n, &ldb_bytes, aligned_pitch(k * es), 1);
+      if (operand_space(A, m, k * es, lda_bytes)) copy(&A, m, &lda_bytes, aligned_pitch(k * es), 1);
     }
     const int64_t blocks = cdiv64(ap.job[0].total + ap.job[1].total, kAlignThreads / 32);
     st = launch_op(gemm_align_kernel, dim3((unsigned)(blocks < 64ll * sms ? blocks : 64ll * sms)), kAlignThreads, 0, 1,
                    stream, ap);
     if (st != GEMV_OK) return st;
   }
-  if (k > 0 && (!encode(&p.map_b, B, dtype, n, k, ldb_bytes, kTileRows) ||
-                !encode(&p.map_a, A, dtype, m, k, lda_bytes, pair ? p.cols / 2 : p.cols)))
-    return cuda_failure((int)cudaErrorNotSupported);
-  void (*fn)(GemmParams) = pair ? (e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>)
-                                : (e4m3 ? gemm_split_kernel<true> : gemm_split_kernel<false>);
+  bool mapped = true;
+  if (shift.classes) {
+    for (int j = 0; j < shift.classes; ++j) {
+      const char *row = static_cast<const char *>(B) + j * ldb_bytes;
+      const int lead = (int)((uintptr_t)row & 15);
+      mapped = mapped && encode(&p.map_class[j], row - lead, dtype, cdiv64(n - j, shift.classes), k + lead / es,
+                                ldb_bytes * shift.classes, kTileRows);
+    }
+    mapped = mapped && encode(&p.map_a, A, dtype, m * shift.classes, shift.pitch / es, lda_bytes, p.cols);
+  } else if (k > 0) {
+    mapped = encode(&p.map_b, B, dtype, n, k, ldb_bytes, kTileRows) &&
+             encode(&p.map_a, A, dtype, m, k, lda_bytes, pair ? p.cols / 2 : p.cols);
+  }
+  if (!mapped) return cuda_failure((int)cudaErrorNotSupported);
   int64_t grid = tiles * p.splits;
   if (pair) grid = 2 * (tiles < sms / 2 ? tiles : sms / 2);
-  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlone);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_failure((int)e);
-  }
-  return launch_op(fn, dim3((unsigned)grid), pair ? kPairThreads : kSplitThreads, (size_t)plan.smem,
-                   pair ? 2 : p.splits, stream, p);
+  if (shift.classes)
+    return launch_gemm(e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>, p, grid, plan, stream);
+  if (pair)
+    return launch_gemm<GemmParams>(e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>, p, grid, plan, stream);
+  return launch_gemm<GemmParams>(e4m3 ? gemm_split_kernel<true, false> : gemm_split_kernel<false, false>, p, grid, plan,
+                                 stream);
 }

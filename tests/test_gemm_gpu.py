@@ -78,6 +78,40 @@ def test_strides_and_offsets(cuda_dev, dtype, m, n, k, pad_a, pad_b, off):
         assert (buf[outside] == 7).all()
 
 
+# few vectors and enough weights that rows off 16 bytes are read in place, by
+# every number of row classes and with bytes of other rows or of none before them
+IN_PLACE = [(1, 1100, 1001, 0, 0), (17, 1301, 999, 0, 3), (30, 1200, 1004, 0, 0), (2, 1050, 1008, 0, 5),
+            (33, 2200, 520, 1, 0), (1, 4500, 261, 0, 0), (60, 4100, 1900, 4, 1)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k,pad_b,off", IN_PLACE)
+def test_rows_read_in_place(cuda_dev, dtype, m, n, k, pad_b, off):
+    A, B = _operands(m, n, k, dtype, cuda_dev, 61, 0, pad_b, off)
+    bias = ref.uniform((n,), torch.float32, 63, cuda_dev)
+    _check(g.gemm_fused(B, A, bias=bias, activation="relu"), B, A, "in place", bias=bias, activation="relu")
+    gen = torch.Generator(device=cuda_dev)
+    gen.manual_seed(n)
+    A.copy_(torch.randint(-3, 4, (m, k), generator=gen, device=cuda_dev).float())
+    B.copy_(torch.randint(-3, 4, (n, k), generator=gen, device=cuda_dev).float())
+    assert torch.equal(g.gemm_fused(B, A, out_dtype=torch.float32).double(), A.double() @ B.double().t())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k,pad_b,off", IN_PLACE)
+def test_rows_read_in_place_keep_to_themselves(cuda_dev, dtype, m, n, k, pad_b, off):
+    """NaN (and infinities, where the type has them) in one row do not reach its neighbours."""
+    A, B = _operands(m, n, k, dtype, cuda_dev, 67, 0, pad_b, off)
+    hit = [0, n // 2, n - 1]
+    clean = g.gemm_fused(B, A)
+    B[hit] = torch.tensor([[float("nan")], [float("nan" if dtype == E4M3 else "inf")], [float("nan")]],
+                          device=cuda_dev).to(dtype).expand(3, k)
+    c = g.gemm_fused(B, A)
+    others = torch.ones(n, dtype=torch.bool, device=cuda_dev)
+    others[hit] = False
+    assert torch.equal(c[:, others], clean[:, others]) and not torch.isfinite(c[:, hit]).any()
+
+
 @pytest.mark.parametrize("dtype,out_dtype", [(torch.float16, torch.float16), (torch.bfloat16, torch.bfloat16),
                                              (torch.bfloat16, torch.float32), (E4M3, torch.float16),
                                              (E4M3, torch.bfloat16), (E4M3, torch.float32)])
@@ -234,7 +268,7 @@ def test_refusals(cuda_dev):
     g.gemm_fused(B, A, wide[:, :16], residual=wide[:, 16:32])  # column ranges of one matrix do not overlap
 
 
-@pytest.mark.parametrize("m,n,k,pad", [(3, 200, 4096, 0), (3, 200, 4095, 1), (150, 900, 640, 0)])
+@pytest.mark.parametrize("m,n,k,pad", [(3, 200, 4096, 0), (3, 200, 4095, 1), (150, 900, 640, 0), (3, 700, 4095, 0)])
 def test_a_wait_that_gives_up(cuda_dev, m, n, k, pad):
     """A wait for operands given no polls: the call returns, its tiles hold NaN, the
     counter says so, and the next call is right."""
