@@ -344,6 +344,19 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   auto row_of = [&](int s, int array) { return BACK ? steps - 1 - s - (array == 2 ? 1 : 0) : s; };
   const raw *inputs[3] = {at<raw>(p.x, b, 0, c0), at<raw>(p.g, b, 0, c0), at<raw>(p.h, b, 0, c0)};
   const int64_t pitch[3] = {p.x.step, p.g.step, p.h.step};
+  // Without TMA: where rows start within their 16 bytes.  Step u of a thread has
+  // offset[array] + u * stride[array] in every round and every group, as kSteps
+  // rows are a multiple of 16 bytes; but of 8 for the 16-bit gradient's 4 steps,
+  // where `flip` is bit 3 of an odd group.
+  uint32_t offset[3] = {}, stride[3] = {}, flip = 0;
+  if constexpr (!TMA) {
+#pragma unroll
+    for (int array = 0; array < S::kArrays; ++array) {
+      stride[array] = (uint32_t)pitch[array] * (BACK ? (uint32_t)-ES : (uint32_t)ES);
+      offset[array] = (uint32_t)(uintptr_t)inputs[array] + (uint32_t)row_of(0, array) * (uint32_t)pitch[array] * ES;
+    }
+    if (N * ES % 16 != 0) flip = (group & 1) * 8;
+  }
   // Row r of a tile in shared memory holds step r of it, backward step kTime - 1 - r.
   auto request = [&](int round) {
     if (round >= rounds || *(volatile int *)&sh.failed) return;
@@ -405,19 +418,11 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
     wait_for<false>(smem_u32(&sh.full[stage]), (round / S::kStages) & 1, &sh.failed, p.polls);
     const char *mine = dynamic + stage * S::kStageBytes + side * 8 +
                        (BACK ? S::kTime - 1 - group * N : group * N) * S::kRowPitch;
-    // without TMA: where this thread's first row of each array starts within its 16 bytes
-    uint32_t offset[3] = {};
-    if constexpr (!TMA) {
-#pragma unroll
-      for (int array = 0; array < S::kArrays; ++array)
-        offset[array] = (uint32_t)(uintptr_t)inputs[array] +
-                        (uint32_t)row_of(s0, array) * (uint32_t)pitch[array] * (uint32_t)ES;
-    }
     auto words = [&](int u, int array) {
       const char *from = mine + array * S::kArrayBytes + (BACK ? -u : u) * S::kRowPitch;
       if constexpr (TMA) return *reinterpret_cast<const uint2 *>(from);
-      const uint32_t off = offset[array] + (uint32_t)(BACK ? -u : u) * (uint32_t)pitch[array] * (uint32_t)ES;
-      from += off & 12;
+      const uint32_t off = offset[array] + (uint32_t)u * stride[array];
+      from += N * ES % 16 != 0 && (pitch[array] & 1) ? (off ^ flip) & 12 : off & 12;
       uint2 w = make_uint2(lds32(from), lds32(from + 4));
       if constexpr (ES == 2) {
         const uint32_t bits = (off & 2) * 8;
@@ -433,12 +438,6 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
       } else {
         f[0] = __uint_as_float(w.x);
         f[1] = __uint_as_float(w.y);
-      }
-      if constexpr (!TMA) {  // what follows a row's end is not its own
-        if (channels < V) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) f[e] = e < channels ? f[e] : 0.f;
-        }
       }
     };
     auto input = [&](int u, int array, float (&f)[V]) { widen(words(u, array), f); };
@@ -634,8 +633,13 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
     raw *out0 = at<raw>(BACK ? p.dx : p.h, b, row_of(s0, 0), c), *out1 = at<raw>(p.dg, b, row_of(s0, 0), c);
     const int64_t out_pitch0 = BACK ? -p.dx.step : p.h.step, out_pitch1 = -p.dg.step;
     const bool whole = c0 + S::kWidth <= p.width;
-    // All lanes of the warp call it together; `in`: this thread's step exists.
-    auto write = [&](raw *to, const float (&f)[V], const bool in) {
+    const uint32_t at0 = (uint32_t)(uintptr_t)at<raw>(BACK ? p.dx : p.h, b, row_of(0, 0), c0),
+                   at1 = BACK ? (uint32_t)(uintptr_t)at<raw>(p.dg, b, row_of(0, 0), c0) : 0;
+    auto out_at = [&](int u, uint32_t first, int64_t pitch) { return TMA ? 0u : first + (uint32_t)u * (uint32_t)pitch * ES; };
+    // All lanes of the warp call it together; `in`: this thread's step exists;
+    // without TMA, `at` is the address modulo 8 of the group's channels, the same
+    // for all groups of a warp (their rows are 4 or 8 apart).
+    auto write = [&](raw *to, const uint32_t at, const float (&f)[V], const bool in) {
       if constexpr (V == 2) {
         if (TMA) {
           if (in) *reinterpret_cast<float2 *>(to) = make_float2(f[0], f[1]);
@@ -653,18 +657,29 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
 #pragma unroll
           for (int e = 0; e < V; ++e)
             if (in && e < channels) to[e] = E::put(f[e]);
-        } else if (((uintptr_t)to & 2) == 0) {  // the same for all groups of a warp, 8 rows apart
+        } else if ((at & 2) == 0) {
           if (in) {
-            *reinterpret_cast<uint32_t *>(to) = lo;
-            *reinterpret_cast<uint32_t *>(to + 2) = hi;
+            if (at & 4) {
+              *reinterpret_cast<uint32_t *>(to) = lo;
+              *reinterpret_cast<uint32_t *>(to + 2) = hi;
+            } else {
+              *reinterpret_cast<uint2 *>(to) = make_uint2(lo, hi);
+            }
           }
-        } else {  // 4-byte words across neighbouring lanes
+        } else {  // words across neighbouring lanes
           const uint32_t next = __shfl_down_sync(0xffffffffu, lo, 1, LANES);
           if (in) {
+            const uint32_t w0 = __funnelshift_r(lo, hi, 16), w1 = __funnelshift_r(hi, next, 16);
             if (side == 0) to[0] = (raw)(lo & 0xffffu);
-            *reinterpret_cast<uint32_t *>(to + 1) = __funnelshift_r(lo, hi, 16);
-            if (side < LANES - 1) *reinterpret_cast<uint32_t *>(to + 3) = __funnelshift_r(hi, next, 16);
-            else to[3] = (raw)(hi >> 16);
+            if (side == LANES - 1) {
+              *reinterpret_cast<uint32_t *>(to + 1) = w0;
+              to[3] = (raw)(hi >> 16);
+            } else if (at & 4) {  // 6: the words start on 8 bytes
+              *reinterpret_cast<uint2 *>(to + 1) = make_uint2(w0, w1);
+            } else {
+              *reinterpret_cast<uint32_t *>(to + 1) = w0;
+              *reinterpret_cast<uint32_t *>(to + 3) = w1;
+            }
           }
         }
       }
@@ -674,8 +689,8 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
       for (int u = 0; u < N; ++u) {
 #pragma unroll
         for (int e = 0; e < V; ++e) now[e] = __int_as_float(0x7fc00000);
-        write(out0 + u * out_pitch0, now, channels > 0 && s0 + u < steps);
-        if (BACK) write(out1 + u * out_pitch1, now, channels > 0 && s0 + u < steps);
+        write(out0 + u * out_pitch0, out_at(u, at0, out_pitch0), now, channels > 0 && s0 + u < steps);
+        if (BACK) write(out1 + u * out_pitch1, out_at(u, at1, out_pitch1), now, channels > 0 && s0 + u < steps);
       }
       continue;
     }
@@ -704,8 +719,8 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
           dg[e] = d[e] == 0.f ? 0.f : dg[e];
           dg[e + 1] = d[e + 1] == 0.f ? 0.f : dg[e + 1];
         }
-        write(out0 + u * out_pitch0, dx, in);
-        write(out1 + u * out_pitch1, dg, in);
+        write(out0 + u * out_pitch0, out_at(u, at0, out_pitch0), dx, in);
+        write(out1 + u * out_pitch1, out_at(u, at1, out_pitch1), dg, in);
       } else {
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
@@ -716,7 +731,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
             fma2(now[e], now[e + 1], d[e], d[e + 1], now[e], now[e + 1], xf[e], xf[e + 1]);
           }
         }
-        write(out0 + u * out_pitch0, now, in);
+        write(out0 + u * out_pitch0, out_at(u, at0, out_pitch0), now, in);
       }
     };
 #pragma unroll
