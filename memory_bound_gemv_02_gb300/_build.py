@@ -2,14 +2,18 @@
 
 Each translation unit is compiled for sm_103a in parallel, then linked into a
 shared library with the CUDA runtime linked statically (so the library does
-not depend on which libcudart the host process loaded).  No torch extension
-ABI is involved: the Python side talks to the library through ctypes.
+not depend on which libcudart the host process loaded).  The library knows
+nothing of torch: Python calls it through ctypes, and for the operators of
+gemv_ops.h through ``_lib/operators_py.so``, a small extension module that turns
+torch tensors into pointers, sizes and strides (host code, built against the
+installed torch and linked with the library).
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 import threading
 from concurrent.futures import ThreadPoolExecutor
 
@@ -22,6 +26,9 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "libgemv.so")
 HOST_TOOL_SRC = "bench_tool_main.cu"
 HOST_TOOL = os.path.join(LIBDIR, "gemv_bench_tool")  # native host-overhead and read-ceiling measurements
+
+EXTENSION_SRC = "operators_py.cpp"
+EXTENSION = os.path.join(LIBDIR, "operators_py.so")
 
 SOURCES = ["gemv_api.cu", "gemv_kernels_f16.cu", "gemv_kernels_bf16.cu", "gemv_bulk_f16.cu", "gemv_bulk_bf16.cu",
            "gla_decode.cu", "rms_norm.cu", "gated_scan.cu", "gemm.cu"]
@@ -45,11 +52,32 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(HOST_TOOL):
+    products = (LIB, HOST_TOOL, EXTENSION)
+    if not all(os.path.exists(f) for f in products):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST_TOOL))
-    deps = [os.path.join(CSRC, s) for s in SOURCES + [HOST_TOOL_SRC]] + HEADERS + [os.path.abspath(__file__)]
+    t = min(os.path.getmtime(f) for f in products)
+    deps = [os.path.join(CSRC, s) for s in SOURCES + [HOST_TOOL_SRC, EXTENSION_SRC]] + HEADERS + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _torch_dir() -> str:
+    import torch
+    return os.path.dirname(os.path.abspath(torch.__file__))
+
+
+def _run(cmd, what: str) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_extension() -> str:
+    obj = os.path.join(OBJDIR, "operators_py.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", os.path.join(CSRC, EXTENSION_SRC), "-o", obj,
+          "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(_torch_dir(), "include"), "-I" + cuda,
+          "-I" + INCLUDE], f"g++ failed for {EXTENSION_SRC}")
+    return obj
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -71,15 +99,22 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 print(r.stdout + r.stderr)
             return obj
 
-        with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+        with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+            extension_obj = ex.submit(_compile_extension)
             objs = list(ex.map(compile_one, SOURCES))
+            extension_obj = extension_obj.result()
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [exe, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", tmp, *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
-        # the native measurement tool, linked against the library just built
+        # the extension module and the native measurement tool, linked against the library just built
+        tmp = EXTENSION + f".tmp{os.getpid()}"
+        _run(["g++", "-shared", "-o", tmp, extension_obj, "-L" + LIBDIR, "-lgemv", "-Wl,-rpath,$ORIGIN",
+              "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+             "extension link failed")
+        os.replace(tmp, EXTENSION)
         tmp = HOST_TOOL + f".tmp{os.getpid()}"
         cmd = [exe, *NVCC_FLAGS, *extra_flags, os.path.join(CSRC, HOST_TOOL_SRC), "-o", tmp,
                "-L" + LIBDIR, "-lgemv", "-Xlinker", "-rpath,$ORIGIN"]

@@ -1,7 +1,9 @@
 """Python entry points of the operators in include/gemv_ops.h, with the C
 names: ``rms_norm_fused``, ``gemm_fused``, ``gemm_workspace``, ``gated_scan`` and
-``gated_scan_backward`` (imported into the package).  As in the package
-itself, tensors are only turned into pointers, sizes and strides.
+``gated_scan_backward`` (imported into the package).  Tensors are only turned into
+pointers, sizes and strides; that happens in an extension module
+(csrc/operators_py.cpp), as a decoded token's kernels are shorter than the same
+checks in Python.
 
 Without a ``stream`` argument the calls run on the current torch stream of
 the tensors' device.  Outputs may be passed in or are allocated.
@@ -9,19 +11,16 @@ the tensors' device.  Outputs may be passed in or are allocated.
 from __future__ import annotations
 
 import ctypes
-import struct
+import importlib.machinery
+import importlib.util
 
 import torch
-from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
 
-from . import ACTIVATIONS, _check, _lib_with_operators, _stream_handle
+from . import ACTIVATIONS, GEMV_ERR_SCRATCH, _build, _check, _stream_handle, lib
 
 GEMV_TYPE_F16, GEMV_TYPE_BF16, GEMV_TYPE_F32, GEMV_TYPE_E4M3 = 0, 1, 2, 3
 GEMV_ACT_LOG_SIGMOID = 4
 
-TYPE_CODES = {torch.float16: GEMV_TYPE_F16, torch.bfloat16: GEMV_TYPE_BF16, torch.float32: GEMV_TYPE_F32,
-              torch.float8_e4m3fn: GEMV_TYPE_E4M3}
-_ROW_TYPES = (torch.float16, torch.bfloat16, torch.float32)
 _F32, _E4M3, _BF16 = torch.float32, torch.float8_e4m3fn, torch.bfloat16
 
 #: activations of ``gemm_fused``: those of ``gemv_fused`` and log(sigmoid(y))
@@ -35,56 +34,25 @@ class GemmEpilogue(ctypes.Structure):
                 ("ldr", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
-# the same layout as bytes: a third of the time that filling the structure takes
-_pack_epilogue = struct.Struct("@ffPPPPqii").pack
-
-# The checks below are written for the time they take (a decoded token's calls
-# are shorter than their Python side): one look per attribute, device indexes
-# instead of device objects, and the raw stream of a device instead of torch's
-# stream object.  What is wrong is spelled out only once it is.
+_calls = None
 
 
-def _launch(device: int, stream, fn, args, where: str) -> None:
-    """Call an entry point with ``device`` current (switched only if it is not)."""
-    if stream is None:
-        stream = _cuda_getCurrentRawStream(device)
-    else:
-        stream = _stream_handle(stream)
-    if _cuda_getDevice() == device:
-        st = fn(*args, stream)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, stream)
-    if st:
-        _check(st, where)
+def _load():
+    """The extension module (raises if it has not been built)."""
+    global _calls
+    if _calls is None:
+        lib()
+        loader = importlib.machinery.ExtensionFileLoader("operators_py", _build.EXTENSION)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("operators_py", loader))
+        loader.exec_module(module)
+        _calls = module
+    return _calls
 
 
-def _refuse(t, name: str, shape, dtype, device) -> None:
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must have shape {tuple(shape)} on cuda:{device}, got {tuple(t.shape)} on {t.device}")
-
-
-def _rows(t: torch.Tensor, name: str, shape, dtype, device: int) -> int:
-    """Row stride of a 2-d CUDA tensor with unit column stride."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _refuse(t, name, shape, dtype, device)
-    ld, unit = t.stride()
-    rows, cols = shape
-    if unit != 1 and cols > 1 and rows:
-        raise ValueError(f"{name} must have unit column stride")
-    return ld if rows > 1 else cols
-
-
-def _vector(t, name: str, size: int, dtype, other, device: int):
-    """Pointer of an optional dense 1-d CUDA tensor (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype and t.dtype is not other:
-        raise TypeError(f"{name} must be {dtype} or {other}, got {t.dtype}")
-    if t.shape != (size,) or t.get_device() != device or (size > 1 and t.stride() != (1,)):
-        raise ValueError(f"{name} must be a contiguous tensor of {size} elements on cuda:{device}")
-    return t.data_ptr()
+def _dims(t, dims: int, name: str):
+    if t.dim() != dims or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dims}-d CUDA tensor")
+    return t.shape
 
 
 def rms_norm_fused(x, weight, residual=None, eps: float = 1e-6, eight_bit: bool = False, y=None, scale=None,
@@ -97,43 +65,18 @@ def rms_norm_fused(x, weight, residual=None, eps: float = 1e-6, eight_bit: bool 
     multiplied by; otherwise y has x's dtype and scale is None.
     ``residual_out`` (x's dtype; may be ``residual`` or ``x`` itself) receives s.
     Returns (y, scale, residual_out), the last None without a residual."""
-    dt, shape, dev = x.dtype, x.shape, x.get_device()
-    if len(shape) != 2 or dev < 0:
-        raise ValueError("x must be a 2-d CUDA tensor")
-    if dt not in _ROW_TYPES:
-        raise TypeError(f"x must be float16, bfloat16 or float32, got {dt}")
-    rows, d = shape
-    ldx = _rows(x, "x", shape, dt, dev)
-    w = _vector(weight, "weight", d, dt, _F32, dev)
-    out_dt = _E4M3 if eight_bit else dt
     if y is None:
-        y = torch.empty(shape, dtype=out_dt, device=x.device)
-    ldy = _rows(y, "y", shape, out_dt, dev)
-    if eight_bit:
-        if scale is None:
-            scale = torch.empty(rows, dtype=_F32, device=x.device)
-        sc = _vector(scale, "scale", rows, _F32, _F32, dev)
-    elif scale is not None:
-        raise ValueError("scale belongs to eight_bit=True")
-    else:
-        sc = None
-    if residual is not None:
-        ldr, rp = _rows(residual, "residual", shape, dt, dev), residual.data_ptr()
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dt, device=x.device)
-        if residual_out is residual:
-            ldo, op = ldr, rp
-        else:
-            ldo, op = _rows(residual_out, "residual_out", shape, dt, dev), residual_out.data_ptr()
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    else:
-        ldr = ldo = d
-        rp = op = None
-    code = TYPE_CODES[dt]
-    _launch(dev, stream, _lib_with_operators().rms_norm_fused,
-            (x.data_ptr(), ldx, rp, ldr, w, code if weight.dtype is dt else GEMV_TYPE_F32, y.data_ptr(), ldy, sc, op,
-             ldo, rows, d, eps, code, GEMV_TYPE_E4M3 if eight_bit else code), "rms_norm_fused")
+        _dims(x, 2, "x")
+        y = torch.empty_like(x, dtype=_E4M3 if eight_bit else None, memory_format=torch.contiguous_format)
+    if eight_bit and scale is None:
+        scale = torch.empty(_dims(x, 2, "x")[0], dtype=_F32, device=x.device)
+    if residual is not None and residual_out is None:
+        _dims(x, 2, "x")
+        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    st = (_calls or _load()).rms_norm_fused(x, weight, residual, eps, eight_bit, y, scale, residual_out,
+                                            stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "rms_norm_fused")
     return y, scale, residual_out
 
 
@@ -149,88 +92,33 @@ def gemm_fused(B, A, c=None, out_dtype=None, alpha: float = 1.0, beta: float = 1
     ``c``.  ``activation``: 'none', 'relu', 'sigmoid', 'silu' or 'log_sigmoid'.
     Operands with rows off 16 bytes are copied first (memory from torch's
     allocator).  Returns c (m, n)."""
-    dt, shape_a, shape_b, dev = A.dtype, A.shape, B.shape, A.get_device()
-    if len(shape_a) != 2 or len(shape_b) != 2 or shape_a[1] != shape_b[1]:
-        raise ValueError(f"shape mismatch: B {tuple(shape_b)}, A {tuple(shape_a)}")
-    if dev < 0:
-        raise ValueError("A and B must be CUDA tensors")
-    if dt is not _BF16 and dt is not _E4M3 and dt is not torch.float16:
-        raise TypeError(f"A and B must be float16, bfloat16 or float8_e4m3fn, got {dt}")
-    lda, ldb = _rows(A, "A", shape_a, dt, dev), _rows(B, "B", shape_b, dt, dev)
-    (m, k), n = shape_a, shape_b[0]
-    if out_dtype is None:
-        out_dtype = c.dtype if c is not None else _BF16 if dt is _E4M3 else dt
-    if out_dtype not in _ROW_TYPES:
-        raise TypeError(f"out_dtype must be float16, bfloat16 or float32, got {out_dtype}")
-    shape = (m, n)
     if c is None:
-        c = torch.empty(shape, dtype=out_dtype, device=A.device)
-    ldc = _rows(c, "c", shape, out_dtype, dev)
-    out_code = TYPE_CODES[out_dtype]
-    if residual is None:
-        ldr, rp = n, 0
-    else:
-        ldr, rp = _rows(residual, "residual", shape, out_dtype, dev), residual.data_ptr()
-    ep = _pack_epilogue(alpha, beta, _vector(scale_a, "scale_a", m, _F32, _F32, dev) or 0,
-                        _vector(scale_b, "scale_b", n, _F32, _F32, dev) or 0,
-                        _vector(bias, "bias", n, _F32, out_dtype, dev) or 0, rp, ldr,
-                        out_code if bias is not None and bias.dtype is out_dtype else GEMV_TYPE_F32,
-                        GEMM_ACTIVATIONS[activation])
-    pb, pa = B.data_ptr(), A.data_ptr()
-    es = 1 if dt is _E4M3 else 2
-    space = ws = None
-    if k and m and n and (pa | pb | (lda * es if m > 1 else 0) | (ldb * es if n > 1 else 0)) & 15:
-        need = ctypes.c_int64(0)
-        _check(_lib_with_operators().gemm_workspace(pb, ldb, pa, lda, m, n, k, TYPE_CODES[dt], ctypes.byref(need)),
-               "gemm_workspace")
-        space = need.value
-        ws = torch.empty(space, dtype=torch.uint8, device=A.device)
+        rows, cols = _dims(A, 2, "A")[0], _dims(B, 2, "B")[0]
+        c = torch.empty((rows, cols), dtype=out_dtype or (_BF16 if A.dtype is _E4M3 else A.dtype), device=A.device)
+    elif out_dtype is not None and c.dtype is not out_dtype:
+        raise TypeError(f"c must be {out_dtype}, got {c.dtype}")
+    if stream is not None:
+        stream = _stream_handle(stream)
+    args = (B, A, c, alpha, beta, scale_a, scale_b, bias, GEMM_ACTIVATIONS[activation], residual)
+    calls = _calls or _load()
+    st = calls.gemm_fused(*args, None, stream)
+    if st == GEMV_ERR_SCRATCH:  # operands off 16 bytes: nothing was launched yet
+        workspace = torch.empty(gemm_workspace(B, A), dtype=torch.uint8, device=A.device)
         if stream is not None:  # keep the memory until that stream is past the call
-            ws.record_stream(torch.cuda.ExternalStream(_stream_handle(stream), device=A.device))
-    _launch(dev, stream, _lib_with_operators().gemm_fused,
-            (pb, ldb, pa, lda, c.data_ptr(), ldc, m, n, k, TYPE_CODES[dt], out_code, ep,
-             None if ws is None else ws.data_ptr(), space or 0), "gemm_fused")
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=A.device))
+        st = calls.gemm_fused(*args, workspace, stream)
+    if st:
+        _check(st, "gemm_fused")
     return c
 
 
 def gemm_workspace(B, A) -> int:
     """Bytes that ``gemm_fused`` copies for these operands: 0 where their bases
     and row strides are multiples of 16 bytes."""
-    dt, dev = A.dtype, A.get_device()
-    lda, ldb = _rows(A, "A", A.shape, dt, dev), _rows(B, "B", B.shape, dt, dev)
-    need = ctypes.c_int64(0)
-    _check(_lib_with_operators().gemm_workspace(B.data_ptr(), ldb, A.data_ptr(), lda, A.shape[0], B.shape[0],
-                                                A.shape[1], TYPE_CODES[dt], ctypes.byref(need)), "gemm_workspace")
-    return need.value
-
-
-def _sequence(t, name: str, shape, dtype, device: int):
-    """(pointer, batch stride, step stride) of a (batch, steps, width) tensor."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _refuse(t, name, shape, dtype, device)
-    sb, ss, sw = t.stride()
-    if sw != 1 and shape[2] > 1:
-        raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t.data_ptr(), (sb if shape[0] > 1 else shape[1] * shape[2]), (ss if shape[1] > 1 else shape[2])
-
-
-def _carry(t, name: str, shape, device: int):
-    if t is None:
-        return None
-    if t.dtype is not _F32:
-        raise TypeError(f"{name} must be float32, got {t.dtype}")
-    if t.shape != shape or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor on cuda:{device}")
-    return t.data_ptr()
-
-
-def _sequence_type(x):
-    dt, dev, shape = x.dtype, x.get_device(), x.shape
-    if len(shape) != 3 or dev < 0:
-        raise ValueError("sequences must be 3-d CUDA tensors (batch, steps, width)")
-    if dt not in _ROW_TYPES:
-        raise TypeError(f"sequences must be float16, bfloat16 or float32, got {dt}")
-    return dt, dev, shape
+    need = (_calls or _load()).gemm_workspace(B, A)
+    if need < 0:
+        _check(need, "gemm_workspace")
+    return need
 
 
 def gated_scan(x, g, h0=None, h=None, state=None, stream=None):
@@ -243,17 +131,15 @@ def gated_scan(x, g, h0=None, h=None, state=None, stream=None):
     (batch, width); ``state`` receives the last step's unrounded h and may be
     ``h0`` (in-place decoding with steps = 1).  g = -inf starts a new sequence.
     Returns (h, state)."""
-    dt, dev, shape = _sequence_type(x)
-    carry = (shape[0], shape[2])
     if h is None:
-        h = torch.empty(shape, dtype=dt, device=x.device)
+        _dims(x, 3, "x")
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
     if state is None:
-        state = torch.empty(carry, dtype=_F32, device=x.device)
-    first = _carry(h0, "h0", carry, dev)
-    last = first if state is h0 else _carry(state, "state", carry, dev)
-    _launch(dev, stream, _lib_with_operators().gated_scan,
-            (*_sequence(x, "x", shape, dt, dev), *_sequence(g, "g", shape, dt, dev), first,
-             *_sequence(h, "h", shape, dt, dev), last, *shape, TYPE_CODES[dt]), "gated_scan")
+        batch, _, width = _dims(x, 3, "x")
+        state = torch.empty((batch, width), dtype=_F32, device=x.device)
+    st = (_calls or _load()).gated_scan(x, g, h0, h, state, stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "gated_scan")
     return h, state
 
 
@@ -261,17 +147,17 @@ def gated_scan_backward(dh, g, h, h0=None, dstate=None, dx=None, dg=None, dh0=No
     """The gradient of ``gated_scan``: ``dh`` is the gradient of h, ``dstate``
     that of the returned state (float32, optional); ``g``, ``h`` and ``h0`` as in
     and from the forward call.  Returns (dx, dg, dh0)."""
-    dt, dev, shape = _sequence_type(dh)
-    carry = (shape[0], shape[2])
     if dx is None:
-        dx = torch.empty(shape, dtype=dt, device=dh.device)
+        _dims(dh, 3, "dh")
+        dx = torch.empty_like(dh, memory_format=torch.contiguous_format)
     if dg is None:
-        dg = torch.empty(shape, dtype=dt, device=dh.device)
+        _dims(dh, 3, "dh")
+        dg = torch.empty_like(dh, memory_format=torch.contiguous_format)
     if dh0 is None:
-        dh0 = torch.empty(carry, dtype=_F32, device=dh.device)
-    _launch(dev, stream, _lib_with_operators().gated_scan_backward,
-            (*_sequence(dh, "dh", shape, dt, dev), *_sequence(g, "g", shape, dt, dev),
-             *_sequence(h, "h", shape, dt, dev), _carry(h0, "h0", carry, dev), _carry(dstate, "dstate", carry, dev),
-             *_sequence(dx, "dx", shape, dt, dev), *_sequence(dg, "dg", shape, dt, dev),
-             _carry(dh0, "dh0", carry, dev), *shape, TYPE_CODES[dt]), "gated_scan_backward")
+        batch, _, width = _dims(dh, 3, "dh")
+        dh0 = torch.empty((batch, width), dtype=_F32, device=dh.device)
+    st = (_calls or _load()).gated_scan_backward(dh, g, h, h0, dstate, dx, dg, dh0,
+                                                 stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "gated_scan_backward")
     return dx, dg, dh0
