@@ -310,19 +310,25 @@ struct AlignParams {
   AlignJob job[2];
 };
 
+// n / d for n >= 0, d > 0: in 32 bits where both fit, in a quarter of the time.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  return ((n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
+
 // A warp copies a piece: four times 512 bytes of a row, read as the aligned
 // 16-byte blocks that hold them (a lane's upper block is its neighbour's lower
 // one).  Memory-bound: it reads and writes the operand once.
 __global__ void __launch_bounds__(kAlignThreads) gemm_align_kernel(AlignParams p) {
-  allow_dependents();
   wait_for_predecessor();
+  allow_dependents();  // in this order: the product may read B, which is not written here, once it runs
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kAlignThreads / 32);
   for (int64_t i = (int64_t)blockIdx.x * (kAlignThreads / 32) + (threadIdx.x >> 5); i < p.job[0].total + p.job[1].total;
        i += warps) {
     const AlignJob &j = i < p.job[0].total ? p.job[0] : p.job[1];
-    const int64_t n = i < p.job[0].total ? i : i - p.job[0].total, line = n / j.pieces, piece = n - line * j.pieces;
-    const int64_t number = line / j.rows, row = line - number * j.rows;
+    const int64_t n = i < p.job[0].total ? i : i - p.job[0].total;
+    const int64_t line = quotient(n, j.pieces), piece = n - line * j.pieces;
+    const int64_t number = quotient(line, j.rows), row = line - number * j.rows;
     const int lead = (int)((j.class_base + (uint32_t)number * j.class_pitch) & 15);
     // byte d of the copy is byte d - lead of the row
     const uintptr_t start = (uintptr_t)(j.src + row * j.ld), end = start + (uintptr_t)j.bytes;
@@ -405,9 +411,13 @@ __global__ void __launch_bounds__(kSplitThreads)
     lead = (int)((p.base + (uint32_t)number * p.pitch) & 15);
   }
   // this CTA's share of k, whole steps, as even as they come
-  const int begin = (int)((int64_t)p.steps * split / p.splits), end = (int)((int64_t)p.steps * (split + 1) / p.splits);
+  const int begin = (int)((int64_t)p.steps * split / p.splits);
+  int end = (int)((int64_t)p.steps * (split + 1) / p.splits);
   const CUtensorMap *map_b = &p.map_b;
-  if constexpr (SHIFTED) map_b = &p.map_class[number];
+  if constexpr (SHIFTED) {
+    map_b = &p.map_class[number];
+    if (number + classes * j0 >= p.n) end = begin;  // the class has no rows here
+  }
   const uint32_t columns = p.cols <= 32 ? 32 : p.cols <= 64 ? 64 : p.cols <= 128 ? 128 : 256;
 
   if (threadIdx.x == 0) {
@@ -431,19 +441,32 @@ __global__ void __launch_bounds__(kSplitThreads)
   // After the allocation: a dependent kernel that started first could hold the
   // TMEM that this one waits for.
   allow_dependents();
-  wait_for_predecessor();
+  if (!SHIFTED || warp != 0) wait_for_predecessor();
 
   if (warp == 0) {
     const bool elected = elect_one();
     Ring r;
-    int step = begin;
+    int step = begin, ahead = begin;
+    if constexpr (SHIFTED) {
+      // gemm_align_kernel lets this kernel start once its own predecessor has
+      // completed, and does not write B: the ring's B tiles come meanwhile.
+      for (; ahead < end && ahead - begin < p.stages; ++ahead)
+        if (elected) {
+          mbar_expect_tx(smem_u32(&sh.full[ahead - begin]), stage_bytes);
+          tma_load<1>(tiles + (ahead - begin) * stage_bytes, map_b, ahead * (E4M3 ? kRowBytes : kRowBytes / 2), (int32_t)j0,
+                      smem_u32(&sh.full[ahead - begin]));
+        }
+      wait_for_predecessor();
+    }
     for (; step < end; ++step) {
       if (step - begin >= p.stages && !wait_for<false>(smem_u32(&sh.empty[r.stage]), r.phase ^ 1, &sh.failed, kPolls)) break;
       if (elected) {
         const uint32_t bar = smem_u32(&sh.full[r.stage]), at = tiles + r.stage * stage_bytes;
-        mbar_expect_tx(bar, stage_bytes);
         const int32_t x = step * (E4M3 ? kRowBytes : kRowBytes / 2);
-        tma_load<1>(at, map_b, x, (int32_t)j0, bar);
+        if (!SHIFTED || step >= ahead) {
+          mbar_expect_tx(bar, stage_bytes);
+          tma_load<1>(at, map_b, x, (int32_t)j0, bar);
+        }
         tma_load<1>(at + kTileBytes, &p.map_a, x, (int32_t)row0, bar);
       }
       r.next(p.stages);
