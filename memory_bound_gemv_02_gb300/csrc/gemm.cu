@@ -17,7 +17,7 @@
 // its classes of rows that start alike (ShiftedParams).  Shifting rows into place
 // within the product was slower than either at every size (77 x 4099 x 7169 fp16:
 // 72 us with cp.async of the covering blocks, 220 with a bulk copy per row, 37
-// copied first, 26 by classes): 128-byte pieces of 128 rows are the wrong shape
+// copied first, 22 by classes): 128-byte pieces of 128 rows are the wrong shape
 // for anything but a tensor map.
 //
 // Two kernels:
@@ -297,17 +297,18 @@ __device__ __forceinline__ void tile_at(int t, int tiles_n, int tiles_m, int ban
 // -------------------------------------------------------- rows off 16 bytes --
 
 // One operand to copy: `rows` rows of `bytes` bytes, `ld` apart, to rows of
-// `pitch` (a multiple of 16) in the workspace; `pieces` of 2 KB per row.  For
-// each of the classes of ShiftedParams once, behind as many zeros as the class
-// has bytes before its rows; zeros follow the row up to the pitch.
+// `pitch` (a multiple of 16) in the workspace, zeros behind each row.  For each
+// class (of ShiftedParams) once, with as many zeros in front as the class has
+// bytes before its rows.  A row is done in `pieces` of LOADS x 512 bytes.
 struct AlignJob {
   const char *src;
   char *dst;
-  int64_t ld, bytes, pitch, pieces, rows, total;  // total: classes x rows x pieces
-  uint32_t class_base, class_pitch;               // modulo 16
+  int64_t ld, bytes, pitch, rows, pieces, total;  // total: classes x rows x pieces
+  uint32_t class_base, class_pitch;
 };
 struct AlignParams {
   AlignJob job[2];
+  int32_t b_in_place;  // the product reads B before this kernel's end
 };
 
 // n / d for n >= 0, d > 0: in 32 bits where both fit, in a quarter of the time.
@@ -315,12 +316,33 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
   return ((n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
 }
 
-// A warp copies a piece: four times 512 bytes of a row, read as the aligned
+// The bytes from .. to - 1 of 16, zeros elsewhere.
+__device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int to) {  // of a word
+  from = from < 0 ? 0 : from;
+  if (to <= from || from >= 4) return 0;
+  if (to < 4) w &= (1u << (8 * to)) - 1;
+  return w & ~((1u << (8 * from)) - 1);
+}
+__device__ __forceinline__ uint4 keep_bytes(const uint4 &v, int from, int to) {
+  return make_uint4(keep_bytes(v.x, from, to), keep_bytes(v.y, from - 4, to - 4), keep_bytes(v.z, from - 8, to - 8),
+                    keep_bytes(v.w, from - 12, to - 12));
+}
+
+// A warp copies a piece: 512 bytes of a row at a time, read as the aligned
 // 16-byte blocks that hold them (a lane's upper block is its neighbour's lower
-// one).  Memory-bound: it reads and writes the operand once.
-__global__ void __launch_bounds__(kAlignThreads) gemm_align_kernel(AlignParams p) {
+// one).  Memory-bound for B: it reads and writes the operand once.  For A's
+// copies each class has warps of its own: a warp that wrote all classes' from one
+// read took twice as long (8 classes of one row of 14338 bytes: 7 us, now 4).
+// LOADS: 2 spread a small copy over more warps (1 x 1001 x 999 fp16 7.3 -> 6.8 us
+// for the whole call), 4 keep more in flight for a large one (512 x 4099 x 7169
+// 65 -> 60).
+template <int LOADS>
+__global__ void __launch_bounds__(kAlignThreads, 4) gemm_align_kernel(AlignParams p) {
+  // A product that reads B in place may do so once it runs: not before what
+  // precedes this kernel has completed.
+  if (!p.b_in_place) allow_dependents();
   wait_for_predecessor();
-  allow_dependents();  // in this order: the product may read B, which is not written here, once it runs
+  allow_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kAlignThreads / 32);
   for (int64_t i = (int64_t)blockIdx.x * (kAlignThreads / 32) + (threadIdx.x >> 5); i < p.job[0].total + p.job[1].total;
@@ -333,33 +355,24 @@ __global__ void __launch_bounds__(kAlignThreads) gemm_align_kernel(AlignParams p
     // byte d of the copy is byte d - lead of the row
     const uintptr_t start = (uintptr_t)(j.src + row * j.ld), end = start + (uintptr_t)j.bytes;
     const int off = (int)((start - lead) & 15);
-    const uintptr_t block = start - lead - off + (uintptr_t)(piece * 2048 + lane * 16);
-    char *to = j.dst + line * j.pitch + piece * 2048 + lane * 16;
-    uint4 lo[4], hi[4];
+    const int64_t d0 = piece * (LOADS * 512) + lane * 16, bytes = lead + j.bytes;
+    const uintptr_t block = start - lead - off + (uintptr_t)d0;
+    uint4 lo[LOADS], up[LOADS];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < LOADS; ++u) {
       const uintptr_t at = block + (uintptr_t)(u * 512);
       lo[u] = at < end && at + 16 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at)) : zero4();
-      hi[u] = lane == 31 && at + 16 < end && at + 32 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at + 16)) : zero4();
+      up[u] = lane == 31 && at + 16 < end && at + 32 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at + 16)) : zero4();
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      uint4 up;
-      up.x = __shfl_down_sync(0xffffffffu, lo[u].x, 1);
-      up.y = __shfl_down_sync(0xffffffffu, lo[u].y, 1);
-      up.z = __shfl_down_sync(0xffffffffu, lo[u].z, 1);
-      up.w = __shfl_down_sync(0xffffffffu, lo[u].w, 1);
-      if (lane == 31) up = hi[u];
-      uint4 v = shifted(lo[u], up, off);
-      const int64_t d = piece * 2048 + u * 512 + lane * 16;
-      if (d < lead || d + 16 > lead + j.bytes) {  // the row's ends: zeros outside
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int b = 0; b < 16; ++b)
-          if (d + b < lead || d + b >= lead + j.bytes) w[b / 4] &= ~(0xffu << (b % 4 * 8));
-        v = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      if (d < j.pitch) *reinterpret_cast<uint4 *>(to + u * 512) = v;
+    for (int u = 0; u < LOADS; ++u) {
+      const uint4 next = make_uint4(__shfl_down_sync(0xffffffffu, lo[u].x, 1), __shfl_down_sync(0xffffffffu, lo[u].y, 1),
+                                    __shfl_down_sync(0xffffffffu, lo[u].z, 1), __shfl_down_sync(0xffffffffu, lo[u].w, 1));
+      uint4 v = shifted(lo[u], lane < 31 ? next : up[u], off);
+      const int64_t d = d0 + u * 512;
+      if (d < lead || d + 16 > bytes)  // the row's ends: zeros outside
+        v = keep_bytes(v, lead - (int)(d < 16 ? d : 16), bytes - d < 16 ? (bytes - d < 0 ? 0 : (int)(bytes - d)) : 16);
+      if (d < j.pitch) *reinterpret_cast<uint4 *>(j.dst + line * j.pitch + d) = v;
     }
   }
 }
@@ -448,8 +461,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     Ring r;
     int step = begin, ahead = begin;
     if constexpr (SHIFTED) {
-      // gemm_align_kernel lets this kernel start once its own predecessor has
-      // completed, and does not write B: the ring's B tiles come meanwhile.
+      // gemm_align_kernel does not write B, and lets this kernel start once its
+      // own predecessor has completed: the ring's B tiles come meanwhile.
       for (; ahead < end && ahead - begin < p.stages; ++ahead)
         if (elected) {
           mbar_expect_tx(smem_u32(&sh.full[ahead - begin]), stage_bytes);
@@ -890,18 +903,18 @@ struct Shifted {
 
 // In place where reading B twice and writing it once costs more than the copies
 // of A, the rows of C written 16 bytes apart and each class's last tile.  Measured
-// with cold weights, in place / copied (us): fp16 n x k = 4099 x 7169, m = 1 18 / 33,
-// 77 26 / 39, 256 54 / 69, 512 80 / 60; 18433 x 4095, m = 1 31 / 72, 128 46 / 83,
-// 256 69 / 84, 512 127 / 106; 1001 x 999, m = 1 7.8 / 7.9, 128 10.8 / 9.9.  8 bits (twice the
+// with cold weights, in place / copied (us): fp16 n x k = 4099 x 7169, m = 1 16 / 33,
+// 77 22 / 39, 256 54 / 69, 512 80 / 60; 18433 x 4095, m = 1 30 / 72, 128 44 / 83,
+// 256 65 / 84, 512 127 / 106; 1001 x 999, m = 1 6.8 / 7.9, 128 10.8 / 8.9.  8 bits (twice the
 // classes, half the copy): 4099 x 7169, m = 1 15 / 20, 77 20 / 23, 128 31 / 27;
-// 18433 x 4095, m = 16 22 / 35, 128 43 / 42, 256 88 / 43.
+// 18433 x 4095, m = 16 20 / 35, 77 38 / 41, 128 43 / 42, 256 88 / 43.
 Shifted shifted_rows(const void *B, int64_t n, int64_t ldb_bytes, int64_t m, int64_t k, int es) {
   const int64_t k_bytes = k * es;
   Shifted s = {};
   if (n == 0 || k_bytes == 0 || tma_ok(B, n, ldb_bytes)) return s;
   int classes = 1;
   while (n > 1 && ldb_bytes * classes % 16 != 0) classes *= 2;
-  if (n * k_bytes < (1 << 20) || classes * m > n || classes * m > 1024 * es) return s;
+  if (n * k_bytes < (1 << 20) || classes * m > n || classes * m > 1280 * es) return s;
   if (ldb_bytes * classes >= (1ll << 40) || m * classes > INT32_MAX) return s;
   s.classes = classes;
   for (int j = 0; j < classes; ++j) {
@@ -1033,25 +1046,29 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
     AlignParams ap = {};
     char *to = static_cast<char *>(workspace);
     int jobs = 0;
+    const int loads = space > (16 << 20) ? 4 : 2;
     auto copy = [&](const void **from, int64_t rows, int64_t *ld, int64_t pitch, int copies) {
       AlignJob &job = ap.job[jobs++];
-      job = {static_cast<const char *>(*from), to, *ld, k * es, pitch, cdiv64(pitch, 2048), rows, 0, 0, 0};
+      job = {static_cast<const char *>(*from), to, *ld, k * es, pitch, rows, cdiv64(pitch, loads * 512), 0, 0, 0};
       job.total = copies * rows * job.pieces;
+      if (shift.classes) {
+        job.class_base = p.base;
+        job.class_pitch = p.pitch;
+      }
       *from = to;
       *ld = pitch;
       to += (copies * rows * pitch + 255) / 256 * 256;
     };
     if (shift.classes) {
       copy(&A, m, &lda_bytes, shift.pitch, shift.classes);
-      ap.job[0].class_base = p.base;
-      ap.job[0].class_pitch = p.pitch;
     } else {
       if (operand_space(B, n, k * es, ldb_bytes)) copy(&B, n, &ldb_bytes, aligned_pitch(k * es), 1);
       if (operand_space(A, m, k * es, lda_bytes)) copy(&A, m, &lda_bytes, aligned_pitch(k * es), 1);
     }
     const int64_t blocks = cdiv64(ap.job[0].total + ap.job[1].total, kAlignThreads / 32);
-    st = launch_op(gemm_align_kernel, dim3((unsigned)(blocks < 64ll * sms ? blocks : 64ll * sms)), kAlignThreads, 0, 1,
-                   stream, ap);
+    ap.b_in_place = shift.classes ? 1 : 0;
+    st = launch_op(loads == 4 ? gemm_align_kernel<4> : gemm_align_kernel<2>,
+                   dim3((unsigned)(blocks < 64ll * sms ? blocks : 64ll * sms)), kAlignThreads, 0, 1, stream, ap);
     if (st != GEMV_OK) return st;
   }
   bool mapped = true;
