@@ -43,6 +43,7 @@ constexpr int kRowBytes = 128;                   // bytes of k per tile row
 constexpr int kTileRows = 128;                   // rows of B per CTA
 constexpr int kTileBytes = kTileRows * kRowBytes;
 constexpr int kMaxStages = 8;
+constexpr int kPrefetchSteps = 4;                // of B that L2 is asked for while the predecessor ends
 constexpr int kMmaSteps = kRowBytes / 32;        // instructions per stage
 constexpr int kPolls = kWaitPolls;               // polls of one wait before it gives up
 constexpr int kEpilogueWarps = 8;                 // of gemm_pair_kernel
@@ -454,6 +455,11 @@ __global__ void __launch_bounds__(kSplitThreads)
   // After the allocation: a dependent kernel that started first could hold the
   // TMEM that this one waits for.
   allow_dependents();
+  // The first B tiles into L2 meanwhile (they are loaded after the wait): 1 x
+  // 4096 x 4096 bf16 10.2 -> 9.8 us back to back, 8 bit 7.7 -> 7.1; with 2 steps half of it.
+  if (!SHIFTED && warp == 0 && elect_one())
+    for (int step = begin; step < end && step - begin < kPrefetchSteps; ++step)
+      tma_prefetch(map_b, step * (E4M3 ? kRowBytes : kRowBytes / 2), (int32_t)j0);
   if (!SHIFTED || warp != 0) wait_for_predecessor();
 
   if (warp == 0) {
