@@ -209,6 +209,8 @@ struct Tile {
   static constexpr int kWidth = LANES * V;
   static constexpr int kGroups = kScanThreads / LANES;
   static constexpr int kPerWarp = 32 / LANES;
+  // 8 steps unaligned need 168 registers backward, which leaves one CTA per SM: 4 x
+  // 8192 x 4095 bf16 562 us, with 4 steps and two CTAs 495.
   static constexpr int kSteps = TMA || !BACK ? 8 : 4;
   static constexpr int kTime = kGroups * kSteps;
   static constexpr int kArrays = BACK ? 3 : 2;
@@ -286,14 +288,14 @@ struct alignas(8) TileShared {
 //      again, writing them.
 // (With threads composing the maps of all their channels, four times as many
 // words, and one warp sending for all, step 2 was half of a round: 1 x 65536 x
-// 1024 bf16 125 us forward, 149 backward, now 91 and 118.)
+// 1024 bf16 125 us forward, 149 backward, now 90 and 118.)
 // Rounds alternate between two sets of maps, so that no further barrier is
 // needed: a CTA sends the maps of a round after its threads have read those of
 // the round before.  The tiles of the rounds ahead are copied into shared memory
 // meanwhile: by TMA, or, where a row of an input does not start on 16 bytes, as
 // the aligned 16-byte blocks that cover its channels, whose words a thread joins
 // to its own.  (A bulk copy per row instead: one per 17 cycles and SM at best,
-// 245 us forward for 1 x 65537 x 1001 fp16; now 198.)
+// 245 us forward for 1 x 65537 x 1001 fp16; now 189.)
 //
 // Steps run on plain products and sums, which are right as long as everything
 // is finite and no product of decays is 0; since what is not finite stays so to
@@ -855,7 +857,15 @@ int launch_scan(const ScanParams &p, int sms, uint32_t *timeouts, cudaStream_t s
   const int es = type_bytes(TYPE);
   const bool vectors = p.width * es % 16 == 0 && on_boundary(p.x, p, es) && on_boundary(p.g, p, es) &&
                        on_boundary(p.h, p, es) && (!BACK || (on_boundary(p.dx, p, es) && on_boundary(p.dg, p, es)));
-  if (p.steps <= 4 || (p.steps <= 64 && p.batch * p.width * es >= (int64_t)sms * 128 * 16))
+  // Chains of 128 bytes; of 64 where clusters of those would leave SMs without a CTA.
+  const int64_t units = p.batch * ((p.width * es + 127) / 128);
+  // A thread per channel takes 2 us and about 0.2 per step, tiles about 2.6 us for
+  // every 2 x SMs chains, however few of a tile's steps there are: bf16 forward,
+  // walk / tiles (us), 25 x 12 x 3968 4.6 / 15.3, 25 x 48 x 3968 17.0 / 17.9, 25 x 64 x 3968
+  // 22.5 / 18.7, 25 x 12 x 1024 4.4 / 5.6, 25 x 24 x 1024 6.6 / 5.5, 8 x 12 x 512 4.3 / 3.2,
+  // 64 x 96 x 8192 56 / 88.  (Long sequences are not compared: tiles reach 93 % of the
+  // memory's rate, the walk 60 %.)
+  if (p.steps <= 4 || (p.steps <= 96 && (int64_t)p.steps * sms * 2 <= 10 * units))
     return vectors ? launch_walk<TYPE, true, BACK>(p, stream) : launch_walk<TYPE, false, BACK>(p, stream);
   // TMA copies need strides that are not 0 (shared rows) and fit their maps.
   auto mapped = [&](const Strided &s) {
@@ -863,9 +873,7 @@ int launch_scan(const ScanParams &p, int sms, uint32_t *timeouts, cudaStream_t s
            (p.batch == 1 || (s.batch > 0 && s.batch * es < (1ll << 40)));
   };
   const bool tma = vectors && mapped(p.x) && mapped(p.g) && (!BACK || mapped(p.h));
-  // Chains of 128 bytes; of 64 where clusters of those would leave SMs without a CTA.
-  const int64_t wide = p.batch * ((p.width * es + 127) / 128) * kMaxScanCluster;
-  if (wide < sms)
+  if (units * kMaxScanCluster < sms)
     return tma ? launch_tiles<TYPE, true, BACK, 8>(p, sms, timeouts, stream)
                : launch_tiles<TYPE, false, BACK, 8>(p, sms, timeouts, stream);
   return tma ? launch_tiles<TYPE, true, BACK, 16>(p, sms, timeouts, stream)

@@ -122,9 +122,15 @@ __device__ __forceinline__ T *in_register(T *v) {
   return v;
 }
 
-// The epilogue of one launch, and of one thread's column j of C.  ACT is its
-// activation: the caller's loop over the columns is compiled for each.
+// The activation of a launch: the loops over an epilogue's columns are compiled
+// for each.
 template <int ACT>
+struct Activation {};
+
+// The epilogue of one launch, and of one thread's column j of C.  Pairs read the
+// residual a block ahead (fetch()): in its turn 7656 x 8486 x 512 e4m3 took 164 us,
+// so 139.  With one tile per CTA that gains less (959 x 960 x 8576 fp16 30 -> 27) and
+// costs calls without a residual its registers and start (1024 x 1024 e4m3 4.1 -> 4.5).
 struct Column {
   static constexpr int kF16 = 1, kF32 = 2, kPairs = 4;  // bits of `how`
   int32_t m, how;
@@ -135,12 +141,12 @@ struct Column {
   bool live, odd, together;
   float factor, shift;
 
-  __device__ explicit Column(const GemmParams &p)
-      : m(in_register(p.m)),
-        how(in_register((p.out_type == GEMV_TYPE_F16 ? kF16 : p.out_type == GEMV_TYPE_F32 ? kF32 : 0) |
-                        (p.pairs ? kPairs : 0))),
-        scale_a(in_register(p.scale_a)) {
+  __device__ __forceinline__ void init(const GemmParams &p) {
     const uint32_t es = p.out_type == GEMV_TYPE_F32 ? 4 : 2;
+    m = in_register(p.m);
+    how = in_register((p.out_type == GEMV_TYPE_F16 ? kF16 : p.out_type == GEMV_TYPE_F32 ? kF32 : 0) |
+                      (p.pairs ? kPairs : 0));
+    scale_a = in_register(p.scale_a);
     pitch = in_register((uint32_t)p.ldc * es);
     res_pitch = in_register((uint32_t)p.ldr * es);
   }
@@ -195,9 +201,26 @@ struct Column {
     }
   }
 
-  // rows i0 .. of C from their sums: as many of the COUNT as there are, at most `most`
+  // The residual's rows i0 .. (as write() takes them), not yet converted.
   template <int COUNT>
-  __device__ __forceinline__ void write(int i0, const float (&sum)[COUNT], int most = COUNT) const {
+  __device__ __forceinline__ void fetch(int i0, uint32_t (&raw)[COUNT], int most = COUNT) const {
+    if (!res || !live) return;
+    const int rows = m - i0 < most ? m - i0 : most;
+    const char *r = res + (int64_t)i0 * res_pitch;
+    if (how & kF32) {
+#pragma unroll
+      for (int e = 0; e < COUNT; ++e) raw[e] = e < rows ? *row<uint32_t>(r, res_pitch, e) : 0;
+    } else {
+#pragma unroll
+      for (int e = 0; e < COUNT; ++e) raw[e] = e < rows ? *row<uint16_t>(r, res_pitch, e) : 0;
+    }
+  }
+
+  // rows i0 .. of C from their sums and the residual's: as many of the COUNT as
+  // there are, at most `most`
+  template <int ACT, int COUNT>
+  __device__ __forceinline__ void write(Activation<ACT>, int i0, const float (&sum)[COUNT], const uint32_t (&raw)[COUNT],
+                                        int most = COUNT) const {
     const int rows = m - i0 < most ? m - i0 : most;
     float y[COUNT];
     if (scale_a) {
@@ -211,21 +234,15 @@ struct Column {
 #pragma unroll
     for (int e = 0; e < COUNT; ++e) y[e] = activated<ACT>(y[e]);
     if (res && live) {
-      const char *r = res + (int64_t)i0 * res_pitch;
       if (how & kF32) {
 #pragma unroll
-        for (int e = 0; e < COUNT; ++e) y[e] += e < rows ? *row<float>(r, res_pitch, e) : 0.f;
+        for (int e = 0; e < COUNT; ++e) y[e] += __uint_as_float(raw[e]);
+      } else if (how & kF16) {
+#pragma unroll
+        for (int e = 0; e < COUNT; ++e) y[e] += F16::to_float((uint16_t)raw[e]);
       } else {
-        uint16_t raw[COUNT];
 #pragma unroll
-        for (int e = 0; e < COUNT; ++e) raw[e] = e < rows ? *row<uint16_t>(r, res_pitch, e) : 0;
-        if (how & kF16) {
-#pragma unroll
-          for (int e = 0; e < COUNT; ++e) y[e] += F16::to_float(raw[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < COUNT; ++e) y[e] += BF16::to_float(raw[e]);
-        }
+        for (int e = 0; e < COUNT; ++e) y[e] += BF16::to_float((uint16_t)raw[e]);
       }
     }
     char *at = c + (int64_t)i0 * pitch;
@@ -238,17 +255,24 @@ struct Column {
       else store<uint16_t>(at, rows, y, [](float v) { return BF16::from_float(v); });
     }
   }
+  // The same with the residual read in its turn.
+  template <int ACT, int COUNT>
+  __device__ __forceinline__ void write(Activation<ACT> act, int i0, const float (&sum)[COUNT], int most = COUNT) const {
+    uint32_t raw[COUNT];
+    fetch(i0, raw, most);
+    write(act, i0, sum, raw, most);
+  }
 };
 
-// run(Column<act>) for the launch's activation.
+// run(Activation<act>) for the launch's activation.
 template <class Run>
-__device__ __forceinline__ void with_column(const GemmParams &p, Run run) {
-  switch (p.act) {
-    case GEMV_ACT_RELU: run(Column<GEMV_ACT_RELU>(p)); break;
-    case GEMV_ACT_SIGMOID: run(Column<GEMV_ACT_SIGMOID>(p)); break;
-    case GEMV_ACT_SILU: run(Column<GEMV_ACT_SILU>(p)); break;
-    case GEMV_ACT_LOG_SIGMOID: run(Column<GEMV_ACT_LOG_SIGMOID>(p)); break;
-    default: run(Column<GEMV_ACT_NONE>(p)); break;
+__device__ __forceinline__ void with_activation(int act, Run run) {
+  switch (act) {
+    case GEMV_ACT_RELU: run(Activation<GEMV_ACT_RELU>()); break;
+    case GEMV_ACT_SIGMOID: run(Activation<GEMV_ACT_SIGMOID>()); break;
+    case GEMV_ACT_SILU: run(Activation<GEMV_ACT_SILU>()); break;
+    case GEMV_ACT_LOG_SIGMOID: run(Activation<GEMV_ACT_LOG_SIGMOID>()); break;
+    default: run(Activation<GEMV_ACT_NONE>()); break;
   }
 }
 
@@ -462,6 +486,13 @@ __global__ void __launch_bounds__(kSplitThreads)
       tma_prefetch(map_b, step * (E4M3 ? kRowBytes : kRowBytes / 2), (int32_t)j0);
   if (!SHIFTED || warp != 0) wait_for_predecessor();
 
+  // All warps write C: a quarter of the lanes each (the one TMEM gives them), and
+  // 16 columns in turn, or with a split a few of the CTA's share.
+  constexpr int kTurns = kSplitThreads / 128, kAtOnce = 4;
+  const int quarter = warp & 3, turn = warp >> 2, l = quarter * 32 + lane;
+  const int share = p.cols / p.splits;
+  Column col;
+
   if (warp == 0) {
     const bool elected = elect_one();
     Ring r;
@@ -541,14 +572,11 @@ __global__ void __launch_bounds__(kSplitThreads)
   }
   if (p.splits > 1) cluster_sync();
 
-  // All warps: a quarter of the lanes each (the one TMEM gives them), and 16
-  // columns in turn.
-  constexpr int kTurns = kSplitThreads / 128;
-  const int quarter = warp & 3, turn = warp >> 2, l = quarter * 32 + lane;
   const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
   if (p.splits == 1) {
-    with_column(p, [&](auto col) {
-      col.begin(p, number + classes * (j0 + l));
+    col.init(p);
+    col.begin(p, number + classes * (j0 + l));
+    with_activation(p.act, [&](auto act) {
 #pragma unroll 1
       for (int c = turn * 16; c < p.cols && i0 + c < p.m; c += 16 * kTurns) {
         float v[16];
@@ -557,12 +585,11 @@ __global__ void __launch_bounds__(kSplitThreads)
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = failed ? nan : 0.f;
         }
-        col.write((int)i0 + c, v);
+        col.write(act, (int)i0 + c, v);
       }
     });
   } else {
     // Column c goes to CTA c / share, as [source][column][lane].
-    const int share = p.cols / p.splits;
     for (int c = turn * 16; c < p.cols; c += 16 * kTurns) {
       float v[16];
       tmem_load16(from + c, v);
@@ -578,19 +605,20 @@ __global__ void __launch_bounds__(kSplitThreads)
       }
     }
     cluster_sync();
+    col.init(p);
+    col.begin(p, number + classes * (j0 + l));
     const float *parts = reinterpret_cast<const float *>(dynamic + (tiles - smem_u32(dynamic))) + l;
-    with_column(p, [&](auto col) {
-      col.begin(p, number + classes * (j0 + l));
-      constexpr int kAtOnce = 4;
+    with_activation(p.act, [&](auto act) {
+      const int first = (int)i0 + split * share;
 #pragma unroll 1
-      for (int c = turn * kAtOnce; c < share && i0 + split * share + c < p.m; c += kTurns * kAtOnce) {
+      for (int c = turn * kAtOnce; c < share && first + c < p.m; c += kTurns * kAtOnce) {
         float v[kAtOnce] = {};
         for (int s = 0; s < p.splits; ++s) {
 #pragma unroll
           for (int e = 0; e < kAtOnce; ++e)
             if (c + e < share) v[e] += parts[(s * share + c + e) * kTileRows];
         }
-        col.write((int)i0 + split * share + c, v, share - c);
+        col.write(act, first + c, v, share - c);
       }
     });
   }
@@ -720,7 +748,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
   } else {
     const int quarter = warp & 3, part = (warp - 2) >> 2, l = quarter * 32 + lane;
     const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
-    with_column(p, [&](auto col) {
+    Column col;
+    col.init(p);
+    with_activation(p.act, [&](auto act) {
       bool ok = true;
       int turn = 0;
       for (int t = first; t < count; t += pairs, ++turn) {
@@ -728,7 +758,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
         int tn, tm;
         tile_at(t, p.tiles_n, p.tiles_m, kPairBand, &tn, &tm);
         const int i0 = tm * p.cols, end = min(p.cols, p.m - i0);
+        const bool residual = p.residual != nullptr;
+        uint32_t raw[16];
         col.begin(p, (int64_t)tn * (2 * kTileRows) + rank * kTileRows + l);
+        if (residual) col.fetch(i0 + part * 16, raw, end - part * 16);
         if (ok) {
           // a whole product: some polls for each of its steps
           ok = wait_for<false>(smem_u32(&sh.sums[acc]), (turn >> 1) & 1, &sh.failed, kPolls + 64ll * p.steps);
@@ -736,16 +769,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_pair_kernel(const __grid
           tc_fence_after();
         }
         const uint32_t at = from + (uint32_t)(acc * kAccumulatorColumns);
+        auto turns = [&](const bool ahead) {
 #pragma unroll 1
-        for (int c = part * 16; c < end; c += kEpilogueWarps * 4) {
-          float v[16];
-          tmem_load16(at + c, v);
-          if (!ok) {
+          for (int c = part * 16; c < end; c += kEpilogueWarps * 4) {
+            float v[16];
+            uint32_t next[16];
+            if (ahead) col.fetch(i0 + c + kEpilogueWarps * 4, next, end - c - kEpilogueWarps * 4);
+            tmem_load16(at + c, v);
+            if (!ok) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fc00000);
+              for (int e = 0; e < 16; ++e) v[e] = __int_as_float(0x7fc00000);
+            }
+            if (ahead) {
+              col.write(act, i0 + c, v, raw);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) raw[e] = next[e];
+            } else {
+              col.write(act, i0 + c, v);
+            }
           }
-          col.write(i0 + c, v);
-        }
+        };
+        if (residual) turns(true);
+        else turns(false);
         tc_fence_before();
         __syncwarp();
         if (ok && lane == 0) mbar_arrive_cluster(cluster_address(smem_u32(&sh.free_[acc]), 0));
