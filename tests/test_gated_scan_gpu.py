@@ -224,6 +224,32 @@ def test_repeatable_and_on_a_stream(cuda_dev):
         assert all(torch.equal(p, q) for p, q in zip(grads, grads2))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("b,t,d", [(2, 40, 96), (25, 12, 640), (1, 3000, 512), (2, 700, 65), (3, 300, 2048)])
+def test_calls_back_to_back(cuda_dev, dtype, b, t, d):
+    """Calls on two sets of inputs in turn, nothing waited for between them: every
+    one gives what it gives alone, and no input changes."""
+    sets = [_inputs(b, t, d, dtype, cuda_dev, 71 + 10 * i) for i in range(2)]
+    dhs = [ref.uniform((b, t, d), dtype, 91 + i, cuda_dev) for i in range(2)]
+    kept = [[v.clone() for v in s] for s in sets]
+    alone = []
+    for (x, gate, h0), dh in zip(sets, dhs):
+        h, state = g.gated_scan(x, gate, h0=h0)
+        torch.cuda.synchronize()
+        grads = g.gated_scan_backward(dh, gate, h, h0=h0, dstate=state)
+        torch.cuda.synchronize()
+        alone.append((h, state, *grads))
+    outs = [[torch.empty_like(v) for v in a] for a in alone]
+    for i in (0, 1, 0, 1, 0):
+        (x, gate, h0), (h, state, dx, dg, dh0) = sets[i], outs[i]
+        g.gated_scan(x, gate, h0=h0, h=h, state=state)
+        g.gated_scan_backward(dhs[i], gate, h, h0=h0, dstate=state, dx=dx, dg=dg, dh0=dh0)
+    torch.cuda.synchronize()
+    for a, o in zip(alone, outs):
+        assert all(torch.equal(p, q) for p, q in zip(a, o))
+    assert all(torch.equal(p, q) for s, k in zip(sets, kept) for p, q in zip(s, k))
+
+
 @pytest.mark.parametrize("b,t,d", [(2, 700, 64), (1, 5000, 512), (2, 700, 65), (40, 200, 512)])
 def test_a_wait_that_gives_up(cuda_dev, b, t, d):
     """Waits for copies given no polls: the calls return, their outputs are NaN, the
