@@ -16,7 +16,7 @@ import importlib.util
 
 import torch
 
-from . import ACTIVATIONS, GEMV_ERR_SCRATCH, _build, _check, _stream_handle, lib
+from . import ACTIVATIONS, _build, _check, _stream_handle, lib
 
 GEMV_TYPE_F16, GEMV_TYPE_BF16, GEMV_TYPE_F32, GEMV_TYPE_E4M3 = 0, 1, 2, 3
 GEMV_ACT_LOG_SIGMOID = 4
@@ -81,7 +81,7 @@ def rms_norm_fused(x, weight, residual=None, eps: float = 1e-6, eight_bit: bool 
 
 
 def gemm_fused(B, A, c=None, out_dtype=None, alpha: float = 1.0, beta: float = 1.0, scale_a=None, scale_b=None,
-               bias=None, activation: str = "none", residual=None, stream=None) -> torch.Tensor:
+               bias=None, activation: str = "none", residual=None, stream=None, workspace=None) -> torch.Tensor:
     """c = act(alpha * scale_a scale_b^T * (A @ B.T) + beta * bias) + residual.
 
     ``B``: (n, k) weights and ``A``: (m, k) vectors, both float16, bfloat16 or
@@ -90,31 +90,24 @@ def gemm_fused(B, A, c=None, out_dtype=None, alpha: float = 1.0, beta: float = 1
     ``scale_a`` (m,) and ``scale_b`` (n,): float32.  ``bias``: (n,), float32 or
     the output's dtype.  ``residual``: (m, n) in the output's dtype, may be
     ``c``.  ``activation``: 'none', 'relu', 'sigmoid', 'silu' or 'log_sigmoid'.
-    Operands with rows off 16 bytes are copied first (memory from torch's
-    allocator).  Returns c (m, n)."""
+    Operands with rows off 16 bytes are copied first, to ``workspace`` (any
+    tensor of ``gemm_workspace`` bytes) or to memory that torch's allocator has
+    for the call's stream.  Returns c (m, n)."""
     if c is None:
         rows, cols = _dims(A, 2, "A")[0], _dims(B, 2, "B")[0]
         c = torch.empty((rows, cols), dtype=out_dtype or (_BF16 if A.dtype is _E4M3 else A.dtype), device=A.device)
     elif out_dtype is not None and c.dtype is not out_dtype:
         raise TypeError(f"c must be {out_dtype}, got {c.dtype}")
-    if stream is not None:
-        stream = _stream_handle(stream)
-    args = (B, A, c, alpha, beta, scale_a, scale_b, bias, GEMM_ACTIVATIONS[activation], residual)
-    calls = _calls or _load()
-    st = calls.gemm_fused(*args, None, stream)
-    if st == GEMV_ERR_SCRATCH:  # operands off 16 bytes: nothing was launched yet
-        workspace = torch.empty(gemm_workspace(B, A), dtype=torch.uint8, device=A.device)
-        if stream is not None:  # keep the memory until that stream is past the call
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=A.device))
-        st = calls.gemm_fused(*args, workspace, stream)
+    st = (_calls or _load()).gemm_fused(B, A, c, alpha, beta, scale_a, scale_b, bias, GEMM_ACTIVATIONS[activation],
+                                        residual, workspace, stream if stream is None else _stream_handle(stream))
     if st:
         _check(st, "gemm_fused")
     return c
 
 
 def gemm_workspace(B, A) -> int:
-    """Bytes that ``gemm_fused`` copies for these operands: 0 where their bases
-    and row strides are multiples of 16 bytes."""
+    """Bytes of workspace that ``gemm_fused`` takes for these operands: 0 where
+    their bases and row strides are multiples of 16 bytes."""
     need = (_calls or _load()).gemm_workspace(B, A)
     if need < 0:
         _check(need, "gemm_workspace")

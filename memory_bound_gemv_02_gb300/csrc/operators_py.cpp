@@ -8,6 +8,7 @@
 // status; a wrong argument raises TypeError or ValueError.
 #include <Python.h>
 
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -122,22 +123,49 @@ float number(PyObject *o) {
   return (float)v;
 }
 
-// The call with its device current, on the given stream (None: torch's current
-// one of that device); other Python threads may run meanwhile.
+// Other Python threads may run while this lives.
+struct WithoutGil {
+  PyThreadState *const state = PyEval_SaveThread();
+  ~WithoutGil() { PyEval_RestoreThread(state); }
+};
+
+// The given stream (None: torch's current one of the device).
+cudaStream_t stream_of(PyObject *stream, int64_t device) {
+  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
+  if (s == nullptr && PyErr_Occurred()) throw Raised();
+  return s;
+}
+
+// Device memory of torch's allocator that belongs to a stream, while this lives:
+// the stream's earlier work is done with it when the stream's next kernel starts,
+// and what is allocated on the stream later comes after that kernel.  A block of
+// another stream's would need both waits.
+class StreamMemory {
+ public:
+  StreamMemory(int64_t bytes, cudaStream_t stream)
+      : p_(bytes > 0 ? c10::cuda::CUDACachingAllocator::raw_alloc_with_stream((size_t)bytes, stream) : nullptr) {}
+  ~StreamMemory() {
+    if (p_) c10::cuda::CUDACachingAllocator::raw_delete(p_);
+  }
+  StreamMemory(const StreamMemory &) = delete;
+  StreamMemory &operator=(const StreamMemory &) = delete;
+  void *get() const { return p_; }
+
+ private:
+  void *const p_;
+};
+
+// call(stream) with its device current.
 template <class Call>
 PyObject *launch(int64_t device, PyObject *stream, Call call) {
-  cudaStream_t s;
-  if (stream == Py_None) {
-    s = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-  } else {
-    s = reinterpret_cast<cudaStream_t>(PyLong_AsVoidPtr(stream));
-    if (s == nullptr && PyErr_Occurred()) throw Raised();
-  }
+  const cudaStream_t s = stream_of(stream, device);
   const c10::cuda::CUDAGuard guard((c10::DeviceIndex)device);
   int status;
-  Py_BEGIN_ALLOW_THREADS;
-  status = call(s);
-  Py_END_ALLOW_THREADS;
+  {
+    const WithoutGil released;
+    status = call(s);
+  }
   return PyLong_FromLong(status);
 }
 
@@ -148,6 +176,12 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, Body body) {
     if (got != want) raise(PyExc_TypeError, "%zd arguments expected, got %zd", want, got);
     return body();
   } catch (const Raised &) {
+  } catch (const c10::OutOfMemoryError &e) {
+    PyObject *const torch = PyImport_ImportModule("torch");
+    PyObject *const type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    if (type) PyErr_SetString(type, e.what_without_backtrace());
+    Py_XDECREF(type);
+    Py_XDECREF(torch);
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
   }
@@ -190,7 +224,8 @@ PyObject *py_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t count) {
   });
 }
 
-// B, A, c, alpha, beta, scale_a, scale_b, bias, activation, residual, workspace, stream
+// B, A, c, alpha, beta, scale_a, scale_b, bias, activation, residual, workspace, stream.
+// Without a workspace, what the operands need is allocated here, on the call's stream.
 PyObject *py_gemm(PyObject *, PyObject *const *a, Py_ssize_t count) {
   return guarded(count, 12, [&]() {
     const Tensor &B = tensor(a[0], "B"), &A = tensor(a[1], "A"), &c = tensor(a[2], "c");
@@ -227,12 +262,19 @@ PyObject *py_gemm(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (a[10] != Py_None) {
       const Tensor &w = tensor(a[10], "workspace");
       check_device(w, "workspace", dev);
+      if (!w.is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
       workspace = w.data_ptr();
       bytes = (int64_t)w.nbytes();
     }
+    const bool given = a[10] != Py_None;
     return launch(dev, a[11], [&](cudaStream_t s) {
-      return gemm_fused(mb.p, mb.ld, ma.p, ma.ld, mc.p, mc.ld, m, n, k, type_code(type), type_code(out), &ep, workspace,
-                        bytes, s);
+      if (!given) {
+        const int st = gemm_workspace(mb.p, mb.ld, ma.p, ma.ld, m, n, k, type_code(type), &bytes);
+        if (st != GEMV_OK) return st;
+      }
+      const StreamMemory own(given ? 0 : bytes, s);
+      return gemm_fused(mb.p, mb.ld, ma.p, ma.ld, mc.p, mc.ld, m, n, k, type_code(type), type_code(out), &ep,
+                        given ? workspace : own.get(), bytes, s);
     });
   });
 }

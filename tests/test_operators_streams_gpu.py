@@ -1,0 +1,99 @@
+"""The operators called with a stream of their own while other work is pending,
+and from several streams and host threads at once.
+
+Torch's allocator hands a freed block out again at once, in the order of the
+stream that it belongs to.  Memory that a call allocates for itself has to
+belong to the stream it runs on: a block of the current stream's may still be
+read or written by work queued there.
+"""
+from __future__ import annotations
+
+import gc
+
+import pytest
+import torch
+
+import memory_bound_gemv_02_gb300 as g
+import operator_refs as ref
+
+pytestmark = pytest.mark.gpu
+
+DELAY = 20_000_000  # cycles, some 10 ms: far longer than the calls below
+
+# B copied, B and A copied, B read in place and A copied per class of rows
+UNALIGNED = [(300, 1025, 999, 0), (700, 900, 1001, 0), (17, 1301, 999, 3), (30, 1200, 1004, 0)]
+
+
+def _whole(m, n, k, dtype, dev, off=0):
+    """Operands of small whole numbers: every partial sum is exact in fp32."""
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(m * n + k)
+    out = []
+    for rows in (m, n):
+        buf = torch.zeros(rows * k + off, device=dev).to(dtype)
+        v = buf[off:].view(rows, k)
+        v.copy_(torch.randint(-3, 4, (rows, k), generator=gen, device=dev).float())
+        out.append(v)
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("m,n,k,off", UNALIGNED)
+def test_copies_do_not_take_pending_memory(cuda_dev, m, n, k, off, dtype):
+    """A block of the workspace's size, freed while the current stream has still to
+    read it, keeps its contents, and the product on another stream is exact."""
+    A, B = _whole(m, n, k, dtype, cuda_dev, off)
+    want = A.double() @ B.double().t()
+    size = g.gemm_workspace(B, A)
+    assert size > 0
+    out = torch.empty((m, n), device=cuda_dev)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # the block freed next is the one of its size
+    temporary = torch.full((size,), 7, dtype=torch.uint8, device=cuda_dev)
+    torch.cuda._sleep(DELAY)
+    kept = temporary.clone()
+    del temporary
+    gc.collect()
+    g.gemm_fused(B, A, out, stream=side)
+    side.synchronize()
+    assert torch.equal(out.double(), want)
+    torch.cuda.synchronize()
+    assert (kept == 7).all()
+
+
+@pytest.mark.parametrize("m,n,k,off", UNALIGNED)
+def test_a_given_workspace(cuda_dev, m, n, k, off):
+    A, B = _whole(m, n, k, torch.bfloat16, cuda_dev, off)
+    want = A.double() @ B.double().t()
+    size = g.gemm_workspace(B, A)
+    room = torch.full((size + 512,), 9, dtype=torch.uint8, device=cuda_dev)
+    c = g.gemm_fused(B, A, out_dtype=torch.float32, workspace=room[256:256 + size])
+    assert torch.equal(c.double(), want)
+    assert (room[:256] == 9).all() and (room[256 + size:] == 9).all() and (room[256:256 + size] != 9).any()
+    with pytest.raises(g.GemvError) as e:
+        g.gemm_fused(B, A, workspace=room[:size - 1])
+    assert e.value.status == g.GEMV_ERR_SCRATCH
+    with pytest.raises(g.GemvError) as e:
+        g.gemm_fused(B, A, workspace=room[8:])
+    assert e.value.status == g.GEMV_ERR_ALIGN
+    with pytest.raises(ValueError):
+        g.gemm_fused(B, A, workspace=room[::2])
+
+
+@pytest.mark.parametrize("m,n,k,off", UNALIGNED)
+def test_copies_in_a_graph(cuda_dev, m, n, k, off):
+    A, B = _whole(m, n, k, torch.bfloat16, cuda_dev, off)
+    out = torch.empty((m, n), device=cuda_dev)
+    g.gemm_fused(B, A, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.gemm_fused(B, A, out)
+    for scale in (1, -1, 2):
+        A.copy_(A.float() * scale)
+        want = A.double() @ B.double().t()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.double(), want)
