@@ -6,7 +6,9 @@ pointers, sizes and strides; that happens in an extension module
 checks in Python.
 
 Without a ``stream`` argument the calls run on the current torch stream of
-the tensors' device.  Outputs may be passed in or are allocated.
+the tensors' device.  Outputs may be passed in or are allocated, on the stream
+that the call runs on; ordering that stream after the inputs' work, and its
+readers after the call, is the caller's.  Results carry no gradient history.
 """
 from __future__ import annotations
 
@@ -55,6 +57,18 @@ def _dims(t, dims: int, name: str):
     return t.shape
 
 
+def _new(make, stream, device):
+    """make()'s tensor, for a call on ``stream``: of that stream's memory (a block
+    of the current stream's may still be in use there), and not handed out again
+    before the current stream has read it."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=device)):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def rms_norm_fused(x, weight, residual=None, eps: float = 1e-6, eight_bit: bool = False, y=None, scale=None,
                    residual_out=None, stream=None):
     """s = x + residual; y = s * weight / sqrt(mean(s^2) + eps) per row.
@@ -67,12 +81,14 @@ def rms_norm_fused(x, weight, residual=None, eps: float = 1e-6, eight_bit: bool 
     Returns (y, scale, residual_out), the last None without a residual."""
     if y is None:
         _dims(x, 2, "x")
-        y = torch.empty_like(x, dtype=_E4M3 if eight_bit else None, memory_format=torch.contiguous_format)
+        y = _new(lambda: torch.empty_like(x, dtype=_E4M3 if eight_bit else None, memory_format=torch.contiguous_format),
+                 stream, x.device)
     if eight_bit and scale is None:
-        scale = torch.empty(_dims(x, 2, "x")[0], dtype=_F32, device=x.device)
+        rows = _dims(x, 2, "x")[0]
+        scale = _new(lambda: torch.empty(rows, dtype=_F32, device=x.device), stream, x.device)
     if residual is not None and residual_out is None:
         _dims(x, 2, "x")
-        residual_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        residual_out = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, x.device)
     st = (_calls or _load()).rms_norm_fused(x, weight, residual, eps, eight_bit, y, scale, residual_out,
                                             stream if stream is None else _stream_handle(stream))
     if st:
@@ -95,7 +111,8 @@ def gemm_fused(B, A, c=None, out_dtype=None, alpha: float = 1.0, beta: float = 1
     for the call's stream.  Returns c (m, n)."""
     if c is None:
         rows, cols = _dims(A, 2, "A")[0], _dims(B, 2, "B")[0]
-        c = torch.empty((rows, cols), dtype=out_dtype or (_BF16 if A.dtype is _E4M3 else A.dtype), device=A.device)
+        dtype = out_dtype or (_BF16 if A.dtype is _E4M3 else A.dtype)
+        c = _new(lambda: torch.empty((rows, cols), dtype=dtype, device=A.device), stream, A.device)
     elif out_dtype is not None and c.dtype is not out_dtype:
         raise TypeError(f"c must be {out_dtype}, got {c.dtype}")
     st = (_calls or _load()).gemm_fused(B, A, c, alpha, beta, scale_a, scale_b, bias, GEMM_ACTIVATIONS[activation],
@@ -126,10 +143,10 @@ def gated_scan(x, g, h0=None, h=None, state=None, stream=None):
     Returns (h, state)."""
     if h is None:
         _dims(x, 3, "x")
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, x.device)
     if state is None:
         batch, _, width = _dims(x, 3, "x")
-        state = torch.empty((batch, width), dtype=_F32, device=x.device)
+        state = _new(lambda: torch.empty((batch, width), dtype=_F32, device=x.device), stream, x.device)
     st = (_calls or _load()).gated_scan(x, g, h0, h, state, stream if stream is None else _stream_handle(stream))
     if st:
         _check(st, "gated_scan")
@@ -142,13 +159,13 @@ def gated_scan_backward(dh, g, h, h0=None, dstate=None, dx=None, dg=None, dh0=No
     and from the forward call.  Returns (dx, dg, dh0)."""
     if dx is None:
         _dims(dh, 3, "dh")
-        dx = torch.empty_like(dh, memory_format=torch.contiguous_format)
+        dx = _new(lambda: torch.empty_like(dh, memory_format=torch.contiguous_format), stream, dh.device)
     if dg is None:
         _dims(dh, 3, "dh")
-        dg = torch.empty_like(dh, memory_format=torch.contiguous_format)
+        dg = _new(lambda: torch.empty_like(dh, memory_format=torch.contiguous_format), stream, dh.device)
     if dh0 is None:
         batch, _, width = _dims(dh, 3, "dh")
-        dh0 = torch.empty((batch, width), dtype=_F32, device=dh.device)
+        dh0 = _new(lambda: torch.empty((batch, width), dtype=_F32, device=dh.device), stream, dh.device)
     st = (_calls or _load()).gated_scan_backward(dh, g, h, h0, dstate, dx, dg, dh0,
                                                  stream if stream is None else _stream_handle(stream))
     if st:

@@ -97,3 +97,59 @@ def test_copies_in_a_graph(cuda_dev, m, n, k, off):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.double(), want)
+
+
+def _calls(dev):
+    """name -> (call(stream) -> outputs that the call allocates, the value that each
+    holds throughout); the inputs are made here."""
+    ones = torch.ones((64, 512), device=dev)
+    weight, zeros = ones[0], torch.zeros((64, 512), device=dev)
+    eye = torch.eye(256, device=dev).to(torch.bfloat16)
+    others = 1 - eye
+    steps, reset = torch.ones((2, 64, 256), device=dev), torch.full((2, 64, 256), float("-inf"), device=dev)
+    return {
+        "norm": (lambda s: g.rms_norm_fused(ones, weight, residual=zeros, eps=0.0, stream=s)[::2], (1, 1)),
+        "norm_8": (lambda s: g.rms_norm_fused(ones, weight, eps=0.0, eight_bit=True, stream=s)[:2], (448, 1 / 448)),
+        "gemm": (lambda s: (g.gemm_fused(eye, eye, residual=others, stream=s),), (1,)),
+        "scan": (lambda s: g.gated_scan(steps, reset, stream=s), (1, 1)),
+        "grad": (lambda s: g.gated_scan_backward(steps, reset, steps, stream=s), (1, 0, 0)),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm_8", "gemm", "scan", "grad"])
+def test_outputs_do_not_take_pending_memory(cuda_dev, name):
+    """Blocks of the outputs' sizes, freed while the current stream has still to read
+    them, keep their contents when a call on another stream allocates its outputs."""
+    call, want = _calls(cuda_dev)[name]
+    side = torch.cuda.Stream()
+    sizes = [t.numel() * t.element_size() for t in call(None)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    temporary = [torch.full((size,), 7, dtype=torch.uint8, device=cuda_dev) for size in sizes]
+    torch.cuda._sleep(DELAY)
+    kept = [t.clone() for t in temporary]
+    del temporary
+    gc.collect()
+    out = call(side)
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in kept)
+    for t, v in zip(out, want):
+        assert ((t.double() - v).abs() <= 1e-6 * v).all(), name
+
+
+def test_outputs_outlive_their_readers(cuda_dev):
+    """An output freed while the current stream has still to read it is not handed
+    out again on the call's stream."""
+    call, _ = _calls(cuda_dev)["gemm"]
+    side = torch.cuda.Stream()
+    call(side)
+    torch.cuda.synchronize()
+    (out,) = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(DELAY)
+    kept = out.clone()
+    del out
+    with torch.cuda.stream(side):
+        overwritten = torch.full((256, 256), 5, dtype=torch.bfloat16, device=cuda_dev)
+    torch.cuda.synchronize()
+    assert (kept == 1).all() and (overwritten == 5).all()
