@@ -982,12 +982,26 @@ int64_t operand_space(const void *p, int64_t rows, int64_t k_bytes, int64_t ld_b
   return (rows * aligned_pitch(k_bytes) + 255) / 256 * 256;
 }
 
+// The copies of unaligned operands that come before a product.
+struct GemmCopies {
+  AlignParams p;
+  int64_t blocks;  // 0: none
+  int loads;
+};
+
+// The copies and the product, once nothing but the launches can fail.
 template <class P>
-int launch_gemm(void (*fn)(P), const P &p, int64_t grid, const GemmPlan &plan, cudaStream_t stream) {
+int launch_gemm(void (*fn)(P), const P &p, int64_t grid, const GemmPlan &plan, const GemmCopies &copies,
+                cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlone);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return cuda_failure((int)e);
+  }
+  if (copies.blocks > 0) {
+    const int st = launch_op(copies.loads == 4 ? gemm_align_kernel<4> : gemm_align_kernel<2>,
+                             dim3((unsigned)copies.blocks), kAlignThreads, 0, 1, stream, copies.p);
+    if (st != GEMV_OK) return st;
   }
   return launch_op(fn, dim3((unsigned)grid), plan.pair ? kPairThreads : kSplitThreads, (size_t)plan.smem,
                    plan.pair ? 2 : plan.splits, stream, p);
@@ -1093,22 +1107,23 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   p.pitch = (uint32_t)(ldb * es) & 15;
   // operands that TMA cannot read in place, copied with rows that it can
   int64_t ldb_bytes = ldb * es, lda_bytes = lda * es;
+  GemmCopies copies = {};
   if (space > 0) {
-    AlignParams ap = {};
+    AlignParams &ap = copies.p;
     char *to = static_cast<char *>(workspace);
     int jobs = 0;
-    const int loads = space > (16 << 20) ? 4 : 2;
-    auto copy = [&](const void **from, int64_t rows, int64_t *ld, int64_t pitch, int copies) {
+    const int loads = copies.loads = space > (16 << 20) ? 4 : 2;
+    auto copy = [&](const void **from, int64_t rows, int64_t *ld, int64_t pitch, int times) {
       AlignJob &job = ap.job[jobs++];
       job = {static_cast<const char *>(*from), to, *ld, k * es, pitch, rows, cdiv64(pitch, loads * 512), 0, 0, 0};
-      job.total = copies * rows * job.pieces;
+      job.total = times * rows * job.pieces;
       if (shift.classes) {
         job.class_base = p.base;
         job.class_pitch = p.pitch;
       }
       *from = to;
       *ld = pitch;
-      to += (copies * rows * pitch + 255) / 256 * 256;
+      to += (times * rows * pitch + 255) / 256 * 256;
     };
     if (shift.classes) {
       copy(&A, m, &lda_bytes, shift.pitch, shift.classes);
@@ -1118,9 +1133,7 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
     }
     const int64_t blocks = cdiv64(ap.job[0].total + ap.job[1].total, kAlignThreads / 32);
     ap.b_in_place = shift.classes ? 1 : 0;
-    st = launch_op(loads == 4 ? gemm_align_kernel<4> : gemm_align_kernel<2>,
-                   dim3((unsigned)(blocks < 64ll * sms ? blocks : 64ll * sms)), kAlignThreads, 0, 1, stream, ap);
-    if (st != GEMV_OK) return st;
+    copies.blocks = blocks < 64ll * sms ? blocks : 64ll * sms;
   }
   bool mapped = true;
   if (shift.classes) {
@@ -1139,9 +1152,9 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   int64_t grid = tiles * p.splits;
   if (pair) grid = 2 * (tiles < sms / 2 ? tiles : sms / 2);
   if (shift.classes)
-    return launch_gemm(e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>, p, grid, plan, stream);
+    return launch_gemm(e4m3 ? gemm_split_kernel<true, true> : gemm_split_kernel<false, true>, p, grid, plan, copies, stream);
   if (pair)
-    return launch_gemm<GemmParams>(e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>, p, grid, plan, stream);
+    return launch_gemm<GemmParams>(e4m3 ? gemm_pair_kernel<true> : gemm_pair_kernel<false>, p, grid, plan, copies, stream);
   return launch_gemm<GemmParams>(e4m3 ? gemm_split_kernel<true, false> : gemm_split_kernel<false, false>, p, grid, plan,
-                                 stream);
+                                 copies, stream);
 }
