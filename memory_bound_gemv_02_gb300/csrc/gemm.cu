@@ -353,6 +353,18 @@ __device__ __forceinline__ uint4 keep_bytes(const uint4 &v, int from, int to) {
                     keep_bytes(v.w, from - 12, to - 12));
 }
 
+// 16 bytes that are read once.  The operands may be what the preceding kernel
+// wrote: a coherent load, in the order that the source has it, after
+// wait_for_predecessor().
+__device__ __forceinline__ uint4 load_once(uintptr_t at) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(at)
+               : "memory");
+  return v;
+}
+
 // A warp copies a piece: 512 bytes of a row at a time, read as the aligned
 // 16-byte blocks that hold them (a lane's upper block is its neighbour's lower
 // one).  Memory-bound for B: it reads and writes the operand once.  For A's
@@ -386,8 +398,8 @@ __global__ void __launch_bounds__(kAlignThreads, 4) gemm_align_kernel(AlignParam
 #pragma unroll
     for (int u = 0; u < LOADS; ++u) {
       const uintptr_t at = block + (uintptr_t)(u * 512);
-      lo[u] = at < end && at + 16 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at)) : zero4();
-      up[u] = lane == 31 && at + 16 < end && at + 32 > start ? ldg_stream(reinterpret_cast<const uint4 *>(at + 16)) : zero4();
+      lo[u] = at < end && at + 16 > start ? load_once(at) : zero4();
+      up[u] = lane == 31 && at + 16 < end && at + 32 > start ? load_once(at + 16) : zero4();
     }
 #pragma unroll
     for (int u = 0; u < LOADS; ++u) {

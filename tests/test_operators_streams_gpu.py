@@ -99,6 +99,26 @@ def test_copies_in_a_graph(cuda_dev, m, n, k, off):
         assert torch.equal(out.double(), want)
 
 
+@pytest.mark.parametrize("m,n,k,off", UNALIGNED)
+def test_copies_read_what_the_kernel_before_wrote(cuda_dev, m, n, k, off):
+    """A product over unaligned vectors that the call just before it, a norm, writes:
+    the copy kernel starts early and must not read them before they are there."""
+    _, B = _whole(m, n, k, torch.bfloat16, cuda_dev, off)
+    signs = torch.randint(0, 2, (m, k), device=cuda_dev).to(torch.bfloat16) * 2 - 1
+    weight = torch.ones(k, device=cuda_dev)
+    y, out = torch.zeros((m, k), dtype=torch.bfloat16, device=cuda_dev), torch.empty((m, n), device=cuda_dev)
+    inputs = [signs, -signs] * 4
+    wants = [s.double() @ B.double().t() for s in inputs[:2]]
+    outs = [torch.empty_like(out) for _ in inputs]
+    torch.cuda.synchronize()
+    for s, c in zip(inputs, outs):  # rows of +-1: the norm gives them back
+        g.rms_norm_fused(s, weight, eps=0.0, y=y)
+        g.gemm_fused(B, y, c)
+    torch.cuda.synchronize()
+    for i, c in enumerate(outs):
+        assert torch.equal(c.double(), wants[i % 2])
+
+
 def _calls(dev):
     """name -> (call(stream) -> outputs that the call allocates, the value that each
     holds throughout); the inputs are made here."""
