@@ -1056,12 +1056,14 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
   gemm_epilogue ep = {};
   ep.alpha = 1.f;
   if (epilogue != nullptr) ep = *epilogue;
+  if (!ep.residual) ep.ldr = n;  // means nothing then
   if (ep.activation < GEMV_ACT_NONE || ep.activation > GEMV_ACT_LOG_SIGMOID) return GEMV_ERR_ARG;
   if (ep.bias && ep.bias_dtype != GEMV_TYPE_F32 && ep.bias_dtype != out_dtype) return GEMV_ERR_ARG;
   if (ep.residual && (ep.ldr < n || !span_fits(m, ep.ldr))) return GEMV_ERR_ARG;
   if (m == 0 || n == 0) return GEMV_OK;
   if (!C || (k > 0 && (!A || !B))) return GEMV_ERR_ARG;
   const int es = type_bytes(dtype), oe = type_bytes(out_dtype);
+  if (m > 1 && (ldc > ep.ldr ? ldc : ep.ldr) * oe > (int64_t)UINT32_MAX) return GEMV_ERR_ARG;
   const int be = ep.bias && ep.bias_dtype == GEMV_TYPE_F32 ? 4 : oe;
   if (k > 0 && ((uintptr_t)A | (uintptr_t)B) % (uintptr_t)es) return GEMV_ERR_ALIGN;
   if (((uintptr_t)C | (uintptr_t)ep.residual) % (uintptr_t)oe || (uintptr_t)ep.bias % (uintptr_t)be ||
@@ -1089,7 +1091,6 @@ extern "C" int gemm_fused(const void *B, int64_t ldb, const void *A, int64_t lda
                        workspace}))
     return GEMV_ERR_DEVICE;
   if (m == 1) ldc = ep.ldr = n;
-  if ((ldc > ep.ldr ? ldc : ep.ldr) * oe > (int64_t)UINT32_MAX) return GEMV_ERR_ARG;
   ShiftedParams p = {};
   p.C = C;
   p.ldc = ldc; p.ldr = ep.ldr;
