@@ -18,8 +18,9 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 // Rows whose squares overflow fp32 (or nearly vanish in it) are scaled by a
-// power of two for their statistics.
-constexpr float kShrink = 0x1p-64f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
+// power of two for their statistics.  Shrunk, the largest element is 2^32 and the
+// squares of a row of any length add up within range.
+constexpr float kShrink = 0x1p-96f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
 constexpr int kUnits = 2;             // 16-byte units per thread and row,
 constexpr int kMaxRowThreads = 1024;  // at 64 registers a thread
 constexpr int kSmallThreads = 256;   // of CTAs that hold several rows
