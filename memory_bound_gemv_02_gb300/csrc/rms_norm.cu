@@ -21,6 +21,7 @@ constexpr float kE4m3Max = 448.f;
 // power of two for their statistics.  Shrunk, the largest element is 2^32 and the
 // squares of a row of any length add up within range.
 constexpr float kShrink = 0x1p-96f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
+constexpr float kSmallTop = 0x1p-100f, kLeastTop = 0x1p-119f;  // max|s w| that calls for lift_of(); 448 / it is finite
 constexpr int kUnits = 2;             // 16-byte units per thread and row,
 constexpr int kMaxRowThreads = 1024;  // at 64 registers a thread
 constexpr int kSmallThreads = 256;   // of CTAs that hold several rows
@@ -174,15 +175,32 @@ __device__ __forceinline__ float rescale(float sum) {
   return isinf(sum) ? kShrink : sum < kSmallSum ? kGrow : 1.f;
 }
 
+// The 8-bit form needs max|s w| itself.  Where that leaves fp32's range, or falls so
+// low that 448 / max would (weights of 1e-37 or of 1e30 do either), s is scaled once
+// more, by a power of two: by 2^60 or 2^-60 of what the sum of squares says s is, so
+// that s stays within 2^61 and the products come within range.  Its exponent, 0
+// where nothing is to be done (a row of zeros, NaN or infinities in s).
+__device__ __forceinline__ int exponent_of(float v) { return (int)(__float_as_uint(v) >> 23) - 127; }  // v >= 0
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
+__device__ __forceinline__ bool top_in_range(float top) { return top >= kSmallTop && top < __int_as_float(0x7f800000); }
+__device__ __forceinline__ int lift_of(float pre, float sum, float top) {
+  const bool small = top < kSmallTop && (top > 0.f || sum > 0.f);
+  if (!small && !(isinf(top) && !isinf(sum))) return 0;
+  const int root = exponent_of(sum) / 2;
+  // pre times 2^lift is a float too
+  return small ? min(60 - root, 120 - exponent_of(pre)) : max(-60 - root, -140 - exponent_of(pre));
+}
+
+// top: of s scaled by `pre` and 2^lift.
 template <bool EIGHT>
-__device__ __forceinline__ RowFactors row_factors(float pre, float sum, float top, int64_t d, float eps) {
+__device__ __forceinline__ RowFactors row_factors(float pre, int lift, float sum, float top, int64_t d, float eps) {
   const float rstd = rsqrtf(sum / (float)d + eps * pre * pre);  // pre is a power of two: exact
   RowFactors f{rstd, 0.f};
   if (EIGHT) {
     // top is max|t|: a row of zeros has scale 1; one with a NaN or an
     // infinity (rstd 0) has no scale.
-    f.scale = top == 0.f ? 1.f : top * rstd / kE4m3Max;
-    f.mul = top == 0.f ? 0.f : isinf(top) ? __int_as_float(0x7fc00000) : kE4m3Max / top;
+    f.scale = top == 0.f ? 1.f : top * rstd / kE4m3Max * power_of_two(-lift);
+    f.mul = top == 0.f ? 0.f : isinf(top) ? __int_as_float(0x7fc00000) : kE4m3Max / max_nan(top, kLeastTop);
   }
   return f;
 }
@@ -256,12 +274,21 @@ __global__ void __launch_bounds__(kSmallThreads) rms_norm_small_kernel(NormParam
       for (int e = 0; e < V; ++e) s[e] *= pre;
       reduce();
     }
-    const RowFactors g = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
+    int lift = 0;
+    if (EIGHT && __any_sync(0xffffffffu, !top_in_range(top))) {  // as rare
+      lift = lift_of(pre, sum, top);
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] *= power_of_two(lift);
+      const float kept = sum;
+      reduce();
+      sum = kept;
+    }
+    const RowFactors g = row_factors<EIGHT>(pre, lift, sum, top, p.d, p.eps);
     if (EIGHT && u == 0 && in) p.scale[row] = g.scale;
     if (in) {
       float y[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = (s[e] * w[e]) * g.mul;
+      for (int e = 0; e < V; ++e) y[e] = EIGHT ? (s[e] * w[e]) * g.mul : (s[e] * g.mul) * w[e];
       store_y<TYPE, EIGHT>(SHIFT ? row_y : static_cast<char *>(p.y) + row * p.ldy * OE, u, y);
     }
     if constexpr (SHIFT) {
@@ -288,7 +315,7 @@ constexpr int64_t kHalfSm = 110 * 1024, kWholeSm = 224 * 1024;  // shared memory
 // aligned blocks that cover its row, and a row's outputs are staged in the
 // memory of its inputs.
 template <int TYPE, bool EIGHT, bool SHIFT>
-__global__ void __launch_bounds__(kMaxRowThreads) rms_norm_ring_kernel(NormParams p) {
+__global__ void __launch_bounds__(kMaxRowThreads, 1) rms_norm_ring_kernel(NormParams p) {
   using E = Elem<TYPE>;
   typedef typename E::raw raw;
   constexpr int V = E::VEC, ES = (int)sizeof(raw), OE = EIGHT ? 1 : ES, N = kUnits;
@@ -418,15 +445,28 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_ring_kernel(NormParam
       }
     }
     const float pre = rescale(sum);
-    if (pre != 1.f) {  // rare: squares beyond fp32's range
+    int lift = 0;
+    if (pre != 1.f || (EIGHT && !top_in_range(top))) {  // rare: beyond fp32's range
+      float by = pre;
+#pragma unroll 1
+      for (;;) {
+        if (by != 1.f) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
+          for (int i = 0; i < N; ++i) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[i][e] *= pre;
+            for (int e = 0; e < V; ++e) s[i][e] *= by;
+          }
+          const float kept = sum;
+          reduce();
+          if (lift != 0) sum = kept;
+        }
+        if (!EIGHT || lift != 0 || top_in_range(top)) break;
+        lift = lift_of(pre, sum, top);
+        if (lift == 0) break;
+        by = power_of_two(lift);
       }
-      reduce();
     }
-    const RowFactors f = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
+    const RowFactors f = row_factors<EIGHT>(pre, lift, sum, top, p.d, p.eps);
     if (EIGHT && tid == 0) p.scale[row] = f.scale;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -436,8 +476,13 @@ __global__ void __launch_bounds__(kMaxRowThreads) rms_norm_ring_kernel(NormParam
       load_weights(u, w);
 #pragma unroll
       for (int e = 0; e < V; e += 2) {
-        mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
-        mul2(y[e], y[e + 1], y[e], y[e + 1], f.mul, f.mul);
+        if constexpr (EIGHT) {
+          mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+          mul2(y[e], y[e + 1], y[e], y[e + 1], f.mul, f.mul);
+        } else {  // s / rms first: neither it nor the product leaves the range that y has
+          mul2(y[e], y[e + 1], s[i][e], s[i][e + 1], f.mul, f.mul);
+          mul2(y[e], y[e + 1], y[e], y[e + 1], w[e], w[e + 1]);
+        }
       }
       store_y<TYPE, EIGHT>(SHIFT ? from_r : static_cast<char *>(p.y) + row * p.ldy * OE, u, y);
     }
@@ -496,8 +541,8 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
         for (int e = 0; e < V; ++e) w[e] = static_cast<const float *>(p.w)[u * V + e];
       }
     };
-    float sum, top, pre = 1.f;
-    for (;;) {
+    float sum, top;
+    auto reduce = [&](const float by) {
       sum = top = 0.f;
 #pragma unroll 4
       for (int64_t u = threadIdx.x; u < units; u += kLongThreads) {
@@ -506,18 +551,33 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
         if (EIGHT) weights(u, w);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          s[e] *= pre;
+          s[e] *= by;
           sum = fmaf(s[e], s[e], sum);
           if (EIGHT) top = max_nan(top, fabsf(s[e] * w[e]));
         }
       }
       row_reduce<EIGHT>(sum, top, kLongThreads, part[turn]);
       turn ^= 1;
-      if (pre != 1.f) break;
-      pre = rescale(sum);
-      if (pre == 1.f) break;
+    };
+    reduce(1.f);
+    const float pre = rescale(sum);
+    float by = pre;
+    int lift = 0;
+    if (pre != 1.f || (EIGHT && !top_in_range(top))) {  // rare: beyond fp32's range
+#pragma unroll 1
+      for (;;) {
+        if (by != 1.f || lift != 0) {
+          const float kept = sum;
+          reduce(by);
+          if (lift != 0) sum = kept;
+        }
+        if (!EIGHT || lift != 0 || top_in_range(top)) break;
+        lift = lift_of(pre, sum, top);
+        if (lift == 0) break;
+        by = pre * power_of_two(lift);
+      }
     }
-    const RowFactors f = row_factors<EIGHT>(pre, sum, top, p.d, p.eps);
+    const RowFactors f = row_factors<EIGHT>(pre, lift, sum, top, p.d, p.eps);
     if (EIGHT && threadIdx.x == 0) p.scale[row] = f.scale;
     raw *ro = p.ro ? static_cast<raw *>(p.ro) + row * p.ldo : nullptr;
 #pragma unroll 2
@@ -526,7 +586,8 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
       values(u, s);
       weights(u, w);
 #pragma unroll
-      for (int e = 0; e < V; ++e) y[e] = ((s[e] * pre) * w[e]) * f.mul;
+      for (int e = 0; e < V; ++e)
+        y[e] = EIGHT ? ((s[e] * by) * w[e]) * f.mul : ((s[e] * by) * f.mul) * w[e];
       if constexpr (VECTOR) {
         if (ro) reinterpret_cast<uint4 *>(ro)[u] = E::pack(s);
         if constexpr (!EIGHT) {

@@ -26,7 +26,9 @@ def _check(x, w, r, eps, label):
     y64, s64 = ref.rms_norm(x, w, r, eps)
     assert torch.isfinite(s64.float()).all()  # the sums are within range
     rel = ref.rms_norm_rel(x.shape[1])
-    ref.check(y, y64, rel * y64.abs() + ref.half_ulp(y64, y.dtype) + 2 * TINY, f"{label} y")
+    beyond = torch.isinf(y64.to(y.dtype))  # a norm that its type rounds to an infinity
+    y_out = torch.where(beyond, y64.to(y.dtype).double(), y64)
+    ref.check(y, y_out, rel * y64.abs() + ref.half_ulp(y64, y.dtype) + 2 * TINY, f"{label} y")
     peak = y64.abs().amax(dim=1)
     want = torch.where(peak == 0, 1.0, peak / 448)
     ref.check(scale, want, 2 * rel * want + 2 * TINY, f"{label} scale")
@@ -49,3 +51,21 @@ def test_rows_near_the_largest_value(cuda_dev, dtype, d):
     x = ref.uniform((2, d), dtype, 4, cuda_dev, -1, 1)
     x[:, d // 2] = 3.0e38
     _check(x, w, None, 1e-6, "one large")
+
+
+@pytest.mark.parametrize("dtype", [torch.float16] + WIDE)
+@pytest.mark.parametrize("wdtype", WIDE)
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("size,weight", [(1.0, 1e-37), (1.0, 1e-40), (2e-3, 1e-36), (1e-12, 1e-37), (1e-30, 1e-30),
+                                         (1e20, 1e30), (3e38, 1e30), (1e18, 1e-38), (3.3e38, 1.6e38), (3.3e38, 1e-40)])
+def test_weights_near_the_ends_of_the_range(cuda_dev, dtype, wdtype, d, size, weight):
+    """s w leaves fp32's range, or 448 / max|s w| does; s / rms times w does not."""
+    if wdtype not in (dtype, torch.float32) or (dtype == torch.float16 and not 1e-3 <= size <= 1e4):
+        pytest.skip("not a combination of types, or not a value of x's type")
+    x = (ref.uniform((4, d), torch.float32, 5, cuda_dev, -1, 1) * size).to(dtype)
+    x[1, ::2] = 0
+    w = (ref.uniform((d,), torch.float32, 6, cuda_dev, 0.25, 1) * weight).to(wdtype)
+    _check(x, w, None, 0.0 if 1e-13 <= size <= 1e37 else 1e-6, f"{size} {weight}")
+    w[::3] = 0
+    w[-1] = 1.5 * weight
+    _check(x, w, None, 1e-6, f"{size} {weight}, some weights 0")
