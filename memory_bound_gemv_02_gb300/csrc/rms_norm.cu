@@ -19,8 +19,10 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 // Rows whose squares overflow fp32 (or nearly vanish in it) are scaled by a
 // power of two for their statistics.  Shrunk, the largest element is 2^32 and the
-// squares of a row of any length add up within range.
-constexpr float kShrink = 0x1p-96f, kGrow = 0x1p40f, kSmallSum = 0x1p-80f;
+// squares of a row of any length add up within range.  Grown by 2^40, squares that
+// still vanish are nothing beside eps times 2^80; with an eps too small for that
+// it is by 2^100, where no value's square vanishes.
+constexpr float kShrink = 0x1p-96f, kGrow = 0x1p40f, kGrowMore = 0x1p100f, kSmallSum = 0x1p-80f, kSmallEps = 0x1p-80f;
 constexpr float kSmallTop = 0x1p-100f, kLeastTop = 0x1p-119f;  // max|s w| that calls for lift_of(); 448 / it is finite
 constexpr int kUnits = 2;             // 16-byte units per thread and row,
 constexpr int kMaxRowThreads = 1024;  // at 64 registers a thread
@@ -171,8 +173,8 @@ struct RowFactors {
 };
 
 // The factor that brings a row's squares into fp32's range (1 nearly always).
-__device__ __forceinline__ float rescale(float sum) {
-  return isinf(sum) ? kShrink : sum < kSmallSum ? kGrow : 1.f;
+__device__ __forceinline__ float rescale(float sum, float eps) {
+  return isinf(sum) ? kShrink : sum < kSmallSum ? (eps < kSmallEps ? kGrowMore : kGrow) : 1.f;
 }
 
 // The 8-bit form needs max|s w| itself.  Where that leaves fp32's range, or falls so
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kSmallThreads) rms_norm_small_kernel(NormParam
       if (SHIFT) reinterpret_cast<uint4 *>(row_s)[u] = E::pack(s);
       else reinterpret_cast<uint4 *>(static_cast<raw *>(p.ro) + row * p.ldo)[u] = E::pack(s);
     }
-    const float pre = rescale(sum);
+    const float pre = rescale(sum, p.eps);
     if (__any_sync(0xffffffffu, pre != 1.f)) {  // rare; lanes reduce together whichever row needs it
 #pragma unroll
       for (int e = 0; e < V; ++e) s[e] *= pre;
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(kMaxRowThreads, 1) rms_norm_ring_kernel(NormPa
         else reinterpret_cast<uint4 *>(static_cast<raw *>(p.ro) + row * p.ldo)[u] = E::pack(s[i]);
       }
     }
-    const float pre = rescale(sum);
+    const float pre = rescale(sum, p.eps);
     int lift = 0;
     if (pre != 1.f || (EIGHT && !top_in_range(top))) {  // rare: beyond fp32's range
       float by = pre;
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(kLongThreads) rms_norm_long_kernel(NormParams 
       turn ^= 1;
     };
     reduce(1.f);
-    const float pre = rescale(sum);
+    const float pre = rescale(sum, p.eps);
     float by = pre;
     int lift = 0;
     if (pre != 1.f || (EIGHT && !top_in_range(top))) {  // rare: beyond fp32's range

@@ -69,3 +69,15 @@ def test_weights_near_the_ends_of_the_range(cuda_dev, dtype, wdtype, d, size, we
     w[::3] = 0
     w[-1] = 1.5 * weight
     _check(x, w, None, 1e-6, f"{size} {weight}, some weights 0")
+
+
+@pytest.mark.parametrize("dtype", WIDE)
+@pytest.mark.parametrize("d", WIDTHS)
+@pytest.mark.parametrize("size", [1e-12, 1e-24, 1e-32, 1e-36, 1e-38, 1e-40])
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-30, 1e-24, 1e-20, 1e-6])
+def test_rows_near_the_smallest_value(cuda_dev, dtype, d, size, eps):
+    """Squares that vanish in fp32, with an eps that does not count, or does."""
+    x = (ref.uniform((4, d), torch.float32, 7, cuda_dev, 0.25, 1) * size).to(dtype)
+    x[1, 1::2] = 0
+    w = ref.uniform((d,), dtype, 8, cuda_dev, 0.5, 1.5)
+    _check(x, w, None, eps, f"{size} {eps}")
