@@ -147,7 +147,8 @@ int gemm_workspace(const void *B, int64_t ldb, const void *A, int64_t lda, int64
  *     h[t] = exp(g[t]) * h[t-1] + x[t]     (0 <= t < steps, h[-1] = h0)
  *
  * in fp32; h is rounded once per element when stored, the carried state is not
- * rounded.  A g of minus infinity (or below -87.3, where the exponential leaves
+ * rounded.  A decay exp(g) is within 4 units of 2^-24, relative, with 16-bit
+ * storage within 4 + 1.25 |g|.  A g of minus infinity (or below -87.3, where the exponential leaves
  * fp32's normal range) drops what came before, whatever it holds: tokens of packed documents do not
  * see one another, NaN and infinities included.
  *

@@ -59,29 +59,46 @@ __device__ __forceinline__ float decayed(float a, float v) { return a == 0.f ? 0
 // its series (the next term is below 6e-9 relative): within 0.6 u and without
 // the bias of a third of a unit per step that the special function unit's 2^t
 // has there, which gave the last state of 8192 steps 1.6e-6 of relative error
-// instead of 2e-7.  Elsewhere in two instructions, zero below the normal range.
+// instead of 2e-7.  Elsewhere 2^t with t = g log2(e), zero below the normal range.
+//
+// t's rounding, and the constant's, are up to 1.25 |g| u of the result, 65 u at -87.
+// What is proportional to one decay (dg, dh0, a state that nothing is added to)
+// shows it in fp32, so there (FULL) the part of g log2(e) that t has not is put
+// back: within 4 u everywhere, for 4 x 4096 x 4096 120.5 -> 122 us forward, 1 x 65536 x
+// 1024 121.5 -> 129.  With 16-bit storage, whose rounding is 2^15 u or more, it is
+// left out: 4 x 8192 x 4096 bf16 would take 147 us instead of 128.
 constexpr float kLog2e = 1.4426950408889634f, kNearOne = 0.125f;
+constexpr float kLog2eRest = 1.92596299e-8f, kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_fast(float t) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return r;
 }
+template <bool FULL>
 __device__ __forceinline__ void decay2(float &g0, float &g1) {
   float t0, t1, p0, p1;
   mul2(t0, t1, g0, g1, kLog2e, kLog2e);
-  t0 = exp2_fast(t0);
-  t1 = exp2_fast(t1);
+  float e0 = exp2_fast(t0), e1 = exp2_fast(t1);
+  if constexpr (FULL) {
+    fma2(t0, t1, g0, g1, kLog2e, kLog2e, -t0, -t1);
+    fma2(t0, t1, g0, g1, kLog2eRest, kLog2eRest, t0, t1);
+    fma2(t0, t1, t0, t1, kLn2, kLn2, 1.f, 1.f);
+    // 1 within 2e-5, but for infinities, a type's lowest value and the like, whose
+    // power is 0 or infinite and has to stay so
+    mul2(e0, e1, e0, e1, fminf(fabsf(t0), 2.f), fminf(fabsf(t1), 2.f));
+  }
   fma2(p0, p1, g0, g1, 1.f / 120, 1.f / 120, 1.f / 24, 1.f / 24);
   fma2(p0, p1, g0, g1, p0, p1, 1.f / 6, 1.f / 6);
   fma2(p0, p1, g0, g1, p0, p1, 0.5f, 0.5f);
   fma2(p0, p1, g0, g1, p0, p1, 1.f, 1.f);
   fma2(p0, p1, g0, g1, p0, p1, 1.f, 1.f);
-  g0 = fabsf(g0) < kNearOne ? p0 : t0;
-  g1 = fabsf(g1) < kNearOne ? p1 : t1;
+  g0 = fabsf(g0) < kNearOne ? p0 : e0;
+  g1 = fabsf(g1) < kNearOne ? p1 : e1;
 }
+template <bool FULL>
 __device__ __forceinline__ float decay(float g) {
   float other = 0.f;
-  decay2(g, other);
+  decay2<FULL>(g, other);
   return g;
 }
 
@@ -142,6 +159,7 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
   using L = Lane<TYPE, VECTOR>;
   typedef typename L::raw raw;
   constexpr int V = L::V, U = 4;
+  constexpr bool kFull = TYPE == GEMV_TYPE_F32;
   allow_dependents();
   wait_for_predecessor();
   const int64_t per_row = p.width / V, i = (int64_t)blockIdx.x * kWalkThreads + threadIdx.x;
@@ -177,7 +195,7 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float a = decay(gf[e]);
+          const float a = decay<kFull>(gf[e]);
           out[e] = v[e] + xf[e];
           v[e] = decayed(a, out[e]);
           dg[e] = a == 0.f ? 0.f : v[e] * hf[e];
@@ -186,7 +204,7 @@ __global__ void __launch_bounds__(kWalkThreads) gated_walk_kernel(ScanParams p) 
         L::store(at<raw>(p.dg, b, t, c), dg);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = advance<false>(decay(gf[e]), v[e], xf[e]);
+        for (int e = 0; e < V; ++e) v[e] = advance<false>(decay<kFull>(gf[e]), v[e], xf[e]);
         L::store(at<raw>(p.h, b, t, c), v);
       }
     }
@@ -308,6 +326,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
   using S = Tile<TYPE, TMA, BACK, LANES>;
   typedef typename E::raw raw;
   constexpr int V = S::V, N = S::kSteps, ES = (int)sizeof(raw);
+  constexpr bool kFull = TYPE == GEMV_TYPE_F32;
   extern __shared__ __align__(128) char dynamic[];
   __shared__ TileShared sh;
   float *all_warp_maps = reinterpret_cast<float *>(dynamic + S::kStages * S::kStageBytes);
@@ -462,7 +481,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
 #pragma unroll
       for (int e = 0; e < V; e += 2) {
         float &a0 = a[u][e], &a1 = a[u][e + 1];
-        decay2(a0, a1);
+        decay2<kFull>(a0, a1);
         if constexpr (BACK) {
           add2(B[e], B[e + 1], B[e], B[e + 1], xf[e], xf[e + 1]);
           mul2(B[e], B[e + 1], B[e], B[e + 1], a0, a1);
@@ -488,7 +507,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
         input(u, 0, xf);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float d = decay(gf[e]);
+          const float d = decay<kFull>(gf[e]);
           B[e] = advance<BACK>(d, B[e], xf[e]);
           A[e] = chain(A[e], d);
         }
@@ -746,7 +765,7 @@ __global__ void __launch_bounds__(kScanThreads, Tile<TYPE, TMA, BACK, LANES>::kC
         float d[V];
         input(u, 1, d);
 #pragma unroll
-        for (int e = 0; e < V; ++e) d[e] = decay(d[e]);
+        for (int e = 0; e < V; ++e) d[e] = decay<kFull>(d[e]);
         step(u, d, true);
       }
     }
