@@ -886,10 +886,11 @@ int launch_scan(const ScanParams &p, int sms, uint32_t *timeouts, cudaStream_t s
   // memory's rate, the walk 60 %.)
   if (p.steps <= 4 || (p.steps <= 96 && (int64_t)p.steps * sms * 2 <= 10 * units))
     return vectors ? launch_walk<TYPE, true, BACK>(p, stream) : launch_walk<TYPE, false, BACK>(p, stream);
-  // TMA copies need strides that are not 0 (shared rows) and fit their maps.
+  // A tensor map's strides are at least a row's width (not those of shared rows or
+  // of windows that overlap) and below 2^40.
   auto mapped = [&](const Strided &s) {
-    return (p.steps == 1 || (s.step > 0 && s.step * es < (1ll << 40))) &&
-           (p.batch == 1 || (s.batch > 0 && s.batch * es < (1ll << 40)));
+    return (p.steps == 1 || (s.step >= p.width && s.step * es < (1ll << 40))) &&
+           (p.batch == 1 || (s.batch >= p.width && s.batch * es < (1ll << 40)));
   };
   const bool tma = vectors && mapped(p.x) && mapped(p.g) && (!BACK || mapped(p.h));
   if (units * kMaxScanCluster < sms)
