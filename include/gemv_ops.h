@@ -30,8 +30,10 @@
  * An output overlaps no other buffer of its call, except where an entry says
  * that it may be the very same buffer as an input; a partial overlap returns
  * GEMV_ERR_ALIAS.  Buffers whose rows interleave without sharing an element
- * (column ranges of one matrix, as two halves of a projection's output) do not
- * overlap.
+ * (column ranges of one matrix, as two halves of a projection's output; rows
+ * between another's) do not overlap, as long as their columns are apart modulo
+ * the greatest common divisor of all strides; spans that cross otherwise count
+ * as overlapping.
  */
 #ifndef GEMV_GB300_OPS_H_
 #define GEMV_GB300_OPS_H_

@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <numeric>
 
 #include "ops_internal.h"
 #include "tc_ptx.cuh"
@@ -808,17 +809,11 @@ bool rows_apart(const Strided &s, int64_t batch, int64_t steps, int64_t width) {
   return true;
 }
 
-// The buffer as rows on one pitch where its strides allow that, else as its
-// whole span.
+// Rows on one pitch that every row of the buffer is among.
 Rows as_rows(const Strided &s, int64_t batch, int64_t steps, int64_t width, int es) {
-  if (batch == 1) return Rows{s.p, steps, width * es, s.step * es};
-  if (steps == 1) return Rows{s.p, batch, width * es, s.batch * es};
-  if (s.step > 0 && s.batch % s.step == 0)
-    return Rows{s.p, (batch - 1) * (s.batch / s.step) + steps, width * es, s.step * es};
-  if (s.batch > 0 && s.step % s.batch == 0)
-    return Rows{s.p, (steps - 1) * (s.step / s.batch) + batch, width * es, s.batch * es};
-  const int64_t span = (batch - 1) * s.batch + (steps - 1) * s.step + width;
-  return Rows{s.p, 1, span * es, span * es};
+  const int64_t pitch = std::gcd(batch > 1 ? s.batch : 0, steps > 1 ? s.step : 0);
+  const int64_t last = (batch - 1) * s.batch + (steps - 1) * s.step;  // a multiple of it
+  return Rows{s.p, pitch > 0 ? last / pitch + 1 : 1, width * es, pitch * es};
 }
 
 // Whether every row of a buffer starts on 16 bytes.

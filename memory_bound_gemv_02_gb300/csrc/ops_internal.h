@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <numeric>
 
 #include "gemv_kernels.cuh"
 #include "gemv_ops.h"
@@ -101,18 +102,20 @@ struct Rows {
   int64_t rows, width, pitch;
 };
 
-// Whether two buffers share a byte.  Rows on one common pitch that lie in
-// disjoint column ranges do not; otherwise the spans from first to last byte
-// decide.
+// Whether two buffers share a byte.  Rows of both start at one place modulo the
+// greatest common divisor of their pitches (a single row has the other's): where
+// that leaves their columns apart they do not.  Otherwise the spans from first to
+// last byte decide.
 inline bool rows_overlap(const Rows &a, const Rows &b) {
   if (a.p == nullptr || b.p == nullptr || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
   const uintptr_t a0 = (uintptr_t)a.p, a1 = a0 + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
   const uintptr_t b0 = (uintptr_t)b.p, b1 = b0 + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
   if (a1 <= b0 || b1 <= a0) return false;
-  if (a.rows > 1 && b.rows > 1 && a.pitch == b.pitch && a.pitch > 0) {
-    const int64_t off = b0 >= a0 ? (int64_t)((b0 - a0) % (uintptr_t)a.pitch)
-                                 : (a.pitch - (int64_t)((a0 - b0) % (uintptr_t)a.pitch)) % a.pitch;
-    if (off >= a.width && off + b.width <= a.pitch) return false;
+  const int64_t pitch = std::gcd(a.rows > 1 ? a.pitch : 0, b.rows > 1 ? b.pitch : 0);
+  if (pitch > 0) {
+    const int64_t off = b0 >= a0 ? (int64_t)((b0 - a0) % (uintptr_t)pitch)
+                                 : (pitch - (int64_t)((a0 - b0) % (uintptr_t)pitch)) % pitch;
+    if (off >= a.width && off + b.width <= pitch) return false;
   }
   return true;
 }
