@@ -71,7 +71,7 @@ def run_blocks(blocks, x, states):
 
 
 class GatedScan(torch.autograd.Function):
-    """h = gated_scan(x, g, h0) with its gradient; returns (h, last state)."""
+    """h = gated_scan(x, g, h0) with its gradient; returns (h, last state).  h0 may be None (zero)."""
 
     @staticmethod
     def forward(ctx, x, g, h0):
@@ -83,7 +83,7 @@ class GatedScan(torch.autograd.Function):
     def backward(ctx, dh, dstate):
         g, h, h0 = ctx.saved_tensors
         dx, dg, dh0 = g300.gated_scan_backward(dh.contiguous(), g, h, h0=h0, dstate=dstate.contiguous())
-        return dx, dg, dh0
+        return dx, dg, None if h0 is None else dh0
 
 
 def main():
