@@ -7,6 +7,9 @@ nothing of torch: Python calls it through ctypes, and for the operators of
 gemv_ops.h through ``_lib/operators_py.so``, a small extension module that turns
 torch tensors into pointers, sizes and strides (host code, built against the
 installed torch and linked with the library).
+
+Run as a script, this file builds the library and the measurement tool alone,
+without torch or Python's headers.
 """
 from __future__ import annotations
 
@@ -29,6 +32,7 @@ HOST_TOOL = os.path.join(LIBDIR, "gemv_bench_tool")  # native host-overhead and 
 
 EXTENSION_SRC = "operators_py.cpp"
 EXTENSION = os.path.join(LIBDIR, "operators_py.so")
+EXTENSION_STAMP = os.path.join(LIBDIR, "operators_py.built")  # what it was built against
 
 SOURCES = ["gemv_api.cu", "gemv_kernels_f16.cu", "gemv_kernels_bf16.cu", "gemv_bulk_f16.cu", "gemv_bulk_bf16.cu",
            "gla_decode.cu", "rms_norm.cu", "gated_scan.cu", "gemm.cu"]
@@ -51,13 +55,31 @@ def nvcc() -> str:
     return cand
 
 
-def _stale() -> bool:
-    products = (LIB, HOST_TOOL, EXTENSION)
+def _older(products, sources) -> bool:
+    """Whether a product is missing or older than one of the sources."""
     if not all(os.path.exists(f) for f in products):
         return True
     t = min(os.path.getmtime(f) for f in products)
-    deps = [os.path.join(CSRC, s) for s in SOURCES + [HOST_TOOL_SRC, EXTENSION_SRC]] + HEADERS + [os.path.abspath(__file__)]
-    return any(os.path.getmtime(d) > t for d in deps)
+    return any(os.path.getmtime(d) > t for d in sources)
+
+
+def _stale_library() -> bool:
+    deps = [os.path.join(CSRC, s) for s in SOURCES + [HOST_TOOL_SRC]] + HEADERS + [os.path.abspath(__file__)]
+    return _older((LIB, HOST_TOOL), deps)
+
+
+def _extension_target() -> str:
+    """What the extension module's binary interface depends on."""
+    import torch
+    return f"torch {torch.__version__} python {sysconfig.get_config_var('SOABI')}"
+
+
+def _stale_extension() -> bool:
+    header = os.path.join(INCLUDE, "gemv_ops.h")
+    if _older((EXTENSION, EXTENSION_STAMP), (os.path.join(CSRC, EXTENSION_SRC), header, os.path.abspath(__file__))):
+        return True
+    with open(EXTENSION_STAMP) as f:
+        return f.read() != _extension_target()
 
 
 def _torch_dir() -> str:
@@ -80,49 +102,58 @@ def _compile_extension() -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile (if needed) and return the path of ``libgemv.so``."""
+def _link_extension(obj: str) -> None:
+    tmp = EXTENSION + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + LIBDIR, "-lgemv", "-Wl,-rpath,$ORIGIN",
+          "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+         "extension link failed")
+    os.replace(tmp, EXTENSION)
+    with open(EXTENSION_STAMP, "w") as f:
+        f.write(_extension_target())
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=(), extension: bool = True) -> str:
+    """Compile (if needed) and return the path of ``libgemv.so``; with
+    ``extension`` (the operators' torch entry points) the module next to it too.
+    The library is in place before the extension's errors are raised."""
     with _lock:
-        if not force and not _stale():
+        library = force or _stale_library()
+        extension = extension and (force or _stale_extension())
+        if not library and not extension:
             return LIB
         os.makedirs(OBJDIR, exist_ok=True)
         os.makedirs(LIBDIR, exist_ok=True)
-        exe = nvcc()
-
-        def compile_one(src):
-            obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
-            cmd = [exe, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
-            r = subprocess.run(cmd, capture_output=True, text=True)
-            if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
-            if verbose and (r.stdout or r.stderr):
-                print(r.stdout + r.stderr)
-            return obj
-
         with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-            extension_obj = ex.submit(_compile_extension)
-            objs = list(ex.map(compile_one, SOURCES))
-            extension_obj = extension_obj.result()
-        tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [exe, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", tmp, *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, LIB)
-        # the extension module and the native measurement tool, linked against the library just built
-        tmp = EXTENSION + f".tmp{os.getpid()}"
-        _run(["g++", "-shared", "-o", tmp, extension_obj, "-L" + LIBDIR, "-lgemv", "-Wl,-rpath,$ORIGIN",
-              "-L" + os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
-             "extension link failed")
-        os.replace(tmp, EXTENSION)
-        tmp = HOST_TOOL + f".tmp{os.getpid()}"
-        cmd = [exe, *NVCC_FLAGS, *extra_flags, os.path.join(CSRC, HOST_TOOL_SRC), "-o", tmp,
-               "-L" + LIBDIR, "-lgemv", "-Xlinker", "-rpath,$ORIGIN"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"measurement tool build failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, HOST_TOOL)
+            extension_obj = ex.submit(_compile_extension) if extension else None
+            if library:
+                _build_library(ex, verbose, extra_flags)
+            if extension:
+                _link_extension(extension_obj.result())
         return LIB
+
+
+def _build_library(ex: ThreadPoolExecutor, verbose: bool, extra_flags) -> None:
+    exe = nvcc()
+
+    def compile_one(src):
+        obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
+        cmd = [exe, *NVCC_FLAGS, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        if verbose and (r.stdout or r.stderr):
+            print(r.stdout + r.stderr)
+        return obj
+
+    objs = list(ex.map(compile_one, SOURCES))
+    tmp = LIB + f".tmp{os.getpid()}"
+    _run([exe, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", tmp, *objs], "link failed")
+    os.replace(tmp, LIB)
+    # the native measurement tool, linked against the library just built
+    tmp = HOST_TOOL + f".tmp{os.getpid()}"
+    _run([exe, *NVCC_FLAGS, *extra_flags, os.path.join(CSRC, HOST_TOOL_SRC), "-o", tmp, "-L" + LIBDIR, "-lgemv",
+          "-Xlinker", "-rpath,$ORIGIN"], "measurement tool build failed")
+    os.replace(tmp, HOST_TOOL)
 
 
 def ensure_built() -> str:
@@ -131,3 +162,7 @@ def ensure_built() -> str:
 
 def lib_path() -> str:
     return LIB
+
+
+if __name__ == "__main__":
+    print(build(extension=False))
