@@ -9,6 +9,7 @@ read or written by work queued there.
 from __future__ import annotations
 
 import gc
+import threading
 
 import pytest
 import torch
@@ -173,3 +174,86 @@ def test_outputs_outlive_their_readers(cuda_dev):
         overwritten = torch.full((256, 256), 5, dtype=torch.bfloat16, device=cuda_dev)
     torch.cuda.synchronize()
     assert (kept == 1).all() and (overwritten == 5).all()
+
+
+def _work(dev, seed):
+    """(call -> outputs) of every operator and kernel, on inputs of their own."""
+    bf16, e4m3 = torch.bfloat16, torch.float8_e4m3fn
+
+    def rand(i, *shape, dtype=bf16, lo=-1.0, hi=1.0):
+        return ref.uniform(shape, dtype, 100 * seed + i, dev, lo, hi)
+
+    def product(i, m, n, k, dtype):
+        B, A = rand(i, n, k, dtype=dtype), rand(i + 1, m, k, dtype=dtype)
+        return lambda: (g.gemm_fused(B, A, activation="silu"),)
+
+    def norm(i, rows, d, eight):
+        x, r, w = rand(i, rows, d), rand(i + 1, rows, d), rand(i + 2, d)
+        return lambda: tuple(t for t in g.rms_norm_fused(x, w, residual=r, eight_bit=eight) if t is not None)
+
+    def scan(i, b, t, d):
+        x, gate, h0 = rand(i, b, t, d), rand(i + 1, b, t, d, lo=-1.5, hi=0.0), rand(i + 2, b, d, dtype=torch.float32)
+
+        def call():
+            h, state = g.gated_scan(x, gate, h0=h0)
+            return (h, state, *g.gated_scan_backward(x, gate, h, h0=h0, dstate=state))
+        return call
+
+    return [product(1, 1, 2048, 2048, bf16), product(3, 20, 1000, 1024, e4m3), product(5, 600, 2048, 512, bf16),
+            product(7, 17, 1301, 999, bf16), product(9, 300, 700, 1001, e4m3), norm(11, 200, 4096, True),
+            norm(14, 100, 1001, False), norm(17, 900, 64, True), norm(20, 3, 40000, False), scan(23, 2, 1, 512),
+            scan(26, 1, 3000, 256), scan(29, 2, 700, 65), scan(32, 40, 300, 512)]
+
+
+def _same(a, b):
+    return all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, b))
+
+
+def test_several_streams_at_once(cuda_dev):
+    """All operators on four streams, nothing waited for between the calls: each
+    gives, to the bit, what it gives alone."""
+    work = _work(cuda_dev, 1)
+    alone = []
+    for call in work:
+        alone.append(call())
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    results = []
+    for turn in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                for j in range(len(work)):
+                    k = (j * (2 * i + 1) + turn) % len(work)
+                    results.append((k, work[k]()))
+    torch.cuda.synchronize()
+    assert all(_same(out, alone[k]) for k, out in results)
+    assert g.gemv_wait_timeouts() == 0
+
+
+def test_several_host_threads(cuda_dev):
+    """Six threads, each on a stream of its own, in different orders."""
+    work = _work(cuda_dev, 2)
+    alone = []
+    for call in work:
+        alone.append(call())
+        torch.cuda.synchronize()
+    wrong = []
+
+    def body(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for turn in range(8):
+                kept = []
+                for j in range(len(work)):
+                    k = (j * (2 * i + 1) + turn * 5 + i) % len(work)
+                    kept.append((k, work[k]()))
+                s.synchronize()
+                wrong.extend((i, turn, k) for k, out in kept if not _same(out, alone[k]))
+
+    threads = [threading.Thread(target=body, args=(i,)) for i in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not wrong and g.gemv_wait_timeouts() == 0
