@@ -271,19 +271,22 @@ __global__ void __launch_bounds__(kSmallThreads) rms_norm_small_kernel(NormParam
       else reinterpret_cast<uint4 *>(static_cast<raw *>(p.ro) + row * p.ldo)[u] = E::pack(s);
     }
     const float pre = rescale(sum, p.eps);
-    if (__any_sync(0xffffffffu, pre != 1.f)) {  // rare; lanes reduce together whichever row needs it
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[e] *= pre;
-      reduce();
-    }
     int lift = 0;
-    if (EIGHT && __any_sync(0xffffffffu, !top_in_range(top))) {  // as rare
-      lift = lift_of(pre, sum, top);
+    // rare: beyond fp32's range; lanes reduce together whichever row needs it
+    if (__any_sync(0xffffffffu, pre != 1.f || (EIGHT && !top_in_range(top)))) {
+      float by = pre;
+#pragma unroll 1
+      for (int pass = 0; pass < (EIGHT ? 2 : 1); ++pass) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) s[e] *= power_of_two(lift);
-      const float kept = sum;
-      reduce();
-      sum = kept;
+        for (int e = 0; e < V; ++e) s[e] *= by;
+        const float kept = sum;
+        reduce();
+        if (pass > 0) sum = kept;
+        if (EIGHT && pass == 0) {
+          lift = top_in_range(top) ? 0 : lift_of(pre, sum, top);
+          by = power_of_two(lift);
+        }
+      }
     }
     const RowFactors g = row_factors<EIGHT>(pre, lift, sum, top, p.d, p.eps);
     if (EIGHT && u == 0 && in) p.scale[row] = g.scale;
