@@ -19,9 +19,11 @@
  * GEMV_* status codes, nothing launched on failure, nothing thrown.  The calls
  * allocate nothing and keep nothing, so any number may run at once on any
  * streams, and all can be captured in a CUDA graph.  Each launches one kernel
- * (gemm_fused() two for unaligned operands) as a programmatic dependent launch,
- * which reads and writes nothing before the preceding kernel has completed.  Results are bitwise reproducible: every sum
- * runs in an order fixed by the sizes, strides and alignment.
+ * (gemm_fused() two for unaligned operands) as a programmatic dependent launch:
+ * it may start early, but reads and writes no operand before the work ahead of
+ * the call has completed.  (A product that reads unaligned rows of B in place
+ * does so while its own copy of A is made.)  Results are bitwise reproducible:
+ * every sum runs in an order fixed by the sizes, strides and alignment.
  *
  * Kernels that wait on their own copies or on another CTA of their cluster do so
  * for a bounded number of polls: a wait that runs out writes NaN to what its CTA
@@ -150,9 +152,13 @@ int gemm_workspace(const void *B, int64_t ldb, const void *A, int64_t lda, int64
  *
  * in fp32; h is rounded once per element when stored, the carried state is not
  * rounded.  A decay exp(g) is within 4 units of 2^-24, relative, with 16-bit
- * storage within 4 + 1.25 |g|.  A g of minus infinity (or below -87.3, where the exponential leaves
- * fp32's normal range) drops what came before, whatever it holds: tokens of packed documents do not
- * see one another, NaN and infinities included.
+ * storage within 4 + 1.25 |g|.  A g of minus infinity (or below -87.3, where the
+ * exponential leaves fp32's normal range) drops what came before, whatever it
+ * holds: tokens of packed documents do not see one another, NaN and infinities
+ * included.  Decays above 1 (g > 0) are taken as well; but runs of up to 2048
+ * steps are joined by the product of their decays, and where such a product, or
+ * one decay, passes fp32's largest value, what follows may be infinite or NaN
+ * although h is not.  (A state of zeros stays right.)
  *
  *  x, g, h      (batch, steps, width) of `dtype` (GEMV_TYPE_F16, _BF16 or _F32),
  *               unit stride along width, batch and step strides in elements

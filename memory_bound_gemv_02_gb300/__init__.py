@@ -129,7 +129,9 @@ def lib() -> ctypes.CDLL:
 
 
 def _lib_with_operators() -> ctypes.CDLL:
-    """The loaded library with the argument types of the operators set."""
+    """The loaded library with the argument types of the operators set: their C
+    entry points for ctypes, with ``GemmEpilogue``.  The package's own functions go
+    through the extension module instead."""
     global _operators_ready
     if _operators_ready:
         return _lib

@@ -8,7 +8,12 @@ checks in Python.
 Without a ``stream`` argument the calls run on the current torch stream of
 the tensors' device.  Outputs may be passed in or are allocated, on the stream
 that the call runs on; ordering that stream after the inputs' work, and its
-readers after the call, is the caller's.  Results carry no gradient history.
+readers after the call, is the caller's.
+
+Like the rest of the package the calls are not recorded by autograd: results of
+tensors that require a gradient do not.  ``gated_scan_backward`` is the
+recurrence's gradient, examples/gated_block.py makes a torch.autograd.Function
+of the two.
 """
 from __future__ import annotations
 
@@ -30,7 +35,8 @@ GEMM_ACTIVATIONS = {**ACTIVATIONS, "log_sigmoid": GEMV_ACT_LOG_SIGMOID}
 
 
 class GemmEpilogue(ctypes.Structure):
-    """Mirror of ``gemm_epilogue`` in include/gemv_ops.h."""
+    """Mirror of ``gemm_epilogue`` in include/gemv_ops.h, for calls of the C library
+    by ctypes."""
     _fields_ = [("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("scale_a", ctypes.c_void_p),
                 ("scale_b", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
                 ("ldr", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
@@ -140,7 +146,7 @@ def gated_scan(x, g, h0=None, h=None, state=None, stream=None):
     width) storage; inputs may be expanded).  ``h0`` and ``state``: float32
     (batch, width); ``state`` receives the last step's unrounded h and may be
     ``h0`` (in-place decoding with steps = 1).  g = -inf starts a new sequence.
-    Returns (h, state)."""
+    Not recorded by autograd.  Returns (h, state)."""
     if h is None:
         _dims(x, 3, "x")
         h = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, x.device)

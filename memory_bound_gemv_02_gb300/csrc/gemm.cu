@@ -102,7 +102,8 @@ __device__ __forceinline__ float load_typed(const void *p, int64_t i, int type) 
 template <int ACT>
 __device__ __forceinline__ float activated(float y) {
   if (ACT == GEMV_ACT_RELU) return y != y ? y : fmaxf(y, 0.f);
-  // __fdividef: 2 ulp; a denominator above 2^126 gives 0, as it should here
+  // __fdividef: 2 ulp; a denominator above 2^126 gives 0, where the sigmoid is below
+  // 1.2e-38 and the silu within 1.1e-36 of 0
   if (ACT == GEMV_ACT_SIGMOID) return __fdividef(1.f, 1.f + expf(-y));
   if (ACT == GEMV_ACT_SILU) return __fdividef(y, 1.f + expf(-y));
   if (ACT == GEMV_ACT_LOG_SIGMOID) return fminf(y, 0.f) - log1pf(expf(-fabsf(y)));
@@ -129,7 +130,7 @@ struct Activation {};
 
 // The epilogue of one launch, and of one thread's column j of C.  Pairs read the
 // residual a block ahead (fetch()): in its turn 7656 x 8486 x 512 e4m3 took 164 us,
-// so 139.  With one tile per CTA that gains less (959 x 960 x 8576 fp16 30 -> 27) and
+// so 135.  With one tile per CTA that gains less (959 x 960 x 8576 fp16 30 -> 27) and
 // costs calls without a residual its registers and start (1024 x 1024 e4m3 4.1 -> 4.5).
 struct Column {
   static constexpr int kF16 = 1, kF32 = 2, kPairs = 4;  // bits of `how`
@@ -885,9 +886,8 @@ struct GemmPlan {
 //                       call
 // Clusters are only taken where all run at once, with a seventh of the slots
 // left for where they do not fit (256 x 28672 x 8192 bf16, 256 columns over 2
-// CTAs in several waves: 121 against 94 in pairs).  The choice is within 5 % of
-// the fastest form on all but six of the shapes and within 10 % on all.  Some
-// of them (bf16, measured): 512 x 4096 x 4096 pairs of 128 columns 18.6, of 256
+// CTAs in several waves: 121 against 94 in pairs).  Some of the shapes (bf16,
+// measured): 512 x 4096 x 4096 pairs of 128 columns 18.6, of 256
 // 23.0; 256 x 14336 x 4096 pairs 27.5, one tile per CTA 33.7; 256 x 1024 x 1024
 // 64 columns 6.8, 256 columns 12.0.
 GemmPlan gemm_plan(int64_t m, int64_t n, int64_t steps, int64_t operand_bytes, int sms, bool split_only) {

@@ -2,7 +2,8 @@
 // and strides here, after the checks that the C entry points cannot make (types,
 // shapes, devices).  A decoded token's kernels take 3 to 5 us; the same checks
 // made in Python with the call through ctypes took 7 to 9 us of host time per
-// call, with these it is 3 to 5 (the launch alone is 1.5).
+// call, with these it is 3 to 5 (the launch alone is 1.5); a product over unaligned
+// operands, two launches and their workspace, 5.5 to 6.4.
 //
 // Each function takes its arguments by position and returns the entry point's
 // status; a wrong argument raises TypeError or ValueError.
