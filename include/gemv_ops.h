@@ -155,7 +155,7 @@ int gemm_workspace(const void *B, int64_t ldb, const void *A, int64_t lda, int64
  * storage within 4 + 1.25 |g|.  A g of minus infinity (or below -87.3, where the
  * exponential leaves fp32's normal range) drops what came before, whatever it
  * holds: tokens of packed documents do not see one another, NaN and infinities
- * included.  Decays above 1 (g > 0) are taken as well; but runs of up to 2048
+ * included.  Decays above 1 (g > 0) are taken as well; but runs of up to 256
  * steps are joined by the product of their decays, and where such a product, or
  * one decay, passes fp32's largest value, what follows may be infinite or NaN
  * although h is not.  (A state of zeros stays right.)
