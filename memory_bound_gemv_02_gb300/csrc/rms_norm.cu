@@ -318,7 +318,8 @@ constexpr int64_t kHalfSm = 110 * 1024, kWholeSm = 224 * 1024;  // shared memory
 // plain loads and as many rows in flight as registers allow, 8192 x 7168 bf16
 // took 88 us.)  The weights are kept in shared memory.  SHIFT: a copy takes the
 // aligned blocks that cover its row, and a row's outputs are staged in the
-// memory of its inputs.
+// memory of its inputs.  (One CTA per SM named: left to itself the compiler fits
+// two of 1024 threads by spilling, 8192 x 4097 fp32 8 bit 133.7 us, so 130.8.)
 template <int TYPE, bool EIGHT, bool SHIFT>
 __global__ void __launch_bounds__(kMaxRowThreads, 1) rms_norm_ring_kernel(NormParams p) {
   using E = Elem<TYPE>;
