@@ -4,6 +4,9 @@ from __future__ import annotations
 
 import ctypes
 
+import pytest
+import torch
+
 P = [0x7F0000000000 + i * 0x100000000 for i in range(10)]  # never dereferenced
 
 
@@ -57,3 +60,47 @@ def test_rows_between_another_buffers_rows(gemv_lib):
     # one sequence's row between another buffer's
     assert scan(P[0], (64, 32), P[0] + 32 * e, (32, 32), b=1, t=1) not in _refused(g)
     assert scan(P[0], (64, 64), P[0] + 32 * e, (64, 64), b=10, t=1) not in _refused(g)
+
+
+def test_the_extension_module_counts_as_the_library_does(gemv_lib):
+    """gemm_workspace through torch tensors, on views with strides and offsets."""
+    g, L = gemv_lib, gemv_lib._lib_with_operators()
+    buf = torch.zeros(40000, dtype=torch.bfloat16)
+    for m, n, k, lda, ldb, off in ((4, 32, 64, 64, 64, 0), (4, 32, 64, 65, 64, 0), (4, 32, 64, 64, 67, 0),
+                                   (1, 32, 64, 99, 72, 3), (4, 32, 57, 65, 65, 1), (5, 1, 9, 9, 9, 2), (3, 700, 11, 11, 13, 5)):
+        A = buf[off:].as_strided((m, k), (lda, 1))
+        B = torch.zeros(40000, dtype=torch.bfloat16)[off:].as_strided((n, k), (ldb, 1))
+        want = ctypes.c_int64(-1)
+        assert L.gemm_workspace(B.data_ptr(), ldb if n > 1 else k, A.data_ptr(), lda if m > 1 else k, m, n, k, 1,
+                                ctypes.byref(want)) == g.GEMV_OK
+        assert g.gemm_workspace(B, A) == want.value
+    with pytest.raises(TypeError):
+        g.gemm_workspace(B.half(), A)
+    with pytest.raises(ValueError):
+        g.gemm_workspace(B[:, :-1], A)
+
+
+def test_the_extension_module_refuses_before_cuda(gemv_lib):
+    """Wrong arguments and host tensors raise in every entry point, without a GPU."""
+    g = gemv_lib
+    calls = g._operators._load()
+    x, w, seq = torch.zeros((2, 8)), torch.zeros(8), torch.zeros((2, 3, 8))
+    y, scale = torch.zeros((2, 8)), torch.zeros(2)
+    with pytest.raises(ValueError, match="CUDA"):
+        calls.rms_norm_fused(x, w, None, 1e-6, False, y, None, None, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        calls.gemm_fused(x.half(), x.half(), y.half(), 1.0, 1.0, None, None, None, 0, None, None, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        calls.gated_scan(seq, seq, None, seq, None, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        calls.gated_scan_backward(seq, seq, seq, None, None, seq, seq, None, None)
+    for f in (calls.rms_norm_fused, calls.gemm_fused, calls.gemm_workspace, calls.gated_scan, calls.gated_scan_backward):
+        with pytest.raises(TypeError, match="arguments expected"):
+            f(x)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        calls.gemm_fused(x.half(), [1.0], y, 1.0, 1.0, None, None, None, 0, None, None, None)
+    for call in (lambda: g.rms_norm_fused(x, w), lambda: g.rms_norm_fused(x, w, eight_bit=True, y=y, stream=0),
+                 lambda: g.gemm_fused(x.half(), x.half()), lambda: g.gated_scan(seq, seq),
+                 lambda: g.gated_scan_backward(seq, seq, seq)):
+        with pytest.raises(ValueError):
+            call()

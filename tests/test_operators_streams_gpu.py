@@ -257,3 +257,15 @@ def test_several_host_threads(cuda_dev):
         t.join()
     torch.cuda.synchronize()
     assert not wrong and g.gemv_wait_timeouts() == 0
+
+
+def test_forms_of_a_stream(cuda_dev):
+    """A stream as torch's object, as a handle, and the default stream as 0."""
+    side = torch.cuda.Stream()
+    for name, (call, want) in _calls(cuda_dev).items():
+        torch.cuda.synchronize()
+        for stream in (None, 0, torch.cuda.default_stream(), side, side.cuda_stream):
+            out = call(stream)
+            torch.cuda.synchronize()
+            for t, v in zip(out, want):
+                assert ((t.double() - v).abs() <= 1e-6 * v).all(), (name, stream)

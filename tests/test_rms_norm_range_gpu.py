@@ -53,15 +53,18 @@ def test_rows_near_the_largest_value(cuda_dev, dtype, d):
     _check(x, w, None, 1e-6, "one large")
 
 
-@pytest.mark.parametrize("dtype", [torch.float16] + WIDE)
-@pytest.mark.parametrize("wdtype", WIDE)
+SIZES = [(1.0, 1e-37), (1.0, 1e-40), (2e-3, 1e-36), (1e-12, 1e-37), (1e-30, 1e-30), (1e20, 1e30), (3e38, 1e30),
+         (1e18, 1e-38), (3.3e38, 1.6e38), (3.3e38, 1e-40)]
+# x's type, the weight's, the size of either (fp16 holds the first three sizes of x, and no such weight)
+WEIGHTED = [(torch.float16, torch.float32, *v) for v in SIZES[:3]] + \
+    [(dtype, wdtype, *v) for dtype, wdtype in ((torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                               (torch.float32, torch.float32)) for v in SIZES]
+
+
+@pytest.mark.parametrize("dtype,wdtype,size,weight", WEIGHTED)
 @pytest.mark.parametrize("d", WIDTHS)
-@pytest.mark.parametrize("size,weight", [(1.0, 1e-37), (1.0, 1e-40), (2e-3, 1e-36), (1e-12, 1e-37), (1e-30, 1e-30),
-                                         (1e20, 1e30), (3e38, 1e30), (1e18, 1e-38), (3.3e38, 1.6e38), (3.3e38, 1e-40)])
 def test_weights_near_the_ends_of_the_range(cuda_dev, dtype, wdtype, d, size, weight):
     """s w leaves fp32's range, or 448 / max|s w| does; s / rms times w does not."""
-    if wdtype not in (dtype, torch.float32) or (dtype == torch.float16 and not 1e-3 <= size <= 1e4):
-        pytest.skip("not a combination of types, or not a value of x's type")
     x = (ref.uniform((4, d), torch.float32, 5, cuda_dev, -1, 1) * size).to(dtype)
     x[1, ::2] = 0
     w = (ref.uniform((d,), torch.float32, 6, cuda_dev, 0.25, 1) * weight).to(wdtype)
