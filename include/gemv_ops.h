@@ -205,6 +205,145 @@ int gated_scan_backward(const void *dh, int64_t dh_batch, int64_t dh_step, const
                         int64_t dg_batch, int64_t dg_step, float *dh0, int64_t batch, int64_t steps,
                         int64_t width, int dtype, cudaStream_t stream);
 
+/*
+ * Residual addition and layer norm, for `rows` rows of d elements:
+ *
+ *     s       = x + residual                   (s = x without a residual)
+ *     mean    = mean_j(s[j]),   rstd = 1 / sqrt(mean_j((s[j] - mean)^2) + eps)
+ *     y[j]    = (s[j] - mean) * rstd * weight[j] + bias[j]
+ *
+ * s, the statistics and y are fp32 until the one rounding of each output; y is
+ * formed from the unrounded s, and the variance from differences from the mean.
+ *
+ *  x, residual   (rows, d) of `dtype` (GEMV_TYPE_F16, _BF16 or _F32), row strides
+ *                ldx, ldr >= d elements; residual may be NULL.
+ *  weight, bias  d elements each, of `dtype` or fp32 (param_dtype); either may be
+ *                NULL (ones, zeros).
+ *  y             (rows, d) of `dtype`, row stride ldy.
+ *  mean, rstd    rows fp32 values each, what layer_norm_backward() takes, or NULL.
+ *  residual_out  (rows, d) of `dtype`, row stride ldo, or NULL; needs a residual.
+ *                It may be residual or x itself (same pointer and stride).
+ *
+ * Rows whose squares leave fp32's range are scaled first, so every row of finite s
+ * gets its norm.  A row that holds a NaN or an infinity gives NaN throughout; a row
+ * of equal values with eps == 0 is 0 / 0.  rows == 0 or d == 0 launches nothing.
+ * Any alignment and stride work; 16-byte aligned rows take 16-byte accesses.
+ */
+int layer_norm_fused(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                     const void *bias, int param_dtype, void *y, int64_t ldy, float *mean, float *rstd,
+                     void *residual_out, int64_t ldo, int64_t rows, int64_t d, float eps, int dtype,
+                     cudaStream_t stream);
+
+/*
+ * The gradient of layer_norm_fused(): with dy the gradient of y and ds that of
+ * residual_out from elsewhere, xh = (s - mean) * rstd and t = dy * weight,
+ *
+ *     dx[j]      = rstd * (t[j] - mean_j(t) - xh[j] * mean_j(t * xh)) + ds[j]
+ *     dweight[j] = sum_rows dy[j] * xh[j],     dbias[j] = sum_rows dy[j]
+ *
+ * in fp32 on the stored s (residual_out, or x without a residual); dx is the
+ * gradient of both x and the residual.
+ *
+ *  dy, s, ds     (rows, d) of `dtype`, row strides >= d; ds may be NULL (zeros).
+ *  weight        d elements of `dtype` or fp32 (weight_dtype), or NULL (ones).
+ *  mean, rstd    as the forward call stored them.
+ *  dx            (rows, d) of `dtype`; may be ds itself (same pointer and stride).
+ *  dweight,      d fp32 values each, or NULL; rows == 0 gives zeros.
+ *  dbias
+ *  workspace     layer_norm_workspace() bytes of the caller's (16-byte aligned,
+ *                overlapping nothing, free again after the call's work on the
+ *                stream); none where both sums are NULL.  A shorter one returns
+ *                GEMV_ERR_SCRATCH.
+ *
+ * Two kernels, with rows too long for a CTA's registers (beyond 16384 16-bit or
+ * 8192 other elements) three.
+ */
+int layer_norm_backward(const void *dy, int64_t lddy, const void *s, int64_t lds, const void *weight,
+                        int weight_dtype, const float *mean, const float *rstd, const void *ds, int64_t ldds,
+                        void *dx, int64_t lddx, float *dweight, float *dbias, int64_t rows, int64_t d, int dtype,
+                        void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/* The workspace of layer_norm_backward() in *bytes.  A pure host function. */
+int layer_norm_workspace(int64_t rows, int64_t d, int64_t *bytes);
+
+/* A (batch, steps, heads, size) operand with unit stride along size; strides in elements. */
+typedef struct gemv_heads {
+  void *p;
+  int64_t batch, step, head;
+} gemv_heads;
+
+/* Sizes and types of gated_delta(). */
+typedef struct gated_delta_shape {
+  int64_t batch, steps, heads, heads_k, dk, dv;
+  int32_t dtype;      /* of q, k, v, o: GEMV_TYPE_F16 or GEMV_TYPE_BF16 */
+  int32_t gate_dtype; /* of g and beta: `dtype` or GEMV_TYPE_F32 */
+  float scale;
+} gated_delta_shape;
+
+/*
+ * The gated delta rule, for each sequence and head, on a state S of (dk, dv):
+ *
+ *     d[t] = beta[t] * (v[t] - exp(g[t]) * S[t-1]^T k[t])
+ *     S[t] = exp(g[t]) * S[t-1] + k[t] d[t]^T         (0 <= t < steps, S[-1] = h0)
+ *     o[t] = scale * S[t]^T q[t]
+ *
+ * the decode step of gla_decode() with one decay per head and with what the state
+ * already answers to k taken out of v first.  Head i of v, g, beta, o and of the
+ * state goes with head i / (heads / heads_k) of q and k; heads is a multiple of
+ * heads_k.  The state is fp32; o is rounded once.
+ *
+ *  q, k        (batch, steps, heads_k, dk) of `dtype`, dk <= 256.
+ *  v, o        (batch, steps, heads, dv) of `dtype`.
+ *  g, beta     (batch, steps, heads) of gate_dtype.
+ *              Input strides may be any values >= 0; an output's rows must not overlap.
+ *  h0          (batch, heads, dk, dv) fp32, dense, or NULL (zero).
+ *  state       the same, the state after the last step (h0 for steps == 0), or
+ *              NULL.  May be h0 itself: steps == 1 is then an in-place decode step.
+ *  workspace   gated_delta_workspace() bytes of the caller's (16-byte aligned,
+ *              overlapping nothing, free again after the call's work on the
+ *              stream); a shorter one returns GEMV_ERR_SCRATCH.
+ *
+ * Up to 48 steps are walked one by one in fp32, by one kernel.  Longer sequences are
+ * cut into chunks of 64 steps, whose products run on the tensor cores by two
+ * kernels, the state and what comes from it as sums of two bf16 (products within
+ * 2^-16 of their terms).  Operands whose rows are not on 16 bytes are copied first,
+ * one kernel each.
+ *
+ * A g of minus infinity (or below -87.3, where the exponential leaves fp32's normal
+ * range) starts a new document.  With beta * |k|^2 <= 2 the state stays bounded; the
+ * rule itself diverges beyond.  Values have to be finite: a NaN or an infinity in q,
+ * k, v, beta or h0 may reach every output of its head from the start of its chunk
+ * on, past new documents too.  0 <= batch, heads <= 65535.
+ */
+int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_heads *k, const gemv_heads *v,
+                const gemv_heads *g, const gemv_heads *beta, const float *h0, const gemv_heads *o, float *state,
+                void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The gradient of gated_delta(): d_o is the gradient of o, dstate that of the last
+ * state (fp32, dense, or NULL for zero).  dq, dk, dv, dg, dbeta: gradients in the
+ * types of what they belong to, those of shared heads of q and k summed over the
+ * heads that share them; dg is 0 where a new document starts.  dh0: fp32, dense, or
+ * NULL; may be dstate itself.  steps == 0 copies dstate (or 0) to it.  An input
+ * shared along a stride of 0 gets one gradient per use.
+ *
+ * The forward pass leaves nothing behind for it: states and corrections are computed
+ * again from the inputs, chunk by chunk, and kept in `workspace`
+ * (gated_delta_workspace() with d_o).  Three kernels, and one more for shared heads.
+ */
+int gated_delta_backward(const gated_delta_shape *shape, const gemv_heads *d_o, const gemv_heads *q,
+                         const gemv_heads *k, const gemv_heads *v, const gemv_heads *g, const gemv_heads *beta,
+                         const float *h0, const float *dstate, const gemv_heads *dq, const gemv_heads *dk,
+                         const gemv_heads *dv, const gemv_heads *dg, const gemv_heads *dbeta, float *dh0,
+                         void *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The workspace of gated_delta() (d_o NULL) or of gated_delta_backward() for these
+ * operands, in *bytes.  A pure host function.
+ */
+int gated_delta_workspace(const gated_delta_shape *shape, const gemv_heads *q, const gemv_heads *k,
+                          const gemv_heads *v, const gemv_heads *d_o, int64_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

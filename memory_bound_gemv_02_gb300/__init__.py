@@ -14,7 +14,9 @@ Names follow the C entry points: ``gemv``, ``gemv_ex``, ``gemv_fused``, ``gemv_p
 ``gemv_host``, ``gemv_splitk_noalloc``, ``gemv_wait_timeouts``,
 ``gemv_debug_wait_budget``, ``gla_decode``, ``gla_decode_ex``, and the operators
 of include/gemv_ops.h: ``rms_norm_fused``, ``gemm_fused``,
-``gemm_workspace``, ``gated_scan``, ``gated_scan_backward``.
+``gemm_workspace``, ``gated_scan``, ``gated_scan_backward``, ``layer_norm_fused``,
+``layer_norm_backward``, ``layer_norm_workspace``, ``gated_delta``,
+``gated_delta_backward``, ``gated_delta_workspace``.
 """
 from __future__ import annotations
 
@@ -52,7 +54,9 @@ ENTRY_POINTS = ("gemv", "gemv_ex", "gemv_fused", "gemv_prepare", "gemv_plan", "g
 
 
 #: the entry points of include/gemv_ops.h
-OPERATOR_ENTRY_POINTS = ("rms_norm_fused", "gemm_fused", "gemm_workspace", "gated_scan", "gated_scan_backward")
+OPERATOR_ENTRY_POINTS = ("rms_norm_fused", "gemm_fused", "gemm_workspace", "gated_scan", "gated_scan_backward",
+                         "layer_norm_fused", "layer_norm_backward", "layer_norm_workspace", "gated_delta",
+                         "gated_delta_backward", "gated_delta_workspace")
 
 
 class GemvConfig(ctypes.Structure):
@@ -145,6 +149,16 @@ def _lib_with_operators() -> ctypes.CDLL:
     L.gemm_workspace.argtypes = [vp, i64, vp, i64, i64, i64, i64, i32, ctypes.POINTER(i64)]
     L.gated_scan.argtypes = seq + seq + [vp] + seq + [vp, i64, i64, i64, i32, vp]
     L.gated_scan_backward.argtypes = seq * 3 + [vp, vp] + seq * 2 + [vp, i64, i64, i64, i32, vp]
+    L.layer_norm_fused.argtypes = [vp, i64, vp, i64, vp, vp, i32, vp, i64, vp, vp, vp, i64, i64, i64, ctypes.c_float,
+                                   i32, vp]
+    L.layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64, i64, i32, vp,
+                                      i64, vp]
+    L.layer_norm_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
+    heads = ctypes.POINTER(Heads)
+    L.gated_delta.argtypes = [ctypes.POINTER(GatedDeltaShape)] + [heads] * 5 + [vp, heads, vp, vp, i64, vp]
+    L.gated_delta_backward.argtypes = [ctypes.POINTER(GatedDeltaShape)] + [heads] * 6 + [vp, vp] + [heads] * 5 + \
+        [vp, vp, i64, vp]
+    L.gated_delta_workspace.argtypes = [ctypes.POINTER(GatedDeltaShape)] + [heads] * 4 + [ctypes.POINTER(i64)]
     for name in OPERATOR_ENTRY_POINTS:
         getattr(L, name).restype = i32
     _operators_ready = True
@@ -400,5 +414,6 @@ def gla_decode(q, k, v, gk, S, scale: float, S_new=None, o=None, stream=None, va
 
 # The operators around the product, built on the helpers above.
 from ._operators import (GEMM_ACTIVATIONS, GEMV_ACT_LOG_SIGMOID, GEMV_TYPE_BF16, GEMV_TYPE_E4M3,  # noqa: E402
-                         GEMV_TYPE_F16, GEMV_TYPE_F32, GemmEpilogue, gated_scan, gated_scan_backward, gemm_fused,
-                         gemm_workspace, rms_norm_fused)
+                         GEMV_TYPE_F16, GEMV_TYPE_F32, GatedDeltaShape, GemmEpilogue, Heads, gated_delta,
+                         gated_delta_backward, gated_delta_workspace, gated_scan, gated_scan_backward, gemm_fused,
+                         gemm_workspace, layer_norm_backward, layer_norm_fused, layer_norm_workspace, rms_norm_fused)

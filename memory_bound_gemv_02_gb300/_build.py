@@ -35,10 +35,11 @@ EXTENSION = os.path.join(LIBDIR, "operators_py.so")
 EXTENSION_STAMP = os.path.join(LIBDIR, "operators_py.built")  # what it was built against
 
 SOURCES = ["gemv_api.cu", "gemv_kernels_f16.cu", "gemv_kernels_bf16.cu", "gemv_bulk_f16.cu", "gemv_bulk_bf16.cu",
-           "gla_decode.cu", "rms_norm.cu", "gated_scan.cu", "gemm.cu"]
+           "gla_decode.cu", "rms_norm.cu", "gated_scan.cu", "gemm.cu", "layer_norm.cu", "gated_delta.cu",
+           "gated_delta_chunks.cu", "gated_delta_gradient.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("gemv_internal.h", "gemv_kernels.cuh", "gemv_tiles.cuh",
                                            "gemv_bulk.cuh", "ops_internal.h", "tc_ptx.cuh",
-                                           "tensor_map.h")] + \
+                                           "tensor_map.h", "gated_delta.h", "gated_delta_mma.cuh")] + \
     [os.path.join(INCLUDE, h) for h in ("gemv.h", "gemv_ops.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

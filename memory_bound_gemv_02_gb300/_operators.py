@@ -1,6 +1,8 @@
 """Python entry points of the operators in include/gemv_ops.h, with the C
-names: ``rms_norm_fused``, ``gemm_fused``, ``gemm_workspace``, ``gated_scan`` and
-``gated_scan_backward`` (imported into the package).  Tensors are only turned into
+names: ``rms_norm_fused``, ``gemm_fused``, ``gemm_workspace``, ``gated_scan``,
+``gated_scan_backward``, ``layer_norm_fused``, ``layer_norm_backward``,
+``layer_norm_workspace``, ``gated_delta``, ``gated_delta_backward`` and
+``gated_delta_workspace`` (imported into the package).  Tensors are only turned into
 pointers, sizes and strides; that happens in an extension module
 (csrc/operators_py.cpp), as a decoded token's kernels are shorter than the same
 checks in Python.
@@ -13,7 +15,8 @@ readers after the call, is the caller's.
 Like the rest of the package the calls are not recorded by autograd: results of
 tensors that require a gradient do not.  ``gated_scan_backward`` is the
 recurrence's gradient, examples/gated_block.py makes a torch.autograd.Function
-of the two.
+of the two; examples/delta_block.py does so for the layer norm and the gated
+delta rule.
 """
 from __future__ import annotations
 
@@ -23,7 +26,7 @@ import importlib.util
 
 import torch
 
-from . import ACTIVATIONS, _build, _check, _stream_handle, lib
+from . import ACTIVATIONS, _build, _check, _lib_with_operators, _stream_handle, lib
 
 GEMV_TYPE_F16, GEMV_TYPE_BF16, GEMV_TYPE_F32, GEMV_TYPE_E4M3 = 0, 1, 2, 3
 GEMV_ACT_LOG_SIGMOID = 4
@@ -40,6 +43,18 @@ class GemmEpilogue(ctypes.Structure):
     _fields_ = [("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("scale_a", ctypes.c_void_p),
                 ("scale_b", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
                 ("ldr", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    """Mirror of ``gemv_heads`` in include/gemv_ops.h, for calls of the C library."""
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_int64), ("step", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class GatedDeltaShape(ctypes.Structure):
+    """Mirror of ``gated_delta_shape`` in include/gemv_ops.h, for calls of the C library."""
+    _fields_ = [("batch", ctypes.c_int64), ("steps", ctypes.c_int64), ("heads", ctypes.c_int64),
+                ("heads_k", ctypes.c_int64), ("dk", ctypes.c_int64), ("dv", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 _calls = None
@@ -177,3 +192,127 @@ def gated_scan_backward(dh, g, h, h0=None, dstate=None, dx=None, dg=None, dh0=No
     if st:
         _check(st, "gated_scan_backward")
     return dx, dg, dh0
+
+
+def layer_norm_fused(x, weight=None, bias=None, residual=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
+                     residual_out=None, stats: bool = False, stream=None):
+    """s = x + residual; y = (s - mean(s)) * rstd * weight + bias per row, with
+    rstd = 1 / sqrt(var(s) + eps).
+
+    ``x`` and ``residual``: (rows, d), float16, bfloat16 or float32, unit column
+    stride; ``weight`` and ``bias``: (d,), in x's dtype or float32 (both alike), or
+    None.  ``mean`` and ``rstd``: float32, one per row, for ``layer_norm_backward``;
+    allocated with ``stats``.  ``residual_out`` (x's dtype; may be ``residual`` or
+    ``x`` itself) receives s.  Returns (y, mean, rstd, residual_out), the statistics
+    None if not asked for, the last None without a residual."""
+    if y is None:
+        _dims(x, 2, "x")
+        y = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, x.device)
+    if stats:
+        rows = _dims(x, 2, "x")[0]
+        if mean is None:
+            mean = _new(lambda: torch.empty(rows, dtype=_F32, device=x.device), stream, x.device)
+        if rstd is None:
+            rstd = _new(lambda: torch.empty(rows, dtype=_F32, device=x.device), stream, x.device)
+    if residual is not None and residual_out is None:
+        _dims(x, 2, "x")
+        residual_out = _new(lambda: torch.empty_like(x, memory_format=torch.contiguous_format), stream, x.device)
+    st = (_calls or _load()).layer_norm_fused(x, weight, bias, residual, eps, y, mean, rstd, residual_out,
+                                              stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "layer_norm_fused")
+    return y, mean, rstd, residual_out
+
+
+def layer_norm_backward(dy, s, weight, mean, rstd, ds=None, dx=None, dweight=None, dbias=None, stream=None,
+                        workspace=None):
+    """The gradient of ``layer_norm_fused``: ``dy`` is the gradient of y, ``ds`` that
+    of residual_out from elsewhere (optional); ``s`` is residual_out (x without a
+    residual), ``mean`` and ``rstd`` are the forward call's.  dx, the gradient of x
+    and of the residual, may be ``ds``.  ``dweight`` and ``dbias``: float32 (d,).
+    ``workspace``: any tensor of ``layer_norm_workspace`` bytes, or torch's allocator
+    has memory for the call's stream.  Returns (dx, dweight, dbias)."""
+    if dx is None:
+        _dims(s, 2, "s")
+        dx = _new(lambda: torch.empty_like(s, memory_format=torch.contiguous_format), stream, s.device)
+    if dweight is None:
+        d = _dims(s, 2, "s")[1]
+        dweight = _new(lambda: torch.empty(d, dtype=_F32, device=s.device), stream, s.device)
+    if dbias is None:
+        d = _dims(s, 2, "s")[1]
+        dbias = _new(lambda: torch.empty(d, dtype=_F32, device=s.device), stream, s.device)
+    st = (_calls or _load()).layer_norm_backward(dy, s, weight, mean, rstd, ds, dx, dweight, dbias, workspace,
+                                                 stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "layer_norm_backward")
+    return dx, dweight, dbias
+
+
+def layer_norm_workspace(rows: int, d: int) -> int:
+    """Bytes of workspace that ``layer_norm_backward`` takes."""
+    need = ctypes.c_int64(0)
+    _check(_lib_with_operators().layer_norm_workspace(rows, d, ctypes.byref(need)), "layer_norm_workspace")
+    return need.value
+
+
+def gated_delta(q, k, v, g, beta, scale: float, h0=None, o=None, state=None, stream=None, workspace=None):
+    """The gated delta rule along sequences: per head, on a state S (dk, dv),
+
+        d = beta * (v - exp(g) * S^T k);  S = exp(g) * S + outer(k, d);  o = scale * S^T q
+
+    for each step.  ``q`` and ``k``: (batch, steps, heads_k, dk), ``v`` and ``o``:
+    (batch, steps, heads, dv), float16 or bfloat16, unit stride along the last
+    dimension, other strides free; heads is a multiple of heads_k, whose heads are
+    shared by consecutive heads of v.  ``g`` and ``beta``: (batch, steps, heads), in
+    q's dtype or float32 (both alike).  ``h0`` and ``state``: float32
+    (batch, heads, dk, dv); ``state`` receives the last S and may be ``h0`` (in-place
+    decoding).  g = -inf starts a new document.  ``workspace`` (sequences of more
+    than 48 steps): any tensor of ``gated_delta_workspace`` bytes, or torch's
+    allocator has memory for the call's stream.  Not recorded by autograd.  Returns
+    (o, state)."""
+    if o is None:
+        _dims(v, 4, "v")
+        o = _new(lambda: torch.empty_like(v, memory_format=torch.contiguous_format), stream, v.device)
+    if state is None:
+        batch, _, heads, dv = _dims(v, 4, "v")
+        dk = _dims(q, 4, "q")[3]
+        state = _new(lambda: torch.empty((batch, heads, dk, dv), dtype=_F32, device=v.device), stream, v.device)
+    st = (_calls or _load()).gated_delta(q, k, v, g, beta, scale, h0, o, state, workspace,
+                                         stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "gated_delta")
+    return o, state
+
+
+def gated_delta_backward(do, q, k, v, g, beta, scale: float, h0=None, dstate=None, dq=None, dk=None, dv=None, dg=None,
+                         dbeta=None, dh0=None, stream=None, workspace=None):
+    """The gradient of ``gated_delta``: ``do`` is the gradient of o, ``dstate`` that of
+    the returned state (float32, optional); the other inputs as in the forward call,
+    which keeps nothing for this one.  ``workspace``: any tensor of
+    ``gated_delta_workspace`` bytes (with ``do``), or torch's allocator has memory
+    for the call's stream.  Returns (dq, dk, dv, dg, dbeta, dh0)."""
+    def like(given, t, dims, name):
+        if given is not None:
+            return given
+        _dims(t, dims, name)
+        return _new(lambda: torch.empty_like(t, memory_format=torch.contiguous_format), stream, t.device)
+
+    dq, dk, dv = like(dq, q, 4, "q"), like(dk, k, 4, "k"), like(dv, v, 4, "v")
+    dg, dbeta = like(dg, g, 3, "g"), like(dbeta, beta, 3, "beta")
+    if dh0 is None:
+        batch, _, heads, size = v.shape
+        dh0 = _new(lambda: torch.empty((batch, heads, q.shape[3], size), dtype=_F32, device=v.device), stream, v.device)
+    st = (_calls or _load()).gated_delta_backward(do, q, k, v, g, beta, scale, h0, dstate, dq, dk, dv, dg, dbeta, dh0,
+                                                  workspace, stream if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "gated_delta_backward")
+    return dq, dk, dv, dg, dbeta, dh0
+
+
+def gated_delta_workspace(q, k, v, do=None) -> int:
+    """Bytes of workspace that ``gated_delta`` takes for these operands, or, with
+    ``do``, ``gated_delta_backward``."""
+    need = (_calls or _load()).gated_delta_workspace(q, k, v, do)
+    if need < 0:
+        _check(need, "gated_delta_workspace")
+    return need

@@ -1,0 +1,71 @@
+// Shared by the kernels of gated_delta() and gated_delta_backward() (gemv_ops.h):
+// where operands lie, the workspace of sequences cut into chunks, and the
+// launches.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gemv_ops.h"
+#include "ops_internal.h"
+
+namespace gemvk {
+
+constexpr int kDeltaChunk = 64;    // steps per chunk
+constexpr int kDeltaSlice = 64;    // columns of v per CTA of the chains
+constexpr int kDeltaMostDk = 256;
+
+// (batch, steps, heads, size) elements with unit stride along size.
+struct HeadsOf {
+  const void *p;
+  int64_t batch, step, head;
+};
+
+// The same, of 16-bit elements whose rows are copied 16 bytes at a time.
+struct TileSource {
+  const uint16_t *p;
+  int64_t batch, step, head;
+  int32_t units;  // 16-byte units of a row; elements behind are zero
+};
+
+// What a chunk's gates come to, 64 of each: beta; the decay from before the chunk
+// to the step (0 past a new document); that from the step to the chunk's end; the
+// sum of log decays up to the step in two floats, and the count of documents begun.
+enum { kBeta = 0, kFirst = 64, kLast = 128, kTotalHi = 192, kTotalLo = 256, kDocs = 320, kGateFloats = 384 };
+
+// A chunk of one head: T = (I + A)^-1 and P as sums of two bf16 (64 x 64 each), the gates.
+constexpr int kMatrix = kDeltaChunk * kDeltaChunk;
+constexpr int64_t kRecordHalfs = 4 * kMatrix;  // T, T's rest, P, P's rest
+constexpr int64_t kRecordBytes = kRecordHalfs * 2 + kGateFloats * 4;
+
+struct DeltaParams {
+  HeadsOf q, k, v, g, beta, d_o;
+  TileSource tq, tk, tv, td;  // q, k, v, d_o for the chunk kernels
+  const float *h0, *dstate;
+  HeadsOf o, dq, dk, dv, dg, dbeta;  // outputs
+  float *state, *dh0;
+  char *records;                   // (batch, heads, chunks) of kRecordBytes
+  uint16_t *start, *end;           // gradient: states before a chunk, gradients behind it, (.., 2, dvp, DK) bf16
+  uint16_t *corrections, *dcorr;   // and its corrections and their gradients, (.., 2, dvp, 64)
+  float *dq32, *dk32;              // gradients per head of v where heads of k are shared
+  float scale;
+  int32_t batch, steps, heads, heads_k, dk_size, dv_size, chunks;
+  int32_t gates_f32, f16, vector_o, vector_dv;
+};
+
+// Copies of operands whose rows are not on 16 bytes, padded to 16.
+struct PackParams {
+  HeadsOf from;
+  uint16_t *to;
+  int32_t steps, heads, size, padded;
+  int64_t rows;  // batch * heads * steps
+};
+
+int launch_delta_steps(const DeltaParams &p, int sms, cudaStream_t stream);
+int launch_delta_pack(const PackParams &p, cudaStream_t stream);
+int launch_delta_chunks(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream);
+int launch_delta_walks(const DeltaParams &p, int dk_padded, cudaStream_t stream);
+int launch_delta_gradient(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream);
+
+}  // namespace gemvk

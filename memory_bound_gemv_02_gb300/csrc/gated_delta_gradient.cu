@@ -1,0 +1,425 @@
+// The gradient of the gated delta rule (see gated_delta_backward() in gemv_ops.h), from
+// what the two walks over the chunks have kept: the state S before a chunk and the
+// gradient dS' of the state behind it, the corrections D and the gradients dR of what
+// they are solved from.  With f_ij = exp(G_i - G_j), per chunk, all chunks at once:
+//
+//     dP_ij = scale f_ij dO_i . D_j  (j <= i),     M_ij = -f_ij dR_i . D_j  (j < i)
+//     dQ    = scale exp(G) dO S^T + dP K
+//     X     = -exp(G) dR S^T + M K
+//     dK    = beta X + (beta M)^T K + dP^T Q + exp(G_last - G) D dS'^T
+//     dbeta = dR . V + K . X   (row by row),       dV = beta dR  (stored by the walk)
+//
+// The gradient of g_t is what is carried over step t, from before it to behind it:
+//
+//     dg_t = sum_{j < t <= i} (dP_ij q_i . k_j + beta_i M_ij k_i . k_j)
+//            + sum_{i >= t} (q_i . dQ_i + beta_i k_i . X_i  of the terms with S)
+//            + sum_{j < t} (k_j . dK_j  of the term with dS') + exp(G_last) <S, dS'>
+//
+// sums of terms that do pass the step, not differences of sums of all terms: exactly 0
+// where a document starts, and no cancellation where decays are strong.
+//
+// 16 steps x 64 columns of dk per warp, three sets of sums.
+#include "gated_delta_mma.cuh"
+
+namespace gemvk {
+namespace {
+
+constexpr int kTilePitch = kDeltaChunk + 8;
+constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
+
+template <int DK>
+struct Grad {
+  static constexpr int kParts = DK / 64, kThreads = 128 * kParts, kSlice = DK == 256 ? 32 : 64;
+  static constexpr int kWide = DK + 8, kNarrow = kSlice + 8;  // row pitches
+  static constexpr int kTile = kDeltaChunk * kWide * 2, kStates = kSlice * kWide * 2, kSteps = kSlice * kTilePitch * 2,
+                       kValues = kDeltaChunk * kNarrow * 2;
+  static constexpr int kK = 0, kQ = kTile, kStage = 2 * kTile;
+  // a slice of v's columns
+  static constexpr int kS = kStage, kR = kS + 2 * kStates, kDo = kR + 2 * kSteps, kV = kDo + kValues, kE = kV + kValues,
+                       kD = kE + 2 * kStates, kStageEnd = kD + 2 * kSteps;
+  // afterwards in the same place: dP, M, beta M as two bf16 each, and the terms of dg
+  static constexpr int kDp = kStage, kM = kDp + 2 * kPairBytes, kBm = kM + 2 * kPairBytes, kW = kBm + 2 * kPairBytes,
+                       kWPitch = kDeltaChunk + 1, kAfter = kW + kDeltaChunk * kWPitch * 4;
+  static constexpr int kGates = kStageEnd > kAfter ? kStageEnd : kAfter, kRows = kGates + kGateFloats * 4,
+                       kSums = kRows + 4 * kParts * kDeltaChunk * 4, kBytes = kSums + (kThreads + 32) * 4;
+};
+
+__device__ __forceinline__ float gate_decay(const float *gates, int i, int j) {
+  if (gates[kDocs + i] != gates[kDocs + j]) return 0.f;
+  return expf((gates[kTotalHi + i] - gates[kTotalHi + j]) + (gates[kTotalLo + i] - gates[kTotalLo + j]));
+}
+
+__device__ __forceinline__ void put_gate(const HeadsOf &h, bool f32, bool f16, int64_t b, int64_t t, int64_t head, float v) {
+  void *const to = const_cast<void *>(h.p);
+  const int64_t at = b * h.batch + t * h.step + head * h.head;
+  if (f32) static_cast<float *>(to)[at] = v;
+  else static_cast<uint16_t *>(to)[at] = f16 ? Elem<GEMV_TYPE_F16>::put(v) : Elem<GEMV_TYPE_BF16>::put(v);
+}
+
+// Row sums of c times the elements of X (steps, dk) in the sums' layout: lanes with lane % 4 == 0 of a quad end up
+// with those of rows lane / 4 (x) and 8 further (y).
+template <bool F16>
+__device__ __forceinline__ float2 row_dots(const FragC (&c)[8], const char *X, int pitch, int row, int col) {
+  const int lane = threadIdx.x & 31;
+  float2 sum = make_float2(0.f, 0.f);
+  const uint16_t *const x = reinterpret_cast<const uint16_t *>(X) + (row + lane / 4) * pitch + col + lane % 4 * 2;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const float2 lo = unpack_input<F16>(*reinterpret_cast<const uint32_t *>(x + n * 8));
+    const float2 hi = unpack_input<F16>(*reinterpret_cast<const uint32_t *>(x + 8 * pitch + n * 8));
+    sum.x = fmaf(c[n][0], lo.x, fmaf(c[n][1], lo.y, sum.x));
+    sum.y = fmaf(c[n][2], hi.x, fmaf(c[n][3], hi.y, sum.y));
+  }
+#pragma unroll
+  for (int m = 1; m < 4; m *= 2) {
+    sum.x += __shfl_xor_sync(0xffffffffu, sum.x, m);
+    sum.y += __shfl_xor_sync(0xffffffffu, sum.y, m);
+  }
+  return sum;
+}
+
+// 16 x 64 sums to an output (or, for shared heads, to fp32).
+template <bool F16>
+__device__ __forceinline__ void store_rows(const FragC (&c)[8], const HeadsOf &to, float *to32, const DeltaParams &p, int64_t b,
+                                           int64_t head, int t0, int row, int col) {
+  typedef Elem<F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16> E;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = t0 + row + lane / 4 + 8 * h;
+    if (t >= p.steps) continue;
+    float *const at32 = to32 ? to32 + ((b * p.steps + t) * p.heads + head) * p.dk_size : nullptr;
+    uint16_t *const at = static_cast<uint16_t *>(const_cast<void *>(to.p)) + b * to.batch + (int64_t)t * to.step + head * to.head;
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int j = col + n * 8 + lane % 4 * 2 + e;
+        if (j >= p.dk_size) continue;
+        if (to32) at32[j] = c[n][2 * h + e];
+        else at[j] = E::put(c[n][2 * h + e]);
+      }
+  }
+}
+
+template <bool F16, int DK>
+__global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(const DeltaParams p) {
+  typedef Grad<DK> L;
+  constexpr int NT = 8 / L::kParts;  // tiles of 8 columns that a warp has of the 64 x 64 products
+  extern __shared__ __align__(16) char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int row = warp % 4 * 16, part = warp / 4, col = part * 64, mcol = part * NT * 8;
+  const int chunk = blockIdx.x, t0 = chunk * kDeltaChunk;
+  const int64_t b = blockIdx.z, head = blockIdx.y, head_k = head / (p.heads / p.heads_k);
+  const int64_t at = (b * p.heads + head) * p.chunks + chunk;
+  const int slices64 = (p.dv_size + kDeltaSlice - 1) / kDeltaSlice;
+  const int64_t dvp = (int64_t)slices64 * kDeltaSlice;
+  const uint32_t base = smem_u32(smem), K = base + L::kK, Q = base + L::kQ;
+  float *const gates = reinterpret_cast<float *>(smem + L::kGates);
+  float *const rows = reinterpret_cast<float *>(smem + L::kRows);  // (4, parts, 64): q.dQ0, k.X0, k.X, k.Y0
+  float *const sums = reinterpret_cast<float *>(smem + L::kSums);
+  wait_for_predecessor();
+  copy_tile<DK, L::kThreads>(K, p.tk, b, head_k, t0, p.steps, 0);
+  copy_tile<DK, L::kThreads>(Q, p.tq, b, head_k, t0, p.steps, 0);
+  if (tid < kGateFloats / 4)
+    copy16(base + L::kGates + tid * 16, p.records + at * kRecordBytes + kRecordHalfs * 2 + tid * 16, true);
+  FragC dq[8] = {}, x[8] = {}, y[8] = {}, dp[NT] = {}, mm[NT] = {};
+  float whole = 0.f, vr = 0.f;
+  for (int col_v = 0; col_v < p.dv_size; col_v += L::kSlice) {
+    if (col_v > 0) __syncthreads();
+    const uint16_t *const s0 = p.start + (at * 2 * dvp + col_v) * DK, *const s1 = p.end + (at * 2 * dvp + col_v) * DK;
+    const uint16_t *const c0 = p.corrections + (at * 2 * dvp + col_v) * kDeltaChunk,
+                         *const c1 = p.dcorr + (at * 2 * dvp + col_v) * kDeltaChunk;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      copy_dense<L::kSlice, DK, L::kThreads>(base + L::kS + h * L::kStates, s0 + h * dvp * DK);
+      copy_dense<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kR + h * L::kSteps, c1 + h * dvp * kDeltaChunk);
+    }
+    copy_tile<L::kSlice, L::kThreads>(base + L::kDo, p.td, b, head, t0, p.steps, col_v);
+    copy_tile<L::kSlice, L::kThreads>(base + L::kV, p.tv, b, head, t0, p.steps, col_v);
+    copies_close();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      copy_dense<L::kSlice, DK, L::kThreads>(base + L::kE + h * L::kStates, s1 + h * dvp * DK);
+      copy_dense<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kD + h * L::kSteps, c0 + h * dvp * kDeltaChunk);
+    }
+    copies_close();
+    copies_wait<1>();
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < L::kSlice / 16; ++s) {
+      FragA o, r, rr;
+      load_matrices(o, at_kn(base + L::kDo, L::kNarrow, row, s * 16, lane));
+      load_matrices_t(r, at_km(base + L::kR, kTilePitch, s * 16, row, lane));
+      load_matrices_t(rr, at_km(base + L::kR + L::kSteps, kTilePitch, s * 16, row, lane));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t h[4], l[4];
+        load_matrices_t(h, at_kn(base + L::kS, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(l, at_kn(base + L::kS + L::kStates, L::kWide, s * 16, col + n * 16, lane));
+        mma_input_split<F16>(dq[2 * n], dq[2 * n + 1], o, h, l);
+        mma_split_split(x[2 * n], x[2 * n + 1], r, rr, h, l);
+      }
+    }
+    {  // dR . V: step tid % 64, every (threads / 64)th column
+      const int c = tid % 64;
+      const uint16_t *const r = reinterpret_cast<const uint16_t *>(smem + L::kR) + c;
+      const uint16_t *const v = reinterpret_cast<const uint16_t *>(smem + L::kV) + c * L::kNarrow;
+      for (int j = tid / 64; j < L::kSlice; j += L::kThreads / 64) {
+        const float f = BF16::to_float(r[j * kTilePitch]) + BF16::to_float(r[j * kTilePitch + L::kSteps / 2]);
+        vr = fmaf(f, F16 ? Elem<GEMV_TYPE_F16>::get(v[j]) : Elem<GEMV_TYPE_BF16>::get(v[j]), vr);
+      }
+    }
+    copies_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < L::kSlice / 16; ++s) {
+      FragA o, r, rr, d, dd;
+      load_matrices(o, at_kn(base + L::kDo, L::kNarrow, row, s * 16, lane));
+      load_matrices_t(r, at_km(base + L::kR, kTilePitch, s * 16, row, lane));
+      load_matrices_t(rr, at_km(base + L::kR + L::kSteps, kTilePitch, s * 16, row, lane));
+      load_matrices_t(d, at_km(base + L::kD, kTilePitch, s * 16, row, lane));
+      load_matrices_t(dd, at_km(base + L::kD + L::kSteps, kTilePitch, s * 16, row, lane));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t h[4], l[4];
+        load_matrices_t(h, at_kn(base + L::kE, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(l, at_kn(base + L::kE + L::kStates, L::kWide, s * 16, col + n * 16, lane));
+        mma_split_split(y[2 * n], y[2 * n + 1], d, dd, h, l);
+      }
+#pragma unroll
+      for (int n = 0; n < NT / 2; ++n) {
+        if (mcol + n * 16 > row) continue;
+        uint32_t h[4], l[4];
+        load_matrices_t(h, at_kn(base + L::kD, kTilePitch, s * 16, mcol + n * 16, lane));
+        load_matrices_t(l, at_kn(base + L::kD + L::kSteps, kTilePitch, s * 16, mcol + n * 16, lane));
+        mma_input_split<F16>(dp[2 * n], dp[2 * n + 1], o, h, l);
+        mma_split_split(mm[2 * n], mm[2 * n + 1], r, rr, h, l);
+      }
+    }
+    // <S, dS'>: pairs of the slice
+    for (int i = tid; i < L::kSlice * DK / 2; i += L::kThreads) {
+      const int at2 = (i / (DK / 2)) * L::kWide * 2 + i % (DK / 2) * 4;
+      auto both = [&](int area) {
+        const float2 h = unpack_bf16(*reinterpret_cast<const uint32_t *>(smem + area + at2));
+        const float2 l = unpack_bf16(*reinterpret_cast<const uint32_t *>(smem + area + L::kStates + at2));
+        return make_float2(h.x + l.x, h.y + l.y);
+      };
+      const float2 u = both(L::kS), w = both(L::kE);
+      whole = fmaf(u.x, w.x, fmaf(u.y, w.y, whole));
+    }
+  }
+  // the terms with S and dS', scaled, and what they are along the rows of q and k
+  {
+    const int i0 = row + lane / 4;
+    const float f0 = gates[kFirst + i0], f1 = gates[kFirst + i0 + 8], e0 = gates[kLast + i0], e1 = gates[kLast + i0 + 8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        dq[n][e] *= p.scale * (e < 2 ? f0 : f1);
+        x[n][e] *= -(e < 2 ? f0 : f1);
+        y[n][e] *= e < 2 ? e0 : e1;
+      }
+    const float2 a = row_dots<F16>(dq, smem + L::kQ, L::kWide, row, col), c = row_dots<F16>(x, smem + L::kK, L::kWide, row, col),
+                 d = row_dots<F16>(y, smem + L::kK, L::kWide, row, col);
+    if (lane % 4 == 0) {
+      float *const to = rows + part * kDeltaChunk + i0;
+      to[0] = a.x;
+      to[8] = a.y;
+      to[L::kParts * kDeltaChunk] = c.x;
+      to[L::kParts * kDeltaChunk + 8] = c.y;
+      to[3 * L::kParts * kDeltaChunk] = d.x;
+      to[3 * L::kParts * kDeltaChunk + 8] = d.y;
+    }
+  }
+  // q . k and k . k of this warp's part, up to the diagonal
+  FragC qk[NT] = {}, kk[NT] = {};
+#pragma unroll
+  for (int s = 0; s < DK / 16; ++s) {
+    FragA aq, ak;
+    load_matrices(aq, at_kn(Q, L::kWide, row, s * 16, lane));
+    load_matrices(ak, at_kn(K, L::kWide, row, s * 16, lane));
+#pragma unroll
+    for (int n = 0; n < NT / 2; ++n) {
+      if (mcol + n * 16 > row) continue;
+      uint32_t bk[4];
+      load_matrices(bk, at_nk(K, L::kWide, mcol + n * 16, s * 16, lane));
+      mma_inputs<F16>(qk[2 * n], aq, bk[0], bk[1]);
+      mma_inputs<F16>(qk[2 * n + 1], aq, bk[2], bk[3]);
+      mma_inputs<F16>(kk[2 * n], ak, bk[0], bk[1]);
+      mma_inputs<F16>(kk[2 * n + 1], ak, bk[2], bk[3]);
+    }
+  }
+  __syncthreads();  // the slices are done with
+  sums[tid] = vr;
+  float *const W = reinterpret_cast<float *>(smem + L::kW);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = row + lane / 4 + 8 * h, j = mcol + n * 8 + lane % 4 * 2;
+      const float beta = gates[kBeta + i];
+      float u[2] = {}, m[2] = {};
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float w = 0.f;
+        if (j + e <= i) {
+          const float f = gate_decay(gates, i, j + e);
+          u[e] = p.scale * f * dp[n][2 * h + e];
+          if (j + e < i) {
+            m[e] = -f * mm[n][2 * h + e];
+            w = fmaf(u[e], qk[n][2 * h + e], beta * m[e] * kk[n][2 * h + e]);
+          }
+        }
+        W[i * L::kWPitch + j + e] = w;
+      }
+      const int to = (i * kTilePitch + j) * 2;
+      uint32_t big, rest;
+      split(u[0], u[1], big, rest);
+      *reinterpret_cast<uint32_t *>(smem + L::kDp + to) = big;
+      *reinterpret_cast<uint32_t *>(smem + L::kDp + kPairBytes + to) = rest;
+      split(m[0], m[1], big, rest);
+      *reinterpret_cast<uint32_t *>(smem + L::kM + to) = big;
+      *reinterpret_cast<uint32_t *>(smem + L::kM + kPairBytes + to) = rest;
+      split(beta * m[0], beta * m[1], big, rest);
+      *reinterpret_cast<uint32_t *>(smem + L::kBm + to) = big;
+      *reinterpret_cast<uint32_t *>(smem + L::kBm + kPairBytes + to) = rest;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    FragA u, uu, m, mr;
+    if (s * 16 <= row) {  // dQ += dP K, X += M K
+      load_matrices(u, at_kn(base + L::kDp, kTilePitch, row, s * 16, lane));
+      load_matrices(uu, at_kn(base + L::kDp + kPairBytes, kTilePitch, row, s * 16, lane));
+      load_matrices(m, at_kn(base + L::kM, kTilePitch, row, s * 16, lane));
+      load_matrices(mr, at_kn(base + L::kM + kPairBytes, kTilePitch, row, s * 16, lane));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t k[4];
+        load_matrices_t(k, at_kn(K, L::kWide, s * 16, col + n * 16, lane));
+        mma_split_input<F16>(dq[2 * n], dq[2 * n + 1], u, uu, k);
+        mma_split_input<F16>(x[2 * n], x[2 * n + 1], m, mr, k);
+      }
+    }
+    if (s * 16 >= row) {  // Y += dP^T Q + (beta M)^T K
+      load_matrices_t(u, at_km(base + L::kDp, kTilePitch, s * 16, row, lane));
+      load_matrices_t(uu, at_km(base + L::kDp + kPairBytes, kTilePitch, s * 16, row, lane));
+      load_matrices_t(m, at_km(base + L::kBm, kTilePitch, s * 16, row, lane));
+      load_matrices_t(mr, at_km(base + L::kBm + kPairBytes, kTilePitch, s * 16, row, lane));
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t q[4], k[4];
+        load_matrices_t(q, at_kn(Q, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(k, at_kn(K, L::kWide, s * 16, col + n * 16, lane));
+        mma_split_input<F16>(y[2 * n], y[2 * n + 1], u, uu, q);
+        mma_split_input<F16>(y[2 * n], y[2 * n + 1], m, mr, k);
+      }
+    }
+  }
+  {
+    const float2 a = row_dots<F16>(x, smem + L::kK, L::kWide, row, col);
+    if (lane % 4 == 0) {
+      float *const to = rows + (2 * L::kParts + part) * kDeltaChunk + row + lane / 4;
+      to[0] = a.x;
+      to[8] = a.y;
+    }
+    const float b0 = gates[kBeta + row + lane / 4], b1 = gates[kBeta + row + lane / 4 + 8];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[n][e] = fmaf(e < 2 ? b0 : b1, x[n][e], y[n][e]);
+  }
+  const int64_t out_head = p.dq32 ? head : head_k;
+  store_rows<F16>(dq, p.dq, p.dq32, p, b, out_head, t0, row, col);
+  store_rows<F16>(y, p.dk, p.dk32, p, b, out_head, t0, row, col);
+  // the gates' gradients
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, m);
+  if (lane == 0) sums[L::kThreads + warp] = whole;
+  if (tid < kDeltaChunk) {  // column tid of W, summed from below
+    float s = 0.f;
+    for (int i = kDeltaChunk - 1; i >= 0; --i) {
+      s += W[i * L::kWPitch + tid];
+      W[i * L::kWPitch + tid] = s;
+    }
+  }
+  __syncthreads();
+  if (tid < kDeltaChunk && t0 + tid < p.steps) {
+    auto of = [&](int which, int i) {
+      float s = rows[which * L::kParts * kDeltaChunk + i];
+#pragma unroll
+      for (int q = 1; q < L::kParts; ++q) s += rows[(which * L::kParts + q) * kDeltaChunk + i];
+      return s;
+    };
+    float db = of(2, tid);
+#pragma unroll
+    for (int q = 0; q < L::kThreads / 64; ++q) db += sums[q * 64 + tid];
+    put_gate(p.dbeta, p.gates_f32, F16, b, t0 + tid, head, db);
+    float inner = 0.f, ahead = 0.f, before = 0.f, all = 0.f;
+    for (int j = 0; j < tid; ++j) {
+      inner += W[tid * L::kWPitch + j];
+      before += of(3, j);
+    }
+    for (int i = tid; i < kDeltaChunk; ++i) ahead += of(0, i) + gates[kBeta + i] * of(1, i);
+    for (int w = 0; w < L::kThreads / 32; ++w) all += sums[L::kThreads + w];
+    // nothing passes the first step of a document
+    const bool starts = tid == 0 ? gates[kDocs] != 0.f : gates[kDocs + tid] != gates[kDocs + tid - 1];
+    const float dg = starts ? 0.f : inner + ahead + before + gates[kFirst + kDeltaChunk - 1] * all;
+    put_gate(p.dg, p.gates_f32, F16, b, t0 + tid, head, dg);
+  }
+}
+
+// Gradients of shared heads: fp32 per head of v, summed in order.
+template <bool F16>
+__global__ void __launch_bounds__(256) delta_fold_kernel(const DeltaParams p) {
+  typedef Elem<F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16> E;
+  const int group = p.heads / p.heads_k;
+  const int64_t cells = (int64_t)p.batch * p.steps * p.heads_k * p.dk_size;
+  wait_for_predecessor();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < cells; i += (int64_t)gridDim.x * 256) {
+    const int64_t j = i % p.dk_size, head = i / p.dk_size % p.heads_k, token = i / p.dk_size / p.heads_k;
+    const int64_t t = token % p.steps, b = token / p.steps;
+    const int64_t from = (token * p.heads + head * group) * p.dk_size + j;
+    float q = 0.f, k = 0.f;
+    for (int m = 0; m < group; ++m) {
+      q += p.dq32[from + (int64_t)m * p.dk_size];
+      k += p.dk32[from + (int64_t)m * p.dk_size];
+    }
+    static_cast<uint16_t *>(const_cast<void *>(p.dq.p))[b * p.dq.batch + t * p.dq.step + head * p.dq.head + j] = E::put(q);
+    static_cast<uint16_t *>(const_cast<void *>(p.dk.p))[b * p.dk.batch + t * p.dk.step + head * p.dk.head + j] = E::put(k);
+  }
+}
+
+template <bool F16, int DK>
+int launch_gradient(const DeltaParams &p, cudaStream_t stream) {
+  typedef Grad<DK> L;
+  auto fn = delta_gradient_kernel<F16, DK>;
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
+  }
+  return launch_op(fn, dim3((unsigned)p.chunks, (unsigned)p.heads, (unsigned)p.batch), L::kThreads, L::kBytes, 1, stream, p);
+}
+
+template <bool F16>
+int dispatch(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream) {
+  const int st = dk_padded == 64    ? launch_gradient<F16, 64>(p, stream)
+                 : dk_padded == 128 ? launch_gradient<F16, 128>(p, stream)
+                                    : launch_gradient<F16, 256>(p, stream);
+  if (st != GEMV_OK || !p.dq32) return st;
+  const int64_t cells = (int64_t)p.batch * p.steps * p.heads_k * p.dk_size, ctas = (cells + 255) / 256;
+  return launch_op(delta_fold_kernel<F16>, dim3((unsigned)(ctas < 16 * sms ? ctas : 16 * sms)), 256, 0, 1, stream, p);
+}
+
+}  // namespace
+
+int launch_delta_gradient(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream) {
+  const int st = launch_delta_walks(p, dk_padded, stream);
+  if (st != GEMV_OK) return st;
+  return p.f16 ? dispatch<true>(p, dk_padded, sms, stream) : dispatch<false>(p, dk_padded, sms, stream);
+}
+
+}  // namespace gemvk

@@ -1,0 +1,197 @@
+// Matrix fragments for the chunks of gated_delta(): 16 x 8 x 16 products of bf16 with
+// fp32 sums, their operands from shared memory or from sums just made.
+//
+// A sum is fed on as two bf16 that add up to it within 2^-17 (its fragment layout
+// is that of the next product's left operand, so it never leaves the registers); an
+// fp16 input becomes two bf16 exactly.  Products of the two small parts are left out:
+// they are 2^-16 of the whole.  Why not tcgen05: a chain's products are 16 x 64 x 64
+// to 16 x 128 x 64 per warp, each needing the one before at once; through tensor
+// memory every one of them would be written, waited for and read back.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "gated_delta.h"
+#include "tc_ptx.cuh"
+
+namespace gemvk {
+
+typedef uint32_t FragA[4];
+typedef float FragC[4];
+
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void load_matrices_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void store_matrices_t(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(FragC &c, const FragA &a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(FragC &c, const FragA &a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Both operands inputs of the call.
+template <bool F16>
+__device__ __forceinline__ void mma_inputs(FragC &c, const FragA &a, uint32_t b0, uint32_t b1) {
+  if constexpr (F16) mma_f16(c, a, b0, b1);
+  else mma_bf16(c, a, b0, b1);
+}
+
+// a (in the low half) and b as bf16, and what is left of them.
+__device__ __forceinline__ void split(float a, float b, uint32_t &big, uint32_t &rest) {
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(big) : "f"(b), "f"(a));
+  const float ra = a - __uint_as_float(big << 16), rb = b - __uint_as_float(big & 0xffff0000u);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(rest) : "f"(rb), "f"(ra));
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack_input(uint32_t v) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+  else return unpack_bf16(v);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_output(float a, float b) {
+  return F16 ? Elem<GEMV_TYPE_F16>::pair(a, b) : Elem<GEMV_TYPE_BF16>::pair(a, b);
+}
+// An fp16 pair as two pairs of bf16.
+__device__ __forceinline__ void split_half(uint32_t v, uint32_t &big, uint32_t &rest) {
+  const float2 f = unpack_input<true>(v);
+  split(f.x, f.y, big, rest);
+}
+
+// The left operand of a product's next step: the sums of two neighbouring 16 x 8 tiles.
+__device__ __forceinline__ void split_sums(const FragC &c0, const FragC &c1, FragA &big, FragA &rest) {
+  split(c0[0], c0[1], big[0], rest[0]);
+  split(c0[2], c0[3], big[1], rest[1]);
+  split(c1[0], c1[1], big[2], rest[2]);
+  split(c1[2], c1[3], big[3], rest[3]);
+}
+
+// c0, c1 += (big + rest) B for the 16 x 16 block b of an input.
+template <bool F16>
+__device__ __forceinline__ void mma_split_input(FragC &c0, FragC &c1, const FragA &big, const FragA &rest,
+                                                const uint32_t (&b)[4]) {
+  if constexpr (F16) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_half(b[i], h[i], l[i]);
+    mma_bf16(c0, big, h[0], h[1]);
+    mma_bf16(c1, big, h[2], h[3]);
+    mma_bf16(c0, rest, h[0], h[1]);
+    mma_bf16(c1, rest, h[2], h[3]);
+    mma_bf16(c0, big, l[0], l[1]);
+    mma_bf16(c1, big, l[2], l[3]);
+  } else {
+    mma_bf16(c0, big, b[0], b[1]);
+    mma_bf16(c1, big, b[2], b[3]);
+    mma_bf16(c0, rest, b[0], b[1]);
+    mma_bf16(c1, rest, b[2], b[3]);
+  }
+}
+// c0, c1 += (big + rest) (h + l)
+__device__ __forceinline__ void mma_split_split(FragC &c0, FragC &c1, const FragA &big, const FragA &rest,
+                                                const uint32_t (&h)[4], const uint32_t (&l)[4]) {
+  mma_bf16(c0, big, h[0], h[1]);
+  mma_bf16(c1, big, h[2], h[3]);
+  mma_bf16(c0, rest, h[0], h[1]);
+  mma_bf16(c1, rest, h[2], h[3]);
+  mma_bf16(c0, big, l[0], l[1]);
+  mma_bf16(c1, big, l[2], l[3]);
+}
+// c0, c1 += A (h + l) for a left operand that is an input.
+template <bool F16>
+__device__ __forceinline__ void mma_input_split(FragC &c0, FragC &c1, const FragA &a, const uint32_t (&h)[4],
+                                                const uint32_t (&l)[4]) {
+  if constexpr (F16) {
+    FragA big, rest;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_half(a[i], big[i], rest[i]);
+    mma_split_split(c0, c1, big, rest, h, l);
+  } else {
+    mma_bf16(c0, a, h[0], h[1]);
+    mma_bf16(c1, a, h[2], h[3]);
+    mma_bf16(c0, a, l[0], l[1]);
+    mma_bf16(c1, a, l[2], l[3]);
+  }
+}
+
+// Addresses for load_matrices() of a 16 x 16 block at (row, col) of a matrix in shared
+// memory with `pitch` elements per row.
+//   right operand, stored (n, k), plain loads: registers 0, 1 are the first 8 of n
+__device__ __forceinline__ uint32_t at_nk(uint32_t base, int pitch, int n, int k, int lane) {
+  return base + (uint32_t)((n + (lane & 7) + ((lane >> 4) & 1) * 8) * pitch + k + ((lane >> 3) & 1) * 8) * 2;
+}
+//   right operand, stored (k, n), transposing loads; also a left operand stored (m, k),
+//   plain loads
+__device__ __forceinline__ uint32_t at_kn(uint32_t base, int pitch, int k, int n, int lane) {
+  return base + (uint32_t)((k + (lane & 7) + ((lane >> 3) & 1) * 8) * pitch + n + ((lane >> 4) & 1) * 8) * 2;
+}
+//   left operand, stored (k, m), transposing loads; also the sums' layout of a block
+//   stored (column, row): registers 0, 1 the first 8 columns, rows 0-7 and 8-15
+__device__ __forceinline__ uint32_t at_km(uint32_t base, int pitch, int k, int m, int lane) {
+  return base + (uint32_t)((k + (lane & 7) + ((lane >> 4) & 1) * 8) * pitch + m + ((lane >> 3) & 1) * 8) * 2;
+}
+
+// ------------------------------------------------------------- copies ahead --
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// 64 steps from t0 of one head, columns [col, col + COLS), zeros behind the last step and
+// column, to rows of COLS + 8 elements.
+template <int COLS, int THREADS>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const TileSource &s, int64_t b, int64_t head, int64_t t0, int steps,
+                                          int col) {
+  constexpr int UNITS = COLS / 8;
+  const uint16_t *const base = s.p + b * s.batch + head * s.head + t0 * s.step + col;
+#pragma unroll
+  for (int i = 0; i < (kDeltaChunk * UNITS + THREADS - 1) / THREADS; ++i) {
+    const int at = i * THREADS + (int)threadIdx.x;
+    if (kDeltaChunk * UNITS % THREADS != 0 && at >= kDeltaChunk * UNITS) break;
+    const int r = at / UNITS, u = at % UNITS;
+    const bool there = t0 + r < steps && col / 8 + u < s.units;
+    copy16(dst + (uint32_t)(r * (COLS + 8) + u * 8) * 2, there ? base + r * s.step + u * 8 : s.p, there);
+  }
+}
+// ROWS dense rows of COLS elements, to rows of COLS + 8.
+template <int ROWS, int COLS, int THREADS>
+__device__ __forceinline__ void copy_dense(uint32_t dst, const uint16_t *src) {
+  constexpr int UNITS = COLS / 8;
+#pragma unroll
+  for (int i = 0; i < (ROWS * UNITS + THREADS - 1) / THREADS; ++i) {
+    const int at = i * THREADS + (int)threadIdx.x;
+    if (ROWS * UNITS % THREADS != 0 && at >= ROWS * UNITS) break;
+    copy16(dst + (uint32_t)(at / UNITS * (COLS + 8) + at % UNITS * 8) * 2, src + (int64_t)at * 8, true);
+  }
+}
+
+}  // namespace gemvk

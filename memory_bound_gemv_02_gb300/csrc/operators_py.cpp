@@ -325,6 +325,227 @@ PyObject *py_gated_scan_backward(PyObject *, PyObject *const *a, Py_ssize_t coun
   });
 }
 
+// An optional matrix, null for None.
+Matrix optional_matrix(PyObject *o, const char *name, int64_t rows, int64_t cols, ScalarType type, int64_t device) {
+  if (o == Py_None) return {nullptr, cols};
+  return matrix(tensor(o, name), name, rows, cols, type, device);
+}
+
+// A caller's workspace, or none.
+struct Workspace {
+  void *p = nullptr;
+  int64_t bytes = 0;
+  bool given = false;
+};
+Workspace workspace_of(PyObject *o, int64_t device) {
+  if (o == Py_None) return {};
+  const Tensor &w = tensor(o, "workspace");
+  check_device(w, "workspace", device);
+  if (!w.is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+  return {w.data_ptr(), (int64_t)w.nbytes(), true};
+}
+
+// The dtype of a parameter or gate, `type` or fp32, that several share.
+ScalarType shared_type(PyObject *a, PyObject *b, const char *a_name, const char *b_name, ScalarType type) {
+  ScalarType got = a != Py_None ? tensor(a, a_name).scalar_type()
+                   : b != Py_None ? tensor(b, b_name).scalar_type() : type;
+  if (got != ScalarType::Float && got != type)
+    raise(PyExc_TypeError, "%s must be %s or Float, got %s", a != Py_None ? a_name : b_name, c10::toString(type),
+          c10::toString(got));
+  return got;
+}
+
+// x, weight, bias, residual, eps, y, mean, rstd, residual_out, stream
+PyObject *py_layer_norm(PyObject *, PyObject *const *a, Py_ssize_t count) {
+  return guarded(count, 10, [&]() {
+    const Tensor &x = tensor(a[0], "x");
+    const int64_t dev = x.get_device();
+    const ScalarType type = x.scalar_type();
+    if (x.dim() != 2 || dev < 0) raise(PyExc_ValueError, "x must be a 2-d CUDA tensor");
+    if (!row_type(type))
+      raise(PyExc_TypeError, "x must be float16, bfloat16 or float32, got %s", c10::toString(type));
+    const int64_t rows = x.size(0), d = x.size(1);
+    const Matrix mx = matrix(x, "x", rows, d, type, dev);
+    const ScalarType params = shared_type(a[1], a[2], "weight", "bias", type);
+    void *const w = vector(a[1], "weight", d, params, params, dev), *const b = vector(a[2], "bias", d, params, params, dev);
+    const Matrix my = matrix(tensor(a[5], "y"), "y", rows, d, type, dev);
+    float *const mean = static_cast<float *>(vector(a[6], "mean", rows, ScalarType::Float, ScalarType::Float, dev));
+    float *const rstd = static_cast<float *>(vector(a[7], "rstd", rows, ScalarType::Float, ScalarType::Float, dev));
+    if (a[3] == Py_None && a[8] != Py_None) raise(PyExc_ValueError, "residual_out needs a residual");
+    const Matrix mr = optional_matrix(a[3], "residual", rows, d, type, dev),
+                 mo = optional_matrix(a[8], "residual_out", rows, d, type, dev);
+    const float eps = number(a[4]);
+    return launch(dev, a[9], [&](cudaStream_t s) {
+      return layer_norm_fused(mx.p, mx.ld, mr.p, mr.ld, w, b, type_code(params), my.p, my.ld, mean, rstd, mo.p, mo.ld, rows,
+                              d, eps, type_code(type), s);
+    });
+  });
+}
+
+// dy, s, weight, mean, rstd, ds, dx, dweight, dbias, workspace, stream
+PyObject *py_layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
+  return guarded(count, 11, [&]() {
+    const Tensor &x = tensor(a[1], "s");
+    const int64_t dev = x.get_device();
+    const ScalarType type = x.scalar_type(), F = ScalarType::Float;
+    if (x.dim() != 2 || dev < 0) raise(PyExc_ValueError, "s must be a 2-d CUDA tensor");
+    if (!row_type(type))
+      raise(PyExc_TypeError, "s must be float16, bfloat16 or float32, got %s", c10::toString(type));
+    const int64_t rows = x.size(0), d = x.size(1);
+    const Matrix ms = matrix(x, "s", rows, d, type, dev), my = matrix(tensor(a[0], "dy"), "dy", rows, d, type, dev),
+                 md = optional_matrix(a[5], "ds", rows, d, type, dev),
+                 mx = matrix(tensor(a[6], "dx"), "dx", rows, d, type, dev);
+    const ScalarType params = shared_type(a[2], Py_None, "weight", "weight", type);
+    void *const w = vector(a[2], "weight", d, params, params, dev);
+    if (a[3] == Py_None || a[4] == Py_None) raise(PyExc_TypeError, "mean and rstd must be tensors");
+    const float *const mean = static_cast<float *>(vector(a[3], "mean", rows, F, F, dev)),
+                *const rstd = static_cast<float *>(vector(a[4], "rstd", rows, F, F, dev));
+    float *const dw = static_cast<float *>(vector(a[7], "dweight", d, F, F, dev)),
+                *const db = static_cast<float *>(vector(a[8], "dbias", d, F, F, dev));
+    Workspace ws = workspace_of(a[9], dev);
+    return launch(dev, a[10], [&](cudaStream_t s) {
+      if (!ws.given && (dw || db)) {
+        const int st = layer_norm_workspace(rows, d, &ws.bytes);
+        if (st != GEMV_OK) return st;
+      }
+      const StreamMemory own(ws.given ? 0 : ws.bytes, s);
+      return layer_norm_backward(my.p, my.ld, ms.p, ms.ld, w, type_code(params), mean, rstd, md.p, md.ld, mx.p, mx.ld, dw,
+                                 db, rows, d, type_code(type), ws.given ? ws.p : own.get(), ws.bytes, s);
+    });
+  });
+}
+
+// (batch, steps, heads, size), or (batch, steps, heads) of gates.
+gemv_heads heads_of(PyObject *o, const char *name, int64_t batch, int64_t steps, int64_t heads, int64_t size,
+                    ScalarType type, int64_t device) {
+  const Tensor &t = tensor(o, name);
+  check_type(t, name, type);
+  const bool gates = size < 0;
+  if (t.dim() != (gates ? 3 : 4) || t.size(0) != batch || t.size(1) != steps || t.size(2) != heads ||
+      (!gates && t.size(3) != size)) {
+    if (gates)
+      raise(PyExc_ValueError, "%s must have shape (%lld, %lld, %lld)", name, (long long)batch, (long long)steps,
+            (long long)heads);
+    raise(PyExc_ValueError, "%s must have shape (%lld, %lld, %lld, %lld)", name, (long long)batch, (long long)steps,
+          (long long)heads, (long long)size);
+  }
+  check_device(t, name, device);
+  if (!gates && size > 1 && t.stride(3) != 1)
+    raise(PyExc_ValueError, "%s must have unit stride along its last dimension", name);
+  return {t.data_ptr(), batch > 1 ? t.stride(0) : 0, steps > 1 ? t.stride(1) : 0, heads > 1 ? t.stride(2) : 0};
+}
+
+// The sizes, from q and v.
+gated_delta_shape delta_shape(PyObject *q, PyObject *v, bool cuda, ScalarType *type, int64_t *device) {
+  const Tensor &tq = tensor(q, "q"), &tv = tensor(v, "v");
+  if (tq.dim() != 4 || tv.dim() != 4 || (cuda && tv.get_device() < 0))
+    raise(PyExc_ValueError, "q (batch, steps, heads_k, dk) and v (batch, steps, heads, dv) must be 4-d CUDA tensors");
+  *type = tv.scalar_type();
+  if (*type != ScalarType::Half && *type != ScalarType::BFloat16)
+    raise(PyExc_TypeError, "v must be float16 or bfloat16, got %s", c10::toString(*type));
+  *device = tv.get_device();
+  gated_delta_shape s = {};
+  s.batch = tv.size(0);
+  s.steps = tv.size(1);
+  s.heads = tv.size(2);
+  s.heads_k = tq.size(2);
+  s.dk = tq.size(3);
+  s.dv = tv.size(3);
+  if (s.heads_k == 0 ? s.heads != 0 : s.heads % s.heads_k != 0)
+    raise(PyExc_ValueError, "%lld heads of v cannot share %lld of q and k", (long long)s.heads, (long long)s.heads_k);
+  s.dtype = s.gate_dtype = type_code(*type);
+  return s;
+}
+
+// A dense fp32 state, or null for None.
+float *state_of(PyObject *o, const char *name, const gated_delta_shape &s, int64_t device) {
+  if (o == Py_None) return nullptr;
+  const Tensor &t = tensor(o, name);
+  check_type(t, name, ScalarType::Float);
+  if (t.dim() != 4 || t.size(0) != s.batch || t.size(1) != s.heads || t.size(2) != s.dk || t.size(3) != s.dv ||
+      !t.is_contiguous())
+    raise(PyExc_ValueError, "%s must be a contiguous (%lld, %lld, %lld, %lld) tensor", name, (long long)s.batch,
+          (long long)s.heads, (long long)s.dk, (long long)s.dv);
+  check_device(t, name, device);
+  return static_cast<float *>(t.data_ptr());
+}
+
+// q, k, v, g, beta, scale, h0, o, state, workspace, stream
+PyObject *py_gated_delta(PyObject *, PyObject *const *a, Py_ssize_t count) {
+  return guarded(count, 11, [&]() {
+    ScalarType type;
+    int64_t dev;
+    gated_delta_shape s = delta_shape(a[0], a[2], true, &type, &dev);
+    const ScalarType gates = shared_type(a[3], a[4], "g", "beta", type);
+    const gemv_heads q = heads_of(a[0], "q", s.batch, s.steps, s.heads_k, s.dk, type, dev),
+                     k = heads_of(a[1], "k", s.batch, s.steps, s.heads_k, s.dk, type, dev),
+                     v = heads_of(a[2], "v", s.batch, s.steps, s.heads, s.dv, type, dev),
+                     g = heads_of(a[3], "g", s.batch, s.steps, s.heads, -1, gates, dev),
+                     beta = heads_of(a[4], "beta", s.batch, s.steps, s.heads, -1, gates, dev),
+                     o = heads_of(a[7], "o", s.batch, s.steps, s.heads, s.dv, type, dev);
+    s.scale = number(a[5]);
+    s.gate_dtype = type_code(gates);
+    const float *const h0 = state_of(a[6], "h0", s, dev);
+    float *const state = state_of(a[8], "state", s, dev);
+    Workspace ws = workspace_of(a[9], dev);
+    return launch(dev, a[10], [&](cudaStream_t stream) {
+      if (!ws.given) {
+        const int st = gated_delta_workspace(&s, &q, &k, &v, nullptr, &ws.bytes);
+        if (st != GEMV_OK) return st;
+      }
+      const StreamMemory own(ws.given ? 0 : ws.bytes, stream);
+      return gated_delta(&s, &q, &k, &v, &g, &beta, h0, &o, state, ws.given ? ws.p : own.get(), ws.bytes, stream);
+    });
+  });
+}
+
+// do, q, k, v, g, beta, scale, h0, dstate, dq, dk, dv, dg, dbeta, dh0, workspace, stream
+PyObject *py_gated_delta_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
+  return guarded(count, 17, [&]() {
+    ScalarType type;
+    int64_t dev;
+    gated_delta_shape s = delta_shape(a[1], a[3], true, &type, &dev);
+    const ScalarType gates = shared_type(a[4], a[5], "g", "beta", type);
+    auto keys = [&](int i, const char *name) { return heads_of(a[i], name, s.batch, s.steps, s.heads_k, s.dk, type, dev); };
+    auto values = [&](int i, const char *name) { return heads_of(a[i], name, s.batch, s.steps, s.heads, s.dv, type, dev); };
+    auto gate = [&](int i, const char *name) { return heads_of(a[i], name, s.batch, s.steps, s.heads, -1, gates, dev); };
+    const gemv_heads d_o = values(0, "do"), q = keys(1, "q"), k = keys(2, "k"), v = values(3, "v"), g = gate(4, "g"),
+                     beta = gate(5, "beta"), dq = keys(9, "dq"), dk = keys(10, "dk"), dv = values(11, "dv"),
+                     dg = gate(12, "dg"), dbeta = gate(13, "dbeta");
+    s.scale = number(a[6]);
+    s.gate_dtype = type_code(gates);
+    const float *const h0 = state_of(a[7], "h0", s, dev), *const dstate = state_of(a[8], "dstate", s, dev);
+    float *const dh0 = state_of(a[14], "dh0", s, dev);
+    Workspace ws = workspace_of(a[15], dev);
+    return launch(dev, a[16], [&](cudaStream_t stream) {
+      if (!ws.given) {
+        const int st = gated_delta_workspace(&s, &q, &k, &v, &d_o, &ws.bytes);
+        if (st != GEMV_OK) return st;
+      }
+      const StreamMemory own(ws.given ? 0 : ws.bytes, stream);
+      return gated_delta_backward(&s, &d_o, &q, &k, &v, &g, &beta, h0, dstate, &dq, &dk, &dv, &dg, &dbeta, dh0,
+                                  ws.given ? ws.p : own.get(), ws.bytes, stream);
+    });
+  });
+}
+
+// q, k, v, do -> bytes, or a negative status
+PyObject *py_gated_delta_workspace(PyObject *, PyObject *const *a, Py_ssize_t count) {
+  return guarded(count, 4, [&]() {
+    ScalarType type;
+    int64_t dev;
+    const gated_delta_shape s = delta_shape(a[0], a[2], false, &type, &dev);
+    const gemv_heads q = heads_of(a[0], "q", s.batch, s.steps, s.heads_k, s.dk, type, dev),
+                     k = heads_of(a[1], "k", s.batch, s.steps, s.heads_k, s.dk, type, dev),
+                     v = heads_of(a[2], "v", s.batch, s.steps, s.heads, s.dv, type, dev);
+    gemv_heads d_o = {};
+    if (a[3] != Py_None) d_o = heads_of(a[3], "do", s.batch, s.steps, s.heads, s.dv, type, dev);
+    int64_t bytes = 0;
+    const int st = gated_delta_workspace(&s, &q, &k, &v, a[3] != Py_None ? &d_o : nullptr, &bytes);
+    return PyLong_FromLongLong(st == GEMV_OK ? bytes : (int64_t)st);
+  });
+}
+
 template <PyObject *(*FN)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyMethodDef method(const char *name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(FN)), METH_FASTCALL, nullptr};
@@ -338,6 +559,11 @@ extern "C" __attribute__((visibility("default"))) PyObject *PyInit_operators_py(
                                   method<py_gemm_workspace>("gemm_workspace"),
                                   method<py_gated_scan>("gated_scan"),
                                   method<py_gated_scan_backward>("gated_scan_backward"),
+                                  method<py_layer_norm>("layer_norm_fused"),
+                                  method<py_layer_norm_backward>("layer_norm_backward"),
+                                  method<py_gated_delta>("gated_delta"),
+                                  method<py_gated_delta_backward>("gated_delta_backward"),
+                                  method<py_gated_delta_workspace>("gated_delta_workspace"),
                                   {nullptr, nullptr, 0, nullptr}};
   static PyModuleDef module = {PyModuleDef_HEAD_INIT, "operators_py", nullptr, -1, methods, nullptr, nullptr, nullptr,
                                nullptr};
