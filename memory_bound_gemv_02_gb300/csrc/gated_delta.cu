@@ -15,8 +15,6 @@
 namespace gemvk {
 namespace {
 
-constexpr int kRows = 16;  // of the state per warp
-constexpr int kMostWarps = kDeltaMostDk / kRows;
 constexpr float kNoDecay = -87.3f;  // below it exp() leaves fp32's normal range: counts as 0
 
 template <int TYPE>
@@ -29,78 +27,115 @@ __device__ __forceinline__ float gate(const HeadsOf &h, bool f32, int64_t b, int
   return f32 ? static_cast<const float *>(h.p)[at] : Elem<TYPE>::get(static_cast<const uint16_t *>(h.p)[at]);
 }
 
-// A CTA holds the state's columns [32 CW s, 32 CW (s + 1)) of one head: 16 rows per
-// warp, CW columns per lane (side by side where VECTOR, else 32 apart).  Sums over the rows
-// meet in shared memory, one barrier per step: sets of partial sums take turns, and
-// three of q and k, as a warp may be a step ahead of another.
-template <int TYPE, int CW, bool VECTOR>
-__global__ void __launch_bounds__(kMostWarps * 32) delta_steps_kernel(const DeltaParams p) {
-  __shared__ float kq[3][2][kDeltaMostDk];
-  __shared__ float2 part[2][kMostWarps][32 * CW];
+// A CTA holds the state's columns [32 CW s, 32 CW (s + 1)) of one head: RW rows per warp, CW
+// columns per lane (side by side where VECTOR, else 32 apart).  Sums over the rows meet in shared
+// memory, one barrier per step: sets of partial sums take turns, and three of q and
+// k, as a warp may be a step ahead of another.  What a step reads is requested two steps
+// before for q and k, one before for v and the gates.
+template <int TYPE, int RW, int CW, bool VECTOR>
+__global__ void __launch_bounds__(kDeltaMostDk / RW * 32) delta_steps_kernel(const DeltaParams p) {
+  constexpr int kWarps = kDeltaMostDk / RW, kColumns = 32 * CW;
+  __shared__ __align__(16) float kq[3][2][kDeltaMostDk];
+  __shared__ __align__(16) float part[2][2][kWarps][kColumns];  // of S^T k, S^T q
   __shared__ float products[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t b = blockIdx.z, head = blockIdx.y, head_k = head / (p.heads / p.heads_k);
-  const int col0 = blockIdx.x * 32 * CW;
-  auto column = [&](int c) { return col0 + (VECTOR ? lane * CW + c : lane + 32 * c); };
+  const int col0 = blockIdx.x * kColumns;
+  auto local = [&](int c) { return VECTOR ? lane * CW + c : lane + 32 * c; };
+  auto there = [&](int c) { return col0 + local(c) < p.dv_size; };
   wait_for_predecessor();
-  float S[kRows][CW];
+  float S[RW][CW];
   const float *const from = p.h0 ? p.h0 + (b * p.heads + head) * p.dk_size * (int64_t)p.dv_size : nullptr;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int row = warp * kRows + r;
+  for (int r = 0; r < RW; ++r) {
+    const int row = warp * RW + r;
 #pragma unroll
     for (int c = 0; c < CW; ++c) S[r][c] = 0.f;
     if (from == nullptr || row >= p.dk_size) continue;
-    const float *const at = from + (int64_t)row * p.dv_size;
-    if constexpr (VECTOR && CW == 4) {
-      if (column(0) < p.dv_size) {
-        const float4 v = *reinterpret_cast<const float4 *>(at + column(0));
-        S[r][0] = v.x; S[r][1] = v.y; S[r][2] = v.z; S[r][3] = v.w;
+    const float *const at = from + (int64_t)row * p.dv_size + col0;
+    if constexpr (VECTOR && CW == 2) {
+      if (there(0)) {
+        const float2 v = *reinterpret_cast<const float2 *>(at + local(0));
+        S[r][0] = v.x;
+        S[r][1] = v.y;
       }
     } else {
 #pragma unroll
       for (int c = 0; c < CW; ++c)
-        if (column(c) < p.dv_size) S[r][c] = at[column(c)];
+        if (there(c)) S[r][c] = at[local(c)];
     }
   }
-  // q and k of a step: each thread one element of either
-  auto fetch = [&](int t, float &k, float &q) {
-    k = q = 0.f;
-    const int i = threadIdx.x;
-    if (t < p.steps && i < p.dk_size) {
-      k = element<TYPE>(p.k, b, t, head_k, i);
-      q = element<TYPE>(p.q, b, t, head_k, i);
+  // q and k of a step, an element or more of both per thread
+  constexpr int kMine = RW / 32 > 0 ? RW / 32 : 1;
+  auto fetch = [&](int t, float (&k)[kMine], float (&q)[kMine]) {
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int i = threadIdx.x + m * blockDim.x;
+      k[m] = q[m] = 0.f;
+      if (t < p.steps && i < p.dk_size) {
+        k[m] = element<TYPE>(p.k, b, t, head_k, i);
+        q[m] = element<TYPE>(p.q, b, t, head_k, i);
+      }
     }
   };
-  auto keep = [&](int t, float k, float q) {
-    if (threadIdx.x < kDeltaMostDk) {
-      kq[t % 3][0][threadIdx.x] = k;
-      kq[t % 3][1][threadIdx.x] = q;
+  auto keep = [&](int t, const float (&k)[kMine], const float (&q)[kMine]) {
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int i = threadIdx.x + m * blockDim.x;
+      if (i < kDeltaMostDk) {
+        kq[t % 3][0][i] = k[m];
+        kq[t % 3][1][i] = q[m];
+      }
     }
   };
-  float k_next, q_next;
+  struct Step {
+    float v[CW], g, beta;
+  };
+  auto fetch_step = [&](int t) {
+    Step s = {};
+    if (t < p.steps) {
+#pragma unroll
+      for (int c = 0; c < CW; ++c)
+        if (there(c)) s.v[c] = element<TYPE>(p.v, b, t, head, col0 + local(c));
+      s.g = gate<TYPE>(p.g, p.gates_f32, b, t, head);
+      s.beta = gate<TYPE>(p.beta, p.gates_f32, b, t, head);
+    }
+    return s;
+  };
+  float k_next[kMine], q_next[kMine];
   fetch(0, k_next, q_next);
+  Step next = fetch_step(0);
   keep(0, k_next, q_next);
+  fetch(1, k_next, q_next);
   __syncthreads();
   for (int t = 0; t < p.steps; ++t) {
-    float v[CW];
-#pragma unroll
-    for (int c = 0; c < CW; ++c) v[c] = column(c) < p.dv_size ? element<TYPE>(p.v, b, t, head, column(c)) : 0.f;
-    const float g = gate<TYPE>(p.g, p.gates_f32, b, t, head), beta = gate<TYPE>(p.beta, p.gates_f32, b, t, head);
-    const float a = g < kNoDecay ? 0.f : expf(g);
-    fetch(t + 1, k_next, q_next);
-    const float *const k = kq[t % 3][0] + warp * kRows, *const q = kq[t % 3][1] + warp * kRows;
+    const Step now = next;
+    next = fetch_step(t + 1);
+    const float a = now.g < kNoDecay ? 0.f : expf(now.g);
+    const float *const k = kq[t % 3][0] + warp * RW, *const q = kq[t % 3][1] + warp * RW;
     float ks[CW] = {}, qs[CW] = {};
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int r = 0; r < RW; r += 4) {
+      const float4 k4 = *reinterpret_cast<const float4 *>(k + r), q4 = *reinterpret_cast<const float4 *>(q + r);
+      const float kr[4] = {k4.x, k4.y, k4.z, k4.w}, qr[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-      for (int c = 0; c < CW; ++c) {
-        ks[c] = fmaf(k[r], S[r][c], ks[c]);
-        qs[c] = fmaf(q[r], S[r][c], qs[c]);
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (CW == 2) {
+          fma2(ks[0], ks[1], kr[e], kr[e], S[r + e][0], S[r + e][1], ks[0], ks[1]);
+          fma2(qs[0], qs[1], qr[e], qr[e], S[r + e][0], S[r + e][1], qs[0], qs[1]);
+        } else {
+          ks[0] = fmaf(kr[e], S[r + e][0], ks[0]);
+          qs[0] = fmaf(qr[e], S[r + e][0], qs[0]);
+        }
       }
+    }
 #pragma unroll
-    for (int c = 0; c < CW; ++c) part[t & 1][warp][VECTOR ? lane * CW + c : lane + 32 * c] = make_float2(ks[c], qs[c]);
-    if (warp == 0) {  // q . k
+    for (int c = 0; c < CW; ++c) {
+      part[t & 1][0][warp][local(c)] = ks[c];
+      part[t & 1][1][warp][local(c)] = qs[c];
+    }
+    const bool mine = warp == t % warps;  // the warp that writes this step's output
+    if (mine) {
       float dot = 0.f;
       for (int i = lane; i < p.dk_size; i += 32) dot = fmaf(kq[t % 3][0][i], kq[t % 3][1][i], dot);
 #pragma unroll
@@ -108,63 +143,71 @@ __global__ void __launch_bounds__(kMostWarps * 32) delta_steps_kernel(const Delt
       if (lane == 0) products[t & 1] = dot;
     }
     keep(t + 1, k_next, q_next);
+    fetch(t + 2, k_next, q_next);
     __syncthreads();
     float d[CW];
 #pragma unroll
-    for (int c = 0; c < CW; ++c) ks[c] = 0.f;
-    for (int w = 0; w < warps; ++w)
-#pragma unroll
-      for (int c = 0; c < CW; ++c) ks[c] += part[t & 1][w][VECTOR ? lane * CW + c : lane + 32 * c].x;
-#pragma unroll
-    for (int c = 0; c < CW; ++c) d[c] = beta * (v[c] - a * ks[c]);
-    if (warp == 0) {
+    for (int c = 0; c < CW; ++c) {
+      float sum = 0.f;
+      for (int w = 0; w < warps; ++w) sum += part[t & 1][0][w][local(c)];
+      d[c] = now.beta * (now.v[c] - a * sum);
+    }
+    if (mine) {
 #pragma unroll
       for (int c = 0; c < CW; ++c) {
         float sum = 0.f;
-        for (int w = 0; w < warps; ++w) sum += part[t & 1][w][VECTOR ? lane * CW + c : lane + 32 * c].y;
+        for (int w = 0; w < warps; ++w) sum += part[t & 1][1][w][local(c)];
         const float o = p.scale * fmaf(products[t & 1], d[c], a * sum);
-        if (column(c) < p.dv_size)
-          static_cast<uint16_t *>(const_cast<void *>(p.o.p))[b * p.o.batch + t * p.o.step + head * p.o.head + column(c)] =
+        if (there(c))
+          static_cast<uint16_t *>(const_cast<void *>(p.o.p))[b * p.o.batch + t * p.o.step + head * p.o.head + col0 + local(c)] =
               Elem<TYPE>::put(o);
       }
     }
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const float kr = k[r];
+    for (int r = 0; r < RW; r += 4) {
+      const float4 k4 = *reinterpret_cast<const float4 *>(k + r);
+      const float kr[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-      for (int c = 0; c < CW; ++c) S[r][c] = fmaf(kr, d[c], a * S[r][c]);
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (CW == 2) {
+          mul2(S[r + e][0], S[r + e][1], a, a, S[r + e][0], S[r + e][1]);
+          fma2(S[r + e][0], S[r + e][1], kr[e], kr[e], d[0], d[1], S[r + e][0], S[r + e][1]);
+        } else {
+          S[r + e][0] = fmaf(kr[e], d[0], a * S[r + e][0]);
+        }
+      }
     }
   }
   if (p.state == nullptr) return;
   float *const to = p.state + (b * p.heads + head) * p.dk_size * (int64_t)p.dv_size;
 #pragma unroll
-  for (int r = 0; r < kRows; ++r) {
-    const int row = warp * kRows + r;
+  for (int r = 0; r < RW; ++r) {
+    const int row = warp * RW + r;
     if (row >= p.dk_size) continue;
-    float *const at = to + (int64_t)row * p.dv_size;
-    if constexpr (VECTOR && CW == 4) {
-      if (column(0) < p.dv_size) *reinterpret_cast<float4 *>(at + column(0)) = make_float4(S[r][0], S[r][1], S[r][2], S[r][3]);
+    float *const at = to + (int64_t)row * p.dv_size + col0;
+    if constexpr (VECTOR && CW == 2) {
+      if (there(0)) *reinterpret_cast<float2 *>(at + local(0)) = make_float2(S[r][0], S[r][1]);
     } else {
 #pragma unroll
       for (int c = 0; c < CW; ++c)
-        if (column(c) < p.dv_size) at[column(c)] = S[r][c];
+        if (there(c)) at[local(c)] = S[r][c];
     }
   }
 }
 
 template <int TYPE>
 int launch_steps(const DeltaParams &p, int sms, cudaStream_t stream) {
-  const int threads = (p.dk_size + kRows - 1) / kRows * 32;
   const int64_t heads = (int64_t)p.batch * p.heads;
-  auto grid = [&](int cw) {
-    return dim3((unsigned)((p.dv_size + 32 * cw - 1) / (32 * cw)), (unsigned)p.heads, (unsigned)p.batch);
+  auto grid = [&](int columns) {
+    return dim3((unsigned)((p.dv_size + columns - 1) / columns), (unsigned)p.heads, (unsigned)p.batch);
   };
-  const bool vector = p.dv_size % 4 == 0 && ((uintptr_t)p.h0 | (uintptr_t)p.state) % 16 == 0;
-  // Wide columns once they fill the GPU; narrow ones spread a few heads over its SMs.
-  if (heads * ((p.dv_size + 127) / 128) >= 2 * sms && p.dv_size > 64)
-    return vector ? launch_op(delta_steps_kernel<TYPE, 4, true>, grid(4), threads, 0, 1, stream, p)
-                  : launch_op(delta_steps_kernel<TYPE, 4, false>, grid(4), threads, 0, 1, stream, p);
-  return launch_op(delta_steps_kernel<TYPE, 1, false>, grid(1), threads, 0, 1, stream, p);
+  auto threads = [&](int rows) { return (p.dk_size + rows - 1) / rows * 32; };
+  const bool vector = p.dv_size % 2 == 0 && ((uintptr_t)p.h0 | (uintptr_t)p.state) % 8 == 0;
+  // Wide parts of the state once they fill the GPU; narrow ones spread a few heads over its SMs.
+  if (heads * ((p.dv_size + 63) / 64) >= 2 * sms && p.dv_size > 32)
+    return vector ? launch_op(delta_steps_kernel<TYPE, 32, 2, true>, grid(64), threads(32), 0, 1, stream, p)
+                  : launch_op(delta_steps_kernel<TYPE, 32, 2, false>, grid(64), threads(32), 0, 1, stream, p);
+  return launch_op(delta_steps_kernel<TYPE, 16, 1, false>, grid(32), threads(16), 0, 1, stream, p);
 }
 
 // A warp per row.

@@ -17,8 +17,10 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ops_internal.h"
+#include "tc_ptx.cuh"
 
 namespace gemvk {
 namespace {
@@ -26,7 +28,9 @@ namespace {
 constexpr int kRowThreadsMax = 1024;
 constexpr int kSmallThreads = 256;  // of CTAs that hold several rows
 constexpr int kLongThreads = 512;
-constexpr int kScalarUnits = 8;     // elements per thread where rows are not on 16 bytes
+constexpr int kScalarUnits = 8;     // elements per thread of rows within a warp that are not on 16 bytes
+constexpr int kMostStages = 4;      // rows of the ring in shared memory
+constexpr int kRingBytes = 220 * 1024;
 constexpr int kPartials = 304;      // most CTAs of the gradient: two for each of 152 SMs
 constexpr int kColumnThreads = 256;
 // Below this variance (with its eps) squares may have been lost in fp32's subnormals.
@@ -40,6 +44,7 @@ struct LayerNormParams {
   float eps;
   int32_t w_f32;
   int32_t tpr;  // threads per row: a power of two up to 32, or the whole CTA
+  int32_t stages, params_vector;  // of the ring; weight and bias on 16 bytes
 };
 
 struct LayerNormGradParams {
@@ -50,6 +55,7 @@ struct LayerNormGradParams {
   int64_t lddy, lds, ldds, lddx, rows, d;
   int32_t w_f32;
   int32_t tpr;
+  int32_t stages, params_vector;
 };
 
 struct ColumnSumParams {
@@ -113,10 +119,13 @@ struct Access {
   typedef Elem<TYPE> E;
   typedef typename E::raw raw;
   static constexpr int V = VECTOR ? E::VEC : 1;
-  static __device__ __forceinline__ void load(const void *row, int64_t u, float (&f)[V]) {
-    if constexpr (VECTOR) E::unpack(reinterpret_cast<const uint4 *>(row)[u], f);
-    else f[0] = E::get(static_cast<const raw *>(row)[u]);
+  typedef std::conditional_t<VECTOR, uint4, raw> Unit;
+  static __device__ __forceinline__ Unit fetch(const void *row, int64_t u) { return static_cast<const Unit *>(row)[u]; }
+  static __device__ __forceinline__ void widen(const Unit &v, float (&f)[V]) {
+    if constexpr (VECTOR) E::unpack(v, f);
+    else f[0] = E::get(v);
   }
+  static __device__ __forceinline__ void load(const void *row, int64_t u, float (&f)[V]) { widen(fetch(row, u), f); }
   static __device__ __forceinline__ void store(void *row, int64_t u, const float (&f)[V]) {
     if constexpr (VECTOR) reinterpret_cast<uint4 *>(row)[u] = E::pack(f);
     else static_cast<raw *>(row)[u] = E::put(f[0]);
@@ -148,50 +157,374 @@ __device__ __forceinline__ void *row_at(void *p, int64_t row, int64_t ld, int es
   return static_cast<char *>(p) + row * ld * es;
 }
 
-// Rows of up to U units per thread, in registers.
+// Rows of a CTA, copied ahead into shared memory.  Every warp copies what it will read
+// itself, 32 units of 16 bytes side by side per tensor and turn, so a row's arrival is
+// waited for by the warp alone: no barrier, and none to poll.  SHIFT: rows that do not start on 16
+// bytes take the aligned blocks that cover them, one more per warp.
+template <int TYPE, bool SHIFT, int U, int TENSORS>
+struct RowRing {
+  typedef Elem<TYPE> E;
+  static constexpr int V = E::VEC, ES = (int)sizeof(typename E::raw), kBlocks = SHIFT ? 33 : 32;
+  static __host__ __device__ int64_t stage_bytes(int threads, int tensors) {
+    return (int64_t)tensors * U * (threads / 32) * kBlocks * 16;
+  }
+  char *base;
+  int units, row_bytes, threads;
+  __device__ __forceinline__ char *slot(int stage, int tensor, int i) const {
+    return base + (((stage * TENSORS + tensor) * U + i) * (threads / 32) + (int)(threadIdx.x >> 5)) * (kBlocks * 16);
+  }
+  __device__ __forceinline__ void request(int stage, int tensor, const void *row) const {
+    const uintptr_t start = (uintptr_t)row & ~(uintptr_t)15;
+    const int bytes = row_bytes + (SHIFT ? (int)((uintptr_t)row & 15) : 0), lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = (int)threadIdx.x + i * threads;
+      const uint32_t to = smem_u32(slot(stage, tensor, i));
+      if (u * 16 < bytes) copy_ahead(to + lane * 16, start + (int64_t)u * 16);
+      if (SHIFT && lane == 31 && (u + 1) * 16 < bytes) copy_ahead(to + 32 * 16, start + (int64_t)(u + 1) * 16);
+    }
+  }
+  // Unit i of this thread in a row that has arrived, zeros behind its end.
+  __device__ __forceinline__ void get(int stage, int tensor, int i, const void *row, int d, float (&f)[V]) const {
+    const uint4 *const at = reinterpret_cast<const uint4 *>(slot(stage, tensor, i)) + (threadIdx.x & 31);
+    uint4 v = at[0];
+    if constexpr (SHIFT) {
+      const int off = (int)((uintptr_t)row & 15);
+      if (off) v = shifted(v, at[1], off);
+    }
+    E::unpack(v, f);
+    if constexpr (SHIFT) {
+      const int u = (int)threadIdx.x + i * threads;
+      if (u == units - 1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (u * V + e >= d) f[e] = 0.f;
+      }
+    }
+  }
+  // Unit i of an output row; SHIFT: by way of a slot that has been read.
+  __device__ __forceinline__ void put(int stage, int tensor, int i, void *row, int d, const float (&f)[V]) const {
+    const int lane = threadIdx.x & 31, u = (int)threadIdx.x + i * threads;
+    if constexpr (!SHIFT) {
+      if (u < units) reinterpret_cast<uint4 *>(row)[u] = E::pack(f);
+    } else {
+      typedef typename E::raw raw;
+      char *const from = slot(stage, tensor, i);
+      __syncwarp();  // the neighbours have read it
+      reinterpret_cast<uint4 *>(from)[lane] = E::pack(f);
+      __syncwarp();
+      const int first = (u - lane) * V;  // elements of this warp: [first, first + n)
+      const int n = d - first < 32 * V ? d - first : 32 * V;
+      if (n <= 0) return;
+      raw *const to = static_cast<raw *>(row) + first;
+      int head = (int)((16 - ((uintptr_t)to & 15)) & 15) / ES;
+      if (head > n) head = n;
+      const int vectors = (n - head) / V, tail = n - head - vectors * V;
+      const raw *const staged = reinterpret_cast<const raw *>(from);
+      const int off = head * ES;
+      if (lane < head) to[lane] = staged[lane];
+      if (lane < vectors) {
+        const uint4 *const at = reinterpret_cast<const uint4 *>(from) + lane;
+        reinterpret_cast<uint4 *>(to + head)[lane] = off ? shifted(at[0], at[1], off) : at[0];
+      }
+      if (lane < tail) to[n - tail + lane] = staged[n - tail + lane];
+    }
+  }
+  static __device__ __forceinline__ void copy_ahead(uint32_t to, uintptr_t from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  }
+};
+
+__device__ __forceinline__ void ring_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the `ahead` youngest groups have arrived, for the whole warp.
+__device__ __forceinline__ void ring_wait(int ahead) {
+  if (ahead >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (ahead == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (ahead == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+}
+
+// Unit u of a parameter vector, with 16-byte loads where it starts on 16 bytes.
+template <int TYPE>
+__device__ __forceinline__ void ring_param(const void *w, bool f32, bool vector, int u, int d, float (&f)[Elem<TYPE>::VEC]) {
+  constexpr int V = Elem<TYPE>::VEC;
+  if (vector && (u + 1) * V <= d) {
+    Access<TYPE, true>::param(w, f32, u, f);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    float v[1] = {0.f};
+    if (u * V + e < d) Access<TYPE, false>::param(w, f32, u * V + e, v);
+    f[e] = v[0];
+  }
+}
+
+// Rows longer than a warp holds: a CTA takes a row at a time.  Memory-bound; while a row's two reductions run, the
+// rows ahead arrive in shared memory.
+template <int TYPE, bool SHIFT, int U>
+__global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const LayerNormParams p) {
+  typedef RowRing<TYPE, SHIFT, U, 2> Ring;
+  constexpr int V = Ring::V, ES = Ring::ES;
+  extern __shared__ __align__(16) char ring_memory[];
+  __shared__ float2 part[2][32];
+  int turn = 0;
+  const int threads = blockDim.x, d = (int)p.d;
+  const Ring ring{ring_memory, (d + V - 1) / V, d * ES, threads};
+  const float n = (float)p.d;
+  wait_for_predecessor();
+  auto request = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+      ring.request(stage, 0, row_at(p.x, row, p.ldx, ES));
+      if (p.r) ring.request(stage, 1, row_at(p.r, row, p.ldr, ES));
+    }
+    ring_close();
+  };
+  for (int s = 0; s < p.stages - 1; ++s) request(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    ring_wait(p.stages - 2);
+    const void *const x = row_at(p.x, row, p.ldx, ES), *const r = p.r ? row_at(p.r, row, p.ldr, ES) : nullptr;
+    float s[U][V];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[i][e] = 0.f;
+      if ((int)threadIdx.x + i * threads < ring.units) {
+        ring.get(stage, 0, i, x, d, s[i]);
+        if (r) {
+          float t[V];
+          ring.get(stage, 1, i, r, d, t);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], t[e], t[e + 1]);
+        }
+      }
+    }
+    if (p.ro) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) ring.put(stage, 1, i, row_at(p.ro, row, p.ldo, ES), d, s[i]);
+    }
+    float scale = 1.f, mean, fix, rstd;
+    for (bool again = false;; again = true) {
+      float sum = 0.f, more = 0.f;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int e = 0; e < V; e += 2) add2(sum, more, sum, more, s[i][e], s[i][e + 1]);
+      sum += more;
+      more = 0.f;
+      row_sums(sum, more, threads, part, turn);
+      if (!again) {  // every warp has read the row before: its place is free
+        const int next = stage == 0 ? p.stages - 1 : stage - 1;
+        request(row + (int64_t)(p.stages - 1) * gridDim.x, next);
+      }
+      mean = sum / n;
+      float off = 0.f, square = 0.f;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int u = (int)threadIdx.x + i * threads;
+        if (u >= ring.units) continue;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          if (SHIFT && u * V + e >= d) continue;
+          const float c = s[i][e] - mean;
+          off += c;
+          square = fmaf(c, c, square);
+        }
+      }
+      row_sums(off, square, threads, part, turn);
+      fix = off / n;
+      const float v = fmaxf(fmaf(-fix, fix, square / n), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
+      rstd = 1.f / sqrtf(v);
+      if (!(square <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
+      if (again || (square <= 3.4028235e38f && v >= kTinyVariance)) break;
+      float top = 0.f;  // rare: squares beyond fp32's range, or all but lost below it
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) top = fmaxf(top, fabsf(s[i][e]));
+      scale = row_scale(row_max(top, threads, part, turn), p.eps);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[i][e] *= scale;
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = (mean + fix) / scale;
+      if (p.rstd) p.rstd[row] = rstd * scale;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = (int)threadIdx.x + i * threads;
+      if (u < ring.units) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[i][e] = ((s[i][e] - mean) - fix) * rstd;
+        float w[V];
+        if (p.w) {
+          ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) mul2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+        }
+        if (p.b) {
+          ring_param<TYPE>(p.b, p.w_f32, p.params_vector, u, d, w);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+        }
+      }
+      ring.put(stage, 0, i, row_at(p.y, row, p.ldy, ES), d, s[i]);
+    }
+    stage = stage + 1 == p.stages ? 0 : stage + 1;
+  }
+  ring_wait(0);
+}
+
+// The gradient of such rows: one reduction per row, the columns' sums in registers.
+template <int TYPE, bool SHIFT, int U>
+__global__ void __launch_bounds__(kRowThreadsMax) layer_norm_grad_ring_kernel(const LayerNormGradParams p) {
+  typedef RowRing<TYPE, SHIFT, U, 3> Ring;
+  constexpr int V = Ring::V, ES = Ring::ES;
+  extern __shared__ __align__(16) char ring_memory[];
+  __shared__ float2 part[2][32];
+  int turn = 0;
+  const int threads = blockDim.x, d = (int)p.d;
+  const Ring ring{ring_memory, (d + V - 1) / V, d * ES, threads};
+  const float n = (float)p.d;
+  float dw[U][V] = {}, db[U][V] = {};
+  wait_for_predecessor();
+  auto request = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+      ring.request(stage, 0, row_at(p.s, row, p.lds, ES));
+      ring.request(stage, 1, row_at(p.dy, row, p.lddy, ES));
+      if (p.ds) ring.request(stage, 2, row_at(p.ds, row, p.ldds, ES));
+    }
+    ring_close();
+  };
+  for (int s = 0; s < p.stages - 1; ++s) request(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const float mean = p.mean[row], rstd = p.rstd[row];
+    ring_wait(p.stages - 2);
+    const void *const s = row_at(p.s, row, p.lds, ES), *const dy = row_at(p.dy, row, p.lddy, ES),
+               *const ds = p.ds ? row_at(p.ds, row, p.ldds, ES) : nullptr;
+    float xh[U][V], t[U][V];
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = (int)threadIdx.x + i * threads;
+#pragma unroll
+      for (int e = 0; e < V; ++e) xh[i][e] = t[i][e] = 0.f;
+      if (u < ring.units) {
+        ring.get(stage, 0, i, s, d, xh[i]);
+        ring.get(stage, 1, i, dy, d, t[i]);  // (0 behind the row's end, whatever xh is there)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          xh[i][e] = (xh[i][e] - mean) * rstd;
+          db[i][e] += t[i][e];
+          dw[i][e] = fmaf(t[i][e], xh[i][e], dw[i][e]);
+        }
+        if (p.w) {
+          float w[V];
+          ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) mul2(t[i][e], t[i][e + 1], t[i][e], t[i][e + 1], w[e], w[e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          a += t[i][e];
+          b = fmaf(t[i][e], xh[i][e], b);
+        }
+      }
+    }
+    row_sums(a, b, threads, part, turn);
+    {  // every warp has read the row before: its place is free
+      const int next = stage == 0 ? p.stages - 1 : stage - 1;
+      request(row + (int64_t)(p.stages - 1) * gridDim.x, next);
+    }
+    a /= n;
+    b /= n;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      float v[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[e] = (t[i][e] - a - xh[i][e] * b) * rstd;
+      if (ds && (int)threadIdx.x + i * threads < ring.units) {
+        float f[V];
+        ring.get(stage, 2, i, ds, d, f);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) add2(v[e], v[e + 1], v[e], v[e + 1], f[e], f[e + 1]);
+      }
+      ring.put(stage, 0, i, row_at(p.dx, row, p.lddx, ES), d, v);
+    }
+    stage = stage + 1 == p.stages ? 0 : stage + 1;
+  }
+  ring_wait(0);
+  if (p.partial == nullptr) return;
+  float *const out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int u = (int)threadIdx.x + i * threads;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int j = u * V + e;
+      if (j >= d) continue;
+      out[j] = dw[i][e];
+      out[d + j] = db[i][e];
+    }
+  }
+}
+
+// Rows of up to a warp, in registers; what the next round needs is requested before this one's sums.
 template <int TYPE, bool VECTOR, int U>
-__global__ void __launch_bounds__(kRowThreadsMax) layer_norm_kernel(const LayerNormParams p) {
+__global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(const LayerNormParams p) {
   typedef Access<TYPE, VECTOR> A;
   constexpr int V = A::V, ES = sizeof(typename A::raw);
   __shared__ float2 part[2][32];
   int turn = 0;
-  const int tpr = p.tpr, rows_here = blockDim.x / tpr;
-  const int at = threadIdx.x % tpr, group = threadIdx.x / tpr;
-  const int64_t units = p.d / V;
+  const int tpr = p.tpr, rows_here = kSmallThreads / tpr;
+  const int at = threadIdx.x % tpr, group = threadIdx.x / tpr, units = (int)(p.d / V);
   const float n = (float)p.d;
+  const int64_t step = (int64_t)gridDim.x * rows_here;
+  typename A::Unit x[U], r[U];
+  auto request = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = at + i * tpr;
+      if (row < p.rows && u < units) {
+        x[i] = A::fetch(row_at(p.x, row, p.ldx, ES), u);
+        if (p.r) r[i] = A::fetch(row_at(p.r, row, p.ldr, ES), u);
+      }
+    }
+  };
   wait_for_predecessor();
-  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < p.rows; row0 += (int64_t)gridDim.x * rows_here) {
+  request((int64_t)blockIdx.x * rows_here + group);
+  for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < p.rows; row0 += step) {
     const int64_t row = row0 + group;
     const bool live = row < p.rows;
     float s[U][V];
-    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t u = at + (int64_t)i * tpr;
 #pragma unroll
       for (int e = 0; e < V; ++e) s[i][e] = 0.f;
-      if (live && u < units) {
-        A::load(row_at(p.x, row, p.ldx, ES), u, s[i]);
+      if (live && at + i * tpr < units) {
+        A::widen(x[i], s[i]);
         if (p.r) {
-          float r[V];
-          A::load(row_at(p.r, row, p.ldr, ES), u, r);
+          float t[V];
+          A::widen(r[i], t);
 #pragma unroll
-          for (int e = 0; e < V; ++e) s[i][e] += r[e];
+          for (int e = 0; e < V; ++e) s[i][e] += t[e];
         }
       }
     }
+    request(row + step);
     if (p.ro && live) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t u = at + (int64_t)i * tpr;
-        if (u < units) A::store(row_at(p.ro, row, p.ldo, ES), u, s[i]);
-      }
+      for (int i = 0; i < U; ++i)
+        if (at + i * tpr < units) A::store(row_at(p.ro, row, p.ldo, ES), at + i * tpr, s[i]);
     }
     float scale = 1.f, mean, fix, rstd;
-    bool again = false;
-    for (;;) {
-      sum = 0.f;
-      float none = 0.f;
+    for (bool again = false;; again = true) {
+      float sum = 0.f, none = 0.f;
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
@@ -201,7 +534,7 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_kernel(const LayerN
       float off = 0.f, square = 0.f;
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (at + (int64_t)i * tpr < units) {
+        if (at + i * tpr < units) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             const float c = s[i][e] - mean;
@@ -211,36 +544,30 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_kernel(const LayerN
         }
       row_sums(off, square, tpr, part, turn);
       fix = off / n;
-      const float var = fmaxf(fmaf(-fix, fix, square / n), 0.f);  // (a NaN becomes 0: square tells)
-      const float v = var + p.eps * scale * scale;
+      const float v = fmaxf(fmaf(-fix, fix, square / n), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
       rstd = 1.f / sqrtf(v);
       if (!(square <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
-      // rare: squares beyond fp32's range, or all but lost below it
-      bool rare = !again && live && (!(square <= 3.4028235e38f) || v < kTinyVariance);
-      if (tpr <= 32) rare = __any_sync(0xffffffffu, rare);
-      if (!rare) break;
-      again = true;
+      // rare: squares beyond fp32's range, or all but lost below it; a warp's rows go together
+      if (again || !__any_sync(0xffffffffu, live && (!(square <= 3.4028235e38f) || v < kTinyVariance))) break;
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) top = fmaxf(top, fabsf(s[i][e]));
-      top = row_max(top, tpr, part, turn);
-      scale = row_scale(top, p.eps);
+      scale = row_scale(row_max(top, tpr, part, turn), p.eps);
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) s[i][e] *= scale;
     }
     if (!live) continue;
-    const float m = mean + fix;
     if (at == 0) {
-      if (p.mean) p.mean[row] = m / scale;
+      if (p.mean) p.mean[row] = (mean + fix) / scale;
       if (p.rstd) p.rstd[row] = rstd * scale;
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t u = at + (int64_t)i * tpr;
+      const int u = at + i * tpr;
       if (u >= units) continue;
       float w[V], b[V];
       if (p.w) A::param(p.w, p.w_f32, u, w);
@@ -342,48 +669,60 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(const Lay
   }
 }
 
-// The gradient of rows of up to U units per thread.
+// The gradient of rows of up to a warp.
 template <int TYPE, bool VECTOR, int U>
-__global__ void __launch_bounds__(kRowThreadsMax) layer_norm_grad_kernel(const LayerNormGradParams p) {
+__global__ void __launch_bounds__(kSmallThreads, 2) layer_norm_grad_small_kernel(const LayerNormGradParams p) {
   typedef Access<TYPE, VECTOR> A;
   constexpr int V = A::V, ES = sizeof(typename A::raw);
-  extern __shared__ float columns[];  // (2, d): the sums of groups before, where rows share a CTA
+  extern __shared__ float columns[];  // (2, d): the sums of the groups before
   __shared__ float2 part[2][32];
   int turn = 0;
-  const int tpr = p.tpr, groups = blockDim.x / tpr;
-  const int at = threadIdx.x % tpr, group = threadIdx.x / tpr;
-  const int64_t units = p.d / V;
+  const int tpr = p.tpr, groups = kSmallThreads / tpr;
+  const int at = threadIdx.x % tpr, group = threadIdx.x / tpr, units = (int)(p.d / V);
   const float n = (float)p.d;
+  const int64_t step = (int64_t)gridDim.x * groups;
   float w[U][V], dw[U][V], db[U][V];
+  typename A::Unit s[U], dy[U], ds[U];
+  float mean_next = 0.f, rstd_next = 0.f;
+  auto request = [&](int64_t row) {
+    if (row >= p.rows) return;
+    mean_next = p.mean[row];
+    rstd_next = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = at + i * tpr;
+      if (u < units) {
+        s[i] = A::fetch(row_at(p.s, row, p.lds, ES), u);
+        dy[i] = A::fetch(row_at(p.dy, row, p.lddy, ES), u);
+        if (p.ds) ds[i] = A::fetch(row_at(p.ds, row, p.ldds, ES), u);
+      }
+    }
+  };
   wait_for_predecessor();
+  request((int64_t)blockIdx.x * groups + group);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    const int64_t u = at + (int64_t)i * tpr;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       w[i][e] = 1.f;
       dw[i][e] = db[i][e] = 0.f;
     }
-    if (p.w && u < units) A::param(p.w, p.w_f32, u, w[i]);
+    if (p.w && at + i * tpr < units) A::param(p.w, p.w_f32, at + i * tpr, w[i]);
   }
-  for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < p.rows; row0 += (int64_t)gridDim.x * groups) {
+  for (int64_t row0 = (int64_t)blockIdx.x * groups; row0 < p.rows; row0 += step) {
     const int64_t row = row0 + group;
     const bool live = row < p.rows;
-    float xh[U][V], t[U][V];
-    float mean = 0.f, rstd = 0.f;
-    if (live) {
-      mean = p.mean[row];
-      rstd = p.rstd[row];
-    }
+    float xh[U][V], t[U][V], more[U][V];
+    const float mean = mean_next, rstd = rstd_next;
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t u = at + (int64_t)i * tpr;
 #pragma unroll
-      for (int e = 0; e < V; ++e) xh[i][e] = t[i][e] = 0.f;
-      if (live && u < units) {
-        A::load(row_at(p.s, row, p.lds, ES), u, xh[i]);
-        A::load(row_at(p.dy, row, p.lddy, ES), u, t[i]);
+      for (int e = 0; e < V; ++e) xh[i][e] = t[i][e] = more[i][e] = 0.f;
+      if (live && at + i * tpr < units) {
+        A::widen(s[i], xh[i]);
+        A::widen(dy[i], t[i]);
+        if (p.ds) A::widen(ds[i], more[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           xh[i][e] = (xh[i][e] - mean) * rstd;
@@ -395,57 +734,39 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_grad_kernel(const L
         }
       }
     }
+    request(row + step);
     row_sums(a, b, tpr, part, turn);
     a /= n;
     b /= n;
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t u = at + (int64_t)i * tpr;
+      const int u = at + i * tpr;
       if (u >= units) continue;
-      float ds[V];
-      if (p.ds) A::load(row_at(p.ds, row, p.ldds, ES), u, ds);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float v = (t[i][e] - a - xh[i][e] * b) * rstd;
-        if (p.ds) v += ds[e];
-        t[i][e] = v;
-      }
+      for (int e = 0; e < V; ++e) t[i][e] = (t[i][e] - a - xh[i][e] * b) * rstd + more[i][e];
       A::store(row_at(p.dx, row, p.lddx, ES), u, t[i]);
     }
   }
   if (p.partial == nullptr) return;
   float *const out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
-  if (groups == 1) {
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int64_t u = at + (int64_t)i * tpr;
-      if (u >= units) continue;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        out[u * V + e] = dw[i][e];
-        out[p.d + u * V + e] = db[i][e];
-      }
-    }
-    return;
-  }
-  for (int turn_of = 0; turn_of < groups; ++turn_of) {
+  for (int of = 0; of < groups; ++of) {
     __syncthreads();
-    if (group != turn_of) continue;
+    if (group != of) continue;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int64_t u = at + (int64_t)i * tpr;
+      const int u = at + i * tpr;
       if (u >= units) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         const int64_t j = u * V + e;
-        columns[j] = turn_of == 0 ? dw[i][e] : columns[j] + dw[i][e];
-        columns[p.d + j] = turn_of == 0 ? db[i][e] : columns[p.d + j] + db[i][e];
+        columns[j] = of == 0 ? dw[i][e] : columns[j] + dw[i][e];
+        columns[p.d + j] = of == 0 ? db[i][e] : columns[p.d + j] + db[i][e];
       }
     }
   }
   __syncthreads();
-  for (int j = threadIdx.x; j < 2 * p.d; j += blockDim.x) out[j] = columns[j];
+  for (int j = threadIdx.x; j < 2 * p.d; j += kSmallThreads) out[j] = columns[j];
 }
 
 // Rows of any length: dx alone, the row read twice.
@@ -546,52 +867,96 @@ __global__ void __launch_bounds__(kColumnThreads) layer_norm_fold_kernel(const C
   }
 }
 
-struct Shape {
-  int tpr, threads;
-  bool held;  // in registers
-};
-
-// Threads for rows of `units` units with u of them per thread: part of a warp,
-// or a CTA of whole warps.
-Shape row_shape(int64_t units, int u) {
-  const int64_t need = (units + u - 1) / u;
-  if (need > kRowThreadsMax) return {kLongThreads, kLongThreads, false};
-  if (need > 32) return {(int)((need + 31) / 32 * 32), (int)((need + 31) / 32 * 32), true};
+// Rows within part of a warp: threads per row.
+int small_row(int64_t units, int u) {
   int tpr = 1;
-  while (tpr < need) tpr *= 2;
-  return {tpr, kSmallThreads, true};
+  while (tpr * u < units) tpr *= 2;
+  return tpr;
+}
+
+// The ring of rows of `units` units, U per thread: threads, CTAs per SM, stages and bytes.
+struct RingShape {
+  int threads, per_sm, stages;
+  size_t bytes;
+};
+template <class Ring, int U>
+RingShape ring_shape(int64_t units, int tensors) {
+  RingShape r;
+  r.threads = (int)((units + 32 * U - 1) / (32 * U) * 32);
+  r.per_sm = kRowThreadsMax / r.threads < 16 ? kRowThreadsMax / r.threads : 16;  // 64 registers each
+  const int64_t stage = Ring::stage_bytes(r.threads, tensors);
+  r.stages = kMostStages;
+  while (r.stages > 2 && r.per_sm * (r.stages * stage + 1024) > kRingBytes) --r.stages;
+  while (r.per_sm > 1 && r.per_sm * (r.stages * stage + 1024) > kRingBytes) --r.per_sm;
+  r.bytes = (size_t)(r.stages * stage);
+  return r;
+}
+
+template <class P>
+int launch_ring(void (*fn)(P), const RingShape &r, int64_t grid, cudaStream_t stream, const P &p) {
+  if (r.bytes > 40 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return cuda_failure((int)e);
+    }
+  }
+  return launch_op(fn, dim3((unsigned)grid), r.threads, r.bytes, 1, stream, p);
+}
+
+template <int TYPE, bool SHIFT, int U>
+int launch_norm_ring(LayerNormParams p, int sms, cudaStream_t stream) {
+  typedef RowRing<TYPE, SHIFT, U, 2> Ring;
+  const RingShape r = ring_shape<Ring, U>((p.d + Ring::V - 1) / Ring::V, 2);
+  p.stages = r.stages;
+  const int64_t grid = p.rows < (int64_t)sms * r.per_sm ? p.rows : (int64_t)sms * r.per_sm;
+  return launch_ring(layer_norm_ring_kernel<TYPE, SHIFT, U>, r, grid, stream, p);
 }
 
 template <int TYPE, bool VECTOR>
 int launch_norm(LayerNormParams p, int sms, cudaStream_t stream) {
-  constexpr int V = Access<TYPE, VECTOR>::V, U = VECTOR ? 2 : kScalarUnits;
-  const int64_t units = p.d / V;
-  const Shape s = row_shape(units, U);
-  if (!s.held) {
-    const int64_t grid = p.rows < (int64_t)sms * 4 ? p.rows : (int64_t)sms * 4;
-    return launch_op(layer_norm_long_kernel<TYPE, VECTOR>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
+  constexpr int V = Access<TYPE, VECTOR>::V, U = VECTOR ? 2 : kScalarUnits, W = Elem<TYPE>::VEC;
+  const int64_t units = p.d / V, blocks = (p.d + W - 1) / W;
+  if (units <= 32 * U) {
+    p.tpr = small_row(units, U);
+    const int64_t here = kSmallThreads / p.tpr, ctas = (p.rows + here - 1) / here, most = (int64_t)sms * 4;
+    return launch_op(layer_norm_small_kernel<TYPE, VECTOR, U>, dim3((unsigned)(ctas < most ? ctas : most)), kSmallThreads,
+                     0, 1, stream, p);
   }
-  p.tpr = s.tpr;
-  const int64_t here = s.threads / s.tpr, ctas = (p.rows + here - 1) / here;
-  return launch_op(layer_norm_kernel<TYPE, VECTOR, U>, dim3((unsigned)(ctas < (1 << 20) ? ctas : 1 << 20)), s.threads, 0,
-                   1, stream, p);
+  if (blocks <= 512) return launch_norm_ring<TYPE, !VECTOR, 1>(p, sms, stream);
+  if (blocks <= 2 * kRowThreadsMax) return launch_norm_ring<TYPE, !VECTOR, 2>(p, sms, stream);
+  const int64_t grid = p.rows < (int64_t)sms * 4 ? p.rows : (int64_t)sms * 4;
+  return launch_op(layer_norm_long_kernel<TYPE, VECTOR>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
 }
 
 int partial_count(int64_t rows) { return (int)(rows < kPartials ? rows : kPartials); }
 
+template <int TYPE, bool SHIFT, int U>
+int launch_grad_ring(LayerNormGradParams p, int *count, cudaStream_t stream) {
+  typedef RowRing<TYPE, SHIFT, U, 3> Ring;
+  const RingShape r = ring_shape<Ring, U>((p.d + Ring::V - 1) / Ring::V, 3);
+  p.stages = r.stages;
+  const int most = kPartials / 2 * (r.per_sm < 2 ? 1 : 2);
+  *count = (int)(p.rows < most ? p.rows : most);
+  return launch_ring(layer_norm_grad_ring_kernel<TYPE, SHIFT, U>, r, *count, stream, p);
+}
+
 template <int TYPE, bool VECTOR>
 int launch_grad(LayerNormGradParams p, float *dw, float *db, cudaStream_t stream) {
-  constexpr int V = Access<TYPE, VECTOR>::V, U = VECTOR ? 2 : kScalarUnits;
-  const int64_t units = p.d / V;
-  const Shape s = row_shape(units, U);
-  int st;
-  int count;
-  if (s.held) {
-    p.tpr = s.tpr;
-    const int64_t here = s.threads / s.tpr, ctas = (p.rows + here - 1) / here;
+  constexpr int V = Access<TYPE, VECTOR>::V, U = VECTOR ? 2 : kScalarUnits, W = Elem<TYPE>::VEC;
+  const int64_t units = p.d / V, blocks = (p.d + W - 1) / W;
+  int st, count;
+  if (units <= 32 * U) {
+    p.tpr = small_row(units, U);
+    const int64_t here = kSmallThreads / p.tpr, ctas = (p.rows + here - 1) / here;
     count = partial_count(ctas);
-    st = launch_op(layer_norm_grad_kernel<TYPE, VECTOR, U>, dim3((unsigned)count), s.threads,
-                   here > 1 ? (size_t)p.d * 8 : 0, 1, stream, p);
+    st = launch_op(layer_norm_grad_small_kernel<TYPE, VECTOR, U>, dim3((unsigned)count), kSmallThreads, (size_t)p.d * 8, 1,
+                   stream, p);
+  } else if (blocks <= kRowThreadsMax) {
+    st = launch_grad_ring<TYPE, !VECTOR, 1>(p, &count, stream);
+  } else if (blocks <= 2 * kRowThreadsMax) {
+    st = launch_grad_ring<TYPE, !VECTOR, 2>(p, &count, stream);
   } else {
     count = partial_count(p.rows);
     st = launch_op(layer_norm_grad_long_kernel<TYPE, VECTOR>, dim3((unsigned)count), kLongThreads, 0, 1, stream, p);
@@ -655,10 +1020,11 @@ extern "C" int layer_norm_fused(const void *x, int64_t ldx, const void *residual
   p.x = x; p.r = residual; p.w = weight; p.b = bias; p.y = y; p.ro = residual_out; p.mean = mean; p.rstd = rstd;
   p.ldx = ldx; p.ldr = ldr; p.ldy = ldy; p.ldo = ldo; p.rows = rows; p.d = d; p.eps = eps;
   p.w_f32 = param_dtype == GEMV_TYPE_F32 ? 1 : 0;
+  p.params_vector = on_boundary(weight, 0, es, 1) && on_boundary(bias, 0, es, 1) ? 1 : 0;
   // 16-byte accesses where every row and both parameters start on 16 bytes
   const bool vector = d % (16 / es) == 0 && on_boundary(x, ldx, es, rows) && on_boundary(residual, ldr, es, rows) &&
                       on_boundary(y, ldy, es, rows) && on_boundary(residual_out, ldo, es, rows) &&
-                      on_boundary(weight, 0, es, 1) && on_boundary(bias, 0, es, 1);
+                      p.params_vector;
   if (dtype == GEMV_TYPE_F16)
     return vector ? launch_norm<GEMV_TYPE_F16, true>(p, sms, stream) : launch_norm<GEMV_TYPE_F16, false>(p, sms, stream);
   if (dtype == GEMV_TYPE_BF16)
@@ -724,8 +1090,9 @@ extern "C" int layer_norm_backward(const void *dy, int64_t lddy, const void *s, 
   p.partial = sums ? static_cast<float *>(workspace) : nullptr;
   p.lddy = lddy; p.lds = lds; p.ldds = ldds; p.lddx = lddx; p.rows = rows; p.d = d;
   p.w_f32 = weight_dtype == GEMV_TYPE_F32 ? 1 : 0;
+  p.params_vector = on_boundary(weight, 0, es, 1) ? 1 : 0;
   const bool vector = d % (16 / es) == 0 && on_boundary(dy, lddy, es, rows) && on_boundary(s, lds, es, rows) &&
-                      on_boundary(ds, ldds, es, rows) && on_boundary(dx, lddx, es, rows) && on_boundary(weight, 0, es, 1);
+                      on_boundary(ds, ldds, es, rows) && on_boundary(dx, lddx, es, rows) && p.params_vector;
   if (dtype == GEMV_TYPE_F16)
     return vector ? launch_grad<GEMV_TYPE_F16, true>(p, dweight, dbias, stream)
                   : launch_grad<GEMV_TYPE_F16, false>(p, dweight, dbias, stream);
