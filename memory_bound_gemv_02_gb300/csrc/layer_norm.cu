@@ -87,6 +87,18 @@ __device__ __forceinline__ void row_sums(float &a, float &b, int tpr, float2 (*p
   turn ^= 1;
 }
 
+// The sum of a alone, of CTA-wide rows.
+__device__ __forceinline__ float row_sum(float a, int tpr, float2 (*part)[32], int &turn) {
+  for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[turn][threadIdx.x >> 5].x = a;
+  __syncthreads();
+  a = lane < tpr / 32 ? part[turn][lane].x : 0.f;
+  for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+  turn ^= 1;
+  return a;
+}
+
 __device__ __forceinline__ float row_max(float a, int tpr, float2 (*part)[32], int &turn) {
   const int width = tpr < 32 ? tpr : 32;
   for (int m = width / 2; m > 0; m >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
@@ -168,69 +180,73 @@ struct RowRing {
   static __host__ __device__ int64_t stage_bytes(int threads, int tensors) {
     return (int64_t)tensors * U * (threads / 32) * kBlocks * 16;
   }
-  char *base;
-  int units, row_bytes, threads;
-  __device__ __forceinline__ char *slot(int stage, int tensor, int i) const {
-    return base + (((stage * TENSORS + tensor) * U + i) * (threads / 32) + (int)(threadIdx.x >> 5)) * (kBlocks * 16);
+  char *mine;  // this lane's block of the first stage and tensor
+  int units, row_bytes, threads, turn_bytes;
+  __device__ __forceinline__ RowRing(char *base, int d, int threads)
+      : units((d + V - 1) / V), row_bytes(d * ES), threads(threads), turn_bytes(threads / 32 * kBlocks * 16) {
+    mine = base + ((int)(threadIdx.x >> 5) * kBlocks + (int)(threadIdx.x & 31)) * 16;
   }
-  __device__ __forceinline__ void request(int stage, int tensor, const void *row) const {
-    const uintptr_t start = (uintptr_t)row & ~(uintptr_t)15;
+  __device__ __forceinline__ int stage_size() const { return TENSORS * U * turn_bytes; }
+  // `at`: the stage's offset
+  __device__ __forceinline__ char *slot(int at, int tensor, int i) const { return mine + at + (tensor * U + i) * turn_bytes; }
+  __device__ __forceinline__ void request(int at, int tensor, const char *row) const {
+    const char *const start = SHIFT ? reinterpret_cast<const char *>((uintptr_t)row & ~(uintptr_t)15) : row;
     const int bytes = row_bytes + (SHIFT ? (int)((uintptr_t)row & 15) : 0), lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int u = (int)threadIdx.x + i * threads;
-      const uint32_t to = smem_u32(slot(stage, tensor, i));
-      if (u * 16 < bytes) copy_ahead(to + lane * 16, start + (int64_t)u * 16);
-      if (SHIFT && lane == 31 && (u + 1) * 16 < bytes) copy_ahead(to + 32 * 16, start + (int64_t)(u + 1) * 16);
+      const uint32_t to = smem_u32(slot(at, tensor, i));
+      if (u * 16 < bytes) copy_ahead(to, start + u * 16);
+      if (SHIFT && lane == 31 && (u + 1) * 16 < bytes) copy_ahead(to + 16, start + (u + 1) * 16);
     }
   }
   // Unit i of this thread in a row that has arrived, zeros behind its end.
-  __device__ __forceinline__ void get(int stage, int tensor, int i, const void *row, int d, float (&f)[V]) const {
-    const uint4 *const at = reinterpret_cast<const uint4 *>(slot(stage, tensor, i)) + (threadIdx.x & 31);
-    uint4 v = at[0];
+  __device__ __forceinline__ void get(int at, int tensor, int i, const char *row, float (&f)[V]) const {
+    const uint4 *const from = reinterpret_cast<const uint4 *>(slot(at, tensor, i));
+    uint4 v = from[0];
     if constexpr (SHIFT) {
       const int off = (int)((uintptr_t)row & 15);
-      if (off) v = shifted(v, at[1], off);
+      if (off) v = shifted(v, from[1], off);
     }
     E::unpack(v, f);
-    if constexpr (SHIFT) {
-      const int u = (int)threadIdx.x + i * threads;
-      if (u == units - 1) {
+    if constexpr (SHIFT) clear_tail((int)threadIdx.x + i * threads, f);
+  }
+  __device__ __forceinline__ void clear_tail(int u, float (&f)[V]) const {
+    if (u != units - 1) return;
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (u * V + e >= d) f[e] = 0.f;
-      }
-    }
+    for (int e = 0; e < V; ++e)
+      if ((u * V + e) * ES >= row_bytes) f[e] = 0.f;
   }
   // Unit i of an output row; SHIFT: by way of a slot that has been read.
-  __device__ __forceinline__ void put(int stage, int tensor, int i, void *row, int d, const float (&f)[V]) const {
+  __device__ __forceinline__ void put(int at, int tensor, int i, char *row, const float (&f)[V]) const {
     const int lane = threadIdx.x & 31, u = (int)threadIdx.x + i * threads;
     if constexpr (!SHIFT) {
-      if (u < units) reinterpret_cast<uint4 *>(row)[u] = E::pack(f);
+      if (u < units) *reinterpret_cast<uint4 *>(row + u * 16) = E::pack(f);
     } else {
       typedef typename E::raw raw;
-      char *const from = slot(stage, tensor, i);
+      char *const staged = slot(at, tensor, i);
       __syncwarp();  // the neighbours have read it
-      reinterpret_cast<uint4 *>(from)[lane] = E::pack(f);
+      *reinterpret_cast<uint4 *>(staged) = E::pack(f);
       __syncwarp();
-      const int first = (u - lane) * V;  // elements of this warp: [first, first + n)
+      const char *const from = staged - lane * 16;
+      const int first = (u - lane) * V, d = row_bytes / ES;  // elements of this warp: [first, first + n)
       const int n = d - first < 32 * V ? d - first : 32 * V;
       if (n <= 0) return;
-      raw *const to = static_cast<raw *>(row) + first;
+      raw *const to = reinterpret_cast<raw *>(row) + first;
       int head = (int)((16 - ((uintptr_t)to & 15)) & 15) / ES;
       if (head > n) head = n;
       const int vectors = (n - head) / V, tail = n - head - vectors * V;
-      const raw *const staged = reinterpret_cast<const raw *>(from);
+      const raw *const values = reinterpret_cast<const raw *>(from);
       const int off = head * ES;
-      if (lane < head) to[lane] = staged[lane];
+      if (lane < head) to[lane] = values[lane];
       if (lane < vectors) {
-        const uint4 *const at = reinterpret_cast<const uint4 *>(from) + lane;
-        reinterpret_cast<uint4 *>(to + head)[lane] = off ? shifted(at[0], at[1], off) : at[0];
+        const uint4 *const at16 = reinterpret_cast<const uint4 *>(from) + lane;
+        reinterpret_cast<uint4 *>(to + head)[lane] = off ? shifted(at16[0], at16[1], off) : at16[0];
       }
-      if (lane < tail) to[n - tail + lane] = staged[n - tail + lane];
+      if (lane < tail) to[n - tail + lane] = values[n - tail + lane];
     }
   }
-  static __device__ __forceinline__ void copy_ahead(uint32_t to, uintptr_t from) {
+  static __device__ __forceinline__ void copy_ahead(uint32_t to, const char *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
   }
 };
@@ -261,8 +277,18 @@ __device__ __forceinline__ void ring_param(const void *w, bool f32, bool vector,
   }
 }
 
-// Rows longer than a warp holds: a CTA takes a row at a time.  Memory-bound; while a row's two reductions run, the
-// rows ahead arrive in shared memory.
+// Rows of `stride` bytes from `base`, one per CTA and round; null stays null.
+struct RowWalk {
+  char *at;
+  int64_t step;
+  __device__ __forceinline__ RowWalk(const void *base, int64_t ld, int es)
+      : at(base ? static_cast<char *>(const_cast<void *>(base)) + blockIdx.x * ld * es : nullptr),
+        step(base ? gridDim.x * ld * es : 0) {}
+  __device__ __forceinline__ void next() { at += step; }
+};
+
+// Rows longer than a warp holds: a CTA takes a row at a time.  Memory-bound; while a row's two
+// reductions run, the rows ahead arrive in shared memory.
 template <int TYPE, bool SHIFT, int U>
 __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const LayerNormParams p) {
   typedef RowRing<TYPE, SHIFT, U, 2> Ring;
@@ -270,40 +296,47 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
   extern __shared__ __align__(16) char ring_memory[];
   __shared__ float2 part[2][32];
   int turn = 0;
-  const int threads = blockDim.x, d = (int)p.d;
-  const Ring ring{ring_memory, (d + V - 1) / V, d * ES, threads};
-  const float n = (float)p.d;
-  wait_for_predecessor();
-  auto request = [&](int64_t row, int stage) {
-    if (row < p.rows) {
-      ring.request(stage, 0, row_at(p.x, row, p.ldx, ES));
-      if (p.r) ring.request(stage, 1, row_at(p.r, row, p.ldr, ES));
+  const int threads = blockDim.x, d = (int)p.d, rows = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  const Ring ring(ring_memory, d, threads);
+  const float share = 1.f / (float)p.d;
+  RowWalk x(p.x, p.ldx, ES), r(p.r, p.ldr, ES), y(p.y, p.ldy, ES), ro(p.ro, p.ldo, ES);
+  RowWalk x_ahead = x, r_ahead = r;
+  int requested = 0, to = 0, at = 0;
+  const int stage_size = ring.stage_size(), ring_size = p.stages * stage_size;
+  auto request = [&]() {
+    if (requested < rows) {
+      ring.request(to, 0, x_ahead.at);
+      if (r_ahead.at) ring.request(to, 1, r_ahead.at);
+      x_ahead.next();
+      r_ahead.next();
     }
+    ++requested;
+    to = to + stage_size == ring_size ? 0 : to + stage_size;
     ring_close();
   };
-  for (int s = 0; s < p.stages - 1; ++s) request(blockIdx.x + (int64_t)s * gridDim.x, s);
-  int stage = 0;
+  wait_for_predecessor();
+  for (int s = 0; s < p.stages - 1; ++s) request();
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     ring_wait(p.stages - 2);
-    const void *const x = row_at(p.x, row, p.ldx, ES), *const r = p.r ? row_at(p.r, row, p.ldr, ES) : nullptr;
     float s[U][V];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) s[i][e] = 0.f;
       if ((int)threadIdx.x + i * threads < ring.units) {
-        ring.get(stage, 0, i, x, d, s[i]);
-        if (r) {
+        ring.get(at, 0, i, x.at, s[i]);
+        if (r.at) {
           float t[V];
-          ring.get(stage, 1, i, r, d, t);
+          ring.get(at, 1, i, r.at, t);
 #pragma unroll
           for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], t[e], t[e + 1]);
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[i][e] = 0.f;
       }
     }
-    if (p.ro) {
+    if (ro.at) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) ring.put(stage, 1, i, row_at(p.ro, row, p.ldo, ES), d, s[i]);
+      for (int i = 0; i < U; ++i) ring.put(at, 1, i, ro.at, s[i]);
     }
     float scale = 1.f, mean, fix, rstd;
     for (bool again = false;; again = true) {
@@ -312,33 +345,32 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
       for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < V; e += 2) add2(sum, more, sum, more, s[i][e], s[i][e + 1]);
-      sum += more;
-      more = 0.f;
-      row_sums(sum, more, threads, part, turn);
-      if (!again) {  // every warp has read the row before: its place is free
-        const int next = stage == 0 ? p.stages - 1 : stage - 1;
-        request(row + (int64_t)(p.stages - 1) * gridDim.x, next);
-      }
-      mean = sum / n;
-      float off = 0.f, square = 0.f;
+      sum = row_sum(sum + more, threads, part, turn);
+      if (!again) request();  // (over the row before, which the warp has read)
+      mean = sum * share;
+      float off[2] = {}, square[2] = {};
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int u = (int)threadIdx.x + i * threads;
         if (u >= ring.units) continue;
+        float c[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          if (SHIFT && u * V + e >= d) continue;
-          const float c = s[i][e] - mean;
-          off += c;
-          square = fmaf(c, c, square);
+        for (int e = 0; e < V; e += 2) add2(c[e], c[e + 1], s[i][e], s[i][e + 1], -mean, -mean);
+        if constexpr (SHIFT) ring.clear_tail(u, c);
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+          add2(off[0], off[1], off[0], off[1], c[e], c[e + 1]);
+          fma2(square[0], square[1], c[e], c[e + 1], c[e], c[e + 1], square[0], square[1]);
         }
       }
-      row_sums(off, square, threads, part, turn);
-      fix = off / n;
-      const float v = fmaxf(fmaf(-fix, fix, square / n), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
+      off[0] += off[1];
+      square[0] += square[1];
+      row_sums(off[0], square[0], threads, part, turn);
+      fix = off[0] * share;
+      const float v = fmaxf(fmaf(-fix, fix, square[0] * share), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
       rstd = 1.f / sqrtf(v);
-      if (!(square <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
-      if (again || (square <= 3.4028235e38f && v >= kTinyVariance)) break;
+      if (!(square[0] <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
+      if (again || (square[0] <= 3.4028235e38f && v >= kTinyVariance)) break;
       float top = 0.f;  // rare: squares beyond fp32's range, or all but lost below it
 #pragma unroll
       for (int i = 0; i < U; ++i)
@@ -354,27 +386,32 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
       if (p.mean) p.mean[row] = (mean + fix) / scale;
       if (p.rstd) p.rstd[row] = rstd * scale;
     }
+    const float less = -fix * rstd;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int u = (int)threadIdx.x + i * threads;
       if (u < ring.units) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[i][e] = ((s[i][e] - mean) - fix) * rstd;
-        float w[V];
-        if (p.w) {
-          ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
-#pragma unroll
-          for (int e = 0; e < V; e += 2) mul2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+        for (int e = 0; e < V; e += 2) {
+          add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], -mean, -mean);
+          fma2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], rstd, rstd, less, less);
         }
-        if (p.b) {
-          ring_param<TYPE>(p.b, p.w_f32, p.params_vector, u, d, w);
+        float w[V], b[V];
+        if (p.w) ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
+        if (p.b) ring_param<TYPE>(p.b, p.w_f32, p.params_vector, u, d, b);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+        for (int e = 0; e < V; e += 2) {
+          if (p.w) mul2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
+          if (p.b) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], b[e], b[e + 1]);
         }
       }
-      ring.put(stage, 0, i, row_at(p.y, row, p.ldy, ES), d, s[i]);
+      ring.put(at, 0, i, y.at, s[i]);
     }
-    stage = stage + 1 == p.stages ? 0 : stage + 1;
+    at = at + stage_size == ring_size ? 0 : at + stage_size;
+    x.next();
+    r.next();
+    y.next();
+    ro.next();
   }
   ring_wait(0);
 }
@@ -384,79 +421,100 @@ template <int TYPE, bool SHIFT, int U>
 __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_grad_ring_kernel(const LayerNormGradParams p) {
   typedef RowRing<TYPE, SHIFT, U, 3> Ring;
   constexpr int V = Ring::V, ES = Ring::ES;
+  constexpr bool kHeld = U == 1;  // the weight stays in registers
   extern __shared__ __align__(16) char ring_memory[];
   __shared__ float2 part[2][32];
   int turn = 0;
-  const int threads = blockDim.x, d = (int)p.d;
-  const Ring ring{ring_memory, (d + V - 1) / V, d * ES, threads};
-  const float n = (float)p.d;
-  float dw[U][V] = {}, db[U][V] = {};
-  wait_for_predecessor();
-  auto request = [&](int64_t row, int stage) {
-    if (row < p.rows) {
-      ring.request(stage, 0, row_at(p.s, row, p.lds, ES));
-      ring.request(stage, 1, row_at(p.dy, row, p.lddy, ES));
-      if (p.ds) ring.request(stage, 2, row_at(p.ds, row, p.ldds, ES));
+  const int threads = blockDim.x, d = (int)p.d, rows = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
+  const Ring ring(ring_memory, d, threads);
+  const float share = 1.f / (float)p.d;
+  RowWalk s(p.s, p.lds, ES), dy(p.dy, p.lddy, ES), ds(p.ds, p.ldds, ES), dx(p.dx, p.lddx, ES);
+  RowWalk s_ahead = s, dy_ahead = dy, ds_ahead = ds;
+  int requested = 0, to = 0, at = 0;
+  const int stage_size = ring.stage_size(), ring_size = p.stages * stage_size;
+  auto request = [&]() {
+    if (requested < rows) {
+      ring.request(to, 0, s_ahead.at);
+      ring.request(to, 1, dy_ahead.at);
+      if (ds_ahead.at) ring.request(to, 2, ds_ahead.at);
+      s_ahead.next();
+      dy_ahead.next();
+      ds_ahead.next();
     }
+    ++requested;
+    to = to + stage_size == ring_size ? 0 : to + stage_size;
     ring_close();
   };
-  for (int s = 0; s < p.stages - 1; ++s) request(blockIdx.x + (int64_t)s * gridDim.x, s);
-  int stage = 0;
+  float dw[U][V] = {}, db[U][V] = {}, w[V];
+  wait_for_predecessor();
+  for (int i = 0; i < p.stages - 1; ++i) request();
+  auto weight = [&](int u) {
+    if (p.w && u < ring.units) {
+      ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = 1.f;
+    }
+  };
+  if (kHeld) weight((int)threadIdx.x);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float mean = p.mean[row], rstd = p.rstd[row];
+    const float rstd = p.rstd[row], less = -p.mean[row];
     ring_wait(p.stages - 2);
-    const void *const s = row_at(p.s, row, p.lds, ES), *const dy = row_at(p.dy, row, p.lddy, ES),
-               *const ds = p.ds ? row_at(p.ds, row, p.ldds, ES) : nullptr;
     float xh[U][V], t[U][V];
-    float a = 0.f, b = 0.f;
+    float a[2] = {}, b[2] = {};
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int u = (int)threadIdx.x + i * threads;
-#pragma unroll
-      for (int e = 0; e < V; ++e) xh[i][e] = t[i][e] = 0.f;
       if (u < ring.units) {
-        ring.get(stage, 0, i, s, d, xh[i]);
-        ring.get(stage, 1, i, dy, d, t[i]);  // (0 behind the row's end, whatever xh is there)
+        if (!kHeld) weight(u);
+        ring.get(at, 0, i, s.at, xh[i]);
+        ring.get(at, 1, i, dy.at, t[i]);  // (0 behind the row's end, whatever xh is there)
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          xh[i][e] = (xh[i][e] - mean) * rstd;
-          db[i][e] += t[i][e];
-          dw[i][e] = fmaf(t[i][e], xh[i][e], dw[i][e]);
+        for (int e = 0; e < V; e += 2) {
+          float &x0 = xh[i][e], &x1 = xh[i][e + 1], &t0 = t[i][e], &t1 = t[i][e + 1];
+          add2(x0, x1, x0, x1, less, less);
+          mul2(x0, x1, x0, x1, rstd, rstd);
+          add2(db[i][e], db[i][e + 1], db[i][e], db[i][e + 1], t0, t1);
+          fma2(dw[i][e], dw[i][e + 1], t0, t1, x0, x1, dw[i][e], dw[i][e + 1]);
+          mul2(t0, t1, t0, t1, w[e], w[e + 1]);
+          add2(a[0], a[1], a[0], a[1], t0, t1);
+          fma2(b[0], b[1], t0, t1, x0, x1, b[0], b[1]);
         }
-        if (p.w) {
-          float w[V];
-          ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
+      } else {
 #pragma unroll
-          for (int e = 0; e < V; e += 2) mul2(t[i][e], t[i][e + 1], t[i][e], t[i][e + 1], w[e], w[e + 1]);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          a += t[i][e];
-          b = fmaf(t[i][e], xh[i][e], b);
-        }
+        for (int e = 0; e < V; ++e) xh[i][e] = t[i][e] = 0.f;
       }
     }
-    row_sums(a, b, threads, part, turn);
-    {  // every warp has read the row before: its place is free
-      const int next = stage == 0 ? p.stages - 1 : stage - 1;
-      request(row + (int64_t)(p.stages - 1) * gridDim.x, next);
-    }
-    a /= n;
-    b /= n;
+    a[0] += a[1];
+    b[0] += b[1];
+    row_sums(a[0], b[0], threads, part, turn);
+    request();  // over the row before, which the warp has read
+    const float ma = -a[0] * share, mb = -b[0] * share;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      float v[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[e] = (t[i][e] - a - xh[i][e] * b) * rstd;
-      if (ds && (int)threadIdx.x + i * threads < ring.units) {
-        float f[V];
-        ring.get(stage, 2, i, ds, d, f);
-#pragma unroll
-        for (int e = 0; e < V; e += 2) add2(v[e], v[e + 1], v[e], v[e + 1], f[e], f[e + 1]);
+      for (int e = 0; e < V; e += 2) {
+        float &t0 = t[i][e], &t1 = t[i][e + 1];
+        add2(t0, t1, t0, t1, ma, ma);
+        fma2(t0, t1, xh[i][e], xh[i][e + 1], mb, mb, t0, t1);
       }
-      ring.put(stage, 0, i, row_at(p.dx, row, p.lddx, ES), d, v);
+      if (ds.at && (int)threadIdx.x + i * threads < ring.units) {
+        float f[V];
+        ring.get(at, 2, i, ds.at, f);
+#pragma unroll
+        for (int e = 0; e < V; e += 2)
+          fma2(t[i][e], t[i][e + 1], t[i][e], t[i][e + 1], rstd, rstd, f[e], f[e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 2) mul2(t[i][e], t[i][e + 1], t[i][e], t[i][e + 1], rstd, rstd);
+      }
+      ring.put(at, 0, i, dx.at, t[i]);
     }
-    stage = stage + 1 == p.stages ? 0 : stage + 1;
+    at = at + stage_size == ring_size ? 0 : at + stage_size;
+    s.next();
+    dy.next();
+    ds.next();
+    dx.next();
   }
   ring_wait(0);
   if (p.partial == nullptr) return;
