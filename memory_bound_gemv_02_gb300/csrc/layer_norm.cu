@@ -65,52 +65,57 @@ struct ColumnSumParams {
   int32_t count;
 };
 
-// Sums of a and b over the tpr threads of a row.  Rows of up to a warp take
-// shuffles alone; CTA-wide rows one barrier, as two sets of partials take turns.
-__device__ __forceinline__ void row_sums(float &a, float &b, int tpr, float2 (*part)[32], int &turn) {
-  const int width = tpr < 32 ? tpr : 32;
-  for (int m = width / 2; m > 0; m >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, m);
-    b += __shfl_xor_sync(0xffffffffu, b, m);
-  }
-  if (tpr <= 32) return;
-  const int warps = tpr / 32, lane = threadIdx.x & 31;
-  if (lane == 0) part[turn][threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  const float2 v = lane < warps ? part[turn][lane] : make_float2(0.f, 0.f);
-  a = v.x;
-  b = v.y;
-  for (int m = 16; m > 0; m >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, m);
-    b += __shfl_xor_sync(0xffffffffu, b, m);
-  }
-  turn ^= 1;
+// Sums of a and b over the `tpr` neighbouring lanes of a row (a power of two).
+__device__ __forceinline__ void lane_sums(float &a, float &b, int tpr) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1)
+    if (tpr > m) {
+      a += __shfl_xor_sync(0xffffffffu, a, m);
+      b += __shfl_xor_sync(0xffffffffu, b, m);
+    }
 }
 
-// The sum of a alone, of CTA-wide rows.
-__device__ __forceinline__ float row_sum(float a, int tpr, float2 (*part)[32], int &turn) {
+// The same over a CTA, with one barrier: two sets of partial sums take turns.
+__device__ __forceinline__ void row_sums(float &a, float &b, int threads, float2 (*part)[32], int &turn) {
+  lane_sums(a, b, 32);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[turn][threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = lane < threads / 32 ? part[turn][lane] : make_float2(0.f, 0.f);
+  a = v.x;
+  b = v.y;
+  lane_sums(a, b, 32);
+  turn ^= 1;
+}
+__device__ __forceinline__ float row_sum(float a, int threads, float2 (*part)[32], int &turn) {
+#pragma unroll
   for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
   const int lane = threadIdx.x & 31;
   if (lane == 0) part[turn][threadIdx.x >> 5].x = a;
   __syncthreads();
-  a = lane < tpr / 32 ? part[turn][lane].x : 0.f;
+  a = lane < threads / 32 ? part[turn][lane].x : 0.f;
+#pragma unroll
   for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
   turn ^= 1;
   return a;
 }
 
-__device__ __forceinline__ float row_max(float a, int tpr, float2 (*part)[32], int &turn) {
-  const int width = tpr < 32 ? tpr : 32;
-  for (int m = width / 2; m > 0; m >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
-  if (tpr <= 32) return a;
+__device__ __forceinline__ float lane_max(float a, int tpr) {
+  for (int m = tpr / 2; m > 0; m >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
+  return a;
+}
+__device__ __forceinline__ float row_max(float a, int threads, float2 (*part)[32], int &turn) {
+  a = lane_max(a, 32);
   const int lane = threadIdx.x & 31;
   if (lane == 0) part[turn][threadIdx.x >> 5] = make_float2(a, 0.f);
   __syncthreads();
-  a = lane < tpr / 32 ? part[turn][lane].x : 0.f;
-  for (int m = 16; m > 0; m >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, m));
+  a = lane_max(lane < threads / 32 ? part[turn][lane].x : 0.f, 32);
   turn ^= 1;
   return a;
 }
+
+// 1 / scale for a power of two.
+__device__ __forceinline__ float reciprocal(float scale) { return __int_as_float((254 << 23) - __float_as_int(scale)); }
 
 // A power of two that brings a row whose largest magnitude is `top` to about 1,
 // with eps scaled by its square still finite.
@@ -168,6 +173,15 @@ __device__ __forceinline__ const void *row_at(const void *p, int64_t row, int64_
 __device__ __forceinline__ void *row_at(void *p, int64_t row, int64_t ld, int es) {
   return static_cast<char *>(p) + row * ld * es;
 }
+
+// Rows `first`, `first` + `step`, ... of a matrix; null stays null.
+struct RowWalk {
+  char *at;
+  int64_t bytes;
+  __device__ __forceinline__ RowWalk(const void *base, int64_t ld, int es, int64_t first, int64_t step)
+      : at(base ? static_cast<char *>(const_cast<void *>(base)) + first * ld * es : nullptr), bytes(base ? step * ld * es : 0) {}
+  __device__ __forceinline__ void next() { at += bytes; }
+};
 
 // Rows of a CTA, copied ahead into shared memory.  Every warp copies what it will read
 // itself, 32 units of 16 bytes side by side per tensor and turn, so a row's arrival is
@@ -261,11 +275,12 @@ __device__ __forceinline__ void ring_wait(int ahead) {
   __syncwarp();
 }
 
-// Unit u of a parameter vector, with 16-byte loads where it starts on 16 bytes.
-template <int TYPE>
+// Unit u of a parameter vector, with 16-byte loads where it starts on 16 bytes (without
+// SHIFT it does, and holds whole units).
+template <int TYPE, bool SHIFT>
 __device__ __forceinline__ void ring_param(const void *w, bool f32, bool vector, int u, int d, float (&f)[Elem<TYPE>::VEC]) {
   constexpr int V = Elem<TYPE>::VEC;
-  if (vector && (u + 1) * V <= d) {
+  if (!SHIFT || (vector && (u + 1) * V <= d)) {
     Access<TYPE, true>::param(w, f32, u, f);
     return;
   }
@@ -277,29 +292,22 @@ __device__ __forceinline__ void ring_param(const void *w, bool f32, bool vector,
   }
 }
 
-// Rows of `stride` bytes from `base`, one per CTA and round; null stays null.
-struct RowWalk {
-  char *at;
-  int64_t step;
-  __device__ __forceinline__ RowWalk(const void *base, int64_t ld, int es)
-      : at(base ? static_cast<char *>(const_cast<void *>(base)) + blockIdx.x * ld * es : nullptr),
-        step(base ? gridDim.x * ld * es : 0) {}
-  __device__ __forceinline__ void next() { at += step; }
-};
-
 // Rows longer than a warp holds: a CTA takes a row at a time.  Memory-bound; while a row's two
 // reductions run, the rows ahead arrive in shared memory.
 template <int TYPE, bool SHIFT, int U>
 __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const LayerNormParams p) {
   typedef RowRing<TYPE, SHIFT, U, 2> Ring;
   constexpr int V = Ring::V, ES = Ring::ES;
+  constexpr bool kHeld = U == 1;  // weight and bias stay in registers
   extern __shared__ __align__(16) char ring_memory[];
   __shared__ float2 part[2][32];
   int turn = 0;
   const int threads = blockDim.x, d = (int)p.d, rows = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const Ring ring(ring_memory, d, threads);
   const float share = 1.f / (float)p.d;
-  RowWalk x(p.x, p.ldx, ES), r(p.r, p.ldr, ES), y(p.y, p.ldy, ES), ro(p.ro, p.ldo, ES);
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  RowWalk x(p.x, p.ldx, ES, first, step), r(p.r, p.ldr, ES, first, step), y(p.y, p.ldy, ES, first, step),
+      ro(p.ro, p.ldo, ES, first, step);
   RowWalk x_ahead = x, r_ahead = r;
   int requested = 0, to = 0, at = 0;
   const int stage_size = ring.stage_size(), ring_size = p.stages * stage_size;
@@ -314,8 +322,20 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
     to = to + stage_size == ring_size ? 0 : to + stage_size;
     ring_close();
   };
+  float w[V], b[V];
+  auto params = [&](int u) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      w[e] = 1.f;
+      b[e] = 0.f;
+    }
+    if (u >= ring.units) return;
+    if (p.w) ring_param<TYPE, SHIFT>(p.w, p.w_f32, p.params_vector, u, d, w);
+    if (p.b) ring_param<TYPE, SHIFT>(p.b, p.w_f32, p.params_vector, u, d, b);
+  };
   wait_for_predecessor();
   for (int s = 0; s < p.stages - 1; ++s) request();
+  if (kHeld) params((int)threadIdx.x);
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     ring_wait(p.stages - 2);
     float s[U][V];
@@ -368,7 +388,7 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
       row_sums(off[0], square[0], threads, part, turn);
       fix = off[0] * share;
       const float v = fmaxf(fmaf(-fix, fix, square[0] * share), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
-      rstd = 1.f / sqrtf(v);
+      rstd = rsqrtf(v);
       if (!(square[0] <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
       if (again || (square[0] <= 3.4028235e38f && v >= kTinyVariance)) break;
       float top = 0.f;  // rare: squares beyond fp32's range, or all but lost below it
@@ -383,7 +403,7 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
         for (int e = 0; e < V; ++e) s[i][e] *= scale;
     }
     if (threadIdx.x == 0) {
-      if (p.mean) p.mean[row] = (mean + fix) / scale;
+      if (p.mean) p.mean[row] = (mean + fix) * reciprocal(scale);
       if (p.rstd) p.rstd[row] = rstd * scale;
     }
     const float less = -fix * rstd;
@@ -396,14 +416,9 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_ring_kernel(const L
           add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], -mean, -mean);
           fma2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], rstd, rstd, less, less);
         }
-        float w[V], b[V];
-        if (p.w) ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
-        if (p.b) ring_param<TYPE>(p.b, p.w_f32, p.params_vector, u, d, b);
+        if (!kHeld) params(u);
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-          if (p.w) mul2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1]);
-          if (p.b) add2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], b[e], b[e + 1]);
-        }
+        for (int e = 0; e < V; e += 2) fma2(s[i][e], s[i][e + 1], s[i][e], s[i][e + 1], w[e], w[e + 1], b[e], b[e + 1]);
       }
       ring.put(at, 0, i, y.at, s[i]);
     }
@@ -428,7 +443,9 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_grad_ring_kernel(co
   const int threads = blockDim.x, d = (int)p.d, rows = (int)((p.rows - blockIdx.x + gridDim.x - 1) / gridDim.x);
   const Ring ring(ring_memory, d, threads);
   const float share = 1.f / (float)p.d;
-  RowWalk s(p.s, p.lds, ES), dy(p.dy, p.lddy, ES), ds(p.ds, p.ldds, ES), dx(p.dx, p.lddx, ES);
+  const int64_t first = blockIdx.x, step = gridDim.x;
+  RowWalk s(p.s, p.lds, ES, first, step), dy(p.dy, p.lddy, ES, first, step), ds(p.ds, p.ldds, ES, first, step),
+      dx(p.dx, p.lddx, ES, first, step);
   RowWalk s_ahead = s, dy_ahead = dy, ds_ahead = ds;
   int requested = 0, to = 0, at = 0;
   const int stage_size = ring.stage_size(), ring_size = p.stages * stage_size;
@@ -450,15 +467,20 @@ __global__ void __launch_bounds__(kRowThreadsMax) layer_norm_grad_ring_kernel(co
   for (int i = 0; i < p.stages - 1; ++i) request();
   auto weight = [&](int u) {
     if (p.w && u < ring.units) {
-      ring_param<TYPE>(p.w, p.w_f32, p.params_vector, u, d, w);
+      ring_param<TYPE, SHIFT>(p.w, p.w_f32, p.params_vector, u, d, w);
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e) w[e] = 1.f;
     }
   };
   if (kHeld) weight((int)threadIdx.x);
+  float rstd_next = p.rstd[blockIdx.x], mean_next = p.mean[blockIdx.x];
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-    const float rstd = p.rstd[row], less = -p.mean[row];
+    const float rstd = rstd_next, less = -mean_next;
+    if (row + gridDim.x < p.rows) {
+      rstd_next = p.rstd[row + gridDim.x];
+      mean_next = p.mean[row + gridDim.x];
+    }
     ring_wait(p.stages - 2);
     float xh[U][V], t[U][V];
     float a[2] = {}, b[2] = {};
@@ -537,25 +559,28 @@ template <int TYPE, bool VECTOR, int U>
 __global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(const LayerNormParams p) {
   typedef Access<TYPE, VECTOR> A;
   constexpr int V = A::V, ES = sizeof(typename A::raw);
-  __shared__ float2 part[2][32];
-  int turn = 0;
   const int tpr = p.tpr, rows_here = kSmallThreads / tpr;
   const int at = threadIdx.x % tpr, group = threadIdx.x / tpr, units = (int)(p.d / V);
-  const float n = (float)p.d;
-  const int64_t step = (int64_t)gridDim.x * rows_here;
+  const float share = 1.f / (float)p.d;
+  const int64_t step = (int64_t)gridDim.x * rows_here, start = (int64_t)blockIdx.x * rows_here + group;
+  RowWalk x_ahead(p.x, p.ldx, ES, start, step), r_ahead(p.r, p.ldr, ES, start, step), y(p.y, p.ldy, ES, start, step),
+      ro(p.ro, p.ldo, ES, start, step);
   typename A::Unit x[U], r[U];
   auto request = [&](int64_t row) {
+    if (row >= p.rows) return;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int u = at + i * tpr;
-      if (row < p.rows && u < units) {
-        x[i] = A::fetch(row_at(p.x, row, p.ldx, ES), u);
-        if (p.r) r[i] = A::fetch(row_at(p.r, row, p.ldr, ES), u);
+      if (u < units) {
+        x[i] = A::fetch(x_ahead.at, u);
+        if (p.r) r[i] = A::fetch(r_ahead.at, u);
       }
     }
+    x_ahead.next();
+    r_ahead.next();
   };
   wait_for_predecessor();
-  request((int64_t)blockIdx.x * rows_here + group);
+  request(start);
   for (int64_t row0 = (int64_t)blockIdx.x * rows_here; row0 < p.rows; row0 += step) {
     const int64_t row = row0 + group;
     const bool live = row < p.rows;
@@ -578,8 +603,9 @@ __global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(cons
     if (p.ro && live) {
 #pragma unroll
       for (int i = 0; i < U; ++i)
-        if (at + i * tpr < units) A::store(row_at(p.ro, row, p.ldo, ES), at + i * tpr, s[i]);
+        if (at + i * tpr < units) A::store(ro.at, at + i * tpr, s[i]);
     }
+    ro.next();
     float scale = 1.f, mean, fix, rstd;
     for (bool again = false;; again = true) {
       float sum = 0.f, none = 0.f;
@@ -587,8 +613,8 @@ __global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(cons
       for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) sum += s[i][e];
-      row_sums(sum, none, tpr, part, turn);
-      mean = sum / n;
+      lane_sums(sum, none, tpr);
+      mean = sum * share;
       float off = 0.f, square = 0.f;
 #pragma unroll
       for (int i = 0; i < U; ++i)
@@ -600,10 +626,10 @@ __global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(cons
             square = fmaf(c, c, square);
           }
         }
-      row_sums(off, square, tpr, part, turn);
-      fix = off / n;
-      const float v = fmaxf(fmaf(-fix, fix, square / n), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
-      rstd = 1.f / sqrtf(v);
+      lane_sums(off, square, tpr);
+      fix = off * share;
+      const float v = fmaxf(fmaf(-fix, fix, square * share), 0.f) + p.eps * scale * scale;  // (a NaN becomes 0: square tells)
+      rstd = rsqrtf(v);
       if (!(square <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
       // rare: squares beyond fp32's range, or all but lost below it; a warp's rows go together
       if (again || !__any_sync(0xffffffffu, live && (!(square <= 3.4028235e38f) || v < kTinyVariance))) break;
@@ -612,15 +638,16 @@ __global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(cons
       for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) top = fmaxf(top, fabsf(s[i][e]));
-      scale = row_scale(row_max(top, tpr, part, turn), p.eps);
+      scale = row_scale(lane_max(top, tpr), p.eps);
 #pragma unroll
       for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) s[i][e] *= scale;
     }
     if (!live) continue;
+    const float less = -fix * rstd;
     if (at == 0) {
-      if (p.mean) p.mean[row] = (mean + fix) / scale;
+      if (p.mean) p.mean[row] = (mean + fix) * reciprocal(scale);
       if (p.rstd) p.rstd[row] = rstd * scale;
     }
 #pragma unroll
@@ -632,13 +659,14 @@ __global__ void __launch_bounds__(kSmallThreads, 4) layer_norm_small_kernel(cons
       if (p.b) A::param(p.b, p.w_f32, u, b);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        float y = ((s[i][e] - mean) - fix) * rstd;
-        if (p.w) y *= w[e];
-        if (p.b) y += b[e];
-        s[i][e] = y;
+        float v = fmaf(s[i][e] - mean, rstd, less);
+        if (p.w) v *= w[e];
+        if (p.b) v += b[e];
+        s[i][e] = v;
       }
-      A::store(row_at(p.y, row, p.ldy, ES), u, s[i]);
+      A::store(y.at, u, s[i]);
     }
+    y.next();
   }
 }
 
@@ -692,7 +720,7 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(const Lay
       row_sums(off, square, kLongThreads, part, turn);
       fix = off / n;
       const float v = fmaxf(fmaf(-fix, fix, square / n), 0.f) + p.eps * scale * scale;
-      rstd = 1.f / sqrtf(v);
+      rstd = rsqrtf(v);
       if (!(square <= 3.4028235e38f)) rstd = __int_as_float(0x7fc00000);
       if (again || (square <= 3.4028235e38f && v >= kTinyVariance)) break;
       float top = 0.f;
@@ -705,7 +733,7 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(const Lay
       scale = row_scale(row_max(top, kLongThreads, part, turn), p.eps);
     }
     if (threadIdx.x == 0) {
-      if (p.mean) p.mean[row] = (mean + fix) / scale;
+      if (p.mean) p.mean[row] = (mean + fix) * reciprocal(scale);
       if (p.rstd) p.rstd[row] = rstd * scale;
     }
 #pragma unroll 2
@@ -733,12 +761,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) layer_norm_grad_small_kernel
   typedef Access<TYPE, VECTOR> A;
   constexpr int V = A::V, ES = sizeof(typename A::raw);
   extern __shared__ float columns[];  // (2, d): the sums of the groups before
-  __shared__ float2 part[2][32];
-  int turn = 0;
   const int tpr = p.tpr, groups = kSmallThreads / tpr;
   const int at = threadIdx.x % tpr, group = threadIdx.x / tpr, units = (int)(p.d / V);
-  const float n = (float)p.d;
-  const int64_t step = (int64_t)gridDim.x * groups;
+  const float share = 1.f / (float)p.d;
+  const int64_t step = (int64_t)gridDim.x * groups, start = (int64_t)blockIdx.x * groups + group;
+  RowWalk s_ahead(p.s, p.lds, ES, start, step), dy_ahead(p.dy, p.lddy, ES, start, step),
+      ds_ahead(p.ds, p.ldds, ES, start, step), dx(p.dx, p.lddx, ES, start, step);
   float w[U][V], dw[U][V], db[U][V];
   typename A::Unit s[U], dy[U], ds[U];
   float mean_next = 0.f, rstd_next = 0.f;
@@ -750,14 +778,17 @@ __global__ void __launch_bounds__(kSmallThreads, 2) layer_norm_grad_small_kernel
     for (int i = 0; i < U; ++i) {
       const int u = at + i * tpr;
       if (u < units) {
-        s[i] = A::fetch(row_at(p.s, row, p.lds, ES), u);
-        dy[i] = A::fetch(row_at(p.dy, row, p.lddy, ES), u);
-        if (p.ds) ds[i] = A::fetch(row_at(p.ds, row, p.ldds, ES), u);
+        s[i] = A::fetch(s_ahead.at, u);
+        dy[i] = A::fetch(dy_ahead.at, u);
+        if (p.ds) ds[i] = A::fetch(ds_ahead.at, u);
       }
     }
+    s_ahead.next();
+    dy_ahead.next();
+    ds_ahead.next();
   };
   wait_for_predecessor();
-  request((int64_t)blockIdx.x * groups + group);
+  request(start);
 #pragma unroll
   for (int i = 0; i < U; ++i) {
 #pragma unroll
@@ -793,9 +824,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) layer_norm_grad_small_kernel
       }
     }
     request(row + step);
-    row_sums(a, b, tpr, part, turn);
-    a /= n;
-    b /= n;
+    lane_sums(a, b, tpr);
+    a *= share;
+    b *= share;
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -803,8 +834,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) layer_norm_grad_small_kernel
       if (u >= units) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e) t[i][e] = (t[i][e] - a - xh[i][e] * b) * rstd + more[i][e];
-      A::store(row_at(p.dx, row, p.lddx, ES), u, t[i]);
+      A::store(dx.at, u, t[i]);
     }
+    dx.next();
   }
   if (p.partial == nullptr) return;
   float *const out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
@@ -982,7 +1014,7 @@ int launch_norm(LayerNormParams p, int sms, cudaStream_t stream) {
     return launch_op(layer_norm_small_kernel<TYPE, VECTOR, U>, dim3((unsigned)(ctas < most ? ctas : most)), kSmallThreads,
                      0, 1, stream, p);
   }
-  if (blocks <= 512) return launch_norm_ring<TYPE, !VECTOR, 1>(p, sms, stream);
+  if (blocks <= kRowThreadsMax) return launch_norm_ring<TYPE, !VECTOR, 1>(p, sms, stream);
   if (blocks <= 2 * kRowThreadsMax) return launch_norm_ring<TYPE, !VECTOR, 2>(p, sms, stream);
   const int64_t grid = p.rows < (int64_t)sms * 4 ? p.rows : (int64_t)sms * 4;
   return launch_op(layer_norm_long_kernel<TYPE, VECTOR>, dim3((unsigned)grid), kLongThreads, 0, 1, stream, p);
