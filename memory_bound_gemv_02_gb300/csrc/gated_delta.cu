@@ -488,7 +488,7 @@ extern "C" int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, 
     if ((st = tile_source(s, *packed[i], i, l.pack[i], ws, tiles[i], stream)) != GEMV_OK) return st;
   p.records = ws + l.records;
   p.vector_o = on_units(*o, s.dv) ? 1 : 0;
-  return launch_delta_chunks(p, padded_dk(s.dk), sms, stream);
+  return launch_delta_chunks(p, padded_dk(s.dk), false, sms, stream);
 }
 
 extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_heads *d_o, const gemv_heads *q,

@@ -31,7 +31,7 @@ struct TileSource {
 
 // What a chunk's gates come to, 64 of each: beta; the decay from before the chunk
 // to the step (0 past a new document); that from the step to the chunk's end; the
-// sum of log decays up to the step in two floats, and the count of documents begun.
+// sum of log decays (to base 2) up to the step in two floats, and the count of documents begun.
 enum { kBeta = 0, kFirst = 64, kLast = 128, kTotalHi = 192, kTotalLo = 256, kDocs = 320, kGateFloats = 384 };
 
 // A chunk of one head: T = (I + A)^-1 and P as sums of two bf16 (64 x 64 each), the gates.
@@ -64,8 +64,13 @@ struct PackParams {
 
 int launch_delta_steps(const DeltaParams &p, int sms, cudaStream_t stream);
 int launch_delta_pack(const PackParams &p, cudaStream_t stream);
-int launch_delta_chunks(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream);
-int launch_delta_walks(const DeltaParams &p, int dk_padded, cudaStream_t stream);
+// The chunks' matrices and the walk over them, or (gradient) the gradient's two walks.
+int launch_delta_chunks_f16(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream);
+int launch_delta_chunks_bf16(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream);
+inline int launch_delta_chunks(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream) {
+  return p.f16 ? launch_delta_chunks_f16(p, dk_padded, gradient, sms, stream)
+               : launch_delta_chunks_bf16(p, dk_padded, gradient, sms, stream);
+}
 int launch_delta_gradient(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream);
 
 }  // namespace gemvk

@@ -1,0 +1,754 @@
+// The gated delta rule over chunks of 64 steps (see gated_delta() in gemv_ops.h).
+//
+// With G_i the sum of log decays up to step i of a chunk and S the state before it,
+// the corrections D of all its steps solve one triangular system:
+//
+//     A_ij = beta_i exp(G_i - G_j) k_i . k_j   (j < i)
+//     (I + A) D = beta (V - exp(G) K S)
+//     O = scale (exp(G) Q S) + P D,   P_ij = scale exp(G_i - G_j) q_i . k_j   (j <= i)
+//     S' = exp(G_last) S + (exp(G_last - G) K)^T D
+//
+// Decays are exponentials of differences, never quotients, and 0 across a new
+// document.  One kernel makes T = (I + A)^-1 and P of every chunk, all at once; a second walks the
+// chunks in order, 16 columns of v per warp: these are independent of one another all
+// along, so a warp keeps its part of S^T in registers as fp32 sums and needs nothing of the
+// others.  The gradient's two walks are the same kernel: forward, keeping S and D; and
+// backward over
+//
+//     dD = P^T dO + (exp(G_last - G) K) dS',   dR = T^T dD
+//     dS = exp(G_last) dS' + scale (exp(G) Q)^T dO - (beta exp(G) K)^T dR
+//
+// which needs neither S nor D, so both walks run side by side.
+#pragma once
+
+#include "gated_delta_mma.cuh"
+
+namespace gemvk {
+namespace {
+
+constexpr float kNoDecay = -87.3f;
+constexpr int kPrepareThreads = 128;
+constexpr int kTilePitch = kDeltaChunk + 8;  // of 64 x 64 matrices in shared memory
+constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
+
+__device__ __forceinline__ float gate_at(const HeadsOf &h, bool f32, bool f16, int64_t b, int64_t t, int64_t head) {
+  const int64_t at = b * h.batch + t * h.step + head * h.head;
+  if (f32) return static_cast<const float *>(h.p)[at];
+  const uint16_t v = static_cast<const uint16_t *>(h.p)[at];
+  return f16 ? Elem<GEMV_TYPE_F16>::get(v) : Elem<GEMV_TYPE_BF16>::get(v);
+}
+
+// The gates of a chunk by one warp, two steps per lane.  Log decays (to base 2) are
+// summed in 64-bit fixed point, as a difference of two sums is wanted to fp32's
+// precision however large they are; beyond 2^24 exp() has long left fp32.
+__device__ __forceinline__ void chunk_gates(const DeltaParams &p, int64_t b, int64_t head, int t0, float *gates) {
+  constexpr float kOne = 4294967296.f, kUnit = 1.f / kOne, kMost = 16777216.f;  // 2^32, 2^24
+  const int lane = threadIdx.x & 31;
+  long long total[2];
+  int docs[2];
+  bool lost = false;  // a NaN
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = t0 + 2 * lane + j;
+    const bool there = t < p.steps;
+    const float g = there ? gate_at(p.g, p.gates_f32, p.f16, b, t, head) : 0.f;
+    gates[kBeta + 2 * lane + j] = there ? gate_at(p.beta, p.gates_f32, p.f16, b, t, head) : 0.f;
+    lost = lost || g != g;
+    docs[j] = g < kNoDecay ? 1 : 0;
+    total[j] = g < kNoDecay ? 0 : __float2ll_rn(fminf(g * 1.44269504f, kMost) * kOne);
+  }
+  lost = __any_sync(0xffffffffu, lost);
+  total[1] += total[0];
+  docs[1] += docs[0];
+  long long sum = total[1];
+  int count = docs[1];
+#pragma unroll
+  for (int m = 1; m < 32; m *= 2) {
+    const long long s = __shfl_up_sync(0xffffffffu, sum, m);
+    const int c = __shfl_up_sync(0xffffffffu, count, m);
+    if (lane >= m) {
+      sum += s;
+      count += c;
+    }
+  }
+  const long long before = sum - total[1], whole = __shfl_sync(0xffffffffu, sum, 31);
+  const int docs_before = count - docs[1], docs_all = __shfl_sync(0xffffffffu, count, 31);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const long long s = before + total[j];
+    const int d = docs_before + docs[j], i = 2 * lane + j;
+    const float hi = lost ? __int_as_float(0x7fc00000) : __ll2float_rn(s) * kUnit;
+    gates[kFirst + i] = d == 0 ? power2(hi) : 0.f;
+    gates[kLast + i] = d == docs_all ? power2(lost ? hi : __ll2float_rn(whole - s) * kUnit) : 0.f;
+    gates[kTotalHi + i] = hi;
+    gates[kTotalLo + i] = lost ? hi : __ll2float_rn(s - __float2ll_rn(hi * kOne)) * kUnit;
+    gates[kDocs + i] = (float)d;
+  }
+}
+
+// The 16 x 16 blocks on the diagonal of T = (I + A)^-1 by substitution in fp32, a warp
+// per block, a lane per column; A's blocks with 20 floats a row.
+constexpr int kDiagPitch = 20;
+__device__ __forceinline__ void invert_diagonal(const float *A, char *T) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 15;
+  const float *const a = A + warp * 16 * kDiagPitch;
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float v[2] = {i == j ? 1.f : 0.f, 0.f};
+#pragma unroll
+    for (int m = 0; m < i; m += 4) {
+      const float4 r = *reinterpret_cast<const float4 *>(a + i * kDiagPitch + m);
+      const float q[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e < i) v[e & 1] = fmaf(-q[e], x[m + e], v[e & 1]);
+    }
+    x[i] = v[0] + v[1];
+  }
+  // two rows per lane half: bf16 and the rest
+  uint16_t *const to = reinterpret_cast<uint16_t *>(T) + warp * 16 * (kTilePitch + 1) + j;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if ((i & 1) != lane / 16) continue;
+    uint32_t big, rest;
+    split(x[i], 0.f, big, rest);
+    to[i * kTilePitch] = (uint16_t)big;
+    to[kPairBytes / 2 + i * kTilePitch] = (uint16_t)rest;
+  }
+}
+
+// c0, c1 = X^T Y^T for 16 x 16 blocks as two bf16: X stored (k, m), Y stored (n, k).
+__device__ __forceinline__ void block_product(FragC &c0, FragC &c1, uint32_t X, uint32_t Y, int lane) {
+  FragA big, rest;
+  uint32_t h[4], l[4];
+  load_matrices_t(big, at_km(X, kTilePitch, 0, 0, lane));
+  load_matrices_t(rest, at_km(X + kPairBytes, kTilePitch, 0, 0, lane));
+  load_matrices(h, at_nk(Y, kTilePitch, 0, 0, lane));
+  load_matrices(l, at_nk(Y + kPairBytes, kTilePitch, 0, 0, lane));
+  mma_split_split(c0, c1, big, rest, h, l);
+}
+// c0, c1 -= Z^T Y^T for sums Z^T just made.
+__device__ __forceinline__ void block_minus(FragC &c0, FragC &c1, const FragC &z0, const FragC &z1, uint32_t Y, int lane) {
+  FragA big, rest;
+  uint32_t h[4], l[4];
+  split_sums(z0, z1, big, rest);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    big[i] ^= 0x80008000u;
+    rest[i] ^= 0x80008000u;
+  }
+  load_matrices(h, at_nk(Y, kTilePitch, 0, 0, lane));
+  load_matrices(l, at_nk(Y + kPairBytes, kTilePitch, 0, 0, lane));
+  mma_split_split(c0, c1, big, rest, h, l);
+}
+// A block of T^T, to T.
+__device__ __forceinline__ void store_block(uint32_t T, const FragC &c0, const FragC &c1, int lane) {
+  FragA big, rest;
+  split_sums(c0, c1, big, rest);
+  store_matrices_t(at_km(T, kTilePitch, 0, 0, lane), big);
+  store_matrices_t(at_km(T + kPairBytes, kTilePitch, 0, 0, lane), rest);
+}
+__device__ __forceinline__ uint32_t block_of(uint32_t M, int i, int j) { return M + (i * 16 * kTilePitch + j * 16) * 2; }
+
+// The blocks of T below the diagonal, T_lo = -T_22 A_21 T_11, for halves of 32 and of 64, on
+// the tensor cores: transposed, so that the inner product's sums are the outer one's left
+// operand.
+__device__ __forceinline__ void invert_below(uint32_t A, uint32_t T) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < 2) {
+    const int i = 2 * warp + 1, j = 2 * warp;
+    FragC z[2] = {}, c[2] = {};
+    block_product(z[0], z[1], block_of(T, j, j), block_of(A, i, j), lane);
+    block_minus(c[0], c[1], z[0], z[1], block_of(T, i, i), lane);
+    store_block(block_of(T, i, j), c[0], c[1], lane);
+  }
+  __syncthreads();
+  const int j = warp & 1, i = 2 + warp / 2;  // one block of the lower left quarter per warp
+  FragC c[2] = {};
+#pragma unroll
+  for (int m = 2; m < 4; ++m) {  // Z = A_21 T_11, row of blocks m
+    if (m > i) continue;
+    FragC z[2] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k >= j) block_product(z[0], z[1], block_of(T, k, j), block_of(A, m, k), lane);
+    block_minus(c[0], c[1], z[0], z[1], block_of(T, i, m), lane);
+  }
+  store_block(block_of(T, i, j), c[0], c[1], lane);
+}
+
+template <int DK>
+struct Prepare {
+  static constexpr int kTiles = 2 * kDeltaChunk * (DK + 8) * 2;
+  // afterwards in the same place: A and T (P before it) as two bf16 each, A's diagonal in fp32
+  static constexpr int kA = 0, kT = 2 * kPairBytes, kDiag = kT + 2 * kPairBytes, kAfter = kDiag + 64 * kDiagPitch * 4,
+                       kGates = kTiles > kAfter ? kTiles : kAfter, kBytes = kGates + kGateFloats * 4;
+};
+
+// 2 x 64 rows of 64 from shared memory, 16 bytes at a time.
+__device__ __forceinline__ void store_matrix(uint16_t *to, const char *from) {
+#pragma unroll
+  for (int n = 0; n < 2 * kMatrix / 8 / kPrepareThreads; ++n) {
+    const int i = n * kPrepareThreads + (int)threadIdx.x;
+    reinterpret_cast<uint4 *>(to)[i] = *reinterpret_cast<const uint4 *>(from + i / 8 * kTilePitch * 2 + i % 8 * 16);
+  }
+}
+
+// T, P and the gates of one chunk, for all heads that share its q and k.
+template <bool F16, int DK>
+__global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const DeltaParams p) {
+  typedef Prepare<DK> L;
+  extern __shared__ __align__(16) char smem[];
+  constexpr int PITCH = DK + 8;
+  float *const gates = reinterpret_cast<float *>(smem + L::kGates), *const diagonal = reinterpret_cast<float *>(smem + L::kDiag);
+  const uint32_t base = smem_u32(smem), K = base, Q = K + kDeltaChunk * PITCH * 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int chunk = blockIdx.x, t0 = chunk * kDeltaChunk;
+  const int64_t b = blockIdx.z, head_k = blockIdx.y;
+  const int group = p.heads / p.heads_k;
+  wait_for_predecessor();
+  copy_tile<DK, kPrepareThreads>(K, p.tk, b, head_k, t0, p.steps, 0);
+  copy_tile<DK, kPrepareThreads>(Q, p.tq, b, head_k, t0, p.steps, 0);
+  copies_close();
+  if (warp == 0) chunk_gates(p, b, head_k * group, t0, gates);
+  copies_wait<0>();
+  __syncthreads();
+  // rows 16 warp .. of K K^T and Q K^T, up to the diagonal
+  FragC kk[8] = {}, qk[8] = {};
+#pragma unroll
+  for (int s = 0; s < DK / 16; ++s) {
+    FragA ak, aq;
+    load_matrices(ak, at_kn(K, PITCH, warp * 16, s * 16, lane));
+    load_matrices(aq, at_kn(Q, PITCH, warp * 16, s * 16, lane));
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      if (n > warp) continue;
+      uint32_t bk[4];
+      load_matrices(bk, at_nk(K, PITCH, n * 16, s * 16, lane));
+      mma_inputs<F16>(kk[2 * n], ak, bk[0], bk[1]);
+      mma_inputs<F16>(kk[2 * n + 1], ak, bk[2], bk[3]);
+      mma_inputs<F16>(qk[2 * n], aq, bk[0], bk[1]);
+      mma_inputs<F16>(qk[2 * n + 1], aq, bk[2], bk[3]);
+    }
+  }
+  for (int m = 0; m < group; ++m) {
+    const int64_t head = head_k * group + m;
+    char *const record = p.records + ((b * p.heads + head) * p.chunks + chunk) * kRecordBytes;
+    uint16_t *const out = reinterpret_cast<uint16_t *>(record);
+    if (m > 0) {
+      __syncthreads();  // the matrices of the head before are done with
+      if (warp == 0) chunk_gates(p, b, head, t0, gates);
+    }
+    __syncthreads();  // the tiles are done with
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = warp * 16 + lane / 4 + 8 * h, j = n * 8 + lane % 4 * 2, at = (i * kTilePitch + j) * 2;
+        float a[2] = {}, v[2] = {};
+        if (n / 2 <= warp) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (j + e > i) continue;
+            const float f = chunk_decay(gates, i, j + e);
+            v[e] = p.scale * f * qk[n][2 * h + e];
+            if (j + e < i) a[e] = gates[kBeta + i] * f * kk[n][2 * h + e];
+          }
+          if (n / 2 == warp)
+            *reinterpret_cast<float2 *>(diagonal + i * kDiagPitch + j - warp * 16) = make_float2(a[0], a[1]);
+        }
+        uint32_t big, rest;
+        split(v[0], v[1], big, rest);
+        *reinterpret_cast<uint32_t *>(smem + L::kT + at) = big;
+        *reinterpret_cast<uint32_t *>(smem + L::kT + kPairBytes + at) = rest;
+        split(a[0], a[1], big, rest);
+        *reinterpret_cast<uint32_t *>(smem + L::kA + at) = big;
+        *reinterpret_cast<uint32_t *>(smem + L::kA + kPairBytes + at) = rest;
+      }
+    }
+    __syncthreads();
+    store_matrix(out + 2 * kMatrix, smem + L::kT);
+    __syncthreads();
+    {  // zeros above the diagonal's blocks of T, their inverses on it
+#pragma unroll
+      for (int n = 0; n < 3; ++n) {
+        if (n + 1 + warp > 3) continue;
+        const int at = ((warp * 16 + lane / 2) * kTilePitch + (n + 1 + warp) * 16 + lane % 2 * 8) * 2;
+        *reinterpret_cast<uint4 *>(smem + L::kT + at) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(smem + L::kT + kPairBytes + at) = make_uint4(0, 0, 0, 0);
+      }
+      invert_diagonal(diagonal, smem + L::kT);
+    }
+    __syncthreads();
+    invert_below(base + L::kA, base + L::kT);
+    __syncthreads();
+    store_matrix(out, smem + L::kT);
+    float *const kept = reinterpret_cast<float *>(record + kRecordHalfs * 2);
+    for (int at = threadIdx.x; at < kGateFloats; at += kPrepareThreads) kept[at] = gates[at];
+  }
+}
+
+// ------------------------------------------------------------------ walks --
+
+enum { kWalkOut = 0, kWalkKeep = 1 };  // gated_delta(); the gradient's two walks
+
+// A CTA's walk: TEAMS teams of SPLIT warps, each with 16 columns of v (rows of S^T); a
+// team's warps have DK / SPLIT columns of S^T each, so products with the state are sums over the
+// team, and what is solved for is solved in blocks of 16 steps, dealt so that the
+// triangles' work evens out.  Two warps to a scheduler are wanted as one waits for its own
+// products otherwise.
+template <int DK, int TEAMS, int SPLIT>
+struct Walk {
+  static constexpr int kThreads = TEAMS * SPLIT * 32, kSlice = TEAMS * 16, kColumns = DK / SPLIT, kTiles = kColumns / 8,
+                       kBlocks = 4 / SPLIT;  // of 16 steps, per warp
+  static constexpr int kWide = kDeltaChunk * (DK + 8) * 2, kNarrow = kSlice + 8;
+  // a stage
+  static constexpr int kK = 0, kQ = kWide, kV = 2 * kWide, kT = kV + kDeltaChunk * kNarrow * 2, kP = kT + 2 * kPairBytes,
+                       kGates = kP + 2 * kPairBytes, kStage = kGates + 3 * kDeltaChunk * 4;
+  // exchanged within a team: the sums that each warp has of the others' blocks (1 KB each), and
+  // twice the left operands of all four blocks
+  static constexpr int kForeign = 4 - kBlocks, kSums = SPLIT * kForeign * 1024, kOperands = 4 * 1024,
+                       kTeam = kSums + 2 * kOperands;
+  static constexpr int kStages = 2 * kStage + TEAMS * kTeam <= 227 * 1024 ? 2 : 1;
+  static constexpr int kExchange = kStages * kStage, kBytes = kExchange + TEAMS * kTeam;
+  // Block `n` of a warp's kBlocks.
+  static __device__ __forceinline__ int block(int part, int n) {
+    if constexpr (SPLIT == 4) return part;
+    else if constexpr (SPLIT == 2) return n == 0 ? part : 3 - part;
+    else return n;
+  }
+  static __device__ __forceinline__ int owner(int block) {
+    if constexpr (SPLIT == 4) return block;
+    else if constexpr (SPLIT == 2) return block < 2 ? block : 3 - block;
+    else return 0;
+  }
+  // Where a warp leaves its sums of another's block.
+  static __device__ __forceinline__ int foreign(int part, int block) {
+    return part * kForeign + (SPLIT == 4 ? block - (block > part ? 1 : 0) : block / 2);
+  }
+};
+
+// The warps of a team, waiting for one another.
+template <int SPLIT>
+__device__ __forceinline__ void team_sync(int team) {
+  if constexpr (SPLIT > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(SPLIT * 32) : "memory");
+}
+
+// 16 steps x 16 columns of an output, from the sums' layout.
+template <bool F16>
+__device__ __forceinline__ void store_block16(const FragC &c0, const FragC &c1, const HeadsOf &to, bool vector, int64_t b,
+                                              int64_t head, int t0, int steps, int col0, int cols) {
+  typedef Elem<F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16> E;
+  const int lane = threadIdx.x & 31;
+  uint16_t *const out = static_cast<uint16_t *>(const_cast<void *>(to.p)) + b * to.batch + head * to.head + (int64_t)t0 * to.step + col0;
+  if (vector) {
+    // Lanes 4 apart hold neighbouring columns of the same steps: transposed in 8 x 8 blocks, a lane has two
+    // neighbouring columns of one step.
+    uint32_t r[4] = {pack_output<F16>(c0[0], c0[1]), pack_output<F16>(c0[2], c0[3]), pack_output<F16>(c1[0], c1[1]),
+                     pack_output<F16>(c1[2], c1[3])};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %0;" : "+r"(r[i]));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = h * 8 + lane / 4;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int u = i * 8 + lane % 4 * 2;
+        if (t0 + t < steps && col0 + u < cols) *reinterpret_cast<uint32_t *>(out + t * to.step + u) = r[2 * h + i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = e / 4 * 8 + lane % 4 * 2 + e % 2, u = lane / 4 + e / 2 % 2 * 8;
+      if (t0 + t < steps && col0 + u < cols) out[t * to.step + u] = E::put(e < 4 ? c0[e % 4] : c1[e % 4]);
+    }
+  }
+}
+
+// Sums in rows of `pitch` elements (16 rows of v's columns), as bf16 and the rest `plane` behind.
+template <int N>
+__device__ __forceinline__ void keep_split(const FragC (&c)[N], uint16_t *to, int pitch, int64_t plane) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t big, rest;
+      split(c[n][2 * h], c[n][2 * h + 1], big, rest);
+      uint16_t *const at = to + (lane / 4 + 8 * h) * pitch + n * 8 + lane % 4 * 2;
+      *reinterpret_cast<uint32_t *>(at) = big;
+      *reinterpret_cast<uint32_t *>(at + plane) = rest;
+    }
+}
+
+// S^T's rows [row0, row0 + 16), columns [col0, col0 + 8 N).
+template <int N>
+__device__ __forceinline__ void load_state(const float *from, int dk_size, int dv_size, int row0, int col0, FragC (&S)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = row0 + lane / 4 + (e / 2) * 8, i = col0 + n * 8 + lane % 4 * 2 + e % 2;
+      S[n][e] = from && j < dv_size && i < dk_size ? from[(int64_t)i * dv_size + j] : 0.f;
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_state(float *to, int dk_size, int dv_size, int row0, int col0, const FragC (&S)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = row0 + lane / 4 + (e / 2) * 8, i = col0 + n * 8 + lane % 4 * 2 + e % 2;
+      if (j < dv_size && i < dk_size) to[(int64_t)i * dv_size + j] = S[n][e];
+    }
+}
+
+// A left operand's two parts in a team's memory.
+__device__ __forceinline__ void put_operand(char *to, int block, const FragA &big, const FragA &rest) {
+  uint4 *const at = reinterpret_cast<uint4 *>(to) + block * 64 + (threadIdx.x & 31);
+  at[0] = make_uint4(big[0], big[1], big[2], big[3]);
+  at[32] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+}
+__device__ __forceinline__ void get_operand(const char *from, int block, FragA &big, FragA &rest) {
+  const uint4 *const at = reinterpret_cast<const uint4 *>(from) + block * 64 + (threadIdx.x & 31);
+  const uint4 v = at[0], w = at[32];
+  big[0] = v.x; big[1] = v.y; big[2] = v.z; big[3] = v.w;
+  rest[0] = w.x; rest[1] = w.y; rest[2] = w.z; rest[3] = w.w;
+}
+
+template <bool F16, int DK, int TEAMS, int SPLIT, int MODE, bool BACK>
+__device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b, int64_t head, int slice) {
+  typedef Walk<DK, TEAMS, SPLIT> L;
+  constexpr int N = L::kTiles, NB = L::kBlocks;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / SPLIT, part = warp % SPLIT;
+  const int64_t head_k = head / (p.heads / p.heads_k), bh = b * p.heads + head;
+  const int row0 = slice * L::kSlice + team * 16, col0 = part * L::kColumns;  // of S^T
+  const int64_t dvp = (int64_t)((p.dv_size + kDeltaSlice - 1) / kDeltaSlice) * kDeltaSlice,
+                cells = (int64_t)p.dk_size * p.dv_size;
+  // (sums serves K S and O in turn: the one is read before the second wait, the other written after it)
+  char *const sums = smem + L::kExchange + team * L::kTeam, *const solved = sums + L::kSums,
+       *const update = solved + L::kOperands;
+  auto request = [&](int i) {
+    if (i < p.chunks) {
+      const int chunk = BACK ? p.chunks - 1 - i : i, t0 = chunk * kDeltaChunk;
+      const uint32_t at = smem_u32(smem + i % L::kStages * L::kStage);
+      const char *const record = p.records + (bh * p.chunks + chunk) * kRecordBytes;
+      const uint16_t *const m = reinterpret_cast<const uint16_t *>(record);
+      copy_tile<DK, L::kThreads>(at + L::kK, p.tk, b, head_k, t0, p.steps, 0);
+      if (BACK || MODE == kWalkOut) copy_tile<DK, L::kThreads>(at + L::kQ, p.tq, b, head_k, t0, p.steps, 0);
+      copy_tile<L::kSlice, L::kThreads>(at + L::kV, BACK ? p.td : p.tv, b, head, t0, p.steps, slice * L::kSlice);
+      copy_dense<2 * kDeltaChunk, kDeltaChunk, L::kThreads>(at + L::kT, m);
+      if (BACK || MODE == kWalkOut) copy_dense<2 * kDeltaChunk, kDeltaChunk, L::kThreads>(at + L::kP, m + 2 * kMatrix);
+      if (threadIdx.x < 3 * kDeltaChunk / 4)
+        copy16(at + L::kGates + threadIdx.x * 16, record + kRecordHalfs * 2 + threadIdx.x * 16, true);
+    }
+    copies_close();
+  };
+  // c (16 x 64, every warp's part of a sum) to sums over the team, in the warp's own blocks
+  auto give = [&](char *to, const FragC (&c)[8]) {
+    if constexpr (SPLIT > 1) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (L::owner(n) == part) continue;
+        float4 *const at = reinterpret_cast<float4 *>(to + L::foreign(part, n) * 1024 + lane * 16);
+        at[0] = make_float4(c[2 * n][0], c[2 * n][1], c[2 * n][2], c[2 * n][3]);
+        at[32] = make_float4(c[2 * n + 1][0], c[2 * n + 1][1], c[2 * n + 1][2], c[2 * n + 1][3]);
+      }
+    }
+  };
+  auto gather = [&](const char *from, const FragC (&c)[8], FragC (&own)[2 * NB]) {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const int n = L::block(part, i);
+      FragC &x = own[2 * i], &y = own[2 * i + 1];
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        if (m == n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = c[2 * m][e];
+            y[e] = c[2 * m + 1][e];
+          }
+        }
+#pragma unroll
+      for (int w = 1; w < SPLIT; ++w) {
+        const float4 *const at =
+            reinterpret_cast<const float4 *>(from + L::foreign((part + w) % SPLIT, n) * 1024 + lane * 16);
+        const float4 u = at[0], v = at[32];
+        x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+        y[0] += v.x; y[1] += v.y; y[2] += v.z; y[3] += v.w;
+      }
+    }
+  };
+  FragC S[N];
+  wait_for_predecessor();
+  if (L::kStages == 2) request(0);
+  {
+    const float *const from = BACK ? p.dstate : p.h0;
+    load_state<N>(from ? from + bh * cells : nullptr, p.dk_size, p.dv_size, row0, col0, S);
+  }
+  const bool live = MODE == kWalkKeep || row0 < p.dv_size;  // (without columns a team only copies, or keeps zeros)
+  for (int i = 0; i < p.chunks; ++i) {
+    request(L::kStages == 2 ? i + 1 : i);
+    copies_wait<L::kStages - 1>();
+    __syncthreads();
+    const int chunk = BACK ? p.chunks - 1 - i : i, t0 = chunk * kDeltaChunk;
+    char *const stage = smem + i % L::kStages * L::kStage;
+    const uint32_t at = smem_u32(stage), K = at + L::kK, Q = at + L::kQ, V = at + L::kV, T = at + L::kT, P = at + L::kP;
+    const float *const gates = reinterpret_cast<const float *>(stage + L::kGates);
+    if (live) {
+      auto pair = [&](int which, int n) { return *reinterpret_cast<const float2 *>(gates + which + n * 8 + lane % 4 * 2); };
+      auto scale_steps = [&](FragC &c, float2 f) {
+        c[0] *= f.x;
+        c[1] *= f.y;
+        c[2] *= f.x;
+        c[3] *= f.y;
+      };
+      if constexpr (MODE == kWalkKeep) {
+        uint16_t *const to = (BACK ? p.end : p.start) + ((bh * p.chunks + chunk) * 2 * dvp + row0) * DK + col0;
+        keep_split<N>(S, to, DK, dvp * DK);
+      }
+      // products of the state's part with K, and with Q for the output
+      FragC r[8] = {}, o[8] = {};
+#pragma unroll
+      for (int s = 0; s < N / 2; ++s) {
+        FragA big, rest;
+        split_sums(S[2 * s], S[2 * s + 1], big, rest);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          uint32_t x[4];
+          load_matrices(x, at_nk(K, DK + 8, n * 16, col0 + s * 16, lane));
+          mma_split_input<F16>(r[2 * n], r[2 * n + 1], big, rest, x);
+          if constexpr (MODE == kWalkOut) {
+            load_matrices(x, at_nk(Q, DK + 8, n * 16, col0 + s * 16, lane));
+            mma_split_input<F16>(o[2 * n], o[2 * n + 1], big, rest, x);
+          }
+        }
+      }
+      give(sums, r);
+      team_sync<SPLIT>(team);
+      FragC own[2 * NB];  // the warp's blocks of steps
+      gather(sums, r, own);
+#pragma unroll
+      for (int i2 = 0; i2 < NB; ++i2) {
+        const int n = L::block(part, i2);
+        FragC &c0 = own[2 * i2], &c1 = own[2 * i2 + 1];
+        if constexpr (!BACK) {  // R = beta (V - first (K S))
+          uint32_t v[4];
+          load_matrices_t(v, at_km(V, L::kNarrow, n * 16, team * 16, lane));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float2 beta = pair(kBeta, 2 * n + h), first = pair(kFirst, 2 * n + h);
+            const float2 lo = unpack_input<F16>(v[2 * h]), hi = unpack_input<F16>(v[2 * h + 1]);
+            FragC &c = h == 0 ? c0 : c1;
+            c[0] = beta.x * (lo.x - first.x * c[0]);
+            c[1] = beta.y * (lo.y - first.y * c[1]);
+            c[2] = beta.x * (hi.x - first.x * c[2]);
+            c[3] = beta.y * (hi.y - first.y * c[3]);
+          }
+        } else {  // dD = last (K dS) + P^T dO
+          scale_steps(c0, pair(kLast, 2 * n));
+          scale_steps(c1, pair(kLast, 2 * n + 1));
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (s < n) continue;
+            FragA a;
+            uint32_t h[4], l[4];
+            load_matrices_t(a, at_km(V, L::kNarrow, s * 16, team * 16, lane));
+            load_matrices_t(h, at_kn(P, kTilePitch, s * 16, n * 16, lane));
+            load_matrices_t(l, at_kn(P + kPairBytes, kTilePitch, s * 16, n * 16, lane));
+            mma_input_split<F16>(c0, c1, a, h, l);
+          }
+        }
+        FragA big, rest;
+        split_sums(c0, c1, big, rest);
+        put_operand(solved, n, big, rest);
+      }
+      team_sync<SPLIT>(team);
+      // D = T R, or dR = T^T dD, block by block
+      FragC d[2 * NB] = {};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        FragA big, rest;
+        get_operand(solved, s, big, rest);
+#pragma unroll
+        for (int i2 = 0; i2 < NB; ++i2) {
+          const int n = L::block(part, i2);
+          if (BACK ? s < n : s > n) continue;
+          uint32_t h[4], l[4];
+          if constexpr (BACK) {
+            load_matrices_t(h, at_kn(T, kTilePitch, s * 16, n * 16, lane));
+            load_matrices_t(l, at_kn(T + kPairBytes, kTilePitch, s * 16, n * 16, lane));
+          } else {
+            load_matrices(h, at_nk(T, kTilePitch, n * 16, s * 16, lane));
+            load_matrices(l, at_nk(T + kPairBytes, kTilePitch, n * 16, s * 16, lane));
+          }
+          mma_split_split(d[2 * i2], d[2 * i2 + 1], big, rest, h, l);
+        }
+      }
+      if constexpr (MODE == kWalkKeep) {
+        uint16_t *const to = (BACK ? p.dcorr : p.corrections) + ((bh * p.chunks + chunk) * 2 * dvp + row0) * kDeltaChunk;
+#pragma unroll
+        for (int i2 = 0; i2 < NB; ++i2) {
+          const FragC two[2] = {{d[2 * i2][0], d[2 * i2][1], d[2 * i2][2], d[2 * i2][3]},
+                                {d[2 * i2 + 1][0], d[2 * i2 + 1][1], d[2 * i2 + 1][2], d[2 * i2 + 1][3]}};
+          keep_split<2>(two, to + L::block(part, i2) * 16, kDeltaChunk, dvp * kDeltaChunk);
+        }
+      }
+      if constexpr (MODE == kWalkOut) {  // this warp's part of O: first scale (Q S) + P D
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          const float2 first = pair(kFirst, n);
+          scale_steps(o[n], make_float2(p.scale * first.x, p.scale * first.y));
+        }
+#pragma unroll
+        for (int i2 = 0; i2 < NB; ++i2) {
+          const int s = L::block(part, i2);
+          FragA big, rest;
+          split_sums(d[2 * i2], d[2 * i2 + 1], big, rest);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            if (n < s) continue;
+            uint32_t h[4], l[4];
+            load_matrices(h, at_nk(P, kTilePitch, n * 16, s * 16, lane));
+            load_matrices(l, at_nk(P + kPairBytes, kTilePitch, n * 16, s * 16, lane));
+            mma_split_split(o[2 * n], o[2 * n + 1], big, rest, h, l);
+          }
+        }
+        give(sums, o);
+      }
+      // what the state gains: last D, or -beta first dR (beta dR is dV)
+#pragma unroll
+      for (int i2 = 0; i2 < NB; ++i2) {
+        const int n = L::block(part, i2);
+        FragC &c0 = d[2 * i2], &c1 = d[2 * i2 + 1];
+        if constexpr (!BACK) {
+          scale_steps(c0, pair(kLast, 2 * n));
+          scale_steps(c1, pair(kLast, 2 * n + 1));
+        } else {
+          scale_steps(c0, pair(kBeta, 2 * n));
+          scale_steps(c1, pair(kBeta, 2 * n + 1));
+          store_block16<F16>(c0, c1, p.dv, p.vector_dv, b, head, t0 + n * 16, p.steps, row0, p.dv_size);
+          const float2 f0 = pair(kFirst, 2 * n), f1 = pair(kFirst, 2 * n + 1);
+          scale_steps(c0, make_float2(-f0.x, -f0.y));
+          scale_steps(c1, make_float2(-f1.x, -f1.y));
+        }
+        FragA big, rest;
+        split_sums(c0, c1, big, rest);
+        put_operand(update, n, big, rest);
+      }
+      const float whole = gates[kFirst + kDeltaChunk - 1];
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[n][e] *= whole;
+      if constexpr (BACK) {  // + (scale first dO)^T Q
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          FragA a, big, rest;
+          load_matrices_t(a, at_km(V, L::kNarrow, s * 16, team * 16, lane));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // scaled by step: the left operand's columns
+            const float2 first = pair(kFirst, 2 * s + h);
+            const float2 lo = unpack_input<F16>(a[2 * h]), hi = unpack_input<F16>(a[2 * h + 1]);
+            const float x = p.scale * first.x, y = p.scale * first.y;
+            split(lo.x * x, lo.y * y, big[2 * h], rest[2 * h]);
+            split(hi.x * x, hi.y * y, big[2 * h + 1], rest[2 * h + 1]);
+          }
+#pragma unroll
+          for (int n = 0; n < N / 2; ++n) {
+            uint32_t x[4];
+            load_matrices_t(x, at_kn(Q, DK + 8, s * 16, col0 + n * 16, lane));
+            mma_split_input<F16>(S[2 * n], S[2 * n + 1], big, rest, x);
+          }
+        }
+      }
+      team_sync<SPLIT>(team);
+      if constexpr (MODE == kWalkOut) {
+        FragC mine[2 * NB];
+        gather(sums, o, mine);
+#pragma unroll
+        for (int i2 = 0; i2 < NB; ++i2)
+          store_block16<F16>(mine[2 * i2], mine[2 * i2 + 1], p.o, p.vector_o, b, head, t0 + L::block(part, i2) * 16, p.steps,
+                             row0, p.dv_size);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        FragA big, rest;
+        get_operand(update, s, big, rest);
+#pragma unroll
+        for (int n = 0; n < N / 2; ++n) {
+          uint32_t x[4];
+          load_matrices_t(x, at_kn(K, DK + 8, s * 16, col0 + n * 16, lane));
+          mma_split_input<F16>(S[2 * n], S[2 * n + 1], big, rest, x);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  float *const to = BACK ? p.dh0 : p.state;
+  if ((BACK || MODE == kWalkOut) && to) store_state<N>(to + bh * cells, p.dk_size, p.dv_size, row0, col0, S);
+}
+
+template <bool F16, int DK, int TEAMS, int SPLIT>
+__global__ void __launch_bounds__(TEAMS * SPLIT * 32) delta_walk_kernel(const DeltaParams p) {
+  extern __shared__ __align__(16) char smem[];
+  walk<F16, DK, TEAMS, SPLIT, kWalkOut, false>(p, smem, blockIdx.z, blockIdx.y, blockIdx.x);
+}
+
+// The gradient's two walks: columns of v backward in the first half of the grid, forward in the second.
+template <bool F16, int DK, int TEAMS, int SPLIT>
+__global__ void __launch_bounds__(TEAMS * SPLIT * 32) delta_walks_kernel(const DeltaParams p) {
+  extern __shared__ __align__(16) char smem[];
+  const int slices = gridDim.x / 2, slice = blockIdx.x % slices;
+  if ((int)blockIdx.x < slices) walk<F16, DK, TEAMS, SPLIT, kWalkKeep, true>(p, smem, blockIdx.z, blockIdx.y, slice);
+  else walk<F16, DK, TEAMS, SPLIT, kWalkKeep, false>(p, smem, blockIdx.z, blockIdx.y, slice);
+}
+
+template <class P>
+int launch_large(void (*fn)(P), dim3 grid, int threads, int smem, cudaStream_t stream, const P &p) {
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
+  }
+  return launch_op(fn, grid, threads, (size_t)smem, 1, stream, p);
+}
+
+template <bool F16, int DK, int TEAMS, int SPLIT>
+int launch_walk(const DeltaParams &p, bool gradient, cudaStream_t stream) {
+  typedef Walk<DK, TEAMS, SPLIT> L;
+  static_assert(L::kBytes <= 227 * 1024, "a stage and what teams exchange");
+  // (the gradient keeps all of 64 columns)
+  const int columns = gradient ? (p.dv_size + kDeltaSlice - 1) / kDeltaSlice * kDeltaSlice : p.dv_size;
+  const unsigned slices = (unsigned)((columns + L::kSlice - 1) / L::kSlice);
+  const dim3 grid(gradient ? 2 * slices : slices, (unsigned)p.heads, (unsigned)p.batch);
+  return gradient ? launch_large(delta_walks_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, stream, p)
+                  : launch_large(delta_walk_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, stream, p);
+}
+
+template <bool F16, int DK>
+int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t stream) {
+  const int st = launch_large(delta_prepare_kernel<F16, DK>,
+                              dim3((unsigned)p.chunks, (unsigned)p.heads_k, (unsigned)p.batch), kPrepareThreads,
+                              Prepare<DK>::kBytes, stream, p);
+  if (st != GEMV_OK) return st;
+  // Few heads: one team of four warps per CTA while that leaves each its own SM.
+  const int64_t teams = (int64_t)p.batch * p.heads * ((p.dv_size + 15) / 16) * (gradient ? 2 : 1);
+  return teams <= sms ? launch_walk<F16, DK, 1, 4>(p, gradient, stream) : launch_walk<F16, DK, 4, 2>(p, gradient, stream);
+}
+
+template <bool F16>
+int dispatch(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream) {
+  return dk_padded == 64    ? launch_chunks<F16, 64>(p, gradient, sms, stream)
+         : dk_padded == 128 ? launch_chunks<F16, 128>(p, gradient, sms, stream)
+                            : launch_chunks<F16, 256>(p, gradient, sms, stream);
+}
+
+}  // namespace
+
+}  // namespace gemvk

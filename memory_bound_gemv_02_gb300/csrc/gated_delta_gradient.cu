@@ -44,11 +44,6 @@ struct Grad {
                        kSums = kRows + 4 * kParts * kDeltaChunk * 4, kBytes = kSums + (kThreads + 32) * 4;
 };
 
-__device__ __forceinline__ float gate_decay(const float *gates, int i, int j) {
-  if (gates[kDocs + i] != gates[kDocs + j]) return 0.f;
-  return expf((gates[kTotalHi + i] - gates[kTotalHi + j]) + (gates[kTotalLo + i] - gates[kTotalLo + j]));
-}
-
 __device__ __forceinline__ void put_gate(const HeadsOf &h, bool f32, bool f16, int64_t b, int64_t t, int64_t head, float v) {
   void *const to = const_cast<void *>(h.p);
   const int64_t at = b * h.batch + t * h.step + head * h.head;
@@ -265,7 +260,7 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       for (int e = 0; e < 2; ++e) {
         float w = 0.f;
         if (j + e <= i) {
-          const float f = gate_decay(gates, i, j + e);
+          const float f = chunk_decay(gates, i, j + e);
           u[e] = p.scale * f * dp[n][2 * h + e];
           if (j + e < i) {
             m[e] = -f * mm[n][2 * h + e];
@@ -417,7 +412,7 @@ int dispatch(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream) 
 }  // namespace
 
 int launch_delta_gradient(const DeltaParams &p, int dk_padded, int sms, cudaStream_t stream) {
-  const int st = launch_delta_walks(p, dk_padded, stream);
+  const int st = launch_delta_chunks(p, dk_padded, true, sms, stream);
   if (st != GEMV_OK) return st;
   return p.f16 ? dispatch<true>(p, dk_padded, sms, stream) : dispatch<false>(p, dk_padded, sms, stream);
 }

@@ -155,6 +155,18 @@ __device__ __forceinline__ uint32_t at_km(uint32_t base, int pitch, int k, int m
   return base + (uint32_t)((k + (lane & 7) + ((lane >> 4) & 1) * 8) * pitch + m + ((lane >> 3) & 1) * 8) * 2;
 }
 
+// 2^x within 2 units of 2^-23, 0 below fp32's normal range.
+__device__ __forceinline__ float power2(float x) {
+  float v;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(x));
+  return v;
+}
+// The decay from step j to step i >= j of a chunk, 0 across a new document.
+__device__ __forceinline__ float chunk_decay(const float *gates, int i, int j) {
+  if (gates[kDocs + i] != gates[kDocs + j]) return 0.f;
+  return power2((gates[kTotalHi + i] - gates[kTotalHi + j]) + (gates[kTotalLo + i] - gates[kTotalLo + j]));
+}
+
 // ------------------------------------------------------------- copies ahead --
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
