@@ -186,12 +186,14 @@ struct Prepare {
                        kGates = kTiles > kAfter ? kTiles : kAfter, kBytes = kGates + kGateFloats * 4;
 };
 
-// 2 x 64 rows of 64 from shared memory, 16 bytes at a time.
-__device__ __forceinline__ void store_matrix(uint16_t *to, const char *from) {
+// The blocks on and below the diagonal of two 64 x 64 matrices, 16 bytes at a time (nothing
+// reads those above).
+__device__ __forceinline__ void store_lower(uint16_t *to, const char *from) {
 #pragma unroll
   for (int n = 0; n < 2 * kMatrix / 8 / kPrepareThreads; ++n) {
     const int i = n * kPrepareThreads + (int)threadIdx.x;
-    reinterpret_cast<uint4 *>(to)[i] = *reinterpret_cast<const uint4 *>(from + i / 8 * kTilePitch * 2 + i % 8 * 16);
+    if (i % 8 / 2 <= i / 8 % 64 / 16)
+      reinterpret_cast<uint4 *>(to)[i] = *reinterpret_cast<const uint4 *>(from + i / 8 * kTilePitch * 2 + i % 8 * 16);
   }
 }
 
@@ -241,49 +243,48 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
       if (warp == 0) chunk_gates(p, b, head, t0, gates);
     }
     __syncthreads();  // the tiles are done with
+    const int i0 = warp * 16 + lane / 4, j0 = lane % 4 * 2;
+    float hi[2], lo[2], docs[2], beta[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      hi[h] = gates[kTotalHi + i0 + 8 * h];
+      lo[h] = gates[kTotalLo + i0 + 8 * h];
+      docs[h] = gates[kDocs + i0 + 8 * h];
+      beta[h] = gates[kBeta + i0 + 8 * h];
+    }
 #pragma unroll
     for (int n = 0; n < 8; ++n) {
+      if (n / 2 > warp) continue;
+      const int j = n * 8 + j0;
+      const float2 hj = *reinterpret_cast<const float2 *>(gates + kTotalHi + j),
+                   lj = *reinterpret_cast<const float2 *>(gates + kTotalLo + j),
+                   dj = *reinterpret_cast<const float2 *>(gates + kDocs + j);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int i = warp * 16 + lane / 4 + 8 * h, j = n * 8 + lane % 4 * 2, at = (i * kTilePitch + j) * 2;
-        float a[2] = {}, v[2] = {};
-        if (n / 2 <= warp) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (j + e > i) continue;
-            const float f = chunk_decay(gates, i, j + e);
-            v[e] = p.scale * f * qk[n][2 * h + e];
-            if (j + e < i) a[e] = gates[kBeta + i] * f * kk[n][2 * h + e];
-          }
-          if (n / 2 == warp)
-            *reinterpret_cast<float2 *>(diagonal + i * kDiagPitch + j - warp * 16) = make_float2(a[0], a[1]);
-        }
+        const int i = i0 + 8 * h, at = (i * kTilePitch + j) * 2;
+        // from step j to step i: nothing above the diagonal or across a new document
+        const float f0 = j <= i && docs[h] == dj.x ? power2((hi[h] - hj.x) + (lo[h] - lj.x)) : 0.f;
+        const float f1 = j < i && docs[h] == dj.y ? power2((hi[h] - hj.y) + (lo[h] - lj.y)) : 0.f;
+        const float a0 = j < i ? beta[h] * f0 * kk[n][2 * h] : 0.f, a1 = j + 1 < i ? beta[h] * f1 * kk[n][2 * h + 1] : 0.f;
+        if (n / 2 == warp)
+          *reinterpret_cast<float2 *>(diagonal + i * kDiagPitch + j - warp * 16) = make_float2(a0, a1);
         uint32_t big, rest;
-        split(v[0], v[1], big, rest);
+        split(j <= i ? p.scale * f0 * qk[n][2 * h] : 0.f, j < i ? p.scale * f1 * qk[n][2 * h + 1] : 0.f, big, rest);
         *reinterpret_cast<uint32_t *>(smem + L::kT + at) = big;
         *reinterpret_cast<uint32_t *>(smem + L::kT + kPairBytes + at) = rest;
-        split(a[0], a[1], big, rest);
+        split(a0, a1, big, rest);
         *reinterpret_cast<uint32_t *>(smem + L::kA + at) = big;
         *reinterpret_cast<uint32_t *>(smem + L::kA + kPairBytes + at) = rest;
       }
     }
     __syncthreads();
-    store_matrix(out + 2 * kMatrix, smem + L::kT);
+    store_lower(out + 2 * kMatrix, smem + L::kT);
     __syncthreads();
-    {  // zeros above the diagonal's blocks of T, their inverses on it
-#pragma unroll
-      for (int n = 0; n < 3; ++n) {
-        if (n + 1 + warp > 3) continue;
-        const int at = ((warp * 16 + lane / 2) * kTilePitch + (n + 1 + warp) * 16 + lane % 2 * 8) * 2;
-        *reinterpret_cast<uint4 *>(smem + L::kT + at) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(smem + L::kT + kPairBytes + at) = make_uint4(0, 0, 0, 0);
-      }
-      invert_diagonal(diagonal, smem + L::kT);
-    }
+    invert_diagonal(diagonal, smem + L::kT);
     __syncthreads();
     invert_below(base + L::kA, base + L::kT);
     __syncthreads();
-    store_matrix(out, smem + L::kT);
+    store_lower(out, smem + L::kT);
     float *const kept = reinterpret_cast<float *>(record + kRecordHalfs * 2);
     for (int at = threadIdx.x; at < kGateFloats; at += kPrepareThreads) kept[at] = gates[at];
   }
@@ -420,6 +421,20 @@ __device__ __forceinline__ void get_operand(const char *from, int block, FragA &
   rest[0] = w.x; rest[1] = w.y; rest[2] = w.z; rest[3] = w.w;
 }
 
+// S += a X for a left operand a of 16 steps and those steps' rows of X, from column `col` on.
+template <bool F16, int DK, int N>
+__device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, const FragA &rest, uint32_t X, int step, int col) {
+  constexpr int NB = N / 2 < 4 ? N / 2 : 4;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int m = 0; m < N / 2; m += NB) {
+    uint32_t x[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load_matrices_t(x[n], at_kn(X, DK + 8, step, col + (m + n) * 16, lane));
+    mma_split_inputs<F16>(&S[2 * m], big, rest, x);
+  }
+}
+
 template <bool F16, int DK, int TEAMS, int SPLIT, int MODE, bool BACK>
 __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b, int64_t head, int slice) {
   typedef Walk<DK, TEAMS, SPLIT> L;
@@ -441,8 +456,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       copy_tile<DK, L::kThreads>(at + L::kK, p.tk, b, head_k, t0, p.steps, 0);
       if (BACK || MODE == kWalkOut) copy_tile<DK, L::kThreads>(at + L::kQ, p.tq, b, head_k, t0, p.steps, 0);
       copy_tile<L::kSlice, L::kThreads>(at + L::kV, BACK ? p.td : p.tv, b, head, t0, p.steps, slice * L::kSlice);
-      copy_dense<2 * kDeltaChunk, kDeltaChunk, L::kThreads>(at + L::kT, m);
-      if (BACK || MODE == kWalkOut) copy_dense<2 * kDeltaChunk, kDeltaChunk, L::kThreads>(at + L::kP, m + 2 * kMatrix);
+      copy_lower<L::kThreads>(at + L::kT, m);
+      if (BACK || MODE == kWalkOut) copy_lower<L::kThreads>(at + L::kP, m + 2 * kMatrix);
       if (threadIdx.x < 3 * kDeltaChunk / 4)
         copy16(at + L::kGates + threadIdx.x * 16, record + kRecordHalfs * 2 + threadIdx.x * 16, true);
     }
@@ -518,16 +533,15 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       for (int s = 0; s < N / 2; ++s) {
         FragA big, rest;
         split_sums(S[2 * s], S[2 * s + 1], big, rest);
+        uint32_t x[4][4], y[4][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          uint32_t x[4];
-          load_matrices(x, at_nk(K, DK + 8, n * 16, col0 + s * 16, lane));
-          mma_split_input<F16>(r[2 * n], r[2 * n + 1], big, rest, x);
-          if constexpr (MODE == kWalkOut) {
-            load_matrices(x, at_nk(Q, DK + 8, n * 16, col0 + s * 16, lane));
-            mma_split_input<F16>(o[2 * n], o[2 * n + 1], big, rest, x);
-          }
+        for (int n = 0; n < 4; ++n) load_matrices(x[n], at_nk(K, DK + 8, n * 16, col0 + s * 16, lane));
+        if constexpr (MODE == kWalkOut) {
+#pragma unroll
+          for (int n = 0; n < 4; ++n) load_matrices(y[n], at_nk(Q, DK + 8, n * 16, col0 + s * 16, lane));
         }
+        mma_split_inputs<F16>(r, big, rest, x);
+        if constexpr (MODE == kWalkOut) mma_split_inputs<F16>(o, big, rest, y);
       }
       give(sums, r);
       team_sync<SPLIT>(team);
@@ -659,12 +673,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
             split(lo.x * x, lo.y * y, big[2 * h], rest[2 * h]);
             split(hi.x * x, hi.y * y, big[2 * h + 1], rest[2 * h + 1]);
           }
-#pragma unroll
-          for (int n = 0; n < N / 2; ++n) {
-            uint32_t x[4];
-            load_matrices_t(x, at_kn(Q, DK + 8, s * 16, col0 + n * 16, lane));
-            mma_split_input<F16>(S[2 * n], S[2 * n + 1], big, rest, x);
-          }
+          state_plus<F16, DK>(S, big, rest, Q, s * 16, col0);
         }
       }
       team_sync<SPLIT>(team);
@@ -680,12 +689,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       for (int s = 0; s < 4; ++s) {
         FragA big, rest;
         get_operand(update, s, big, rest);
-#pragma unroll
-        for (int n = 0; n < N / 2; ++n) {
-          uint32_t x[4];
-          load_matrices_t(x, at_kn(K, DK + 8, s * 16, col0 + n * 16, lane));
-          mma_split_input<F16>(S[2 * n], S[2 * n + 1], big, rest, x);
-        }
+        state_plus<F16, DK>(S, big, rest, K, s * 16, col0);
       }
     }
     __syncthreads();
@@ -695,14 +699,14 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
 }
 
 template <bool F16, int DK, int TEAMS, int SPLIT>
-__global__ void __launch_bounds__(TEAMS * SPLIT * 32) delta_walk_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(TEAMS * SPLIT * 32, 1) delta_walk_kernel(const DeltaParams p) {
   extern __shared__ __align__(16) char smem[];
   walk<F16, DK, TEAMS, SPLIT, kWalkOut, false>(p, smem, blockIdx.z, blockIdx.y, blockIdx.x);
 }
 
 // The gradient's two walks: columns of v backward in the first half of the grid, forward in the second.
 template <bool F16, int DK, int TEAMS, int SPLIT>
-__global__ void __launch_bounds__(TEAMS * SPLIT * 32) delta_walks_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(TEAMS * SPLIT * 32, 1) delta_walks_kernel(const DeltaParams p) {
   extern __shared__ __align__(16) char smem[];
   const int slices = gridDim.x / 2, slice = blockIdx.x % slices;
   if ((int)blockIdx.x < slices) walk<F16, DK, TEAMS, SPLIT, kWalkKeep, true>(p, smem, blockIdx.z, blockIdx.y, slice);

@@ -40,13 +40,13 @@ __device__ __forceinline__ void store_matrices_t(uint32_t addr, const uint32_t (
 }
 
 __device__ __forceinline__ void mma_bf16(FragC &c, const FragA &a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16(FragC &c, const FragA &a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -138,6 +138,44 @@ __device__ __forceinline__ void mma_input_split(FragC &c0, FragC &c1, const Frag
   }
 }
 
+// The same for NB blocks at once, so that a product does not wait for the one before.
+template <bool F16, int NB>
+__device__ __forceinline__ void mma_split_inputs(FragC *c, const FragA &big, const FragA &rest, const uint32_t (&b)[NB][4]) {
+  if constexpr (F16) {
+    uint32_t h[NB][4], l[NB][4];
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) split_half(b[n][i], h[n][i], l[n][i]);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[2 * n], big, h[n][0], h[n][1]);
+      mma_bf16(c[2 * n + 1], big, h[n][2], h[n][3]);
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[2 * n], rest, h[n][0], h[n][1]);
+      mma_bf16(c[2 * n + 1], rest, h[n][2], h[n][3]);
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[2 * n], big, l[n][0], l[n][1]);
+      mma_bf16(c[2 * n + 1], big, l[n][2], l[n][3]);
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[2 * n], big, b[n][0], b[n][1]);
+      mma_bf16(c[2 * n + 1], big, b[n][2], b[n][3]);
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      mma_bf16(c[2 * n], rest, b[n][0], b[n][1]);
+      mma_bf16(c[2 * n + 1], rest, b[n][2], b[n][3]);
+    }
+  }
+}
+
 // Addresses for load_matrices() of a 16 x 16 block at (row, col) of a matrix in shared
 // memory with `pitch` elements per row.
 //   right operand, stored (n, k), plain loads: registers 0, 1 are the first 8 of n
@@ -183,15 +221,20 @@ __device__ __forceinline__ void copies_wait() {
 template <int COLS, int THREADS>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const TileSource &s, int64_t b, int64_t head, int64_t t0, int steps,
                                           int col) {
-  constexpr int UNITS = COLS / 8;
-  const uint16_t *const base = s.p + b * s.batch + head * s.head + t0 * s.step + col;
+  constexpr int UNITS = COLS / 8, ROWS = THREADS / UNITS;  // rows that a round takes
+  static_assert(THREADS % UNITS == 0 && kDeltaChunk % (ROWS < kDeltaChunk ? ROWS : kDeltaChunk) == 0, "whole rows");
+  const int r0 = (int)threadIdx.x / UNITS, u = (int)threadIdx.x % UNITS;
+  const uint16_t *from = s.p + b * s.batch + head * s.head + (t0 + r0) * s.step + col + u * 8;
+  const int64_t next = ROWS * s.step;
+  uint32_t to = dst + (uint32_t)(r0 * (COLS + 8) + u * 8) * 2;
+  const bool column = col / 8 + u < s.units;
+  int left = column ? steps - (int)t0 - r0 : 0;  // steps from this thread's first row on
 #pragma unroll
-  for (int i = 0; i < (kDeltaChunk * UNITS + THREADS - 1) / THREADS; ++i) {
-    const int at = i * THREADS + (int)threadIdx.x;
-    if (kDeltaChunk * UNITS % THREADS != 0 && at >= kDeltaChunk * UNITS) break;
-    const int r = at / UNITS, u = at % UNITS;
-    const bool there = t0 + r < steps && col / 8 + u < s.units;
-    copy16(dst + (uint32_t)(r * (COLS + 8) + u * 8) * 2, there ? base + r * s.step + u * 8 : s.p, there);
+  for (int i = 0; i < (kDeltaChunk + ROWS - 1) / ROWS; ++i) {
+    if (ROWS <= kDeltaChunk || r0 < kDeltaChunk) copy16(to, left > 0 ? from : s.p, left > 0);
+    from += next;
+    to += ROWS * (COLS + 8) * 2;
+    left -= ROWS;
   }
 }
 // ROWS dense rows of COLS elements, to rows of COLS + 8.
@@ -203,6 +246,16 @@ __device__ __forceinline__ void copy_dense(uint32_t dst, const uint16_t *src) {
     const int at = i * THREADS + (int)threadIdx.x;
     if (ROWS * UNITS % THREADS != 0 && at >= ROWS * UNITS) break;
     copy16(dst + (uint32_t)(at / UNITS * (COLS + 8) + at % UNITS * 8) * 2, src + (int64_t)at * 8, true);
+  }
+}
+// The 16 x 16 blocks on and below the diagonal of two 64 x 64 matrices, dense, to rows
+// of 72.
+template <int THREADS>
+__device__ __forceinline__ void copy_lower(uint32_t dst, const uint16_t *src) {
+#pragma unroll
+  for (int i = 0; i < 2 * kMatrix / 8 / THREADS; ++i) {
+    const int at = i * THREADS + (int)threadIdx.x, row = at / 8, u = at % 8;
+    if (u / 2 <= row % 64 / 16) copy16(dst + (uint32_t)(row * (kDeltaChunk + 8) + u * 8) * 2, src + at * 8, true);
   }
 }
 
