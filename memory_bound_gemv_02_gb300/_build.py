@@ -36,7 +36,8 @@ EXTENSION_STAMP = os.path.join(LIBDIR, "operators_py.built")  # what it was buil
 
 SOURCES = ["gemv_api.cu", "gemv_kernels_f16.cu", "gemv_kernels_bf16.cu", "gemv_bulk_f16.cu", "gemv_bulk_bf16.cu",
            "gla_decode.cu", "rms_norm.cu", "gated_scan.cu", "gemm.cu", "layer_norm.cu", "gated_delta.cu",
-           "gated_delta_chunks_f16.cu", "gated_delta_chunks_bf16.cu", "gated_delta_gradient.cu"]
+           "gated_delta_chunks_f16.cu", "gated_delta_chunks_bf16.cu", "gated_delta_gradient.cu",
+           "gated_delta_tensor.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("gemv_internal.h", "gemv_kernels.cuh", "gemv_tiles.cuh",
                                            "gemv_bulk.cuh", "ops_internal.h", "tc_ptx.cuh",
                                            "tensor_map.h", "gated_delta.h", "gated_delta_mma.cuh",

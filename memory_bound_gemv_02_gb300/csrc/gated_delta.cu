@@ -385,7 +385,7 @@ int check_types(const gated_delta_shape &s) {
   return GEMV_OK;
 }
 
-void fill(DeltaParams &p, const gated_delta_shape &s, const gemv_heads *q, const gemv_heads *k, const gemv_heads *v,
+int fill(DeltaParams &p, int dev, const gated_delta_shape &s, const gemv_heads *q, const gemv_heads *k, const gemv_heads *v,
           const gemv_heads *g, const gemv_heads *beta, const float *h0) {
   p.q = heads_of(q); p.k = heads_of(k); p.v = heads_of(v); p.g = heads_of(g); p.beta = heads_of(beta);
   p.h0 = h0;
@@ -395,6 +395,8 @@ void fill(DeltaParams &p, const gated_delta_shape &s, const gemv_heads *q, const
   p.chunks = (int32_t)((s.steps + kDeltaChunk - 1) / kDeltaChunk);
   p.gates_f32 = s.gate_dtype == GEMV_TYPE_F32 ? 1 : 0;
   p.f16 = s.dtype == GEMV_TYPE_F16 ? 1 : 0;
+  p.polls = take_wait_budget(kWaitPolls);
+  return wait_counter(dev, &p.timeouts);
 }
 
 struct Operand {
@@ -478,7 +480,7 @@ extern "C" int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, 
   if (s.steps == 0) return copy_state(h0, state, cells, stream);
   if (!on_device(dev, {q->p, k->p, v->p, g->p, beta->p, o->p, need > 0 ? workspace : nullptr})) return GEMV_ERR_DEVICE;
   DeltaParams p = {};
-  fill(p, s, q, k, v, g, beta, h0);
+  if ((st = fill(p, dev, s, q, k, v, g, beta, h0)) != GEMV_OK) return st;
   p.o = heads_of(o);
   p.state = state;
   if (s.steps <= kWalkSteps) return launch_delta_steps(p, sms, stream);
@@ -542,7 +544,7 @@ extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_h
   if (!on_device(dev, {d_o->p, q->p, k->p, v->p, g->p, beta->p, dq->p, dk->p, dv->p, dg->p, dbeta->p, workspace}))
     return GEMV_ERR_DEVICE;
   DeltaParams p = {};
-  fill(p, s, q, k, v, g, beta, h0);
+  if ((st = fill(p, dev, s, q, k, v, g, beta, h0)) != GEMV_OK) return st;
   p.d_o = heads_of(d_o);
   p.dstate = dstate;
   p.dq = heads_of(dq); p.dk = heads_of(dk); p.dv = heads_of(dv); p.dg = heads_of(dg); p.dbeta = heads_of(dbeta);

@@ -52,6 +52,8 @@ struct DeltaParams {
   float scale;
   int32_t batch, steps, heads, heads_k, dk_size, dv_size, chunks;
   int32_t gates_f32, f16, vector_o, vector_dv;
+  int32_t polls;       // of the tensor walk's waits
+  uint32_t *timeouts;
 };
 
 // Copies of operands whose rows are not on 16 bytes, padded to 16.
@@ -67,6 +69,8 @@ int launch_delta_pack(const PackParams &p, cudaStream_t stream);
 // The chunks' matrices and the walk over them, or (gradient) the gradient's two walks.
 int launch_delta_chunks_f16(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream);
 int launch_delta_chunks_bf16(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream);
+// The walks alone, of bf16 with 64 < dk <= 128 and more than 64 columns of v.
+int launch_delta_tensor(const DeltaParams &p, bool gradient, cudaStream_t stream);
 inline int launch_delta_chunks(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream) {
   return p.f16 ? launch_delta_chunks_f16(p, dk_padded, gradient, sms, stream)
                : launch_delta_chunks_bf16(p, dk_padded, gradient, sms, stream);

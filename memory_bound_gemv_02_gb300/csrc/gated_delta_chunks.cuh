@@ -743,7 +743,9 @@ int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t str
   if (st != GEMV_OK) return st;
   // Few heads: one team of four warps per CTA while that leaves each its own SM.
   const int64_t teams = (int64_t)p.batch * p.heads * ((p.dv_size + 15) / 16) * (gradient ? 2 : 1);
-  return teams <= sms ? launch_walk<F16, DK, 1, 4>(p, gradient, stream) : launch_walk<F16, DK, 4, 2>(p, gradient, stream);
+  if (teams <= sms) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);
+  if (!F16 && DK == 128 && p.dv_size > 64) return launch_delta_tensor(p, gradient, stream);
+  return launch_walk<F16, DK, 4, 2>(p, gradient, stream);
 }
 
 template <bool F16>

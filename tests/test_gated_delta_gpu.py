@@ -74,6 +74,22 @@ def test_backward(cuda_dev, size, dtype, gates):
     check_backward(x, None, do, None, run_back(x, do), "without states")
 
 
+MANY = [  # enough heads for a CTA of wide columns each
+    (4, 64, 2, 6, 128, 128), (4, 70, 6, 6, 128, 128), (2, 200, 10, 10, 100, 99), (5, 129, 5, 5, 72, 200),
+    (3, 193, 4, 8, 65, 128), (20, 49, 1, 2, 128, 65), (4, 130, 3, 9, 64, 128), (3, 100, 8, 8, 256, 96)]
+
+
+@pytest.mark.parametrize("size", MANY)
+@pytest.mark.parametrize("dtype,gates", [(BF16, F32), (F16, F32), (BF16, BF16)])
+def test_many_heads(cuda_dev, size, dtype, gates):
+    x, h0, do, dstate = make(cuda_dev, *size, dtype, gates, resets=(size[1] // 3,))
+    o, state = run(x, h0)
+    check_forward(x, h0, o, state)
+    check_backward(x, h0, do, dstate, run_back(x, do, h0, dstate))
+    o, state = run(x)
+    check_forward(x, None, o, state, "from zero")
+
+
 @pytest.mark.parametrize("steps,resets", [(40, (0, 1, 39)), (200, (0,)), (200, (63, 64, 65)), (200, (128, 199)),
                                           (130, tuple(range(130))), (300, (17, 100, 101, 256))])
 def test_new_documents(cuda_dev, steps, resets):
@@ -313,3 +329,21 @@ def test_refusals(cuda_dev):
     with pytest.raises(g.GemvError) as e:
         run(y, h0)
     assert e.value.status == g.GEMV_ERR_ARG
+
+
+@pytest.mark.parametrize("size", [(4, 130, 6, 6, 128, 128)])
+def test_a_wait_that_gives_up(cuda_dev, size):
+    """Waits without a poll: NaN instead of a hang, a count, and nothing left behind."""
+    x, h0, do, dstate = make(cuda_dev, *size, BF16)
+    want = (*run(x, h0), *run_back(x, do, h0, dstate))
+    torch.cuda.synchronize()
+    g.gemv_wait_timeouts(reset=True)
+    for back in (False, True):
+        g.gemv_debug_wait_budget(0)
+        got = run_back(x, do, h0, dstate) if back else run(x, h0)
+        torch.cuda.synchronize()
+        assert torch.isnan(got[-1]).all() and torch.isnan(got[0].float()).all()
+        assert g.gemv_wait_timeouts(reset=True) > 0
+    g.gemv_debug_wait_budget(-1)
+    got = (*run(x, h0), *run_back(x, do, h0, dstate))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
