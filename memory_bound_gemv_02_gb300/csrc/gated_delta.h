@@ -46,8 +46,9 @@ struct DeltaParams {
   HeadsOf o, dq, dk, dv, dg, dbeta;  // outputs
   float *state, *dh0;
   char *records;                   // (batch, heads, chunks) of kRecordBytes
-  uint16_t *start, *end;           // gradient: states before a chunk, gradients behind it, (.., 2, dvp, DK) bf16
-  uint16_t *corrections, *dcorr;   // and its corrections and their gradients, (.., 2, dvp, 64)
+  // gradient: states before a chunk and gradients behind it, (.., 2, DK / 8, dvp, 8) bf16, and its
+  // corrections and their gradients, (.., 2, 8, dvp, 8)
+  uint16_t *start, *end, *corrections, *dcorr;
   float *dq32, *dk32;              // gradients per head of v where heads of k are shared
   float scale;
   int32_t batch, steps, heads, heads_k, dk_size, dv_size, chunks;

@@ -368,9 +368,10 @@ __device__ __forceinline__ void store_block16(const FragC &c0, const FragC &c1, 
   }
 }
 
-// Sums in rows of `pitch` elements (16 rows of v's columns), as bf16 and the rest `plane` behind.
+// Sums of 16 rows, kept for the gradient as bf16 and the rest `plane` behind: tiles of 8 columns
+// are `rows` rows of 16 bytes each.
 template <int N>
-__device__ __forceinline__ void keep_split(const FragC (&c)[N], uint16_t *to, int pitch, int64_t plane) {
+__device__ __forceinline__ void keep_split(const FragC *c, uint16_t *to, int64_t rows, int64_t plane) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 0; n < N; ++n)
@@ -378,7 +379,7 @@ __device__ __forceinline__ void keep_split(const FragC (&c)[N], uint16_t *to, in
     for (int h = 0; h < 2; ++h) {
       uint32_t big, rest;
       split(c[n][2 * h], c[n][2 * h + 1], big, rest);
-      uint16_t *const at = to + (lane / 4 + 8 * h) * pitch + n * 8 + lane % 4 * 2;
+      uint16_t *const at = to + (n * rows + lane / 4 + 8 * h) * 8 + lane % 4 * 2;
       *reinterpret_cast<uint32_t *>(at) = big;
       *reinterpret_cast<uint32_t *>(at + plane) = rest;
     }
@@ -524,8 +525,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         c[3] *= f.y;
       };
       if constexpr (MODE == kWalkKeep) {
-        uint16_t *const to = (BACK ? p.end : p.start) + ((bh * p.chunks + chunk) * 2 * dvp + row0) * DK + col0;
-        keep_split<N>(S, to, DK, dvp * DK);
+        uint16_t *const to = (BACK ? p.end : p.start) + (bh * p.chunks + chunk) * 2 * dvp * DK;
+        keep_split<N>(S, to + (col0 / 8 * dvp + row0) * 8, dvp, dvp * DK);
       }
       // products of the state's part with K, and with Q for the output
       FragC r[8] = {}, o[8] = {};
@@ -605,13 +606,10 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         }
       }
       if constexpr (MODE == kWalkKeep) {
-        uint16_t *const to = (BACK ? p.dcorr : p.corrections) + ((bh * p.chunks + chunk) * 2 * dvp + row0) * kDeltaChunk;
+        uint16_t *const to = (BACK ? p.dcorr : p.corrections) + (bh * p.chunks + chunk) * 2 * dvp * kDeltaChunk;
 #pragma unroll
-        for (int i2 = 0; i2 < NB; ++i2) {
-          const FragC two[2] = {{d[2 * i2][0], d[2 * i2][1], d[2 * i2][2], d[2 * i2][3]},
-                                {d[2 * i2 + 1][0], d[2 * i2 + 1][1], d[2 * i2 + 1][2], d[2 * i2 + 1][3]}};
-          keep_split<2>(two, to + L::block(part, i2) * 16, kDeltaChunk, dvp * kDeltaChunk);
-        }
+        for (int i2 = 0; i2 < NB; ++i2)
+          keep_split<2>(&d[2 * i2], to + (L::block(part, i2) * 2 * dvp + row0) * 8, dvp, dvp * kDeltaChunk);
       }
       if constexpr (MODE == kWalkOut) {  // this warp's part of O: first scale (Q S) + P D
 #pragma unroll

@@ -122,21 +122,21 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
   float whole = 0.f, vr = 0.f;
   for (int col_v = 0; col_v < p.dv_size; col_v += L::kSlice) {
     if (col_v > 0) __syncthreads();
-    const uint16_t *const s0 = p.start + (at * 2 * dvp + col_v) * DK, *const s1 = p.end + (at * 2 * dvp + col_v) * DK;
-    const uint16_t *const c0 = p.corrections + (at * 2 * dvp + col_v) * kDeltaChunk,
-                         *const c1 = p.dcorr + (at * 2 * dvp + col_v) * kDeltaChunk;
+    const uint16_t *const s0 = p.start + at * 2 * dvp * DK + col_v * 8, *const s1 = p.end + at * 2 * dvp * DK + col_v * 8;
+    const uint16_t *const c0 = p.corrections + at * 2 * dvp * kDeltaChunk + col_v * 8,
+                         *const c1 = p.dcorr + at * 2 * dvp * kDeltaChunk + col_v * 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      copy_dense<L::kSlice, DK, L::kThreads>(base + L::kS + h * L::kStates, s0 + h * dvp * DK);
-      copy_dense<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kR + h * L::kSteps, c1 + h * dvp * kDeltaChunk);
+      copy_kept<L::kSlice, DK, L::kThreads>(base + L::kS + h * L::kStates, s0 + h * dvp * DK, dvp);
+      copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kR + h * L::kSteps, c1 + h * dvp * kDeltaChunk, dvp);
     }
     copy_tile<L::kSlice, L::kThreads>(base + L::kDo, p.td, b, head, t0, p.steps, col_v);
     copy_tile<L::kSlice, L::kThreads>(base + L::kV, p.tv, b, head, t0, p.steps, col_v);
     copies_close();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      copy_dense<L::kSlice, DK, L::kThreads>(base + L::kE + h * L::kStates, s1 + h * dvp * DK);
-      copy_dense<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kD + h * L::kSteps, c0 + h * dvp * kDeltaChunk);
+      copy_kept<L::kSlice, DK, L::kThreads>(base + L::kE + h * L::kStates, s1 + h * dvp * DK, dvp);
+      copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kD + h * L::kSteps, c0 + h * dvp * kDeltaChunk, dvp);
     }
     copies_close();
     copies_wait<1>();

@@ -237,15 +237,20 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, const TileSource &s, int
     left -= ROWS;
   }
 }
-// ROWS dense rows of COLS elements, to rows of COLS + 8.
+// ROWS rows of COLS elements of what the walks have kept (units of 8 columns, `rows` of 16
+// bytes each), to rows of COLS + 8.
 template <int ROWS, int COLS, int THREADS>
-__device__ __forceinline__ void copy_dense(uint32_t dst, const uint16_t *src) {
-  constexpr int UNITS = COLS / 8;
+__device__ __forceinline__ void copy_kept(uint32_t dst, const uint16_t *src, int64_t rows) {
+  constexpr int UNITS = COLS / 8, ROUND = THREADS / ROWS;  // units that a round takes
+  static_assert(THREADS % ROWS == 0, "whole units");
+  const int r = threadIdx.x % ROWS, u0 = threadIdx.x / ROWS;
+  const uint16_t *from = src + (u0 * rows + r) * 8;
+  const int64_t next = ROUND * rows * 8;
+  dst += (uint32_t)(r * (COLS + 8) + u0 * 8) * 2;
 #pragma unroll
-  for (int i = 0; i < (ROWS * UNITS + THREADS - 1) / THREADS; ++i) {
-    const int at = i * THREADS + (int)threadIdx.x;
-    if (ROWS * UNITS % THREADS != 0 && at >= ROWS * UNITS) break;
-    copy16(dst + (uint32_t)(at / UNITS * (COLS + 8) + at % UNITS * 8) * 2, src + (int64_t)at * 8, true);
+  for (int i = 0; i < (UNITS + ROUND - 1) / ROUND; ++i) {
+    if (UNITS % ROUND == 0 || u0 + i * ROUND < UNITS) copy16(dst + i * ROUND * 16, from, true);
+    from += next;
   }
 }
 // The 16 x 16 blocks on and below the diagonal of two 64 x 64 matrices, dense, to rows

@@ -15,14 +15,17 @@
 // or as columns of the same tile: descriptors with the one or the other major.
 //
 // The walk is a chain: per chunk three products of 512 + 240 + 512 cycles (two, three,
-// two terms of split operands at 8192 flops a cycle) and between them what the threads do, 128 x 128 + 2 x 128 x 64
-// values converted by eight warps.
+// two terms of split operands at 8192 flops a cycle) and between them what the threads do,
+// 128 x 128 + 2 x 128 x 64 values converted: sixteen warps for that alone.  Copies into shared
+// memory, outputs and what the gradient keeps have warps of their own, beside the chain.
 #include "gated_delta_mma.cuh"
 
 namespace gemvk {
 namespace {
 
-constexpr int kComputeWarps = 8, kTensorThreads = 32 * (kComputeWarps + 2), kCopyWarp = 8, kIssueWarp = 9;
+constexpr int kGroups = 4, kComputeWarps = 4 * kGroups, kDrainWarps = 4, kCopyWarps = 3;
+constexpr int kFirstCopy = kComputeWarps + kDrainWarps, kIssueWarp = kFirstCopy + kCopyWarps,
+              kTensorThreads = 32 * (kIssueWarp + 1);
 constexpr int kRowsPerCta = 128, kWidth = 128;  // columns of v; dk
 constexpr int kTileBytes64 = 64 * 128;          // 64 rows of 64 elements, swizzled
 constexpr int kOffK = 0, kOffQ = 2 * kTileBytes64, kOffT = 4 * kTileBytes64, kOffP = 6 * kTileBytes64,
@@ -34,8 +37,9 @@ constexpr uint32_t kColS = 0, kColSA = 128, kColW = 256, kColWA = 320, kColD = 3
 
 struct TensorShared {
   uint64_t full[2], empty[2];
-  uint64_t state_ready, right_ready, solved_ready, out_read;     // from the threads
+  uint64_t state_ready, right_ready, solved_ready;               // from the computing threads
   uint64_t products, solved, updated, out_done, drained;         // from the tensor cores
+  uint64_t state_read, out_read;                                 // from the draining threads
   uint32_t tmem;
   int failed;
 };
@@ -52,6 +56,11 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&v)[
           "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const float (&v)[16]) {
   uint32_t u[16];
@@ -76,10 +85,22 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// 16 values as two bf16 each, pairs of neighbours.
-__device__ __forceinline__ void split16(const float (&v)[16], uint32_t (&big)[16], uint32_t (&rest)[16], int at) {
+// 16 values as two bf16 each, pairs of neighbours, to 8 columns of tensor memory each.
+__device__ __forceinline__ void store_split16(const float (&v)[16], uint32_t to, uint32_t to_rest) {
+  uint32_t big[8], rest[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) split(v[2 * i], v[2 * i + 1], big[at + i], rest[at + i]);
+  for (int i = 0; i < 8; ++i) split(v[2 * i], v[2 * i + 1], big[i], rest[i]);
+  tmem_store8(to, big);
+  tmem_store8(to_rest, rest);
+}
+
+// 16 gates, the same for all threads.
+__device__ __forceinline__ void load_gates(const float *from, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 f = reinterpret_cast<const float4 *>(from)[i];
+    v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+  }
 }
 
 template <int MODE, bool BACK>
@@ -97,55 +118,48 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
   auto wait = [&](uint64_t *bar, int parity) {
     return wait_for<false>(smem_u32(bar), (uint32_t)parity & 1u, &sh.failed, p.polls) && !*(volatile int *)&sh.failed;
   };
-  if (warp == kCopyWarp) {
-    auto copy_swizzled = [&](uint32_t to, const TileSource &s, int64_t h, int t0) {
-      // lane: unit lane % 16 of 16 bytes, every second row
-      const int u = lane % 16, r0 = lane / 16;
-      const uint16_t *from = s.p + b * s.batch + h * s.head + (int64_t)(t0 + r0) * s.step + u * 8;
+  if (warp >= kFirstCopy && warp < kIssueWarp) {
+    // one warp K and T, one Q and P, one V (or dO) and the gates; 16 bytes per lane
+    const int part = warp - kFirstCopy, u = lane % 16, r0 = lane / 16;
+    auto copy_rows = [&](uint32_t to, const TileSource &s, int64_t h, int t0, int unit0, bool swizzled) {
+      const uint16_t *from = s.p + b * s.batch + h * s.head + (int64_t)(t0 + r0) * s.step + (unit0 + u) * 8;
       const int64_t next = 2 * s.step;
-      int left = u < s.units ? p.steps - t0 - r0 : 0;
+      const int left = unit0 + u < s.units ? p.steps - t0 - r0 : 0;
+      // a row's place in 8 changes by 2 per round: two bits of the swizzled address
+      const uint32_t at = swizzled ? to + (uint32_t)(u / 8 * kTileBytes64 + r0 * 128 + ((u % 8) ^ r0) * 16)
+                                   : to + (uint32_t)(r0 * 256 + u * 16);
 #pragma unroll 8
       for (int i = 0; i < 32; ++i) {
-        const int r = 2 * i + r0;
-        copy16(to + (uint32_t)(u / 8 * kTileBytes64 + r * 128 + ((u % 8) ^ (r & 7)) * 16), left > 0 ? from : s.p, left > 0);
+        copy16(swizzled ? (at ^ (uint32_t)((2 * i & 7) * 16)) + 256 * i : at + 512 * i, left > 2 * i ? from : s.p, left > 2 * i);
         from += next;
-        left -= 2;
       }
     };
     auto copy_blocks = [&](uint32_t to, const uint16_t *from) {  // two matrices' blocks on and below the diagonal
-      const int u = lane % 8, r0 = lane / 8;
+      const int v = lane % 8;
 #pragma unroll 8
       for (int i = 0; i < 32; ++i) {
-        const int row = 4 * i + r0;
-        if (u / 2 <= row % 64 / 16) copy16(to + (uint32_t)(row * 128 + (u ^ (row & 7)) * 16), from + row * 64 + u * 8, true);
+        const int row = i * 4 + lane / 8;
+        if (v / 2 <= row % 64 / 16) copy16(to + (uint32_t)(row * 128 + (v ^ (row & 7)) * 16), from + row * 64 + v * 8, true);
       }
     };
     for (int i = 0; i < p.chunks; ++i) {
       if (i >= 2 && !wait(&sh.empty[i & 1], i / 2 - 1)) break;
-      {
-        const int chunk = chunk_of(i), t0 = chunk * kDeltaChunk;
-        const uint32_t at = base + (uint32_t)((i & 1) * kStageBytes);
-        const char *const record = p.records + (bh * p.chunks + chunk) * kRecordBytes;
-        const uint16_t *const m = reinterpret_cast<const uint16_t *>(record);
-        copy_swizzled(at + kOffK, p.tk, head_k, t0);
-        if (kQ) copy_swizzled(at + kOffQ, p.tq, head_k, t0);
+      const int chunk = chunk_of(i), t0 = chunk * kDeltaChunk;
+      const uint32_t at = base + (uint32_t)((i & 1) * kStageBytes);
+      const char *const record = p.records + (bh * p.chunks + chunk) * kRecordBytes;
+      const uint16_t *const m = reinterpret_cast<const uint16_t *>(record);
+      if (part == 0) {
+        copy_rows(at + kOffK, p.tk, head_k, t0, 0, true);
         copy_blocks(at + kOffT, m);
-        if (kQ) copy_blocks(at + kOffP, m + 2 * kMatrix);
-        {  // V or dO, as it is: 128 columns from the slice's first
-          const TileSource &s = BACK ? p.td : p.tv;
-          const int u = lane % 16, r0 = lane / 16;
-          const uint16_t *from = s.p + b * s.batch + head * s.head + (int64_t)(t0 + r0) * s.step + slice * kRowsPerCta + u * 8;
-          const int64_t next = 2 * s.step;
-          int left = slice * (kRowsPerCta / 8) + u < s.units ? p.steps - t0 - r0 : 0;
-#pragma unroll 8
-          for (int r = 0; r < 32; ++r) {
-            copy16(at + kOffV + (uint32_t)((2 * r + r0) * 256 + u * 16), left > 0 ? from : s.p, left > 0);
-            from += next;
-            left -= 2;
-          }
+      } else if (part == 1) {
+        if (kQ) {
+          copy_rows(at + kOffQ, p.tq, head_k, t0, 0, true);
+          copy_blocks(at + kOffP, m + 2 * kMatrix);
         }
-        for (int u = lane; u < kGateBytes / 16; u += 32)
-          copy16(base + (uint32_t)(2 * kStageBytes + i % kGateRing * kGateBytes + u * 16), record + kRecordHalfs * 2 + u * 16, true);
+      } else {
+        copy_rows(at + kOffV, BACK ? p.td : p.tv, head, t0, slice * (kRowsPerCta / 8), false);
+        for (int v = lane; v < kGateBytes / 16; v += 32)
+          copy16(base + (uint32_t)(2 * kStageBytes + i % kGateRing * kGateBytes + v * 16), record + kRecordHalfs * 2 + v * 16, true);
       }
       copies_close();
       copies_wait<0>();
@@ -233,17 +247,27 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
     wait_for<false>(smem_u32(&sh.drained), 0, &none, kWaitPolls);
     return;
   }
-  // ------------------------------------------------------- a thread per row and half --
-  const int half = warp / 4, row = warp % 4 * 32 + lane;  // of the columns; of S^T
-  const int j = slice * kRowsPerCta + row;                // column of v
+  const int row = warp % 4 * 32 + lane;     // of S^T
+  const int j = slice * kRowsPerCta + row;  // column of v
   const bool there = j < p.dv_size;
   const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-  const float nan = __int_as_float(0x7fc00000);
+  const float nan = __int_as_float(0x7fc07fc0);  // (as two bf16 too)
   auto give = [&](uint64_t *bar) {  // what this warp has written to tensor memory, or read from it
     tmem_stored();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive(bar);
+  };
+  auto get = [&](bool ok, uint32_t column, float (&v)[2][16]) {  // 32 columns
+    if (ok) {
+      tmem_request16(lanes + column, v[0]);
+      tmem_request16(lanes + column + 16, v[1]);
+      tmem_arrived16(v[0]);
+      tmem_arrived16(v[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) v[e / 16][e % 16] = nan;
+    }
   };
   auto get16 = [&](bool ok, uint32_t column, float (&v)[16]) {
     if (ok) {
@@ -253,182 +277,204 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
       for (int e = 0; e < 16; ++e) v[e] = nan;
     }
   };
-  // 16 steps x this thread's column of an output
-  auto store_steps = [&](const HeadsOf &to, const float (&v)[16], int t) {
-    if (!there) return;
-    uint16_t *at = static_cast<uint16_t *>(const_cast<void *>(to.p)) + b * to.batch + head * to.head + (int64_t)t * to.step + j;
+  auto gates_of = [&](int i) { return reinterpret_cast<const float *>(ring + i % kGateRing * kGateBytes); };
+  if (warp >= kComputeWarps) {
+    // ---------------------------------------------------- outputs, a thread per row --
+    // 16 steps x this thread's column of an output: lanes trade, so that each has two columns of
+    // every second step
+    auto store_steps = [&](const HeadsOf &to, bool pairs, const float (&v)[16], int t) {
+      uint16_t *const rows = static_cast<uint16_t *>(const_cast<void *>(to.p)) + b * to.batch + head * to.head;
+      const int odd = lane & 1;
+      if (pairs) {
+        char *at = reinterpret_cast<char *>(rows + (int64_t)(t + odd) * to.step + (j - odd));
+        const int64_t next = 4 * to.step;
+        const int left = there ? p.steps - t - odd : 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (t + e < p.steps) *at = BF16::from_float(v[e]);
-      at += to.step;
+        for (int e = 0; e < 16; e += 2) {
+          const uint32_t mine = Elem<GEMV_TYPE_BF16>::pair(v[e], v[e + 1]), other = __shfl_xor_sync(0xffffffffu, mine, 1);
+          const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+          if (left > e) *reinterpret_cast<uint32_t *>(at) = both;
+          at += next;
+        }
+      } else if (there) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (t + e < p.steps) rows[(int64_t)(t + e) * to.step + j] = BF16::from_float(v[e]);
+      }
+    };
+    // 16 columns of tensor memory (32 of bf16) as they are, for the gradient: units of 8 columns, rows
+    // of all of v's columns
+    auto keep = [&](bool ok, uint32_t column, uint16_t *to) {
+      float v[16];
+      get16(ok, column, v);
+      if (j >= dvp) return;
+      uint4 *at = reinterpret_cast<uint4 *>(to) + j;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        at[0] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                           __float_as_uint(v[4 * q + 3]));
+        at += dvp;
+      }
+    };
+    for (int i = 0; i < p.chunks; ++i) {
+      const int chunk = chunk_of(i), t0 = chunk * kDeltaChunk;
+      const int64_t record = bh * p.chunks + chunk;
+      const float *const gates = gates_of(i);
+      if constexpr (kOut) {
+        const bool ok = wait(&sh.out_done, i);
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float u[2][16], v[2][16];
+          get(ok, kColO + h * 32, u);
+          get(ok, kColD + h * 32, v);
+          if (h == 1) give(&sh.out_read);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int c = h * 32 + q * 16;
+            float first[16];
+            load_gates(gates + kFirst + c, first);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[q][e] = fmaf(p.scale * first[e], u[q][e], v[q][e]);
+            store_steps(p.o, p.vector_o, v[q], t0 + c);
+          }
+        }
+      } else {
+        bool ok = wait(&sh.state_ready, i);
+        tc_fence_after();
+        uint16_t *const to = (BACK ? p.end : p.start) + record * 2 * dvp * kWidth;
+#pragma unroll 1
+        for (int h = 0; h < 8; ++h)
+          keep(ok, kColSA + h * 16, to + (int64_t)(h / 4) * dvp * kWidth + (int64_t)(h % 4) * 4 * dvp * 8);
+        give(&sh.state_read);
+        ok = wait(&sh.solved_ready, i) && ok;
+        tc_fence_after();
+        uint16_t *const to_d = (BACK ? p.dcorr : p.corrections) + record * 2 * dvp * kDeltaChunk;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          keep(ok, kColWA + h * 16, to_d + (int64_t)h * 4 * dvp * 8);
+          keep(ok, kColWA + 32 + h * 16, to_d + dvp * kDeltaChunk + (int64_t)h * 4 * dvp * 8);
+        }
+        if constexpr (BACK) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float big[16], rest[16], v[16], beta[16];
+            get16(ok, kColWA + h * 16, big);
+            get16(ok, kColWA + 32 + h * 16, rest);
+            if (h == 1) give(&sh.out_read);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              load_gates(gates + kBeta + h * 32 + q * 16, beta);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 x = unpack_bf16(__float_as_uint(big[q * 8 + e])), y = unpack_bf16(__float_as_uint(rest[q * 8 + e]));
+                v[2 * e] = beta[2 * e] * (x.x + y.x);
+                v[2 * e + 1] = beta[2 * e + 1] * (x.y + y.y);
+              }
+              store_steps(p.dv, p.vector_dv, v, t0 + h * 32 + q * 16);
+            }
+          }
+        } else {
+          give(&sh.out_read);
+        }
+      }
     }
-  };
-  // O of chunk i from its two sums
-  auto store_out = [&](int i) {
-    const bool ok = wait(&sh.out_done, i);
-    tc_fence_after();
-    const float *const gates = reinterpret_cast<const float *>(ring + i % kGateRing * kGateBytes);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = half * 32 + h * 16;
-      float u[16], v[16];
-      get16(ok, kColO + c, u);
-      get16(ok, kColD + c, v);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = fmaf(p.scale * gates[kFirst + c + e], u[e], v[e]);
-      store_steps(p.o, v, chunk_of(i) * kDeltaChunk + c);
-    }
-    give(&sh.out_read);
-  };
+    return;
+  }
+  // ------------------------------- the chain, a thread per row and quarter of the columns --
+  const int group = warp / 4, c0 = group * 16;  // steps [c0, c0 + 16), columns of the state [2 c0, 2 c0 + 32)
   const float *const from = (BACK ? p.dstate : p.h0) ? (BACK ? p.dstate : p.h0) + bh * cells : nullptr;
   for (int i = 0; i < p.chunks; ++i) {
-    const int chunk = chunk_of(i), t0 = chunk * kDeltaChunk;
-    const int64_t record = bh * p.chunks + chunk;
-    const float *const gates = reinterpret_cast<const float *>(ring + i % kGateRing * kGateBytes);
+    const float *const gates = gates_of(i);
     const uint16_t *const values = reinterpret_cast<const uint16_t *>(smem + (i & 1) * kStageBytes + kOffV) + row;
     bool ok = wait(&sh.full[i & 1], i / 2);
-    if (i > 0) ok = wait(&sh.updated, i - 1) && ok;
+    if (i > 0) {
+      ok = wait(&sh.updated, i - 1) && ok;
+      if (!kOut) ok = wait(&sh.state_read, i - 1) && ok;
+    }
     tc_fence_after();
-    if (BACK) {  // dO, as it is, for P^T dO (its place has been read: the state waited for all)
-      uint32_t v[16];
+    float s[2][16];
+    if (i == 0) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int c = half * 32 + 2 * e;
-        v[e] = (uint32_t)values[c * 128] | (uint32_t)values[(c + 1) * 128] << 16;
+      for (int e = 0; e < 32; ++e) {
+        const int k = 2 * c0 + e;
+        s[e / 16][e % 16] = from && there && k < p.dk_size ? from[(int64_t)k * p.dv_size + j] : 0.f;
       }
-      tmem_store16(lanes + kColD + half * 16, v);
+    } else {
+      get(ok, kColS + 2 * c0, s);
+    }
+    if (BACK) {  // dO, as it is, for P^T dO (its place has been read: the state waited for all)
+      uint32_t v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (uint32_t)values[(c0 + 2 * e) * 128] | (uint32_t)values[(c0 + 2 * e + 1) * 128] << 16;
+      tmem_store8(lanes + kColD + group * 8, v);
     }
     const float whole = gates[kFirst + kDeltaChunk - 1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // the state as a left operand, then scaled
-      const int c = half * 64 + h * 32;
-      uint32_t big[16], rest[16];
+    for (int q = 0; q < 2; ++q) {  // the state as a left operand, then scaled
+      store_split16(s[q], lanes + kColSA + c0 + q * 8, lanes + kColSA + 64 + c0 + q * 8);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float s[16];
-        if (i == 0) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int k = c + q * 16 + e;
-            s[e] = from && there && k < p.dk_size ? from[(int64_t)k * p.dv_size + j] : 0.f;
-          }
-        } else {
-          get16(ok, kColS + c + q * 16, s);
-        }
-        split16(s, big, rest, q * 8);
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) mul2(s[e], s[e + 1], s[e], s[e + 1], whole, whole);
-        tmem_store16(lanes + kColS + c + q * 16, s);
-      }
-      tmem_store16(lanes + kColSA + c / 2, big);
-      tmem_store16(lanes + kColSA + 64 + c / 2, rest);
-      if constexpr (!kOut) {
-        if (j < dvp) {
-          uint4 *const to = reinterpret_cast<uint4 *>((BACK ? p.end : p.start) + (record * 2 * dvp + j) * kWidth + c);
-          uint4 *const to_rest = to + dvp * kWidth / 8;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            to[q] = make_uint4(big[4 * q], big[4 * q + 1], big[4 * q + 2], big[4 * q + 3]);
-            to_rest[q] = make_uint4(rest[4 * q], rest[4 * q + 1], rest[4 * q + 2], rest[4 * q + 3]);
-          }
-        }
-      }
+      for (int e = 0; e < 16; e += 2) mul2(s[q][e], s[q][e + 1], s[q][e], s[q][e + 1], whole, whole);
+      tmem_store16(lanes + kColS + 2 * c0 + q * 16, s[q]);
     }
     give(&sh.state_ready);
-    if (kOut && i > 0) store_out(i - 1);
+    float first[16], other[16];
+    load_gates(gates + kFirst + c0, first);
+    load_gates(gates + (BACK ? kLast : kBeta) + c0, other);
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = BF16::to_float(values[(c0 + e) * 128]);
+    if (!kOut && i > 0) ok = wait(&sh.out_read, i - 1) && ok;  // the corrections before have been kept
     ok = wait(&sh.products, i) && ok;
     tc_fence_after();
     {  // R = beta (V - first W), or dD = last W + P^T dO
-      uint32_t big[16], rest[16], scaled[16], scaled_rest[16];
+      float r[16];
+      get16(ok, kColW + c0, r);
+      if constexpr (!BACK) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c = half * 32 + q * 16;
-        float r[16];
-        get16(ok, kColW + c, r);
-        if constexpr (!BACK) {
+        for (int e = 0; e < 16; ++e) r[e] = other[e] * fmaf(-first[e], r[e], v[e]);
+      } else {
+        float u[16];
+        get16(ok, kColO + c0, u);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            r[e] = gates[kBeta + c + e] * (BF16::to_float(values[(c + e) * 128]) - gates[kFirst + c + e] * r[e]);
-        } else {
-          float u[16];
-          get16(ok, kColO + c, u);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = fmaf(gates[kLast + c + e], r[e], u[e]);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = p.scale * gates[kFirst + c + e] * BF16::to_float(values[(c + e) * 128]);
-          split16(u, scaled, scaled_rest, q * 8);
-        }
-        split16(r, big, rest, q * 8);
+        for (int e = 0; e < 16; ++e) r[e] = fmaf(other[e], r[e], u[e]);
       }
-      tmem_store16(lanes + kColWA + half * 16, big);
-      tmem_store16(lanes + kColWA + 32 + half * 16, rest);
+      store_split16(r, lanes + kColWA + group * 8, lanes + kColWA + 32 + group * 8);
       if constexpr (BACK) {
-        // (both halves have read P^T dO: their columns are written over)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] *= p.scale * first[e];
+        // (all groups have read P^T dO: their columns are written over)
         tc_fence_before();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
         tc_fence_after();
-        tmem_store16(lanes + kColO + half * 16, scaled);
-        tmem_store16(lanes + kColO + 32 + half * 16, scaled_rest);
+        store_split16(v, lanes + kColO + group * 8, lanes + kColO + 32 + group * 8);
       }
     }
     give(&sh.right_ready);
+    if (BACK) load_gates(gates + kBeta + c0, other);
+    else load_gates(gates + kLast + c0, other);
     ok = wait(&sh.solved, i) && ok;
     tc_fence_after();
     {
-      uint32_t big[16], rest[16], kept[16], kept_rest[16];
+      float d[16];
+      get16(ok, kColD + c0, d);
+      store_split16(d, lanes + kColWA + group * 8, lanes + kColWA + 32 + group * 8);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int c = half * 32 + q * 16;
-        float d[16];
-        get16(ok, kColD + c, d);
-        split16(d, kept, kept_rest, q * 8);
-        if constexpr (!BACK) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) d[e] *= gates[kLast + c + e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) d[e] *= gates[kBeta + c + e];
-          store_steps(p.dv, d, t0 + c);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) d[e] *= -gates[kFirst + c + e];
-        }
-        split16(d, big, rest, q * 8);
-      }
-      tmem_store16(lanes + kColW + half * 16, big);
-      tmem_store16(lanes + kColW + 32 + half * 16, rest);
-      if constexpr (kOut) {
-        tmem_store16(lanes + kColWA + half * 16, kept);
-        tmem_store16(lanes + kColWA + 32 + half * 16, kept_rest);
-      }
+      for (int e = 0; e < 16; ++e) d[e] *= BACK ? -first[e] * other[e] : other[e];
+      store_split16(d, lanes + kColW + group * 8, lanes + kColW + 32 + group * 8);
       give(&sh.solved_ready);
-      if constexpr (!kOut) {
-        if (j < dvp) {
-          uint4 *const to = reinterpret_cast<uint4 *>((BACK ? p.dcorr : p.corrections) + (record * 2 * dvp + j) * kDeltaChunk + half * 32);
-          uint4 *const to_rest = to + dvp * kDeltaChunk / 8;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            to[q] = make_uint4(kept[4 * q], kept[4 * q + 1], kept[4 * q + 2], kept[4 * q + 3]);
-            to_rest[q] = make_uint4(kept_rest[4 * q], kept_rest[4 * q + 1], kept_rest[4 * q + 2], kept_rest[4 * q + 3]);
-          }
-        }
-      }
     }
     if (lane == 0) arrive(&sh.empty[i & 1]);
   }
-  if (kOut) store_out(p.chunks - 1);
   const bool ok = wait(&sh.updated, p.chunks - 1);
   tc_fence_after();
   float *const to = BACK ? p.dh0 : kOut ? p.state : nullptr;
   if (to != nullptr) {
+    float s[2][16];
+    get(ok, kColS + 2 * c0, s);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = half * 64 + q * 16;
-      float s[16];
-      get16(ok, kColS + c, s);
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (there && c + e < p.dk_size) to[bh * cells + (int64_t)(c + e) * p.dv_size + j] = s[e];
-    }
+    for (int e = 0; e < 32; ++e)
+      if (there && 2 * c0 + e < p.dk_size) to[bh * cells + (int64_t)(2 * c0 + e) * p.dv_size + j] = s[e / 16][e % 16];
   }
 }
 
@@ -442,11 +488,11 @@ __global__ void __launch_bounds__(kTensorThreads, 1) delta_tensor_kernel(const D
   if (threadIdx.x == 0) {
     sh.failed = 0;
     for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&sh.full[s]), 1);
+      mbar_init(smem_u32(&sh.full[s]), kCopyWarps);
       mbar_init(smem_u32(&sh.empty[s]), 1 + kComputeWarps);
     }
-    for (uint64_t *bar : {&sh.state_ready, &sh.right_ready, &sh.solved_ready, &sh.out_read})
-      mbar_init(smem_u32(bar), kComputeWarps);
+    for (uint64_t *bar : {&sh.state_ready, &sh.right_ready, &sh.solved_ready}) mbar_init(smem_u32(bar), kComputeWarps);
+    for (uint64_t *bar : {&sh.state_read, &sh.out_read}) mbar_init(smem_u32(bar), kDrainWarps);
     for (uint64_t *bar : {&sh.products, &sh.solved, &sh.updated, &sh.out_done, &sh.drained}) mbar_init(smem_u32(bar), 1);
     mbar_init_fence();
   }
