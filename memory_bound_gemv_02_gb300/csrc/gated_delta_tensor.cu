@@ -16,14 +16,14 @@
 //
 // The walk is a chain: per chunk three products of 512 + 240 + 512 cycles (two, three,
 // two terms of split operands at 8192 flops a cycle) and between them what the threads do,
-// 128 x 128 + 2 x 128 x 64 values converted: sixteen warps for that alone.  Copies into shared
+// 128 x 128 + 2 x 128 x 64 values converted: eight warps for that alone.  Copies into shared
 // memory, outputs and what the gradient keeps have warps of their own, beside the chain.
 #include "gated_delta_mma.cuh"
 
 namespace gemvk {
 namespace {
 
-constexpr int kGroups = 4, kComputeWarps = 4 * kGroups, kDrainWarps = 4, kCopyWarps = 3;
+constexpr int kGroups = 2, kComputeWarps = 4 * kGroups, kDrainWarps = 4, kCopyWarps = 3;
 constexpr int kFirstCopy = kComputeWarps + kDrainWarps, kIssueWarp = kFirstCopy + kCopyWarps,
               kTensorThreads = 32 * (kIssueWarp + 1);
 constexpr int kRowsPerCta = 128, kWidth = 128;  // columns of v; dk
@@ -280,9 +280,9 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
   auto gates_of = [&](int i) { return reinterpret_cast<const float *>(ring + i % kGateRing * kGateBytes); };
   if (warp >= kComputeWarps) {
     // ---------------------------------------------------- outputs, a thread per row --
-    // 16 steps x this thread's column of an output: lanes trade, so that each has two columns of
-    // every second step
-    auto store_steps = [&](const HeadsOf &to, bool pairs, const float (&v)[16], int t) {
+    // 32 steps (pairs of neighbours) x this thread's column of an output: lanes trade, so that each has
+    // two columns of every second step
+    auto store_steps = [&](const HeadsOf &to, bool pairs, const uint32_t (&v)[16], int t) {
       uint16_t *const rows = static_cast<uint16_t *>(const_cast<void *>(to.p)) + b * to.batch + head * to.head;
       const int odd = lane & 1;
       if (pairs) {
@@ -290,23 +290,21 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
         const int64_t next = 4 * to.step;
         const int left = there ? p.steps - t - odd : 0;
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const uint32_t mine = Elem<GEMV_TYPE_BF16>::pair(v[e], v[e + 1]), other = __shfl_xor_sync(0xffffffffu, mine, 1);
-          const uint32_t both = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-          if (left > e) *reinterpret_cast<uint32_t *>(at) = both;
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, v[e], 1);
+          const uint32_t both = odd ? __byte_perm(other, v[e], 0x7632) : __byte_perm(v[e], other, 0x5410);
+          if (left > 2 * e) *reinterpret_cast<uint32_t *>(at) = both;
           at += next;
         }
       } else if (there) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (t + e < p.steps) rows[(int64_t)(t + e) * to.step + j] = BF16::from_float(v[e]);
+        for (int e = 0; e < 32; ++e)
+          if (t + e < p.steps) rows[(int64_t)(t + e) * to.step + j] = (uint16_t)(v[e / 2] >> (e % 2 * 16));
       }
     };
     // 16 columns of tensor memory (32 of bf16) as they are, for the gradient: units of 8 columns, rows
     // of all of v's columns
-    auto keep = [&](bool ok, uint32_t column, uint16_t *to) {
-      float v[16];
-      get16(ok, column, v);
+    auto keep = [&](const float (&v)[16], uint16_t *to) {
       if (j >= dvp) return;
       uint4 *at = reinterpret_cast<uint4 *>(to) + j;
 #pragma unroll
@@ -323,66 +321,75 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
       if constexpr (kOut) {
         const bool ok = wait(&sh.out_done, i);
         tc_fence_after();
+        uint32_t out[2][16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float u[2][16], v[2][16];
-          get(ok, kColO + h * 32, u);
-          get(ok, kColD + h * 32, v);
-          if (h == 1) give(&sh.out_read);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c = h * 32 + q * 16;
-            float first[16];
-            load_gates(gates + kFirst + c, first);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[q][e] = fmaf(p.scale * first[e], u[q][e], v[q][e]);
-            store_steps(p.o, p.vector_o, v[q], t0 + c);
+        for (int h = 0; h < 4; ++h) {
+          float u[16], v[16], first[16];
+          if (ok) {
+            tmem_request16(lanes + kColO + h * 16, u);
+            tmem_request16(lanes + kColD + h * 16, v);
           }
+          load_gates(gates + kFirst + h * 16, first);
+          if (ok) {
+            tmem_arrived16(u);
+            tmem_arrived16(v);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) u[e] = v[e] = nan;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            out[h / 2][h % 2 * 8 + e / 2] =
+                Elem<GEMV_TYPE_BF16>::pair(fmaf(p.scale * first[e], u[e], v[e]), fmaf(p.scale * first[e + 1], u[e + 1], v[e + 1]));
         }
+        give(&sh.out_read);
+        store_steps(p.o, p.vector_o, out[0], t0);
+        store_steps(p.o, p.vector_o, out[1], t0 + 32);
       } else {
         bool ok = wait(&sh.state_ready, i);
         tc_fence_after();
         uint16_t *const to = (BACK ? p.end : p.start) + record * 2 * dvp * kWidth;
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h)
-          keep(ok, kColSA + h * 16, to + (int64_t)(h / 4) * dvp * kWidth + (int64_t)(h % 4) * 4 * dvp * 8);
-        give(&sh.state_read);
+        for (int h = 0; h < 4; ++h) {
+          float v[2][16];
+          get(ok, kColSA + h * 32, v);
+          if (h == 3) give(&sh.state_read);
+          uint16_t *const at = to + (int64_t)(h / 2) * dvp * kWidth + (int64_t)(h % 2) * 8 * dvp * 8;
+          keep(v[0], at);
+          keep(v[1], at + 4 * dvp * 8);
+        }
         ok = wait(&sh.solved_ready, i) && ok;
         tc_fence_after();
         uint16_t *const to_d = (BACK ? p.dcorr : p.corrections) + record * 2 * dvp * kDeltaChunk;
+        float big[2][16], rest[2][16];
+        get(ok, kColWA, big);
+        get(ok, kColWA + 32, rest);
+        give(&sh.out_read);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          keep(ok, kColWA + h * 16, to_d + (int64_t)h * 4 * dvp * 8);
-          keep(ok, kColWA + 32 + h * 16, to_d + dvp * kDeltaChunk + (int64_t)h * 4 * dvp * 8);
-        }
-        if constexpr (BACK) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float big[16], rest[16], v[16], beta[16];
-            get16(ok, kColWA + h * 16, big);
-            get16(ok, kColWA + 32 + h * 16, rest);
-            if (h == 1) give(&sh.out_read);
+          keep(big[h], to_d + (int64_t)h * 4 * dvp * 8);
+          keep(rest[h], to_d + dvp * kDeltaChunk + (int64_t)h * 4 * dvp * 8);
+          if constexpr (BACK) {
+            uint32_t dv[16];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
+              float beta[16];
               load_gates(gates + kBeta + h * 32 + q * 16, beta);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float2 x = unpack_bf16(__float_as_uint(big[q * 8 + e])), y = unpack_bf16(__float_as_uint(rest[q * 8 + e]));
-                v[2 * e] = beta[2 * e] * (x.x + y.x);
-                v[2 * e + 1] = beta[2 * e + 1] * (x.y + y.y);
+                const float2 x = unpack_bf16(__float_as_uint(big[h][q * 8 + e])), y = unpack_bf16(__float_as_uint(rest[h][q * 8 + e]));
+                dv[q * 8 + e] = Elem<GEMV_TYPE_BF16>::pair(beta[2 * e] * (x.x + y.x), beta[2 * e + 1] * (x.y + y.y));
               }
-              store_steps(p.dv, p.vector_dv, v, t0 + h * 32 + q * 16);
             }
+            store_steps(p.dv, p.vector_dv, dv, t0 + h * 32);
           }
-        } else {
-          give(&sh.out_read);
         }
       }
     }
     return;
   }
-  // ------------------------------- the chain, a thread per row and quarter of the columns --
-  const int group = warp / 4, c0 = group * 16;  // steps [c0, c0 + 16), columns of the state [2 c0, 2 c0 + 32)
+  // ---------------------------------- the chain, a thread per row and half of the columns --
+  const int group = warp / 4, c0 = group * 32;  // steps [c0, c0 + 32), columns of the state [2 c0, 2 c0 + 64)
   const float *const from = (BACK ? p.dstate : p.h0) ? (BACK ? p.dstate : p.h0) + bh * cells : nullptr;
   for (int i = 0; i < p.chunks; ++i) {
     const float *const gates = gates_of(i);
@@ -393,88 +400,111 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
       if (!kOut) ok = wait(&sh.state_read, i - 1) && ok;
     }
     tc_fence_after();
-    float s[2][16];
-    if (i == 0) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const int k = 2 * c0 + e;
-        s[e / 16][e % 16] = from && there && k < p.dk_size ? from[(int64_t)k * p.dv_size + j] : 0.f;
-      }
-    } else {
-      get(ok, kColS + 2 * c0, s);
-    }
-    if (BACK) {  // dO, as it is, for P^T dO (its place has been read: the state waited for all)
-      uint32_t v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (uint32_t)values[(c0 + 2 * e) * 128] | (uint32_t)values[(c0 + 2 * e + 1) * 128] << 16;
-      tmem_store8(lanes + kColD + group * 8, v);
-    }
     const float whole = gates[kFirst + kDeltaChunk - 1];
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {  // the state as a left operand, then scaled
-      store_split16(s[q], lanes + kColSA + c0 + q * 8, lanes + kColSA + 64 + c0 + q * 8);
+    for (int h = 0; h < 2; ++h) {  // the state as a left operand, then scaled
+      const int c = c0 + h * 16;
+      float s[2][16];
+      if (i == 0) {
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) mul2(s[q][e], s[q][e + 1], s[q][e], s[q][e + 1], whole, whole);
-      tmem_store16(lanes + kColS + 2 * c0 + q * 16, s[q]);
+        for (int e = 0; e < 32; ++e) {
+          const int k = 2 * c + e;
+          s[e / 16][e % 16] = from && there && k < p.dk_size ? from[(int64_t)k * p.dv_size + j] : 0.f;
+        }
+      } else {
+        get(ok, kColS + 2 * c, s);
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        store_split16(s[q], lanes + kColSA + c + q * 8, lanes + kColSA + 64 + c + q * 8);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) mul2(s[q][e], s[q][e + 1], s[q][e], s[q][e + 1], whole, whole);
+        tmem_store16(lanes + kColS + 2 * c + q * 16, s[q]);
+      }
+    }
+    if (BACK) {  // dO, as it is, for P^T dO (its place has been read: the state waited for all)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = c0 + q * 16 + 2 * e;
+          v[e] = (uint32_t)values[c * 128] | (uint32_t)values[(c + 1) * 128] << 16;
+        }
+        tmem_store8(lanes + kColD + c0 / 2 + q * 8, v);
+      }
     }
     give(&sh.state_ready);
-    float first[16], other[16];
-    load_gates(gates + kFirst + c0, first);
-    load_gates(gates + (BACK ? kLast : kBeta) + c0, other);
-    float v[16];
+    float v[2][16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = BF16::to_float(values[(c0 + e) * 128]);
+    for (int e = 0; e < 32; ++e) v[e / 16][e % 16] = BF16::to_float(values[(c0 + e) * 128]);
     if (!kOut && i > 0) ok = wait(&sh.out_read, i - 1) && ok;  // the corrections before have been kept
     ok = wait(&sh.products, i) && ok;
     tc_fence_after();
-    {  // R = beta (V - first W), or dD = last W + P^T dO
-      float r[16];
-      get16(ok, kColW + c0, r);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {  // R = beta (V - first W), or dD = last W + P^T dO
+      const int c = c0 + q * 16;
+      float r[16], first[16], other[16];
+      get16(ok, kColW + c, r);
+      load_gates(gates + (BACK ? kLast : kBeta) + c, other);
       if constexpr (!BACK) {
+        load_gates(gates + kFirst + c, first);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = other[e] * fmaf(-first[e], r[e], v[e]);
+        for (int e = 0; e < 16; ++e) r[e] = other[e] * fmaf(-first[e], r[e], v[q][e]);
       } else {
-        float u[16];
-        get16(ok, kColO + c0, u);
+        get16(ok, kColO + c, first);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) r[e] = fmaf(other[e], r[e], u[e]);
+        for (int e = 0; e < 16; ++e) r[e] = fmaf(other[e], r[e], first[e]);
       }
-      store_split16(r, lanes + kColWA + group * 8, lanes + kColWA + 32 + group * 8);
-      if constexpr (BACK) {
+      store_split16(r, lanes + kColWA + c / 2, lanes + kColWA + 32 + c / 2);
+    }
+    if constexpr (BACK) {
+      // (both groups have read P^T dO: their columns are written over)
+      tc_fence_before();
+      asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
+      tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] *= p.scale * first[e];
-        // (all groups have read P^T dO: their columns are written over)
-        tc_fence_before();
-        asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
-        tc_fence_after();
-        store_split16(v, lanes + kColO + group * 8, lanes + kColO + 32 + group * 8);
+      for (int q = 0; q < 2; ++q) {
+        const int c = c0 + q * 16;
+        float first[16];
+        load_gates(gates + kFirst + c, first);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[q][e] *= p.scale * first[e];
+        store_split16(v[q], lanes + kColO + c / 2, lanes + kColO + 32 + c / 2);
       }
     }
     give(&sh.right_ready);
-    if (BACK) load_gates(gates + kBeta + c0, other);
-    else load_gates(gates + kLast + c0, other);
     ok = wait(&sh.solved, i) && ok;
     tc_fence_after();
-    {
-      float d[16];
-      get16(ok, kColD + c0, d);
-      store_split16(d, lanes + kColWA + group * 8, lanes + kColWA + 32 + group * 8);
+    float d[2][16];
+    get(ok, kColD + c0, d);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) d[e] *= BACK ? -first[e] * other[e] : other[e];
-      store_split16(d, lanes + kColW + group * 8, lanes + kColW + 32 + group * 8);
-      give(&sh.solved_ready);
+    for (int q = 0; q < 2; ++q) {  // D, and what the state gains of it: last D, or -beta first dR
+      const int c = c0 + q * 16;
+      float f[16], g[16];
+      load_gates(gates + (BACK ? kBeta : kLast) + c, f);
+      if (BACK) load_gates(gates + kFirst + c, g);
+      store_split16(d[q], lanes + kColWA + c / 2, lanes + kColWA + 32 + c / 2);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) d[q][e] *= BACK ? -g[e] * f[e] : f[e];
+      store_split16(d[q], lanes + kColW + c / 2, lanes + kColW + 32 + c / 2);
     }
+    give(&sh.solved_ready);
     if (lane == 0) arrive(&sh.empty[i & 1]);
   }
   const bool ok = wait(&sh.updated, p.chunks - 1);
   tc_fence_after();
   float *const to = BACK ? p.dh0 : kOut ? p.state : nullptr;
   if (to != nullptr) {
-    float s[2][16];
-    get(ok, kColS + 2 * c0, s);
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (there && 2 * c0 + e < p.dk_size) to[bh * cells + (int64_t)(2 * c0 + e) * p.dv_size + j] = s[e / 16][e % 16];
+    for (int h = 0; h < 2; ++h) {
+      const int c = 2 * c0 + h * 32;
+      float s[2][16];
+      get(ok, kColS + c, s);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (there && c + e < p.dk_size) to[bh * cells + (int64_t)(c + e) * p.dv_size + j] = s[e / 16][e % 16];
+    }
   }
 }
 
