@@ -316,6 +316,10 @@ HeadsOf heads_of(const gemv_heads *h) { return {h->p, h->batch, h->step, h->head
 
 int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+// Whether the heads that share q and k are a cluster of CTAs, whose gradients of those are
+// summed without leaving the SMs.
+bool sums_in_clusters(const gated_delta_shape &s) { return s.heads == s.heads_k || (s.heads / s.heads_k <= 8 && s.dk <= 128); }
+
 struct Layout {
   int64_t records, start, end, corrections, dcorr, dq32, dk32, pack[4], bytes;
 };
@@ -337,7 +341,7 @@ Layout layout_of(const gated_delta_shape &s, bool backward, const gemv_heads *co
     l.end = take(n * 2 * dvp * dkp * 2);
     l.corrections = take(n * 2 * dvp * kDeltaChunk * 2);
     l.dcorr = take(n * 2 * dvp * kDeltaChunk * 2);
-    if (s.heads != s.heads_k) {
+    if (!sums_in_clusters(s)) {
       l.dq32 = take(s.batch * s.steps * s.heads * s.dk * 4);
       l.dk32 = take(s.batch * s.steps * s.heads * s.dk * 4);
     }
@@ -558,8 +562,8 @@ extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_h
   p.end = reinterpret_cast<uint16_t *>(ws + l.end);
   p.corrections = reinterpret_cast<uint16_t *>(ws + l.corrections);
   p.dcorr = reinterpret_cast<uint16_t *>(ws + l.dcorr);
-  p.dq32 = s.heads != s.heads_k ? reinterpret_cast<float *>(ws + l.dq32) : nullptr;
-  p.dk32 = s.heads != s.heads_k ? reinterpret_cast<float *>(ws + l.dk32) : nullptr;
+  p.dq32 = !sums_in_clusters(s) ? reinterpret_cast<float *>(ws + l.dq32) : nullptr;
+  p.dk32 = !sums_in_clusters(s) ? reinterpret_cast<float *>(ws + l.dk32) : nullptr;
   p.vector_dv = on_units(*dv, s.dv) ? 1 : 0;
   return launch_delta_gradient(p, padded_dk(s.dk), sms, stream);
 }

@@ -29,18 +29,24 @@ constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
 
 template <int DK>
 struct Grad {
-  static constexpr int kParts = DK / 64, kThreads = 128 * kParts, kSlice = DK == 256 ? 32 : 64;
+  static constexpr int kParts = DK / 64, kThreads = 128 * kParts, kSlice = 32;
   static constexpr int kWide = DK + 8, kNarrow = kSlice + 8;  // row pitches
   static constexpr int kTile = kDeltaChunk * kWide * 2, kStates = kSlice * kWide * 2, kSteps = kSlice * kTilePitch * 2,
                        kValues = kDeltaChunk * kNarrow * 2;
   static constexpr int kK = 0, kQ = kTile, kStage = 2 * kTile;
-  // a slice of v's columns
-  static constexpr int kS = kStage, kR = kS + 2 * kStates, kDo = kR + 2 * kSteps, kV = kDo + kValues, kE = kV + kValues,
-                       kD = kE + 2 * kStates, kStageEnd = kD + 2 * kSteps;
+  // a slice of v's columns, two of them in flight where they fit
+  static constexpr int kS = 0, kR = kS + 2 * kStates, kDo = kR + 2 * kSteps, kV = kDo + kValues, kE = kV + kValues,
+                       kD = kE + 2 * kStates, kSliceBytes = kD + 2 * kSteps;
+  static constexpr int kSlices = DK == 256 ? 1 : 2, kStageEnd = kStage + kSlices * kSliceBytes;
   // afterwards in the same place: dP, M, beta M as two bf16 each, and the terms of dg
   static constexpr int kDp = kStage, kM = kDp + 2 * kPairBytes, kBm = kM + 2 * kPairBytes, kW = kBm + 2 * kPairBytes,
                        kWPitch = kDeltaChunk + 1, kAfter = kW + kDeltaChunk * kWPitch * 4;
-  static constexpr int kGates = kStageEnd > kAfter ? kStageEnd : kAfter, kRows = kGates + kGateFloats * 4,
+  // and after that: dQ and dK of one head, fp32, for the cluster
+  static constexpr int kSumPitch = DK + 4, kDq = kStage, kDk = kDq + kDeltaChunk * kSumPitch * 4,
+                       kSumsEnd = kDk + kDeltaChunk * kSumPitch * 4;
+  static constexpr bool kClustered = DK <= 128;  // (of 256, more than a CTA's memory)
+  static constexpr int kPlain = kStageEnd > kAfter ? kStageEnd : kAfter,
+                       kGates = kClustered && kSumsEnd > kPlain ? kSumsEnd : kPlain, kRows = kGates + kGateFloats * 4,
                        kSums = kRows + 4 * kParts * kDeltaChunk * 4, kBytes = kSums + (kThreads + 32) * 4;
 };
 
@@ -97,6 +103,22 @@ __device__ __forceinline__ void store_rows(const FragC (&c)[8], const HeadsOf &t
   }
 }
 
+// 16 x 64 sums, in rows of `pitch` floats.
+__device__ __forceinline__ void put_rows(const FragC (&c)[8], float *to, int pitch, int row, int col) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = 0; n < 8; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2 *>(to + (row + lane / 4 + 8 * h) * pitch + col + n * 8 + lane % 4 * 2) =
+          make_float2(c[n][2 * h], c[n][2 * h + 1]);
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 template <bool F16, int DK>
 __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(const DeltaParams p) {
   typedef Grad<DK> L;
@@ -104,8 +126,10 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
   extern __shared__ __align__(16) char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = warp % 4 * 16, part = warp / 4, col = part * 64, mcol = part * NT * 8;
-  const int chunk = blockIdx.x, t0 = chunk * kDeltaChunk;
-  const int64_t b = blockIdx.z, head = blockIdx.y, head_k = head / (p.heads / p.heads_k);
+  // (heads along x: those that share q and k are a cluster)
+  const int64_t token = blockIdx.x / p.heads, head = blockIdx.x % p.heads, head_k = head / (p.heads / p.heads_k);
+  const int64_t b = token / p.chunks;
+  const int chunk = (int)(token % p.chunks), t0 = chunk * kDeltaChunk;
   const int64_t at = (b * p.heads + head) * p.chunks + chunk;
   const int slices64 = (p.dv_size + kDeltaSlice - 1) / kDeltaSlice;
   const int64_t dvp = (int64_t)slices64 * kDeltaSlice;
@@ -120,89 +144,83 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
     copy16(base + L::kGates + tid * 16, p.records + at * kRecordBytes + kRecordHalfs * 2 + tid * 16, true);
   FragC dq[8] = {}, x[8] = {}, y[8] = {}, dp[NT] = {}, mm[NT] = {};
   float whole = 0.f, vr = 0.f;
+  const uint16_t *const s0 = p.start + at * 2 * dvp * DK, *const s1 = p.end + at * 2 * dvp * DK;
+  const uint16_t *const c0 = p.corrections + at * 2 * dvp * kDeltaChunk, *const c1 = p.dcorr + at * 2 * dvp * kDeltaChunk;
+  auto request = [&](int col_v) {
+    if (col_v < p.dv_size) {
+      const uint32_t to = base + L::kStage + col_v / L::kSlice % L::kSlices * L::kSliceBytes;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        copy_kept<L::kSlice, DK, L::kThreads>(to + L::kS + h * L::kStates, s0 + h * dvp * DK + col_v * 8, dvp);
+        copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(to + L::kR + h * L::kSteps, c1 + h * dvp * kDeltaChunk + col_v * 8, dvp);
+        copy_kept<L::kSlice, DK, L::kThreads>(to + L::kE + h * L::kStates, s1 + h * dvp * DK + col_v * 8, dvp);
+        copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(to + L::kD + h * L::kSteps, c0 + h * dvp * kDeltaChunk + col_v * 8, dvp);
+      }
+      copy_tile<L::kSlice, L::kThreads>(to + L::kDo, p.td, b, head, t0, p.steps, col_v);
+      copy_tile<L::kSlice, L::kThreads>(to + L::kV, p.tv, b, head, t0, p.steps, col_v);
+    }
+    copies_close();
+  };
+  request(0);
   for (int col_v = 0; col_v < p.dv_size; col_v += L::kSlice) {
-    if (col_v > 0) __syncthreads();
-    const uint16_t *const s0 = p.start + at * 2 * dvp * DK + col_v * 8, *const s1 = p.end + at * 2 * dvp * DK + col_v * 8;
-    const uint16_t *const c0 = p.corrections + at * 2 * dvp * kDeltaChunk + col_v * 8,
-                         *const c1 = p.dcorr + at * 2 * dvp * kDeltaChunk + col_v * 8;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      copy_kept<L::kSlice, DK, L::kThreads>(base + L::kS + h * L::kStates, s0 + h * dvp * DK, dvp);
-      copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kR + h * L::kSteps, c1 + h * dvp * kDeltaChunk, dvp);
-    }
-    copy_tile<L::kSlice, L::kThreads>(base + L::kDo, p.td, b, head, t0, p.steps, col_v);
-    copy_tile<L::kSlice, L::kThreads>(base + L::kV, p.tv, b, head, t0, p.steps, col_v);
-    copies_close();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      copy_kept<L::kSlice, DK, L::kThreads>(base + L::kE + h * L::kStates, s1 + h * dvp * DK, dvp);
-      copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(base + L::kD + h * L::kSteps, c0 + h * dvp * kDeltaChunk, dvp);
-    }
-    copies_close();
-    copies_wait<1>();
+    if (L::kSlices == 2) request(col_v + L::kSlice);
+    copies_wait<L::kSlices - 1>();
     __syncthreads();
-#pragma unroll
-    for (int s = 0; s < L::kSlice / 16; ++s) {
-      FragA o, r, rr;
-      load_matrices(o, at_kn(base + L::kDo, L::kNarrow, row, s * 16, lane));
-      load_matrices_t(r, at_km(base + L::kR, kTilePitch, s * 16, row, lane));
-      load_matrices_t(rr, at_km(base + L::kR + L::kSteps, kTilePitch, s * 16, row, lane));
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t h[4], l[4];
-        load_matrices_t(h, at_kn(base + L::kS, L::kWide, s * 16, col + n * 16, lane));
-        load_matrices_t(l, at_kn(base + L::kS + L::kStates, L::kWide, s * 16, col + n * 16, lane));
-        mma_input_split<F16>(dq[2 * n], dq[2 * n + 1], o, h, l);
-        mma_split_split(x[2 * n], x[2 * n + 1], r, rr, h, l);
-      }
-    }
-    {  // dR . V: step tid % 64, every (threads / 64)th column
-      const int c = tid % 64;
-      const uint16_t *const r = reinterpret_cast<const uint16_t *>(smem + L::kR) + c;
-      const uint16_t *const v = reinterpret_cast<const uint16_t *>(smem + L::kV) + c * L::kNarrow;
-      for (int j = tid / 64; j < L::kSlice; j += L::kThreads / 64) {
-        const float f = BF16::to_float(r[j * kTilePitch]) + BF16::to_float(r[j * kTilePitch + L::kSteps / 2]);
-        vr = fmaf(f, F16 ? Elem<GEMV_TYPE_F16>::get(v[j]) : Elem<GEMV_TYPE_BF16>::get(v[j]), vr);
-      }
-    }
-    copies_wait<0>();
-    __syncthreads();
+    char *const slice = smem + L::kStage + col_v / L::kSlice % L::kSlices * L::kSliceBytes;
+    const uint32_t from = smem_u32(slice);
 #pragma unroll
     for (int s = 0; s < L::kSlice / 16; ++s) {
       FragA o, r, rr, d, dd;
-      load_matrices(o, at_kn(base + L::kDo, L::kNarrow, row, s * 16, lane));
-      load_matrices_t(r, at_km(base + L::kR, kTilePitch, s * 16, row, lane));
-      load_matrices_t(rr, at_km(base + L::kR + L::kSteps, kTilePitch, s * 16, row, lane));
-      load_matrices_t(d, at_km(base + L::kD, kTilePitch, s * 16, row, lane));
-      load_matrices_t(dd, at_km(base + L::kD + L::kSteps, kTilePitch, s * 16, row, lane));
+      load_matrices(o, at_kn(from + L::kDo, L::kNarrow, row, s * 16, lane));
+      load_matrices_t(r, at_km(from + L::kR, kTilePitch, s * 16, row, lane));
+      load_matrices_t(rr, at_km(from + L::kR + L::kSteps, kTilePitch, s * 16, row, lane));
+      load_matrices_t(d, at_km(from + L::kD, kTilePitch, s * 16, row, lane));
+      load_matrices_t(dd, at_km(from + L::kD + L::kSteps, kTilePitch, s * 16, row, lane));
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        uint32_t h[4], l[4];
-        load_matrices_t(h, at_kn(base + L::kE, L::kWide, s * 16, col + n * 16, lane));
-        load_matrices_t(l, at_kn(base + L::kE + L::kStates, L::kWide, s * 16, col + n * 16, lane));
-        mma_split_split(y[2 * n], y[2 * n + 1], d, dd, h, l);
+        uint32_t h[4], l[4], eh[4], el[4];
+        load_matrices_t(h, at_kn(from + L::kS, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(l, at_kn(from + L::kS + L::kStates, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(eh, at_kn(from + L::kE, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(el, at_kn(from + L::kE + L::kStates, L::kWide, s * 16, col + n * 16, lane));
+        mma_input_split<F16>(dq[2 * n], dq[2 * n + 1], o, h, l);
+        mma_split_split(x[2 * n], x[2 * n + 1], r, rr, h, l);
+        mma_split_split(y[2 * n], y[2 * n + 1], d, dd, eh, el);
       }
 #pragma unroll
       for (int n = 0; n < NT / 2; ++n) {
         if (mcol + n * 16 > row) continue;
         uint32_t h[4], l[4];
-        load_matrices_t(h, at_kn(base + L::kD, kTilePitch, s * 16, mcol + n * 16, lane));
-        load_matrices_t(l, at_kn(base + L::kD + L::kSteps, kTilePitch, s * 16, mcol + n * 16, lane));
+        load_matrices_t(h, at_kn(from + L::kD, kTilePitch, s * 16, mcol + n * 16, lane));
+        load_matrices_t(l, at_kn(from + L::kD + L::kSteps, kTilePitch, s * 16, mcol + n * 16, lane));
         mma_input_split<F16>(dp[2 * n], dp[2 * n + 1], o, h, l);
         mma_split_split(mm[2 * n], mm[2 * n + 1], r, rr, h, l);
       }
     }
+    {  // dR . V: step tid % 64, every (threads / 64)th column
+      const int c = tid % 64;
+      const uint16_t *const r = reinterpret_cast<const uint16_t *>(slice + L::kR) + c;
+      const uint16_t *const v = reinterpret_cast<const uint16_t *>(slice + L::kV) + c * L::kNarrow;
+#pragma unroll 4
+      for (int j = tid / 64; j < L::kSlice; j += L::kThreads / 64) {
+        const float f = BF16::to_float(r[j * kTilePitch]) + BF16::to_float(r[j * kTilePitch + L::kSteps / 2]);
+        vr = fmaf(f, F16 ? Elem<GEMV_TYPE_F16>::get(v[j]) : Elem<GEMV_TYPE_BF16>::get(v[j]), vr);
+      }
+    }
     // <S, dS'>: pairs of the slice
+#pragma unroll 4
     for (int i = tid; i < L::kSlice * DK / 2; i += L::kThreads) {
       const int at2 = (i / (DK / 2)) * L::kWide * 2 + i % (DK / 2) * 4;
       auto both = [&](int area) {
-        const float2 h = unpack_bf16(*reinterpret_cast<const uint32_t *>(smem + area + at2));
-        const float2 l = unpack_bf16(*reinterpret_cast<const uint32_t *>(smem + area + L::kStates + at2));
+        const float2 h = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + at2));
+        const float2 l = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + L::kStates + at2));
         return make_float2(h.x + l.x, h.y + l.y);
       };
       const float2 u = both(L::kS), w = both(L::kE);
       whole = fmaf(u.x, w.x, fmaf(u.y, w.y, whole));
     }
+    __syncthreads();
+    if (L::kSlices == 1) request(col_v + L::kSlice);
   }
   // the terms with S and dS', scaled, and what they are along the rows of q and k
   {
@@ -246,8 +264,7 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       mma_inputs<F16>(kk[2 * n + 1], ak, bk[2], bk[3]);
     }
   }
-  __syncthreads();  // the slices are done with
-  sums[tid] = vr;
+  sums[tid] = vr;  // (the slices are done with)
   float *const W = reinterpret_cast<float *>(smem + L::kW);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -326,9 +343,12 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[n][e] = fmaf(e < 2 ? b0 : b1, x[n][e], y[n][e]);
   }
-  const int64_t out_head = p.dq32 ? head : head_k;
-  store_rows<F16>(dq, p.dq, p.dq32, p, b, out_head, t0, row, col);
-  store_rows<F16>(y, p.dk, p.dk32, p, b, out_head, t0, row, col);
+  const bool shared = p.heads != p.heads_k, clustered = L::kClustered && shared && p.dq32 == nullptr;
+  if (!clustered) {
+    const int64_t out_head = shared ? head : head_k;
+    store_rows<F16>(dq, p.dq, p.dq32, p, b, out_head, t0, row, col);
+    store_rows<F16>(y, p.dk, p.dk32, p, b, out_head, t0, row, col);
+  }
   // the gates' gradients
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, m);
@@ -364,6 +384,41 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
     const float dg = starts ? 0.f : inner + ahead + before + gates[kFirst + kDeltaChunk - 1] * all;
     put_gate(p.dg, p.gates_f32, F16, b, t0 + tid, head, dg);
   }
+  if constexpr (L::kClustered) {
+    if (clustered) {  // a CTA per head that shares q and k: each sums its part of the rows, in the heads' order
+      __syncthreads();
+      put_rows(dq, reinterpret_cast<float *>(smem + L::kDq), L::kSumPitch, row, col);
+      put_rows(y, reinterpret_cast<float *>(smem + L::kDk), L::kSumPitch, row, col);
+      cluster_sync();
+      typedef Elem<F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16> E;
+      const int group = p.heads / p.heads_k, rank = (int)cluster_rank();
+      const int first = kDeltaChunk * rank / group, last = kDeltaChunk * (rank + 1) / group;
+      for (int i = tid; i < (last - first) * (DK / 2); i += L::kThreads) {
+        const int r = first + i / (DK / 2), j = i % (DK / 2) * 2;
+        if (t0 + r >= p.steps || j >= p.dk_size) continue;
+        float q0 = 0.f, q1 = 0.f, k0 = 0.f, k1 = 0.f;
+        for (int m = 0; m < group; ++m) {
+          const uint32_t from = cluster_address(base + L::kDq + (uint32_t)(r * L::kSumPitch + j) * 4, (uint32_t)m);
+          const float2 u = ld_cluster2(from), v = ld_cluster2(from + L::kDk - L::kDq);
+          q0 += u.x;
+          q1 += u.y;
+          k0 += v.x;
+          k1 += v.y;
+        }
+        const int64_t q_at = b * p.dq.batch + (int64_t)(t0 + r) * p.dq.step + head_k * p.dq.head + j,
+                      k_at = b * p.dk.batch + (int64_t)(t0 + r) * p.dk.step + head_k * p.dk.head + j;
+        uint16_t *const to_q = static_cast<uint16_t *>(const_cast<void *>(p.dq.p)) + q_at,
+                 *const to_k = static_cast<uint16_t *>(const_cast<void *>(p.dk.p)) + k_at;
+        to_q[0] = E::put(q0);
+        to_k[0] = E::put(k0);
+        if (j + 1 < p.dk_size) {
+          to_q[1] = E::put(q1);
+          to_k[1] = E::put(k1);
+        }
+      }
+      cluster_sync();  // its memory is read until then
+    }
+  }
 }
 
 // Gradients of shared heads: fp32 per head of v, summed in order.
@@ -396,7 +451,8 @@ int launch_gradient(const DeltaParams &p, cudaStream_t stream) {
     cudaGetLastError();
     return cuda_failure((int)e);
   }
-  return launch_op(fn, dim3((unsigned)p.chunks, (unsigned)p.heads, (unsigned)p.batch), L::kThreads, L::kBytes, 1, stream, p);
+  const int cluster = p.dq32 == nullptr ? p.heads / p.heads_k : 1;
+  return launch_op(fn, dim3((unsigned)((int64_t)p.chunks * p.heads * p.batch)), L::kThreads, L::kBytes, cluster, stream, p);
 }
 
 template <bool F16>

@@ -39,7 +39,7 @@ struct TensorShared {
   uint64_t full[2], empty[2];
   uint64_t state_ready, right_ready, solved_ready;               // from the computing threads
   uint64_t products, solved, updated, out_done, drained;         // from the tensor cores
-  uint64_t state_read, out_read;                                 // from the draining threads
+  uint64_t out_read;                                             // from the draining threads
   uint32_t tmem;
   int failed;
 };
@@ -346,19 +346,7 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
         store_steps(p.o, p.vector_o, out[0], t0);
         store_steps(p.o, p.vector_o, out[1], t0 + 32);
       } else {
-        bool ok = wait(&sh.state_ready, i);
-        tc_fence_after();
-        uint16_t *const to = (BACK ? p.end : p.start) + record * 2 * dvp * kWidth;
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          float v[2][16];
-          get(ok, kColSA + h * 32, v);
-          if (h == 3) give(&sh.state_read);
-          uint16_t *const at = to + (int64_t)(h / 2) * dvp * kWidth + (int64_t)(h % 2) * 8 * dvp * 8;
-          keep(v[0], at);
-          keep(v[1], at + 4 * dvp * 8);
-        }
-        ok = wait(&sh.solved_ready, i) && ok;
+        const bool ok = wait(&sh.solved_ready, i);
         tc_fence_after();
         uint16_t *const to_d = (BACK ? p.dcorr : p.corrections) + record * 2 * dvp * kDeltaChunk;
         float big[2][16], rest[2][16];
@@ -393,12 +381,10 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
   const float *const from = (BACK ? p.dstate : p.h0) ? (BACK ? p.dstate : p.h0) + bh * cells : nullptr;
   for (int i = 0; i < p.chunks; ++i) {
     const float *const gates = gates_of(i);
+    const int64_t record = bh * p.chunks + chunk_of(i);
     const uint16_t *const values = reinterpret_cast<const uint16_t *>(smem + (i & 1) * kStageBytes + kOffV) + row;
     bool ok = wait(&sh.full[i & 1], i / 2);
-    if (i > 0) {
-      ok = wait(&sh.updated, i - 1) && ok;
-      if (!kOut) ok = wait(&sh.state_read, i - 1) && ok;
-    }
+    if (i > 0) ok = wait(&sh.updated, i - 1) && ok;
     tc_fence_after();
     const float whole = gates[kFirst + kDeltaChunk - 1];
 #pragma unroll
@@ -416,10 +402,24 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
       }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        store_split16(s[q], lanes + kColSA + c + q * 8, lanes + kColSA + 64 + c + q * 8);
+        uint32_t big[8], rest[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) split(s[q][2 * e], s[q][2 * e + 1], big[e], rest[e]);
+        tmem_store8(lanes + kColSA + c + q * 8, big);
+        tmem_store8(lanes + kColSA + 64 + c + q * 8, rest);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) mul2(s[q][e], s[q][e + 1], s[q][e], s[q][e + 1], whole, whole);
         tmem_store16(lanes + kColS + 2 * c + q * 16, s[q]);
+        if constexpr (!kOut) {  // kept for the gradient: units of 8 columns, rows of all of v's columns
+          if (j < dvp) {
+            uint4 *const at = reinterpret_cast<uint4 *>((BACK ? p.end : p.start) + record * 2 * dvp * kWidth) +
+                              (int64_t)(c / 4 + q * 2) * dvp + j;
+            at[0] = make_uint4(big[0], big[1], big[2], big[3]);
+            at[dvp] = make_uint4(big[4], big[5], big[6], big[7]);
+            at[dvp * kWidth / 8] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            at[dvp * kWidth / 8 + dvp] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
+          }
+        }
       }
     }
     if (BACK) {  // dO, as it is, for P^T dO (its place has been read: the state waited for all)
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kTensorThreads, 1) delta_tensor_kernel(const D
       mbar_init(smem_u32(&sh.empty[s]), 1 + kComputeWarps);
     }
     for (uint64_t *bar : {&sh.state_ready, &sh.right_ready, &sh.solved_ready}) mbar_init(smem_u32(bar), kComputeWarps);
-    for (uint64_t *bar : {&sh.state_read, &sh.out_read}) mbar_init(smem_u32(bar), kDrainWarps);
+    mbar_init(smem_u32(&sh.out_read), kDrainWarps);
     for (uint64_t *bar : {&sh.products, &sh.solved, &sh.updated, &sh.out_done, &sh.drained}) mbar_init(smem_u32(bar), 1);
     mbar_init_fence();
   }

@@ -90,6 +90,13 @@ def test_many_heads(cuda_dev, size, dtype, gates):
     check_forward(x, None, o, state, "from zero")
 
 
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 9, 16])
+@pytest.mark.parametrize("dk", [40, 128, 200])
+def test_gradients_of_shared_heads(cuda_dev, group, dk):
+    x, h0, do, dstate = make(cuda_dev, 1, 100, 2, 2 * group, dk, 32, BF16)
+    check_backward(x, h0, do, dstate, run_back(x, do, h0, dstate))
+
+
 @pytest.mark.parametrize("steps,resets", [(40, (0, 1, 39)), (200, (0,)), (200, (63, 64, 65)), (200, (128, 199)),
                                           (130, tuple(range(130))), (300, (17, 100, 101, 256))])
 def test_new_documents(cuda_dev, steps, resets):
