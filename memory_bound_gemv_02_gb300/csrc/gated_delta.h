@@ -46,8 +46,8 @@ struct DeltaParams {
   HeadsOf o, dq, dk, dv, dg, dbeta;  // outputs
   float *state, *dh0;
   char *records;                   // (batch, heads, chunks) of kRecordBytes
-  // gradient: states before a chunk and gradients behind it, (.., 2, DK / 8, dvp, 8) bf16, and its
-  // corrections and their gradients, (.., 2, 8, dvp, 8)
+  // gradient: states before a chunk and gradients behind it, (.., 2, dvp / 32, DK / 8, 32, 8) bf16, and its
+  // corrections and their gradients, (.., 2, dvp / 32, 8, 32, 8)
   uint16_t *start, *end, *corrections, *dcorr;
   float *dq32, *dk32;              // gradients per head of v where heads of k are shared
   float scale;
@@ -56,6 +56,13 @@ struct DeltaParams {
   int32_t polls;       // of the tensor walk's waits
   uint32_t *timeouts;
 };
+
+// Where the gradient finds unit u (8 columns, 16 bytes) of row j among `units` of them: 32 rows of
+// all columns lie side by side.
+constexpr int kKeptRows = 32;
+__host__ __device__ inline int64_t kept_unit(int64_t j, int64_t u, int64_t units) {
+  return (j / kKeptRows * units + u) * kKeptRows + j % kKeptRows;
+}
 
 // Copies of operands whose rows are not on 16 bytes, padded to 16.
 struct PackParams {

@@ -368,10 +368,10 @@ __device__ __forceinline__ void store_block16(const FragC &c0, const FragC &c1, 
   }
 }
 
-// Sums of 16 rows, kept for the gradient as bf16 and the rest `plane` behind: tiles of 8 columns
-// are `rows` rows of 16 bytes each.
+// Sums of 16 rows (from the plane's row `row`, column 8 `unit` of 8 `units`), kept for the
+// gradient as bf16 and the rest `plane` behind.
 template <int N>
-__device__ __forceinline__ void keep_split(const FragC *c, uint16_t *to, int64_t rows, int64_t plane) {
+__device__ __forceinline__ void keep_split(const FragC *c, uint16_t *to, int row, int unit, int units, int64_t plane) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int n = 0; n < N; ++n)
@@ -379,7 +379,7 @@ __device__ __forceinline__ void keep_split(const FragC *c, uint16_t *to, int64_t
     for (int h = 0; h < 2; ++h) {
       uint32_t big, rest;
       split(c[n][2 * h], c[n][2 * h + 1], big, rest);
-      uint16_t *const at = to + (n * rows + lane / 4 + 8 * h) * 8 + lane % 4 * 2;
+      uint16_t *const at = to + kept_unit(row + lane / 4 + 8 * h, unit + n, units) * 8 + lane % 4 * 2;
       *reinterpret_cast<uint32_t *>(at) = big;
       *reinterpret_cast<uint32_t *>(at + plane) = rest;
     }
@@ -526,7 +526,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       };
       if constexpr (MODE == kWalkKeep) {
         uint16_t *const to = (BACK ? p.end : p.start) + (bh * p.chunks + chunk) * 2 * dvp * DK;
-        keep_split<N>(S, to + (col0 / 8 * dvp + row0) * 8, dvp, dvp * DK);
+        keep_split<N>(S, to, row0, col0 / 8, DK / 8, dvp * DK);
       }
       // products of the state's part with K, and with Q for the output
       FragC r[8] = {}, o[8] = {};
@@ -609,7 +609,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         uint16_t *const to = (BACK ? p.dcorr : p.corrections) + (bh * p.chunks + chunk) * 2 * dvp * kDeltaChunk;
 #pragma unroll
         for (int i2 = 0; i2 < NB; ++i2)
-          keep_split<2>(&d[2 * i2], to + (L::block(part, i2) * 2 * dvp + row0) * 8, dvp, dvp * kDeltaChunk);
+          keep_split<2>(&d[2 * i2], to, row0, L::block(part, i2) * 2, 8, dvp * kDeltaChunk);
       }
       if constexpr (MODE == kWalkOut) {  // this warp's part of O: first scale (Q S) + P D
 #pragma unroll

@@ -29,9 +29,9 @@ constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
 
 template <int DK>
 struct Grad {
-  static constexpr int kParts = DK / 64, kThreads = 128 * kParts, kSlice = 32;
+  static constexpr int kParts = DK / 64, kThreads = 128 * kParts, kSlice = kKeptRows;
   static constexpr int kWide = DK + 8, kNarrow = kSlice + 8;  // row pitches
-  static constexpr int kTile = kDeltaChunk * kWide * 2, kStates = kSlice * kWide * 2, kSteps = kSlice * kTilePitch * 2,
+  static constexpr int kTile = kDeltaChunk * kWide * 2, kStates = kSlice * DK * 2, kSteps = kSlice * kDeltaChunk * 2,
                        kValues = kDeltaChunk * kNarrow * 2;
   static constexpr int kK = 0, kQ = kTile, kStage = 2 * kTile;
   // a slice of v's columns, two of them in flight where they fit
@@ -47,7 +47,7 @@ struct Grad {
   static constexpr bool kClustered = DK <= 128;  // (of 256, more than a CTA's memory)
   static constexpr int kPlain = kStageEnd > kAfter ? kStageEnd : kAfter,
                        kGates = kClustered && kSumsEnd > kPlain ? kSumsEnd : kPlain, kRows = kGates + kGateFloats * 4,
-                       kSums = kRows + 4 * kParts * kDeltaChunk * 4, kBytes = kSums + (kThreads + 32) * 4;
+                       kSums = kRows + 4 * kParts * kDeltaChunk * 4, kBytes = kSums + (kThreads / 32 * kDeltaChunk + 32) * 4;
 };
 
 __device__ __forceinline__ void put_gate(const HeadsOf &h, bool f32, bool f16, int64_t b, int64_t t, int64_t head, float v) {
@@ -133,28 +133,47 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
   const int64_t at = (b * p.heads + head) * p.chunks + chunk;
   const int slices64 = (p.dv_size + kDeltaSlice - 1) / kDeltaSlice;
   const int64_t dvp = (int64_t)slices64 * kDeltaSlice;
+  __shared__ uint64_t arrived[2];
+  __shared__ int failed;
   const uint32_t base = smem_u32(smem), K = base + L::kK, Q = base + L::kQ;
   float *const gates = reinterpret_cast<float *>(smem + L::kGates);
   float *const rows = reinterpret_cast<float *>(smem + L::kRows);  // (4, parts, 64): q.dQ0, k.X0, k.X, k.Y0
   float *const sums = reinterpret_cast<float *>(smem + L::kSums);
+  if (tid == 0) {
+    failed = 0;
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&arrived[s]), 1);
+    mbar_init_fence();
+  }
+  __syncthreads();
   wait_for_predecessor();
   copy_tile<DK, L::kThreads>(K, p.tk, b, head_k, t0, p.steps, 0);
   copy_tile<DK, L::kThreads>(Q, p.tq, b, head_k, t0, p.steps, 0);
   if (tid < kGateFloats / 4)
     copy16(base + L::kGates + tid * 16, p.records + at * kRecordBytes + kRecordHalfs * 2 + tid * 16, true);
   FragC dq[8] = {}, x[8] = {}, y[8] = {}, dp[NT] = {}, mm[NT] = {};
-  float whole = 0.f, vr = 0.f;
+  float whole = 0.f, vr[8] = {};
   const uint16_t *const s0 = p.start + at * 2 * dvp * DK, *const s1 = p.end + at * 2 * dvp * DK;
   const uint16_t *const c0 = p.corrections + at * 2 * dvp * kDeltaChunk, *const c1 = p.dcorr + at * 2 * dvp * kDeltaChunk;
+  int issued = 0;  // slices whose copies were started, in warp 0
+  bool ok = true;
   auto request = [&](int col_v) {
     if (col_v < p.dv_size) {
-      const uint32_t to = base + L::kStage + col_v / L::kSlice % L::kSlices * L::kSliceBytes;
+      const int turn = col_v / L::kSlice % L::kSlices;
+      const uint32_t to = base + L::kStage + turn * L::kSliceBytes;
+      if (warp == 0 && ok) {
+        const uint32_t bar = smem_u32(&arrived[turn]);
+        ++issued;
+        if (lane == 0) {
+          mbar_expect_tx(bar, 4 * (L::kStates + L::kSteps));
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        copy_kept<L::kSlice, DK, L::kThreads>(to + L::kS + h * L::kStates, s0 + h * dvp * DK + col_v * 8, dvp);
-        copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(to + L::kR + h * L::kSteps, c1 + h * dvp * kDeltaChunk + col_v * 8, dvp);
-        copy_kept<L::kSlice, DK, L::kThreads>(to + L::kE + h * L::kStates, s1 + h * dvp * DK + col_v * 8, dvp);
-        copy_kept<L::kSlice, kDeltaChunk, L::kThreads>(to + L::kD + h * L::kSteps, c0 + h * dvp * kDeltaChunk + col_v * 8, dvp);
+          for (int h = 0; h < 2; ++h) {
+            copy_bulk(to + L::kS + h * L::kStates, s0 + (h * dvp + col_v) * DK, L::kStates, bar);
+            copy_bulk(to + L::kE + h * L::kStates, s1 + (h * dvp + col_v) * DK, L::kStates, bar);
+            copy_bulk(to + L::kR + h * L::kSteps, c1 + (h * dvp + col_v) * kDeltaChunk, L::kSteps, bar);
+            copy_bulk(to + L::kD + h * L::kSteps, c0 + (h * dvp + col_v) * kDeltaChunk, L::kSteps, bar);
+          }
+        }
+        __syncwarp();
       }
       copy_tile<L::kSlice, L::kThreads>(to + L::kDo, p.td, b, head, t0, p.steps, col_v);
       copy_tile<L::kSlice, L::kThreads>(to + L::kV, p.tv, b, head, t0, p.steps, col_v);
@@ -165,24 +184,26 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
   for (int col_v = 0; col_v < p.dv_size; col_v += L::kSlice) {
     if (L::kSlices == 2) request(col_v + L::kSlice);
     copies_wait<L::kSlices - 1>();
+    const int number = col_v / L::kSlice, turn = number % L::kSlices;
+    ok = wait_for<false>(smem_u32(&arrived[turn]), (uint32_t)(number / L::kSlices) & 1u, &failed, p.polls) && ok;
     __syncthreads();
-    char *const slice = smem + L::kStage + col_v / L::kSlice % L::kSlices * L::kSliceBytes;
+    char *const slice = smem + L::kStage + turn * L::kSliceBytes;
     const uint32_t from = smem_u32(slice);
 #pragma unroll
     for (int s = 0; s < L::kSlice / 16; ++s) {
       FragA o, r, rr, d, dd;
       load_matrices(o, at_kn(from + L::kDo, L::kNarrow, row, s * 16, lane));
-      load_matrices_t(r, at_km(from + L::kR, kTilePitch, s * 16, row, lane));
-      load_matrices_t(rr, at_km(from + L::kR + L::kSteps, kTilePitch, s * 16, row, lane));
-      load_matrices_t(d, at_km(from + L::kD, kTilePitch, s * 16, row, lane));
-      load_matrices_t(dd, at_km(from + L::kD + L::kSteps, kTilePitch, s * 16, row, lane));
+      load_matrices_t(r, kept_km<L::kSlice>(from + L::kR, s * 16, row, lane));
+      load_matrices_t(rr, kept_km<L::kSlice>(from + L::kR + L::kSteps, s * 16, row, lane));
+      load_matrices_t(d, kept_km<L::kSlice>(from + L::kD, s * 16, row, lane));
+      load_matrices_t(dd, kept_km<L::kSlice>(from + L::kD + L::kSteps, s * 16, row, lane));
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         uint32_t h[4], l[4], eh[4], el[4];
-        load_matrices_t(h, at_kn(from + L::kS, L::kWide, s * 16, col + n * 16, lane));
-        load_matrices_t(l, at_kn(from + L::kS + L::kStates, L::kWide, s * 16, col + n * 16, lane));
-        load_matrices_t(eh, at_kn(from + L::kE, L::kWide, s * 16, col + n * 16, lane));
-        load_matrices_t(el, at_kn(from + L::kE + L::kStates, L::kWide, s * 16, col + n * 16, lane));
+        load_matrices_t(h, kept_kn<L::kSlice>(from + L::kS, s * 16, col + n * 16, lane));
+        load_matrices_t(l, kept_kn<L::kSlice>(from + L::kS + L::kStates, s * 16, col + n * 16, lane));
+        load_matrices_t(eh, kept_kn<L::kSlice>(from + L::kE, s * 16, col + n * 16, lane));
+        load_matrices_t(el, kept_kn<L::kSlice>(from + L::kE + L::kStates, s * 16, col + n * 16, lane));
         mma_input_split<F16>(dq[2 * n], dq[2 * n + 1], o, h, l);
         mma_split_split(x[2 * n], x[2 * n + 1], r, rr, h, l);
         mma_split_split(y[2 * n], y[2 * n + 1], d, dd, eh, el);
@@ -191,37 +212,58 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       for (int n = 0; n < NT / 2; ++n) {
         if (mcol + n * 16 > row) continue;
         uint32_t h[4], l[4];
-        load_matrices_t(h, at_kn(from + L::kD, kTilePitch, s * 16, mcol + n * 16, lane));
-        load_matrices_t(l, at_kn(from + L::kD + L::kSteps, kTilePitch, s * 16, mcol + n * 16, lane));
+        load_matrices_t(h, kept_kn<L::kSlice>(from + L::kD, s * 16, mcol + n * 16, lane));
+        load_matrices_t(l, kept_kn<L::kSlice>(from + L::kD + L::kSteps, s * 16, mcol + n * 16, lane));
         mma_input_split<F16>(dp[2 * n], dp[2 * n + 1], o, h, l);
         mma_split_split(mm[2 * n], mm[2 * n + 1], r, rr, h, l);
       }
     }
-    {  // dR . V: step tid % 64, every (threads / 64)th column
-      const int c = tid % 64;
-      const uint16_t *const r = reinterpret_cast<const uint16_t *>(slice + L::kR) + c;
-      const uint16_t *const v = reinterpret_cast<const uint16_t *>(slice + L::kV) + c * L::kNarrow;
-#pragma unroll 4
-      for (int j = tid / 64; j < L::kSlice; j += L::kThreads / 64) {
-        const float f = BF16::to_float(r[j * kTilePitch]) + BF16::to_float(r[j * kTilePitch + L::kSteps / 2]);
-        vr = fmaf(f, F16 ? Elem<GEMV_TYPE_F16>::get(v[j]) : Elem<GEMV_TYPE_BF16>::get(v[j]), vr);
+    // dR . V: 8 steps of a column of v per thread
+    for (int i = tid; i < L::kSlice * 8; i += L::kThreads) {
+      const int u = i % 8, j = i / 8;
+      const uint4 big = *reinterpret_cast<const uint4 *>(slice + L::kR + (u * L::kSlice + j) * 16),
+                  rest = *reinterpret_cast<const uint4 *>(slice + L::kR + L::kSteps + (u * L::kSlice + j) * 16);
+      const uint16_t *const v = reinterpret_cast<const uint16_t *>(slice + L::kV) + u * 8 * L::kNarrow + j;
+      const uint32_t bw[4] = {big.x, big.y, big.z, big.w}, rw[4] = {rest.x, rest.y, rest.z, rest.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_bf16(bw[e]), g = unpack_bf16(rw[e]);
+        const uint16_t v0 = v[2 * e * L::kNarrow], v1 = v[(2 * e + 1) * L::kNarrow];
+        vr[2 * e] = fmaf(f.x + g.x, F16 ? Elem<GEMV_TYPE_F16>::get(v0) : Elem<GEMV_TYPE_BF16>::get(v0), vr[2 * e]);
+        vr[2 * e + 1] = fmaf(f.y + g.y, F16 ? Elem<GEMV_TYPE_F16>::get(v1) : Elem<GEMV_TYPE_BF16>::get(v1), vr[2 * e + 1]);
       }
     }
-    // <S, dS'>: pairs of the slice
-#pragma unroll 4
-    for (int i = tid; i < L::kSlice * DK / 2; i += L::kThreads) {
-      const int at2 = (i / (DK / 2)) * L::kWide * 2 + i % (DK / 2) * 4;
-      auto both = [&](int area) {
-        const float2 h = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + at2));
-        const float2 l = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + L::kStates + at2));
+    // <S, dS'>: 8 columns of a row per thread
+#pragma unroll
+    for (int i = tid; i < L::kSlice * DK / 8; i += L::kThreads) {
+      auto word = [&](int area, int e) {
+        const float2 h = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + i * 16 + e * 4));
+        const float2 l = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + L::kStates + i * 16 + e * 4));
         return make_float2(h.x + l.x, h.y + l.y);
       };
-      const float2 u = both(L::kS), w = both(L::kE);
-      whole = fmaf(u.x, w.x, fmaf(u.y, w.y, whole));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 u = word(L::kS, e), w = word(L::kE, e);
+        whole = fmaf(u.x, w.x, fmaf(u.y, w.y, whole));
+      }
     }
     __syncthreads();
     if (L::kSlices == 1) request(col_v + L::kSlice);
   }
+  if (*(volatile int *)&failed) {  // a copy that did not arrive: nothing of this chunk is known
+    if (warp == 0) {
+      int none = 0;
+      for (int n = issued > L::kSlices ? issued - L::kSlices : 0; n < issued; ++n)
+        wait_for<false>(smem_u32(&arrived[n % L::kSlices]), (uint32_t)(n / L::kSlices) & 1u, &none, kWaitPolls);
+      if (lane == 0) atomicAdd(p.timeouts, 1u);
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) dq[n][e] = x[n][e] = y[n][e] = __int_as_float(0x7fc00000);
+    whole = __int_as_float(0x7fc00000);
+  }
+  __syncthreads();
   // the terms with S and dS', scaled, and what they are along the rows of q and k
   {
     const int i0 = row + lane / 4;
@@ -264,7 +306,12 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       mma_inputs<F16>(kk[2 * n + 1], ak, bk[2], bk[3]);
     }
   }
-  sums[tid] = vr;  // (the slices are done with)
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {  // lanes 8 apart have other columns of the same steps
+    vr[e] += __shfl_xor_sync(0xffffffffu, vr[e], 8);
+    vr[e] += __shfl_xor_sync(0xffffffffu, vr[e], 16);
+    if (lane < 8) sums[warp * kDeltaChunk + lane * 8 + e] = vr[e];
+  }
   float *const W = reinterpret_cast<float *>(smem + L::kW);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -350,39 +397,74 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
     store_rows<F16>(y, p.dk, p.dk32, p, b, out_head, t0, row, col);
   }
   // the gates' gradients
+  float *const totals = sums + L::kThreads / 32 * kDeltaChunk;
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) whole += __shfl_xor_sync(0xffffffffu, whole, m);
-  if (lane == 0) sums[L::kThreads + warp] = whole;
-  if (tid < kDeltaChunk) {  // column tid of W, summed from below
+  if (lane == 0) totals[warp] = whole;
+  // columns of W summed from below, in pieces of 64 / parts rows
+  constexpr int kPieces = L::kThreads / kDeltaChunk, kPiece = kDeltaChunk / kPieces;
+  const int step = tid % kDeltaChunk, piece = tid / kDeltaChunk;
+  {
     float s = 0.f;
-    for (int i = kDeltaChunk - 1; i >= 0; --i) {
-      s += W[i * L::kWPitch + tid];
-      W[i * L::kWPitch + tid] = s;
+#pragma unroll
+    for (int i = kPiece - 1; i >= 0; --i) {
+      float &w = W[(piece * kPiece + i) * L::kWPitch + step];
+      s += w;
+      w = s;
     }
   }
   __syncthreads();
-  if (tid < kDeltaChunk && t0 + tid < p.steps) {
+  {  // what passes step `step` of the products: W's columns before it, from its row down
+    const int mine = step / kPiece;
+    float s = 0.f;
+#pragma unroll 4
+    for (int j = piece; j < step; j += kPieces) {
+      s += W[step * L::kWPitch + j];
+      for (int below = mine + 1; below < kPieces; ++below) s += W[below * kPiece * L::kWPitch + j];
+    }
+    __syncthreads();
+    W[piece * kDeltaChunk + step] = s;  // (W has been read)
+  }
+  __syncthreads();
+  if (tid < 32) {  // two steps per lane
     auto of = [&](int which, int i) {
       float s = rows[which * L::kParts * kDeltaChunk + i];
 #pragma unroll
       for (int q = 1; q < L::kParts; ++q) s += rows[(which * L::kParts + q) * kDeltaChunk + i];
       return s;
     };
-    float db = of(2, tid);
+    float ahead[2], before[2], all = 0.f;
 #pragma unroll
-    for (int q = 0; q < L::kThreads / 64; ++q) db += sums[q * 64 + tid];
-    put_gate(p.dbeta, p.gates_f32, F16, b, t0 + tid, head, db);
-    float inner = 0.f, ahead = 0.f, before = 0.f, all = 0.f;
-    for (int j = 0; j < tid; ++j) {
-      inner += W[tid * L::kWPitch + j];
-      before += of(3, j);
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * lane + e;
+      ahead[e] = of(0, i) + gates[kBeta + i] * of(1, i);
+      before[e] = of(3, i);
     }
-    for (int i = tid; i < kDeltaChunk; ++i) ahead += of(0, i) + gates[kBeta + i] * of(1, i);
-    for (int w = 0; w < L::kThreads / 32; ++w) all += sums[L::kThreads + w];
-    // nothing passes the first step of a document
-    const bool starts = tid == 0 ? gates[kDocs] != 0.f : gates[kDocs + tid] != gates[kDocs + tid - 1];
-    const float dg = starts ? 0.f : inner + ahead + before + gates[kFirst + kDeltaChunk - 1] * all;
-    put_gate(p.dg, p.gates_f32, F16, b, t0 + tid, head, dg);
+    float up = before[0] + before[1], down = ahead[0] + ahead[1];
+#pragma unroll
+    for (int m = 1; m < 32; m *= 2) {
+      const float u = __shfl_up_sync(0xffffffffu, up, m), v = __shfl_down_sync(0xffffffffu, down, m);
+      if (lane >= m) up += u;
+      if (lane + m < 32) down += v;
+    }
+    const float first_up = __shfl_up_sync(0xffffffffu, up, 1), first_down = __shfl_down_sync(0xffffffffu, down, 1);
+    const float below = lane == 0 ? 0.f : first_up, above = lane == 31 ? 0.f : first_down;
+    for (int w = 0; w < L::kThreads / 32; ++w) all += totals[w];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = 2 * lane + e;
+      if (t0 + i >= p.steps) continue;
+      float db = of(2, i), inner = 0.f;
+      for (int w = 0; w < L::kThreads / 32; ++w) db += sums[w * kDeltaChunk + i];
+      put_gate(p.dbeta, p.gates_f32, F16, b, t0 + i, head, db);
+#pragma unroll
+      for (int w = 0; w < kPieces; ++w) inner += W[w * kDeltaChunk + i];
+      // nothing passes the first step of a document
+      const bool starts = i == 0 ? gates[kDocs] != 0.f : gates[kDocs + i] != gates[kDocs + i - 1];
+      const float state = above + (e == 0 ? ahead[0] + ahead[1] : ahead[1]) + below + (e == 0 ? 0.f : before[0]);
+      const float dg = starts ? 0.f : inner + state + gates[kFirst + kDeltaChunk - 1] * all;
+      put_gate(p.dg, p.gates_f32, F16, b, t0 + i, head, dg);
+    }
   }
   if constexpr (L::kClustered) {
     if (clustered) {  // a CTA per head that shares q and k: each sums its part of the rows, in the heads' order
@@ -393,6 +475,7 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       typedef Elem<F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16> E;
       const int group = p.heads / p.heads_k, rank = (int)cluster_rank();
       const int first = kDeltaChunk * rank / group, last = kDeltaChunk * (rank + 1) / group;
+#pragma unroll 4
       for (int i = tid; i < (last - first) * (DK / 2); i += L::kThreads) {
         const int r = first + i / (DK / 2), j = i % (DK / 2) * 2;
         if (t0 + r >= p.steps || j >= p.dk_size) continue;

@@ -237,21 +237,18 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, const TileSource &s, int
     left -= ROWS;
   }
 }
-// ROWS rows of COLS elements of what the walks have kept (units of 8 columns, `rows` of 16
-// bytes each), to rows of COLS + 8.
-template <int ROWS, int COLS, int THREADS>
-__device__ __forceinline__ void copy_kept(uint32_t dst, const uint16_t *src, int64_t rows) {
-  constexpr int UNITS = COLS / 8, ROUND = THREADS / ROWS;  // units that a round takes
-  static_assert(THREADS % ROWS == 0, "whole units");
-  const int r = threadIdx.x % ROWS, u0 = threadIdx.x / ROWS;
-  const uint16_t *from = src + (u0 * rows + r) * 8;
-  const int64_t next = ROUND * rows * 8;
-  dst += (uint32_t)(r * (COLS + 8) + u0 * 8) * 2;
-#pragma unroll
-  for (int i = 0; i < (UNITS + ROUND - 1) / ROUND; ++i) {
-    if (UNITS % ROUND == 0 || u0 + i * ROUND < UNITS) copy16(dst + i * ROUND * 16, from, true);
-    from += next;
-  }
+// What the walks keep lies in units of 8 columns, a row's 16 bytes after the other's
+// (kept_unit()), in shared memory too: 8 rows of a unit are 128 bytes side by side, which
+// load_matrices() wants.
+// Addresses of a 16 x 16 block, for transposing loads: as a right operand stored (k, n), as a
+// left operand stored (k, m).
+template <int ROWS>
+__device__ __forceinline__ uint32_t kept_kn(uint32_t base, int k, int n, int lane) {
+  return base + (uint32_t)((n / 8 + ((lane >> 4) & 1)) * ROWS + k + (lane & 7) + ((lane >> 3) & 1) * 8) * 16;
+}
+template <int ROWS>
+__device__ __forceinline__ uint32_t kept_km(uint32_t base, int k, int m, int lane) {
+  return base + (uint32_t)((m / 8 + ((lane >> 3) & 1)) * ROWS + k + (lane & 7) + ((lane >> 4) & 1) * 8) * 16;
 }
 // The 16 x 16 blocks on and below the diagonal of two 64 x 64 matrices, dense, to rows
 // of 72.

@@ -302,16 +302,15 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
           if (t + e < p.steps) rows[(int64_t)(t + e) * to.step + j] = (uint16_t)(v[e / 2] >> (e % 2 * 16));
       }
     };
-    // 16 columns of tensor memory (32 of bf16) as they are, for the gradient: units of 8 columns, rows
-    // of all of v's columns
-    auto keep = [&](const float (&v)[16], uint16_t *to) {
+    // 16 columns of tensor memory (32 of bf16) of the corrections as they are, for the gradient
+    auto keep = [&](const float (&v)[16], uint16_t *to, int unit) {
       if (j >= dvp) return;
-      uint4 *at = reinterpret_cast<uint4 *>(to) + j;
+      uint4 *at = reinterpret_cast<uint4 *>(to) + kept_unit(j, unit, 8);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         at[0] = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
                            __float_as_uint(v[4 * q + 3]));
-        at += dvp;
+        at += kKeptRows;
       }
     };
     for (int i = 0; i < p.chunks; ++i) {
@@ -355,8 +354,8 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
         give(&sh.out_read);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          keep(big[h], to_d + (int64_t)h * 4 * dvp * 8);
-          keep(rest[h], to_d + dvp * kDeltaChunk + (int64_t)h * 4 * dvp * 8);
+          keep(big[h], to_d, h * 4);
+          keep(rest[h], to_d + dvp * kDeltaChunk, h * 4);
           if constexpr (BACK) {
             uint32_t dv[16];
 #pragma unroll
@@ -410,14 +409,14 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
 #pragma unroll
         for (int e = 0; e < 16; e += 2) mul2(s[q][e], s[q][e + 1], s[q][e], s[q][e + 1], whole, whole);
         tmem_store16(lanes + kColS + 2 * c + q * 16, s[q]);
-        if constexpr (!kOut) {  // kept for the gradient: units of 8 columns, rows of all of v's columns
+        if constexpr (!kOut) {  // kept for the gradient
           if (j < dvp) {
             uint4 *const at = reinterpret_cast<uint4 *>((BACK ? p.end : p.start) + record * 2 * dvp * kWidth) +
-                              (int64_t)(c / 4 + q * 2) * dvp + j;
+                              kept_unit(j, c / 4 + q * 2, kWidth / 8);
             at[0] = make_uint4(big[0], big[1], big[2], big[3]);
-            at[dvp] = make_uint4(big[4], big[5], big[6], big[7]);
+            at[kKeptRows] = make_uint4(big[4], big[5], big[6], big[7]);
             at[dvp * kWidth / 8] = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-            at[dvp * kWidth / 8 + dvp] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
+            at[dvp * kWidth / 8 + kKeptRows] = make_uint4(rest[4], rest[5], rest[6], rest[7]);
           }
         }
       }
