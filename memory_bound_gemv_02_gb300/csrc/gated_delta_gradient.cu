@@ -414,13 +414,20 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
     }
   }
   __syncthreads();
-  {  // what passes step `step` of the products: W's columns before it, from its row down
-    const int mine = step / kPiece;
+  {  // the pieces below added; a piece's first row holds its total
     float s = 0.f;
-#pragma unroll 4
-    for (int j = piece; j < step; j += kPieces) {
-      s += W[step * L::kWPitch + j];
-      for (int below = mine + 1; below < kPieces; ++below) s += W[below * kPiece * L::kWPitch + j];
+    for (int below = piece + 1; below < kPieces; ++below) s += W[below * kPiece * L::kWPitch + step];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) W[(piece * kPiece + i) * L::kWPitch + step] += s;
+  }
+  __syncthreads();
+  {  // what passes step `step` of the products: W's columns before it, from its row down
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const int j = piece * kPiece + i;
+      s += j < step ? W[step * L::kWPitch + j] : 0.f;
     }
     __syncthreads();
     W[piece * kDeltaChunk + step] = s;  // (W has been read)
