@@ -303,7 +303,7 @@ typedef struct gated_delta_shape {
  *              overlapping nothing, free again after the call's work on the
  *              stream); a shorter one returns GEMV_ERR_SCRATCH.
  *
- * Up to 48 steps are walked one by one in fp32, by one kernel.  Longer sequences are
+ * Up to 12 steps are walked one by one in fp32, by one kernel.  Longer sequences are
  * cut into chunks of 64 steps, whose products run on the tensor cores by two
  * kernels, the state and what comes from it as sums of two bf16 (products within
  * 2^-16 of their terms).  Operands whose rows are not on 16 bytes are copied first,

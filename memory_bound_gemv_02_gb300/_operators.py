@@ -267,7 +267,7 @@ def gated_delta(q, k, v, g, beta, scale: float, h0=None, o=None, state=None, str
     q's dtype or float32 (both alike).  ``h0`` and ``state``: float32
     (batch, heads, dk, dv); ``state`` receives the last S and may be ``h0`` (in-place
     decoding).  g = -inf starts a new document.  ``workspace`` (sequences of more
-    than 48 steps): any tensor of ``gated_delta_workspace`` bytes, or torch's
+    than 12 steps): any tensor of ``gated_delta_workspace`` bytes, or torch's
     allocator has memory for the call's stream.  Not recorded by autograd.  Returns
     (o, state)."""
     if o is None:

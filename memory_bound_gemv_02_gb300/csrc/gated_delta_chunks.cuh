@@ -739,10 +739,16 @@ int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t str
                               dim3((unsigned)p.chunks, (unsigned)p.heads_k, (unsigned)p.batch), kPrepareThreads,
                               Prepare<DK>::kBytes, stream, p);
   if (st != GEMV_OK) return st;
-  // Few heads: one team of four warps per CTA while that leaves each its own SM.
-  const int64_t teams = (int64_t)p.batch * p.heads * ((p.dv_size + 15) / 16) * (gradient ? 2 : 1);
-  if (teams <= sms) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);
-  if (!F16 && DK == 128 && p.dv_size > 64) return launch_delta_tensor(p, gradient, stream);
+  // Few heads: a team of four warps per CTA while there is one CTA per SM, or two in the
+  // gradient, whose chains wait for memory as well.  More: the tensor walk where there is one; but
+  // in the gradient wider CTAs while they fill the GPU once.  1024 steps, 128 x 128 bf16, forward
+  // (us) teams / tensor / wide, 8 heads 47 / 65 / 78, 16 47 / 65 / 79, 20 84 / 67 / 80, 64 165 / 80 / 91,
+  // 128 288 / 110 / 173; gradient 8 heads 74 / 115 / 113, 16 135 / 150 / 142, 20 170 / 176 / 168,
+  // 32 232 / 204 / 194, 64 409 / 325 / 349.
+  const int64_t heads = (int64_t)p.batch * p.heads, walks = gradient ? 2 : 1;
+  if (heads * ((p.dv_size + 15) / 16) <= sms) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);
+  const bool once = heads * walks * ((p.dv_size + kDeltaSlice - 1) / kDeltaSlice) <= sms;
+  if (!F16 && DK == 128 && p.dv_size > 64 && !(gradient && once)) return launch_delta_tensor(p, gradient, stream);
   return launch_walk<F16, DK, 4, 2>(p, gradient, stream);
 }
 

@@ -51,7 +51,7 @@ def run_back(x, do, h0=None, dstate=None, **kw):
 
 
 SIZES = [  # batch, steps, heads of k, of v, dk, dv
-    (1, 1, 1, 1, 1, 1), (2, 1, 2, 4, 128, 128), (3, 2, 1, 3, 17, 5), (1, 7, 2, 2, 256, 130), (2, 48, 1, 2, 64, 33),
+    (1, 1, 1, 1, 1, 1), (2, 1, 2, 4, 128, 128), (3, 2, 1, 3, 17, 5), (1, 7, 2, 2, 256, 130), (2, 12, 1, 2, 64, 33), (2, 13, 2, 2, 72, 40),
     (1, 49, 1, 1, 128, 128), (2, 63, 2, 2, 64, 64), (1, 64, 1, 2, 96, 72), (1, 65, 2, 2, 128, 200), (2, 128, 1, 1, 256, 64),
     (1, 129, 1, 3, 40, 8), (1, 200, 2, 4, 100, 99), (1, 300, 1, 1, 255, 31), (1, 193, 1, 1, 1, 3)]
 
@@ -76,7 +76,7 @@ def test_backward(cuda_dev, size, dtype, gates):
 
 MANY = [  # enough heads for a CTA of wide columns each
     (4, 64, 2, 6, 128, 128), (4, 70, 6, 6, 128, 128), (2, 200, 10, 10, 100, 99), (5, 129, 5, 5, 72, 200),
-    (3, 193, 4, 8, 65, 128), (20, 49, 1, 2, 128, 65), (4, 130, 3, 9, 64, 128), (3, 100, 8, 8, 256, 96)]
+    (4, 70, 5, 10, 128, 128), (5, 193, 8, 8, 100, 99), (8, 129, 3, 6, 65, 130), (3, 193, 4, 8, 65, 128), (20, 49, 1, 2, 128, 65), (4, 130, 3, 9, 64, 128), (3, 100, 8, 8, 256, 96)]
 
 
 @pytest.mark.parametrize("size", MANY)
@@ -301,7 +301,7 @@ def test_a_given_workspace(cuda_dev):
         with pytest.raises(g.GemvError) as e:
             (run_back(x, do, h0, dstate, workspace=ws[:-1]) if back else run(x, h0, workspace=ws[:-1]))
         assert e.value.status == g.GEMV_ERR_SCRATCH
-    y, h0, _, _ = make(cuda_dev, 1, 48, 1, 2, 40, 24, F16)
+    y, h0, _, _ = make(cuda_dev, 1, 12, 1, 2, 40, 24, F16)
     assert g.gated_delta_workspace(y["q"], y["k"], y["v"]) == 0
 
 
@@ -338,7 +338,7 @@ def test_refusals(cuda_dev):
     assert e.value.status == g.GEMV_ERR_ARG
 
 
-@pytest.mark.parametrize("size", [(4, 130, 6, 6, 128, 128)])
+@pytest.mark.parametrize("size", [(4, 130, 10, 10, 128, 128)])
 def test_a_wait_that_gives_up(cuda_dev, size):
     """Waits without a poll: NaN instead of a hang, a count, and nothing left behind."""
     x, h0, do, dstate = make(cuda_dev, *size, BF16)
