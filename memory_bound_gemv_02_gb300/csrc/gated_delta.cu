@@ -568,5 +568,6 @@ extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_h
   p.dq32 = !sums_in_clusters(s) ? reinterpret_cast<float *>(ws + l.dq32) : nullptr;
   p.dk32 = !sums_in_clusters(s) ? reinterpret_cast<float *>(ws + l.dk32) : nullptr;
   p.vector_dv = on_units(*dv, s.dv) ? 1 : 0;
+  p.vector_dqk = on_units(*dq, s.dk) && on_units(*dk, s.dk) ? 1 : 0;
   return launch_delta_gradient(p, padded_dk(s.dk), sms, stream);
 }

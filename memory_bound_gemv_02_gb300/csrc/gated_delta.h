@@ -52,7 +52,7 @@ struct DeltaParams {
   float *dq32, *dk32;              // gradients per head of v where heads of k are shared
   float scale;
   int32_t batch, steps, heads, heads_k, dk_size, dv_size, chunks;
-  int32_t gates_f32, f16, vector_o, vector_dv;
+  int32_t gates_f32, f16, vector_o, vector_dv, vector_dqk;  // outputs whose rows are on 16 bytes
   int32_t polls;       // of the tensor walk's waits
   uint32_t *timeouts;
 };

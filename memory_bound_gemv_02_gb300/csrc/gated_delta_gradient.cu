@@ -92,14 +92,19 @@ __device__ __forceinline__ void store_rows(const FragC (&c)[8], const HeadsOf &t
     float *const at32 = to32 ? to32 + ((b * p.steps + t) * p.heads + head) * p.dk_size : nullptr;
     uint16_t *const at = static_cast<uint16_t *>(const_cast<void *>(to.p)) + b * to.batch + (int64_t)t * to.step + head * to.head;
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+    for (int n = 0; n < 8; ++n) {
+      const int j = col + n * 8 + lane % 4 * 2;
+      if (p.vector_dqk && !to32) {
+        if (j < p.dk_size) *reinterpret_cast<uint32_t *>(at + j) = pack_output<F16>(c[n][2 * h], c[n][2 * h + 1]);
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int j = col + n * 8 + lane % 4 * 2 + e;
-        if (j >= p.dk_size) continue;
-        if (to32) at32[j] = c[n][2 * h + e];
-        else at[j] = E::put(c[n][2 * h + e]);
+        if (j + e >= p.dk_size) continue;
+        if (to32) at32[j + e] = c[n][2 * h + e];
+        else at[j + e] = E::put(c[n][2 * h + e]);
       }
+    }
   }
 }
 
@@ -113,10 +118,29 @@ __device__ __forceinline__ void put_rows(const FragC (&c)[8], float *to, int pit
       *reinterpret_cast<float2 *>(to + (row + lane / 4 + 8 * h) * pitch + col + n * 8 + lane % 4 * 2) =
           make_float2(c[n][2 * h], c[n][2 * h + 1]);
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void add4(float4 &s, const float4 &v) {
+  s.x += v.x;
+  s.y += v.y;
+  s.z += v.z;
+  s.w += v.w;
+}
+// Four neighbouring values of a row of `size`.
+template <bool F16>
+__device__ __forceinline__ void put4(uint16_t *to, const float4 &v, int left, bool vector) {
+  const uint2 w = make_uint2(pack_output<F16>(v.x, v.y), pack_output<F16>(v.z, v.w));
+  if (vector) {
+    *reinterpret_cast<uint2 *>(to) = w;
+    return;
+  }
+  to[0] = (uint16_t)w.x;
+  if (left > 1) to[1] = (uint16_t)(w.x >> 16);
+  if (left > 2) to[2] = (uint16_t)w.y;
+  if (left > 3) to[3] = (uint16_t)(w.y >> 16);
 }
 
 template <bool F16, int DK>
@@ -236,16 +260,16 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
     // <S, dS'>: 8 columns of a row per thread
 #pragma unroll
     for (int i = tid; i < L::kSlice * DK / 8; i += L::kThreads) {
-      auto word = [&](int area, int e) {
-        const float2 h = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + i * 16 + e * 4));
-        const float2 l = unpack_bf16(*reinterpret_cast<const uint32_t *>(slice + area + L::kStates + i * 16 + e * 4));
-        return make_float2(h.x + l.x, h.y + l.y);
+      auto unit = [&](int area) { return *reinterpret_cast<const uint4 *>(slice + area + i * 16); };
+      const uint4 sh = unit(L::kS), sl = unit(L::kS + L::kStates), eh = unit(L::kE), el = unit(L::kE + L::kStates);
+      auto add = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+        const float2 u = unpack_bf16(a), v = unpack_bf16(b), w = unpack_bf16(c), z = unpack_bf16(d);
+        whole = fmaf(u.x + v.x, w.x + z.x, fmaf(u.y + v.y, w.y + z.y, whole));
       };
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 u = word(L::kS, e), w = word(L::kE, e);
-        whole = fmaf(u.x, w.x, fmaf(u.y, w.y, whole));
-      }
+      add(sh.x, sl.x, eh.x, el.x);
+      add(sh.y, sl.y, eh.y, el.y);
+      add(sh.z, sl.z, eh.z, el.z);
+      add(sh.w, sl.w, eh.w, el.w);
     }
     __syncthreads();
     if (L::kSlices == 1) request(col_v + L::kSlice);
@@ -479,32 +503,22 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       put_rows(dq, reinterpret_cast<float *>(smem + L::kDq), L::kSumPitch, row, col);
       put_rows(y, reinterpret_cast<float *>(smem + L::kDk), L::kSumPitch, row, col);
       cluster_sync();
-      typedef Elem<F16 ? GEMV_TYPE_F16 : GEMV_TYPE_BF16> E;
       const int group = p.heads / p.heads_k, rank = (int)cluster_rank();
       const int first = kDeltaChunk * rank / group, last = kDeltaChunk * (rank + 1) / group;
+      uint16_t *const to_q = static_cast<uint16_t *>(const_cast<void *>(p.dq.p)) + b * p.dq.batch + head_k * p.dq.head,
+               *const to_k = static_cast<uint16_t *>(const_cast<void *>(p.dk.p)) + b * p.dk.batch + head_k * p.dk.head;
 #pragma unroll 4
-      for (int i = tid; i < (last - first) * (DK / 2); i += L::kThreads) {
-        const int r = first + i / (DK / 2), j = i % (DK / 2) * 2;
+      for (int i = tid; i < (last - first) * (DK / 4); i += L::kThreads) {
+        const int r = first + i / (DK / 4), j = i % (DK / 4) * 4;
         if (t0 + r >= p.steps || j >= p.dk_size) continue;
-        float q0 = 0.f, q1 = 0.f, k0 = 0.f, k1 = 0.f;
+        float4 q = {}, k = {};
         for (int m = 0; m < group; ++m) {
           const uint32_t from = cluster_address(base + L::kDq + (uint32_t)(r * L::kSumPitch + j) * 4, (uint32_t)m);
-          const float2 u = ld_cluster2(from), v = ld_cluster2(from + L::kDk - L::kDq);
-          q0 += u.x;
-          q1 += u.y;
-          k0 += v.x;
-          k1 += v.y;
+          add4(q, ld_cluster4(from));
+          add4(k, ld_cluster4(from + L::kDk - L::kDq));
         }
-        const int64_t q_at = b * p.dq.batch + (int64_t)(t0 + r) * p.dq.step + head_k * p.dq.head + j,
-                      k_at = b * p.dk.batch + (int64_t)(t0 + r) * p.dk.step + head_k * p.dk.head + j;
-        uint16_t *const to_q = static_cast<uint16_t *>(const_cast<void *>(p.dq.p)) + q_at,
-                 *const to_k = static_cast<uint16_t *>(const_cast<void *>(p.dk.p)) + k_at;
-        to_q[0] = E::put(q0);
-        to_k[0] = E::put(k0);
-        if (j + 1 < p.dk_size) {
-          to_q[1] = E::put(q1);
-          to_k[1] = E::put(k1);
-        }
+        put4<F16>(to_q + (int64_t)(t0 + r) * p.dq.step + j, q, p.dk_size - j, p.vector_dqk);
+        put4<F16>(to_k + (int64_t)(t0 + r) * p.dk.step + j, k, p.dk_size - j, p.vector_dqk);
       }
       cluster_sync();  // its memory is read until then
     }
