@@ -9,6 +9,10 @@
  *                         m > 1, 8-bit operands, a residual in the epilogue)
  *   gated_scan            the gated linear recurrence over a sequence
  *   gated_scan_backward   its gradient
+ *   layer_norm_fused      residual addition, layer norm
+ *   layer_norm_backward   its gradient, with the weight's and the bias's
+ *   gated_delta           the gated delta rule over a sequence
+ *   gated_delta_backward  its gradient
  *
  * The source pages have no counterpart of these entry points; the recurrence
  * is the per-channel decay of gla_decode() (TileLang Case Studies, Case D
@@ -19,7 +23,8 @@
  * GEMV_* status codes, nothing launched on failure, nothing thrown.  The calls
  * allocate nothing and keep nothing, so any number may run at once on any
  * streams, and all can be captured in a CUDA graph.  Each launches one kernel
- * (gemm_fused() two for unaligned operands) as a programmatic dependent launch:
+ * (gemm_fused() two for unaligned operands; layer_norm_backward(), gated_delta() and
+ * its gradient as their entries say) as a programmatic dependent launch:
  * it may start early, but reads and writes no operand before the work ahead of
  * the call has completed.  (A product that reads unaligned rows of B in place
  * does so while its own copy of A is made.)  Results are bitwise reproducible:
@@ -256,7 +261,7 @@ int layer_norm_fused(const void *x, int64_t ldx, const void *residual, int64_t l
  *                GEMV_ERR_SCRATCH.
  *
  * Two kernels, with rows too long for a CTA's registers (beyond 16384 16-bit or
- * 8192 other elements) three.
+ * 8192 fp32 elements) three.
  */
 int layer_norm_backward(const void *dy, int64_t lddy, const void *s, int64_t lds, const void *weight,
                         int weight_dtype, const float *mean, const float *rstd, const void *ds, int64_t ldds,
