@@ -3,7 +3,8 @@
 //
 //     S_t = a S_{t-1} + k d^T,  d = beta (v - a S_{t-1}^T k),  o = scale S_t^T q,  a = exp(g)
 //
-// One pass over the state: with S in registers, S^T k and S^T q come out of the same
+// Memory-bound for one step: 64 x 32 heads of 128 x 128 take 50 us, 5.4 TB/s, of 40 at the copy
+// rate.  One pass over the state: with S in registers, S^T k and S^T q come out of the same
 // walk, and o = scale (a S_{t-1}^T q + (q . k) d) needs no second one.  A single step
 // reads and writes the state once; the rest is nothing beside it.
 #include "gated_delta.h"

