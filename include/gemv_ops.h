@@ -317,7 +317,7 @@ typedef struct gated_delta_shape {
  * A g of minus infinity (or below -87.3, where the exponential leaves fp32's normal
  * range) starts a new document.  With beta * |k|^2 <= 2 the state stays bounded; the
  * rule itself diverges beyond.  Values have to be finite: a NaN or an infinity in q,
- * k, v, beta or h0 may reach every output of its head from the start of its chunk
+ * k, v, g, beta or h0 (but for a g of minus infinity) may reach every output of its head from the start of its chunk
  * on, past new documents too.  0 <= batch, heads <= 65535.
  */
 int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_heads *k, const gemv_heads *v,

@@ -312,7 +312,7 @@ struct Walk {
   // exchanged within a team: the sums that each warp has of the others' blocks (1 KB each), and
   // twice the left operands of all four blocks
   static constexpr int kForeign = 4 - kBlocks, kSums = SPLIT * kForeign * 1024, kOperands = 4 * 1024,
-                       kTeam = kSums + 2 * kOperands;
+                       kFactors = 2 * kOperands + kSums, kTeam = kFactors + 16;
   static constexpr int kStages = 2 * kStage + TEAMS * kTeam <= 227 * 1024 ? 2 : 1;
   static constexpr int kExchange = kStages * kStage, kBytes = kExchange + TEAMS * kTeam;
   // Block `n` of a warp's kBlocks.
@@ -424,9 +424,11 @@ __device__ __forceinline__ void get_operand(const char *from, int block, FragA &
   rest[0] = w.x; rest[1] = w.y; rest[2] = w.z; rest[3] = w.w;
 }
 
-// S += a X for a left operand a of 16 steps and those steps' rows of X, from column `col` on.
+// S += a X for a left operand a of 16 steps and those steps' rows of X, from column `col` on;
+// `back` scales the product.
 template <bool F16, int DK, int N>
-__device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, const FragA &rest, uint32_t X, int step, int col) {
+__device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, const FragA &rest, float back, uint32_t X, int step,
+                                           int col) {
   constexpr int NB = N / 2 < 4 ? N / 2 : 4;
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -434,7 +436,16 @@ __device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, cons
     uint32_t x[NB][4];
 #pragma unroll
     for (int n = 0; n < NB; ++n) load_matrices_t(x[n], at_kn(X, DK + 8, step, col + (m + n) * 16, lane));
-    mma_split_inputs<F16>(&S[2 * m], big, rest, x);
+    if constexpr (F16) {
+      FragC c[2 * NB] = {};
+      mma_split_inputs<F16>(c, big, rest, x);
+#pragma unroll
+      for (int n = 0; n < 2 * NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[2 * m + n][e] = fmaf(c[n][e], back, S[2 * m + n][e]);
+    } else {
+      mma_split_inputs<F16>(&S[2 * m], big, rest, x);
+    }
   }
 }
 
@@ -450,6 +461,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
   // (sums serves K S and O in turn: the one is read before the second wait, the other written after it)
   char *const sums = smem + L::kExchange + team * L::kTeam, *const solved = sums + L::kSums,
        *const update = solved + L::kOperands;
+  float *const factors = reinterpret_cast<float *>(sums + L::kFactors);  // of update's blocks
   auto request = [&](int i) {
     if (i < p.chunks) {
       const int chunk = BACK ? p.chunks - 1 - i : i, t0 = chunk * kDeltaChunk;
@@ -532,10 +544,17 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       }
       // products of the state's part with K, and with Q for the output
       FragC r[8] = {}, o[8] = {};
+      Scale scale = {1.f, 1.f};
+      if constexpr (F16) {
+        float top = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) top = largest(top, S[n]);
+        scale = scale_for(top);
+      }
 #pragma unroll
       for (int s = 0; s < N / 2; ++s) {
         FragA big, rest;
-        split_sums(S[2 * s], S[2 * s + 1], big, rest);
+        split_sums_for<F16>(S[2 * s], S[2 * s + 1], scale, big, rest);
         uint32_t x[4][4], y[4][4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) load_matrices(x[n], at_nk(K, DK + 8, n * 16, col0 + s * 16, lane));
@@ -545,6 +564,15 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         }
         mma_split_inputs<F16>(r, big, rest, x);
         if constexpr (MODE == kWalkOut) mma_split_inputs<F16>(o, big, rest, y);
+      }
+      if constexpr (F16) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            r[n][e] *= scale.back;
+            if (MODE == kWalkOut) o[n][e] *= scale.back;
+          }
       }
       give(sums, r);
       team_sync<SPLIT>(team);
@@ -652,7 +680,12 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
           scale_steps(c1, make_float2(-f1.x, -f1.y));
         }
         FragA big, rest;
-        split_sums(c0, c1, big, rest);
+        Scale factor = {1.f, 1.f};
+        if constexpr (F16) {
+          factor = scale_for(largest(largest(0.f, c0), c1));
+          if (lane == 0) factors[n] = factor.back;
+        }
+        split_sums_for<F16>(c0, c1, factor, big, rest);
         put_operand(update, n, big, rest);
       }
       const float whole = gates[kFirst + kDeltaChunk - 1];
@@ -665,15 +698,21 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         for (int s = 0; s < 4; ++s) {
           FragA a, big, rest;
           load_matrices_t(a, at_km(V, L::kNarrow, s * 16, team * 16, lane));
+          FragC c[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // scaled by step: the left operand's columns
             const float2 first = pair(kFirst, 2 * s + h);
             const float2 lo = unpack_input<F16>(a[2 * h]), hi = unpack_input<F16>(a[2 * h + 1]);
             const float x = p.scale * first.x, y = p.scale * first.y;
-            split(lo.x * x, lo.y * y, big[2 * h], rest[2 * h]);
-            split(hi.x * x, hi.y * y, big[2 * h + 1], rest[2 * h + 1]);
+            c[h][0] = lo.x * x;
+            c[h][1] = lo.y * y;
+            c[h][2] = hi.x * x;
+            c[h][3] = hi.y * y;
           }
-          state_plus<F16, DK>(S, big, rest, Q, s * 16, col0);
+          Scale factor = {1.f, 1.f};
+          if constexpr (F16) factor = scale_for(largest(largest(0.f, c[0]), c[1]));
+          split_sums_for<F16>(c[0], c[1], factor, big, rest);
+          state_plus<F16, DK>(S, big, rest, factor.back, Q, s * 16, col0);
         }
       }
       team_sync<SPLIT>(team);
@@ -689,7 +728,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       for (int s = 0; s < 4; ++s) {
         FragA big, rest;
         get_operand(update, s, big, rest);
-        state_plus<F16, DK>(S, big, rest, K, s * 16, col0);
+        state_plus<F16, DK>(S, big, rest, F16 ? factors[s] : 1.f, K, s * 16, col0);
       }
     }
     __syncthreads();

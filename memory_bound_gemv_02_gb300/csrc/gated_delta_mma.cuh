@@ -138,41 +138,54 @@ __device__ __forceinline__ void mma_input_split(FragC &c0, FragC &c1, const Frag
   }
 }
 
-// The same for NB blocks at once, so that a product does not wait for the one before.
+// In the walks a left operand that was computed meets fp16 inputs as two fp16 (two
+// products instead of three, and nothing to convert of the inputs): scaled by a power of two
+// so that the largest of the warp's is 2^8 to 2^9, the products scaled back.  What is below 2^-33 of the largest is lost.
+struct Scale {
+  float to, back;
+};
+__device__ __forceinline__ Scale scale_for(float top) {  // the largest magnitude of the lane's values
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+  int e = __float_as_int(top) >> 23;
+  e = e < 9 ? 9 : e > 254 ? 254 : e;
+  return {__int_as_float((262 - e) << 23), __int_as_float((e - 8) << 23)};
+}
+__device__ __forceinline__ float largest(float top, const FragC &c) {
+  return fmaxf(fmaxf(top, fmaxf(fabsf(c[0]), fabsf(c[1]))), fmaxf(fabsf(c[2]), fabsf(c[3])));
+}
+template <bool F16>
+__device__ __forceinline__ void split_for(float a, float b, const Scale &s, uint32_t &big, uint32_t &rest) {
+  if constexpr (F16) {
+    a *= s.to;
+    b *= s.to;
+    big = Elem<GEMV_TYPE_F16>::pair(a, b);
+    const float2 f = unpack_input<true>(big);
+    rest = Elem<GEMV_TYPE_F16>::pair(a - f.x, b - f.y);
+  } else {
+    split(a, b, big, rest);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ void split_sums_for(const FragC &c0, const FragC &c1, const Scale &s, FragA &big, FragA &rest) {
+  split_for<F16>(c0[0], c0[1], s, big[0], rest[0]);
+  split_for<F16>(c0[2], c0[3], s, big[1], rest[1]);
+  split_for<F16>(c1[0], c1[1], s, big[2], rest[2]);
+  split_for<F16>(c1[2], c1[3], s, big[3], rest[3]);
+}
+
+// c += (big + rest) B for NB blocks at once, so that a product does not wait for the one before.
 template <bool F16, int NB>
 __device__ __forceinline__ void mma_split_inputs(FragC *c, const FragA &big, const FragA &rest, const uint32_t (&b)[NB][4]) {
-  if constexpr (F16) {
-    uint32_t h[NB][4], l[NB][4];
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+  for (int n = 0; n < NB; ++n) {
+    mma_inputs<F16>(c[2 * n], big, b[n][0], b[n][1]);
+    mma_inputs<F16>(c[2 * n + 1], big, b[n][2], b[n][3]);
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) split_half(b[n][i], h[n][i], l[n][i]);
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      mma_bf16(c[2 * n], big, h[n][0], h[n][1]);
-      mma_bf16(c[2 * n + 1], big, h[n][2], h[n][3]);
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      mma_bf16(c[2 * n], rest, h[n][0], h[n][1]);
-      mma_bf16(c[2 * n + 1], rest, h[n][2], h[n][3]);
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      mma_bf16(c[2 * n], big, l[n][0], l[n][1]);
-      mma_bf16(c[2 * n + 1], big, l[n][2], l[n][3]);
-    }
-  } else {
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      mma_bf16(c[2 * n], big, b[n][0], b[n][1]);
-      mma_bf16(c[2 * n + 1], big, b[n][2], b[n][3]);
-    }
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      mma_bf16(c[2 * n], rest, b[n][0], b[n][1]);
-      mma_bf16(c[2 * n + 1], rest, b[n][2], b[n][3]);
-    }
+  for (int n = 0; n < NB; ++n) {
+    mma_inputs<F16>(c[2 * n], rest, b[n][0], b[n][1]);
+    mma_inputs<F16>(c[2 * n + 1], rest, b[n][2], b[n][3]);
   }
 }
 

@@ -133,6 +133,47 @@ def test_strong_and_absent_decays(cuda_dev, steps):
         check_backward(x, h0, do, dstate, run_back(x, do, h0, dstate), f"g = {level}")
 
 
+@pytest.mark.parametrize("heads", [1, 24])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size", [1e6, 1e-6, 1e30, 0.0])
+def test_states_beyond_their_inputs_range(cuda_dev, heads, dtype, size):
+    """States (and gradients of the last) far above and below what fp16 holds; beta
+    of 0 leaves v out where it would be lost beside them."""
+    x, h0, do, dstate = make(cuda_dev, 1, 140, heads, heads, 64, 48, dtype)
+    h0, dstate = h0 * size, dstate * size
+    x["scale"] = min(1.0, 0.1 / size) if size else 1.0  # o within its type
+    o, state = run(x, h0)
+    check_forward(x, h0, o, state)
+    x["scale"] = min(x["scale"], 1e-3)
+    do = do * min(1.0, 1e3 * size) if size < 1 else do
+    x["v"].zero_()
+    dv_scale = 1.0 if size <= 1e3 else 1e3 / size  # dv and dk within theirs
+    got = run_back(x, do, h0 * dv_scale, dstate * dv_scale)
+    check_backward(x, h0 * dv_scale, do, dstate * dv_scale, got)
+
+
+def test_heads_do_not_meet(cuda_dev):
+    """A NaN in one head's v leaves the other heads' bits as they were, and what is not
+    a step of the call is not read."""
+    x, h0, do, dstate = make(cuda_dev, 2, 150, 2, 4, 64, 64, BF16)
+    want = (*run(x, h0), *run_back(x, do, h0, dstate))
+    y = {**x, "v": x["v"].clone()}
+    y["v"][1, 70, 2] = float("nan")
+    got = (*run(y, h0), *run_back(y, do, h0, dstate))
+    for i, heads in ((0, 4), (1, 4), (4, 4), (5, 4), (6, 4), (7, 4)):  # o, state, dv, dg, dbeta, dh0
+        a, b = (t[i] if i in (1, 7) else t[i].transpose(1, 2) for t in (got, want))
+        keep = torch.ones((2, heads), dtype=torch.bool, device=cuda_dev)
+        keep[1, 2] = False
+        assert torch.equal(a[keep], b[keep]), i
+    long = torch.full((2, 200, 2 * 128 + 256), float("nan"), dtype=BF16, device=cuda_dev)
+    for n, at, heads in (("q", 0, 2), ("k", 128, 2), ("v", 256, 4)):
+        part = long[:, :150, at:at + heads * 64].unflatten(2, (heads, 64))
+        part.copy_(x[n])
+        y[n] = part
+    got = (*run(y, h0), *run_back(y, do, h0, dstate))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("steps", [30, 200])
 def test_gates_at_their_ends(cuda_dev, steps):
     """beta of 0 (nothing written; its gradient is there), 1 with equal keys, and 2."""
