@@ -303,7 +303,10 @@ enum { kWalkOut = 0, kWalkKeep = 1 };  // gated_delta(); the gradient's two walk
 // products otherwise.
 template <int DK, int TEAMS, int SPLIT>
 struct Walk {
-  static constexpr int kThreads = TEAMS * SPLIT * 32, kSlice = TEAMS * 16, kColumns = DK / SPLIT, kTiles = kColumns / 8,
+  // Teams of four leave registers for as many threads again, that copy while the others compute.
+  static constexpr bool kCopiers = SPLIT == 4;
+  static constexpr int kWalkers = TEAMS * SPLIT * 32, kCopying = kCopiers ? 128 : kWalkers,
+                       kThreads = kWalkers + (kCopiers ? kCopying : 0), kSlice = TEAMS * 16, kColumns = DK / SPLIT, kTiles = kColumns / 8,
                        kBlocks = 4 / SPLIT;  // of 16 steps, per warp
   static constexpr int kWide = kDeltaChunk * (DK + 8) * 2, kNarrow = kSlice + 8;
   // a stage
@@ -462,19 +465,19 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
   char *const sums = smem + L::kExchange + team * L::kTeam, *const solved = sums + L::kSums,
        *const update = solved + L::kOperands;
   float *const factors = reinterpret_cast<float *>(sums + L::kFactors);  // of update's blocks
+  const int tid = L::kCopiers ? (int)threadIdx.x - L::kWalkers : (int)threadIdx.x;
   auto request = [&](int i) {
     if (i < p.chunks) {
       const int chunk = BACK ? p.chunks - 1 - i : i, t0 = chunk * kDeltaChunk;
       const uint32_t at = smem_u32(smem + i % L::kStages * L::kStage);
       const char *const record = p.records + (bh * p.chunks + chunk) * kRecordBytes;
       const uint16_t *const m = reinterpret_cast<const uint16_t *>(record);
-      copy_tile<DK, L::kThreads>(at + L::kK, p.tk, b, head_k, t0, p.steps, 0);
-      if (BACK || MODE == kWalkOut) copy_tile<DK, L::kThreads>(at + L::kQ, p.tq, b, head_k, t0, p.steps, 0);
-      copy_tile<L::kSlice, L::kThreads>(at + L::kV, BACK ? p.td : p.tv, b, head, t0, p.steps, slice * L::kSlice);
-      copy_lower<L::kThreads>(at + L::kT, m);
-      if (BACK || MODE == kWalkOut) copy_lower<L::kThreads>(at + L::kP, m + 2 * kMatrix);
-      if (threadIdx.x < 3 * kDeltaChunk / 4)
-        copy16(at + L::kGates + threadIdx.x * 16, record + kRecordHalfs * 2 + threadIdx.x * 16, true);
+      copy_tile<DK, L::kCopying>(at + L::kK, p.tk, b, head_k, t0, p.steps, 0, tid);
+      if (BACK || MODE == kWalkOut) copy_tile<DK, L::kCopying>(at + L::kQ, p.tq, b, head_k, t0, p.steps, 0, tid);
+      copy_tile<L::kSlice, L::kCopying>(at + L::kV, BACK ? p.td : p.tv, b, head, t0, p.steps, slice * L::kSlice, tid);
+      copy_lower<L::kCopying>(at + L::kT, m, tid);
+      if (BACK || MODE == kWalkOut) copy_lower<L::kCopying>(at + L::kP, m + 2 * kMatrix, tid);
+      if (tid < 3 * kDeltaChunk / 4) copy16(at + L::kGates + tid * 16, record + kRecordHalfs * 2 + tid * 16, true);
     }
     copies_close();
   };
@@ -514,17 +517,32 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       }
     }
   };
-  FragC S[N];
   wait_for_predecessor();
-  if (L::kStages == 2) request(0);
+  if (L::kCopiers && tid >= 0) {
+    // a stage ahead where there are two, else between the chunks
+    if (L::kStages == 2) request(0);
+    for (int i = 0; i < p.chunks; ++i) {
+      if (L::kStages == 1) request(i);
+      copies_wait<0>();
+      __syncthreads();
+      if (L::kStages == 2) request(i + 1);
+      __syncthreads();
+    }
+    copies_wait<0>();
+    return;
+  }
+  FragC S[N];
+  if (!L::kCopiers && L::kStages == 2) request(0);
   {
     const float *const from = BACK ? p.dstate : p.h0;
     load_state<N>(from ? from + bh * cells : nullptr, p.dk_size, p.dv_size, row0, col0, S);
   }
   const bool live = MODE == kWalkKeep || row0 < p.dv_size;  // (without columns a team only copies, or keeps zeros)
   for (int i = 0; i < p.chunks; ++i) {
-    request(L::kStages == 2 ? i + 1 : i);
-    copies_wait<L::kStages - 1>();
+    if (!L::kCopiers) {
+      request(L::kStages == 2 ? i + 1 : i);
+      copies_wait<L::kStages - 1>();
+    }
     __syncthreads();
     const int chunk = BACK ? p.chunks - 1 - i : i, t0 = chunk * kDeltaChunk;
     char *const stage = smem + i % L::kStages * L::kStage;
@@ -738,14 +756,14 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
 }
 
 template <bool F16, int DK, int TEAMS, int SPLIT>
-__global__ void __launch_bounds__(TEAMS * SPLIT * 32, 1) delta_walk_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(Walk<DK, TEAMS, SPLIT>::kThreads, 1) delta_walk_kernel(const DeltaParams p) {
   extern __shared__ __align__(16) char smem[];
   walk<F16, DK, TEAMS, SPLIT, kWalkOut, false>(p, smem, blockIdx.z, blockIdx.y, blockIdx.x);
 }
 
 // The gradient's two walks: columns of v backward in the first half of the grid, forward in the second.
 template <bool F16, int DK, int TEAMS, int SPLIT>
-__global__ void __launch_bounds__(TEAMS * SPLIT * 32, 1) delta_walks_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(Walk<DK, TEAMS, SPLIT>::kThreads, 1) delta_walks_kernel(const DeltaParams p) {
   extern __shared__ __align__(16) char smem[];
   const int slices = gridDim.x / 2, slice = blockIdx.x % slices;
   if ((int)blockIdx.x < slices) walk<F16, DK, TEAMS, SPLIT, kWalkKeep, true>(p, smem, blockIdx.z, blockIdx.y, slice);

@@ -233,10 +233,10 @@ __device__ __forceinline__ void copies_wait() {
 // column, to rows of COLS + 8 elements.
 template <int COLS, int THREADS>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const TileSource &s, int64_t b, int64_t head, int64_t t0, int steps,
-                                          int col) {
+                                          int col, int tid = (int)threadIdx.x) {
   constexpr int UNITS = COLS / 8, ROWS = THREADS / UNITS;  // rows that a round takes
   static_assert(THREADS % UNITS == 0 && kDeltaChunk % (ROWS < kDeltaChunk ? ROWS : kDeltaChunk) == 0, "whole rows");
-  const int r0 = (int)threadIdx.x / UNITS, u = (int)threadIdx.x % UNITS;
+  const int r0 = tid / UNITS, u = tid % UNITS;
   const uint16_t *from = s.p + b * s.batch + head * s.head + (t0 + r0) * s.step + col + u * 8;
   const int64_t next = ROWS * s.step;
   uint32_t to = dst + (uint32_t)(r0 * (COLS + 8) + u * 8) * 2;
@@ -266,10 +266,10 @@ __device__ __forceinline__ uint32_t kept_km(uint32_t base, int k, int m, int lan
 // The 16 x 16 blocks on and below the diagonal of two 64 x 64 matrices, dense, to rows
 // of 72.
 template <int THREADS>
-__device__ __forceinline__ void copy_lower(uint32_t dst, const uint16_t *src) {
+__device__ __forceinline__ void copy_lower(uint32_t dst, const uint16_t *src, int tid) {
 #pragma unroll
   for (int i = 0; i < 2 * kMatrix / 8 / THREADS; ++i) {
-    const int at = i * THREADS + (int)threadIdx.x, row = at / 8, u = at % 8;
+    const int at = i * THREADS + tid, row = at / 8, u = at % 8;
     if (u / 2 <= row % 64 / 16) copy16(dst + (uint32_t)(row * (kDeltaChunk + 8) + u * 8) * 2, src + at * 8, true);
   }
 }
