@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
 
 enum { kWalkOut = 0, kWalkKeep = 1 };  // gated_delta(); the gradient's two walks
 
-// (8 heads of 128 x 128, 1024 steps bf16: 2.6 us a chunk by teams of four warps, 4.9 by one warp
-// alone.)  A CTA's walk: TEAMS teams of SPLIT warps, each with 16 columns of v (rows of S^T); a
+// (8 heads of 128 x 128, 1024 steps bf16: 2.2 us a chunk by teams of four warps, copies by warps of
+// their own; 2.6 with the copies among them, 4.9 by one warp alone.)  A CTA's walk: TEAMS teams of SPLIT warps, each with 16 columns of v (rows of S^T); a
 // team's warps have DK / SPLIT columns of S^T each, so products with the state are sums over the
 // team, and what is solved for is solved in blocks of 16 steps, dealt so that the
 // triangles' work evens out.  Two warps to a scheduler are wanted as one waits for its own
@@ -798,16 +798,16 @@ int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t str
                               dim3((unsigned)p.chunks, (unsigned)p.heads_k, (unsigned)p.batch), kPrepareThreads,
                               Prepare<DK>::kBytes, stream, p);
   if (st != GEMV_OK) return st;
-  // Few heads: a team of four warps per CTA while there is one CTA per SM, or two in the
-  // gradient, whose chains wait for memory as well.  More: the tensor walk where there is one; but
-  // in the gradient wider CTAs while they fill the GPU once.  1024 steps, 128 x 128 bf16, forward
-  // (us) teams / tensor / wide, 8 heads 47 / 65 / 78, 16 47 / 65 / 79, 20 84 / 67 / 80, 64 165 / 80 / 91,
-  // 128 288 / 110 / 173; gradient 8 heads 74 / 115 / 113, 16 135 / 150 / 142, 20 170 / 176 / 168,
-  // 32 232 / 204 / 194, 64 409 / 325 / 349.
+  // Few heads: a team of four warps per CTA while each has an SM; without a tensor walk to go to,
+  // forward, up to two a SM.  More: the tensor walk where there is one, but in the gradient
+  // wider CTAs while they fill the GPU once.  1024 steps, 128 x 128 bf16, forward (us) teams / tensor /
+  // wide, 8 heads 40 / 66 / 78, 16 40 / 66 / 78, 20 70 / 67 / 81, 32 72 / 69 / 82, 64 139 / 84 / 90, 128 243 / 105 / 174;
+  // gradient 8 heads 67 / 112 / 110, 16 121 / 145 / 134, 20 156 / 169 / 158, 32 212 / 201 / 182, 64 372 / 297 / 329.
   const int64_t heads = (int64_t)p.batch * p.heads, walks = gradient ? 2 : 1;
-  if (heads * ((p.dv_size + 15) / 16) <= sms) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);
+  const bool tensor = !F16 && DK == 128 && p.dv_size > 64;
+  if (heads * ((p.dv_size + 15) / 16) <= (tensor || gradient ? sms : 2 * sms)) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);
   const bool once = heads * walks * ((p.dv_size + kDeltaSlice - 1) / kDeltaSlice) <= sms;
-  if (!F16 && DK == 128 && p.dv_size > 64 && !(gradient && once)) return launch_delta_tensor(p, gradient, stream);
+  if (tensor && !(gradient && once)) return launch_delta_tensor(p, gradient, stream);
   return launch_walk<F16, DK, 4, 2>(p, gradient, stream);
 }
 

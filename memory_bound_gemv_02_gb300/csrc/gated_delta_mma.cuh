@@ -2,11 +2,11 @@
 // fp32 sums, their operands from shared memory or from sums just made.
 //
 // A sum is fed on as two bf16 that add up to it within 2^-17 (its fragment layout
-// is that of the next product's left operand, so it never leaves the registers); an
-// fp16 input becomes two bf16 exactly.  Products of the two small parts are left out:
-// they are 2^-16 of the whole.  Why not tcgen05: a chain's products are 16 x 64 x 64
-// to 16 x 128 x 64 per warp, each needing the one before at once; through tensor
-// memory every one of them would be written, waited for and read back.
+// is that of the next product's left operand, so it never leaves the registers); beside
+// fp16 inputs as two scaled fp16, or the input becomes two bf16 exactly.  Products of two
+// small parts are left out: they are 2^-16 of the whole.  Why not tcgen05 throughout: where heads are few a
+// chain's products are 16 x 64 x 64 to 16 x 128 x 64 per warp, each needing the one before at once;
+// through tensor memory each takes some 400 cycles of issue, commit and wake besides.
 #pragma once
 
 #include <cuda_fp16.h>
