@@ -231,7 +231,8 @@ int gated_scan_backward(const void *dh, int64_t dh_batch, int64_t dh_step, const
  *
  * Rows whose squares leave fp32's range are scaled first, so every row of finite s
  * gets its norm.  A row that holds a NaN or an infinity gives NaN throughout; a row
- * of equal values with eps == 0 is 0 / 0.  rows == 0 or d == 0 launches nothing.
+ * of equal values with eps == 0 is 0 / 0.  rows == 0 or d == 0 launches nothing (mean
+ * and rstd are not written).
  * Any alignment and stride work; 16-byte aligned rows take 16-byte accesses.
  */
 int layer_norm_fused(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
@@ -318,7 +319,8 @@ typedef struct gated_delta_shape {
  * range) starts a new document.  With beta * |k|^2 <= 2 the state stays bounded; the
  * rule itself diverges beyond.  Values have to be finite: a NaN or an infinity in q,
  * k, v, g, beta or h0 (but for a g of minus infinity) may reach every output of its head from the start of its chunk
- * on, past new documents too.  0 <= batch, heads <= 65535.
+ * on, past new documents too.  0 <= batch, heads <= 65535.  Where dk is 0 there is no
+ * state and o is an empty sum, zeros.
  */
 int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_heads *k, const gemv_heads *v,
                 const gemv_heads *g, const gemv_heads *beta, const float *h0, const gemv_heads *o, float *state,
@@ -330,7 +332,9 @@ int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_
  * types of what they belong to, those of shared heads of q and k summed over the
  * heads that share them; dg is 0 where a new document starts.  dh0: fp32, dense, or
  * NULL; may be dstate itself.  steps == 0 copies dstate (or 0) to it.  An input
- * shared along a stride of 0 gets one gradient per use.
+ * shared along a stride of 0 gets one gradient per use.  Without keys (dk 0), values
+ * (dv 0) or heads of v the gradients that have elements are empty sums, zeros (a null
+ * pointer leaves one out).
  *
  * The forward pass leaves nothing behind for it: states and corrections are computed
  * again from the inputs, chunk by chunk, and kept in `workspace`

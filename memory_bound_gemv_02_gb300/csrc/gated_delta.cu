@@ -224,7 +224,23 @@ __global__ void __launch_bounds__(256) delta_pack_kernel(const PackParams p) {
   }
 }
 
+// A thread per element: calls without a head, key or value are no path of their own.
+__global__ void __launch_bounds__(256) delta_zero_kernel(const ZeroParams p) {
+  wait_for_predecessor();
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.cells; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / p.size, t = row / p.heads % p.steps, b = row / p.heads / p.steps;
+    const int64_t at = b * p.to.batch + t * p.to.step + row % p.heads * p.to.head + i % p.size;
+    if (p.bytes == 4) static_cast<uint32_t *>(const_cast<void *>(p.to.p))[at] = 0;
+    else static_cast<uint16_t *>(const_cast<void *>(p.to.p))[at] = 0;
+  }
+}
+
 }  // namespace
+
+int launch_delta_zero(const ZeroParams &p, cudaStream_t stream) {
+  const int64_t ctas = (p.cells + 255) / 256;
+  return launch_op(delta_zero_kernel, dim3((unsigned)(ctas < 8192 ? ctas : 8192)), 256, 0, 1, stream, p);
+}
 
 int launch_delta_steps(const DeltaParams &p, int sms, cudaStream_t stream) {
   return p.f16 ? launch_steps<GEMV_TYPE_F16>(p, sms, stream) : launch_steps<GEMV_TYPE_BF16>(p, sms, stream);
@@ -246,9 +262,10 @@ int padded_dk(int64_t dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }
 
 bool shape_ok(const gated_delta_shape &s) {
   if (s.batch < 0 || s.steps < 0 || s.heads < 0 || s.heads_k < 0 || s.dk < 0 || s.dv < 0) return false;
-  if (s.batch > 65535 || s.heads > 65535 || s.steps > INT32_MAX / 2 || s.dk > kDeltaMostDk || s.dv > (1 << 20)) return false;
+  const int64_t heads = s.heads > s.heads_k ? s.heads : s.heads_k;
+  if (s.batch > 65535 || heads > 65535 || s.steps > INT32_MAX / 2 || s.dk > kDeltaMostDk || s.dv > (1 << 20)) return false;
   if (s.heads > 0 && (s.heads_k == 0 || s.heads % s.heads_k != 0)) return false;
-  if (s.batch * s.heads > INT32_MAX / ((s.steps + kDeltaChunk) / kDeltaChunk)) return false;  // chunks of all heads
+  if (s.batch * heads > INT32_MAX / ((s.steps + kDeltaChunk) / kDeltaChunk)) return false;  // chunks of all heads
   return !(s.scale != s.scale);
 }
 
@@ -425,6 +442,37 @@ bool overlap(const Operand &a, const Operand &b, const gated_delta_shape &s) {
 }
 Rows span_of(const Operand &o, const gated_delta_shape &s) { return span_of(*o.h, s.batch, s.steps, o.heads, o.size, o.es); }
 
+// A call without heads, keys or values (there is no state then): the outputs that still have
+// elements are empty sums.  Null ones are left out.
+int write_zeros(const gated_delta_shape &s, std::initializer_list<Operand> outs, std::initializer_list<Operand> ins,
+                cudaStream_t stream) {
+  auto cells = [&](const Operand &o) { return o.h->p ? s.batch * s.steps * o.heads * o.size : 0; };
+  int st, dev = -1, sms = 0;
+  bool any = false;
+  for (const Operand &o : outs) {
+    if (cells(o) == 0) continue;
+    if ((st = check_operand(o, s, true)) != GEMV_OK) return st;
+    for (const Operand &i : ins) {
+      if (cells(i) == 0) continue;
+      if ((st = check_operand(i, s, false)) != GEMV_OK) return st;
+      if (overlap(o, i, s)) return GEMV_ERR_ALIAS;
+    }
+    for (const Operand &other : outs)
+      if (&other != &o && cells(other) > 0 && overlap(o, other, s)) return GEMV_ERR_ALIAS;
+    any = true;
+  }
+  if (!any) return GEMV_OK;
+  if ((st = current_device(&dev, &sms)) != GEMV_OK) return st;
+  for (const Operand &o : outs)
+    if (cells(o) > 0 && !on_device(dev, {o.h->p})) return GEMV_ERR_DEVICE;
+  for (const Operand &o : outs) {
+    if (cells(o) == 0) continue;
+    const ZeroParams z = {heads_of(o.h), s.steps, o.heads, o.size, cells(o), o.es};
+    if ((st = launch_delta_zero(z, stream)) != GEMV_OK) return st;
+  }
+  return GEMV_OK;
+}
+
 }  // namespace
 }  // namespace gemvk
 
@@ -452,11 +500,11 @@ extern "C" int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, 
   int st = check_types(s);
   if (st != GEMV_OK) return st;
   if (!shape_ok(s)) return GEMV_ERR_ARG;
-  if (empty(s)) return GEMV_OK;
   const int ge = type_bytes(s.gate_dtype);
   const Operand in[] = {{q, s.heads_k, s.dk, 2}, {k, s.heads_k, s.dk, 2}, {v, s.heads, s.dv, 2}, {g, s.heads, 1, ge},
                         {beta, s.heads, 1, ge}};
   const Operand out = {o, s.heads, s.dv, 2};
+  if (empty(s)) return write_zeros(s, {out}, {in[0], in[1], in[2], in[3], in[4]}, stream);
   const int64_t cells = s.batch * s.heads * s.dk * s.dv;
   if (((uintptr_t)h0 | (uintptr_t)state) % 4u) return GEMV_ERR_ALIGN;
   const Rows H0{h0, 1, cells * 4, cells * 4}, S{state, 1, cells * 4, cells * 4};
@@ -511,12 +559,12 @@ extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_h
   int st = check_types(s);
   if (st != GEMV_OK) return st;
   if (!shape_ok(s)) return GEMV_ERR_ARG;
-  if (empty(s)) return GEMV_OK;
   const int ge = type_bytes(s.gate_dtype);
   const Operand in[] = {{d_o, s.heads, s.dv, 2}, {q, s.heads_k, s.dk, 2}, {k, s.heads_k, s.dk, 2}, {v, s.heads, s.dv, 2},
                         {g, s.heads, 1, ge}, {beta, s.heads, 1, ge}};
   const Operand out[] = {{dq, s.heads_k, s.dk, 2}, {dk, s.heads_k, s.dk, 2}, {dv, s.heads, s.dv, 2}, {dg, s.heads, 1, ge},
                          {dbeta, s.heads, 1, ge}};
+  if (empty(s)) return write_zeros(s, {out[0], out[1], out[2], out[3], out[4]}, {in[0], in[1], in[2], in[3], in[4], in[5]}, stream);
   const int64_t cells = s.batch * s.heads * s.dk * s.dv;
   if (((uintptr_t)h0 | (uintptr_t)dstate | (uintptr_t)dh0) % 4u) return GEMV_ERR_ALIGN;
   const Rows H0{h0, 1, cells * 4, cells * 4}, DS{dstate, 1, cells * 4, cells * 4}, D0{dh0, 1, cells * 4, cells * 4};

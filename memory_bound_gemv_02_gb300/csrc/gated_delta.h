@@ -72,7 +72,15 @@ struct PackParams {
   int64_t rows;  // batch * heads * steps
 };
 
+// An output that is an empty sum.
+struct ZeroParams {
+  HeadsOf to;
+  int64_t steps, heads, size, cells;
+  int32_t bytes;  // of an element
+};
+
 int launch_delta_steps(const DeltaParams &p, int sms, cudaStream_t stream);
+int launch_delta_zero(const ZeroParams &p, cudaStream_t stream);
 int launch_delta_pack(const PackParams &p, cudaStream_t stream);
 // The chunks' matrices and the walk over them, or (gradient) the gradient's two walks.
 int launch_delta_chunks_f16(const DeltaParams &p, int dk_padded, bool gradient, int sms, cudaStream_t stream);
