@@ -311,9 +311,11 @@ typedef struct gated_delta_shape {
  *
  * Up to 12 steps are walked one by one in fp32, by one kernel.  Longer sequences are
  * cut into chunks of 64 steps, whose products run on the tensor cores by two
- * kernels, the state and what comes from it as sums of two bf16, or of two scaled
- * fp16 beside fp16 inputs (products within 2^-16 of their terms).  Operands whose
- * rows are not on 16 bytes are copied first, one kernel each.
+ * kernels, the state and what comes from it as sums of two bf16 (within 2^-17), or of
+ * two scaled fp16 beside fp16 inputs (within 2^-22, or 2^-34 of the largest of their
+ * column of v), with fp32 sums; the product of two remainders is left out (2^-16).  Columns of v never
+ * meet: an error is small against its own column.  Operands whose rows are not on 16
+ * bytes are copied first, one kernel each.
  *
  * A g of minus infinity (or below -87.3, where the exponential leaves fp32's normal
  * range) starts a new document.  With beta * |k|^2 <= 2 the state stays bounded; the

@@ -315,7 +315,7 @@ struct Walk {
   // exchanged within a team: the sums that each warp has of the others' blocks (1 KB each), and
   // twice the left operands of all four blocks
   static constexpr int kForeign = 4 - kBlocks, kSums = SPLIT * kForeign * 1024, kOperands = 4 * 1024,
-                       kFactors = 2 * kOperands + kSums, kTeam = kFactors + 16;
+                       kFactors = 2 * kOperands + kSums, kTeam = kFactors + 4 * 16 * 4;
   static constexpr int kStages = 2 * kStage + TEAMS * kTeam <= 227 * 1024 ? 2 : 1;
   static constexpr int kExchange = kStages * kStage, kBytes = kExchange + TEAMS * kTeam;
   // Block `n` of a warp's kBlocks.
@@ -428,10 +428,10 @@ __device__ __forceinline__ void get_operand(const char *from, int block, FragA &
 }
 
 // S += a X for a left operand a of 16 steps and those steps' rows of X, from column `col` on;
-// `back` scales the product.
+// back0 and back1 scale the product's rows lane / 4 and lane / 4 + 8.
 template <bool F16, int DK, int N>
-__device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, const FragA &rest, float back, uint32_t X, int step,
-                                           int col) {
+__device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, const FragA &rest, float back0, float back1, uint32_t X,
+                                           int step, int col) {
   constexpr int NB = N / 2 < 4 ? N / 2 : 4;
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -445,7 +445,7 @@ __device__ __forceinline__ void state_plus(FragC (&S)[N], const FragA &big, cons
 #pragma unroll
       for (int n = 0; n < 2 * NB; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[2 * m + n][e] = fmaf(c[n][e], back, S[2 * m + n][e]);
+        for (int e = 0; e < 4; ++e) S[2 * m + n][e] = fmaf(c[n][e], e < 2 ? back0 : back1, S[2 * m + n][e]);
     } else {
       mma_split_inputs<F16>(&S[2 * m], big, rest, x);
     }
@@ -464,7 +464,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
   // (sums serves K S and O in turn: the one is read before the second wait, the other written after it)
   char *const sums = smem + L::kExchange + team * L::kTeam, *const solved = sums + L::kSums,
        *const update = solved + L::kOperands;
-  float *const factors = reinterpret_cast<float *>(sums + L::kFactors);  // of update's blocks
+  float *const factors = reinterpret_cast<float *>(sums + L::kFactors);  // of update's blocks, 16 rows each
   const int tid = L::kCopiers ? (int)threadIdx.x - L::kWalkers : (int)threadIdx.x;
   auto request = [&](int i) {
     if (i < p.chunks) {
@@ -562,12 +562,15 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       }
       // products of the state's part with K, and with Q for the output
       FragC r[8] = {}, o[8] = {};
-      Scale scale = {1.f, 1.f};
+      Scale scale = no_scale();
       if constexpr (F16) {
-        float top = 0.f;
+        float top0 = 0.f, top1 = 0.f;
 #pragma unroll
-        for (int n = 0; n < N; ++n) top = largest(top, S[n]);
-        scale = scale_for(top);
+        for (int n = 0; n < N; ++n) {
+          top0 = largest(top0, S[n], 0);
+          top1 = largest(top1, S[n], 1);
+        }
+        scale = scale_for(top0, top1);
       }
 #pragma unroll
       for (int s = 0; s < N / 2; ++s) {
@@ -588,8 +591,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         for (int n = 0; n < 8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            r[n][e] *= scale.back;
-            if (MODE == kWalkOut) o[n][e] *= scale.back;
+            r[n][e] *= scale.back[e / 2];
+            if (MODE == kWalkOut) o[n][e] *= scale.back[e / 2];
           }
       }
       give(sums, r);
@@ -698,10 +701,13 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
           scale_steps(c1, make_float2(-f1.x, -f1.y));
         }
         FragA big, rest;
-        Scale factor = {1.f, 1.f};
+        Scale factor = no_scale();
         if constexpr (F16) {
-          factor = scale_for(largest(largest(0.f, c0), c1));
-          if (lane == 0) factors[n] = factor.back;
+          factor = scale_for(largest(largest(0.f, c0, 0), c1, 0), largest(largest(0.f, c0, 1), c1, 1));
+          if (lane % 4 == 0) {
+            factors[n * 16 + lane / 4] = factor.back[0];
+            factors[n * 16 + lane / 4 + 8] = factor.back[1];
+          }
         }
         split_sums_for<F16>(c0, c1, factor, big, rest);
         put_operand(update, n, big, rest);
@@ -727,10 +733,10 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
             c[h][2] = hi.x * x;
             c[h][3] = hi.y * y;
           }
-          Scale factor = {1.f, 1.f};
-          if constexpr (F16) factor = scale_for(largest(largest(0.f, c[0]), c[1]));
+          Scale factor = no_scale();
+          if constexpr (F16) factor = scale_for(largest(largest(0.f, c[0], 0), c[1], 0), largest(largest(0.f, c[0], 1), c[1], 1));
           split_sums_for<F16>(c[0], c[1], factor, big, rest);
-          state_plus<F16, DK>(S, big, rest, factor.back, Q, s * 16, col0);
+          state_plus<F16, DK>(S, big, rest, factor.back[0], factor.back[1], Q, s * 16, col0);
         }
       }
       team_sync<SPLIT>(team);
@@ -746,7 +752,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       for (int s = 0; s < 4; ++s) {
         FragA big, rest;
         get_operand(update, s, big, rest);
-        state_plus<F16, DK>(S, big, rest, F16 ? factors[s] : 1.f, K, s * 16, col0);
+        const float *const back = factors + s * 16 + lane / 4;
+        state_plus<F16, DK>(S, big, rest, F16 ? back[0] : 1.f, F16 ? back[8] : 1.f, K, s * 16, col0);
       }
     }
     __syncthreads();

@@ -139,26 +139,35 @@ __device__ __forceinline__ void mma_input_split(FragC &c0, FragC &c1, const Frag
 }
 
 // In the walks a left operand that was computed meets fp16 inputs as two fp16 (two
-// products instead of three, and nothing to convert of the inputs): scaled by a power of two
-// so that the largest of the warp's is 2^8 to 2^9, the products scaled back.  What is below 2^-33 of the largest is lost.
+// products instead of three, and nothing to convert of the inputs): each of its rows, a column of v,
+// scaled by a power of two so that the largest of the row here is 2^8 to 2^9, the products scaled
+// back.  What is below 2^-33 of that is lost; columns of v, which never meet, share no scale.
 struct Scale {
-  float to, back;
+  float to[2], back[2];  // of rows lane / 4 and lane / 4 + 8
 };
-__device__ __forceinline__ Scale scale_for(float top) {  // the largest magnitude of the lane's values
+__device__ __forceinline__ Scale scale_for(float top0, float top1) {  // the largest magnitudes of the lane's values in both rows
+  Scale s;
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-  int e = __float_as_int(top) >> 23;
-  e = e < 9 ? 9 : e > 254 ? 254 : e;
-  return {__int_as_float((262 - e) << 23), __int_as_float((e - 8) << 23)};
+  for (int h = 0; h < 2; ++h) {
+    float top = h == 0 ? top0 : top1;
+#pragma unroll
+    for (int m = 1; m < 4; m *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    int e = __float_as_int(top) >> 23;
+    e = e < 9 ? 9 : e > 254 ? 254 : e;
+    s.to[h] = __int_as_float((262 - e) << 23);
+    s.back[h] = __int_as_float((e - 8) << 23);
+  }
+  return s;
 }
-__device__ __forceinline__ float largest(float top, const FragC &c) {
-  return fmaxf(fmaxf(top, fmaxf(fabsf(c[0]), fabsf(c[1]))), fmaxf(fabsf(c[2]), fabsf(c[3])));
+__device__ __forceinline__ Scale no_scale() { return {{1.f, 1.f}, {1.f, 1.f}}; }
+__device__ __forceinline__ float largest(float top, const FragC &c, int h) {  // of row lane / 4 + 8 h
+  return fmaxf(top, fmaxf(fabsf(c[2 * h]), fabsf(c[2 * h + 1])));
 }
 template <bool F16>
-__device__ __forceinline__ void split_for(float a, float b, const Scale &s, uint32_t &big, uint32_t &rest) {
+__device__ __forceinline__ void split_for(float a, float b, float to, uint32_t &big, uint32_t &rest) {
   if constexpr (F16) {
-    a *= s.to;
-    b *= s.to;
+    a *= to;
+    b *= to;
     big = Elem<GEMV_TYPE_F16>::pair(a, b);
     const float2 f = unpack_input<true>(big);
     rest = Elem<GEMV_TYPE_F16>::pair(a - f.x, b - f.y);
@@ -168,10 +177,10 @@ __device__ __forceinline__ void split_for(float a, float b, const Scale &s, uint
 }
 template <bool F16>
 __device__ __forceinline__ void split_sums_for(const FragC &c0, const FragC &c1, const Scale &s, FragA &big, FragA &rest) {
-  split_for<F16>(c0[0], c0[1], s, big[0], rest[0]);
-  split_for<F16>(c0[2], c0[3], s, big[1], rest[1]);
-  split_for<F16>(c1[0], c1[1], s, big[2], rest[2]);
-  split_for<F16>(c1[2], c1[3], s, big[3], rest[3]);
+  split_for<F16>(c0[0], c0[1], s.to[0], big[0], rest[0]);
+  split_for<F16>(c0[2], c0[3], s.to[1], big[1], rest[1]);
+  split_for<F16>(c1[0], c1[1], s.to[0], big[2], rest[2]);
+  split_for<F16>(c1[2], c1[3], s.to[1], big[3], rest[3]);
 }
 
 // c += (big + rest) B for NB blocks at once, so that a product does not wait for the one before.
