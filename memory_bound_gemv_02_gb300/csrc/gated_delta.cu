@@ -16,16 +16,9 @@
 namespace gemvk {
 namespace {
 
-constexpr float kNoDecay = -87.3f;  // below it exp() leaves fp32's normal range: counts as 0
-
 template <int TYPE>
 __device__ __forceinline__ float element(const HeadsOf &h, int64_t b, int64_t t, int64_t head, int64_t i) {
   return Elem<TYPE>::get(static_cast<const typename Elem<TYPE>::raw *>(h.p)[b * h.batch + t * h.step + head * h.head + i]);
-}
-template <int TYPE>
-__device__ __forceinline__ float gate(const HeadsOf &h, bool f32, int64_t b, int64_t t, int64_t head) {
-  const int64_t at = b * h.batch + t * h.step + head * h.head;
-  return f32 ? static_cast<const float *>(h.p)[at] : Elem<TYPE>::get(static_cast<const uint16_t *>(h.p)[at]);
 }
 
 // A CTA holds the state's columns [32 CW s, 32 CW (s + 1)) of one head: RW rows per warp, CW
@@ -98,8 +91,8 @@ __global__ void __launch_bounds__(kDeltaMostDk / RW * 32) delta_steps_kernel(con
 #pragma unroll
       for (int c = 0; c < CW; ++c)
         if (there(c)) s.v[c] = element<TYPE>(p.v, b, t, head, col0 + local(c));
-      s.g = gate<TYPE>(p.g, p.gates_f32, b, t, head);
-      s.beta = gate<TYPE>(p.beta, p.gates_f32, b, t, head);
+      s.g = gate_at(p.g, p.gates_f32, TYPE == GEMV_TYPE_F16, b, t, head);
+      s.beta = gate_at(p.beta, p.gates_f32, TYPE == GEMV_TYPE_F16, b, t, head);
     }
     return s;
   };
@@ -601,7 +594,6 @@ extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_h
     return GEMV_ERR_DEVICE;
   DeltaParams p = {};
   if ((st = fill(p, dev, s, q, k, v, g, beta, h0)) != GEMV_OK) return st;
-  p.d_o = heads_of(d_o);
   p.dstate = dstate;
   p.dq = heads_of(dq); p.dk = heads_of(dk); p.dv = heads_of(dv); p.dg = heads_of(dg); p.dbeta = heads_of(dbeta);
   p.dh0 = dh0;

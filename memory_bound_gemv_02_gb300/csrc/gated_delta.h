@@ -15,12 +15,20 @@ namespace gemvk {
 constexpr int kDeltaChunk = 64;    // steps per chunk
 constexpr int kDeltaSlice = 64;    // columns of v per CTA of the chains
 constexpr int kDeltaMostDk = 256;
+constexpr float kNoDecay = -87.3f;  // below it exp() leaves fp32's normal range: counts as 0
 
 // (batch, steps, heads, size) elements with unit stride along size.
 struct HeadsOf {
   const void *p;
   int64_t batch, step, head;
 };
+
+__device__ __forceinline__ float gate_at(const HeadsOf &h, bool f32, bool f16, int64_t b, int64_t t, int64_t head) {
+  const int64_t at = b * h.batch + t * h.step + head * h.head;
+  if (f32) return static_cast<const float *>(h.p)[at];
+  const uint16_t v = static_cast<const uint16_t *>(h.p)[at];
+  return f16 ? Elem<GEMV_TYPE_F16>::get(v) : Elem<GEMV_TYPE_BF16>::get(v);
+}
 
 // The same, of 16-bit elements whose rows are copied 16 bytes at a time.
 struct TileSource {
@@ -40,7 +48,7 @@ constexpr int64_t kRecordHalfs = 4 * kMatrix;  // T, T's rest, P, P's rest
 constexpr int64_t kRecordBytes = kRecordHalfs * 2 + kGateFloats * 4;
 
 struct DeltaParams {
-  HeadsOf q, k, v, g, beta, d_o;
+  HeadsOf q, k, v, g, beta;
   TileSource tq, tk, tv, td;  // q, k, v, d_o for the chunk kernels
   const float *h0, *dstate;
   HeadsOf o, dq, dk, dv, dg, dbeta;  // outputs

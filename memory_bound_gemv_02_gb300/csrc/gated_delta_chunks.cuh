@@ -26,17 +26,7 @@
 namespace gemvk {
 namespace {
 
-constexpr float kNoDecay = -87.3f;
 constexpr int kPrepareThreads = 128;
-constexpr int kTilePitch = kDeltaChunk + 8;  // of 64 x 64 matrices in shared memory
-constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
-
-__device__ __forceinline__ float gate_at(const HeadsOf &h, bool f32, bool f16, int64_t b, int64_t t, int64_t head) {
-  const int64_t at = b * h.batch + t * h.step + head * h.head;
-  if (f32) return static_cast<const float *>(h.p)[at];
-  const uint16_t v = static_cast<const uint16_t *>(h.p)[at];
-  return f16 ? Elem<GEMV_TYPE_F16>::get(v) : Elem<GEMV_TYPE_BF16>::get(v);
-}
 
 // The gates of a chunk by one warp, two steps per lane.  Log decays (to base 2) are
 // summed in 64-bit fixed point, as a difference of two sums is wanted to fp32's
@@ -303,6 +293,7 @@ enum { kWalkOut = 0, kWalkKeep = 1 };  // gated_delta(); the gradient's two walk
 // products otherwise.
 template <int DK, int TEAMS, int SPLIT>
 struct Walk {
+  static_assert(SPLIT == 2 || SPLIT == 4, "how blocks are dealt");
   // Teams of four leave registers for as many threads again, that copy while the others compute.
   static constexpr bool kCopiers = SPLIT == 4;
   static constexpr int kWalkers = TEAMS * SPLIT * 32, kCopying = kCopiers ? 128 : kWalkers,
@@ -321,13 +312,11 @@ struct Walk {
   // Block `n` of a warp's kBlocks.
   static __device__ __forceinline__ int block(int part, int n) {
     if constexpr (SPLIT == 4) return part;
-    else if constexpr (SPLIT == 2) return n == 0 ? part : 3 - part;
-    else return n;
+    else return n == 0 ? part : 3 - part;
   }
   static __device__ __forceinline__ int owner(int block) {
     if constexpr (SPLIT == 4) return block;
-    else if constexpr (SPLIT == 2) return block < 2 ? block : 3 - block;
-    else return 0;
+    else return block < 2 ? block : 3 - block;
   }
   // Where a warp leaves its sums of another's block.
   static __device__ __forceinline__ int foreign(int part, int block) {
@@ -338,7 +327,7 @@ struct Walk {
 // The warps of a team, waiting for one another.
 template <int SPLIT>
 __device__ __forceinline__ void team_sync(int team) {
-  if constexpr (SPLIT > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(SPLIT * 32) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(SPLIT * 32) : "memory");
 }
 
 // 16 steps x 16 columns of an output, from the sums' layout.
@@ -483,14 +472,12 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
   };
   // c (16 x 64, every warp's part of a sum) to sums over the team, in the warp's own blocks
   auto give = [&](char *to, const FragC (&c)[8]) {
-    if constexpr (SPLIT > 1) {
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        if (L::owner(n) == part) continue;
-        float4 *const at = reinterpret_cast<float4 *>(to + L::foreign(part, n) * 1024 + lane * 16);
-        at[0] = make_float4(c[2 * n][0], c[2 * n][1], c[2 * n][2], c[2 * n][3]);
-        at[32] = make_float4(c[2 * n + 1][0], c[2 * n + 1][1], c[2 * n + 1][2], c[2 * n + 1][3]);
-      }
+    for (int n = 0; n < 4; ++n) {
+      if (L::owner(n) == part) continue;
+      float4 *const at = reinterpret_cast<float4 *>(to + L::foreign(part, n) * 1024 + lane * 16);
+      at[0] = make_float4(c[2 * n][0], c[2 * n][1], c[2 * n][2], c[2 * n][3]);
+      at[32] = make_float4(c[2 * n + 1][0], c[2 * n + 1][1], c[2 * n + 1][2], c[2 * n + 1][3]);
     }
   };
   auto gather = [&](const char *from, const FragC (&c)[8], FragC (&own)[2 * NB]) {
@@ -777,16 +764,6 @@ __global__ void __launch_bounds__(Walk<DK, TEAMS, SPLIT>::kThreads, 1) delta_wal
   else walk<F16, DK, TEAMS, SPLIT, kWalkKeep, false>(p, smem, blockIdx.z, blockIdx.y, slice);
 }
 
-template <class P>
-int launch_large(void (*fn)(P), dim3 grid, int threads, int smem, cudaStream_t stream, const P &p) {
-  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_failure((int)e);
-  }
-  return launch_op(fn, grid, threads, (size_t)smem, 1, stream, p);
-}
-
 template <bool F16, int DK, int TEAMS, int SPLIT>
 int launch_walk(const DeltaParams &p, bool gradient, cudaStream_t stream) {
   typedef Walk<DK, TEAMS, SPLIT> L;
@@ -795,21 +772,25 @@ int launch_walk(const DeltaParams &p, bool gradient, cudaStream_t stream) {
   const int columns = gradient ? (p.dv_size + kDeltaSlice - 1) / kDeltaSlice * kDeltaSlice : p.dv_size;
   const unsigned slices = (unsigned)((columns + L::kSlice - 1) / L::kSlice);
   const dim3 grid(gradient ? 2 * slices : slices, (unsigned)p.heads, (unsigned)p.batch);
-  return gradient ? launch_large(delta_walks_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, stream, p)
-                  : launch_large(delta_walk_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, stream, p);
+  return gradient ? launch_large(delta_walks_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, L::kBytes, 1, stream, p)
+                  : launch_large(delta_walk_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, L::kBytes, 1, stream, p);
 }
 
 template <bool F16, int DK>
 int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t stream) {
   const int st = launch_large(delta_prepare_kernel<F16, DK>,
                               dim3((unsigned)p.chunks, (unsigned)p.heads_k, (unsigned)p.batch), kPrepareThreads,
-                              Prepare<DK>::kBytes, stream, p);
+                              Prepare<DK>::kBytes, Prepare<DK>::kBytes, 1, stream, p);
   if (st != GEMV_OK) return st;
   // Few heads: a team of four warps per CTA while each has an SM; without a tensor walk to go to,
   // forward, up to two a SM.  More: the tensor walk where there is one, but in the gradient
   // wider CTAs while they fill the GPU once.  1024 steps, 128 x 128 bf16, forward (us) teams / tensor /
   // wide, 8 heads 40 / 66 / 78, 16 40 / 66 / 78, 20 70 / 67 / 81, 32 72 / 69 / 82, 64 139 / 84 / 90, 128 243 / 105 / 174;
   // gradient 8 heads 67 / 112 / 110, 16 121 / 145 / 134, 20 156 / 169 / 158, 32 212 / 201 / 182, 64 372 / 297 / 329.
+  // Teams / wide elsewhere, on both sides of the border: 128 x 128 f16, forward 38 heads 80 / 90, 40 115 / 94, gradient
+  // 19 143 / 159, 32 239 / 208; 64 x 64 f16 76 78 / 78, 80 109 / 82, gradient 38 124 / 130, 40 153 / 151 (bf16 71 / 72,
+  // 99 / 76, 106 / 108, 133 / 128); 256 x 256 bf16 19 124 / 120, 20 176 / 123, gradient 9 192 / 205, 12 292 / 261 (f16
+  // 132 / 133, 187 / 136, 227 / 246, 341 / 313); 128 x 64 bf16 76 83 / 92, 80 114 / 95, gradient 38 144 / 158, 40 171 / 174.
   const int64_t heads = (int64_t)p.batch * p.heads, walks = gradient ? 2 : 1;
   const bool tensor = !F16 && DK == 128 && p.dv_size > 64;
   if (heads * ((p.dv_size + 15) / 16) <= (tensor || gradient ? sms : 2 * sms)) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);

@@ -26,9 +26,6 @@
 namespace gemvk {
 namespace {
 
-constexpr int kTilePitch = kDeltaChunk + 8;
-constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
-
 template <int DK>
 struct Grad {
   static constexpr int kParts = DK / 64, kThreads = 128 * kParts, kSlice = kKeptRows;
@@ -551,14 +548,9 @@ __global__ void __launch_bounds__(256) delta_fold_kernel(const DeltaParams p) {
 template <bool F16, int DK>
 int launch_gradient(const DeltaParams &p, cudaStream_t stream) {
   typedef Grad<DK> L;
-  auto fn = delta_gradient_kernel<F16, DK>;
-  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_failure((int)e);
-  }
   const int cluster = p.dq32 == nullptr ? p.heads / p.heads_k : 1;
-  return launch_op(fn, dim3((unsigned)((int64_t)p.chunks * p.heads * p.batch)), L::kThreads, L::kBytes, cluster, stream, p);
+  return launch_large(delta_gradient_kernel<F16, DK>, dim3((unsigned)((int64_t)p.chunks * p.heads * p.batch)), L::kThreads,
+                      L::kBytes, L::kBytes, cluster, stream, p);
 }
 
 template <bool F16>

@@ -18,6 +18,9 @@
 
 namespace gemvk {
 
+constexpr int kTilePitch = kDeltaChunk + 8;  // of 64 x 64 matrices in shared memory
+constexpr int kPairBytes = kDeltaChunk * kTilePitch * 2;
+
 typedef uint32_t FragA[4];
 typedef float FragC[4];
 

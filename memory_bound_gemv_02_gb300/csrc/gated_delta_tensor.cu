@@ -548,15 +548,9 @@ __global__ void __launch_bounds__(kTensorThreads, 1) delta_tensor_kernel(const D
 
 template <int MODE>
 int launch(const DeltaParams &p, cudaStream_t stream) {
-  auto fn = delta_tensor_kernel<MODE>;
-  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTensorBytes);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_failure((int)e);
-  }
   const unsigned slices = (unsigned)((p.dv_size + kRowsPerCta - 1) / kRowsPerCta);
-  return launch_op(fn, dim3(MODE == 0 ? slices : 2 * slices, (unsigned)p.heads, (unsigned)p.batch), kTensorThreads,
-                   kTensorBytes, 1, stream, p);
+  return launch_large(delta_tensor_kernel<MODE>, dim3(MODE == 0 ? slices : 2 * slices, (unsigned)p.heads, (unsigned)p.batch),
+                      kTensorThreads, kTensorBytes, kTensorBytes, 1, stream, p);
 }
 
 }  // namespace

@@ -989,15 +989,8 @@ RingShape ring_shape(int64_t units, int tensors) {
 
 template <class P>
 int launch_ring(void (*fn)(P), const RingShape &r, int64_t grid, cudaStream_t stream, const P &p) {
-  if (r.bytes > 40 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return cuda_failure((int)e);
-    }
-  }
-  return launch_op(fn, dim3((unsigned)grid), r.threads, r.bytes, 1, stream, p);
+  return r.bytes > 40 * 1024 ? launch_large(fn, dim3((unsigned)grid), r.threads, r.bytes, 226 * 1024, 1, stream, p)
+                             : launch_op(fn, dim3((unsigned)grid), r.threads, r.bytes, 1, stream, p);
 }
 
 template <int TYPE, bool SHIFT, int U>

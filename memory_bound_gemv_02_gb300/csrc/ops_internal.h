@@ -152,4 +152,16 @@ int launch_op(void (*fn)(P), dim3 grid, int threads, size_t smem, int cluster, c
   return GEMV_OK;
 }
 
+// The same with more dynamic shared memory than a kernel has without asking: up to `most`, the
+// same in every call of a kernel, as host threads may set it between another's setting and launch.
+template <class P>
+int launch_large(void (*fn)(P), dim3 grid, int threads, size_t smem, int most, int cluster, cudaStream_t stream, const P &p) {
+  const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_failure((int)e);
+  }
+  return launch_op(fn, grid, threads, smem, cluster, stream, p);
+}
+
 }  // namespace gemvk
