@@ -311,18 +311,24 @@ typedef struct gated_delta_shape {
  *
  * Up to 12 steps are walked one by one in fp32, by one kernel.  Longer sequences are
  * cut into chunks of 64 steps, whose products run on the tensor cores by two
- * kernels, the state and what comes from it as sums of two bf16 (within 2^-17), or of
- * two scaled fp16 beside fp16 inputs (within 2^-22, or 2^-34 of the largest of their
- * column of v), with fp32 sums; the product of two remainders is left out (2^-16).  Columns of v never
- * meet: an error is small against its own column.  Operands whose rows are not on 16
- * bytes are copied first, one kernel each.
+ * kernels, with fp32 sums and state: operands that are computed (the state, the corrections, a
+ * chunk's matrices) enter as sums of two bf16 (within 2^-17), what meets fp16 q and k as
+ * two scaled fp16 (within 2^-22, or 2^-34 of the largest of the column of v), and the product of
+ * two remainders is left out (2^-16).  With unit keys and beta <= 1 the state ends within about
+ * 5e-6 of itself, and o before its rounding; with 12 steps or fewer within 2e-7.  (Keys that
+ * repeat with beta * |k|^2 near 2 make a chunk's terms cancel: up to 300 times that.)  Columns of v never
+ * meet: an error is small against its own column.  The workspace is 34 KB per chunk and
+ * head.  Operands whose rows are not on 16 bytes are copied there first, one kernel each.
  *
  * A g of minus infinity (or below -87.3, where the exponential leaves fp32's normal
- * range) starts a new document.  With beta * |k|^2 <= 2 the state stays bounded; the
- * rule itself diverges beyond.  Values have to be finite: a NaN or an infinity in q,
+ * range) starts a new document.  With g <= 0 and beta * |k|^2 <= 2 the state stays bounded; the
+ * rule itself diverges beyond.  Decays above 1 (g > 0) are taken as well, but where one, or the
+ * product of a chunk's, passes fp32's largest value, what follows may be infinite or NaN
+ * although the state is not.  Values have to be finite: a NaN or an infinity in q,
  * k, v, g, beta or h0 (but for a g of minus infinity) may reach every output of its head from the start of its chunk
- * on, past new documents too.  0 <= batch, heads <= 65535.  Where dk is 0 there is no
- * state and o is an empty sum, zeros.
+ * on, past new documents too.  0 <= batch, heads <= 65535, steps < 2^30, dv <= 2^20, and
+ * batch * heads * chunks fits 31 bits.  Where dk is 0 there is no state and o is an empty
+ * sum, zeros.
  */
 int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_heads *k, const gemv_heads *v,
                 const gemv_heads *g, const gemv_heads *beta, const float *h0, const gemv_heads *o, float *state,
@@ -339,8 +345,15 @@ int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_
  * pointer leaves one out).
  *
  * The forward pass leaves nothing behind for it: states and corrections are computed
- * again from the inputs, chunk by chunk, and kept in `workspace`
- * (gated_delta_workspace() with d_o).  Three kernels, and one more for shared heads.
+ * again from the inputs, chunk by chunk (any number of steps goes by chunks here), and kept in
+ * `workspace` (gated_delta_workspace() with d_o) as two bf16: 34 KB + 8 dk dv + 512 dv bytes
+ * per chunk and head, dk rounded up to 64, 128 or 256 and dv to a multiple of 64 (231 KB for
+ * 128 x 128).  To bound it, take the gradient of a long sequence in parts, the last first: h0 is
+ * the state before a part, dstate the dh0 of the part behind it.  dg, dbeta and dh0 in fp32 are within about 6e-6 of
+ * themselves, other gradients before their rounding.  Values in d_o and dstate have to be finite too.
+ *
+ * Three kernels; one more where more than 8 heads share q and k, or share them with dk > 128;
+ * and one for each of q, k, v and d_o whose rows are not on 16 bytes.
  */
 int gated_delta_backward(const gated_delta_shape *shape, const gemv_heads *d_o, const gemv_heads *q,
                          const gemv_heads *k, const gemv_heads *v, const gemv_heads *g, const gemv_heads *beta,

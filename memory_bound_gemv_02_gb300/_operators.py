@@ -269,7 +269,10 @@ def gated_delta(q, k, v, g, beta, scale: float, h0=None, o=None, state=None, str
     decoding).  g = -inf starts a new document.  ``workspace`` (sequences of more
     than 12 steps): any tensor of ``gated_delta_workspace`` bytes, or torch's
     allocator has memory for the call's stream.  Not recorded by autograd.  Returns
-    (o, state)."""
+    (o, state).
+
+    Up to 12 steps run in fp32 (2e-7 from 64 bits); longer sequences on the tensor
+    cores by chunks, where the last state is within about 5e-6 and o, before its rounding, as well."""
     if o is None:
         _dims(v, 4, "v")
         o = _new(lambda: torch.empty_like(v, memory_format=torch.contiguous_format), stream, v.device)
@@ -290,7 +293,9 @@ def gated_delta_backward(do, q, k, v, g, beta, scale: float, h0=None, dstate=Non
     the returned state (float32, optional); the other inputs as in the forward call,
     which keeps nothing for this one.  ``workspace``: any tensor of
     ``gated_delta_workspace`` bytes (with ``do``), or torch's allocator has memory
-    for the call's stream.  Returns (dq, dk, dv, dg, dbeta, dh0)."""
+    for the call's stream; 231 KB per 64 steps and head of 128 x 128 (long sequences
+    can be taken in parts, the last first, ``dstate`` being the next part's dh0).  Gradients are within about 6e-6
+    before their rounding.  Returns (dq, dk, dv, dg, dbeta, dh0)."""
     def like(given, t, dims, name):
         if given is not None:
             return given
