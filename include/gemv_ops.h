@@ -311,13 +311,13 @@ typedef struct gated_delta_shape {
  *
  * Up to 12 steps are walked one by one in fp32, by one kernel.  Longer sequences are
  * cut into chunks of 64 steps, whose products run on the tensor cores by two
- * kernels, with fp32 sums and state: operands that are computed (the state, the corrections, a
- * chunk's matrices) enter as sums of two bf16 (within 2^-17), what meets fp16 q and k as
- * two scaled fp16 (within 2^-22, or 2^-34 of the largest of the column of v), and the product of
- * two remainders is left out (2^-16).  With unit keys and beta <= 1 the state ends within about
+ * kernels, with fp32 sums and state: operands that are computed (the state, the corrections,
+ * P) enter as sums of two bf16 (within 2^-17), what meets fp16 q and k as
+ * two scaled fp16 (within 2^-22, or 2^-34 of the largest of the column of v), the inverse of a chunk's
+ * system as three bf16; the product of two remainders is left out (2^-16).  With unit keys and beta <= 1 the state ends within about
  * 5e-6 of itself, and o before its rounding; with 12 steps or fewer within 2e-7.  (Keys that
- * repeat with beta * |k|^2 near 2 make a chunk's terms cancel: up to 300 times that.)  Columns of v never
- * meet: an error is small against its own column.  The workspace is 34 KB per chunk and
+ * repeat with beta * |k|^2 near 2 make a chunk's terms cancel: up to 100 times that.)  Columns of v never
+ * meet: an error is small against its own column.  The workspace is 42 KB per chunk and
  * head.  Operands whose rows are not on 16 bytes are copied there first, one kernel each.
  *
  * A g of minus infinity (or below -87.3, where the exponential leaves fp32's normal
@@ -346,8 +346,8 @@ int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_
  *
  * The forward pass leaves nothing behind for it: states and corrections are computed
  * again from the inputs, chunk by chunk (any number of steps goes by chunks here), and kept in
- * `workspace` (gated_delta_workspace() with d_o) as two bf16: 34 KB + 8 dk dv + 512 dv bytes
- * per chunk and head, dk rounded up to 64, 128 or 256 and dv to a multiple of 64 (231 KB for
+ * `workspace` (gated_delta_workspace() with d_o) as two bf16: 42 KB + 8 dk dv + 512 dv bytes
+ * per chunk and head, dk rounded up to 64, 128 or 256 and dv to a multiple of 64 (239 KB for
  * 128 x 128).  To bound it, take the gradient of a long sequence in parts, the last first: h0 is
  * the state before a part, dstate the dh0 of the part behind it.  dg, dbeta and dh0 in fp32 are within about 6e-6 of
  * themselves, other gradients before their rounding.  Values in d_o and dstate have to be finite too.

@@ -293,7 +293,7 @@ def gated_delta_backward(do, q, k, v, g, beta, scale: float, h0=None, dstate=Non
     the returned state (float32, optional); the other inputs as in the forward call,
     which keeps nothing for this one.  ``workspace``: any tensor of
     ``gated_delta_workspace`` bytes (with ``do``), or torch's allocator has memory
-    for the call's stream; 231 KB per 64 steps and head of 128 x 128 (long sequences
+    for the call's stream; 239 KB per 64 steps and head of 128 x 128 (long sequences
     can be taken in parts, the last first, ``dstate`` being the next part's dh0).  Gradients are within about 6e-6
     before their rounding.  Returns (dq, dk, dv, dg, dbeta, dh0)."""
     def like(given, t, dims, name):

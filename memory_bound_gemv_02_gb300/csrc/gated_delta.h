@@ -42,9 +42,13 @@ struct TileSource {
 // sum of log decays (to base 2) up to the step in two floats, and the count of documents begun.
 enum { kBeta = 0, kFirst = 64, kLast = 128, kTotalHi = 192, kTotalLo = 256, kDocs = 320, kGateFloats = 384 };
 
-// A chunk of one head: T = (I + A)^-1 and P as sums of two bf16 (64 x 64 each), the gates.
+// A chunk of one head: T = (I + A)^-1 as a sum of three bf16 and P of two (64 x 64 each), the gates.
+// What T is off by acts on the state again in every chunk, and for keys that repeat with beta |k|^2 near 2, where T's
+// entries are up to 2 throughout, not as a contraction: with two (and two of A in the inversion) a head's state was up to 0.6
+// off after 512 such steps, with three 4e-4.  It costs 2 to 8 % (4 x 8192 steps of 16 heads bf16 541 -> 570 us).
 constexpr int kMatrix = kDeltaChunk * kDeltaChunk;
-constexpr int64_t kRecordHalfs = 4 * kMatrix;  // T, T's rest, P, P's rest
+constexpr int kPartsT = 3, kPartsP = 2;
+constexpr int64_t kRecordP = kPartsT * kMatrix, kRecordHalfs = kRecordP + kPartsP * kMatrix;  // T's parts, P's
 constexpr int64_t kRecordBytes = kRecordHalfs * 2 + kGateFloats * 4;
 
 struct DeltaParams {

@@ -76,6 +76,13 @@ __device__ __forceinline__ void chunk_gates(const DeltaParams &p, int64_t b, int
   }
 }
 
+// While a chunk's matrices are made their 16 x 16 blocks lie one behind the other, row by row of blocks, with
+// 24 numbers a row (8 rows of 16 bytes meet all banks): of T and P those on and below the diagonal, of A those
+// below it.
+constexpr int kBlockPitch = 24, kBlockBytes = 16 * kBlockPitch * 2, kPartBytesT = 10 * kBlockBytes, kPartBytesA = 6 * kBlockBytes;
+__device__ __forceinline__ uint32_t block_of_t(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * kBlockBytes); }
+__device__ __forceinline__ uint32_t block_of_a(int i, int j) { return (uint32_t)((i * (i - 1) / 2 + j) * kBlockBytes); }
+
 // The 16 x 16 blocks on the diagonal of T = (I + A)^-1 by substitution in fp32, a warp
 // per block, a lane per column; A's blocks with 20 floats a row.
 constexpr int kDiagPitch = 20;
@@ -96,50 +103,76 @@ __device__ __forceinline__ void invert_diagonal(const float *A, char *T) {
     }
     x[i] = v[0] + v[1];
   }
-  // two rows per lane half: bf16 and the rest
-  uint16_t *const to = reinterpret_cast<uint16_t *>(T) + warp * 16 * (kTilePitch + 1) + j;
+  // two rows per lane half
+  uint16_t *const to = reinterpret_cast<uint16_t *>(T + block_of_t(warp, warp)) + j;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if ((i & 1) != lane / 16) continue;
-    uint32_t big, rest;
-    split(x[i], 0.f, big, rest);
-    to[i * kTilePitch] = (uint16_t)big;
-    to[kPairBytes / 2 + i * kTilePitch] = (uint16_t)rest;
+    uint32_t part[3];
+    split3(x[i], 0.f, part);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) to[n * (kPartBytesT / 2) + i * kBlockPitch] = (uint16_t)part[n];
   }
 }
 
-// c0, c1 = X^T Y^T for 16 x 16 blocks as two bf16: X stored (k, m), Y stored (n, k).
-__device__ __forceinline__ void block_product(FragC &c0, FragC &c1, uint32_t X, uint32_t Y, int lane) {
-  FragA big, rest;
-  uint32_t h[4], l[4];
-  load_matrices_t(big, at_km(X, kTilePitch, 0, 0, lane));
-  load_matrices_t(rest, at_km(X + kPairBytes, kTilePitch, 0, 0, lane));
-  load_matrices(h, at_nk(Y, kTilePitch, 0, 0, lane));
-  load_matrices(l, at_nk(Y + kPairBytes, kTilePitch, 0, 0, lane));
-  mma_split_split(c0, c1, big, rest, h, l);
+// 16 x 16 blocks as three bf16, for products within fp32's own rounding (of the nine products of
+// parts the three smallest are left out).
+struct Left3 {
+  FragA part[3];
+};
+struct Right3 {
+  uint32_t part[3][4];
+};
+__device__ __forceinline__ void mma_three(FragC &c0, FragC &c1, const Left3 &a, const Right3 &b) {
+#pragma unroll
+  for (int n = 2; n >= 0; --n)  // (the small ones first)
+#pragma unroll
+    for (int i = 0; i <= n; ++i) {
+      mma_bf16(c0, a.part[i], b.part[n - i][0], b.part[n - i][1]);
+      mma_bf16(c1, a.part[i], b.part[n - i][2], b.part[n - i][3]);
+    }
 }
-// c0, c1 -= Z^T Y^T for sums Z^T just made.
-__device__ __forceinline__ void block_minus(FragC &c0, FragC &c1, const FragC &z0, const FragC &z1, uint32_t Y, int lane) {
-  FragA big, rest;
-  uint32_t h[4], l[4];
-  split_sums(z0, z1, big, rest);
+__device__ __forceinline__ Right3 load_right3(uint32_t Y, int part_bytes, int lane) {  // stored (n, k)
+  Right3 r;
+#pragma unroll
+  for (int n = 0; n < 3; ++n) load_matrices(r.part[n], at_nk(Y + n * part_bytes, kBlockPitch, 0, 0, lane));
+  return r;
+}
+__device__ __forceinline__ Left3 left3_of(const FragC &c0, const FragC &c1) {
+  const float v[4][2] = {{c0[0], c0[1]}, {c0[2], c0[3]}, {c1[0], c1[1]}, {c1[2], c1[3]}};
+  Left3 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    big[i] ^= 0x80008000u;
-    rest[i] ^= 0x80008000u;
+    uint32_t part[3];
+    split3(v[i][0], v[i][1], part);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) r.part[n][i] = part[n];
   }
-  load_matrices(h, at_nk(Y, kTilePitch, 0, 0, lane));
-  load_matrices(l, at_nk(Y + kPairBytes, kTilePitch, 0, 0, lane));
-  mma_split_split(c0, c1, big, rest, h, l);
+  return r;
+}
+
+// c0, c1 = X^T Y^T for blocks X of T, stored (k, m), and Y of A, stored (n, k).
+__device__ __forceinline__ void block_product(FragC &c0, FragC &c1, uint32_t X, uint32_t Y, int lane) {
+  Left3 a;
+#pragma unroll
+  for (int n = 0; n < 3; ++n) load_matrices_t(a.part[n], at_km(X + n * kPartBytesT, kBlockPitch, 0, 0, lane));
+  mma_three(c0, c1, a, load_right3(Y, kPartBytesA, lane));
+}
+// c0, c1 -= Z^T Y^T for sums Z^T just made and a block Y of T.
+__device__ __forceinline__ void block_minus(FragC &c0, FragC &c1, const FragC &z0, const FragC &z1, uint32_t Y, int lane) {
+  Left3 a = left3_of(z0, z1);
+#pragma unroll
+  for (int n = 0; n < 3; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.part[n][i] ^= 0x80008000u;
+  mma_three(c0, c1, a, load_right3(Y, kPartBytesT, lane));
 }
 // A block of T^T, to T.
 __device__ __forceinline__ void store_block(uint32_t T, const FragC &c0, const FragC &c1, int lane) {
-  FragA big, rest;
-  split_sums(c0, c1, big, rest);
-  store_matrices_t(at_km(T, kTilePitch, 0, 0, lane), big);
-  store_matrices_t(at_km(T + kPairBytes, kTilePitch, 0, 0, lane), rest);
+  const Left3 a = left3_of(c0, c1);
+#pragma unroll
+  for (int n = 0; n < 3; ++n) store_matrices_t(at_km(T + n * kPartBytesT, kBlockPitch, 0, 0, lane), a.part[n]);
 }
-__device__ __forceinline__ uint32_t block_of(uint32_t M, int i, int j) { return M + (i * 16 * kTilePitch + j * 16) * 2; }
 
 // The blocks of T below the diagonal, T_lo = -T_22 A_21 T_11, for halves of 32 and of 64, on
 // the tensor cores: transposed, so that the inner product's sums are the outer one's left
@@ -149,9 +182,9 @@ __device__ __forceinline__ void invert_below(uint32_t A, uint32_t T) {
   if (warp < 2) {
     const int i = 2 * warp + 1, j = 2 * warp;
     FragC z[2] = {}, c[2] = {};
-    block_product(z[0], z[1], block_of(T, j, j), block_of(A, i, j), lane);
-    block_minus(c[0], c[1], z[0], z[1], block_of(T, i, i), lane);
-    store_block(block_of(T, i, j), c[0], c[1], lane);
+    block_product(z[0], z[1], T + block_of_t(j, j), A + block_of_a(i, j), lane);
+    block_minus(c[0], c[1], z[0], z[1], T + block_of_t(i, i), lane);
+    store_block(T + block_of_t(i, j), c[0], c[1], lane);
   }
   __syncthreads();
   const int j = warp & 1, i = 2 + warp / 2;  // one block of the lower left quarter per warp
@@ -162,33 +195,36 @@ __device__ __forceinline__ void invert_below(uint32_t A, uint32_t T) {
     FragC z[2] = {};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
-      if (k >= j) block_product(z[0], z[1], block_of(T, k, j), block_of(A, m, k), lane);
-    block_minus(c[0], c[1], z[0], z[1], block_of(T, i, m), lane);
+      if (k >= j) block_product(z[0], z[1], T + block_of_t(k, j), A + block_of_a(m, k), lane);
+    block_minus(c[0], c[1], z[0], z[1], T + block_of_t(i, m), lane);
   }
-  store_block(block_of(T, i, j), c[0], c[1], lane);
+  store_block(T + block_of_t(i, j), c[0], c[1], lane);
 }
 
 template <int DK>
 struct Prepare {
   static constexpr int kTiles = 2 * kDeltaChunk * (DK + 8) * 2;
-  // afterwards in the same place: A and T (P before it) as two bf16 each, A's diagonal in fp32
-  static constexpr int kA = 0, kT = 2 * kPairBytes, kDiag = kT + 2 * kPairBytes, kAfter = kDiag + 64 * kDiagPitch * 4,
+  // afterwards in the same place: A and T (P before it) in their parts, A's diagonal in fp32
+  static constexpr int kA = 0, kT = kPartsT * kPartBytesA, kDiag = kT + kPartsT * kPartBytesT, kAfter = kDiag + 64 * kDiagPitch * 4,
                        kGates = kTiles > kAfter ? kTiles : kAfter, kBytes = kGates + kGateFloats * 4;
 };
 
-// The blocks on and below the diagonal of two 64 x 64 matrices, 16 bytes at a time (nothing
+// The blocks on and below the diagonal of 64 x 64 matrices, 16 bytes at a time (nothing
 // reads those above).
+template <int MATRICES>
 __device__ __forceinline__ void store_lower(uint16_t *to, const char *from) {
 #pragma unroll
-  for (int n = 0; n < 2 * kMatrix / 8 / kPrepareThreads; ++n) {
-    const int i = n * kPrepareThreads + (int)threadIdx.x;
-    if (i % 8 / 2 <= i / 8 % 64 / 16)
-      reinterpret_cast<uint4 *>(to)[i] = *reinterpret_cast<const uint4 *>(from + i / 8 * kTilePitch * 2 + i % 8 * 16);
+  for (int n = 0; n < MATRICES * kMatrix / 8 / kPrepareThreads; ++n) {
+    const int at = n * kPrepareThreads + (int)threadIdx.x, row = at / 8 % 64, u = at % 8, i = row / 16, j = u / 2;
+    if (j <= i)
+      reinterpret_cast<uint4 *>(to)[at] = *reinterpret_cast<const uint4 *>(from + at / 512 * kPartBytesT + block_of_t(i, j) +
+                                                                           (row % 16 * kBlockPitch + u % 2 * 8) * 2);
   }
 }
 
-// T, P and the gates of one chunk, for all heads that share its q and k.  8192 chunks of 128: 120
-// us, issue 42 %, barriers between short phases; with the inverse by substitution throughout 285.
+// T, P and the gates of one chunk, for all heads that share its q and k.  8192 chunks of 128: 150
+// us (123 with two parts of T), barriers between short phases; with the inverse by substitution throughout 285, with
+// whole matrices in place of blocks and so three CTAs an SM 158.
 template <bool F16, int DK>
 __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const DeltaParams p) {
   typedef Prepare<DK> L;
@@ -252,7 +288,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
                    dj = *reinterpret_cast<const float2 *>(gates + kDocs + j);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int i = i0 + 8 * h, at = (i * kTilePitch + j) * 2;
+        const int i = i0 + 8 * h, at = (i % 16 * kBlockPitch + j % 16) * 2;  // within a block
         // from step j to step i: nothing above the diagonal or across a new document
         const float f0 = j <= i && docs[h] == dj.x ? power2((hi[h] - hj.x) + (lo[h] - lj.x)) : 0.f;
         const float f1 = j < i && docs[h] == dj.y ? power2((hi[h] - hj.y) + (lo[h] - lj.y)) : 0.f;
@@ -261,21 +297,26 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
           *reinterpret_cast<float2 *>(diagonal + i * kDiagPitch + j - warp * 16) = make_float2(a0, a1);
         uint32_t big, rest;
         split(j <= i ? p.scale * f0 * qk[n][2 * h] : 0.f, j < i ? p.scale * f1 * qk[n][2 * h + 1] : 0.f, big, rest);
-        *reinterpret_cast<uint32_t *>(smem + L::kT + at) = big;
-        *reinterpret_cast<uint32_t *>(smem + L::kT + kPairBytes + at) = rest;
-        split(a0, a1, big, rest);
-        *reinterpret_cast<uint32_t *>(smem + L::kA + at) = big;
-        *reinterpret_cast<uint32_t *>(smem + L::kA + kPairBytes + at) = rest;
+        char *const p_block = smem + L::kT + block_of_t(warp, n / 2) + at;
+        *reinterpret_cast<uint32_t *>(p_block) = big;
+        *reinterpret_cast<uint32_t *>(p_block + kPartBytesT) = rest;
+        if (n / 2 < warp) {
+          uint32_t part[3];
+          split3(a0, a1, part);
+#pragma unroll
+          for (int u = 0; u < 3; ++u)
+            *reinterpret_cast<uint32_t *>(smem + L::kA + u * kPartBytesA + block_of_a(warp, n / 2) + at) = part[u];
+        }
       }
     }
     __syncthreads();
-    store_lower(out + 2 * kMatrix, smem + L::kT);
+    store_lower<kPartsP>(out + kRecordP, smem + L::kT);
     __syncthreads();
     invert_diagonal(diagonal, smem + L::kT);
     __syncthreads();
     invert_below(base + L::kA, base + L::kT);
     __syncthreads();
-    store_lower(out, smem + L::kT);
+    store_lower<kPartsT>(out, smem + L::kT);
     float *const kept = reinterpret_cast<float *>(record + kRecordHalfs * 2);
     for (int at = threadIdx.x; at < kGateFloats; at += kPrepareThreads) kept[at] = gates[at];
   }
@@ -301,8 +342,8 @@ struct Walk {
                        kBlocks = 4 / SPLIT;  // of 16 steps, per warp
   static constexpr int kWide = kDeltaChunk * (DK + 8) * 2, kNarrow = kSlice + 8;
   // a stage
-  static constexpr int kK = 0, kQ = kWide, kV = 2 * kWide, kT = kV + kDeltaChunk * kNarrow * 2, kP = kT + 2 * kPairBytes,
-                       kGates = kP + 2 * kPairBytes, kStage = kGates + 3 * kDeltaChunk * 4;
+  static constexpr int kK = 0, kQ = kWide, kV = 2 * kWide, kT = kV + kDeltaChunk * kNarrow * 2, kP = kT + kPartsT * kPairBytes,
+                       kGates = kP + kPartsP * kPairBytes, kStage = kGates + 3 * kDeltaChunk * 4;
   // exchanged within a team: the sums that each warp has of the others' blocks (1 KB each), and
   // twice the left operands of all four blocks
   static constexpr int kForeign = 4 - kBlocks, kSums = SPLIT * kForeign * 1024, kOperands = 4 * 1024,
@@ -464,8 +505,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       copy_tile<DK, L::kCopying>(at + L::kK, p.tk, b, head_k, t0, p.steps, 0, tid);
       if (BACK || MODE == kWalkOut) copy_tile<DK, L::kCopying>(at + L::kQ, p.tq, b, head_k, t0, p.steps, 0, tid);
       copy_tile<L::kSlice, L::kCopying>(at + L::kV, BACK ? p.td : p.tv, b, head, t0, p.steps, slice * L::kSlice, tid);
-      copy_lower<L::kCopying>(at + L::kT, m, tid);
-      if (BACK || MODE == kWalkOut) copy_lower<L::kCopying>(at + L::kP, m + 2 * kMatrix, tid);
+      copy_lower<kPartsT, L::kCopying>(at + L::kT, m, tid);
+      if (BACK || MODE == kWalkOut) copy_lower<kPartsP, L::kCopying>(at + L::kP, m + kRecordP, tid);
       if (tid < 3 * kDeltaChunk / 4) copy16(at + L::kGates + tid * 16, record + kRecordHalfs * 2 + tid * 16, true);
     }
     copies_close();
@@ -632,15 +673,13 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         for (int i2 = 0; i2 < NB; ++i2) {
           const int n = L::block(part, i2);
           if (BACK ? s < n : s > n) continue;
-          uint32_t h[4], l[4];
-          if constexpr (BACK) {
-            load_matrices_t(h, at_kn(T, kTilePitch, s * 16, n * 16, lane));
-            load_matrices_t(l, at_kn(T + kPairBytes, kTilePitch, s * 16, n * 16, lane));
-          } else {
-            load_matrices(h, at_nk(T, kTilePitch, n * 16, s * 16, lane));
-            load_matrices(l, at_nk(T + kPairBytes, kTilePitch, n * 16, s * 16, lane));
+          uint32_t t[3][4];
+#pragma unroll
+          for (int u = 0; u < 3; ++u) {
+            if constexpr (BACK) load_matrices_t(t[u], at_kn(T + u * kPairBytes, kTilePitch, s * 16, n * 16, lane));
+            else load_matrices(t[u], at_nk(T + u * kPairBytes, kTilePitch, n * 16, s * 16, lane));
           }
-          mma_split_split(d[2 * i2], d[2 * i2 + 1], big, rest, h, l);
+          mma_split_three(d[2 * i2], d[2 * i2 + 1], big, rest, t[0], t[1], t[2]);
         }
       }
       if constexpr (MODE == kWalkKeep) {

@@ -85,6 +85,13 @@ __device__ __forceinline__ void split_half(uint32_t v, uint32_t &big, uint32_t &
   split(f.x, f.y, big, rest);
 }
 
+// The same in three, all of an fp32 number.
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&part)[3]) {
+  split(a, b, part[0], part[1]);
+  const float2 u = unpack_bf16(part[0]), v = unpack_bf16(part[1]);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(part[2]) : "f"((b - u.y) - v.y), "f"((a - u.x) - v.x));
+}
+
 // The left operand of a product's next step: the sums of two neighbouring 16 x 8 tiles.
 __device__ __forceinline__ void split_sums(const FragC &c0, const FragC &c1, FragA &big, FragA &rest) {
   split(c0[0], c0[1], big[0], rest[0]);
@@ -123,6 +130,15 @@ __device__ __forceinline__ void mma_split_split(FragC &c0, FragC &c1, const Frag
   mma_bf16(c1, rest, h[2], h[3]);
   mma_bf16(c0, big, l[0], l[1]);
   mma_bf16(c1, big, l[2], l[3]);
+}
+// c0, c1 += (big + rest) (p0 + p1 + p2), but for rest p2
+__device__ __forceinline__ void mma_split_three(FragC &c0, FragC &c1, const FragA &big, const FragA &rest,
+                                                const uint32_t (&p0)[4], const uint32_t (&p1)[4], const uint32_t (&p2)[4]) {
+  mma_split_split(c0, c1, big, rest, p0, p1);
+  mma_bf16(c0, rest, p1[0], p1[1]);
+  mma_bf16(c1, rest, p1[2], p1[3]);
+  mma_bf16(c0, big, p2[0], p2[1]);
+  mma_bf16(c1, big, p2[2], p2[3]);
 }
 // c0, c1 += A (h + l) for a left operand that is an input.
 template <bool F16>
@@ -275,12 +291,13 @@ template <int ROWS>
 __device__ __forceinline__ uint32_t kept_km(uint32_t base, int k, int m, int lane) {
   return base + (uint32_t)((m / 8 + ((lane >> 3) & 1)) * ROWS + k + (lane & 7) + ((lane >> 4) & 1) * 8) * 16;
 }
-// The 16 x 16 blocks on and below the diagonal of two 64 x 64 matrices, dense, to rows
+// The 16 x 16 blocks on and below the diagonal of MATRICES of 64 x 64, dense, to rows
 // of 72.
-template <int THREADS>
+template <int MATRICES, int THREADS>
 __device__ __forceinline__ void copy_lower(uint32_t dst, const uint16_t *src, int tid) {
+  static_assert(MATRICES * kMatrix / 8 % THREADS == 0, "whole rounds");
 #pragma unroll
-  for (int i = 0; i < 2 * kMatrix / 8 / THREADS; ++i) {
+  for (int i = 0; i < MATRICES * kMatrix / 8 / THREADS; ++i) {
     const int at = i * THREADS + tid, row = at / 8, u = at % 8;
     if (u / 2 <= row % 64 / 16) copy16(dst + (uint32_t)(row * (kDeltaChunk + 8) + u * 8) * 2, src + at * 8, true);
   }

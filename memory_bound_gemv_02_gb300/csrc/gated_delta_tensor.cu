@@ -4,7 +4,7 @@
 // A CTA has 128 columns of v, a row of S^T each: the 128 lanes of tensor memory.  S^T
 // (128 x 128, fp32) stays there all along; every product is 128 rows of one left operand, made by
 // a thread per row and half of the columns from what the product before left, and
-// written to tensor memory as two bf16, times a tile in shared memory:
+// written to tensor memory as two bf16, times a tile in shared memory (T being three, P two):
 //
 //     W  = S^T K^T    (N = 64 steps)       R^T = beta (V^T - first W)
 //     D  = R^T T^T    (N = 64, 48, 32, 16: T's blocks on and below the diagonal)
@@ -14,12 +14,12 @@
 // and the same backward with dS, P^T dO, T^T and Q.  K and Q, T and P are read as rows
 // or as columns of the same tile: descriptors with the one or the other major.
 //
-// The walk is a chain: per chunk three products of 512 + 240 + 512 cycles (two, three,
+// The walk is a chain: per chunk three products of 512 + 400 + 512 cycles (two, five,
 // two terms of split operands at 8192 flops a cycle) and between them what the threads do,
 // 128 x 128 + 2 x 128 x 64 values converted: eight warps for that alone.  Copies into shared
 // memory and outputs have warps of their own, beside the chain.  A chunk takes 3.2 us (6,100
 // cycles), of which the products' issue, commit and wake are some 1,200; 4 x 8192 steps of 16 heads
-// 411 us on 64 SMs (mma.sync with the state in registers, on 128: 538).
+// 416 us on 64 SMs (mma.sync with the state in registers, on 128: 538).
 #include "gated_delta_mma.cuh"
 
 namespace gemvk {
@@ -30,8 +30,8 @@ constexpr int kFirstCopy = kComputeWarps + kDrainWarps, kIssueWarp = kFirstCopy 
               kTensorThreads = 32 * (kIssueWarp + 1);
 constexpr int kRowsPerCta = 128, kWidth = 128;  // columns of v; dk
 constexpr int kTileBytes64 = 64 * 128;          // 64 rows of 64 elements, swizzled
-constexpr int kOffK = 0, kOffQ = 2 * kTileBytes64, kOffT = 4 * kTileBytes64, kOffP = 6 * kTileBytes64,
-              kOffV = 8 * kTileBytes64, kStageBytes = kOffV + 64 * 256;
+constexpr int kOffK = 0, kOffQ = 2 * kTileBytes64, kOffT = 4 * kTileBytes64, kOffP = kOffT + kPartsT * kTileBytes64,
+              kOffV = kOffP + kPartsP * kTileBytes64, kStageBytes = kOffV + 64 * 256;
 constexpr int kGateRing = 4, kGateBytes = 3 * kDeltaChunk * 4;
 constexpr int kTensorBytes = 2 * kStageBytes + kGateRing * kGateBytes + 1024;  // (tiles start on 1024 bytes)
 // columns of tensor memory
@@ -136,10 +136,10 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
         from += next;
       }
     };
-    auto copy_blocks = [&](uint32_t to, const uint16_t *from) {  // two matrices' blocks on and below the diagonal
+    auto copy_blocks = [&](uint32_t to, const uint16_t *from, int matrices) {  // the blocks on and below their diagonals
       const int v = lane % 8;
 #pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < 16 * matrices; ++i) {
         const int row = i * 4 + lane / 8;
         if (v / 2 <= row % 64 / 16) copy16(to + (uint32_t)(row * 128 + (v ^ (row & 7)) * 16), from + row * 64 + v * 8, true);
       }
@@ -152,11 +152,11 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
       const uint16_t *const m = reinterpret_cast<const uint16_t *>(record);
       if (part == 0) {
         copy_rows(at + kOffK, p.tk, head_k, t0, 0, true);
-        copy_blocks(at + kOffT, m);
+        copy_blocks(at + kOffT, m, kPartsT);
       } else if (part == 1) {
         if (kQ) {
           copy_rows(at + kOffQ, p.tq, head_k, t0, 0, true);
-          copy_blocks(at + kOffP, m + 2 * kMatrix);
+          copy_blocks(at + kOffP, m + kRecordP, kPartsP);
         }
       } else {
         copy_rows(at + kOffV, BACK ? p.td : p.tv, head, t0, slice * (kRowsPerCta / 8), false);
@@ -220,6 +220,8 @@ __device__ __forceinline__ void tensor_walk(const DeltaParams &p, char *smem, Te
         triangle(tmem + kColD, tmem + kColWA, at + kOffT, true);
         triangle(tmem + kColD, tmem + kColWA + 32, at + kOffT, false);
         triangle(tmem + kColD, tmem + kColWA, at + kOffT + kTileBytes64, false);
+        triangle(tmem + kColD, tmem + kColWA + 32, at + kOffT + kTileBytes64, false);
+        triangle(tmem + kColD, tmem + kColWA, at + kOffT + 2 * kTileBytes64, false);
         tc_commit<1>(smem_u32(&sh.solved));
         if (kOut) rows_times(tmem + kColO, tmem + kColSA + 64, at + kOffQ, false);
         if (BACK) {  // the state's gain from Q, ready since the right side was

@@ -36,9 +36,10 @@ def _steps(x, heads):
     return torch.cat([x, pad], 1).unflatten(1, (n, CHUNK))
 
 
-def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None):
+def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None, inverse=None):
     """(o, state), or with ``do`` (dq, dk, dv, dg, dbeta, dh0), those of heads of k per head of v; finite g.
-    ``meets`` cuts what the walks multiply with q and k, in place of ``pieces`` of bf16."""
+    ``meets`` cuts what the walks multiply with q and k, in place of ``pieces`` of bf16; ``inverse``: pieces of
+    A and of (I + A)^-1."""
     batch, T, heads, _ = v.shape
     c = lambda x: cut(x, pieces)  # noqa: E731
     meets = meets or c
@@ -48,7 +49,8 @@ def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None):
     f = (G[..., :, None] - G[..., None, :]).tril().exp().tril()
     first, last, whole = G.exp(), (G[..., -1:] - G).exp(), G[..., -1:].exp()
     A = (beta[..., None] * f * (k @ k.mT)).tril(-1)
-    t = c(torch.linalg.inv(torch.eye(CHUNK, dtype=A.dtype, device=A.device) + c(A)))
+    t = torch.linalg.inv(torch.eye(CHUNK, dtype=A.dtype, device=A.device) + cut(A, pieces if inverse is None else inverse))
+    t = cut(t, pieces if inverse is None else inverse)
     P = c(scale * f * (q @ k.mT))
     S = torch.zeros((len(q), q.shape[-1], v.shape[-1]), dtype=q.dtype, device=q.device) if h0 is None else h0.double().flatten(0, 1)
     o, D, starts = [], [], []
