@@ -246,9 +246,10 @@ int launch_delta_pack(const PackParams &p, cudaStream_t stream) {
 
 namespace {
 
-// Steps up to which the state is walked step by step: 1.6 to 12 us a step, a chunk the same
-// whether full or not.  Walk / chunks (us), heads of 128 x 128 bf16, for 8, 16 and 64 steps: 16 heads
-// 15 / 18, 19 / 18, 67 / 18; 512 heads 31 / 48, 55 / 49, 196 / 51; 2048 heads 124 / 162, 221 / 163, 808 / 171.
+// Steps up to which the state is walked step by step: 1 to 12 us a step, a chunk the same
+// whether full or not.  Walk / chunks (us), heads of 128 x 128 bf16, for 8, 12, 16 and 64 steps: 16 heads
+// 13 / 14, 17 / 14, 21 / 14, 68 / 14; 512 heads 33 / 61, 45 / 61, 57 / 61, 224 / 66; 2048 heads 138 / 195, 185 / 196,
+// 230 / 197, 815 / 209.
 constexpr int kWalkSteps = 12;
 
 int padded_dk(int64_t dk) { return dk <= 64 ? 64 : dk <= 128 ? 128 : 256; }

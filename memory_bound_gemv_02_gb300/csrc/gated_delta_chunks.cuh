@@ -223,7 +223,7 @@ __device__ __forceinline__ void store_lower(uint16_t *to, const char *from) {
 }
 
 // T, P and the gates of one chunk, for all heads that share its q and k.  8192 chunks of 128: 150
-// us (123 with two parts of T), barriers between short phases; with the inverse by substitution throughout 285, with
+// us (123 with two parts of T), issue 44 %, barriers between short phases; with the inverse by substitution throughout 285, with
 // whole matrices in place of blocks and so three CTAs an SM 158.
 template <bool F16, int DK>
 __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const DeltaParams p) {
@@ -824,12 +824,12 @@ int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t str
   // Few heads: a team of four warps per CTA while each has an SM; without a tensor walk to go to,
   // forward, up to two a SM.  More: the tensor walk where there is one, but in the gradient
   // wider CTAs while they fill the GPU once.  1024 steps, 128 x 128 bf16, forward (us) teams / tensor /
-  // wide, 8 heads 40 / 66 / 78, 16 40 / 66 / 78, 20 70 / 67 / 81, 32 72 / 69 / 82, 64 139 / 84 / 90, 128 243 / 105 / 174;
-  // gradient 8 heads 67 / 112 / 110, 16 121 / 145 / 134, 20 156 / 169 / 158, 32 212 / 201 / 182, 64 372 / 297 / 329.
-  // Teams / wide elsewhere, on both sides of the border: 128 x 128 f16, forward 38 heads 80 / 90, 40 115 / 94, gradient
-  // 19 143 / 159, 32 239 / 208; 64 x 64 f16 76 78 / 78, 80 109 / 82, gradient 38 124 / 130, 40 153 / 151 (bf16 71 / 72,
-  // 99 / 76, 106 / 108, 133 / 128); 256 x 256 bf16 19 124 / 120, 20 176 / 123, gradient 9 192 / 205, 12 292 / 261 (f16
-  // 132 / 133, 187 / 136, 227 / 246, 341 / 313); 128 x 64 bf16 76 83 / 92, 80 114 / 95, gradient 38 144 / 158, 40 171 / 174.
+  // wide, 8 heads 42 / 67 / 81, 16 43 / 68 / 82, 20 75 / 70 / 84, 32 77 / 72 / 86, 64 150 / 89 / 96, 128 264 / 115 / 188;
+  // gradient 8 heads 66 / 112 / 113, 16 124 / 144 / 138, 20 160 / 168 / 161, 32 219 / 200 / 186, 64 387 / 297 / 341.
+  // Teams / wide elsewhere, on both sides of the border: 128 x 128 f16, forward 38 heads 85 / 95, 40 123 / 101, gradient
+  // 19 149 / 168, 32 251 / 218; 64 x 64 f16 76 84 / 85, 80 117 / 91, gradient 38 130 / 135, 40 162 / 158 (bf16 79 / 80,
+  // 110 / 86, 110 / 116, 141 / 136); 256 x 256 bf16 19 132 / 125, 20 185 / 128, gradient 9 199 / 210, 12 300 / 266 (f16
+  // 139 / 139, 196 / 141, 233 / 250, 347 / 318); 128 x 64 bf16 76 90 / 98, 80 126 / 104, gradient 38 150 / 166, 40 183 / 184.
   const int64_t heads = (int64_t)p.batch * p.heads, walks = gradient ? 2 : 1;
   const bool tensor = !F16 && DK == 128 && p.dv_size > 64;
   if (heads * ((p.dv_size + 15) / 16) <= (tensor || gradient ? sms : 2 * sms)) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);

@@ -17,9 +17,9 @@
 // The walk is a chain: per chunk three products of 512 + 400 + 512 cycles (two, five,
 // two terms of split operands at 8192 flops a cycle) and between them what the threads do,
 // 128 x 128 + 2 x 128 x 64 values converted: eight warps for that alone.  Copies into shared
-// memory and outputs have warps of their own, beside the chain.  A chunk takes 3.2 us (6,100
+// memory and outputs have warps of their own, beside the chain.  A chunk takes 3.3 us (6,200
 // cycles), of which the products' issue, commit and wake are some 1,200; 4 x 8192 steps of 16 heads
-// 416 us on 64 SMs (mma.sync with the state in registers, on 128: 538).
+// 422 us on 64 SMs (mma.sync with the state in registers, on 128: 538).
 #include "gated_delta_mma.cuh"
 
 namespace gemvk {
