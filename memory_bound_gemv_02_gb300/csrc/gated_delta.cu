@@ -335,8 +335,14 @@ int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 // summed without leaving the SMs.
 bool sums_in_clusters(const gated_delta_shape &s) { return s.heads == s.heads_k || (s.heads / s.heads_k <= 8 && s.dk <= 128); }
 
+// Few chunks of few heads have few values of dg and dbeta, and these sums of many terms may be small by chance: one
+// head's dg over two steps was 2e-4 off (2-norm, worst of 40 draws; over 13 to 61 steps 1.6e-5) where fp32 has 3e-7.  There every
+// operand that they see has three parts (3e-6), which takes 48 us in place of 33 for two steps of one head, 57 in place of 44 for 64
+// steps of 16 heads.  In more chunks of heads than these such values are lost among the others (7e-6 at most, emulated).
+constexpr int64_t kFewChunks = 32;
+
 struct Layout {
-  int64_t records, start, end, corrections, dcorr, dq32, dk32, pack[4], bytes;
+  int64_t third_p, records, start, end, corrections, dcorr, dq32, dk32, pack[4], bytes;
 };
 
 // The workspace of a call that goes by chunks; pack[]: copies of q, k, v and d_o.
@@ -351,6 +357,7 @@ Layout layout_of(const gated_delta_shape &s, bool backward, const gemv_heads *co
     return here;
   };
   l.records = take(n * kRecordBytes);
+  l.third_p = backward && n <= kFewChunks ? take(n * kMatrix * 2) : -1;
   if (backward) {
     l.start = take(n * 2 * dvp * dkp * 2);
     l.end = take(n * 2 * dvp * dkp * 2);
@@ -611,5 +618,6 @@ extern "C" int gated_delta_backward(const gated_delta_shape *shape, const gemv_h
   p.dk32 = !sums_in_clusters(s) ? reinterpret_cast<float *>(ws + l.dk32) : nullptr;
   p.vector_dv = on_units(*dv, s.dv) ? 1 : 0;
   p.vector_dqk = on_units(*dq, s.dk) && on_units(*dk, s.dk) ? 1 : 0;
+  p.third_p = l.third_p < 0 ? nullptr : reinterpret_cast<uint16_t *>(ws + l.third_p);
   return launch_delta_gradient(p, padded_dk(s.dk), sms, stream);
 }

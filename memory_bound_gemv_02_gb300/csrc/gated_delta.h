@@ -58,12 +58,15 @@ struct DeltaParams {
   HeadsOf o, dq, dk, dv, dg, dbeta;  // outputs
   float *state, *dh0;
   char *records;                   // (batch, heads, chunks) of kRecordBytes
-  // gradient: states before a chunk and gradients behind it, (.., 2, dvp / 32, DK / 8, 32, 8) bf16, and its
-  // corrections and their gradients, (.., 2, dvp / 32, 8, 32, 8)
+  // gradient: states before a chunk and gradients behind it, (.., 2, dvp / 32, DK / 8, 32, 8) bf16 (or, whole, planes of
+  // fp32), and its corrections and their gradients, (.., 2, dvp / 32, 8, 32, 8)
   uint16_t *start, *end, *corrections, *dcorr;
   float *dq32, *dk32;              // gradients per head of v where heads of k are shared
   float scale;
   int32_t batch, steps, heads, heads_k, dk_size, dv_size, chunks;
+  // gradient of few chunks: P's third part, (batch, heads, chunks) of 64 x 64.  Every operand that dg and dbeta see has
+  // three parts then, what is kept is fp32.
+  uint16_t *third_p;
   int32_t gates_f32, f16, vector_o, vector_dv, vector_dqk;  // outputs whose rows are on 16 bytes
   int32_t polls;       // of the tensor walk's waits
   uint32_t *timeouts;

@@ -115,39 +115,11 @@ __device__ __forceinline__ void invert_diagonal(const float *A, char *T) {
   }
 }
 
-// 16 x 16 blocks as three bf16, for products within fp32's own rounding (of the nine products of
-// parts the three smallest are left out).
-struct Left3 {
-  FragA part[3];
-};
-struct Right3 {
-  uint32_t part[3][4];
-};
-__device__ __forceinline__ void mma_three(FragC &c0, FragC &c1, const Left3 &a, const Right3 &b) {
-#pragma unroll
-  for (int n = 2; n >= 0; --n)  // (the small ones first)
-#pragma unroll
-    for (int i = 0; i <= n; ++i) {
-      mma_bf16(c0, a.part[i], b.part[n - i][0], b.part[n - i][1]);
-      mma_bf16(c1, a.part[i], b.part[n - i][2], b.part[n - i][3]);
-    }
-}
+// A block of A or T in its parts.
 __device__ __forceinline__ Right3 load_right3(uint32_t Y, int part_bytes, int lane) {  // stored (n, k)
   Right3 r;
 #pragma unroll
   for (int n = 0; n < 3; ++n) load_matrices(r.part[n], at_nk(Y + n * part_bytes, kBlockPitch, 0, 0, lane));
-  return r;
-}
-__device__ __forceinline__ Left3 left3_of(const FragC &c0, const FragC &c1) {
-  const float v[4][2] = {{c0[0], c0[1]}, {c0[2], c0[3]}, {c1[0], c1[1]}, {c1[2], c1[3]}};
-  Left3 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t part[3];
-    split3(v[i][0], v[i][1], part);
-#pragma unroll
-    for (int n = 0; n < 3; ++n) r.part[n][i] = part[n];
-  }
   return r;
 }
 
@@ -295,13 +267,13 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
         const float a0 = j < i ? beta[h] * f0 * kk[n][2 * h] : 0.f, a1 = j + 1 < i ? beta[h] * f1 * kk[n][2 * h + 1] : 0.f;
         if (n / 2 == warp)
           *reinterpret_cast<float2 *>(diagonal + i * kDiagPitch + j - warp * 16) = make_float2(a0, a1);
-        uint32_t big, rest;
-        split(j <= i ? p.scale * f0 * qk[n][2 * h] : 0.f, j < i ? p.scale * f1 * qk[n][2 * h + 1] : 0.f, big, rest);
+        uint32_t part[3];
+        split3(j <= i ? p.scale * f0 * qk[n][2 * h] : 0.f, j < i ? p.scale * f1 * qk[n][2 * h + 1] : 0.f, part);
         char *const p_block = smem + L::kT + block_of_t(warp, n / 2) + at;
-        *reinterpret_cast<uint32_t *>(p_block) = big;
-        *reinterpret_cast<uint32_t *>(p_block + kPartBytesT) = rest;
+#pragma unroll
+        for (int u = 0; u < 3; ++u)
+          if (u < kPartsP || p.third_p) *reinterpret_cast<uint32_t *>(p_block + u * kPartBytesT) = part[u];
         if (n / 2 < warp) {
-          uint32_t part[3];
           split3(a0, a1, part);
 #pragma unroll
           for (int u = 0; u < 3; ++u)
@@ -311,6 +283,8 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
     }
     __syncthreads();
     store_lower<kPartsP>(out + kRecordP, smem + L::kT);
+    if (p.third_p)
+      store_lower<1>(p.third_p + ((b * p.heads + head) * p.chunks + chunk) * kMatrix, smem + L::kT + kPartsP * kPartBytesT);
     __syncthreads();
     invert_diagonal(diagonal, smem + L::kT);
     __syncthreads();
@@ -324,7 +298,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 4) delta_prepare_kernel(const
 
 // ------------------------------------------------------------------ walks --
 
-enum { kWalkOut = 0, kWalkKeep = 1 };  // gated_delta(); the gradient's two walks
+enum { kWalkOut = 0, kWalkKeep = 1, kWalkWhole = 2 };  // gated_delta(); the gradient's two walks, and with three parts
 
 // (8 heads of 128 x 128, 1024 steps bf16: 2.2 us a chunk by teams of four warps, copies by warps of
 // their own; 2.6 with the copies among them, 4.9 by one warp alone.)  A CTA's walk: TEAMS teams of SPLIT warps, each with 16 columns of v (rows of S^T); a
@@ -365,6 +339,9 @@ struct Walk {
   }
 };
 
+// What kWalkWhole has besides: the third part of solved, and a stage's of P.
+constexpr int kThirdSolved = 4 * 512;
+
 // The warps of a team, waiting for one another.
 template <int SPLIT>
 __device__ __forceinline__ void team_sync(int team) {
@@ -404,8 +381,8 @@ __device__ __forceinline__ void store_block16(const FragC &c0, const FragC &c1, 
 }
 
 // Sums of 16 rows (from the plane's row `row`, column 8 `unit` of 8 `units`), kept for the
-// gradient as bf16 and the rest `plane` behind.
-template <int N>
+// gradient as bf16 and the rest (WHOLE: what fp32 has besides) `plane` behind.
+template <bool WHOLE, int N>
 __device__ __forceinline__ void keep_split(const FragC *c, uint16_t *to, int row, int unit, int units, int64_t plane) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -413,7 +390,8 @@ __device__ __forceinline__ void keep_split(const FragC *c, uint16_t *to, int row
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t big, rest;
-      split(c[n][2 * h], c[n][2 * h + 1], big, rest);
+      if constexpr (WHOLE) to_planes(c[n][2 * h], c[n][2 * h + 1], big, rest);
+      else split(c[n][2 * h], c[n][2 * h + 1], big, rest);
       uint16_t *const at = to + kept_unit(row + lane / 4 + 8 * h, unit + n, units) * 8 + lane % 4 * 2;
       *reinterpret_cast<uint32_t *>(at) = big;
       *reinterpret_cast<uint32_t *>(at + plane) = rest;
@@ -486,6 +464,7 @@ template <bool F16, int DK, int TEAMS, int SPLIT, int MODE, bool BACK>
 __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b, int64_t head, int slice) {
   typedef Walk<DK, TEAMS, SPLIT> L;
   constexpr int N = L::kTiles, NB = L::kBlocks;
+  constexpr bool kWhole = MODE == kWalkWhole;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, team = warp / SPLIT, part = warp % SPLIT;
   const int64_t head_k = head / (p.heads / p.heads_k), bh = b * p.heads + head;
   const int row0 = slice * L::kSlice + team * 16, col0 = part * L::kColumns;  // of S^T
@@ -495,6 +474,9 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
   char *const sums = smem + L::kExchange + team * L::kTeam, *const solved = sums + L::kSums,
        *const update = solved + L::kOperands;
   float *const factors = reinterpret_cast<float *>(sums + L::kFactors);  // of update's blocks, 16 rows each
+  // kWalkWhole: third parts of solved and of P
+  uint4 *const third = reinterpret_cast<uint4 *>(smem + L::kBytes) + lane;
+  char *const third_p = smem + L::kBytes + kThirdSolved;
   const int tid = L::kCopiers ? (int)threadIdx.x - L::kWalkers : (int)threadIdx.x;
   auto request = [&](int i) {
     if (i < p.chunks) {
@@ -507,6 +489,8 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
       copy_tile<L::kSlice, L::kCopying>(at + L::kV, BACK ? p.td : p.tv, b, head, t0, p.steps, slice * L::kSlice, tid);
       copy_lower<kPartsT, L::kCopying>(at + L::kT, m, tid);
       if (BACK || MODE == kWalkOut) copy_lower<kPartsP, L::kCopying>(at + L::kP, m + kRecordP, tid);
+      if (kWhole && BACK)
+        copy_lower<1, L::kCopying>(smem_u32(third_p + i % L::kStages * kPairBytes), p.third_p + (bh * p.chunks + chunk) * kMatrix, tid);
       if (tid < 3 * kDeltaChunk / 4) copy16(at + L::kGates + tid * 16, record + kRecordHalfs * 2 + tid * 16, true);
     }
     copies_close();
@@ -565,7 +549,7 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
     const float *const from = BACK ? p.dstate : p.h0;
     load_state<N>(from ? from + bh * cells : nullptr, p.dk_size, p.dv_size, row0, col0, S);
   }
-  const bool live = MODE == kWalkKeep || row0 < p.dv_size;  // (without columns a team only copies, or keeps zeros)
+  const bool live = MODE != kWalkOut || row0 < p.dv_size;  // (without columns a team only copies, or keeps zeros)
   for (int i = 0; i < p.chunks; ++i) {
     if (!L::kCopiers) {
       request(L::kStages == 2 ? i + 1 : i);
@@ -584,9 +568,9 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
         c[2] *= f.x;
         c[3] *= f.y;
       };
-      if constexpr (MODE == kWalkKeep) {
+      if constexpr (MODE != kWalkOut) {
         uint16_t *const to = (BACK ? p.end : p.start) + (bh * p.chunks + chunk) * 2 * dvp * DK;
-        keep_split<N>(S, to, row0, col0 / 8, DK / 8, dvp * DK);
+        keep_split<kWhole, N>(S, to, row0, col0 / 8, DK / 8, dvp * DK);
       }
       // products of the state's part with K, and with Q for the output
       FragC r[8] = {}, o[8] = {};
@@ -611,7 +595,13 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
 #pragma unroll
           for (int n = 0; n < 4; ++n) load_matrices(y[n], at_nk(Q, DK + 8, n * 16, col0 + s * 16, lane));
         }
-        mma_split_inputs<F16>(r, big, rest, x);
+        if constexpr (kWhole && !F16) {
+          const Left3 a = left3_of(S[2 * s], S[2 * s + 1]);
+          mma_split_inputs<F16>(r, a.part[2], a.part[1], x);
+          mma_split_inputs<F16>(r, a.part[0], x);
+        } else {
+          mma_split_inputs<F16>(r, big, rest, x);
+        }
         if constexpr (MODE == kWalkOut) mma_split_inputs<F16>(o, big, rest, y);
       }
       if constexpr (F16) {
@@ -651,42 +641,52 @@ __device__ __forceinline__ void walk(const DeltaParams &p, char *smem, int64_t b
           for (int s = 0; s < 4; ++s) {
             if (s < n) continue;
             FragA a;
-            uint32_t h[4], l[4];
+            Right3 b;
             load_matrices_t(a, at_km(V, L::kNarrow, s * 16, team * 16, lane));
-            load_matrices_t(h, at_kn(P, kTilePitch, s * 16, n * 16, lane));
-            load_matrices_t(l, at_kn(P + kPairBytes, kTilePitch, s * 16, n * 16, lane));
-            mma_input_split<F16>(c0, c1, a, h, l);
+            load_matrices_t(b.part[0], at_kn(P, kTilePitch, s * 16, n * 16, lane));
+            load_matrices_t(b.part[1], at_kn(P + kPairBytes, kTilePitch, s * 16, n * 16, lane));
+            if constexpr (kWhole) {
+              load_matrices_t(b.part[2], at_kn(smem_u32(third_p + i % L::kStages * kPairBytes), kTilePitch, s * 16, n * 16, lane));
+              mma_input_three<F16>(c0, c1, a, b);
+            } else {
+              mma_input_split<F16>(c0, c1, a, b.part[0], b.part[1]);
+            }
           }
         }
-        FragA big, rest;
-        split_sums(c0, c1, big, rest);
-        put_operand(solved, n, big, rest);
+        const Left3 a = left3_of(c0, c1);
+        put_operand(solved, n, a.part[0], a.part[1]);
+        if constexpr (kWhole) third[n * 32] = make_uint4(a.part[2][0], a.part[2][1], a.part[2][2], a.part[2][3]);
       }
       team_sync<SPLIT>(team);
       // D = T R, or dR = T^T dD, block by block
       FragC d[2 * NB] = {};
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        FragA big, rest;
-        get_operand(solved, s, big, rest);
+        Left3 a;
+        get_operand(solved, s, a.part[0], a.part[1]);
+        if constexpr (kWhole) {
+          const uint4 v = third[s * 32];
+          a.part[2][0] = v.x; a.part[2][1] = v.y; a.part[2][2] = v.z; a.part[2][3] = v.w;
+        }
 #pragma unroll
         for (int i2 = 0; i2 < NB; ++i2) {
           const int n = L::block(part, i2);
           if (BACK ? s < n : s > n) continue;
-          uint32_t t[3][4];
+          Right3 t;
 #pragma unroll
           for (int u = 0; u < 3; ++u) {
-            if constexpr (BACK) load_matrices_t(t[u], at_kn(T + u * kPairBytes, kTilePitch, s * 16, n * 16, lane));
-            else load_matrices(t[u], at_nk(T + u * kPairBytes, kTilePitch, n * 16, s * 16, lane));
+            if constexpr (BACK) load_matrices_t(t.part[u], at_kn(T + u * kPairBytes, kTilePitch, s * 16, n * 16, lane));
+            else load_matrices(t.part[u], at_nk(T + u * kPairBytes, kTilePitch, n * 16, s * 16, lane));
           }
-          mma_split_three(d[2 * i2], d[2 * i2 + 1], big, rest, t[0], t[1], t[2]);
+          if constexpr (kWhole) mma_three(d[2 * i2], d[2 * i2 + 1], a, t);
+          else mma_split_three(d[2 * i2], d[2 * i2 + 1], a.part[0], a.part[1], t.part[0], t.part[1], t.part[2]);
         }
       }
-      if constexpr (MODE == kWalkKeep) {
+      if constexpr (MODE != kWalkOut) {
         uint16_t *const to = (BACK ? p.dcorr : p.corrections) + (bh * p.chunks + chunk) * 2 * dvp * kDeltaChunk;
 #pragma unroll
         for (int i2 = 0; i2 < NB; ++i2)
-          keep_split<2>(&d[2 * i2], to, row0, L::block(part, i2) * 2, 8, dvp * kDeltaChunk);
+          keep_split<kWhole, 2>(&d[2 * i2], to, row0, L::block(part, i2) * 2, 8, dvp * kDeltaChunk);
       }
       if constexpr (MODE == kWalkOut) {  // this warp's part of O: first scale (Q S) + P D
 #pragma unroll
@@ -795,23 +795,25 @@ __global__ void __launch_bounds__(Walk<DK, TEAMS, SPLIT>::kThreads, 1) delta_wal
 }
 
 // The gradient's two walks: columns of v backward in the first half of the grid, forward in the second.
-template <bool F16, int DK, int TEAMS, int SPLIT>
+template <bool F16, int DK, int TEAMS, int SPLIT, int MODE>
 __global__ void __launch_bounds__(Walk<DK, TEAMS, SPLIT>::kThreads, 1) delta_walks_kernel(const DeltaParams p) {
   extern __shared__ __align__(16) char smem[];
   const int slices = gridDim.x / 2, slice = blockIdx.x % slices;
-  if ((int)blockIdx.x < slices) walk<F16, DK, TEAMS, SPLIT, kWalkKeep, true>(p, smem, blockIdx.z, blockIdx.y, slice);
-  else walk<F16, DK, TEAMS, SPLIT, kWalkKeep, false>(p, smem, blockIdx.z, blockIdx.y, slice);
+  if ((int)blockIdx.x < slices) walk<F16, DK, TEAMS, SPLIT, MODE, true>(p, smem, blockIdx.z, blockIdx.y, slice);
+  else walk<F16, DK, TEAMS, SPLIT, MODE, false>(p, smem, blockIdx.z, blockIdx.y, slice);
 }
 
-template <bool F16, int DK, int TEAMS, int SPLIT>
+template <bool F16, int DK, int TEAMS, int SPLIT, bool WHOLE = false>
 int launch_walk(const DeltaParams &p, bool gradient, cudaStream_t stream) {
   typedef Walk<DK, TEAMS, SPLIT> L;
-  static_assert(L::kBytes <= 227 * 1024, "a stage and what teams exchange");
+  constexpr int MODE = WHOLE ? kWalkWhole : kWalkKeep, BYTES = L::kBytes + (WHOLE ? kThirdSolved + L::kStages * kPairBytes : 0);
+  static_assert(BYTES <= 227 * 1024, "a stage and what teams exchange");
+  static_assert(!WHOLE || TEAMS == 1, "one third part");
   // (the gradient keeps all of 64 columns)
   const int columns = gradient ? (p.dv_size + kDeltaSlice - 1) / kDeltaSlice * kDeltaSlice : p.dv_size;
   const unsigned slices = (unsigned)((columns + L::kSlice - 1) / L::kSlice);
   const dim3 grid(gradient ? 2 * slices : slices, (unsigned)p.heads, (unsigned)p.batch);
-  return gradient ? launch_large(delta_walks_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, L::kBytes, 1, stream, p)
+  return gradient ? launch_large(delta_walks_kernel<F16, DK, TEAMS, SPLIT, MODE>, grid, L::kThreads, BYTES, BYTES, 1, stream, p)
                   : launch_large(delta_walk_kernel<F16, DK, TEAMS, SPLIT>, grid, L::kThreads, L::kBytes, L::kBytes, 1, stream, p);
 }
 
@@ -830,6 +832,7 @@ int launch_chunks(const DeltaParams &p, bool gradient, int sms, cudaStream_t str
   // 19 149 / 168, 32 251 / 218; 64 x 64 f16 76 84 / 85, 80 117 / 91, gradient 38 130 / 135, 40 162 / 158 (bf16 79 / 80,
   // 110 / 86, 110 / 116, 141 / 136); 256 x 256 bf16 19 132 / 125, 20 185 / 128, gradient 9 199 / 210, 12 300 / 266 (f16
   // 139 / 139, 196 / 141, 233 / 250, 347 / 318); 128 x 64 bf16 76 90 / 98, 80 126 / 104, gradient 38 150 / 166, 40 183 / 184.
+  if (gradient && p.third_p) return launch_walk<F16, DK, 1, 4, true>(p, true, stream);
   const int64_t heads = (int64_t)p.batch * p.heads, walks = gradient ? 2 : 1;
   const bool tensor = !F16 && DK == 128 && p.dv_size > 64;
   if (heads * ((p.dv_size + 15) / 16) <= (tensor || gradient ? sms : 2 * sms)) return launch_walk<F16, DK, 1, 4>(p, gradient, stream);

@@ -18,6 +18,8 @@
 // sums of terms that do pass the step, not differences of sums of all terms: exactly 0
 // where a document starts, and no cancellation where decays are strong.
 //
+// Of few chunks (kFewChunks) what the walks kept is fp32 and every operand from it has three parts; else two.
+//
 // 16 steps x 64 columns of dk per warp, three sets of sums.  8192 chunks of 128 x 128: 1.22 ms, the
 // tensor pipe 28 % active and 2 GB read at 1.7 TB/s: one CTA per SM, whose phases (slices of v, the
 // 64 x 64 products, the gates) follow one another.
@@ -142,7 +144,37 @@ __device__ __forceinline__ void put4(uint16_t *to, const float4 &v, int left, bo
   if (left > 3) to[3] = (uint16_t)(w.y >> 16);
 }
 
-template <bool F16, int DK>
+// Two neighbours of what the walks kept.
+template <bool WHOLE>
+__device__ __forceinline__ float2 kept_pair(uint32_t big, uint32_t rest) {
+  if constexpr (WHOLE) {
+    return from_planes(big, rest);
+  } else {
+    const float2 f = unpack_bf16(big), g = unpack_bf16(rest);
+    return make_float2(f.x + g.x, f.y + g.y);
+  }
+}
+// Blocks of what the walks kept as fp32, in three parts.
+template <int ROWS>
+__device__ __forceinline__ Left3 whole_left(uint32_t planes, int plane, int k, int m, int lane) {
+  uint32_t near[4], low[4];
+  load_matrices_t(near, kept_km<ROWS>(planes, k, m, lane));
+  load_matrices_t(low, kept_km<ROWS>(planes + plane, k, m, lane));
+  Left3 r;
+  planes_to_three(near, low, r.part[0], r.part[1], r.part[2]);
+  return r;
+}
+template <int ROWS>
+__device__ __forceinline__ Right3 whole_right(uint32_t planes, int plane, int k, int n, int lane) {
+  uint32_t near[4], low[4];
+  load_matrices_t(near, kept_kn<ROWS>(planes, k, n, lane));
+  load_matrices_t(low, kept_kn<ROWS>(planes + plane, k, n, lane));
+  Right3 r;
+  planes_to_three(near, low, r.part[0], r.part[1], r.part[2]);
+  return r;
+}
+
+template <bool F16, int DK, bool WHOLE>
 __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(const DeltaParams p) {
   typedef Grad<DK> L;
   constexpr int NT = 8 / L::kParts;  // tiles of 8 columns that a warp has of the 64 x 64 products
@@ -212,8 +244,31 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
     __syncthreads();
     char *const slice = smem + L::kStage + turn * L::kSliceBytes;
     const uint32_t from = smem_u32(slice);
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int s = 0; s < L::kSlice / 16; ++s) {
+      for (int s = 0; s < L::kSlice / 16; ++s) {
+        FragA o;
+        load_matrices(o, at_kn(from + L::kDo, L::kNarrow, row, s * 16, lane));
+        const Left3 r = whole_left<L::kSlice>(from + L::kR, L::kSteps, s * 16, row, lane),
+                    d = whole_left<L::kSlice>(from + L::kD, L::kSteps, s * 16, row, lane);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const Right3 state = whole_right<L::kSlice>(from + L::kS, L::kStates, s * 16, col + n * 16, lane);
+          mma_input_three<F16>(dq[2 * n], dq[2 * n + 1], o, state);
+          mma_three(x[2 * n], x[2 * n + 1], r, state);
+          mma_three(y[2 * n], y[2 * n + 1], d, whole_right<L::kSlice>(from + L::kE, L::kStates, s * 16, col + n * 16, lane));
+        }
+#pragma unroll
+        for (int n = 0; n < NT / 2; ++n) {
+          if (mcol + n * 16 > row) continue;
+          const Right3 b = whole_right<L::kSlice>(from + L::kD, L::kSteps, s * 16, mcol + n * 16, lane);
+          mma_input_three<F16>(dp[2 * n], dp[2 * n + 1], o, b);
+          mma_three(mm[2 * n], mm[2 * n + 1], r, b);
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < (WHOLE ? 0 : L::kSlice / 16); ++s) {
       FragA o, r, rr, d, dd;
       load_matrices(o, at_kn(from + L::kDo, L::kNarrow, row, s * 16, lane));
       load_matrices_t(r, kept_km<L::kSlice>(from + L::kR, s * 16, row, lane));
@@ -250,10 +305,10 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       const uint32_t bw[4] = {big.x, big.y, big.z, big.w}, rw[4] = {rest.x, rest.y, rest.z, rest.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack_bf16(bw[e]), g = unpack_bf16(rw[e]);
+        const float2 f = kept_pair<WHOLE>(bw[e], rw[e]);
         const uint16_t v0 = v[2 * e * L::kNarrow], v1 = v[(2 * e + 1) * L::kNarrow];
-        vr[2 * e] = fmaf(f.x + g.x, F16 ? Elem<GEMV_TYPE_F16>::get(v0) : Elem<GEMV_TYPE_BF16>::get(v0), vr[2 * e]);
-        vr[2 * e + 1] = fmaf(f.y + g.y, F16 ? Elem<GEMV_TYPE_F16>::get(v1) : Elem<GEMV_TYPE_BF16>::get(v1), vr[2 * e + 1]);
+        vr[2 * e] = fmaf(f.x, F16 ? Elem<GEMV_TYPE_F16>::get(v0) : Elem<GEMV_TYPE_BF16>::get(v0), vr[2 * e]);
+        vr[2 * e + 1] = fmaf(f.y, F16 ? Elem<GEMV_TYPE_F16>::get(v1) : Elem<GEMV_TYPE_BF16>::get(v1), vr[2 * e + 1]);
       }
     }
     // <S, dS'>: 8 columns of a row per thread
@@ -262,8 +317,8 @@ __global__ void __launch_bounds__(Grad<DK>::kThreads) delta_gradient_kernel(cons
       auto unit = [&](int area) { return *reinterpret_cast<const uint4 *>(slice + area + i * 16); };
       const uint4 sh = unit(L::kS), sl = unit(L::kS + L::kStates), eh = unit(L::kE), el = unit(L::kE + L::kStates);
       auto add = [&](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        const float2 u = unpack_bf16(a), v = unpack_bf16(b), w = unpack_bf16(c), z = unpack_bf16(d);
-        whole = fmaf(u.x + v.x, w.x + z.x, fmaf(u.y + v.y, w.y + z.y, whole));
+        const float2 u = kept_pair<WHOLE>(a, b), w = kept_pair<WHOLE>(c, d);
+        whole = fmaf(u.x, w.x, fmaf(u.y, w.y, whole));
       };
       add(sh.x, sl.x, eh.x, el.x);
       add(sh.y, sl.y, eh.y, el.y);
@@ -545,12 +600,17 @@ __global__ void __launch_bounds__(256) delta_fold_kernel(const DeltaParams p) {
   }
 }
 
-template <bool F16, int DK>
+template <bool F16, int DK, bool WHOLE>
 int launch_gradient(const DeltaParams &p, cudaStream_t stream) {
   typedef Grad<DK> L;
   const int cluster = p.dq32 == nullptr ? p.heads / p.heads_k : 1;
-  return launch_large(delta_gradient_kernel<F16, DK>, dim3((unsigned)((int64_t)p.chunks * p.heads * p.batch)), L::kThreads,
+  return launch_large(delta_gradient_kernel<F16, DK, WHOLE>, dim3((unsigned)((int64_t)p.chunks * p.heads * p.batch)), L::kThreads,
                       L::kBytes, L::kBytes, cluster, stream, p);
+}
+
+template <bool F16, int DK>
+int launch_gradient(const DeltaParams &p, cudaStream_t stream) {
+  return p.third_p ? launch_gradient<F16, DK, true>(p, stream) : launch_gradient<F16, DK, false>(p, stream);
 }
 
 template <bool F16>

@@ -157,6 +157,80 @@ __device__ __forceinline__ void mma_input_split(FragC &c0, FragC &c1, const Frag
   }
 }
 
+// 16 x 16 blocks as three bf16, for products within fp32's own rounding (of the nine products of
+// parts the three smallest are left out).
+struct Left3 {
+  FragA part[3];
+};
+struct Right3 {
+  uint32_t part[3][4];
+};
+__device__ __forceinline__ void mma_three(FragC &c0, FragC &c1, const Left3 &a, const Right3 &b) {
+#pragma unroll
+  for (int n = 2; n >= 0; --n)  // (the small ones first)
+#pragma unroll
+    for (int i = 0; i <= n; ++i) {
+      mma_bf16(c0, a.part[i], b.part[n - i][0], b.part[n - i][1]);
+      mma_bf16(c1, a.part[i], b.part[n - i][2], b.part[n - i][3]);
+    }
+}
+__device__ __forceinline__ Left3 left3_of(const FragC &c0, const FragC &c1) {
+  const float v[4][2] = {{c0[0], c0[1]}, {c0[2], c0[3]}, {c1[0], c1[1]}, {c1[2], c1[3]}};
+  Left3 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t part[3];
+    split3(v[i][0], v[i][1], part);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) r.part[n][i] = part[n];
+  }
+  return r;
+}
+
+// c0, c1 += A b for a left operand that is an input.
+template <bool F16>
+__device__ __forceinline__ void mma_input_three(FragC &c0, FragC &c1, const FragA &a, const Right3 &b) {
+  if constexpr (F16) {
+    FragA big, rest;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_half(a[i], big[i], rest[i]);
+#pragma unroll
+    for (int n = 2; n >= 0; --n) {
+      mma_bf16(c0, big, b.part[n][0], b.part[n][1]);
+      mma_bf16(c1, big, b.part[n][2], b.part[n][3]);
+      if (n == 2) continue;
+      mma_bf16(c0, rest, b.part[n][0], b.part[n][1]);
+      mma_bf16(c1, rest, b.part[n][2], b.part[n][3]);
+    }
+  } else {
+#pragma unroll
+    for (int n = 2; n >= 0; --n) {
+      mma_bf16(c0, a, b.part[n][0], b.part[n][1]);
+      mma_bf16(c1, a, b.part[n][2], b.part[n][3]);
+    }
+  }
+}
+
+// fp32 in two planes of 16 bits: the nearest bf16, and what the low half of its bits takes to be the number again.
+__device__ __forceinline__ void to_planes(float a, float b, uint32_t &near, uint32_t &low) {
+  const uint32_t u = __float_as_uint(a), v = __float_as_uint(b);
+  near = __byte_perm(u + 0x8000u, v + 0x8000u, 0x7632);
+  low = __byte_perm(u, v, 0x5410);
+}
+__device__ __forceinline__ float2 from_planes(uint32_t near, uint32_t low) {
+  return make_float2(__uint_as_float((near << 16) + (uint32_t)((int32_t)(low << 16) >> 16)),
+                     __uint_as_float((near & 0xffff0000u) + (uint32_t)((int32_t)low >> 16)));
+}
+__device__ __forceinline__ void planes_to_three(const uint32_t (&near)[4], const uint32_t (&low)[4], uint32_t (&p0)[4],
+                                                uint32_t (&p1)[4], uint32_t (&p2)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 whole = from_planes(near[i], low[i]), big = unpack_bf16(near[i]);
+    p0[i] = near[i];
+    split(whole.x - big.x, whole.y - big.y, p1[i], p2[i]);
+  }
+}
+
 // In the walks a left operand that was computed meets fp16 inputs as two fp16 (two
 // products instead of three, and nothing to convert of the inputs): each of its rows, a column of v,
 // scaled by a power of two so that the largest of the row here is 2^8 to 2^9, the products scaled
@@ -214,6 +288,16 @@ __device__ __forceinline__ void mma_split_inputs(FragC *c, const FragA &big, con
   for (int n = 0; n < NB; ++n) {
     mma_inputs<F16>(c[2 * n], rest, b[n][0], b[n][1]);
     mma_inputs<F16>(c[2 * n + 1], rest, b[n][2], b[n][3]);
+  }
+}
+
+// c += A B for NB blocks.
+template <bool F16, int NB>
+__device__ __forceinline__ void mma_split_inputs(FragC *c, const FragA &a, const uint32_t (&b)[NB][4]) {
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    mma_inputs<F16>(c[2 * n], a, b[n][0], b[n][1]);
+    mma_inputs<F16>(c[2 * n + 1], a, b[n][2], b[n][3]);
   }
 }
 

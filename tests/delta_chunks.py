@@ -36,13 +36,14 @@ def _steps(x, heads):
     return torch.cat([x, pad], 1).unflatten(1, (n, CHUNK))
 
 
-def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None, inverse=None):
+def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None, inverse=None, uncut=False):
     """(o, state), or with ``do`` (dq, dk, dv, dg, dbeta, dh0), those of heads of k per head of v; finite g.
     ``meets`` cuts what the walks multiply with q and k, in place of ``pieces`` of bf16; ``inverse``: pieces of
-    A and of (I + A)^-1."""
+    A and of (I + A)^-1; ``uncut``: nothing is cut that dg and dbeta of a chunk see, but P, and M and dP."""
     batch, T, heads, _ = v.shape
     c = lambda x: cut(x, pieces)  # noqa: E731
     meets = meets or c
+    w = (lambda x: x) if uncut else c
     q, k, v, g, beta = (_steps(x, heads) for x in (q, k, v, g, beta))
     n = q.shape[1]
     G = g.cumsum(2)
@@ -55,11 +56,11 @@ def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None, 
     S = torch.zeros((len(q), q.shape[-1], v.shape[-1]), dtype=q.dtype, device=q.device) if h0 is None else h0.double().flatten(0, 1)
     o, D, starts = [], [], []
     for i in range(n):
-        s = meets(S)
+        s = S if uncut else meets(S)
         r = beta[:, i, :, None] * (v[:, i] - first[:, i, :, None] * (k[:, i] @ s))
-        d = t[:, i] @ c(r)
+        d = t[:, i] @ w(r)
         o.append(scale * first[:, i, :, None] * (q[:, i] @ s) + P[:, i] @ c(d))
-        starts.append(c(S)), D.append(c(d))
+        starts.append(w(S)), D.append(w(d))
         S = whole[:, i, :, None] * S + k[:, i].mT @ meets(last[:, i, :, None] * d)
     steps = lambda x: x.flatten(1, 2)[:, :T].unflatten(0, (batch, heads)).transpose(1, 2)  # noqa: E731
     if do is None:
@@ -68,14 +69,14 @@ def rule(q, k, v, g, beta, scale, h0, pieces, do=None, dstate=None, meets=None, 
     dS = torch.zeros_like(S) if dstate is None else dstate.double().flatten(0, 1)
     dR, ends = [], []
     for i in reversed(range(n)):
-        s = meets(dS)
+        s = dS if uncut else meets(dS)
         d = P[:, i].mT @ do[:, i] + last[:, i, :, None] * (k[:, i] @ s)
-        r = t[:, i].mT @ c(d)
-        ends.insert(0, c(dS)), dR.insert(0, r)
+        r = t[:, i].mT @ w(d)
+        ends.insert(0, w(dS)), dR.insert(0, r)
         dS = whole[:, i, :, None] * dS + q[:, i].mT @ meets(scale * first[:, i, :, None] * do[:, i]) \
             - k[:, i].mT @ meets((beta * first)[:, i, :, None] * r)
     S, D, dS1, dR = (torch.stack(x, 1) for x in (starts, D, ends, dR))
-    kept = c(dR)
+    kept = w(dR)
     dP, M = scale * f * (do @ D.mT), -(f * (kept @ D.mT)).tril(-1)
     dq0, x0, y0 = scale * first[..., None] * (do @ S.mT), -first[..., None] * (kept @ S.mT), last[..., None] * (D @ dS1.mT)
     W = (dP * (q @ k.mT) + beta[..., None] * M * (k @ k.mT)).tril(-1)
