@@ -346,8 +346,8 @@ int gated_delta(const gated_delta_shape *shape, const gemv_heads *q, const gemv_
  *
  * The forward pass leaves nothing behind for it: states and corrections are computed
  * again from the inputs, chunk by chunk (any number of steps goes by chunks here), and kept in
- * `workspace` (gated_delta_workspace() with d_o) as two bf16 (32 chunks of heads or fewer: as
- * fp32, 8 KB more each): 42 KB + 8 dk dv + 512 dv bytes
+ * `workspace` (gated_delta_workspace() with d_o) as two bf16 (as fp32 where
+ * there are no more than 32 chunks of heads): 256 KB at most, and 42 KB + 8 dk dv + 512 dv bytes
  * per chunk and head, dk rounded up to 64, 128 or 256 and dv to a multiple of 64 (239 KB for
  * 128 x 128).  To bound it, take the gradient of a long sequence in parts, the last first: h0 is
  * the state before a part, dstate the dh0 of the part behind it.  dg, dbeta and dh0 in fp32 are within about 6e-6 of

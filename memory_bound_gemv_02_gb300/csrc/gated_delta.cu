@@ -357,7 +357,9 @@ Layout layout_of(const gated_delta_shape &s, bool backward, const gemv_heads *co
     return here;
   };
   l.records = take(n * kRecordBytes);
-  l.third_p = backward && n <= kFewChunks ? take(n * kMatrix * 2) : -1;
+  // (room for it in longer calls too: a workspace is not to be too short for a call of fewer steps)
+  const int64_t third_p = backward ? take((n < kFewChunks ? n : kFewChunks) * kMatrix * 2) : -1;
+  l.third_p = n <= kFewChunks ? third_p : -1;
   if (backward) {
     l.start = take(n * 2 * dvp * dkp * 2);
     l.end = take(n * 2 * dvp * dkp * 2);

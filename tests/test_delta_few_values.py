@@ -62,3 +62,17 @@ def test_few_values(cuda_dev, size, dtype):
                 assert off(a, w) <= BOUND, (name, seed, off(a, w))
             else:
                 assert bool(((a.double() - w).abs() <= half_ulp(w, dtype) + tol).all()), (name, seed)
+
+
+def test_a_workspace_serves_shorter_calls(gemv_lib):
+    """Fewer steps, sequences or heads never want more of it."""
+    def need(b, t, h, back):
+        v = torch.zeros((b, t, h, 16), dtype=BF16)
+        return gemv_lib.gated_delta_workspace(v, v, v, v if back else None)
+
+    for back in (False, True):
+        steps = [need(1, t, 1, back) for t in range(1, 64 * 36, 21)]
+        heads = [need(2, 70, h, back) for h in range(1, 40)]
+        batch = [need(b, 70, 1, back) for b in range(1, 40)]
+        for sizes in (steps, heads, batch):
+            assert sizes == sorted(sizes)
